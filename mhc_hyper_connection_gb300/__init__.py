@@ -1,5 +1,5 @@
-"""GB300 (sm_103a) mHC pre-mapping forward and backward, and the post-mapping:
-C ABI + thin ctypes binding.
+"""GB300 (sm_103a) mHC pre-mapping and post-mapping, forward and backward, and
+8-bit activation checkpoints: C ABI + thin ctypes binding.
 
 The compute lives in ``libmhc_pre.so`` (built from ``csrc/`` by
 ``python -m mhc_hyper_connection_gb300.build``).  This package only loads it
@@ -13,3 +13,6 @@ from ._binding import (  # noqa: F401
     mhc_pre_mixes_run, mhc_pre_sinkhorn_run,
     mhc_pre_config_default, mhc_pre_create, mhc_pre_destroy, mhc_pre_last_kernel, mhc_pre_last_launch, mhc_pre_run, mhc_pre_run_noalloc, mhc_pre_set_profile_events, mhc_pre_set_wait_test, mhc_pre_status, mhc_pre_weights_size, mhc_pre_prepare_weights,
     mhc_pre_workspace_size, status_string)
+from ._binding import (  # noqa: F401
+    CKPT_BLOCK, Ckpt8, MhcPostBwdArgs, ckpt8_pack, ckpt8_restore, hc_post_backward, hc_post_ckpt, mhc_ckpt8_pack_run,
+    mhc_ckpt8_restore_run, mhc_post_backward_run, mhc_post_ckpt_run)

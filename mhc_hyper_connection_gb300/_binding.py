@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 MHC_OK = 0
 MHC_ERR_NULLPTR = 161001
@@ -62,6 +62,12 @@ class MhcPreBwdArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class MhcPostBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("n", ctypes.c_int64), ("D", ctypes.c_int64), ("grad_out", _P), ("x", _P),
+                ("residual", _P), ("codes", _P), ("scales", _P), ("post", _P), ("comb", _P), ("grad_x", _P),
+                ("grad_residual", _P), ("grad_post", _P), ("grad_comb", _P)]
+
+
 class MhcError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -107,6 +113,14 @@ def library() -> ctypes.CDLL:
             lib.mhc_pre_last_launch.restype = ctypes.c_int32
             lib.mhc_post_run.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P, _P]
             lib.mhc_post_run.restype = ctypes.c_int32
+            lib.mhc_ckpt8_pack_run.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P]
+            lib.mhc_ckpt8_pack_run.restype = ctypes.c_int32
+            lib.mhc_ckpt8_restore_run.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P]
+            lib.mhc_ckpt8_restore_run.restype = ctypes.c_int32
+            lib.mhc_post_ckpt_run.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64] + [_P] * 8
+            lib.mhc_post_ckpt_run.restype = ctypes.c_int32
+            lib.mhc_post_backward_run.argtypes = [ctypes.POINTER(MhcPostBwdArgs), _P]
+            lib.mhc_post_backward_run.restype = ctypes.c_int32
             lib.mhc_pre_backward_workspace_size.argtypes = [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
             lib.mhc_pre_backward_workspace_size.restype = ctypes.c_int32
             lib.mhc_pre_backward_run.argtypes = [_P, ctypes.POINTER(MhcPreBwdArgs), _P]
@@ -220,6 +234,173 @@ def hc_post(x, residual, post, comb, out=None, stream=None):
     if st != MHC_OK:
         raise MhcError(st, "mhc_post_run", last_error())
     return out
+
+
+# ------------------------------------------- 8-bit checkpoints, post-mapping backward
+
+CKPT_BLOCK = 128
+
+
+def mhc_ckpt8_pack_run(rows: int, D: int, dtype: int, x: int, codes: int, scales: int, stream: int = 0) -> int:
+    """The 8-bit form of x (include/mhc_ckpt.h) on raw device pointers."""
+    return library().mhc_ckpt8_pack_run(int(rows), int(D), int(dtype), x or None, codes or None, scales or None,
+                                        stream or None)
+
+
+def mhc_ckpt8_restore_run(rows: int, D: int, dtype: int, codes: int, scales: int, x: int, stream: int = 0) -> int:
+    return library().mhc_ckpt8_restore_run(int(rows), int(D), int(dtype), codes or None, scales or None, x or None,
+                                           stream or None)
+
+
+def mhc_post_ckpt_run(T: int, n: int, D: int, x: int, residual: int, post: int, comb: int, out: int, codes: int,
+                      scales: int, stream: int = 0) -> int:
+    return library().mhc_post_ckpt_run(int(T), int(n), int(D), x or None, residual or None, post or None, comb or None,
+                                       out or None, codes or None, scales or None, stream or None)
+
+
+def mhc_post_backward_run(args: MhcPostBwdArgs, stream: int = 0) -> int:
+    return library().mhc_post_backward_run(ctypes.byref(args), stream or None)
+
+
+class Ckpt8(NamedTuple):
+    """An 8-bit checkpoint of a 16-bit tensor [..., D]: codes uint8 [..., D] and
+    scales uint8 [..., ceil(D / 128)] (block exponent + 127)."""
+    codes: object
+    scales: object
+
+
+def _stream(stream, device) -> int:
+    """Raw handle of a torch stream, an integer, or torch's current stream."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return int(getattr(stream, "cuda_stream", stream))
+
+
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return MHC_DTYPE_BF16
+    if t.dtype == torch.float16:
+        return MHC_DTYPE_FP16
+    raise ValueError(f"a bf16 or fp16 tensor is needed (got {t.dtype})")
+
+
+def _want(t, name: str, dtype, shape, device) -> int:
+    """Address of a tensor that must have this dtype, shape and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    return _ptr(t)
+
+
+def _ckpt_alloc(shape, device) -> Ckpt8:
+    import torch
+    shape = tuple(shape)
+    return Ckpt8(torch.empty(shape, dtype=torch.uint8, device=device),
+                 torch.empty(shape[:-1] + ((shape[-1] + CKPT_BLOCK - 1) // CKPT_BLOCK,), dtype=torch.uint8,
+                             device=device))
+
+
+def _ckpt_ptrs(ckpt, shape, device):
+    import torch
+    shape = torch.Size(shape)
+    blocks = torch.Size(shape[:-1] + ((shape[-1] + CKPT_BLOCK - 1) // CKPT_BLOCK,))
+    return (_want(ckpt.codes, "codes", torch.uint8, shape, device),
+            _want(ckpt.scales, "scales", torch.uint8, blocks, device))
+
+
+def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
+    """The 8-bit checkpoint of x (bf16 or fp16 [..., D], D a multiple of 8):
+    e4m3 codes with one power-of-two scale per 128 columns.  `out` is a Ckpt8
+    to write into.  Raises MhcError on a host-side rejection."""
+    dt = _dtype_code(x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    D = x.shape[-1]
+    if out is None:
+        out = _ckpt_alloc(x.shape, x.device)
+    codes, scales = _ckpt_ptrs(out, x.shape, x.device)
+    st = mhc_ckpt8_pack_run(x.numel() // D if D else 0, D, dt, _ptr(x), codes, scales, _stream(stream, x.device))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_ckpt8_pack_run", last_error())
+    return out
+
+
+def ckpt8_restore(ckpt, dtype=None, out=None, stream=None):
+    """The 16-bit tensor a checkpoint stands for (exact; dtype: the type it was
+    packed from, default bf16)."""
+    import torch
+    codes = ckpt.codes
+    if out is None:
+        out = torch.empty(codes.shape, dtype=dtype or torch.bfloat16, device=codes.device)
+    elif out.shape != codes.shape or out.device != codes.device or dtype not in (None, out.dtype):
+        raise ValueError("out must have the shape and device of the codes, and the given dtype")
+    cp, sp = _ckpt_ptrs(ckpt, codes.shape, codes.device)
+    D = codes.shape[-1]
+    st = mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, _dtype_code(out), cp, sp, _ptr(out),
+                               _stream(stream, codes.device))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_ckpt8_restore_run", last_error())
+    return out
+
+
+def _post_shapes(residual_shape, x, post, comb, device):
+    """Checks of the post-mapping's inputs against the residual's shape; (T, n, D)
+    and the addresses of x, post and comb."""
+    import torch
+    lead, (n, D) = residual_shape[:-2], residual_shape[-2:]
+    T = _tokens(lead)
+    return (T, n, D, _want(x, "x", torch.bfloat16, lead + (D,), device),
+            _want(post, "post", torch.float32, lead + (n,), device),
+            _want(comb, "comb", torch.float32, lead + (n, n), device))
+
+
+def hc_post_ckpt(x, residual, post, comb, out=None, ckpt=None, stream=None):
+    """hc_post that also writes the 8-bit checkpoint of its output in the same
+    pass; returns (out, Ckpt8).  Same tensors and layouts as hc_post."""
+    import torch
+    dev = residual.device
+    T, n, D, xp, pp, cp = _post_shapes(residual.shape, x, post, comb, dev)
+    if out is None:
+        out = torch.empty_like(residual)
+    if ckpt is None:
+        ckpt = _ckpt_alloc(residual.shape, dev)
+    codes, scales = _ckpt_ptrs(ckpt, residual.shape, dev)
+    st = mhc_post_ckpt_run(T, n, D, xp, _want(residual, "residual", torch.bfloat16, residual.shape, dev), pp, cp,
+                           _want(out, "out", torch.bfloat16, residual.shape, dev), codes, scales,
+                           _stream(stream, dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_post_ckpt_run", last_error())
+    return out, ckpt
+
+
+def hc_post_backward(grad_out, x, residual, post, comb, grads=None, stream=None):
+    """Backward of hc_post (include/mhc_post_backward.h): grad_out bf16
+    [T, n, D] (or BSND), the forward's x, post and comb, and its residual as
+    bf16 or as a Ckpt8.  Returns {"grad_x", "grad_residual" (bf16),
+    "grad_post", "grad_comb" (fp32)}, written into `grads` when given."""
+    import torch
+    dev, shape = grad_out.device, grad_out.shape
+    T, n, D, xp, pp, cp = _post_shapes(shape, x, post, comb, dev)
+    if grads is None:
+        grads = {"grad_x": torch.empty_like(x), "grad_residual": torch.empty_like(grad_out),
+                 "grad_post": torch.empty_like(post), "grad_comb": torch.empty_like(comb)}
+    a = MhcPostBwdArgs()
+    a.T, a.n, a.D, a.x, a.post, a.comb = T, n, D, xp, pp, cp
+    a.grad_out = _want(grad_out, "grad_out", torch.bfloat16, shape, dev)
+    if isinstance(residual, Ckpt8):
+        a.codes, a.scales = _ckpt_ptrs(residual, shape, dev)
+    else:
+        a.residual = _want(residual, "residual", torch.bfloat16, shape, dev)
+    a.grad_x = _want(grads["grad_x"], "grad_x", torch.bfloat16, x.shape, dev)
+    a.grad_residual = _want(grads["grad_residual"], "grad_residual", torch.bfloat16, shape, dev)
+    a.grad_post = _want(grads["grad_post"], "grad_post", torch.float32, post.shape, dev)
+    a.grad_comb = _want(grads["grad_comb"], "grad_comb", torch.float32, comb.shape, dev)
+    st = mhc_post_backward_run(a, _stream(stream, dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_post_backward_run", last_error())
+    return grads
 
 
 def mhc_pre_backward_workspace_size(handle, T: int):

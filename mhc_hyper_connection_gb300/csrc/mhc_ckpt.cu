@@ -1,0 +1,288 @@
+// mhc_ckpt.cu -- 8-bit activation checkpoints on sm_103a: pack, restore, and
+// the post-mapping that packs its own output (include/mhc_ckpt.h).
+//
+// All three are streaming kernels bounded by HBM: pack reads 2 and writes 1 +
+// 1/128 bytes an element, restore the reverse, the post-mapping adds 1 + 1/128
+// bytes an output element to what it moves anyway.  A block of 128 columns is
+// 16 lanes of eight elements, so its maximum takes four shuffles on packed
+// 16-bit pairs and each lane turns its own 16 bytes into 8.
+#include "mhc_ckpt.cuh"
+#include "mhc_host.cuh"
+#include "../../include/mhc_ckpt.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kCkptThreads = 256;
+constexpr int kUnroll = 4;     // consecutive blocks of one half-warp, all loads in flight
+
+// kFlat: D is a multiple of 128, so block b starts at element 128 b.
+template <bool F16, bool kFlat>
+__global__ void __launch_bounds__(kCkptThreads)
+    ckpt_pack_kernel(long long total, int nblk, int D, const uint16_t* __restrict__ x, uint8_t* __restrict__ codes,
+                     uint8_t* __restrict__ scales) {
+  const int l = threadIdx.x & 15;
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+  const long long b0 = (((long long)blockIdx.x * kCkptThreads + threadIdx.x) >> 4) * kUnroll;
+  if (b0 >= total) return;                         // whole half-warps leave
+  const uint64_t once = policy_evict_first();
+  long long off[kUnroll];
+  bool in[kUnroll];
+  uint4 v[kUnroll];
+  {
+    long long row = 0;
+    int cb = 0;
+    if (!kFlat) {
+      row = total <= 0xFFFFFFFFll ? (long long)((uint32_t)b0 / (uint32_t)nblk) : b0 / nblk;
+      cb = (int)(b0 - row * nblk);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (kFlat) {
+        off[u] = (b0 + u) * kCkptBlock + l * 8;
+        in[u] = b0 + u < total;
+      } else {
+        const int col = cb * kCkptBlock + l * 8;
+        off[u] = row * D + col;
+        in[u] = b0 + u < total && col < D;
+        if (++cb == nblk) { cb = 0; ++row; }
+      }
+      v[u] = in[u] ? ld_global_v4_hint(x + off[u], once) : make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    uint2 c;
+    const int e = ckpt_block16<F16>(v[u], mask, c);
+    if (in[u]) __stcs(reinterpret_cast<uint2*>(codes + off[u]), c);
+    if (l == 0 && b0 + u < total) scales[b0 + u] = (uint8_t)(e + 127);
+  }
+}
+
+template <bool F16, bool kFlat>
+__global__ void __launch_bounds__(kCkptThreads)
+    ckpt_restore_kernel(long long vecs, int vrow, int nblk, const uint8_t* __restrict__ codes,
+                        const uint8_t* __restrict__ scales, uint16_t* __restrict__ x) {
+  using X = XType<F16>;
+  const uint64_t once = policy_evict_first();
+  const long long v0 = (long long)blockIdx.x * (kCkptThreads * kUnroll) + threadIdx.x;
+  uint2 c[kUnroll];
+  uint32_t sb[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long v = v0 + u * kCkptThreads;
+    c[u] = make_uint2(0, 0);
+    sb[u] = 127;
+    if (v < vecs) {
+      long long sidx = v >> 4;
+      if (!kFlat) {
+        const long long row = vecs <= 0xFFFFFFFFll ? (long long)((uint32_t)v / (uint32_t)vrow) : v / vrow;
+        sidx = row * nblk + ((v - row * vrow) >> 4);
+      }
+      c[u] = __ldcs(reinterpret_cast<const uint2*>(codes) + v);
+      sb[u] = __ldg(scales + sidx);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const long long v = v0 + u * kCkptThreads;
+    if (v >= vecs) break;
+    const float s = ckpt_scale(sb[u]);
+    const uint32_t w[2] = {c[u].x, c[u].y};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = e4m3x2_f2(w[e >> 1] >> (16 * (e & 1)));
+      const typename X::T2 p = X::from_f2(f.x * s, f.y * s);     // exact
+      o[e] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    st_global_v4_hint(x + v * 8, make_uint4(o[0], o[1], o[2], o[3]), once);
+  }
+}
+
+// The post-mapping (out[j] = post[j] x + sum_i comb[i][j] residual[i], one
+// warp a token, fp32 sums in that order, RN-even) and the checkpoint of its
+// rounded output: the 16 lanes that hold a block of 128 columns join their
+// maxima and encode from registers.
+template <int NS>
+__global__ void __launch_bounds__(kCkptThreads)
+    post_ckpt_kernel(int T, int D, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ res,
+                     const float* __restrict__ post, const float* __restrict__ comb, __nv_bfloat16* __restrict__ out,
+                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int kV = NS <= 4 ? 2 : 1;
+  const int lane = threadIdx.x & 31;
+  const int gw = (blockIdx.x * kCkptThreads + threadIdx.x) >> 5, nw = (gridDim.x * kCkptThreads) >> 5;
+  const int nv = D >> 3, nblk = (D + kCkptBlock - 1) / kCkptBlock;
+  const uint64_t once = policy_evict_first();
+  const uint32_t mask = 0xFFFFu << (lane & 16);
+  for (int t = gw; t < T; t += nw) {
+    float pc[NS], cm[NS * NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) pc[j] = __ldg(post + (size_t)t * NS + j);
+#pragma unroll
+    for (int e = 0; e < NS * NS; ++e) cm[e] = __ldg(comb + (size_t)t * NS * NS + e);
+    const __nv_bfloat16* xt = x + (size_t)t * D;
+    const __nv_bfloat16* rt = res + (size_t)t * NS * D;
+    for (int vb = 0; vb < nv; vb += 32 * kV) {     // all lanes stay for the shuffles
+      uint4 xv[kV], rv[kV][NS];
+#pragma unroll
+      for (int q = 0; q < kV; ++q) {
+        const int v = vb + q * 32 + lane;
+        xv[q] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) rv[q][i] = make_uint4(0, 0, 0, 0);
+        if (v < nv) {
+          xv[q] = ld_global_v4_hint(xt + (size_t)v * 8, once);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) rv[q][i] = ld_global_v4_hint(rt + (size_t)i * D + (size_t)v * 8, once);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kV; ++q) {
+        const int v = vb + q * 32 + lane;
+        if ((v & ~15) >= nv) continue;             // this half-warp's block lies beyond the row
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          float acc[8];
+          const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv[q]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(hx[e]);
+            acc[2 * e] = pc[j] * f.x;
+            acc[2 * e + 1] = pc[j] * f.y;
+          }
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const float c = cm[i * NS + j];
+            const __nv_bfloat162* hr = reinterpret_cast<const __nv_bfloat162*>(&rv[q][i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = __bfloat1622float2(hr[e]);
+              acc[2 * e] = fmaf(c, f.x, acc[2 * e]);
+              acc[2 * e + 1] = fmaf(c, f.y, acc[2 * e + 1]);
+            }
+          }
+          uint4 o;
+          __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(&o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ob[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+          if (v >= nv) o = make_uint4(0, 0, 0, 0);   // beyond the row: nothing for the maximum (a NaN coefficient times 0)
+          uint2 c8;
+          const int ex = ckpt_block16<false>(o, mask, c8);
+          const size_t row = (size_t)t * NS + j;
+          if (v < nv) {
+            st_global_v4_hint(out + row * D + (size_t)v * 8, o, once);
+            __stcs(reinterpret_cast<uint2*>(codes + row * D + (size_t)v * 8), c8);
+          }
+          if ((lane & 15) == 0) scales[row * nblk + (v >> 4)] = (uint8_t)(ex + 127);
+        }
+      }
+    }
+  }
+}
+
+template <int NS>
+cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* res, const float* post,
+                             const float* comb, void* out, void* codes, void* scales, cudaStream_t s) {
+  int dev = 0, per_sm = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, post_ckpt_kernel<NS>, kCkptThreads, 0)) != cudaSuccess)
+    return e;
+  const DeviceInfo di = device_info(dev);
+  long long grid = (long long)(di.sms > 0 ? di.sms : 1) * (per_sm > 0 ? per_sm : 1);
+  const long long need = (T * 32 + kCkptThreads - 1) / kCkptThreads;
+  if (grid > need) grid = need;
+  post_ckpt_kernel<NS><<<(int)grid, kCkptThreads, 0, s>>>(
+      (int)T, (int)D, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res), post, comb,
+      static_cast<__nv_bfloat16*>(out), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+  return cudaGetLastError();
+}
+
+mhc_status_t check_matrix(int64_t rows, int64_t D, int32_t dtype, const void* x, const void* codes, const void* scales) {
+  if (dtype != MHC_DTYPE_BF16 && dtype != MHC_DTYPE_FP16)
+    return fail(MHC_ERR_PARAM_INVALID, "dtype must be MHC_DTYPE_BF16 or MHC_DTYPE_FP16 (got %d)", (int)dtype);
+  if (D < 8 || D > (int64_t(1) << 20) || (D % 8) != 0)
+    return fail(MHC_ERR_PARAM_INVALID, "D must be a multiple of 8 in [8, 2^20] (got %lld)", (long long)D);
+  if (rows < 0 || rows > (int64_t(1) << 38) / D)
+    return fail(MHC_ERR_PARAM_INVALID, "rows must be >= 0 and rows * D at most 2^38 (got %lld)", (long long)rows);
+  if (rows == 0) return MHC_OK;
+  if (!x || !codes || !scales) return fail(MHC_ERR_NULLPTR, "x, codes and scales are required");
+  if (!aligned(x, 16)) return fail(MHC_ERR_PARAM_INVALID, "x must be 16-byte aligned");
+  if (!aligned(codes, 8)) return fail(MHC_ERR_PARAM_INVALID, "codes must be 8-byte aligned");
+  return MHC_OK;
+}
+
+}  // namespace
+}  // namespace mhc
+
+using namespace mhc;
+
+extern "C" {
+
+mhc_status_t mhc_ckpt8_pack_run(int64_t rows, int64_t D, int32_t dtype, const void* x, void* codes, void* scales,
+                                void* stream) {
+  clear_error();
+  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales);
+  if (st != MHC_OK || rows == 0) return st;
+  const int nblk = (int)((D + kCkptBlock - 1) / kCkptBlock);
+  const long long total = rows * nblk;
+  const long long per = (kCkptThreads / 16) * kUnroll;
+  const unsigned grid = (unsigned)((total + per - 1) / per);     // rows * D <= 2^38: below 2^31
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  uint8_t *cp = static_cast<uint8_t*>(codes), *sp = static_cast<uint8_t*>(scales);
+  const bool flat = D % kCkptBlock == 0, f16 = dtype == MHC_DTYPE_FP16;
+  auto* k = f16 ? (flat ? ckpt_pack_kernel<true, true> : ckpt_pack_kernel<true, false>)
+                : (flat ? ckpt_pack_kernel<false, true> : ckpt_pack_kernel<false, false>);
+  k<<<grid, kCkptThreads, 0, s>>>(total, nblk, (int)D, xp, cp, sp);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "checkpoint pack launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_ckpt8_restore_run(int64_t rows, int64_t D, int32_t dtype, const void* codes, const void* scales,
+                                   void* x, void* stream) {
+  clear_error();
+  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales);
+  if (st != MHC_OK || rows == 0) return st;
+  const int nblk = (int)((D + kCkptBlock - 1) / kCkptBlock), vrow = (int)(D / 8);
+  const long long vecs = rows * vrow;
+  const long long per = kCkptThreads * kUnroll;
+  const unsigned grid = (unsigned)((vecs + per - 1) / per);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint8_t *cp = static_cast<const uint8_t*>(codes), *sp = static_cast<const uint8_t*>(scales);
+  uint16_t* xp = static_cast<uint16_t*>(x);
+  const bool flat = D % kCkptBlock == 0, f16 = dtype == MHC_DTYPE_FP16;
+  auto* k = f16 ? (flat ? ckpt_restore_kernel<true, true> : ckpt_restore_kernel<true, false>)
+                : (flat ? ckpt_restore_kernel<false, true> : ckpt_restore_kernel<false, false>);
+  k<<<grid, kCkptThreads, 0, s>>>(vecs, vrow, nblk, cp, sp, xp);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "checkpoint restore launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_post_ckpt_run(int64_t T, int64_t n, int64_t D, const void* x, const void* residual, const float* post,
+                               const float* comb, void* out, void* codes, void* scales, void* stream) {
+  clear_error();
+  if (T < 0 || T > (int64_t(1) << 30)) return fail(MHC_ERR_PARAM_INVALID, "T must be in [0, 2^30]");
+  if (n < 1 || n > 8) return fail(MHC_ERR_PARAM_INVALID, "n must be in [1, 8] (got %lld)", (long long)n);
+  if (D < 8 || D > (int64_t(1) << 20) || (D % 8) != 0)
+    return fail(MHC_ERR_PARAM_INVALID, "D must be a multiple of 8 in [8, 2^20] (got %lld)", (long long)D);
+  if (T == 0) return MHC_OK;
+  if (!x || !residual || !post || !comb || !out || !codes || !scales)
+    return fail(MHC_ERR_NULLPTR, "x, residual, post, comb, out, codes and scales are required");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(out, 16))
+    return fail(MHC_ERR_PARAM_INVALID, "x, residual and out must be 16-byte aligned");
+  if (!aligned(codes, 8)) return fail(MHC_ERR_PARAM_INVALID, "codes must be 8-byte aligned");
+  if (!aligned(post, 4) || !aligned(comb, 4)) return fail(MHC_ERR_PARAM_INVALID, "post and comb must be 4-byte aligned");
+  using Fn = cudaError_t (*)(int64_t, int64_t, const void*, const void*, const float*, const float*, void*, void*,
+                             void*, cudaStream_t);
+  static const Fn table[8] = {launch_post_ckpt<1>, launch_post_ckpt<2>, launch_post_ckpt<3>, launch_post_ckpt<4>,
+                              launch_post_ckpt<5>, launch_post_ckpt<6>, launch_post_ckpt<7>, launch_post_ckpt<8>};
+  const cudaError_t e = table[n - 1](T, D, x, residual, post, comb, out, codes, scales, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "post-mapping launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+}  // extern "C"

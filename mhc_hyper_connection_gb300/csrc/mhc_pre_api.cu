@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "mhc_common.cuh"
+#include "mhc_host.cuh"
 #include "../../include/mhc_pre.h"
 #include "../../include/mhc_post.h"
 #include "../../include/mhc_pre_backward.h"
@@ -33,6 +34,10 @@ namespace {
 
 thread_local char g_last_error[512] = "";
 
+}  // namespace
+
+namespace mhc {
+
 mhc_status_t fail(mhc_status_t code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -41,10 +46,53 @@ mhc_status_t fail(mhc_status_t code, const char* fmt, ...) {
   return code;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
+void clear_error() { g_last_error[0] = 0; }
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+DeviceInfo device_info(int dev) {
+  static std::mutex mu;
+  static DeviceInfo cache[64];
+  static bool known[64] = {};
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 0 || dev >= 64) return DeviceInfo{};
+  if (!known[dev]) {
+    DeviceInfo d;
+    cudaDeviceProp prop;
+    if (cudaGetDeviceProperties(&prop, dev) == cudaSuccess) {
+      d.ok = (prop.major == 10 && prop.minor == 3);
+      d.sms = prop.multiProcessorCount;
+      d.max_smem = prop.sharedMemPerBlockOptin;
+      d.l2_bytes = (size_t)prop.l2CacheSize;
+    }
+    cache[dev] = d;
+    known[dev] = true;
+  }
+  return cache[dev];
+}
+
+}  // namespace mhc
+
+namespace {
+
+using mhc::aligned;
+using mhc::device_info;
+using mhc::DeviceInfo;
+using mhc::encode_fn;
+using mhc::EncodeTiledFn;
+using mhc::fail;
 
 typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
 
@@ -59,20 +107,6 @@ CtxGetCurrentFn ctx_get_current_fn() {
     if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<CtxGetCurrentFn>(p);
-  });
-  return fn;
-}
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
   });
   return fn;
 }
@@ -107,36 +141,6 @@ bool encode_4d(CUtensorMap* map, const void* base, const uint64_t dims[4], const
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
-
-struct DeviceInfo {
-  bool ok = false;
-  int sms = 0;
-  size_t max_smem = 0;
-  size_t l2_bytes = 0;
-};
-
-DeviceInfo device_info(int dev) {
-  static std::mutex mu;
-  static DeviceInfo cache[64];
-  static bool known[64] = {};
-  std::lock_guard<std::mutex> lk(mu);
-  if (dev < 0 || dev >= 64) return DeviceInfo{};
-  if (!known[dev]) {
-    DeviceInfo d;
-    cudaDeviceProp prop;
-    if (cudaGetDeviceProperties(&prop, dev) == cudaSuccess) {
-      d.ok = (prop.major == 10 && prop.minor == 3);
-      d.sms = prop.multiProcessorCount;
-      d.max_smem = prop.sharedMemPerBlockOptin;
-      d.l2_bytes = (size_t)prop.l2CacheSize;
-    }
-    cache[dev] = d;
-    known[dev] = true;
-  }
-  return cache[dev];
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Swizzled plane blocks: [chunk][stream][RB rows][128 bytes].
 size_t planes_bytes(const mhc_pre_s* h) {
