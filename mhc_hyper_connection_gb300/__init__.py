@@ -1,5 +1,6 @@
-"""GB300 (sm_103a) mHC pre-mapping and post-mapping, forward and backward, and
-8-bit activation checkpoints: C ABI + thin ctypes binding.
+"""GB300 (sm_103a) mHC pre-mapping and post-mapping, the gated feed-forward block
+between them, each forward and backward, and 8-bit activation checkpoints:
+C ABI + thin ctypes binding.
 
 The compute lives in ``libmhc_pre.so`` (built from ``csrc/`` by
 ``python -m mhc_hyper_connection_gb300.build``).  This package only loads it
@@ -16,3 +17,7 @@ from ._binding import (  # noqa: F401
 from ._binding import (  # noqa: F401
     CKPT_BLOCK, Ckpt8, MhcPostBwdArgs, ckpt8_pack, ckpt8_restore, hc_post_backward, hc_post_ckpt, mhc_ckpt8_pack_run,
     mhc_ckpt8_restore_run, mhc_post_backward_run, mhc_post_ckpt_run)
+from ._binding import (  # noqa: F401
+    MHC_FFN_GELU, MHC_FFN_SILU, MhcFfnArgs, MhcFfnBwdArgs, gated_ffn, gated_ffn_backward, gated_ffn_status,
+    gated_ffn_workspace, mhc_ffn_backward_run, mhc_ffn_backward_workspace_size, mhc_ffn_run, mhc_ffn_status,
+    mhc_ffn_workspace_size)

@@ -68,6 +68,21 @@ class MhcPostBwdArgs(ctypes.Structure):
                 ("grad_residual", _P), ("grad_post", _P), ("grad_comb", _P)]
 
 
+class MhcFfnArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("x", _P), ("w_gate_up", _P), ("w_down", _P), ("y", _P), ("gate_up", _P),
+                ("codes", _P), ("scales", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("wait_limit_us", ctypes.c_uint32), ("withhold_copy", ctypes.c_int32)]
+
+
+class MhcFfnBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("grad_y", _P), ("x", _P), ("w_gate_up", _P), ("w_down", _P),
+                ("gate_up", _P), ("codes", _P), ("scales", _P), ("grad_x", _P), ("grad_w_gate_up", _P),
+                ("grad_w_down", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("wait_limit_us", ctypes.c_uint32), ("withhold_copy", ctypes.c_int32)]
+
+
 class MhcError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -121,6 +136,16 @@ def library() -> ctypes.CDLL:
             lib.mhc_post_ckpt_run.restype = ctypes.c_int32
             lib.mhc_post_backward_run.argtypes = [ctypes.POINTER(MhcPostBwdArgs), _P]
             lib.mhc_post_backward_run.restype = ctypes.c_int32
+            SZP = ctypes.POINTER(ctypes.c_size_t)
+            for f in (lib.mhc_ffn_workspace_size, lib.mhc_ffn_backward_workspace_size):
+                f.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, SZP]
+                f.restype = ctypes.c_int32
+            lib.mhc_ffn_run.argtypes = [ctypes.POINTER(MhcFfnArgs), _P]
+            lib.mhc_ffn_run.restype = ctypes.c_int32
+            lib.mhc_ffn_backward_run.argtypes = [ctypes.POINTER(MhcFfnBwdArgs), _P]
+            lib.mhc_ffn_backward_run.restype = ctypes.c_int32
+            lib.mhc_ffn_status.argtypes = [_P, _P]
+            lib.mhc_ffn_status.restype = ctypes.c_int32
             lib.mhc_pre_backward_workspace_size.argtypes = [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
             lib.mhc_pre_backward_workspace_size.restype = ctypes.c_int32
             lib.mhc_pre_backward_run.argtypes = [_P, ctypes.POINTER(MhcPreBwdArgs), _P]
@@ -400,6 +425,156 @@ def hc_post_backward(grad_out, x, residual, post, comb, grads=None, stream=None)
     st = mhc_post_backward_run(a, _stream(stream, dev))
     if st != MHC_OK:
         raise MhcError(st, "mhc_post_backward_run", last_error())
+    return grads
+
+
+# ------------------------------------------------------- gated feed-forward block
+
+MHC_FFN_SILU = 0
+MHC_FFN_GELU = 1
+_ACTS = {"silu": MHC_FFN_SILU, "gelu": MHC_FFN_GELU}
+
+
+def mhc_ffn_workspace_size(T: int, D: int, F: int):
+    n = ctypes.c_size_t(0)
+    st = library().mhc_ffn_workspace_size(int(T), int(D), int(F), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_ffn_backward_workspace_size(T: int, D: int, F: int):
+    n = ctypes.c_size_t(0)
+    st = library().mhc_ffn_backward_workspace_size(int(T), int(D), int(F), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_ffn_run(args: MhcFfnArgs, stream: int = 0) -> int:
+    return library().mhc_ffn_run(ctypes.byref(args), stream or None)
+
+
+def mhc_ffn_backward_run(args: MhcFfnBwdArgs, stream: int = 0) -> int:
+    return library().mhc_ffn_backward_run(ctypes.byref(args), stream or None)
+
+
+def mhc_ffn_status(workspace: int = 0, stream: int = 0) -> int:
+    return library().mhc_ffn_status(workspace or None, stream or None)
+
+
+def gated_ffn_workspace(T: int, D: int, F: int, device, backward: bool = False):
+    """Scratch (uint8) that gated_ffn, or with backward=True
+    gated_ffn_backward, takes for T tokens: for callers that keep one buffer
+    over calls or want to read its status afterwards."""
+    import torch
+    st, n = (mhc_ffn_backward_workspace_size if backward else mhc_ffn_workspace_size)(T, D, F)
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_ffn_backward_workspace_size" if backward else "mhc_ffn_workspace_size", last_error())
+    ws = torch.empty((max(n, 256),), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def gated_ffn_status(workspace=None, stream=None) -> int:
+    """Waits for `stream` (default: torch's current stream), then the device
+    status of the last call that used `workspace`."""
+    dev = None if workspace is None else workspace.device
+    return mhc_ffn_status(_ptr(workspace) or 0, _stream(stream, dev))
+
+
+def _ffn_scratch(nbytes: int, device, raw_stream: int, own_stream: bool):
+    """Scratch for one call; when it runs on another stream than torch's
+    current one, the allocator is told so."""
+    import torch
+    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    if not own_stream:
+        ws.record_stream(torch.cuda.ExternalStream(raw_stream, device=device))
+    return ws
+
+
+def _ffn_common(a, x, w_gate_up, w_down, act):
+    """Fill the fields that both directions share; (lead dims, device)."""
+    import torch
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
+    a.dtype, a.act = _dtype_code(x), _ACTS[act]
+    lead, D = x.shape[:-1], x.shape[-1]
+    if w_gate_up.dim() != 3 or w_gate_up.shape[0] != 2:
+        raise ValueError("w_gate_up must be [2, F, D]")
+    F = w_gate_up.shape[1]
+    a.T, a.D, a.F = _tokens(lead), D, F
+    a.x = _ptr(x)
+    a.w_gate_up = _want(w_gate_up, "w_gate_up", x.dtype, torch.Size((2, F, D)), x.device)
+    a.w_down = _want(w_down, "w_down", x.dtype, torch.Size((D, F)), x.device)
+    return lead, x.device
+
+
+def _ffn_workspace(a, size, name, workspace, device, stream):
+    """Raw stream and the workspace tensor (kept alive by the caller)."""
+    raw = _stream(stream, device)
+    if workspace is None:
+        st, n = size(a.T, a.D, a.F)
+        if st != MHC_OK:
+            raise MhcError(st, name, last_error())
+        workspace = _ffn_scratch(n, device, raw, stream is None) if n else None
+    if workspace is not None:
+        a.workspace = _ptr(workspace)
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    return raw, workspace
+
+
+def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, workspace=None, stream=None):
+    """y = (act(x Wg^T) (.) x Wu^T) Wd^T (include/mhc_ffn.h): x bf16 or fp16
+    [T, D] (or [B, S, D]), w_gate_up [2, F, D] (Wg, Wu), w_down [D, F], act
+    "silu" or "gelu" (tanh form).  save keeps both projections for the
+    backward: "16bit" as a tensor [T, 2, F], "8bit" as a Ckpt8 of that shape.
+    Returns (y, kept); kept is None without save.  y, kept and workspace are
+    allocated unless given."""
+    import torch
+    a = MhcFfnArgs()
+    lead, dev = _ffn_common(a, x, w_gate_up, w_down, act)
+    shape = lead + (2, a.F)
+    if save == "16bit":
+        if kept is None:
+            kept = torch.empty(shape, dtype=x.dtype, device=dev)
+        a.gate_up = _want(kept, "kept", x.dtype, shape, dev)
+    elif save == "8bit":
+        if kept is None:
+            kept = _ckpt_alloc(shape, dev)
+        a.codes, a.scales = _ckpt_ptrs(kept, shape, dev)
+    elif save is not None or kept is not None:
+        raise ValueError('save must be None, "16bit" or "8bit" (and kept given only with it)')
+    if y is None:
+        y = torch.empty_like(x)
+    a.y = _want(y, "y", x.dtype, x.shape, dev)
+    raw, workspace = _ffn_workspace(a, mhc_ffn_workspace_size, "mhc_ffn_workspace_size", workspace, dev, stream)
+    st = mhc_ffn_run(a, raw)
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_ffn_run", last_error())
+    return y, kept
+
+
+def gated_ffn_backward(grad_y, x, w_gate_up, w_down, kept, act="silu", grads=None, workspace=None, stream=None):
+    """Backward of gated_ffn from what it kept (a tensor or a Ckpt8): returns
+    {"grad_x", "grad_w_gate_up", "grad_w_down"} in x's type, written into
+    `grads` when given."""
+    import torch
+    a = MhcFfnBwdArgs()
+    lead, dev = _ffn_common(a, x, w_gate_up, w_down, act)
+    a.grad_y = _want(grad_y, "grad_y", x.dtype, x.shape, dev)
+    shape = lead + (2, a.F)
+    if isinstance(kept, Ckpt8):
+        a.codes, a.scales = _ckpt_ptrs(kept, shape, dev)
+    else:
+        a.gate_up = _want(kept, "kept", x.dtype, shape, dev)
+    if grads is None:
+        grads = {"grad_x": torch.empty_like(x), "grad_w_gate_up": torch.empty_like(w_gate_up),
+                 "grad_w_down": torch.empty_like(w_down)}
+    a.grad_x = _want(grads["grad_x"], "grad_x", x.dtype, x.shape, dev)
+    a.grad_w_gate_up = _want(grads["grad_w_gate_up"], "grad_w_gate_up", x.dtype, w_gate_up.shape, dev)
+    a.grad_w_down = _want(grads["grad_w_down"], "grad_w_down", x.dtype, w_down.shape, dev)
+    raw, workspace = _ffn_workspace(a, mhc_ffn_backward_workspace_size, "mhc_ffn_backward_workspace_size", workspace,
+                                    dev, stream)
+    st = mhc_ffn_backward_run(a, raw)
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_ffn_backward_run", last_error())
     return grads
 
 

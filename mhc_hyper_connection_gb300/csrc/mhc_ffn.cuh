@@ -1,0 +1,43 @@
+// mhc_ffn.cuh -- launch plumbing shared by the feed-forward block's files.
+#pragma once
+
+#include "mhc_ckpt.cuh"
+
+namespace mhc {
+
+// One matrix product D[M, N] = A B^T on 16-bit operands: operand row r, depth
+// k.  "K-major" operands store k contiguously, "MN-major" ones r.
+struct GemmShape {
+  int M, N, K;                 // rows, columns, depth of the product
+  int tiles_m, tiles_n, kiters;
+  uint32_t idesc;
+  uint32_t* err;               // device error word
+  uint64_t wait_ns;
+  int withhold;                // test hook: leave out the last copy of CTA 0
+  int clear_err;               // first kernel of a call: clear the error word
+};
+
+// Forward: kept = 0 none, 1 16-bit, 2 8-bit.
+struct FfnFwdLaunch {
+  CUtensorMap x, wgu, a, wd;
+  GemmShape gu, down;
+  int T, D, F, act, kept, sms;
+  void *a_buf, *y, *gate_up, *codes, *scales;
+};
+cudaError_t launch_ffn_forward(const FfnFwdLaunch& L, bool f16, cudaStream_t s);
+
+struct FfnBwdLaunch {
+  CUtensorMap gy_k, wd_mn;         // ga = grad_y Wd
+  CUtensorMap gg_k, wgu_mn;        // grad_x = [gg, gu] [Wg; Wu]
+  CUtensorMap gg_mn, x_mn;         // grad_w_gate_up = [gg, gu]^T x
+  CUtensorMap gy_mn, a_mn;         // grad_w_down = grad_y^T a
+  GemmShape ga, gx, gwgu, gwd;
+  int T, D, F, act, kept, sms;
+  const void *gate_up, *codes, *scales;
+  void *gg_buf, *a_buf, *grad_x, *grad_w_gate_up, *grad_w_down;
+};
+cudaError_t launch_ffn_backward(const FfnBwdLaunch& L, bool f16, cudaStream_t s);
+
+constexpr int kFfnTileM = 128, kFfnTileN = 256, kFfnTileK = 64;
+
+}  // namespace mhc

@@ -1,0 +1,239 @@
+// mhc_ffn_api.cu -- host side of include/mhc_ffn.h: argument checks, workspace
+// layout, tensor maps and the launches' shapes.
+#include "mhc_ffn.cuh"
+#include "mhc_host.cuh"
+#include "../../include/mhc_ffn.h"
+
+using namespace mhc;
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct FwdLayout {
+  size_t a, total;
+};
+FwdLayout fwd_layout(int64_t T, int64_t F) {
+  FwdLayout l;
+  l.a = 256;
+  l.total = l.a + up256((size_t)T * F * 2);
+  return l;
+}
+struct BwdLayout {
+  size_t gg, a, total;
+};
+BwdLayout bwd_layout(int64_t T, int64_t F) {
+  BwdLayout l;
+  l.gg = 256;
+  l.a = l.gg + up256((size_t)T * F * 4);
+  l.total = l.a + up256((size_t)T * F * 2);
+  return l;
+}
+
+mhc_status_t check_sizes(int64_t T, int64_t D, int64_t F) {
+  if (T < 0 || T > (int64_t(1) << 24)) return fail(MHC_ERR_PARAM_INVALID, "T must be in [0, 2^24] (got %lld)", (long long)T);
+  if (D < 8 || D > (int64_t(1) << 20) || D % 8 != 0)
+    return fail(MHC_ERR_PARAM_INVALID, "D must be a multiple of 8 in [8, 2^20] (got %lld)", (long long)D);
+  if (F < 8 || F > (int64_t(1) << 20) || F % 8 != 0)
+    return fail(MHC_ERR_PARAM_INVALID, "F must be a multiple of 8 in [8, 2^20] (got %lld)", (long long)F);
+  return MHC_OK;
+}
+
+mhc_status_t check_common(int32_t dtype, int32_t act, uint32_t wait_us, int32_t withhold) {
+  if (dtype != MHC_DTYPE_BF16 && dtype != MHC_DTYPE_FP16)
+    return fail(MHC_ERR_PARAM_INVALID, "dtype must be MHC_DTYPE_BF16 or MHC_DTYPE_FP16 (got %d)", (int)dtype);
+  if (act != MHC_FFN_SILU && act != MHC_FFN_GELU)
+    return fail(MHC_ERR_PARAM_INVALID, "act must be MHC_FFN_SILU or MHC_FFN_GELU (got %d)", (int)act);
+  if (wait_us > 10000000u) return fail(MHC_ERR_PARAM_INVALID, "wait_limit_us must be at most 10 s");
+  if (withhold != 0 && withhold != 1) return fail(MHC_ERR_PARAM_INVALID, "withhold_copy must be 0 or 1");
+  return MHC_OK;
+}
+
+// Tensor [rows, cols] (cols contiguous), planes of it behind one another; box
+// of 64 columns x `box_rows` rows; zeros outside.
+bool map_2d(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t rows, uint64_t planes,
+            uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[3] = {cols, rows, planes};
+  cuuint64_t st[2] = {cols * 2, planes > 1 ? cols * rows * 2 : cols * 2};
+  cuuint32_t b[3] = {64, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d,
+            st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool a_mn, bool b_mn, uint32_t* err,
+                uint32_t wait_us) {
+  GemmShape g;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.tiles_m = (int)((M + kFfnTileM - 1) / kFfnTileM);
+  g.tiles_n = (int)((N + tile_n - 1) / tile_n);
+  g.kiters = (int)((K + kFfnTileK - 1) / kFfnTileK);
+  g.idesc = (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+            ((uint32_t)(kFfnTileN >> 3) << 17) | ((uint32_t)(kFfnTileM >> 4) << 24);
+  g.err = err;
+  g.wait_ns = wait_us ? (uint64_t)wait_us * 1000u : 2000000000ull;
+  g.withhold = 0;
+  g.clear_err = 0;
+  return g;
+}
+
+mhc_status_t device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MHC_ERR_RUNTIME, "no CUDA device");
+  const DeviceInfo di = device_info(dev);
+  if (!di.ok) return fail(MHC_ERR_RUNTIME, "device %d is not an sm_103 GPU", dev);
+  *sms = di.sms;
+  return MHC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mhc_status_t mhc_ffn_workspace_size(int64_t T, int64_t D, int64_t F, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
+  const mhc_status_t st = check_sizes(T, D, F);
+  if (st != MHC_OK) return st;
+  *bytes = T ? fwd_layout(T, F).total : 0;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_ffn_backward_workspace_size(int64_t T, int64_t D, int64_t F, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
+  const mhc_status_t st = check_sizes(T, D, F);
+  if (st != MHC_OK) return st;
+  *bytes = T ? bwd_layout(T, F).total : 0;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
+  clear_error();
+  if (!a) return fail(MHC_ERR_NULLPTR, "args must be non-NULL");
+  const int64_t T = a->T, D = a->D, F = a->F;
+  mhc_status_t st = check_sizes(T, D, F);
+  if (st == MHC_OK) st = check_common(a->dtype, a->act, a->wait_limit_us, a->withhold_copy);
+  if (st != MHC_OK || T == 0) return st;
+  if (!a->x || !a->w_gate_up || !a->w_down || !a->y || !a->workspace)
+    return fail(MHC_ERR_NULLPTR, "x, w_gate_up, w_down, y and the workspace are required");
+  if ((a->codes == nullptr) != (a->scales == nullptr))
+    return fail(MHC_ERR_PARAM_INVALID, "codes and scales go together (both or neither)");
+  if (a->gate_up && a->codes) return fail(MHC_ERR_PARAM_INVALID, "give gate_up or codes, not both");
+  const void* v16[] = {a->x, a->w_gate_up, a->w_down, a->y, a->gate_up, a->codes};
+  for (const void* p : v16)
+    if (!aligned(p, 16)) return fail(MHC_ERR_PARAM_INVALID, "tensors must be 16-byte aligned");
+  if (!aligned(a->workspace, 256)) return fail(MHC_ERR_PARAM_INVALID, "the workspace must be 256-byte aligned");
+  const FwdLayout l = fwd_layout(T, F);
+  if (a->workspace_bytes < l.total)
+    return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
+  FfnFwdLaunch L;
+  if ((st = device(&L.sms)) != MHC_OK) return st;
+  const bool f16 = a->dtype == MHC_DTYPE_FP16;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  L.T = (int)T;
+  L.D = (int)D;
+  L.F = (int)F;
+  L.act = a->act;
+  L.kept = a->gate_up ? 1 : a->codes ? 2 : 0;
+  L.a_buf = ws + l.a;
+  L.y = a->y;
+  L.gate_up = a->gate_up;
+  L.codes = a->codes;
+  L.scales = a->scales;
+  if (!map_2d(&L.x, a->x, f16, D, T, 1, kFfnTileM) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, 128) ||
+      !map_2d(&L.a, L.a_buf, f16, F, T, 1, kFfnTileM) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, 128))
+    return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
+  L.gu = shape(T, F, D, 128, f16, false, false, err, a->wait_limit_us);
+  L.down = shape(T, D, F, kFfnTileN, f16, false, false, err, a->wait_limit_us);
+  L.gu.clear_err = 1;
+  L.down.withhold = a->withhold_copy;
+  const cudaError_t e = launch_ffn_forward(L, f16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
+  clear_error();
+  if (!a) return fail(MHC_ERR_NULLPTR, "args must be non-NULL");
+  const int64_t T = a->T, D = a->D, F = a->F;
+  mhc_status_t st = check_sizes(T, D, F);
+  if (st == MHC_OK) st = check_common(a->dtype, a->act, a->wait_limit_us, a->withhold_copy);
+  if (st != MHC_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!a->grad_w_gate_up || !a->grad_w_down) return fail(MHC_ERR_NULLPTR, "both weight gradients are required");
+  if (T == 0) {
+    cudaError_t e = cudaMemsetAsync(a->grad_w_gate_up, 0, (size_t)D * F * 4, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a->grad_w_down, 0, (size_t)D * F * 2, s);
+    if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "clearing the weight gradients failed: %s", cudaGetErrorString(e));
+    return MHC_OK;
+  }
+  if (!a->grad_y || !a->x || !a->w_gate_up || !a->w_down || !a->grad_x || !a->workspace)
+    return fail(MHC_ERR_NULLPTR, "grad_y, x, w_gate_up, w_down, grad_x and the workspace are required");
+  if ((a->codes == nullptr) != (a->scales == nullptr))
+    return fail(MHC_ERR_PARAM_INVALID, "codes and scales go together (both or neither)");
+  if (!a->gate_up && !a->codes) return fail(MHC_ERR_NULLPTR, "gate_up or codes and scales are required");
+  if (a->gate_up && a->codes) return fail(MHC_ERR_PARAM_INVALID, "give gate_up or codes, not both");
+  const void* v16[] = {a->grad_y, a->x, a->w_gate_up, a->w_down, a->gate_up, a->codes,
+                       a->grad_x, a->grad_w_gate_up, a->grad_w_down};
+  for (const void* p : v16)
+    if (!aligned(p, 16)) return fail(MHC_ERR_PARAM_INVALID, "tensors must be 16-byte aligned");
+  if (!aligned(a->workspace, 256)) return fail(MHC_ERR_PARAM_INVALID, "the workspace must be 256-byte aligned");
+  const BwdLayout l = bwd_layout(T, F);
+  if (a->workspace_bytes < l.total)
+    return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
+  FfnBwdLaunch L;
+  if ((st = device(&L.sms)) != MHC_OK) return st;
+  const bool f16 = a->dtype == MHC_DTYPE_FP16;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  L.T = (int)T;
+  L.D = (int)D;
+  L.F = (int)F;
+  L.act = a->act;
+  L.kept = a->gate_up ? 1 : 2;
+  L.gate_up = a->gate_up;
+  L.codes = a->codes;
+  L.scales = a->scales;
+  L.gg_buf = ws + l.gg;
+  L.a_buf = ws + l.a;
+  L.grad_x = a->grad_x;
+  L.grad_w_gate_up = a->grad_w_gate_up;
+  L.grad_w_down = a->grad_w_down;
+  if (!map_2d(&L.gy_k, a->grad_y, f16, D, T, 1, kFfnTileM) || !map_2d(&L.wd_mn, a->w_down, f16, F, D, 1, 64) ||
+      !map_2d(&L.gg_k, L.gg_buf, f16, 2 * F, T, 1, kFfnTileM) || !map_2d(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, 1, 64) ||
+      !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, 64) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, 64) ||
+      !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, 64) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, 64))
+    return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
+  const uint32_t w = a->wait_limit_us;
+  L.ga = shape(T, F, D, kFfnTileN, f16, false, true, err, w);
+  L.gx = shape(T, D, 2 * F, kFfnTileN, f16, false, true, err, w);
+  L.gwgu = shape(2 * F, D, T, kFfnTileN, f16, true, true, err, w);
+  L.gwd = shape(D, F, T, kFfnTileN, f16, true, true, err, w);
+  L.ga.clear_err = 1;
+  L.gwd.withhold = a->withhold_copy;
+  const cudaError_t e = launch_ffn_backward(L, f16, s);
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward backward launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_ffn_status(const void* workspace, void* stream) {
+  clear_error();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t word = 0;
+  cudaError_t e = cudaSuccess;
+  if (workspace) e = cudaMemcpyAsync(&word, workspace, sizeof word, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "CUDA error: %s", cudaGetErrorString(e));
+  if (word) return fail(MHC_ERR_RUNTIME, "device error word 0x%x: a wait gave up", word);
+  return MHC_OK;
+}
+
+}  // extern "C"

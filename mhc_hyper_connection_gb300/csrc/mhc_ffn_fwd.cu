@@ -1,0 +1,37 @@
+// mhc_ffn_fwd.cu -- forward kernels of the gated feed-forward block.
+#include "mhc_ffn_gemm.cuh"
+
+namespace mhc {
+namespace {
+
+template <bool F16, int kKept>
+cudaError_t gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
+  EpiGateUp<F16, kKept> e;
+  e.a = static_cast<uint16_t*>(L.a_buf);
+  e.gate_up = static_cast<uint16_t*>(L.gate_up);
+  e.codes = static_cast<uint8_t*>(L.codes);
+  e.scales = static_cast<uint8_t*>(L.scales);
+  e.T = L.T;
+  e.F = L.F;
+  e.act = L.act;
+  return launch_gemm<false, false, true>(L.x, L.wgu, L.gu, e, L.sms, s);
+}
+
+template <bool F16>
+cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
+  const cudaError_t e = L.kept == 0 ? gate_up<F16, 0>(L, s) : L.kept == 1 ? gate_up<F16, 1>(L, s) : gate_up<F16, 2>(L, s);
+  if (e != cudaSuccess) return e;
+  EpiStore<F16> o;
+  o.out = static_cast<uint16_t*>(L.y);
+  o.M = L.T;
+  o.N = L.D;
+  return launch_gemm<false, false, false>(L.a, L.wd, L.down, o, L.sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_forward(const FfnFwdLaunch& L, bool f16, cudaStream_t s) {
+  return f16 ? forward<true>(L, s) : forward<false>(L, s);
+}
+
+}  // namespace mhc

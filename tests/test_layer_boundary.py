@@ -20,7 +20,7 @@ def lib():
     return mp.library()
 
 
-@pytest.mark.parametrize("header", ["mhc_ckpt.h", "mhc_post_backward.h"])
+@pytest.mark.parametrize("header", ["mhc_ckpt.h", "mhc_post_backward.h", "mhc_ffn.h"])
 def test_library_exports_every_declared_symbol(lib, header):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
     names = re.findall(r"MHC_API[^;(]*?\b(mhc_[a-z0-9_]+)\s*\(", text)
@@ -78,3 +78,44 @@ def test_post_backward_refusals(lib):
         assert mp.last_error()
     for k in ("grad_out", "x", "residual", "post", "comb", "grad_x", "grad_residual", "grad_post", "grad_comb"):
         assert _post_bwd(**{k: None}) == mp.MHC_ERR_NULLPTR, k
+
+
+def _ffn(backward=False, **kw):
+    a = mp.MhcFfnBwdArgs() if backward else mp.MhcFfnArgs()
+    a.T, a.D, a.F = 4, 64, 128
+    names = ("grad_y", "x", "w_gate_up", "w_down", "gate_up", "grad_x", "grad_w_gate_up", "grad_w_down") if backward \
+        else ("x", "w_gate_up", "w_down", "y")
+    for k in names + ("workspace",):
+        setattr(a, k, P)
+    a.workspace_bytes = 1 << 30
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return (mp.mhc_ffn_backward_run if backward else mp.mhc_ffn_run)(a)
+
+
+def test_ffn_workspace_sizes(lib):
+    assert mp.mhc_ffn_workspace_size(0, 64, 128) == (mp.MHC_OK, 0)
+    assert mp.mhc_ffn_workspace_size(3, 64, 128) == (mp.MHC_OK, 256 + 768)
+    assert mp.mhc_ffn_backward_workspace_size(3, 64, 128) == (mp.MHC_OK, 256 + 1536 + 768)
+    for bad in ((-1, 64, 128), (1, 0, 128), (1, 60, 128), (1, 64, 0), (1, 64, 132), ((1 << 24) + 1, 64, 128),
+                (1, (1 << 20) + 8, 8)):
+        assert mp.mhc_ffn_workspace_size(*bad)[0] == mp.MHC_ERR_PARAM_INVALID
+        assert mp.mhc_ffn_backward_workspace_size(*bad)[0] == mp.MHC_ERR_PARAM_INVALID
+    assert lib.mhc_ffn_workspace_size(1, 8, 8, None) == mp.MHC_ERR_NULLPTR
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_ffn_refusals(lib, backward):
+    assert lib.mhc_ffn_run(None, None) == lib.mhc_ffn_backward_run(None, None) == mp.MHC_ERR_NULLPTR
+    assert ctypes.sizeof(mp.MhcFfnArgs) == 3 * 8 + 8 + 9 * 8 + 8
+    assert ctypes.sizeof(mp.MhcFfnBwdArgs) == 3 * 8 + 8 + 12 * 8 + 8
+    if not backward:
+        assert _ffn(T=0, x=None) == mp.MHC_OK
+    for kw in ({"T": -1}, {"D": 0}, {"D": 60}, {"F": 4}, {"dtype": 2}, {"act": 2}, {"act": -1}, {"x": P + 8},
+               {"w_down": P + 2}, {"workspace": P + 16}, {"workspace_bytes": 100}, {"codes": P}, {"scales": P},
+               {"gate_up": P, "codes": P, "scales": P}, {"wait_limit_us": 10000001}, {"withhold_copy": 2}):
+        assert _ffn(backward, **kw) == mp.MHC_ERR_PARAM_INVALID, kw
+        assert mp.last_error()
+    for k in ("x", "w_gate_up", "w_down", "workspace") + (("grad_y", "gate_up", "grad_x", "grad_w_gate_up", "grad_w_down")
+                                                          if backward else ("y",)):
+        assert _ffn(backward, **{k: None}) == mp.MHC_ERR_NULLPTR, k
