@@ -11,6 +11,7 @@ struct GemmShape {
   int M, N, K;                 // rows, columns, depth of the product
   int tiles_m, tiles_n, kiters;
   uint32_t idesc;
+  int a_mn, b_mn;              // operand stored MN-major
   uint32_t* err;               // device error word
   uint64_t wait_ns;
   int withhold;                // test hook: leave out the last copy of CTA 0
@@ -38,6 +39,7 @@ struct FfnBwdLaunch {
 };
 cudaError_t launch_ffn_backward(const FfnBwdLaunch& L, bool f16, cudaStream_t s);
 
-constexpr int kFfnTileM = 128, kFfnTileN = 256, kFfnTileK = 64;
+constexpr int kFfnTileM = 256, kFfnTileN = 256, kFfnTileK = 64;
+constexpr uint32_t kFfnBoxK = 128, kFfnBoxMn = 64;   // tensor-map box rows of a K-major / MN-major operand
 
 }  // namespace mhc

@@ -75,6 +75,8 @@ GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool 
   g.kiters = (int)((K + kFfnTileK - 1) / kFfnTileK);
   g.idesc = (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
             ((uint32_t)(kFfnTileN >> 3) << 17) | ((uint32_t)(kFfnTileM >> 4) << 24);
+  g.a_mn = a_mn;
+  g.b_mn = b_mn;
   g.err = err;
   g.wait_ns = wait_us ? (uint64_t)wait_us * 1000u : 2000000000ull;
   g.withhold = 0;
@@ -147,8 +149,8 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   L.gate_up = a->gate_up;
   L.codes = a->codes;
   L.scales = a->scales;
-  if (!map_2d(&L.x, a->x, f16, D, T, 1, kFfnTileM) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, 128) ||
-      !map_2d(&L.a, L.a_buf, f16, F, T, 1, kFfnTileM) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, 128))
+  if (!map_2d(&L.x, a->x, f16, D, T, 1, kFfnBoxK) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
+      !map_2d(&L.a, L.a_buf, f16, F, T, 1, kFfnBoxK) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, kFfnBoxK))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
   L.gu = shape(T, F, D, 128, f16, false, false, err, a->wait_limit_us);
   L.down = shape(T, D, F, kFfnTileN, f16, false, false, err, a->wait_limit_us);
@@ -206,10 +208,10 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
   L.grad_x = a->grad_x;
   L.grad_w_gate_up = a->grad_w_gate_up;
   L.grad_w_down = a->grad_w_down;
-  if (!map_2d(&L.gy_k, a->grad_y, f16, D, T, 1, kFfnTileM) || !map_2d(&L.wd_mn, a->w_down, f16, F, D, 1, 64) ||
-      !map_2d(&L.gg_k, L.gg_buf, f16, 2 * F, T, 1, kFfnTileM) || !map_2d(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, 1, 64) ||
-      !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, 64) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, 64) ||
-      !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, 64) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, 64))
+  if (!map_2d(&L.gy_k, a->grad_y, f16, D, T, 1, kFfnBoxK) || !map_2d(&L.wd_mn, a->w_down, f16, F, D, 1, kFfnBoxMn) ||
+      !map_2d(&L.gg_k, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxK) || !map_2d(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, 1, kFfnBoxMn) ||
+      !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxMn) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, kFfnBoxMn) ||
+      !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, kFfnBoxMn) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
   const uint32_t w = a->wait_limit_us;
   L.ga = shape(T, F, D, kFfnTileN, f16, false, true, err, w);

@@ -15,7 +15,7 @@ cudaError_t dgate(const FfnBwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<false, true, false>(L.gy_k, L.wd_mn, L.ga, e, L.sms, s);
+  return launch_gemm<false>(L.gy_k, L.wd_mn, L.ga, e, L.sms, s);
 }
 
 template <bool F16>
@@ -26,14 +26,14 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
   o.out = static_cast<uint16_t*>(L.grad_x);
   o.M = L.T;
   o.N = L.D;
-  if ((e = launch_gemm<false, true, false>(L.gg_k, L.wgu_mn, L.gx, o, L.sms, s)) != cudaSuccess) return e;
+  if ((e = launch_gemm<false>(L.gg_k, L.wgu_mn, L.gx, o, L.sms, s)) != cudaSuccess) return e;
   o.out = static_cast<uint16_t*>(L.grad_w_gate_up);
   o.M = 2 * L.F;
-  if ((e = launch_gemm<true, true, false>(L.gg_mn, L.x_mn, L.gwgu, o, L.sms, s)) != cudaSuccess) return e;
+  if ((e = launch_gemm<false>(L.gg_mn, L.x_mn, L.gwgu, o, L.sms, s)) != cudaSuccess) return e;
   o.out = static_cast<uint16_t*>(L.grad_w_down);
   o.M = L.D;
   o.N = L.F;
-  return launch_gemm<true, true, false>(L.gy_mn, L.a_mn, L.gwd, o, L.sms, s);
+  return launch_gemm<false>(L.gy_mn, L.a_mn, L.gwd, o, L.sms, s);
 }
 
 }  // namespace

@@ -14,7 +14,7 @@ cudaError_t gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<false, false, true>(L.x, L.wgu, L.gu, e, L.sms, s);
+  return launch_gemm<true>(L.x, L.wgu, L.gu, e, L.sms, s);
 }
 
 template <bool F16>
@@ -25,7 +25,7 @@ cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
   o.out = static_cast<uint16_t*>(L.y);
   o.M = L.T;
   o.N = L.D;
-  return launch_gemm<false, false, false>(L.a, L.wd, L.down, o, L.sms, s);
+  return launch_gemm<false>(L.a, L.wd, L.down, o, L.sms, s);
 }
 
 }  // namespace

@@ -1,22 +1,28 @@
 // mhc_ffn_gemm.cuh -- the matrix product of the feed-forward block on the
 // tensor cores, with a fused epilogue.
 //
-// Persistent CTAs take output tiles of 128 x 256.  One warp streams operand
-// chunks of 64 along the depth into a ring of shared-memory stages (TMA, 128-
-// byte swizzle), one thread issues tcgen05.mma on them into one of two tensor-
-// memory accumulators, and two groups of four warps read the accumulators back
-// alternately and run the epilogue, so that a tile's epilogue overlaps the next
-// tile's products.
+// Persistent pairs of CTAs (clusters of two, one tcgen05 cta_group::2) take
+// output tiles of 256 x 256.  Each CTA holds 128 rows of A and 128 of B, so a
+// stage of depth 64 is 32 KB per SM where a tile of its own (128 x 256) would
+// be 48: a third less L2 traffic and six stages instead of four.  In each CTA
+// one warp streams its operand rows into the ring (TMA, 128-byte swizzle, all
+// completing on the even CTA's barriers); one thread of the even CTA issues the
+// products for both into one of two tensor-memory accumulators; and in each CTA
+// two groups of four warps read its 128 rows back alternately and run the
+// epilogue, so that a tile's epilogue overlaps the next tile's products.
 #pragma once
+
+#include <atomic>
 
 #include "mhc_ffn.cuh"
 
 namespace mhc {
 
 constexpr int kGemmThreads = 320;          // producer, MMA issuer, 2 x 4 epilogue warps
-constexpr int kGemmStages = 4;
-constexpr int kGemmABytes = kFfnTileM * kFfnTileK * 2, kGemmBBytes = kFfnTileN * kFfnTileK * 2;
-constexpr int kGemmStageBytes = kGemmABytes + kGemmBBytes;
+constexpr int kGemmStages = 6;
+constexpr int kGemmHalf = 128;             // rows of A and of B that one CTA of the pair holds
+constexpr int kGemmOpBytes = kGemmHalf * kFfnTileK * 2;
+constexpr int kGemmStageBytes = 2 * kGemmOpBytes;
 
 struct GemmTail {
   uint64_t full[kGemmStages], empty[kGemmStages];
@@ -27,17 +33,46 @@ struct GemmTail {
 };
 constexpr size_t kGemmSmem = (size_t)kGemmStages * kGemmStageBytes + sizeof(GemmTail) + 1024;
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+// The address, in the cluster's shared window, of this CTA's object `p` in
+// CTA `rank`.
+__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// Tiled load into this CTA's shared memory, completing on a barrier of either
+// CTA of the pair (`bar`: its address in the cluster's window).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// D[256, N] += A B^T over a depth of 16, A and B halved over the pair.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the products issued
+// so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
       : "memory");
 }
 
 // Tile t of the persistent loop: bands of kBand tile rows, column by column
 // inside a band, so that the CTAs running at one time share operand rows in L2.
-constexpr int kBand = 16;
+constexpr int kBand = 8;
 __device__ __forceinline__ void tile_coords(const GemmShape& g, int t, int& tm, int& tn) {
   const int band = t / (kBand * g.tiles_n), first = band * kBand;
   const int rows = min(kBand, g.tiles_m - first);
@@ -229,10 +264,12 @@ struct EpiDgate {
 
 // ------------------------------------------------------------------ kernel
 
-// kPair: B's 256 rows are 128 rows of plane 0 and the same 128 of plane 1
-// (gate and up); else 256 consecutive rows.
-template <class Epi, bool kAMN, bool kBMN, bool kPair>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+// kPair: B's 256 rows are 128 rows of plane 0 (in the even CTA) and the same
+// 128 of plane 1 (gate and up); else 256 consecutive rows.  A tile's operands
+// may each be K-major or MN-major (g.a_mn, g.b_mn): a stage holds 128 rows of
+// 128 bytes along the depth, or two blocks of 64 depths x 64 rows.
+template <class Epi, bool kPair>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const GemmShape g,
                     const Epi epi) {
   constexpr uint32_t kTmemCols = 512;
@@ -240,6 +277,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   GemmTail* tail = reinterpret_cast<GemmTail*>(smem + kGemmStages * kGemmStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int ntiles = g.tiles_m * g.tiles_n;
   Ctl ctl{&tail->abort, g.err, g.wait_ns};
 
@@ -253,7 +292,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->acc_full[b], 1);
-      mbar_init(&tail->acc_empty[b], 4);
+      mbar_init(&tail->acc_empty[b], 8);         // four warps of each CTA
     }
     mbar_init(&tail->mma_done, 1);
     tail->abort = 0u;
@@ -262,13 +301,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tb);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail->tmem_base)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail->tmem_base)),
                  "r"(kTmemCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();                            // the peer's barriers exist
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
 
@@ -279,108 +319,143 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t ph = 0;
       long long iss = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int t = pair; t < ntiles && ok; t += pairs) {
         int tm, tn;
         tile_coords(g, t, tm, tn);
-        const int m0 = tm * kFfnTileM, n0 = tn * (kPair ? 128 : kFfnTileN);
+        const int m0 = tm * kFfnTileM + (int)rank * kGemmHalf;
+        const int n0 = kPair ? tn * kGemmHalf : tn * kFfnTileN + (int)rank * kGemmHalf;
+        const int plane = kPair ? (int)rank : 0;
         for (int k = 0; k < g.kiters; ++k) {
           if (!wait_bar_sleep(&tail->empty[s], ph ^ 1u, ctl, kErrWaitTimeout)) { ok = false; break; }
-          // test hook: CTA 0 leaves out its last chunk, so the waits on it
-          // give up (no copy is left in flight)
-          if (g.withhold && blockIdx.x == 0 && k == g.kiters - 1 && t + (int)gridDim.x >= ntiles) { ok = false; break; }
-          uint8_t* sa = smem + s * kGemmStageBytes;
-          uint8_t* sb = sa + kGemmABytes;
+          // test hook: the first pair leaves out its last chunk, so the waits
+          // on it give up (no copy is left in flight)
+          if (g.withhold && pair == 0 && k == g.kiters - 1 && t + pairs >= ntiles) { ok = false; break; }
+          const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
+          const uint32_t bar = map_cluster(&tail->full[s], 0);
           const int k0 = k * kFfnTileK;
-          mbar_expect_tx(&tail->full[s], kGemmStageBytes);
-          if constexpr (kAMN) {
-#pragma unroll
-            for (int i = 0; i < kFfnTileM / 64; ++i)
-              tma_load_3d(sa + i * 8192, &ta, &tail->full[s], m0 + 64 * i, k0, 0);
+          if (rank == 0) mbar_expect_tx(&tail->full[s], 2 * kGemmStageBytes);   // both CTAs' copies
+          if (g.a_mn) {
+            tma_load_3d_pair(sa, &ta, bar, m0, k0, 0);
+            tma_load_3d_pair(sa + 8192, &ta, bar, m0 + 64, k0, 0);
           } else {
-            tma_load_3d(sa, &ta, &tail->full[s], k0, m0, 0);
+            tma_load_3d_pair(sa, &ta, bar, k0, m0, 0);
           }
-          if constexpr (kBMN) {
-#pragma unroll
-            for (int i = 0; i < kFfnTileN / 64; ++i)
-              tma_load_3d(sb + i * 8192, &tb, &tail->full[s], n0 + 64 * i, k0, 0);
+          if (g.b_mn) {
+            tma_load_3d_pair(sb, &tb, bar, n0, k0, 0);
+            tma_load_3d_pair(sb + 8192, &tb, bar, n0 + 64, k0, 0);
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d(sb + i * 16384, &tb, &tail->full[s], k0, kPair ? n0 : n0 + 128 * i, kPair ? i : 0);
+            tma_load_3d_pair(sb, &tb, bar, k0, n0, plane);
           }
           ++iss;
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
       }
-      for (long long q = 0; q < (iss < kGemmStages ? iss : kGemmStages); ++q) {   // let issued copies land
-        if (--s < 0) { s = kGemmStages - 1; ph ^= 1u; }
-        mbar_drain(&tail->full[s], ph);
+      if (rank == 0) {
+        for (long long q = 0; q < (iss < kGemmStages ? iss : kGemmStages); ++q) {   // let issued copies land
+          if (--s < 0) { s = kGemmStages - 1; ph ^= 1u; }
+          mbar_drain(&tail->full[s], ph);
+        }
+      }
+      if (!ok) {
+        // A wait gave up: copies of this CTA that the even CTA no longer
+        // counts get a millisecond to land before the pair leaves together.
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000ull) __nanosleep(1000);
       }
     }
   } else if (warp == 1) {
     // ===================================================== MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
+      // byte step of sixteen depths, and the distance of the next 64 rows
+      const uint64_t a0 = g.a_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0), b0 = g.b_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0);
+      const uint32_t astep = (g.a_mn ? 2048u : 32u) >> 4, bstep = (g.b_mn ? 2048u : 32u) >> 4;
       int s = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++n) {
+      for (int t = pair; t < ntiles && ok; t += pairs, ++n) {
         const int b = n & 1;
-        if (!wait_bar_sleep(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrWaitTimeout)) break;
+        if (!wait_bar<true>(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrClusterWait)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(b * kFfnTileN);
         for (int k = 0; k < g.kiters; ++k) {
           if (!wait_bar_sleep(&tail->full[s], ph, ctl, kErrWaitTimeout)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmABytes;
+          const uint32_t sa = smem_u32(smem + s * kGemmStageBytes) >> 4, sb = sa + (kGemmOpBytes >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kFfnTileK / 16; ++ks) {
-            const uint64_t da = kAMN ? sw128_desc_mn(sa + ks * 2048, 8192) : sw128_desc(sa + ks * 32);
-            const uint64_t db = kBMN ? sw128_desc_mn(sb + ks * 2048, 8192) : sw128_desc(sb + ks * 32);
-            mma_bf16(d, da, db, g.idesc, (k | ks) ? 1u : 0u);
-          }
-          mma_commit(&tail->empty[s]);
+          for (int ks = 0; ks < kFfnTileK / 16; ++ks)
+            mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), g.idesc, (k | ks) ? 1u : 0u);
+          commit_pair(&tail->empty[s]);
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
-        if (ok) mma_commit(&tail->acc_full[b]);
+        if (ok) commit_pair(&tail->acc_full[b]);
       }
-      mma_commit(&tail->mma_done);
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&tail->mma_done))
+                   : "memory");
       mbar_drain(&tail->mma_done, 0);
     }
   } else {
     // ===================================================== epilogue
     const int grp = (warp - 2) >> 2, q = warp & 3;
+    const uint32_t row0 = (uint32_t)(q * 32);
     int n = 0;
-    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++n) {
+    for (int t = pair; t < ntiles; t += pairs, ++n) {
       if ((n & 1) != grp) continue;
       int tm, tn;
       tile_coords(g, t, tm, tn);
       if (!wait_bar_sleep(&tail->acc_full[grp], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout)) break;
       tc_fence_after();
-      epi.tile(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kFfnTileN), tm * kFfnTileM + q * 32 + lane, tn);
+      epi.tile(tmem_base + (row0 << 16) + (uint32_t)(grp * kFfnTileN),
+               tm * kFfnTileM + (int)rank * kGemmHalf + q * 32 + lane, tn);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tail->acc_empty[grp]);
+      if (lane == 0) mbar_arrive_remote(&tail->acc_empty[grp], 0);
     }
   }
 
-  // ---- teardown
+  // ---- teardown: the pair leaves together
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
   }
 }
 
-template <bool kAMN, bool kBMN, bool kPair, class Epi>
+// Pairs that fit the device at once (some SMs may have no partner), looked up
+// once per kernel and device.
+template <class Kernel>
+int resident_pairs(Kernel* k, int sms) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sms & ~1));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return 0;
+  return n;
+}
+
+template <bool kPair, class Epi>
 cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const GemmShape& g, const Epi& epi, int sms,
                         cudaStream_t s) {
-  auto* k = ffn_gemm_kernel<Epi, kAMN, kBMN, kPair>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+  auto* k = ffn_gemm_kernel<Epi, kPair>;
+  // per device: the shared-memory limit is set and the pairs counted once
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  int pairs = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (pairs == 0) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    if (e != cudaSuccess) return e;
+    pairs = resident_pairs(k, sms);
+    if (pairs == 0) return cudaErrorInvalidConfiguration;
+    if (dev >= 0 && dev < 64) known[dev].store(pairs, std::memory_order_relaxed);
+  }
   const long long tiles = (long long)g.tiles_m * g.tiles_n;
-  k<<<(unsigned)(tiles < sms ? tiles : sms), kGemmThreads, kGemmSmem, s>>>(ta, tb, g, epi);
+  k<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kGemmThreads, kGemmSmem, s>>>(ta, tb, g, epi);
   return cudaGetLastError();
 }
 
