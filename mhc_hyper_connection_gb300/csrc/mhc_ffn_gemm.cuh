@@ -70,6 +70,29 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// Bounded wait of the product loops.  The clock is read only after a few
+// probes have failed (each may sleep in the barrier for a while): reading it at
+// the head of every wait costs more than a stage of products.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, const Ctl& c, uint32_t code, bool cluster) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (cluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (*c.abort) return false;
+      const uint64_t now = now_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > c.wait_ns) {
+        atomicOr(c.err, code);
+        *c.abort = 1u;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, const Ctl& c) {
+  return mbar_test(bar, parity) || wait_slow(bar, parity, c, kErrWaitTimeout, false);
+}
+
 // Tile t of the persistent loop: bands of kBand tile rows, column by column
 // inside a band, so that the CTAs running at one time share operand rows in L2.
 constexpr int kBand = 8;
@@ -326,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int n0 = kPair ? tn * kGemmHalf : tn * kFfnTileN + (int)rank * kGemmHalf;
         const int plane = kPair ? (int)rank : 0;
         for (int k = 0; k < g.kiters; ++k) {
-          if (!wait_bar_sleep(&tail->empty[s], ph ^ 1u, ctl, kErrWaitTimeout)) { ok = false; break; }
+          if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
           // test hook: the first pair leaves out its last chunk, so the waits
           // on it give up (no copy is left in flight)
           if (g.withhold && pair == 0 && k == g.kiters - 1 && t + pairs >= ntiles) { ok = false; break; }
@@ -374,11 +397,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       for (int t = pair; t < ntiles && ok; t += pairs, ++n) {
         const int b = n & 1;
-        if (!wait_bar<true>(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrClusterWait)) break;
+        if (!wait_slow(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrClusterWait, true)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(b * kFfnTileN);
         for (int k = 0; k < g.kiters; ++k) {
-          if (!wait_bar_sleep(&tail->full[s], ph, ctl, kErrWaitTimeout)) { ok = false; break; }
+          if (!wait_stage(&tail->full[s], ph, ctl)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes) >> 4, sb = sa + (kGemmOpBytes >> 4);
 #pragma unroll
