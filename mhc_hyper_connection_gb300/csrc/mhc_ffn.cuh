@@ -10,6 +10,7 @@ namespace mhc {
 struct GemmShape {
   int M, N, K;                 // rows, columns, depth of the product
   int tiles_m, tiles_n, kiters;
+  int band;                    // tile rows walked together, column by column
   uint32_t idesc;
   int a_mn, b_mn;              // operand stored MN-major
   uint32_t* err;               // device error word

@@ -31,7 +31,7 @@ struct GemmTail {
   uint32_t tmem_base;
   uint32_t abort;
 };
-constexpr size_t kGemmSmem = (size_t)kGemmStages * kGemmStageBytes + sizeof(GemmTail) + 1024;
+constexpr size_t kGemmSmem = (size_t)kGemmStages * kGemmStageBytes + 8 * 4096 + sizeof(GemmTail) + 1024;
 
 // The address, in the cluster's shared window, of this CTA's object `p` in
 // CTA `rank`.
@@ -93,13 +93,12 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, const
   return mbar_test(bar, parity) || wait_slow(bar, parity, c, kErrWaitTimeout, false);
 }
 
-// Tile t of the persistent loop: bands of kBand tile rows, column by column
+// Tile t of the persistent loop: bands of g.band tile rows, column by column
 // inside a band, so that the CTAs running at one time share operand rows in L2.
-constexpr int kBand = 8;
 __device__ __forceinline__ void tile_coords(const GemmShape& g, int t, int& tm, int& tn) {
-  const int band = t / (kBand * g.tiles_n), first = band * kBand;
-  const int rows = min(kBand, g.tiles_m - first);
-  const int r = t - band * kBand * g.tiles_n;
+  const int band = t / (g.band * g.tiles_n), first = band * g.band;
+  const int rows = min(g.band, g.tiles_m - first);
+  const int r = t - band * g.band * g.tiles_n;
   tm = first + r % rows;
   tn = r / rows;
 }
@@ -129,24 +128,58 @@ __device__ __forceinline__ uint4 pack8v(const float* f) {
   return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
 }
 
+// A warp's staging buffer: 32 rows (its accumulator lanes) of 128 bytes in the
+// 128-byte swizzle.  A lane holds one row, so writing rows to memory straight
+// from registers would touch 32 distant lines per instruction, 16 bytes each;
+// through the buffer a warp instruction covers whole rows (kept sums of the
+// forward at T = 4096, D = 4096, F = 8192: 573 -> 538 us).
+constexpr int kStageBuf = 4096;
+
+// 32 rows x 128 bytes to memory: row r at base + r * pitch, the first `bytes`
+// (a multiple of 16) of each row, rows below `rows`.
+__device__ __forceinline__ void stage_flush(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int bytes, int lane) {
+  __syncwarp();
+  const int c = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + sw128(r, c));
+    if (r < rows && c * 16 < bytes) *reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16) = v;
+  }
+  __syncwarp();
+}
+// The same for byte rows whose pitch is only a multiple of 8.
+__device__ __forceinline__ void stage_flush8(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int bytes, int lane) {
+  __syncwarp();
+  const int c = lane & 15;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = i * 2 + (lane >> 4);
+    const uint2 v = *reinterpret_cast<const uint2*>(buf + sw128(r, c >> 1) + (c & 1) * 8);
+    if (r < rows && c * 8 < bytes) *reinterpret_cast<uint2*>(base + (size_t)r * pitch + c * 8) = v;
+  }
+  __syncwarp();
+}
+
 // out[row, col] = round(acc)
 template <bool F16>
 struct EpiStore {
   uint16_t* out;
   int M, N;
-  __device__ __forceinline__ void tile(uint32_t taddr, int row, int tn) const {
+  // taddr: the warp's accumulator lanes; row0: the row of its lane 0
+  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
     const int n0 = tn * kFfnTileN;
-    uint16_t* o = out + (size_t)row * N + n0;
 #pragma unroll 1
-    for (int c = 0; c < kFfnTileN && n0 + c < N; c += 32) {
-      float v[32];
-      tmem_ld32(taddr + c, v);
-      if (row < M) {
+    for (int c = 0; c < kFfnTileN && n0 + c < N; c += 64) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n0 + c + 8 * q < N) *reinterpret_cast<uint4*>(o + c + 8 * q) = pack8v<F16>(v + 8 * q);
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32(taddr + c + 32 * h, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + q)) = pack8v<F16>(v + 8 * q);
       }
-      __syncwarp();                              // whole again before the next accumulator load
+      stage_flush(buf, reinterpret_cast<uint8_t*>(out + (size_t)row0 * N + n0 + c), (size_t)N * 2, M - row0,
+                  min(64, N - n0 - c) * 2, lane);
     }
   }
 };
@@ -158,19 +191,46 @@ struct EpiGateUp {
   uint16_t *a, *gate_up;
   uint8_t *codes, *scales;
   int T, F, act;
-  __device__ __forceinline__ void tile(uint32_t taddr, int row, int tn) const {
-    const int f0 = tn * 128;
-    const bool in = row < T;
-    float inv[2] = {1.0f, 1.0f};
+  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+    const int f0 = tn * 128, rows = T - row0;
+#pragma unroll 1
+    for (int c = 0; c < 128 && f0 + c < F; c += 64) {
+      const int bytes = min(64, F - f0 - c) * 2;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        float g[16], u[16];
+        tmem_ld16(taddr + c + 16 * h, g);
+        tmem_ld16(taddr + 128 + c + 16 * h, u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] *= g[e] * sigmoid_fast(act_arg(g[e], act));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 2 + q)) = pack8v<F16>(u + 8 * q);
+      }
+      stage_flush(buf, reinterpret_cast<uint8_t*>(a + (size_t)row0 * F + f0 + c), (size_t)F * 2, rows, bytes, lane);
+      if constexpr (kKept == 1) {
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_ld32(taddr + p * 128 + c + 32 * h, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + q)) = pack8v<F16>(v + 8 * q);
+          }
+          stage_flush(buf, reinterpret_cast<uint8_t*>(gate_up + ((size_t)row0 * 2 + p) * F + f0 + c), (size_t)F * 4, rows,
+                      bytes, lane);
+        }
+      }
+    }
     if constexpr (kKept == 2) {
       const int nblk = (F + kCkptBlock - 1) / kCkptBlock;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p) {
         float amax = 0.0f;                       // columns beyond F hold zeros (or NaN)
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           float v[32];
-          tmem_ld32(taddr + h * 128 + c, v);
+          tmem_ld32(taddr + p * 128 + c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const float m = fabsf(v[e]);
@@ -178,110 +238,160 @@ struct EpiGateUp {
           }
         }
         const int ex = ckpt_exponent<F16>(amax);
-        inv[h] = pow2_f32(-ex);
-        if (in) scales[((size_t)row * 2 + h) * nblk + tn] = (uint8_t)(ex + 127);
-      }
-    }
+        const float inv = pow2_f32(-ex);
+        if (lane < rows) scales[((size_t)(row0 + lane) * 2 + p) * nblk + tn] = (uint8_t)(ex + 127);
 #pragma unroll 1
-    for (int c = 0; c < 128 && f0 + c < F; c += 16) {
-      float g[16], u[16], p[16];
-      tmem_ld16(taddr + c, g);
-      tmem_ld16(taddr + 128 + c, u);
-      if (in) {
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + p * 128 + c, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = g[e] * sigmoid_fast(act_arg(g[e], act)) * u[e];
+          for (int e = 0; e < 32; ++e)
+            v[e] = fabsf(v[e]) < __int_as_float(0x7F800000) ? v[e] * inv : __int_as_float(0x7FFFFFFF);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int f = f0 + c + 8 * q;
-          if (f >= F) break;
-          *reinterpret_cast<uint4*>(a + (size_t)row * F + f) = pack8v<F16>(p + 8 * q);
-          if constexpr (kKept == 1) {
-            *reinterpret_cast<uint4*>(gate_up + ((size_t)row * 2) * F + f) = pack8v<F16>(g + 8 * q);
-            *reinterpret_cast<uint4*>(gate_up + ((size_t)row * 2 + 1) * F + f) = pack8v<F16>(u + 8 * q);
-          }
-          if constexpr (kKept == 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float v = h ? u[8 * q + e] : g[8 * q + e];
-                w[e] = fabsf(v) < __int_as_float(0x7F800000) ? v * inv[h] : __int_as_float(0x7FFFFFFF);
-              }
-              *reinterpret_cast<uint2*>(codes + ((size_t)row * 2 + h) * F + f) =
-                  make_uint2(e4m3x4(w[0], w[1], w[2], w[3]), e4m3x4(w[4], w[5], w[6], w[7]));
-            }
+          for (int q = 0; q < 2; ++q) {
+            const float* w = v + 16 * q;
+            *reinterpret_cast<uint4*>(buf + sw128(lane, (c >> 4) + q)) =
+                make_uint4(e4m3x4(w[0], w[1], w[2], w[3]), e4m3x4(w[4], w[5], w[6], w[7]),
+                           e4m3x4(w[8], w[9], w[10], w[11]), e4m3x4(w[12], w[13], w[14], w[15]));
           }
         }
+        uint8_t* base = codes + ((size_t)row0 * 2 + p) * F + f0;
+        const int bytes = min(128, F - f0);
+        if (F % 16 == 0) stage_flush(buf, base, (size_t)F * 2, rows, bytes, lane);
+        else stage_flush8(buf, base, (size_t)F * 2, rows, bytes, lane);
       }
-      __syncwarp();
     }
   }
 };
 
 // acc = ga: with the kept g and u, gg = ga u act'(g), gu = ga act(g) and
-// a = act(g) u.  act' = s + z s (1 - s) r'(z).
+// a = act(g) u.  act' = s + z s (1 - s) r'(z).  Thirty-two columns at a time:
+// the kept sums come in over the buffer (g in the first half of its 128-byte
+// rows, u in the second), loaded one step ahead.
 template <bool F16, int kKept>
 struct EpiDgate {
   const uint16_t* gate_up;
   const uint8_t *codes, *scales;
   uint16_t *gg, *a;
   int T, F, act;
-  __device__ __forceinline__ void tile(uint32_t taddr, int row, int tn) const {
-    const int f0 = tn * kFfnTileN;
-    const bool in = row < T;
-    const int nblk = (F + kCkptBlock - 1) / kCkptBlock;
-#pragma unroll 1
-    for (int c = 0; c < kFfnTileN && f0 + c < F; c += 16) {
-      float v[16];
-      tmem_ld16(taddr + c, v);
-      if (in) {
+
+  // g and u of columns [f, f + 32) for eight rows per instruction (lane / 4,
+  // eight columns each): 16 bytes, or 8 from codes
+  struct Kept {
+    uint4 v[2][4];
+    uint32_t s[2];
+  };
+  __device__ __forceinline__ void load(Kept& k, int row0, int f, int lane) const {
+    const int c = (lane & 3) * 8;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int f = f0 + c + 8 * q;
-          if (f >= F) break;
-          float k[2][8], o[3][8];
+    for (int p = 0; p < 2; ++p) {
+      k.s[p] = 127;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const size_t r = (size_t)row * 2 + h;
-            if constexpr (kKept == 1) {
-              const uint4 w = *reinterpret_cast<const uint4*>(gate_up + r * F + f);
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 p = unpack2<F16>(ww[e]);
-                k[h][2 * e] = p.x;
-                k[h][2 * e + 1] = p.y;
-              }
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(codes + r * F + f);
-              const float s = ckpt_scale(scales[r * nblk + (f >> 7)]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 p = e4m3x2_f2((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
-                k[h][2 * e] = p.x * s;
-                k[h][2 * e + 1] = p.y * s;
-              }
-            }
+      for (int i = 0; i < 4; ++i) {
+        const int r = row0 + i * 8 + (lane >> 2);
+        k.v[p][i] = make_uint4(0, 0, 0, 0);
+        if (r < T && f + c < F) {
+          const size_t at = ((size_t)r * 2 + p) * F + f + c;
+          if constexpr (kKept == 1) {
+            k.v[p][i] = *reinterpret_cast<const uint4*>(gate_up + at);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(codes + at);
+            k.v[p][i].x = w.x;
+            k.v[p][i].y = w.y;
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = k[0][e], u = k[1][e], ga = v[8 * q + e];
-            const float s = sigmoid_fast(act_arg(z, act));
-            const float dr = act == 0 ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f, z * z, 1.0f);
-            const float h = z * s;
-            const float dh = fmaf(h * (1.0f - s), dr, s);
-            o[0][e] = ga * u * dh;
-            o[1][e] = ga * h;
-            o[2][e] = h * u;
-          }
-          *reinterpret_cast<uint4*>(gg + ((size_t)row * 2) * F + f) = pack8v<F16>(o[0]);
-          *reinterpret_cast<uint4*>(gg + ((size_t)row * 2 + 1) * F + f) = pack8v<F16>(o[1]);
-          *reinterpret_cast<uint4*>(a + (size_t)row * F + f) = pack8v<F16>(o[2]);
         }
       }
-      __syncwarp();
+      if constexpr (kKept == 2) {
+        const int r = row0 + lane;
+        if (r < T && f < F) k.s[p] = scales[((size_t)r * 2 + p) * ((F + kCkptBlock - 1) / kCkptBlock) + (f >> 7)];
+      }
     }
+  }
+
+  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+    const int f0 = tn * kFfnTileN, rows = T - row0;
+    Kept k;
+    load(k, row0, f0, lane);
+#pragma unroll 1
+    for (int c = 0; c < kFfnTileN && f0 + c < F; c += 32) {
+      const int f = f0 + c;
+      __syncwarp();
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(buf + sw128(i * 8 + (lane >> 2), p * 4 + (lane & 3))) = k.v[p][i];
+      const float s0 = ckpt_scale(k.s[0]), s1 = ckpt_scale(k.s[1]);
+      if (c + 32 < kFfnTileN) load(k, row0, f + 32, lane);
+      float ga[32];
+      tmem_ld32(taddr + c, ga);
+      __syncwarp();
+      uint4 o[3][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float z[8], u[8];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint4 w = *reinterpret_cast<const uint4*>(buf + sw128(lane, p * 4 + q));
+          float* d = p ? u : z;
+          if constexpr (kKept == 1) {
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = unpack2<F16>(ww[e]);
+              d[2 * e] = t.x;
+              d[2 * e + 1] = t.y;
+            }
+          } else {
+            const float s = p ? s1 : s0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = e4m3x2_f2((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+              d[2 * e] = t.x * s;
+              d[2 * e + 1] = t.y * s;
+            }
+          }
+        }
+        float og[8], ou[8], oa[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = sigmoid_fast(act_arg(z[e], act));
+          const float dr = act == 0 ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f, z[e] * z[e], 1.0f);
+          const float h = z[e] * s, gae = ga[8 * q + e];
+          og[e] = gae * u[e] * fmaf(h * (1.0f - s), dr, s);
+          ou[e] = gae * h;
+          oa[e] = h * u[e];
+        }
+        o[0][q] = pack8v<F16>(og);
+        o[1][q] = pack8v<F16>(ou);
+        o[2][q] = pack8v<F16>(oa);
+      }
+      __syncwarp();
+      // gg and gu side by side, then a
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        *reinterpret_cast<uint4*>(buf + sw128(lane, q)) = o[0][q];
+        *reinterpret_cast<uint4*>(buf + sw128(lane, 4 + q)) = o[1][q];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), p = (lane >> 2) & 1, cc = (lane & 3) * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + sw128(r, lane & 7));
+        if (r < rows && f + cc < F) *reinterpret_cast<uint4*>(gg + ((size_t)(row0 + r) * 2 + p) * F + f + cc) = v;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, q)) = o[2][q];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), cc = (lane & 3) * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + sw128(r, lane & 3));
+        if (r < rows && f + cc < F) *reinterpret_cast<uint4*>(a + (size_t)(row0 + r) * F + f + cc) = v;
+      }
+    }
+    __syncwarp();
   }
 };
 
@@ -298,7 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  GemmTail* tail = reinterpret_cast<GemmTail*>(smem + kGemmStages * kGemmStageBytes);
+  uint8_t* bufs = smem + kGemmStages * kGemmStageBytes;          // one staging buffer per epilogue warp
+  GemmTail* tail = reinterpret_cast<GemmTail*>(bufs + 8 * kStageBuf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -429,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (!wait_bar_sleep(&tail->acc_full[grp], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout)) break;
       tc_fence_after();
       epi.tile(tmem_base + (row0 << 16) + (uint32_t)(grp * kFfnTileN),
-               tm * kFfnTileM + (int)rank * kGemmHalf + q * 32 + lane, tn);
+               tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, bufs + (warp - 2) * kStageBuf, lane);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(&tail->acc_empty[grp], 0);
