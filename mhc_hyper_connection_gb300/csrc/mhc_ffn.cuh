@@ -19,7 +19,11 @@ struct GemmShape {
   int clear_err;               // first kernel of a call: clear the error word
 };
 
-// Forward: kept = 0 none, 1 16-bit, 2 8-bit.
+// Up to this many tokens the few-token kernels run (mhc_ffn_few.cuh).
+constexpr int kFewTokens = 128;
+
+// Forward: kept = 0 none, 1 16-bit, 2 8-bit.  For few tokens the maps of x and
+// a have boxes of all tokens.
 struct FfnFwdLaunch {
   CUtensorMap x, wgu, a, wd;
   GemmShape gu, down;
@@ -33,6 +37,7 @@ struct FfnBwdLaunch {
   CUtensorMap gg_k, wgu_mn;        // grad_x = [gg, gu] [Wg; Wu]
   CUtensorMap gg_mn, x_mn;         // grad_w_gate_up = [gg, gu]^T x
   CUtensorMap gy_mn, a_mn;         // grad_w_down = grad_y^T a
+  // for few tokens gy_k and gg_k have boxes of all tokens
   GemmShape ga, gx, gwgu, gwd;
   int T, D, F, act, kept, sms;
   const void *gate_up, *codes, *scales;

@@ -154,8 +154,9 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   L.gate_up = a->gate_up;
   L.codes = a->codes;
   L.scales = a->scales;
-  if (!map_2d(&L.x, a->x, f16, D, T, 1, kFfnBoxK) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
-      !map_2d(&L.a, L.a_buf, f16, F, T, 1, kFfnBoxK) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, kFfnBoxK))
+  const uint32_t tok_box = T <= kFewTokens ? (uint32_t)((T + 15) & ~int64_t(15)) : kFfnBoxK;
+  if (!map_2d(&L.x, a->x, f16, D, T, 1, tok_box) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
+      !map_2d(&L.a, L.a_buf, f16, F, T, 1, tok_box) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, kFfnBoxK))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
   L.gu = shape(T, F, D, 128, f16, false, false, err, a->wait_limit_us);
   L.down = shape(T, D, F, kFfnTileN, f16, false, false, err, a->wait_limit_us);
@@ -213,8 +214,9 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
   L.grad_x = a->grad_x;
   L.grad_w_gate_up = a->grad_w_gate_up;
   L.grad_w_down = a->grad_w_down;
-  if (!map_2d(&L.gy_k, a->grad_y, f16, D, T, 1, kFfnBoxK) || !map_2d(&L.wd_mn, a->w_down, f16, F, D, 1, kFfnBoxMn) ||
-      !map_2d(&L.gg_k, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxK) || !map_2d(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, 1, kFfnBoxMn) ||
+  const uint32_t tok_box = T <= kFewTokens ? (uint32_t)((T + 15) & ~int64_t(15)) : kFfnBoxK;
+  if (!map_2d(&L.gy_k, a->grad_y, f16, D, T, 1, tok_box) || !map_2d(&L.wd_mn, a->w_down, f16, F, D, 1, kFfnBoxMn) ||
+      !map_2d(&L.gg_k, L.gg_buf, f16, 2 * F, T, 1, tok_box) || !map_2d(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, 1, kFfnBoxMn) ||
       !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxMn) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, kFfnBoxMn) ||
       !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, kFfnBoxMn) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");

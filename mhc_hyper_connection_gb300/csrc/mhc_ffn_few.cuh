@@ -1,0 +1,369 @@
+// mhc_ffn_few.cuh -- the feed-forward block's products for few tokens (serving,
+// and the backward of small batches).
+//
+// With up to 128 tokens the weights are read once and used little: the bound is
+// HBM.  So the weights are the 128-row side of the tensor-core product and the
+// tokens its N side (a multiple of 16), each CTA streams its own rows of the
+// weights through a ring of up to 200 KB, and where the rows alone do not fill
+// the device, a cluster of 2, 4 or 8 CTAs shares them, each taking a part of
+// the depth; their fp32 sums are joined over distributed shared memory in rank
+// order (no atomics: the same bits every time).
+#pragma once
+
+#include "mhc_ffn_gemm.cuh"
+
+namespace mhc {
+
+constexpr int kFewThreads = 192;                 // producer, MMA issuer, four epilogue warps
+constexpr int kFewRing = 200 * 1024;
+constexpr int kFewMaxStages = 12;
+constexpr int kFewRows = 128;                    // weight rows of one accumulator
+
+struct FewTail {
+  uint64_t full[kFewMaxStages], empty[kFewMaxStages];
+  uint64_t acc_full;
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+constexpr size_t kFewSmem = kFewRing + sizeof(FewTail) + 1024;
+
+struct FewShape {
+  int rows, T;                 // weight rows of one plane (output columns), tokens
+  int nt;                      // tokens rounded up to 16
+  int tiles, kiters, split;    // 128-row tiles, depth chunks, CTAs that share a tile
+  int stages;
+  int a_mn;                    // weights stored MN-major
+  uint32_t idesc;
+  uint32_t* err;
+  uint64_t wait_ns;
+  int withhold, clear_err;
+};
+
+__host__ __device__ constexpr int few_stage_bytes(bool two, int nt) { return (two ? 2 : 1) * 16384 + nt * 128; }
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// ------------------------------------------------------------- epilogues
+// One warp per token; a lane has four consecutive weight rows r of its sums.
+
+template <bool F16>
+__device__ __forceinline__ uint2 pack4(float4 v) {
+  return make_uint2(pack2<F16>(v.x, v.y), pack2<F16>(v.z, v.w));
+}
+
+template <bool F16>
+struct FewStore {
+  static constexpr bool kTwo = false;
+  uint16_t* out;
+  int N;
+  __device__ __forceinline__ void token(int n, int tile, const float4& v, const float4&, int lane) const {
+    const int r = tile * kFewRows + 4 * lane;
+    if (r < N) *reinterpret_cast<uint2*>(out + (size_t)n * N + r) = pack4<F16>(v);
+  }
+};
+
+template <bool F16, int kKept>
+struct FewGateUp {
+  static constexpr bool kTwo = true;
+  uint16_t *a, *gate_up;
+  uint8_t *codes, *scales;
+  int F, act;
+  __device__ __forceinline__ void token(int n, int tile, const float4& g, const float4& u, int lane) const {
+    const int f = tile * kFewRows + 4 * lane;
+    const bool in = f < F;
+    float4 p;
+    p.x = g.x * sigmoid_fast(act_arg(g.x, act)) * u.x;
+    p.y = g.y * sigmoid_fast(act_arg(g.y, act)) * u.y;
+    p.z = g.z * sigmoid_fast(act_arg(g.z, act)) * u.z;
+    p.w = g.w * sigmoid_fast(act_arg(g.w, act)) * u.w;
+    if (in) *reinterpret_cast<uint2*>(a + (size_t)n * F + f) = pack4<F16>(p);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = h ? u : g;
+      const size_t row = (size_t)n * 2 + h;
+      if constexpr (kKept == 1) {
+        if (in) *reinterpret_cast<uint2*>(gate_up + row * F + f) = pack4<F16>(v);
+      }
+      if constexpr (kKept == 2) {
+        const float inf = __int_as_float(0x7F800000), nan = __int_as_float(0x7FFFFFFF);
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        float amax = 0.0f;                       // columns beyond F hold zeros (or NaN)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = fabsf(e[i]) < inf ? fmaxf(amax, fabsf(e[i])) : amax;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const int ex = ckpt_exponent<F16>(amax);
+        const float inv = pow2_f32(-ex);
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = fabsf(e[i]) < inf ? e[i] * inv : nan;
+        if (in) *reinterpret_cast<uint32_t*>(codes + row * F + f) = e4m3x4(w[0], w[1], w[2], w[3]);
+        if (lane == 0) scales[row * ((F + kCkptBlock - 1) / kCkptBlock) + tile] = (uint8_t)(ex + 127);
+      }
+    }
+  }
+};
+
+template <bool F16, int kKept>
+struct FewDgate {
+  static constexpr bool kTwo = false;
+  const uint16_t* gate_up;
+  const uint8_t *codes, *scales;
+  uint16_t *gg, *a;
+  int F, act;
+  __device__ __forceinline__ void token(int n, int tile, const float4& v, const float4&, int lane) const {
+    const int f = tile * kFewRows + 4 * lane;
+    if (f >= F) return;
+    const float ga[4] = {v.x, v.y, v.z, v.w};
+    float k[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const size_t row = (size_t)n * 2 + p;
+      if constexpr (kKept == 1) {
+        const uint2 w = *reinterpret_cast<const uint2*>(gate_up + row * F + f);
+        const float2 lo = unpack2<F16>(w.x), hi = unpack2<F16>(w.y);
+        k[p][0] = lo.x;
+        k[p][1] = lo.y;
+        k[p][2] = hi.x;
+        k[p][3] = hi.y;
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + row * F + f);
+        const float s = ckpt_scale(scales[row * ((F + kCkptBlock - 1) / kCkptBlock) + tile]);
+        const float2 lo = e4m3x2_f2(w), hi = e4m3x2_f2(w >> 16);
+        k[p][0] = lo.x * s;
+        k[p][1] = lo.y * s;
+        k[p][2] = hi.x * s;
+        k[p][3] = hi.y * s;
+      }
+    }
+    float og[4], ou[4], oa[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gate_grads(k[0][e], k[1][e], ga[e], act, og[e], ou[e], oa[e]);
+    *reinterpret_cast<uint2*>(gg + ((size_t)n * 2) * F + f) = pack4<F16>(make_float4(og[0], og[1], og[2], og[3]));
+    *reinterpret_cast<uint2*>(gg + ((size_t)n * 2 + 1) * F + f) = pack4<F16>(make_float4(ou[0], ou[1], ou[2], ou[3]));
+    *reinterpret_cast<uint2*>(a + (size_t)n * F + f) = pack4<F16>(make_float4(oa[0], oa[1], oa[2], oa[3]));
+  }
+};
+
+// ------------------------------------------------------------------ kernel
+
+template <class Epi>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    ffn_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const FewShape g,
+                   const Epi epi) {
+  constexpr bool kTwo = Epi::kTwo;
+  constexpr uint32_t kTmemCols = 256;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FewTail* tail = reinterpret_cast<FewTail*>(smem + kFewRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = g.split > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / g.split;
+  const int k0 = (int)((long long)g.kiters * rank / g.split), k1 = (int)((long long)g.kiters * (rank + 1) / g.split);
+  const int stage_bytes = few_stage_bytes(kTwo, g.nt), stages = g.stages;
+  Ctl ctl{&tail->abort, g.err, g.wait_ns};
+
+  if (threadIdx.x == 0) {
+    if (g.clear_err && blockIdx.x == 0) *g.err = 0u;      // as in ffn_gemm_kernel
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+    }
+    mbar_init(&tail->acc_full, 1);
+    tail->abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tw);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tail->tmem_base;
+
+  if (warp == 0) {
+    // ===================================================== TMA producer
+    if (lane == 0) {
+      int s = 0, iss = 0;
+      uint32_t ph = 0;
+      for (int k = k0; k < k1; ++k) {
+        if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) break;
+        if (g.withhold && blockIdx.x == 0 && k == k1 - 1) break;   // test hook: the last chunk is left out
+        uint8_t* sw = smem + s * stage_bytes;
+        uint8_t* sx = sw + (kTwo ? 2 : 1) * 16384;
+        const int kk = k * kFfnTileK, r0 = tile * kFewRows;
+        mbar_expect_tx(&tail->full[s], (uint32_t)stage_bytes);
+        if (g.a_mn) {
+          tma_load_3d(sw, &tw, &tail->full[s], r0, kk, 0);
+          tma_load_3d(sw + 8192, &tw, &tail->full[s], r0 + 64, kk, 0);
+        } else {
+          tma_load_3d(sw, &tw, &tail->full[s], kk, r0, 0);
+          if (kTwo) tma_load_3d(sw + 16384, &tw, &tail->full[s], kk, r0, 1);
+        }
+        tma_load_3d(sx, &tx, &tail->full[s], kk, 0, 0);
+        ++iss;
+        if (++s == stages) { s = 0; ph ^= 1u; }
+      }
+      for (int q = 0; q < (iss < stages ? iss : stages); ++q) {   // let issued copies land
+        if (--s < 0) { s = stages - 1; ph ^= 1u; }
+        mbar_drain(&tail->full[s], ph);
+      }
+    }
+  } else if (warp == 1) {
+    // ===================================================== MMA issuer
+    if (lane == 0) {
+      const uint64_t w0 = g.a_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0), x0 = sw128_desc(0);
+      const uint32_t wstep = (g.a_mn ? 2048u : 32u) >> 4;
+      int s = 0;
+      uint32_t ph = 0;
+      for (int k = k0; k < k1; ++k) {
+        if (!wait_stage(&tail->full[s], ph, ctl)) break;
+        tc_fence_after();
+        const uint32_t sw = desc_addr(smem + s * stage_bytes), sx = sw + (((kTwo ? 2 : 1) * 16384) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kFfnTileK / 16; ++ks) {
+          const uint32_t acc = (k > k0 || ks) ? 1u : 0u;
+          mma_bf16(tmem_base, w0 + (sw + ks * wstep), x0 + (sx + ks * 2), g.idesc, acc);
+          if (kTwo) mma_bf16(tmem_base + 128, w0 + (sw + 1024 + ks * wstep), x0 + (sx + ks * 2), g.idesc, acc);
+        }
+        mma_commit(&tail->empty[s]);
+        if (++s == stages) { s = 0; ph ^= 1u; }
+      }
+      mma_commit(&tail->acc_full);
+      mbar_drain(&tail->acc_full, 0);
+    }
+  } else {
+    wait_stage(&tail->acc_full, 0, ctl);
+  }
+  // Everything this CTA issued is done: its ring is free for the sums.  An
+  // aborted CTA takes part in the barriers all the same.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (g.split > 1) cluster_sync_all();
+  tc_fence_after();
+
+  // Sums [column][128 rows] in fp32: columns of tokens, then the second
+  // accumulator's.  Ranks above 0 send theirs to rank 0.
+  const int ncols = (kTwo ? 2 : 1) * g.nt;
+  float* fin = reinterpret_cast<float*>(smem);
+  const int q = warp & 3, row = q * 32 + lane;
+  if (warp >= 2 && rank > 0) {
+    const uint32_t dst = map_cluster(fin + (size_t)(rank - 1) * ncols * 128, 0) + (uint32_t)row * 4;
+    for (int c = 0; c < ncols; c += 16) {
+      float v[16];
+      const int col = c < g.nt ? c : 128 + c - g.nt;
+      tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)col, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) st_cluster_f32(dst + (uint32_t)(c + e) * 512, v[e]);
+    }
+  }
+  if (g.split > 1) cluster_sync_all();
+  if (rank == 0) {
+    if (warp >= 2) {
+      for (int c = 0; c < ncols; c += 16) {
+        float v[16];
+        const int col = c < g.nt ? c : 128 + c - g.nt;
+        tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)col, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          for (int r = 1; r < g.split; ++r) v[e] += fin[((size_t)(r - 1) * ncols + c + e) * 128 + row];
+          fin[(size_t)(c + e) * 128 + row] = v[e];      // this thread's own element of the first sent block
+        }
+      }
+    }
+    __syncthreads();
+    for (int n = warp; n < g.T; n += kFewThreads / 32) {
+      const float4 v = *reinterpret_cast<const float4*>(fin + (size_t)n * 128 + 4 * lane);
+      float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (kTwo) u = *reinterpret_cast<const float4*>(fin + (size_t)(g.nt + n) * 128 + 4 * lane);
+      epi.token(n, tile, v, u, lane);
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+  }
+}
+
+// The few-token shape of a product whose weights have `rows` rows.
+inline FewShape few_shape(const GemmShape& g, int rows, int T, bool f16, bool w_mn = false) {
+  FewShape w = {};
+  w.rows = rows;
+  w.T = T;
+  w.nt = (T + 15) & ~15;
+  w.tiles = (rows + kFewRows - 1) / kFewRows;
+  w.kiters = g.kiters;
+  w.a_mn = w_mn ? 1 : 0;
+  w.idesc = f16 ? idesc_f16(kFewRows, w.nt) : idesc_bf16(kFewRows, w.nt);
+  if (w_mn) w.idesc |= 1u << 15;
+  w.err = g.err;
+  w.wait_ns = g.wait_ns;
+  w.withhold = g.withhold;
+  w.clear_err = g.clear_err;
+  return w;
+}
+
+// CTAs per tile: the most that one wave of clusters holds, with four chunks of
+// the depth each at least and room for the sums that are sent.
+template <class Epi>
+cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, int sms, cudaStream_t s) {
+  auto* k = ffn_few_kernel<Epi>;
+  static std::atomic<int> known[64][4];                    // resident clusters of 1, 2, 4, 8 CTAs per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (known[dev][0].load(std::memory_order_acquire) == 0) {
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem)) != cudaSuccess) return e;
+    for (int i = 3; i >= 0; --i) {
+      int n = 0;
+      attr[0].val.clusterDim.x = 1u << i;
+      cfg.gridDim = dim3((unsigned)(sms >> i << i));
+      if ((e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) != cudaSuccess) return e;
+      known[dev][i].store(n < 1 ? 1 : n, std::memory_order_release);
+    }
+  }
+  const int ncols = (Epi::kTwo ? 2 : 1) * g.nt;
+  g.split = 1;
+  for (int i = 1; i < 4; ++i) {
+    const int S = 1 << i;
+    if (g.tiles <= known[dev][i].load(std::memory_order_relaxed) && g.kiters >= 4 * S &&
+        (size_t)(S - 1) * ncols * 512 <= (size_t)kFewRing)
+      g.split = S;
+  }
+  g.stages = kFewRing / few_stage_bytes(Epi::kTwo, g.nt);
+  if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
+  attr[0].val.clusterDim.x = (unsigned)g.split;
+  cfg.gridDim = dim3((unsigned)(g.tiles * g.split));
+  return cudaLaunchKernelEx(&cfg, k, tw, tx, (const FewShape)g, epi);
+}
+
+}  // namespace mhc

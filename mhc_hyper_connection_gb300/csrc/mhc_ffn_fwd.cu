@@ -1,5 +1,5 @@
 // mhc_ffn_fwd.cu -- forward kernels of the gated feed-forward block.
-#include "mhc_ffn_gemm.cuh"
+#include "mhc_ffn_few.cuh"
 
 namespace mhc {
 namespace {
@@ -28,9 +28,34 @@ cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
   return launch_gemm<false>(L.a, L.wd, L.down, o, L.sms, s);
 }
 
+template <bool F16, int kKept>
+cudaError_t few_gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
+  FewGateUp<F16, kKept> e;
+  e.a = static_cast<uint16_t*>(L.a_buf);
+  e.gate_up = static_cast<uint16_t*>(L.gate_up);
+  e.codes = static_cast<uint8_t*>(L.codes);
+  e.scales = static_cast<uint8_t*>(L.scales);
+  e.F = L.F;
+  e.act = L.act;
+  return launch_few(L.wgu, L.x, few_shape(L.gu, L.F, L.T, F16), e, L.sms, s);
+}
+
+template <bool F16>
+cudaError_t forward_few(const FfnFwdLaunch& L, cudaStream_t s) {
+  const cudaError_t e = L.kept == 0   ? few_gate_up<F16, 0>(L, s)
+                        : L.kept == 1 ? few_gate_up<F16, 1>(L, s)
+                                      : few_gate_up<F16, 2>(L, s);
+  if (e != cudaSuccess) return e;
+  FewStore<F16> o;
+  o.out = static_cast<uint16_t*>(L.y);
+  o.N = L.D;
+  return launch_few(L.wd, L.a, few_shape(L.down, L.D, L.T, F16), o, L.sms, s);
+}
+
 }  // namespace
 
 cudaError_t launch_ffn_forward(const FfnFwdLaunch& L, bool f16, cudaStream_t s) {
+  if (L.T <= kFewTokens) return f16 ? forward_few<true>(L, s) : forward_few<false>(L, s);
   return f16 ? forward<true>(L, s) : forward<false>(L, s);
 }
 

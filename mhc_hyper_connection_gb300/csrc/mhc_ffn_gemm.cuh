@@ -60,6 +60,9 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Start-address field of an operand descriptor.  A shared-memory address holds
+// the CTA's rank in its upper bits, which would run into the fields above.
+__device__ __forceinline__ uint32_t desc_addr(const void* p) { return (smem_u32(p) & 0x3FFFFu) >> 4; }
 // Arrive on the barrier at this offset in both CTAs once the products issued
 // so far are done.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
@@ -113,6 +116,16 @@ __device__ __forceinline__ float act_arg(float z, int act) {
   return act == 0 ? z : 1.5957691216f * z * fmaf(0.044715f, z * z, 1.0f);
 }
 __device__ __forceinline__ float sigmoid_fast(float r) { return __fdividef(1.0f, 1.0f + __expf(-r)); }
+
+// gg = ga u act'(z), gu = ga act(z) and a = act(z) u; act' = s + z s (1 - s) r'(z).
+__device__ __forceinline__ void gate_grads(float z, float u, float ga, int act, float& gg, float& gu, float& a) {
+  const float s = sigmoid_fast(act_arg(z, act));
+  const float dr = act == 0 ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f, z * z, 1.0f);
+  const float h = z * s;
+  gg = ga * u * fmaf(h * (1.0f - s), dr, s);
+  gu = ga * h;
+  a = h * u;
+}
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -264,8 +277,7 @@ struct EpiGateUp {
   }
 };
 
-// acc = ga: with the kept g and u, gg = ga u act'(g), gu = ga act(g) and
-// a = act(g) u.  act' = s + z s (1 - s) r'(z).  Thirty-two columns at a time:
+// acc = ga: gg, gu and a from the kept g and u.  Thirty-two columns at a time:
 // the kept sums come in over the buffer (g in the first half of its 128-byte
 // rows, u in the second), loaded one step ahead.
 template <bool F16, int kKept>
@@ -354,14 +366,7 @@ struct EpiDgate {
         }
         float og[8], ou[8], oa[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = sigmoid_fast(act_arg(z[e], act));
-          const float dr = act == 0 ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f, z[e] * z[e], 1.0f);
-          const float h = z[e] * s, gae = ga[8 * q + e];
-          og[e] = gae * u[e] * fmaf(h * (1.0f - s), dr, s);
-          ou[e] = gae * h;
-          oa[e] = h * u[e];
-        }
+        for (int e = 0; e < 8; ++e) gate_grads(z[e], u[e], ga[8 * q + e], act, og[e], ou[e], oa[e]);
         o[0][q] = pack8v<F16>(og);
         o[1][q] = pack8v<F16>(ou);
         o[2][q] = pack8v<F16>(oa);
@@ -514,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (int k = 0; k < g.kiters; ++k) {
           if (!wait_stage(&tail->full[s], ph, ctl)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kGemmStageBytes) >> 4, sb = sa + (kGemmOpBytes >> 4);
+          const uint32_t sa = desc_addr(smem + s * kGemmStageBytes), sb = sa + (kGemmOpBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < kFfnTileK / 16; ++ks)
             mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), g.idesc, (k | ks) ? 1u : 0u);

@@ -129,16 +129,18 @@ def test_backward(cuda_device, T, D, F, kind, act):
         _check_backward(c, kind, act, got, kept)
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64, 96, 111, 128])
 def test_few_tokens(cuda_device, T):
-    """The serving form: every token count up to 64, a depth and a width that
-    do not divide evenly over the blocks that share them."""
-    from mhc_hyper_connection_gb300 import gated_ffn
+    """Few tokens, forward and backward: a depth and a width that do not divide
+    evenly over the blocks that share them, and ones that do."""
+    from mhc_hyper_connection_gb300 import gated_ffn, gated_ffn_backward
     for kind, act, D, F in (("bf16", "silu", 1544, 2056), ("fp16", "gelu", 2048, 1024)):
         c = _case(cuda_device, T, D, F, kind, T)
         for save in (None, "16bit", "8bit"):
             y, kept = gated_ffn(c["x"], c["w"], c["wd"], act=act, save=save)
             _check_forward(c, kind, act, y, kept)
+            if save:
+                _check_backward(c, kind, act, gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept, act=act), kept)
 
 
 def test_large_and_deep(cuda_device):
