@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import NamedTuple, Optional
+from typing import Optional
 
 MHC_OK = 0
 MHC_ERR_NULLPTR = 161001
@@ -263,7 +263,7 @@ def hc_post(x, residual, post, comb, out=None, stream=None):
 
 # ------------------------------------------- 8-bit checkpoints, post-mapping backward
 
-CKPT_BLOCK = 128
+CKPT_BLOCK = 128      # columns that share one scale
 
 
 def mhc_ckpt8_pack_run(rows: int, D: int, dtype: int, x: int, codes: int, scales: int, stream: int = 0) -> int:
@@ -287,152 +287,10 @@ def mhc_post_backward_run(args: MhcPostBwdArgs, stream: int = 0) -> int:
     return library().mhc_post_backward_run(ctypes.byref(args), stream or None)
 
 
-class Ckpt8(NamedTuple):
-    """An 8-bit checkpoint of a 16-bit tensor [..., D]: codes uint8 [..., D] and
-    scales uint8 [..., ceil(D / 128)] (block exponent + 127)."""
-    codes: object
-    scales: object
-
-
-def _stream(stream, device) -> int:
-    """Raw handle of a torch stream, an integer, or torch's current stream."""
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
-    return int(getattr(stream, "cuda_stream", stream))
-
-
-def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return MHC_DTYPE_BF16
-    if t.dtype == torch.float16:
-        return MHC_DTYPE_FP16
-    raise ValueError(f"a bf16 or fp16 tensor is needed (got {t.dtype})")
-
-
-def _want(t, name: str, dtype, shape, device) -> int:
-    """Address of a tensor that must have this dtype, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} "
-                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-    return _ptr(t)
-
-
-def _ckpt_alloc(shape, device) -> Ckpt8:
-    import torch
-    shape = tuple(shape)
-    return Ckpt8(torch.empty(shape, dtype=torch.uint8, device=device),
-                 torch.empty(shape[:-1] + ((shape[-1] + CKPT_BLOCK - 1) // CKPT_BLOCK,), dtype=torch.uint8,
-                             device=device))
-
-
-def _ckpt_ptrs(ckpt, shape, device):
-    import torch
-    shape = torch.Size(shape)
-    blocks = torch.Size(shape[:-1] + ((shape[-1] + CKPT_BLOCK - 1) // CKPT_BLOCK,))
-    return (_want(ckpt.codes, "codes", torch.uint8, shape, device),
-            _want(ckpt.scales, "scales", torch.uint8, blocks, device))
-
-
-def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
-    """The 8-bit checkpoint of x (bf16 or fp16 [..., D], D a multiple of 8):
-    e4m3 codes with one power-of-two scale per 128 columns.  `out` is a Ckpt8
-    to write into.  Raises MhcError on a host-side rejection."""
-    dt = _dtype_code(x)
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    D = x.shape[-1]
-    if out is None:
-        out = _ckpt_alloc(x.shape, x.device)
-    codes, scales = _ckpt_ptrs(out, x.shape, x.device)
-    st = mhc_ckpt8_pack_run(x.numel() // D if D else 0, D, dt, _ptr(x), codes, scales, _stream(stream, x.device))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_ckpt8_pack_run", last_error())
-    return out
-
-
-def ckpt8_restore(ckpt, dtype=None, out=None, stream=None):
-    """The 16-bit tensor a checkpoint stands for (exact; dtype: the type it was
-    packed from, default bf16)."""
-    import torch
-    codes = ckpt.codes
-    if out is None:
-        out = torch.empty(codes.shape, dtype=dtype or torch.bfloat16, device=codes.device)
-    elif out.shape != codes.shape or out.device != codes.device or dtype not in (None, out.dtype):
-        raise ValueError("out must have the shape and device of the codes, and the given dtype")
-    cp, sp = _ckpt_ptrs(ckpt, codes.shape, codes.device)
-    D = codes.shape[-1]
-    st = mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, _dtype_code(out), cp, sp, _ptr(out),
-                               _stream(stream, codes.device))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_ckpt8_restore_run", last_error())
-    return out
-
-
-def _post_shapes(residual_shape, x, post, comb, device):
-    """Checks of the post-mapping's inputs against the residual's shape; (T, n, D)
-    and the addresses of x, post and comb."""
-    import torch
-    lead, (n, D) = residual_shape[:-2], residual_shape[-2:]
-    T = _tokens(lead)
-    return (T, n, D, _want(x, "x", torch.bfloat16, lead + (D,), device),
-            _want(post, "post", torch.float32, lead + (n,), device),
-            _want(comb, "comb", torch.float32, lead + (n, n), device))
-
-
-def hc_post_ckpt(x, residual, post, comb, out=None, ckpt=None, stream=None):
-    """hc_post that also writes the 8-bit checkpoint of its output in the same
-    pass; returns (out, Ckpt8).  Same tensors and layouts as hc_post."""
-    import torch
-    dev = residual.device
-    T, n, D, xp, pp, cp = _post_shapes(residual.shape, x, post, comb, dev)
-    if out is None:
-        out = torch.empty_like(residual)
-    if ckpt is None:
-        ckpt = _ckpt_alloc(residual.shape, dev)
-    codes, scales = _ckpt_ptrs(ckpt, residual.shape, dev)
-    st = mhc_post_ckpt_run(T, n, D, xp, _want(residual, "residual", torch.bfloat16, residual.shape, dev), pp, cp,
-                           _want(out, "out", torch.bfloat16, residual.shape, dev), codes, scales,
-                           _stream(stream, dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_post_ckpt_run", last_error())
-    return out, ckpt
-
-
-def hc_post_backward(grad_out, x, residual, post, comb, grads=None, stream=None):
-    """Backward of hc_post (include/mhc_post_backward.h): grad_out bf16
-    [T, n, D] (or BSND), the forward's x, post and comb, and its residual as
-    bf16 or as a Ckpt8.  Returns {"grad_x", "grad_residual" (bf16),
-    "grad_post", "grad_comb" (fp32)}, written into `grads` when given."""
-    import torch
-    dev, shape = grad_out.device, grad_out.shape
-    T, n, D, xp, pp, cp = _post_shapes(shape, x, post, comb, dev)
-    if grads is None:
-        grads = {"grad_x": torch.empty_like(x), "grad_residual": torch.empty_like(grad_out),
-                 "grad_post": torch.empty_like(post), "grad_comb": torch.empty_like(comb)}
-    a = MhcPostBwdArgs()
-    a.T, a.n, a.D, a.x, a.post, a.comb = T, n, D, xp, pp, cp
-    a.grad_out = _want(grad_out, "grad_out", torch.bfloat16, shape, dev)
-    if isinstance(residual, Ckpt8):
-        a.codes, a.scales = _ckpt_ptrs(residual, shape, dev)
-    else:
-        a.residual = _want(residual, "residual", torch.bfloat16, shape, dev)
-    a.grad_x = _want(grads["grad_x"], "grad_x", torch.bfloat16, x.shape, dev)
-    a.grad_residual = _want(grads["grad_residual"], "grad_residual", torch.bfloat16, shape, dev)
-    a.grad_post = _want(grads["grad_post"], "grad_post", torch.float32, post.shape, dev)
-    a.grad_comb = _want(grads["grad_comb"], "grad_comb", torch.float32, comb.shape, dev)
-    st = mhc_post_backward_run(a, _stream(stream, dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_post_backward_run", last_error())
-    return grads
-
-
 # ------------------------------------------------------- gated feed-forward block
 
 MHC_FFN_SILU = 0
 MHC_FFN_GELU = 1
-_ACTS = {"silu": MHC_FFN_SILU, "gelu": MHC_FFN_GELU}
 
 
 def mhc_ffn_workspace_size(T: int, D: int, F: int):
@@ -457,125 +315,6 @@ def mhc_ffn_backward_run(args: MhcFfnBwdArgs, stream: int = 0) -> int:
 
 def mhc_ffn_status(workspace: int = 0, stream: int = 0) -> int:
     return library().mhc_ffn_status(workspace or None, stream or None)
-
-
-def gated_ffn_workspace(T: int, D: int, F: int, device, backward: bool = False):
-    """Scratch (uint8) that gated_ffn, or with backward=True
-    gated_ffn_backward, takes for T tokens: for callers that keep one buffer
-    over calls or want to read its status afterwards."""
-    import torch
-    st, n = (mhc_ffn_backward_workspace_size if backward else mhc_ffn_workspace_size)(T, D, F)
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_ffn_backward_workspace_size" if backward else "mhc_ffn_workspace_size", last_error())
-    ws = torch.empty((max(n, 256),), dtype=torch.uint8, device=device)
-    ws[:256].zero_()
-    return ws
-
-
-def gated_ffn_status(workspace=None, stream=None) -> int:
-    """Waits for `stream` (default: torch's current stream), then the device
-    status of the last call that used `workspace`."""
-    dev = None if workspace is None else workspace.device
-    return mhc_ffn_status(_ptr(workspace) or 0, _stream(stream, dev))
-
-
-def _ffn_scratch(nbytes: int, device, raw_stream: int, own_stream: bool):
-    """Scratch for one call; when it runs on another stream than torch's
-    current one, the allocator is told so."""
-    import torch
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    if not own_stream:
-        ws.record_stream(torch.cuda.ExternalStream(raw_stream, device=device))
-    return ws
-
-
-def _ffn_common(a, x, w_gate_up, w_down, act):
-    """Fill the fields that both directions share; (lead dims, device)."""
-    import torch
-    if act not in _ACTS:
-        raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
-    a.dtype, a.act = _dtype_code(x), _ACTS[act]
-    lead, D = x.shape[:-1], x.shape[-1]
-    if w_gate_up.dim() != 3 or w_gate_up.shape[0] != 2:
-        raise ValueError("w_gate_up must be [2, F, D]")
-    F = w_gate_up.shape[1]
-    a.T, a.D, a.F = _tokens(lead), D, F
-    a.x = _ptr(x)
-    a.w_gate_up = _want(w_gate_up, "w_gate_up", x.dtype, torch.Size((2, F, D)), x.device)
-    a.w_down = _want(w_down, "w_down", x.dtype, torch.Size((D, F)), x.device)
-    return lead, x.device
-
-
-def _ffn_workspace(a, size, name, workspace, device, stream):
-    """Raw stream and the workspace tensor (kept alive by the caller)."""
-    raw = _stream(stream, device)
-    if workspace is None:
-        st, n = size(a.T, a.D, a.F)
-        if st != MHC_OK:
-            raise MhcError(st, name, last_error())
-        workspace = _ffn_scratch(n, device, raw, stream is None) if n else None
-    if workspace is not None:
-        a.workspace = _ptr(workspace)
-        a.workspace_bytes = workspace.numel() * workspace.element_size()
-    return raw, workspace
-
-
-def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, workspace=None, stream=None):
-    """y = (act(x Wg^T) (.) x Wu^T) Wd^T (include/mhc_ffn.h): x bf16 or fp16
-    [T, D] (or [B, S, D]), w_gate_up [2, F, D] (Wg, Wu), w_down [D, F], act
-    "silu" or "gelu" (tanh form).  save keeps both projections for the
-    backward: "16bit" as a tensor [T, 2, F], "8bit" as a Ckpt8 of that shape.
-    Returns (y, kept); kept is None without save.  y, kept and workspace are
-    allocated unless given."""
-    import torch
-    a = MhcFfnArgs()
-    lead, dev = _ffn_common(a, x, w_gate_up, w_down, act)
-    shape = lead + (2, a.F)
-    if save == "16bit":
-        if kept is None:
-            kept = torch.empty(shape, dtype=x.dtype, device=dev)
-        a.gate_up = _want(kept, "kept", x.dtype, shape, dev)
-    elif save == "8bit":
-        if kept is None:
-            kept = _ckpt_alloc(shape, dev)
-        a.codes, a.scales = _ckpt_ptrs(kept, shape, dev)
-    elif save is not None or kept is not None:
-        raise ValueError('save must be None, "16bit" or "8bit" (and kept given only with it)')
-    if y is None:
-        y = torch.empty_like(x)
-    a.y = _want(y, "y", x.dtype, x.shape, dev)
-    raw, workspace = _ffn_workspace(a, mhc_ffn_workspace_size, "mhc_ffn_workspace_size", workspace, dev, stream)
-    st = mhc_ffn_run(a, raw)
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_ffn_run", last_error())
-    return y, kept
-
-
-def gated_ffn_backward(grad_y, x, w_gate_up, w_down, kept, act="silu", grads=None, workspace=None, stream=None):
-    """Backward of gated_ffn from what it kept (a tensor or a Ckpt8): returns
-    {"grad_x", "grad_w_gate_up", "grad_w_down"} in x's type, written into
-    `grads` when given."""
-    import torch
-    a = MhcFfnBwdArgs()
-    lead, dev = _ffn_common(a, x, w_gate_up, w_down, act)
-    a.grad_y = _want(grad_y, "grad_y", x.dtype, x.shape, dev)
-    shape = lead + (2, a.F)
-    if isinstance(kept, Ckpt8):
-        a.codes, a.scales = _ckpt_ptrs(kept, shape, dev)
-    else:
-        a.gate_up = _want(kept, "kept", x.dtype, shape, dev)
-    if grads is None:
-        grads = {"grad_x": torch.empty_like(x), "grad_w_gate_up": torch.empty_like(w_gate_up),
-                 "grad_w_down": torch.empty_like(w_down)}
-    a.grad_x = _want(grads["grad_x"], "grad_x", x.dtype, x.shape, dev)
-    a.grad_w_gate_up = _want(grads["grad_w_gate_up"], "grad_w_gate_up", x.dtype, w_gate_up.shape, dev)
-    a.grad_w_down = _want(grads["grad_w_down"], "grad_w_down", x.dtype, w_down.shape, dev)
-    raw, workspace = _ffn_workspace(a, mhc_ffn_backward_workspace_size, "mhc_ffn_backward_workspace_size", workspace,
-                                    dev, stream)
-    st = mhc_ffn_backward_run(a, raw)
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_ffn_backward_run", last_error())
-    return grads
 
 
 def mhc_pre_backward_workspace_size(handle, T: int):

@@ -6,6 +6,8 @@
 // bytes an output element to what it moves anyway.  A block of 128 columns is
 // 16 lanes of eight elements, so its maximum takes four shuffles on packed
 // 16-bit pairs and each lane turns its own 16 bytes into 8.
+#include <atomic>
+
 #include "mhc_ckpt.cuh"
 #include "mhc_host.cuh"
 #include "../../include/mhc_ckpt.h"
@@ -184,13 +186,21 @@ __global__ void __launch_bounds__(kCkptThreads)
 template <int NS>
 cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* res, const float* post,
                              const float* comb, void* out, void* codes, void* scales, cudaStream_t s) {
-  int dev = 0, per_sm = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, post_ckpt_kernel<NS>, kCkptThreads, 0)) != cudaSuccess)
-    return e;
-  const DeviceInfo di = device_info(dev);
-  long long grid = (long long)(di.sms > 0 ? di.sms : 1) * (per_sm > 0 ? per_sm : 1);
+  // CTAs that the device holds at once, looked up once per device
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int resident = known[dev].load(std::memory_order_relaxed);
+  if (resident == 0) {
+    int per_sm = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, post_ckpt_kernel<NS>, kCkptThreads, 0)) != cudaSuccess)
+      return e;
+    resident = (per_sm > 0 ? per_sm : 1) * (device_info(dev).sms > 0 ? device_info(dev).sms : 1);
+    known[dev].store(resident, std::memory_order_relaxed);
+  }
+  long long grid = resident;
   const long long need = (T * 32 + kCkptThreads - 1) / kCkptThreads;
   if (grid > need) grid = need;
   post_ckpt_kernel<NS><<<(int)grid, kCkptThreads, 0, s>>>(
