@@ -4,10 +4,15 @@
 // With up to 128 tokens the weights are read once and used little: the bound is
 // HBM.  So the weights are the 128-row side of the tensor-core product and the
 // tokens its N side (a multiple of 16), each CTA streams its own rows of the
-// weights through a ring of up to 200 KB, and where the rows alone do not fill
-// the device, a cluster of 2, 4 or 8 CTAs shares them, each taking a part of
-// the depth; their fp32 sums are joined over distributed shared memory in rank
-// order (no atomics: the same bits every time).
+// weights through a ring of stages, and where the rows alone do not fill the
+// device, a cluster of 2, 4 or 8 CTAs shares them, each taking a part of the
+// depth.  Their fp32 sums are exchanged over distributed shared memory: each
+// CTA gets all parts of its share of the tokens, adds them in rank order (no
+// atomics: the same bits every time) and finishes those tokens.
+//
+// A product starts while the one before it still runs (programmatic dependent
+// launch): the rings are sized so that CTAs of both fit an SM, and the weights'
+// first chunks are loaded before the wait for the tokens.
 #pragma once
 
 #include "mhc_ffn_gemm.cuh"
@@ -15,7 +20,9 @@
 namespace mhc {
 
 constexpr int kFewThreads = 192;                 // producer, MMA issuer, four epilogue warps
-constexpr int kFewRing = 200 * 1024;
+constexpr int kFewRingTwo = 144 * 1024;          // ring of the gate and up product
+constexpr int kFewRingOne = 76 * 1024;           // ring of the others, beside it on one SM
+constexpr int kFewMinStages = 3;
 constexpr int kFewMaxStages = 12;
 constexpr int kFewRows = 128;                    // weight rows of one accumulator
 
@@ -25,18 +32,18 @@ struct FewTail {
   uint32_t tmem_base;
   uint32_t abort;
 };
-constexpr size_t kFewSmem = kFewRing + sizeof(FewTail) + 1024;
 
 struct FewShape {
   int rows, T;                 // weight rows of one plane (output columns), tokens
   int nt;                      // tokens rounded up to 16
   int tiles, kiters, split;    // 128-row tiles, depth chunks, CTAs that share a tile
-  int stages;
+  int stages, ring;            // stages and bytes of the ring
   int a_mn;                    // weights stored MN-major
   uint32_t idesc;
   uint32_t* err;
   uint64_t wait_ns;
-  int withhold, clear_err;
+  int withhold;
+  int first;                   // first product of a call: clears the error word, waits for nothing
 };
 
 __host__ __device__ constexpr int few_stage_bytes(bool two, int nt) { return (two ? 2 : 1) * 16384 + nt * 128; }
@@ -164,16 +171,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr uint32_t kTmemCols = 256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  FewTail* tail = reinterpret_cast<FewTail*>(smem + kFewRing);
+  FewTail* tail = reinterpret_cast<FewTail*>(smem + g.ring);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = g.split > 1 ? (int)cluster_rank() : 0;
   const int tile = blockIdx.x / g.split;
   const int k0 = (int)((long long)g.kiters * rank / g.split), k1 = (int)((long long)g.kiters * (rank + 1) / g.split);
   const int stage_bytes = few_stage_bytes(kTwo, g.nt), stages = g.stages;
   Ctl ctl{&tail->abort, g.err, g.wait_ns};
+  static_assert(kFewRingTwo >= 2 * 128 * 512 && kFewRingOne >= 128 * 512, "the ring holds the sums of 128 tokens");
 
   if (threadIdx.x == 0) {
-    if (g.clear_err && blockIdx.x == 0) *g.err = 0u;      // as in ffn_gemm_kernel
+    if (g.first && blockIdx.x == 0) *g.err = 0u;          // as in ffn_gemm_kernel
     for (int s = 0; s < stages; ++s) {
       mbar_init(&tail->full[s], 1);
       mbar_init(&tail->empty[s], 1);
@@ -194,27 +202,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
+  pdl_trigger();
 
   if (warp == 0) {
     // ===================================================== TMA producer
     if (lane == 0) {
       int s = 0, iss = 0;
       uint32_t ph = 0;
-      for (int k = k0; k < k1; ++k) {
-        if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) break;
-        if (g.withhold && blockIdx.x == 0 && k == k1 - 1) break;   // test hook: the last chunk is left out
-        uint8_t* sw = smem + s * stage_bytes;
-        uint8_t* sx = sw + (kTwo ? 2 : 1) * 16384;
-        const int kk = k * kFfnTileK, r0 = tile * kFewRows;
-        mbar_expect_tx(&tail->full[s], (uint32_t)stage_bytes);
+      const int r0 = tile * kFewRows;
+      // the weights of a chunk into its stage, which then expects the tokens too
+      auto weights = [&](int k, int st) {
+        uint8_t* sw = smem + st * stage_bytes;
+        const int kk = k * kFfnTileK;
+        mbar_expect_tx(&tail->full[st], (uint32_t)stage_bytes);
         if (g.a_mn) {
-          tma_load_3d(sw, &tw, &tail->full[s], r0, kk, 0);
-          tma_load_3d(sw + 8192, &tw, &tail->full[s], r0 + 64, kk, 0);
+          tma_load_3d(sw, &tw, &tail->full[st], r0, kk, 0);
+          tma_load_3d(sw + 8192, &tw, &tail->full[st], r0 + 64, kk, 0);
         } else {
-          tma_load_3d(sw, &tw, &tail->full[s], kk, r0, 0);
-          if (kTwo) tma_load_3d(sw + 16384, &tw, &tail->full[s], kk, r0, 1);
+          tma_load_3d(sw, &tw, &tail->full[st], kk, r0, 0);
+          if (kTwo) tma_load_3d(sw + 16384, &tw, &tail->full[st], kk, r0, 1);
         }
-        tma_load_3d(sx, &tx, &tail->full[s], kk, 0, 0);
+      };
+      auto tokens = [&](int k, int st) {
+        tma_load_3d(smem + st * stage_bytes + (kTwo ? 2 : 1) * 16384, &tx, &tail->full[st], k * kFfnTileK, 0, 0);
+      };
+      // test hook: the first CTA leaves out its last chunk
+      const int kend = g.withhold && blockIdx.x == 0 ? k1 - 1 : k1;
+      const int early = min(stages, kend - k0);
+      if (!g.first) {
+        for (int k = 0; k < early; ++k) weights(k0 + k, k);
+        pdl_wait();                              // the tokens are the previous product's
+      }
+      for (int k = k0; k < kend; ++k) {
+        if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) break;
+        if (g.first || k - k0 >= early) weights(k, s);
+        tokens(k, s);
         ++iss;
         if (++s == stages) { s = 0; ph ^= 1u; }
       }
@@ -257,42 +279,49 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (g.split > 1) cluster_sync_all();
   tc_fence_after();
 
-  // Sums [column][128 rows] in fp32: columns of tokens, then the second
-  // accumulator's.  Ranks above 0 send theirs to rank 0.
-  const int ncols = (kTwo ? 2 : 1) * g.nt;
-  float* fin = reinterpret_cast<float*>(smem);
-  const int q = warp & 3, row = q * 32 + lane;
-  if (warp >= 2 && rank > 0) {
-    const uint32_t dst = map_cluster(fin + (size_t)(rank - 1) * ncols * 128, 0) + (uint32_t)row * 4;
+  // Exchange: rank d finishes tokens [d per, (d + 1) per).  Every CTA sends its
+  // sums of them, [plane][token][128 rows] in fp32, to block `rank` of d's ring.
+  const int per = g.nt / g.split, ncols = (kTwo ? 2 : 1) * g.nt;
+  const int block = (kTwo ? 2 : 1) * per * 128;            // fp32 values of one CTA's sums
+  float* ring = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int q = warp & 3;
+    const float* mine = ring + (size_t)rank * block + q * 32 + lane;
     for (int c = 0; c < ncols; c += 16) {
       float v[16];
-      const int col = c < g.nt ? c : 128 + c - g.nt;
-      tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)col, v);
+      const int plane = c < g.nt ? 0 : 1, n0 = c - plane * g.nt;
+      tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(plane * 128 + n0), v);
+      if (g.split == 1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) st_cluster_f32(dst + (uint32_t)(c + e) * 512, v[e]);
-    }
-  }
-  if (g.split > 1) cluster_sync_all();
-  if (rank == 0) {
-    if (warp >= 2) {
-      for (int c = 0; c < ncols; c += 16) {
-        float v[16];
-        const int col = c < g.nt ? c : 128 + c - g.nt;
-        tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)col, v);
+        for (int e = 0; e < 16; ++e) const_cast<float*>(mine)[(size_t)(c + e) * 128] = v[e];
+      } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          for (int r = 1; r < g.split; ++r) v[e] += fin[((size_t)(r - 1) * ncols + c + e) * 128 + row];
-          fin[(size_t)(c + e) * 128 + row] = v[e];      // this thread's own element of the first sent block
+          const int n = n0 + e, d = n / per;
+          st_cluster_f32(map_cluster(mine + (size_t)(plane * per + n - d * per) * 128, (uint32_t)d), v[e]);
         }
       }
     }
-    __syncthreads();
-    for (int n = warp; n < g.T; n += kFewThreads / 32) {
-      const float4 v = *reinterpret_cast<const float4*>(fin + (size_t)n * 128 + 4 * lane);
-      float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (kTwo) u = *reinterpret_cast<const float4*>(fin + (size_t)(g.nt + n) * 128 + 4 * lane);
-      epi.token(n, tile, v, u, lane);
+  }
+  if (g.split > 1) cluster_sync_all();
+  else __syncthreads();
+  pdl_wait();                                    // outputs may be what earlier launches still read
+  for (int n = warp; n < per && rank * per + n < g.T; n += kFewThreads / 32) {
+    const float* at = ring + (size_t)n * 128 + 4 * lane;
+    float4 v[2];
+#pragma unroll
+    for (int p = 0; p < (kTwo ? 2 : 1); ++p) {
+      v[p] = *reinterpret_cast<const float4*>(at + (size_t)p * per * 128);
+      for (int r = 1; r < g.split; ++r) {
+        const float4 w = *reinterpret_cast<const float4*>(at + (size_t)r * block + (size_t)p * per * 128);
+        v[p].x += w.x;
+        v[p].y += w.y;
+        v[p].z += w.z;
+        v[p].w += w.w;
+      }
     }
+    if (!kTwo) v[1] = v[0];
+    epi.token(rank * per + n, tile, v[0], v[1], lane);
   }
 
   // ---- teardown
@@ -318,51 +347,47 @@ inline FewShape few_shape(const GemmShape& g, int rows, int T, bool f16, bool w_
   w.err = g.err;
   w.wait_ns = g.wait_ns;
   w.withhold = g.withhold;
-  w.clear_err = g.clear_err;
+  w.first = g.clear_err;
   return w;
 }
 
-// CTAs per tile: the most that one wave of clusters holds, with four chunks of
-// the depth each at least and room for the sums that are sent.
+// CTAs per tile: the most that give every SM one, with four chunks of the
+// depth each at least.
 template <class Epi>
 cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, int sms, cudaStream_t s) {
   auto* k = ffn_few_kernel<Epi>;
-  static std::atomic<int> known[64][4];                    // resident clusters of 1, 2, 4, 8 CTAs per device
+  const int stage = few_stage_bytes(Epi::kTwo, g.nt);
+  g.ring = Epi::kTwo ? kFewRingTwo : kFewRingOne;
+  if (g.ring < kFewMinStages * stage) g.ring = kFewMinStages * stage;
+  g.stages = g.ring / stage;
+  if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
+  g.split = 1;
+  while (g.split < 8 && g.tiles * g.split * 2 <= sms && g.kiters >= 8 * g.split) g.split *= 2;
+  const size_t smem = (size_t)g.ring + sizeof(FewTail) + 1024;
+
+  static std::atomic<bool> known[64];                      // per device: the shared-memory limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!known[dev].load(std::memory_order_relaxed)) {
+    const int most = 200 * 1024;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+    known[dev].store(true, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)g.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(g.tiles * g.split));
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (known[dev][0].load(std::memory_order_acquire) == 0) {
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem)) != cudaSuccess) return e;
-    for (int i = 3; i >= 0; --i) {
-      int n = 0;
-      attr[0].val.clusterDim.x = 1u << i;
-      cfg.gridDim = dim3((unsigned)(sms >> i << i));
-      if ((e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) != cudaSuccess) return e;
-      known[dev][i].store(n < 1 ? 1 : n, std::memory_order_release);
-    }
-  }
-  const int ncols = (Epi::kTwo ? 2 : 1) * g.nt;
-  g.split = 1;
-  for (int i = 1; i < 4; ++i) {
-    const int S = 1 << i;
-    if (g.tiles <= known[dev][i].load(std::memory_order_relaxed) && g.kiters >= 4 * S &&
-        (size_t)(S - 1) * ncols * 512 <= (size_t)kFewRing)
-      g.split = S;
-  }
-  g.stages = kFewRing / few_stage_bytes(Epi::kTwo, g.nt);
-  if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
-  attr[0].val.clusterDim.x = (unsigned)g.split;
-  cfg.gridDim = dim3((unsigned)(g.tiles * g.split));
+  cfg.numAttrs = g.first ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, k, tw, tx, (const FewShape)g, epi);
 }
 

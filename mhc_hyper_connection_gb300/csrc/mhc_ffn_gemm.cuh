@@ -33,6 +33,11 @@ struct GemmTail {
 };
 constexpr size_t kGemmSmem = (size_t)kGemmStages * kGemmStageBytes + 8 * 4096 + sizeof(GemmTail) + 1024;
 
+// Programmatic dependent launch: let the next launch of the stream begin; wait
+// until the launches before this one are complete and their writes visible.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The address, in the cluster's shared window, of this CTA's object `p` in
 // CTA `rank`.
 __device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
