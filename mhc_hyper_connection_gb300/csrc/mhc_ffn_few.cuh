@@ -38,6 +38,7 @@ struct FewShape {
   int nt;                      // tokens rounded up to 16
   int tiles, kiters, split;    // 128-row tiles, depth chunks, CTAs that share a tile
   int stages, ring;            // stages and bytes of the ring
+  int own_room;                // the exchanged sums lie behind the ring, not in it
   int a_mn;                    // weights stored MN-major
   uint32_t idesc;
   uint32_t* err;
@@ -47,6 +48,11 @@ struct FewShape {
 };
 
 __host__ __device__ constexpr int few_stage_bytes(bool two, int nt) { return (two ? 2 : 1) * 16384 + nt * 128; }
+// Tokens that each of `split` CTAs finishes: an equal share, in fours.
+__host__ __device__ constexpr int few_share(int nt, int split) { return (nt / split + 3) & ~3; }
+__host__ __device__ constexpr int few_room_bytes(bool two, int nt, int split) {
+  return (two ? 2 : 1) * split * few_share(nt, split) * 512;
+}
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
@@ -55,9 +61,12 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Place of a row's 16 bytes: eight rows four apart lie in eight different
+// sixteen-byte columns of the banks, and so do eight rows in sequence.
+__device__ __forceinline__ int swz_row(int r) { return r ^ ((r >> 3) & 3); }
 
 // ------------------------------------------------------------- epilogues
 // One warp per token; a lane has four consecutive weight rows r of its sums.
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr uint32_t kTmemCols = 256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  FewTail* tail = reinterpret_cast<FewTail*>(smem + g.ring);
+  FewTail* tail = reinterpret_cast<FewTail*>(smem + g.ring + (g.own_room ? few_room_bytes(kTwo, g.nt, g.split) : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = g.split > 1 ? (int)cluster_rank() : 0;
   const int tile = blockIdx.x / g.split;
@@ -179,6 +188,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int stage_bytes = few_stage_bytes(kTwo, g.nt), stages = g.stages;
   Ctl ctl{&tail->abort, g.err, g.wait_ns};
   static_assert(kFewRingTwo >= 2 * 128 * 512 && kFewRingOne >= 128 * 512, "the ring holds the sums of 128 tokens");
+  static_assert(few_room_bytes(false, 48, 8) <= kFewRingOne && few_room_bytes(true, 112, 8) <= kFewRingTwo,
+                "and of fewer, with shares rounded up");
 
   if (threadIdx.x == 0) {
     if (g.first && blockIdx.x == 0) *g.err = 0u;          // as in ffn_gemm_kernel
@@ -203,6 +214,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
   pdl_trigger();
+  if (g.split > 1) cluster_arrive();             // waited for before the first remote store
 
   if (warp == 0) {
     // ===================================================== TMA producer
@@ -271,57 +283,73 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else {
     wait_stage(&tail->acc_full, 0, ctl);
   }
-  // Everything this CTA issued is done: its ring is free for the sums.  An
-  // aborted CTA takes part in the barriers all the same.
+  // Everything this CTA issued is done.  Where the sums have no room of their
+  // own they go into the rings, which then have to be idle in the whole cluster.
+  // An aborted CTA takes part in the barriers all the same.
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (g.split > 1) cluster_sync_all();
+  if (g.split > 1) {
+    cluster_wait();                              // of the arrival at the start: every CTA is there
+    if (!g.own_room) cluster_sync_all();
+  }
   tc_fence_after();
 
   // Exchange: rank d finishes tokens [d per, (d + 1) per).  Every CTA sends its
-  // sums of them, [plane][token][128 rows] in fp32, to block `rank` of d's ring.
-  const int per = g.nt / g.split, ncols = (kTwo ? 2 : 1) * g.nt;
+  // fp32 sums of them to block `rank` of d's room: [plane][token / 4][row][4
+  // tokens], rows swizzled so that both the lanes' writes (a row each) and
+  // their reads (four rows each) spread over the banks.
+  const int per = few_share(g.nt, g.split), ncols = (kTwo ? 2 : 1) * g.nt;
   const int block = (kTwo ? 2 : 1) * per * 128;            // fp32 values of one CTA's sums
-  float* ring = reinterpret_cast<float*>(smem);
+  float* room = reinterpret_cast<float*>(smem + (g.own_room ? g.ring : 0));
   if (warp >= 2) {
     const int q = warp & 3;
-    const float* mine = ring + (size_t)rank * block + q * 32 + lane;
+    float* mine = room + (size_t)rank * block + swz_row(q * 32 + lane) * 4;
     for (int c = 0; c < ncols; c += 16) {
       float v[16];
       const int plane = c < g.nt ? 0 : 1, n0 = c - plane * g.nt;
       tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(plane * 128 + n0), v);
-      if (g.split == 1) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) const_cast<float*>(mine)[(size_t)(c + e) * 128] = v[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int n = n0 + e, d = n / per;
-          st_cluster_f32(map_cluster(mine + (size_t)(plane * per + n - d * per) * 128, (uint32_t)d), v[e]);
-        }
+      for (int e = 0; e < 16; e += 4) {
+        const int n = n0 + e, d = n / per;
+        float* at = mine + (size_t)(plane * per + n - d * per) * 128;
+        const float4 w = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        if (g.split == 1) *reinterpret_cast<float4*>(at) = w;
+        else st_dsmem_v4(at, (uint32_t)d, w);
       }
     }
   }
   if (g.split > 1) cluster_sync_all();
   else __syncthreads();
   pdl_wait();                                    // outputs may be what earlier launches still read
-  for (int n = warp; n < per && rank * per + n < g.T; n += kFewThreads / 32) {
-    const float* at = ring + (size_t)n * 128 + 4 * lane;
-    float4 v[2];
+  for (int n = warp * 4; n < per && rank * per + n < g.T; n += 4 * (kFewThreads / 32)) {
+    float m[2][4][4];                            // [plane][row][token]
 #pragma unroll
     for (int p = 0; p < (kTwo ? 2 : 1); ++p) {
-      v[p] = *reinterpret_cast<const float4*>(at + (size_t)p * per * 128);
-      for (int r = 1; r < g.split; ++r) {
-        const float4 w = *reinterpret_cast<const float4*>(at + (size_t)r * block + (size_t)p * per * 128);
-        v[p].x += w.x;
-        v[p].y += w.y;
-        v[p].z += w.z;
-        v[p].w += w.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* at = room + (size_t)(p * per + n) * 128 + swz_row(4 * lane + i) * 4;
+        float4 v = *reinterpret_cast<const float4*>(at);
+        for (int r = 1; r < g.split; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(at + (size_t)r * block);
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
+        }
+        m[p][i][0] = v.x;
+        m[p][i][1] = v.y;
+        m[p][i][2] = v.z;
+        m[p][i][3] = v.w;
       }
     }
-    if (!kTwo) v[1] = v[0];
-    epi.token(rank * per + n, tile, v[0], v[1], lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (rank * per + n + t >= g.T) break;
+      const float4 v = make_float4(m[0][0][t], m[0][1][t], m[0][2][t], m[0][3][t]);
+      const float4 u = kTwo ? make_float4(m[1][0][t], m[1][1][t], m[1][2][t], m[1][3][t]) : v;
+      epi.token(rank * per + n + t, tile, v, u, lane);
+    }
   }
 
   // ---- teardown
@@ -362,8 +390,14 @@ cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g,
   g.stages = g.ring / stage;
   if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
   g.split = 1;
-  while (g.split < 8 && g.tiles * g.split * 2 <= sms && g.kiters >= 8 * g.split) g.split *= 2;
-  const size_t smem = (size_t)g.ring + sizeof(FewTail) + 1024;
+  while (g.split < 8 && g.tiles * g.split * 2 <= (Epi::kTwo ? 1 : 2) * sms && g.kiters >= 8 * g.split) g.split *= 2;
+  g.own_room = g.nt <= 32;
+  if (g.own_room) {                                        // within the same total
+    g.ring -= few_room_bytes(Epi::kTwo, g.nt, g.split);
+    if (g.ring < kFewMinStages * stage) g.ring = kFewMinStages * stage;
+    g.stages = g.ring / stage < kFewMaxStages ? g.ring / stage : kFewMaxStages;
+  }
+  const size_t smem = (size_t)g.ring + (g.own_room ? few_room_bytes(Epi::kTwo, g.nt, g.split) : 0) + sizeof(FewTail) + 1024;
 
   static std::atomic<bool> known[64];                      // per device: the shared-memory limit is set
   int dev = 0;
