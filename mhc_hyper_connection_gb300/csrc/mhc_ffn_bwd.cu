@@ -28,7 +28,7 @@ cudaError_t few_dgate(const FfnBwdLaunch& L, cudaStream_t s) {
   e.a = static_cast<uint16_t*>(L.a_buf);
   e.F = L.F;
   e.act = L.act;
-  return launch_few(L.wd_mn, L.gy_k, few_shape(L.ga, L.F, L.T, F16, true), e, L.sms, s);
+  return launch_few(L.wd_mn, L.gy_k, few_shape(L.ga, L.F, L.T, F16, true), e, s);
 }
 
 template <bool F16>
@@ -43,7 +43,7 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
     FewStore<F16> f;
     f.out = static_cast<uint16_t*>(L.grad_x);
     f.N = L.D;
-    e = launch_few(L.wgu_mn, L.gg_k, few_shape(L.gx, L.D, L.T, F16, true), f, L.sms, s);
+    e = launch_few(L.wgu_mn, L.gg_k, few_shape(L.gx, L.D, L.T, F16, true), f, s);
   } else {
     o.out = static_cast<uint16_t*>(L.grad_x);
     o.M = L.T;

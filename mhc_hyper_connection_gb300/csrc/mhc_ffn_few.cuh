@@ -10,18 +10,26 @@
 // CTA gets all parts of its share of the tokens, adds them in rank order (no
 // atomics: the same bits every time) and finishes those tokens.
 //
-// A product starts while the one before it still runs (programmatic dependent
-// launch): the rings are sized so that CTAs of both fit an SM, and the weights'
-// first chunks are loaded before the wait for the tokens.
+// A product's CTAs start as SMs fall free in the one before it (programmatic
+// dependent launch) and load the weights' first chunks before they wait for the
+// tokens.
+//
+// One token, D = 7168, F = 8192: 65.5 us for 352 MB of weights, 79% of the
+// measured copy rate; the two products' loops stream at 6.9 and 5.3 TB/s, the
+// rest is their starts and joins, about 4 us each.  24 tokens at D = 4096, F =
+// 8192: 44.9 us (66%).  As ordinary tiles of 256 tokens these took 114 and 80.
 #pragma once
+
+#include <mutex>
 
 #include "mhc_ffn_gemm.cuh"
 
 namespace mhc {
 
 constexpr int kFewThreads = 192;                 // producer, MMA issuer, four epilogue warps
-constexpr int kFewRingTwo = 144 * 1024;          // ring of the gate and up product
-constexpr int kFewRingOne = 76 * 1024;           // ring of the others, beside it on one SM
+constexpr int kFewRingTwo = 160 * 1024;          // ring (and room) of the gate and up product
+constexpr int kFewRingOne = 76 * 1024;           // of the others: two CTAs fit an SM
+constexpr size_t kFewHalfSm = 112 * 1024;        // shared memory of which two CTAs fit an SM
 constexpr int kFewMinStages = 3;
 constexpr int kFewMaxStages = 12;
 constexpr int kFewRows = 128;                    // weight rows of one accumulator
@@ -379,48 +387,90 @@ inline FewShape few_shape(const GemmShape& g, int rows, int T, bool f16, bool w_
   return w;
 }
 
-// CTAs per tile: the most that give every SM one, with four chunks of the
-// depth each at least.
-template <class Epi>
-cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, int sms, cudaStream_t s) {
-  auto* k = ffn_few_kernel<Epi>;
-  const int stage = few_stage_bytes(Epi::kTwo, g.nt);
-  g.ring = Epi::kTwo ? kFewRingTwo : kFewRingOne;
+// Ring, room and shared memory of a launch with `split` CTAs per tile.
+inline size_t few_layout(FewShape& g, bool two, int split) {
+  const int stage = few_stage_bytes(two, g.nt), room = few_room_bytes(two, g.nt, split);
+  g.split = split;
+  g.own_room = split > 1 && g.nt <= 64;
+  g.ring = (two ? kFewRingTwo : kFewRingOne) - (g.own_room ? room : 0);
   if (g.ring < kFewMinStages * stage) g.ring = kFewMinStages * stage;
-  g.stages = g.ring / stage;
-  if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
-  g.split = 1;
-  while (g.split < 8 && g.tiles * g.split * 2 <= (Epi::kTwo ? 1 : 2) * sms && g.kiters >= 8 * g.split) g.split *= 2;
-  g.own_room = g.nt <= 32;
-  if (g.own_room) {                                        // within the same total
-    g.ring -= few_room_bytes(Epi::kTwo, g.nt, g.split);
-    if (g.ring < kFewMinStages * stage) g.ring = kFewMinStages * stage;
-    g.stages = g.ring / stage < kFewMaxStages ? g.ring / stage : kFewMaxStages;
-  }
-  const size_t smem = (size_t)g.ring + (g.own_room ? few_room_bytes(Epi::kTwo, g.nt, g.split) : 0) + sizeof(FewTail) + 1024;
+  g.stages = g.ring / stage < kFewMaxStages ? g.ring / stage : kFewMaxStages;
+  return (size_t)g.ring + (g.own_room ? room : 0) + sizeof(FewTail) + 1024;
+}
 
-  static std::atomic<bool> known[64];                      // per device: the shared-memory limit is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+// A kernel of the same launch shape that uses no tensor memory: the runtime
+// counts one CTA per SM for those that do, whatever they allocate.
+static __global__ void __launch_bounds__(kFewThreads) few_shape_kernel() {}
+
+// Clusters of 2, 4 and 8 CTAs that the device holds at once, with the shared
+// memory of two CTAs per SM (first row) or of one; looked up once per device.
+struct FewClusters {
+  int n[2][3];
+};
+inline cudaError_t few_clusters(int dev, FewClusters* out) {
+  static std::mutex mu;
+  static FewClusters known[64];
+  static bool have[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!known[dev].load(std::memory_order_relaxed)) {
-    const int most = 200 * 1024;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
-    known[dev].store(true, std::memory_order_relaxed);
+  std::lock_guard<std::mutex> lk(mu);
+  if (!have[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.gridDim = dim3(1024);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    for (int c = 0; c < 2; ++c) {
+      for (int i = 0; i < 3; ++i) {
+        attr[0].val.clusterDim.x = 2u << i;
+        cfg.dynamicSmemBytes = c == 0 ? kFewHalfSm : 160 * 1024;
+        if ((e = cudaOccupancyMaxActiveClusters(&known[dev].n[c][i], few_shape_kernel, &cfg)) != cudaSuccess) return e;
+      }
+    }
+    have[dev] = true;
+  }
+  *out = known[dev];
+  return cudaSuccess;
+}
+
+// CTAs per tile: the most whose clusters the device holds all at once, with
+// four chunks of the depth each at least.
+template <class Epi>
+cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, cudaStream_t s) {
+  auto* k = ffn_few_kernel<Epi>;
+  static std::atomic<bool> ready[64];                      // per device: the shared-memory limit is set
+  int dev = 0;
+  FewClusters fit;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (e = few_clusters(dev, &fit)) != cudaSuccess) return e;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024)) != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)g.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(g.tiles * g.split));
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
+  size_t smem = few_layout(g, Epi::kTwo, 1);
+  for (int i = 0; i < 3; ++i) {
+    FewShape w = g;
+    const size_t bytes = few_layout(w, Epi::kTwo, 2 << i);
+    if (g.kiters < 4 * w.split || g.tiles > fit.n[bytes > kFewHalfSm ? 1 : 0][i]) break;
+    g = w;
+    smem = bytes;
+  }
+  attr[0].val.clusterDim.x = (unsigned)g.split;
+  cfg.gridDim = dim3((unsigned)(g.tiles * g.split));
+  cfg.dynamicSmemBytes = smem;
   cfg.numAttrs = g.first ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, k, tw, tx, (const FewShape)g, epi);
 }

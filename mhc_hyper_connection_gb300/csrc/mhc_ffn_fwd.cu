@@ -37,7 +37,7 @@ cudaError_t few_gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
   e.scales = static_cast<uint8_t*>(L.scales);
   e.F = L.F;
   e.act = L.act;
-  return launch_few(L.wgu, L.x, few_shape(L.gu, L.F, L.T, F16), e, L.sms, s);
+  return launch_few(L.wgu, L.x, few_shape(L.gu, L.F, L.T, F16), e, s);
 }
 
 template <bool F16>
@@ -49,7 +49,7 @@ cudaError_t forward_few(const FfnFwdLaunch& L, cudaStream_t s) {
   FewStore<F16> o;
   o.out = static_cast<uint16_t*>(L.y);
   o.N = L.D;
-  return launch_few(L.wd, L.a, few_shape(L.down, L.D, L.T, F16), o, L.sms, s);
+  return launch_few(L.wd, L.a, few_shape(L.down, L.D, L.T, F16), o, s);
 }
 
 }  // namespace

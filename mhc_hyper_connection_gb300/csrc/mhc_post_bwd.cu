@@ -3,11 +3,12 @@
 //     grad_x = sum_j post[j] g[j]          grad_residual[i] = sum_j comb[i][j] g[j]
 //     grad_post[j] = <g[j], x>             grad_comb[i][j]  = <residual[i], g[j]>
 //
-// One pass over g, x and the residual streams: a lane holds eight columns of
-// all of them, forms the n + 1 output vectors at once and adds its products to
-// n + n^2 running fp32 dot products, which are joined over the lanes once per
-// token.  Bounded by HBM: (2n + 1) 2 bytes read (n + 1/128 n fewer from a
-// checkpoint) and (n + 1) 2 written per column, against 2 (n + n^2) products.
+// One pass over g, x and the residual streams.  Bounded by HBM: (2n + 1) 2
+// bytes read (n - n/128 fewer from a checkpoint) and (n + 1) 2 written per
+// column, against 2 (n + n^2) products.  On the CUDA cores those products took
+// as long as the memory from n = 6 up (n = 8, T = 16384, D = 2048 from a
+// checkpoint: 430 us, 51% of measured HBM), so from n = 3 up they run on the
+// tensor cores (post_bwd_mma_kernel); for n = 1 and 2 a lane forms them itself.
 #include "mhc_ckpt.cuh"
 #include "mhc_host.cuh"
 #include "../../include/mhc_post_backward.h"
@@ -177,10 +178,216 @@ __global__ void __launch_bounds__(kPbThreads) post_bwd_kernel(const PostBwdParam
   }
 }
 
+// ------------------------------------------------------- n = 3 .. 8
+// Rows of a warp's 8 x 32 pieces: the streams of one token (n >= 5), or of two
+// at four rows each.  Lane 4 r + q holds row r, eight columns from 8 q, of g
+// and of the residual; that is at once both operands' register layout of a
+// 16 x 8 x 16 tensor-core product over the columns (their order inside a sum
+// does not matter), whose result is the dot products of all row pairs: no
+// joining over lanes.  The residual rows are the upper eight rows of A, the
+// tokens' x the lower ones.
+//
+// The outputs are products over the rows: [comb; post] (16 x 8) times g (8 x
+// columns).  movmatrix turns a register of g into the B operand, and the result
+// comes out in the layout that g came in: eight consecutive columns a lane.
+// comb and post enter as three bf16 terms (24 bits, as fp32 has), so a product
+// is as exact as in fp32.  Such a split turns an infinity in g into NaN, and two
+// tokens of a warp share the product over rows, so a piece with a result that
+// is not finite is formed again in plain fp32 (direct_piece).
+//
+// Sums: the tensor core adds at most 64 columns, then fp32 registers (a long
+// chain inside it would round toward zero at every step).
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// c = t[0] + t[1] + t[2] in bf16 terms
+__device__ __forceinline__ void split3(float c, float (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    t[i] = __bfloat162float(__float2bfloat16_rn(c));
+    c = fabsf(t[i]) < __int_as_float(0x7F800000) ? c - t[i] : 0.0f;
+  }
+}
+
+// Row r, columns 8 q .. of [comb; post] g in fp32: g's rows come from the lanes
+// that hold them.  `coef` points at the first of this row's n coefficients,
+// `src` is the first row of its token.
+template <int NS>
+__device__ __noinline__ uint4 direct_piece(uint4 g, const float* coef, int src, int lane) {
+  float o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+  for (int j = 0; j < NS; ++j) {
+    const int from = (src + j) * 4 + (lane & 3);
+    uint4 w;
+    w.x = __shfl_sync(0xFFFFFFFFu, g.x, from);
+    w.y = __shfl_sync(0xFFFFFFFFu, g.y, from);
+    w.z = __shfl_sync(0xFFFFFFFFu, g.z, from);
+    w.w = __shfl_sync(0xFFFFFFFFu, g.w, from);
+    float f[8];
+    unpack8(w, f);
+    const float c = coef ? __ldg(coef + j) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = j == 0 ? c * f[e] : fmaf(c, f[e], o[e]);
+  }
+  return pack8(o);
+}
+
+template <int NS, bool kCkpt>
+__global__ void __launch_bounds__(kPbThreads) post_bwd_mma_kernel(const PostBwdParams p) {
+  constexpr int kTok = NS <= 4 ? 2 : 1, kStride = 8 / kTok;          // tokens of a warp, rows between them
+  __shared__ float part[kPbWarps][16 * 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q = lane & 3;
+  const int wpt = p.wpt, sub = warp & (wpt - 1);
+  const long long t0 = ((long long)blockIdx.x * (kPbWarps / wpt) + warp / wpt) * kTok;
+  const int D = p.D, nblk = (D + kCkptBlock - 1) / kCkptBlock;
+  const int tau = r / kStride, s = r % kStride;
+  const bool row_ok = s < NS && t0 + tau < p.T, x_ok = r < kTok && t0 + r < p.T;
+  const size_t row = (size_t)(t0 + tau) * NS + s;                    // of g, the residual and its gradient
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};                           // rows r and 8 + r, columns 2 q, 2 q + 1
+
+  if (t0 < p.T) {                                                    // uniform over the warp
+    const uint64_t once = policy_evict_first();
+    // A operand of the outputs: row r comb, row 8 + r post, over g's rows 2 q, 2 q + 1
+    uint32_t ac[3], ap[3];
+    {
+      float tc[2][3], tp[2][3];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = 2 * q + e, tk = k / kStride, j = k % kStride;
+        const bool ok = j < NS && t0 + tk < p.T;
+        split3(ok && row_ok && tk == tau ? __ldg(p.comb + row * NS + j) : 0.0f, tc[e]);
+        split3(ok && x_ok && tk == r ? __ldg(p.post + (size_t)(t0 + tk) * NS + j) : 0.0f, tp[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        ac[i] = bf16x2(tc[0][i], tc[1][i]);
+        ap[i] = bf16x2(tp[0][i], tp[1][i]);
+      }
+    }
+    const __nv_bfloat16* gp = p.g + row * D + q * 8;
+    const __nv_bfloat16* xp = p.x + (size_t)(t0 + r) * D + q * 8;
+    __nv_bfloat16* gres = p.gres + row * D + q * 8;
+    __nv_bfloat16* gx = p.gx + (size_t)(t0 + r) * D + q * 8;
+    for (int blk = sub; blk < nblk; blk += wpt) {                    // blocks of 128 columns
+      const int c0 = blk * 128, left = D - c0 - q * 8;               // this lane's columns from c0: u * 32 < left
+      uint4 gv[4], xv[4], rv[kCkpt ? 1 : 4];
+      uint2 cv[kCkpt ? 4 : 1];
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = u * 32 < left;
+        gv[u] = in && row_ok ? ld_global_v4_hint(gp + c0 + u * 32, once) : zero;
+        if constexpr (kCkpt)
+          cv[u] = in && row_ok ? __ldcs(reinterpret_cast<const uint2*>(p.codes + row * D + q * 8 + c0 + u * 32)) : make_uint2(0, 0);
+        else
+          rv[u] = in && row_ok ? ld_global_v4_hint(p.res + row * D + q * 8 + c0 + u * 32, once) : zero;
+        xv[u] = in && x_ok ? ld_global_v4_hint(xp + c0 + u * 32, once) : zero;
+      }
+      float scale = 1.0f;
+      if (kCkpt && row_ok) scale = ckpt_scale(__ldg(p.scales + row * nblk + blk));
+      float dot[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t gw[4] = {gv[u].x, gv[u].y, gv[u].z, gv[u].w};
+        const uint32_t xw[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+        uint32_t rw[4];
+        if constexpr (kCkpt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {                              // a code's value is exact in bf16
+            const float2 f = e4m3x2_f2((e < 2 ? cv[u].x : cv[u].y) >> (16 * (e & 1)));
+            rw[e] = bf16x2(f.x, f.y);
+          }
+        } else {
+          rw[0] = rv[u].x;
+          rw[1] = rv[u].y;
+          rw[2] = rv[u].z;
+          rw[3] = rv[u].w;
+        }
+        if ((u & 1) == 0) dot[0] = dot[1] = dot[2] = dot[3] = 0.0f;
+        mma_16816(dot, rw[0], xw[0], rw[1], xw[1], gw[0], gw[1]);
+        mma_16816(dot, rw[2], xw[2], rw[3], xw[3], gw[2], gw[3]);
+        if (u & 1) {
+          acc[0] = fmaf(dot[0], scale, acc[0]);
+          acc[1] = fmaf(dot[1], scale, acc[1]);
+          acc[2] += dot[2];
+          acc[3] += dot[3];
+        }
+        uint32_t o[4], ox[4];
+        float size = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t b = movmatrix(gw[t]);
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_1688(c, ac[2], ap[2], b);                              // smallest terms first
+          mma_16816(c, ac[0], ap[0], ac[1], ap[1], b, b);
+          o[t] = bf16x2(c[0], c[1]);
+          ox[t] = bf16x2(c[2], c[3]);
+          size += fabsf(c[0]) + fabsf(c[1]);
+          size += fabsf(c[2]) + fabsf(c[3]);
+        }
+        uint4 ov = make_uint4(o[0], o[1], o[2], o[3]), oxv = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+        if (__any_sync(0xFFFFFFFFu, !(size < __int_as_float(0x7F800000)))) {
+          ov = direct_piece<NS>(gv[u], row_ok ? p.comb + row * NS : nullptr, tau * kStride, lane);
+          oxv = direct_piece<NS>(gv[u], x_ok ? p.post + (size_t)(t0 + r) * NS : nullptr, x_ok ? r * kStride : 0, lane);
+        }
+        const bool in = u * 32 < left;
+        if (in && row_ok) st_global_v4_hint(gres + c0 + u * 32, ov, once);
+        if (in && x_ok) st_global_v4_hint(gx + c0 + u * 32, oxv, once);
+      }
+    }
+  }
+  if (wpt > 1) {                        // join the token's warps, in warp order
+    float* mine = part[warp];
+    mine[r * 8 + 2 * q] = acc[0];
+    mine[r * 8 + 2 * q + 1] = acc[1];
+    mine[(8 + r) * 8 + 2 * q] = acc[2];
+    mine[(8 + r) * 8 + 2 * q + 1] = acc[3];
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = 1; w < wpt; ++w) {
+      const float* o = part[warp + w];
+      acc[0] += o[r * 8 + 2 * q];
+      acc[1] += o[r * 8 + 2 * q + 1];
+      acc[2] += o[(8 + r) * 8 + 2 * q];
+      acc[3] += o[(8 + r) * 8 + 2 * q + 1];
+    }
+  }
+  if (t0 >= p.T) return;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int k = 2 * q + e, tk = k / kStride, j = k % kStride;
+    if (j < NS && row_ok && tk == tau) p.gcomb[row * NS + j] = acc[e];
+    if (j < NS && x_ok && tk == r) p.gpost[(size_t)(t0 + r) * NS + j] = acc[2 + e];
+  }
+}
+
 template <int NS>
 cudaError_t launch_ns(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
-  if (p.codes) post_bwd_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
-  else post_bwd_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
+  if constexpr (NS <= 2) {
+    if (p.codes) post_bwd_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
+    else post_bwd_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
+  } else {
+    if (p.codes) post_bwd_mma_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
+    else post_bwd_mma_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -229,12 +436,14 @@ extern "C" mhc_status_t mhc_post_backward_run(const mhc_post_bwd_args* a, void* 
   p.gres = static_cast<__nv_bfloat16*>(a->grad_residual);
   p.gpost = a->grad_post;
   p.gcomb = a->grad_comb;
-  // Few tokens: several warps share one, while each still has a vector per
-  // lane, until there are 16 warps per SM.
+  // Few tokens: several warps share one (or two, n = 3 and 4), while each still
+  // has 256 columns, until there are 64 warps per SM (T = 4096, n = 4, D = 4096: 84.9 us
+  // with 16, 80.7 with 64: the last round of CTAs is shorter).
+  const int64_t tok = n == 3 || n == 4 ? 2 : 1, units = (T + tok - 1) / tok;
   p.wpt = 1;
-  while (p.wpt < kPbWarps && T * p.wpt < (int64_t)di.sms * 16 && p.wpt * 256 < D) p.wpt *= 2;
+  while (p.wpt < kPbWarps && units * p.wpt < (int64_t)di.sms * 64 && p.wpt * 256 < D) p.wpt *= 2;
   const int64_t per = kPbWarps / p.wpt;
-  const unsigned grid = (unsigned)((T + per - 1) / per);
+  const unsigned grid = (unsigned)((units + per - 1) / per);
   using Fn = cudaError_t (*)(const PostBwdParams&, unsigned, cudaStream_t);
   static const Fn table[8] = {launch_ns<1>, launch_ns<2>, launch_ns<3>, launch_ns<4>,
                               launch_ns<5>, launch_ns<6>, launch_ns<7>, launch_ns<8>};
