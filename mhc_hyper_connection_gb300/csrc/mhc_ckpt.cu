@@ -102,84 +102,117 @@ __global__ void __launch_bounds__(kCkptThreads)
   }
 }
 
-// The post-mapping (out[j] = post[j] x + sum_i comb[i][j] residual[i], one
-// warp a token, fp32 sums in that order, RN-even) and the checkpoint of its
-// rounded output: the 16 lanes that hold a block of 128 columns join their
-// maxima and encode from registers.
+// The post-mapping (out[j] = post[j] x + sum_i comb[i][j] residual[i], fp32 sums
+// in that order, RN-even) and the checkpoint of its rounded output: the 16 lanes
+// that hold a block of 128 columns join their maxima and encode from registers.
+//
+// A warp takes an equal run of pieces (one token, 256 kV columns); a lane has kV
+// vectors of eight columns of each tensor, copied to its own places in shared
+// memory one piece ahead, so that the copies of a piece run under the work on
+// the one before (with loads into registers instead, at the 16 warps per SM that
+// they leave, T = 4096, n = 4, D = 4096 took 83 us where it takes 67 now, 81% of
+// measured HBM).
+template <int NS>
+struct PcStage {
+  static constexpr int kV = NS <= 4 ? 2 : 1;
+  uint4 x[kV][32], r[kV][NS][32];
+};
+
 template <int NS>
 __global__ void __launch_bounds__(kCkptThreads)
     post_ckpt_kernel(int T, int D, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ res,
                      const float* __restrict__ post, const float* __restrict__ comb, __nv_bfloat16* __restrict__ out,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  constexpr int kV = NS <= 4 ? 2 : 1;
-  const int lane = threadIdx.x & 31;
-  const int gw = (blockIdx.x * kCkptThreads + threadIdx.x) >> 5, nw = (gridDim.x * kCkptThreads) >> 5;
-  const int nv = D >> 3, nblk = (D + kCkptBlock - 1) / kCkptBlock;
+  using Stage = PcStage<NS>;
+  constexpr int kV = Stage::kV;
+  extern __shared__ __align__(16) uint8_t pc_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long gw = (long long)blockIdx.x * (kCkptThreads / 32) + warp, nw = (long long)gridDim.x * (kCkptThreads / 32);
+  const int nv = D >> 3, nblk = (D + kCkptBlock - 1) / kCkptBlock, segs = (nv + 32 * kV - 1) / (32 * kV);
+  const long long pieces = (long long)T * segs;
+  const long long first = pieces * gw / nw, last = pieces * (gw + 1) / nw;
+  if (first >= last) return;
   const uint64_t once = policy_evict_first();
   const uint32_t mask = 0xFFFFu << (lane & 16);
-  for (int t = gw; t < T; t += nw) {
-    float pc[NS], cm[NS * NS];
+  Stage* stages = reinterpret_cast<Stage*>(pc_smem) + 2 * warp;
+  auto fetch = [&](long long t, int seg, Stage& st) {
 #pragma unroll
-    for (int j = 0; j < NS; ++j) pc[j] = __ldg(post + (size_t)t * NS + j);
+    for (int q = 0; q < kV; ++q) {
+      const int v = (seg * kV + q) * 32 + lane;
+      const bool in = v < nv;
+      copy16(&st.x[q][lane], x + (in ? t * D + v * 8 : 0), in, once);
 #pragma unroll
-    for (int e = 0; e < NS * NS; ++e) cm[e] = __ldg(comb + (size_t)t * NS * NS + e);
-    const __nv_bfloat16* xt = x + (size_t)t * D;
-    const __nv_bfloat16* rt = res + (size_t)t * NS * D;
-    for (int vb = 0; vb < nv; vb += 32 * kV) {     // all lanes stay for the shuffles
-      uint4 xv[kV], rv[kV][NS];
+      for (int i = 0; i < NS; ++i) copy16(&st.r[q][i][lane], res + (in ? (t * NS + i) * D + v * 8 : 0), in, once);
+    }
+  };
+  long long t = first / segs;
+  int seg = (int)(first - t * segs);
+  fetch(t, seg, stages[0]);
+  copies_commit();
+  float pc[NS], cm[NS * NS];
+  long long have = -1;                             // token whose coefficients are loaded
+  int buf = 0;
+  for (long long u = first; u < last; ++u, buf ^= 1) {
+    long long tn = t;
+    int sn = seg + 1;
+    if (sn == segs) { sn = 0; ++tn; }
+    if (u + 1 < last) fetch(tn, sn, stages[buf ^ 1]);
+    copies_commit();
+    if (have != t) {
+      have = t;
 #pragma unroll
-      for (int q = 0; q < kV; ++q) {
-        const int v = vb + q * 32 + lane;
-        xv[q] = make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < NS; ++j) pc[j] = __ldg(post + t * NS + j);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) rv[q][i] = make_uint4(0, 0, 0, 0);
-        if (v < nv) {
-          xv[q] = ld_global_v4_hint(xt + (size_t)v * 8, once);
+      for (int e = 0; e < NS * NS; ++e) cm[e] = __ldg(comb + t * (NS * NS) + e);
+    }
+    copies_wait<1>();
+    const Stage& st = stages[buf];
 #pragma unroll
-          for (int i = 0; i < NS; ++i) rv[q][i] = ld_global_v4_hint(rt + (size_t)i * D + (size_t)v * 8, once);
+    for (int q = 0; q < kV; ++q) {
+      const int v = (seg * kV + q) * 32 + lane;
+      if ((v & ~15) >= nv) continue;               // this half-warp's block lies beyond the row
+      const uint4 xv = st.x[q][lane];
+      uint4 rv[NS];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) rv[i] = st.r[q][i][lane];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        float acc[8];
+        const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __bfloat1622float2(hx[e]);
+          acc[2 * e] = pc[j] * f.x;
+          acc[2 * e + 1] = pc[j] * f.y;
         }
-      }
 #pragma unroll
-      for (int q = 0; q < kV; ++q) {
-        const int v = vb + q * 32 + lane;
-        if ((v & ~15) >= nv) continue;             // this half-warp's block lies beyond the row
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          float acc[8];
-          const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv[q]);
+        for (int i = 0; i < NS; ++i) {
+          const float c = cm[i * NS + j];
+          const __nv_bfloat162* hr = reinterpret_cast<const __nv_bfloat162*>(&rv[i]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(hx[e]);
-            acc[2 * e] = pc[j] * f.x;
-            acc[2 * e + 1] = pc[j] * f.y;
+            const float2 f = __bfloat1622float2(hr[e]);
+            acc[2 * e] = fmaf(c, f.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(c, f.y, acc[2 * e + 1]);
           }
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const float c = cm[i * NS + j];
-            const __nv_bfloat162* hr = reinterpret_cast<const __nv_bfloat162*>(&rv[q][i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = __bfloat1622float2(hr[e]);
-              acc[2 * e] = fmaf(c, f.x, acc[2 * e]);
-              acc[2 * e + 1] = fmaf(c, f.y, acc[2 * e + 1]);
-            }
-          }
-          uint4 o;
-          __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(&o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ob[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
-          if (v >= nv) o = make_uint4(0, 0, 0, 0);   // beyond the row: nothing for the maximum (a NaN coefficient times 0)
-          uint2 c8;
-          const int ex = ckpt_block16<false>(o, mask, c8);
-          const size_t row = (size_t)t * NS + j;
-          if (v < nv) {
-            st_global_v4_hint(out + row * D + (size_t)v * 8, o, once);
-            __stcs(reinterpret_cast<uint2*>(codes + row * D + (size_t)v * 8), c8);
-          }
-          if ((lane & 15) == 0) scales[row * nblk + (v >> 4)] = (uint8_t)(ex + 127);
         }
+        uint4 o;
+        __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(&o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ob[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+        if (v >= nv) o = make_uint4(0, 0, 0, 0);   // beyond the row: nothing for the maximum (a NaN coefficient times 0)
+        uint2 c8;
+        const int ex = ckpt_block16<false>(o, mask, c8);
+        const size_t row = (size_t)t * NS + j;
+        if (v < nv) {
+          st_global_v4_hint(out + row * D + (size_t)v * 8, o, once);
+          __stcs(reinterpret_cast<uint2*>(codes + row * D + (size_t)v * 8), c8);
+        }
+        if ((lane & 15) == 0) scales[row * nblk + (v >> 4)] = (uint8_t)(ex + 127);
       }
     }
+    t = tn;
+    seg = sn;
   }
 }
 
@@ -193,17 +226,23 @@ cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* re
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int resident = known[dev].load(std::memory_order_relaxed);
+  constexpr size_t smem = 2 * (kCkptThreads / 32) * sizeof(PcStage<NS>);
   if (resident == 0) {
     int per_sm = 0;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, post_ckpt_kernel<NS>, kCkptThreads, 0)) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(post_ckpt_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+        cudaSuccess)
+      return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, post_ckpt_kernel<NS>, kCkptThreads, smem)) !=
+        cudaSuccess)
       return e;
     resident = (per_sm > 0 ? per_sm : 1) * (device_info(dev).sms > 0 ? device_info(dev).sms : 1);
     known[dev].store(resident, std::memory_order_relaxed);
   }
   long long grid = resident;
-  const long long need = (T * 32 + kCkptThreads - 1) / kCkptThreads;
+  const long long cols = 256 * PcStage<NS>::kV;
+  const long long need = (T * ((D + cols - 1) / cols) + kCkptThreads / 32 - 1) / (kCkptThreads / 32);   // a piece a warp
   if (grid > need) grid = need;
-  post_ckpt_kernel<NS><<<(int)grid, kCkptThreads, 0, s>>>(
+  post_ckpt_kernel<NS><<<(int)grid, kCkptThreads, smem, s>>>(
       (int)T, (int)D, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res), post, comb,
       static_cast<__nv_bfloat16*>(out), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
   return cudaGetLastError();

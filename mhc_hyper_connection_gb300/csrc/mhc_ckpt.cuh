@@ -120,6 +120,24 @@ __device__ __forceinline__ int ckpt_block16(uint4 v, uint32_t mask, uint2& codes
   return e;
 }
 
+// Asynchronous copies of 16 or 8 bytes to shared memory, zeros where `in` is
+// false; each thread waits for its own groups and reads only what it copied.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(in ? 16 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool in, uint64_t policy) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2, %3;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(in ? 8 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Value of a scale byte: 2^(byte - 127).
 __device__ __forceinline__ float ckpt_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 

@@ -9,6 +9,8 @@
 // as long as the memory from n = 6 up (n = 8, T = 16384, D = 2048 from a
 // checkpoint: 430 us, 51% of measured HBM), so from n = 3 up they run on the
 // tensor cores (post_bwd_mma_kernel); for n = 1 and 2 a lane forms them itself.
+#include <atomic>
+
 #include "mhc_ckpt.cuh"
 #include "mhc_host.cuh"
 #include "../../include/mhc_post_backward.h"
@@ -250,9 +252,22 @@ __device__ __noinline__ uint4 direct_piece(uint4 g, const float* coef, int src, 
   return pack8(o);
 }
 
+// A warp's 128 columns in shared memory, each lane's own pieces: four of g, of
+// the residual (16 bytes, or 8 of codes) and, in the lanes with an x row, of x.
+// The next 128 columns are copied while these are worked on.
 template <int NS, bool kCkpt>
-__global__ void __launch_bounds__(kPbThreads) post_bwd_mma_kernel(const PostBwdParams p) {
-  constexpr int kTok = NS <= 4 ? 2 : 1, kStride = 8 / kTok;          // tokens of a warp, rows between them
+struct PbStage {
+  static constexpr int kTok = NS <= 4 ? 2 : 1;                       // tokens of a warp
+  uint4 g[4][32];
+  uint4 x[4][4 * kTok];
+  uint2 r[4][32 * (kCkpt ? 1 : 2)];
+};
+
+template <int NS, bool kCkpt>
+__global__ void __launch_bounds__(kPbThreads, kCkpt ? 3 : 2) post_bwd_mma_kernel(const PostBwdParams p) {
+  using Stage = PbStage<NS, kCkpt>;
+  constexpr int kTok = Stage::kTok, kStride = 8 / kTok;              // rows between the tokens
+  extern __shared__ __align__(16) uint8_t pb_smem[];
   __shared__ float part[kPbWarps][16 * 8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q = lane & 3;
   const int wpt = p.wpt, sub = warp & (wpt - 1);
@@ -286,40 +301,52 @@ __global__ void __launch_bounds__(kPbThreads) post_bwd_mma_kernel(const PostBwdP
     const __nv_bfloat16* xp = p.x + (size_t)(t0 + r) * D + q * 8;
     __nv_bfloat16* gres = p.gres + row * D + q * 8;
     __nv_bfloat16* gx = p.gx + (size_t)(t0 + r) * D + q * 8;
-    for (int blk = sub; blk < nblk; blk += wpt) {                    // blocks of 128 columns
+    Stage* stages = reinterpret_cast<Stage*>(pb_smem) + 2 * warp;
+    auto fetch = [&](int blk, Stage& st) {
       const int c0 = blk * 128, left = D - c0 - q * 8;               // this lane's columns from c0: u * 32 < left
-      uint4 gv[4], xv[4], rv[kCkpt ? 1 : 4];
-      uint2 cv[kCkpt ? 4 : 1];
-      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool in = u * 32 < left;
-        gv[u] = in && row_ok ? ld_global_v4_hint(gp + c0 + u * 32, once) : zero;
-        if constexpr (kCkpt)
-          cv[u] = in && row_ok ? __ldcs(reinterpret_cast<const uint2*>(p.codes + row * D + q * 8 + c0 + u * 32)) : make_uint2(0, 0);
-        else
-          rv[u] = in && row_ok ? ld_global_v4_hint(p.res + row * D + q * 8 + c0 + u * 32, once) : zero;
-        xv[u] = in && x_ok ? ld_global_v4_hint(xp + c0 + u * 32, once) : zero;
+        const bool in = u * 32 < left && row_ok;
+        copy16(&st.g[u][lane], in ? gp + c0 + u * 32 : p.g, in, once);
+        if constexpr (kCkpt) copy8(&st.r[u][lane], in ? p.codes + row * D + q * 8 + c0 + u * 32 : p.codes, in, once);
+        else copy16(&st.r[u][2 * lane], in ? p.res + row * D + q * 8 + c0 + u * 32 : p.res, in, once);
+        if (r < kTok) {
+          const bool xin = u * 32 < left && x_ok;
+          copy16(&st.x[u][lane], xin ? xp + c0 + u * 32 : p.x, xin, once);
+        }
       }
+    };
+    if (sub < nblk) fetch(sub, stages[0]);
+    copies_commit();
+    int buf = 0;
+    for (int blk = sub; blk < nblk; blk += wpt, buf ^= 1) {          // blocks of 128 columns
+      const int c0 = blk * 128, left = D - c0 - q * 8;
+      const Stage& st = stages[buf];
+      if (blk + wpt < nblk) fetch(blk + wpt, stages[buf ^ 1]);
+      copies_commit();
+      copies_wait<1>();
       float scale = 1.0f;
       if (kCkpt && row_ok) scale = ckpt_scale(__ldg(p.scales + row * nblk + blk));
       float dot[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint32_t gw[4] = {gv[u].x, gv[u].y, gv[u].z, gv[u].w};
-        const uint32_t xw[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+        const uint4 gv = st.g[u][lane];
+        const uint4 xv = r < kTok ? st.x[u][lane] : make_uint4(0, 0, 0, 0);
+        const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, xw[4] = {xv.x, xv.y, xv.z, xv.w};
         uint32_t rw[4];
         if constexpr (kCkpt) {
+          const uint2 cv = st.r[u][lane];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {                              // a code's value is exact in bf16
-            const float2 f = e4m3x2_f2((e < 2 ? cv[u].x : cv[u].y) >> (16 * (e & 1)));
+            const float2 f = e4m3x2_f2((e < 2 ? cv.x : cv.y) >> (16 * (e & 1)));
             rw[e] = bf16x2(f.x, f.y);
           }
         } else {
-          rw[0] = rv[u].x;
-          rw[1] = rv[u].y;
-          rw[2] = rv[u].z;
-          rw[3] = rv[u].w;
+          const uint4 rv = *reinterpret_cast<const uint4*>(&st.r[u][2 * lane]);
+          rw[0] = rv.x;
+          rw[1] = rv.y;
+          rw[2] = rv.z;
+          rw[3] = rv.w;
         }
         if ((u & 1) == 0) dot[0] = dot[1] = dot[2] = dot[3] = 0.0f;
         mma_16816(dot, rw[0], xw[0], rw[1], xw[1], gw[0], gw[1]);
@@ -345,8 +372,8 @@ __global__ void __launch_bounds__(kPbThreads) post_bwd_mma_kernel(const PostBwdP
         }
         uint4 ov = make_uint4(o[0], o[1], o[2], o[3]), oxv = make_uint4(ox[0], ox[1], ox[2], ox[3]);
         if (__any_sync(0xFFFFFFFFu, !(size < __int_as_float(0x7F800000)))) {
-          ov = direct_piece<NS>(gv[u], row_ok ? p.comb + row * NS : nullptr, tau * kStride, lane);
-          oxv = direct_piece<NS>(gv[u], x_ok ? p.post + (size_t)(t0 + r) * NS : nullptr, x_ok ? r * kStride : 0, lane);
+          ov = direct_piece<NS>(gv, row_ok ? p.comb + row * NS : nullptr, tau * kStride, lane);
+          oxv = direct_piece<NS>(gv, x_ok ? p.post + (size_t)(t0 + r) * NS : nullptr, x_ok ? r * kStride : 0, lane);
         }
         const bool in = u * 32 < left;
         if (in && row_ok) st_global_v4_hint(gres + c0 + u * 32, ov, once);
@@ -379,14 +406,30 @@ __global__ void __launch_bounds__(kPbThreads) post_bwd_mma_kernel(const PostBwdP
   }
 }
 
+template <int NS, bool kCkpt>
+cudaError_t launch_mma(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
+  constexpr size_t smem = 2 * kPbWarps * sizeof(PbStage<NS, kCkpt>);
+  static std::atomic<bool> ready[64];                      // per device: the shared-memory limit is set
+  auto* k = post_bwd_mma_kernel<NS, kCkpt>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  k<<<grid, kPbThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int NS>
 cudaError_t launch_ns(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
   if constexpr (NS <= 2) {
     if (p.codes) post_bwd_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
     else post_bwd_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
   } else {
-    if (p.codes) post_bwd_mma_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
-    else post_bwd_mma_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
+    return p.codes ? launch_mma<NS, true>(p, grid, s) : launch_mma<NS, false>(p, grid, s);
   }
   return cudaGetLastError();
 }
