@@ -112,11 +112,38 @@ __global__ void __launch_bounds__(kCkptThreads)
 // the one before (with loads into registers instead, at the 16 warps per SM that
 // they leave, T = 4096, n = 4, D = 4096 took 83 us where it takes 67 now, 81% of
 // measured HBM).
+//
+// Two columns share a packed fp32 instruction (the same rounding as two plain
+// ones); the coefficients lie in shared memory, each twice.
 template <int NS>
 struct PcStage {
   static constexpr int kV = NS <= 4 ? 2 : 1;
   uint4 x[kV][32], r[kV][NS][32];
 };
+template <int NS>
+struct PcWarp {
+  PcStage<NS> stages[2];
+  float2 coef[(NS + 1) * NS];            // post[j], then comb[i][j], as (c, c)
+};
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// Two bf16 as packed fp32.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  return (uint64_t)(w << 16) | ((uint64_t)(w & 0xFFFF0000u) << 32);
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 template <int NS>
 __global__ void __launch_bounds__(kCkptThreads)
@@ -124,7 +151,7 @@ __global__ void __launch_bounds__(kCkptThreads)
                      const float* __restrict__ post, const float* __restrict__ comb, __nv_bfloat16* __restrict__ out,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   using Stage = PcStage<NS>;
-  constexpr int kV = Stage::kV;
+  constexpr int kV = Stage::kV, kCoef = NS + NS * NS;
   extern __shared__ __align__(16) uint8_t pc_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long gw = (long long)blockIdx.x * (kCkptThreads / 32) + warp, nw = (long long)gridDim.x * (kCkptThreads / 32);
@@ -134,7 +161,7 @@ __global__ void __launch_bounds__(kCkptThreads)
   if (first >= last) return;
   const uint64_t once = policy_evict_first();
   const uint32_t mask = 0xFFFFu << (lane & 16);
-  Stage* stages = reinterpret_cast<Stage*>(pc_smem) + 2 * warp;
+  PcWarp<NS>& mine = reinterpret_cast<PcWarp<NS>*>(pc_smem)[warp];
   auto fetch = [&](long long t, int seg, Stage& st) {
 #pragma unroll
     for (int q = 0; q < kV; ++q) {
@@ -147,68 +174,85 @@ __global__ void __launch_bounds__(kCkptThreads)
   };
   long long t = first / segs;
   int seg = (int)(first - t * segs);
-  fetch(t, seg, stages[0]);
+  fetch(t, seg, mine.stages[0]);
   copies_commit();
-  float pc[NS], cm[NS * NS];
   long long have = -1;                             // token whose coefficients are loaded
   int buf = 0;
   for (long long u = first; u < last; ++u, buf ^= 1) {
     long long tn = t;
     int sn = seg + 1;
     if (sn == segs) { sn = 0; ++tn; }
-    if (u + 1 < last) fetch(tn, sn, stages[buf ^ 1]);
+    if (u + 1 < last) fetch(tn, sn, mine.stages[buf ^ 1]);
     copies_commit();
     if (have != t) {
       have = t;
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < NS; ++j) pc[j] = __ldg(post + t * NS + j);
-#pragma unroll
-      for (int e = 0; e < NS * NS; ++e) cm[e] = __ldg(comb + t * (NS * NS) + e);
+      for (int k = lane; k < kCoef; k += 32) {
+        const float c = k < NS ? __ldg(post + t * NS + k) : __ldg(comb + t * (NS * NS) + k - NS);
+        mine.coef[k] = make_float2(c, c);
+      }
+      __syncwarp();
     }
     copies_wait<1>();
-    const Stage& st = stages[buf];
+    const Stage& st = mine.stages[buf];
 #pragma unroll
     for (int q = 0; q < kV; ++q) {
       const int v = (seg * kV + q) * 32 + lane;
       if ((v & ~15) >= nv) continue;               // this half-warp's block lies beyond the row
-      const uint4 xv = st.x[q][lane];
-      uint4 rv[NS];
+      const uint64_t* coef = reinterpret_cast<const uint64_t*>(mine.coef);
+      uint64_t xf[4], rf[NS][4];
+      {
+        const uint4 w = st.x[q][lane];
+        xf[0] = widen2(w.x);
+        xf[1] = widen2(w.y);
+        xf[2] = widen2(w.z);
+        xf[3] = widen2(w.w);
+      }
 #pragma unroll
-      for (int i = 0; i < NS; ++i) rv[i] = st.r[q][i][lane];
+      for (int i = 0; i < NS; ++i) {
+        const uint4 w = st.r[q][i][lane];
+        rf[i][0] = widen2(w.x);
+        rf[i][1] = widen2(w.y);
+        rf[i][2] = widen2(w.z);
+        rf[i][3] = widen2(w.w);
+      }
+      auto stream = [&](int j) {
+        const uint64_t c0 = coef[j];
+        uint64_t acc[4];
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        float acc[8];
-        const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __bfloat1622float2(hx[e]);
-          acc[2 * e] = pc[j] * f.x;
-          acc[2 * e + 1] = pc[j] * f.y;
-        }
+        for (int e = 0; e < 4; ++e) acc[e] = mul2(c0, xf[e]);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const float c = cm[i * NS + j];
-          const __nv_bfloat162* hr = reinterpret_cast<const __nv_bfloat162*>(&rv[i]);
+          const uint64_t c = coef[NS + i * NS + j];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(hr[e]);
-            acc[2 * e] = fmaf(c, f.x, acc[2 * e]);
-            acc[2 * e + 1] = fmaf(c, f.y, acc[2 * e + 1]);
-          }
+          for (int e = 0; e < 4; ++e) acc[e] = fma2(c, rf[i][e], acc[e]);
         }
-        uint4 o;
-        __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(&o);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ob[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
-        if (v >= nv) o = make_uint4(0, 0, 0, 0);   // beyond the row: nothing for the maximum (a NaN coefficient times 0)
-        uint2 c8;
-        const int ex = ckpt_block16<false>(o, mask, c8);
+        // beyond the row: nothing for the maximum (a NaN coefficient times 0)
+        return v < nv ? make_uint4(narrow2(acc[0]), narrow2(acc[1]), narrow2(acc[2]), narrow2(acc[3])) : make_uint4(0, 0, 0, 0);
+      };
+      auto store = [&](int j, const uint4& o, const uint2& c8, int ex) {
         const size_t row = (size_t)t * NS + j;
         if (v < nv) {
           st_global_v4_hint(out + row * D + (size_t)v * 8, o, once);
           __stcs(reinterpret_cast<uint2*>(codes + row * D + (size_t)v * 8), c8);
         }
         if ((lane & 15) == 0) scales[row * nblk + (v >> 4)] = (uint8_t)(ex + 127);
+      };
+#pragma unroll
+      for (int j = 0; j + 1 < NS; j += 2) {
+        const uint4 o0 = stream(j), o1 = stream(j + 1);
+        int ex[2];
+        uint2 c8[2];
+        ckpt_block16x2<false>(o0, o1, mask, ex, c8);
+        store(j, o0, c8[0], ex[0]);
+        store(j + 1, o1, c8[1], ex[1]);
+      }
+      if constexpr (NS % 2 == 1) {
+        const uint4 o = stream(NS - 1);
+        uint2 c8;
+        const int ex = ckpt_block16<false>(o, mask, c8);
+        store(NS - 1, o, c8, ex);
       }
     }
     t = tn;
@@ -226,7 +270,7 @@ cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* re
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int resident = known[dev].load(std::memory_order_relaxed);
-  constexpr size_t smem = 2 * (kCkptThreads / 32) * sizeof(PcStage<NS>);
+  constexpr size_t smem = (kCkptThreads / 32) * sizeof(PcWarp<NS>);
   if (resident == 0) {
     int per_sm = 0;
     if ((e = cudaFuncSetAttribute(post_ckpt_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=

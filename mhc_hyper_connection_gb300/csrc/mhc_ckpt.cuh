@@ -120,6 +120,28 @@ __device__ __forceinline__ int ckpt_block16(uint4 v, uint32_t mask, uint2& codes
   return e;
 }
 
+// Two rows' blocks held by the 16 lanes of `mask`: the maxima travel as one
+// packed pair.  Exponents and this lane's codes.
+template <bool F16>
+__device__ __forceinline__ void ckpt_block16x2(uint4 v0, uint4 v1, uint32_t mask, int (&e)[2], uint2 (&codes)[2]) {
+  const uint32_t a = absmax8<F16>(v0), b = absmax8<F16>(v1);
+  uint32_t w = max2<F16>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));     // (max of v0, max of v1)
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) w = max2<F16>(w, __shfl_xor_sync(mask, w, o));
+  using X = XType<F16>;
+  const float2 f = X::to_f2(*reinterpret_cast<typename X::T2*>(&w));
+  const float inf = __int_as_float(0x7F800000);
+  if (!(f.x < inf) || !(f.y < inf)) {
+    e[0] = ckpt_block16<F16>(v0, mask, codes[0]);
+    e[1] = ckpt_block16<F16>(v1, mask, codes[1]);
+    return;
+  }
+  e[0] = ckpt_exponent<F16>(f.x);
+  e[1] = ckpt_exponent<F16>(f.y);
+  codes[0] = ckpt_encode8<F16>(v0, pow2_f32(-e[0]));
+  codes[1] = ckpt_encode8<F16>(v1, pow2_f32(-e[1]));
+}
+
 // Asynchronous copies of 16 or 8 bytes to shared memory, zeros where `in` is
 // false; each thread waits for its own groups and reads only what it copied.
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool in, uint64_t policy) {

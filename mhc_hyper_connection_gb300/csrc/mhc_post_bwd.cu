@@ -22,6 +22,7 @@ constexpr int kPbThreads = 256;
 constexpr int kPbWarps = kPbThreads / 32;
 
 struct PostBwdParams {
+  int codes16;                         // rows of codes are 16-byte aligned
   int T, D, wpt;                       // wpt: warps that share a token (a power of two up to kPbWarps)
   const __nv_bfloat16 *g, *x, *res;
   const uint8_t *codes, *scales;
@@ -252,19 +253,21 @@ __device__ __noinline__ uint4 direct_piece(uint4 g, const float* coef, int src, 
   return pack8(o);
 }
 
-// A warp's 128 columns in shared memory, each lane's own pieces: four of g, of
-// the residual (16 bytes, or 8 of codes) and, in the lanes with an x row, of x.
-// The next 128 columns are copied while these are worked on.
+// A warp's 128 columns in shared memory: each lane's own pieces of g, of the
+// residual and, in the lanes with an x row, of x; codes as rows of 128 bytes, 160
+// apart (free of bank conflicts), copied 16 bytes at a time where their rows are
+// so aligned (n = 8, T = 16384, D = 2048: 238 us, with 8 bytes 248).  The next
+// 128 columns are copied while these are worked on.
 template <int NS, bool kCkpt>
 struct PbStage {
   static constexpr int kTok = NS <= 4 ? 2 : 1;                       // tokens of a warp
   uint4 g[4][32];
   uint4 x[4][4 * kTok];
-  uint2 r[4][32 * (kCkpt ? 1 : 2)];
+  uint4 r[kCkpt ? 80 : 128];
 };
 
 template <int NS, bool kCkpt>
-__global__ void __launch_bounds__(kPbThreads, kCkpt ? 3 : 2) post_bwd_mma_kernel(const PostBwdParams p) {
+__global__ void __launch_bounds__(kPbThreads, 2) post_bwd_mma_kernel(const PostBwdParams p) {
   using Stage = PbStage<NS, kCkpt>;
   constexpr int kTok = Stage::kTok, kStride = 8 / kTok;              // rows between the tokens
   extern __shared__ __align__(16) uint8_t pb_smem[];
@@ -308,8 +311,16 @@ __global__ void __launch_bounds__(kPbThreads, kCkpt ? 3 : 2) post_bwd_mma_kernel
       for (int u = 0; u < 4; ++u) {
         const bool in = u * 32 < left && row_ok;
         copy16(&st.g[u][lane], in ? gp + c0 + u * 32 : p.g, in, once);
-        if constexpr (kCkpt) copy8(&st.r[u][lane], in ? p.codes + row * D + q * 8 + c0 + u * 32 : p.codes, in, once);
-        else copy16(&st.r[u][2 * lane], in ? p.res + row * D + q * 8 + c0 + u * 32 : p.res, in, once);
+        if constexpr (kCkpt) {
+          uint8_t* cr = reinterpret_cast<uint8_t*>(st.r) + r * 160;
+          if (!p.codes16) {
+            copy8(cr + u * 32 + q * 8, in ? p.codes + row * D + q * 8 + c0 + u * 32 : p.codes, in, once);
+          } else if (u < 2) {
+            const int b = u * 64 + q * 16;
+            const bool cin = row_ok && c0 + b < D;
+            copy16(cr + b, cin ? p.codes + row * D + c0 + b : p.codes, cin, once);
+          }
+        } else copy16(&st.r[u * 32 + lane], in ? p.res + row * D + q * 8 + c0 + u * 32 : p.res, in, once);
         if (r < kTok) {
           const bool xin = u * 32 < left && x_ok;
           copy16(&st.x[u][lane], xin ? xp + c0 + u * 32 : p.x, xin, once);
@@ -322,9 +333,11 @@ __global__ void __launch_bounds__(kPbThreads, kCkpt ? 3 : 2) post_bwd_mma_kernel
     for (int blk = sub; blk < nblk; blk += wpt, buf ^= 1) {          // blocks of 128 columns
       const int c0 = blk * 128, left = D - c0 - q * 8;
       const Stage& st = stages[buf];
+      if (kCkpt) __syncwarp();                                       // codes are read by other lanes than copied them
       if (blk + wpt < nblk) fetch(blk + wpt, stages[buf ^ 1]);
       copies_commit();
       copies_wait<1>();
+      if (kCkpt) __syncwarp();
       float scale = 1.0f;
       if (kCkpt && row_ok) scale = ckpt_scale(__ldg(p.scales + row * nblk + blk));
       float dot[4];
@@ -335,14 +348,14 @@ __global__ void __launch_bounds__(kPbThreads, kCkpt ? 3 : 2) post_bwd_mma_kernel
         const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, xw[4] = {xv.x, xv.y, xv.z, xv.w};
         uint32_t rw[4];
         if constexpr (kCkpt) {
-          const uint2 cv = st.r[u][lane];
+          const uint2 cv = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(st.r) + r * 160 + u * 32 + q * 8);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {                              // a code's value is exact in bf16
             const float2 f = e4m3x2_f2((e < 2 ? cv.x : cv.y) >> (16 * (e & 1)));
             rw[e] = bf16x2(f.x, f.y);
           }
         } else {
-          const uint4 rv = *reinterpret_cast<const uint4*>(&st.r[u][2 * lane]);
+          const uint4 rv = st.r[u * 32 + lane];
           rw[0] = rv.x;
           rw[1] = rv.y;
           rw[2] = rv.z;
@@ -472,6 +485,7 @@ extern "C" mhc_status_t mhc_post_backward_run(const mhc_post_bwd_args* a, void* 
   p.x = static_cast<const __nv_bfloat16*>(a->x);
   p.res = static_cast<const __nv_bfloat16*>(a->residual);
   p.codes = static_cast<const uint8_t*>(a->codes);
+  p.codes16 = D % 16 == 0 && aligned(a->codes, 16);
   p.scales = static_cast<const uint8_t*>(a->scales);
   p.post = a->post;
   p.comb = a->comb;
