@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kCkptThreads)
 // vectors of eight columns of each tensor, copied to its own places in shared
 // memory one piece ahead, so that the copies of a piece run under the work on
 // the one before (with loads into registers instead, at the 16 warps per SM that
-// they leave, T = 4096, n = 4, D = 4096 took 83 us where it takes 67 now, 81% of
-// measured HBM).
+// they leave, T = 4096, n = 4, D = 4096 took 83 us where it takes 61.6 now, 89% of
+// measured HBM; n = 8, T = 16384, D = 2048: 250 us, 83%).
 //
 // Two columns share a packed fp32 instruction (the same rounding as two plain
 // ones); the coefficients lie in shared memory, each twice.
@@ -146,7 +146,7 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v) {
 }
 
 template <int NS>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kCkptThreads, 2)
     post_ckpt_kernel(int T, int D, const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ res,
                      const float* __restrict__ post, const float* __restrict__ comb, __nv_bfloat16* __restrict__ out,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -282,10 +282,16 @@ cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* re
     resident = (per_sm > 0 ? per_sm : 1) * (device_info(dev).sms > 0 ? device_info(dev).sms : 1);
     known[dev].store(resident, std::memory_order_relaxed);
   }
-  long long grid = resident;
-  const long long cols = 256 * PcStage<NS>::kV;
-  const long long need = (T * ((D + cols - 1) / cols) + kCkptThreads / 32 - 1) / (kCkptThreads / 32);   // a piece a warp
-  if (grid > need) grid = need;
+  // Runs of kRun pieces keep the rows in flight near one another in memory and
+  // the last round short (T = 32768, n = 4, D = 7168: 895 us with one run per
+  // resident warp, 771 with runs of 8, 758 with 4); where they would leave SMs
+  // idle, equal shares of all.
+  constexpr int kRun = 4;
+  const long long cols = 256 * PcStage<NS>::kV, warps = kCkptThreads / 32;
+  const long long pieces = T * ((D + cols - 1) / cols);
+  long long grid = (pieces + kRun * warps - 1) / (kRun * warps);
+  if (grid < resident) grid = resident;
+  if (grid * warps > pieces) grid = (pieces + warps - 1) / warps;
   post_ckpt_kernel<NS><<<(int)grid, kCkptThreads, smem, s>>>(
       (int)T, (int)D, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res), post, comb,
       static_cast<__nv_bfloat16*>(out), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));

@@ -13,10 +13,14 @@ struct GemmShape {
   int band;                    // tile rows walked together, column by column
   uint32_t idesc;
   int a_mn, b_mn;              // operand stored MN-major
-  uint32_t* err;               // device error word
+};
+
+// What the launches of one call share.
+struct FfnCall {
+  uint32_t* err;               // device error word; the next word counts tiles (ffn_gemm_kernel)
   uint64_t wait_ns;
-  int withhold;                // test hook: leave out the last copy of CTA 0
-  int clear_err;               // first kernel of a call: clear the error word
+  int withhold;                // test hook of the call's last launch
+  int sms;
 };
 
 // Up to this many tokens the few-token kernels run (mhc_ffn_few.cuh).
@@ -27,7 +31,8 @@ constexpr int kFewTokens = 128;
 struct FfnFwdLaunch {
   CUtensorMap x, wgu, a, wd;
   GemmShape gu, down;
-  int T, D, F, act, kept, sms;
+  FfnCall call;
+  int T, D, F, act, kept;
   void *a_buf, *y, *gate_up, *codes, *scales;
 };
 cudaError_t launch_ffn_forward(const FfnFwdLaunch& L, bool f16, cudaStream_t s);
@@ -39,7 +44,8 @@ struct FfnBwdLaunch {
   CUtensorMap gy_mn, a_mn;         // grad_w_down = grad_y^T a
   // for few tokens gy_k and gg_k have boxes of all tokens
   GemmShape ga, gx, gwgu, gwd;
-  int T, D, F, act, kept, sms;
+  FfnCall call;
+  int T, D, F, act, kept;
   const void *gate_up, *codes, *scales;
   void *gg_buf, *a_buf, *grad_x, *grad_w_gate_up, *grad_w_down;
 };

@@ -64,8 +64,7 @@ bool map_2d(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool a_mn, bool b_mn, uint32_t* err,
-                uint32_t wait_us) {
+GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool a_mn, bool b_mn) {
   GemmShape g;
   g.M = (int)M;
   g.N = (int)N;
@@ -82,11 +81,16 @@ GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool 
   g.band = g.band < 4 ? 4 : g.band > 16 ? 16 : g.band;
   g.a_mn = a_mn;
   g.b_mn = b_mn;
-  g.err = err;
-  g.wait_ns = wait_us ? (uint64_t)wait_us * 1000u : 2000000000ull;
-  g.withhold = 0;
-  g.clear_err = 0;
   return g;
+}
+
+FfnCall call(uint32_t* err, uint32_t wait_us, int withhold, int sms) {
+  FfnCall c;
+  c.err = err;
+  c.wait_ns = wait_us ? (uint64_t)wait_us * 1000u : 2000000000ull;
+  c.withhold = withhold;
+  c.sms = sms;
+  return c;
 }
 
 mhc_status_t device(int* sms) {
@@ -140,10 +144,11 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
   FfnFwdLaunch L;
-  if ((st = device(&L.sms)) != MHC_OK) return st;
+  int sms = 0;
+  if ((st = device(&sms)) != MHC_OK) return st;
   const bool f16 = a->dtype == MHC_DTYPE_FP16;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  L.call = call(reinterpret_cast<uint32_t*>(ws), a->wait_limit_us, a->withhold_copy, sms);
   L.T = (int)T;
   L.D = (int)D;
   L.F = (int)F;
@@ -158,10 +163,8 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   if (!map_2d(&L.x, a->x, f16, D, T, 1, tok_box) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
       !map_2d(&L.a, L.a_buf, f16, F, T, 1, tok_box) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, kFfnBoxK))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
-  L.gu = shape(T, F, D, 128, f16, false, false, err, a->wait_limit_us);
-  L.down = shape(T, D, F, kFfnTileN, f16, false, false, err, a->wait_limit_us);
-  L.gu.clear_err = 1;
-  L.down.withhold = a->withhold_copy;
+  L.gu = shape(T, F, D, 128, f16, false, false);
+  L.down = shape(T, D, F, kFfnTileN, f16, false, false);
   const cudaError_t e = launch_ffn_forward(L, f16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;
@@ -197,10 +200,11 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
   FfnBwdLaunch L;
-  if ((st = device(&L.sms)) != MHC_OK) return st;
+  int sms = 0;
+  if ((st = device(&sms)) != MHC_OK) return st;
   const bool f16 = a->dtype == MHC_DTYPE_FP16;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  L.call = call(reinterpret_cast<uint32_t*>(ws), a->wait_limit_us, a->withhold_copy, sms);
   L.T = (int)T;
   L.D = (int)D;
   L.F = (int)F;
@@ -220,13 +224,10 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
       !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxMn) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, kFfnBoxMn) ||
       !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, kFfnBoxMn) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
-  const uint32_t w = a->wait_limit_us;
-  L.ga = shape(T, F, D, kFfnTileN, f16, false, true, err, w);
-  L.gx = shape(T, D, 2 * F, kFfnTileN, f16, false, true, err, w);
-  L.gwgu = shape(2 * F, D, T, kFfnTileN, f16, true, true, err, w);
-  L.gwd = shape(D, F, T, kFfnTileN, f16, true, true, err, w);
-  L.ga.clear_err = 1;
-  L.gwd.withhold = a->withhold_copy;
+  L.ga = shape(T, F, D, kFfnTileN, f16, false, true);
+  L.gx = shape(T, D, 2 * F, kFfnTileN, f16, false, true);
+  L.gwgu = shape(2 * F, D, T, kFfnTileN, f16, true, true);
+  L.gwd = shape(D, F, T, kFfnTileN, f16, true, true);
   const cudaError_t e = launch_ffn_backward(L, f16, s);
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward backward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;

@@ -15,7 +15,7 @@ cudaError_t dgate(const FfnBwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<false>(L.gy_k, L.wd_mn, L.ga, e, L.sms, s);
+  return launch_gemm<false, 1>({{L.gy_k, L.wd_mn, L.ga}}, L.call, e, true, false, s);
 }
 
 template <bool F16, int kKept>
@@ -28,7 +28,7 @@ cudaError_t few_dgate(const FfnBwdLaunch& L, cudaStream_t s) {
   e.a = static_cast<uint16_t*>(L.a_buf);
   e.F = L.F;
   e.act = L.act;
-  return launch_few(L.wd_mn, L.gy_k, few_shape(L.ga, L.F, L.T, F16, true), e, s);
+  return launch_few(L.wd_mn, L.gy_k, few_shape(L.ga, L.call, L.F, L.T, F16, true, true, false), e, s);
 }
 
 template <bool F16>
@@ -37,26 +37,34 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
   cudaError_t e = few ? (L.kept == 1 ? few_dgate<F16, 1>(L, s) : few_dgate<F16, 2>(L, s))
                       : (L.kept == 1 ? dgate<F16, 1>(L, s) : dgate<F16, 2>(L, s));
   if (e != cudaSuccess) return e;
-  EpiStore<F16> o;
-  o.N = L.D;
+  const GemmOperands gx = {L.gg_k, L.wgu_mn, L.gx}, gwgu = {L.gg_mn, L.x_mn, L.gwgu}, gwd = {L.gy_mn, L.a_mn, L.gwd};
+  const StoreTo to_x = {static_cast<uint16_t*>(L.grad_x), L.T, L.D};
+  const StoreTo to_wgu = {static_cast<uint16_t*>(L.grad_w_gate_up), 2 * L.F, L.D};
+  const StoreTo to_wd = {static_cast<uint16_t*>(L.grad_w_down), L.D, L.F};
   if (few) {
     FewStore<F16> f;
-    f.out = static_cast<uint16_t*>(L.grad_x);
+    f.out = to_x.out;
     f.N = L.D;
-    e = launch_few(L.wgu_mn, L.gg_k, few_shape(L.gx, L.D, L.T, F16, true), f, s);
-  } else {
-    o.out = static_cast<uint16_t*>(L.grad_x);
-    o.M = L.T;
-    e = launch_gemm<false>(L.gg_k, L.wgu_mn, L.gx, o, L.sms, s);
+    e = launch_few(L.wgu_mn, L.gg_k, few_shape(L.gx, L.call, L.D, L.T, F16, true, false, false), f, s);
+    if (e != cudaSuccess) return e;
+    EpiStore<F16, 2> o;
+    o.to[0] = to_wgu;
+    o.to[1] = to_wd;
+    return launch_gemm<false, 2>({{gwgu, gwd}}, L.call, o, false, true, s);
   }
-  if (e != cudaSuccess) return e;
-  o.out = static_cast<uint16_t*>(L.grad_w_gate_up);
-  o.M = 2 * L.F;
-  if ((e = launch_gemm<false>(L.gg_mn, L.x_mn, L.gwgu, o, L.sms, s)) != cudaSuccess) return e;
-  o.out = static_cast<uint16_t*>(L.grad_w_down);
-  o.M = L.D;
-  o.N = L.F;
-  return launch_gemm<false>(L.gy_mn, L.a_mn, L.gwd, o, L.sms, s);
+  // The three products that follow are independent: one launch, tiles of the
+  // deepest first.
+  EpiStore<F16, 3> o;
+  if (L.gx.kiters >= L.gwgu.kiters) {
+    o.to[0] = to_x;
+    o.to[1] = to_wgu;
+    o.to[2] = to_wd;
+    return launch_gemm<false, 3>({{gx, gwgu, gwd}}, L.call, o, false, true, s);
+  }
+  o.to[0] = to_wgu;
+  o.to[1] = to_wd;
+  o.to[2] = to_x;
+  return launch_gemm<false, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
 }
 
 }  // namespace

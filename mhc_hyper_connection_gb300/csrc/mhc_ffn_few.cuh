@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 "and of fewer, with shares rounded up");
 
   if (threadIdx.x == 0) {
-    if (g.first && blockIdx.x == 0) *g.err = 0u;          // as in ffn_gemm_kernel
+    if (g.first && blockIdx.x == 0) g.err[0] = g.err[1] = 0u;   // as in ffn_gemm_kernel
     for (int s = 0; s < stages; ++s) {
       mbar_init(&tail->full[s], 1);
       mbar_init(&tail->empty[s], 1);
@@ -370,7 +370,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 }
 
 // The few-token shape of a product whose weights have `rows` rows.
-inline FewShape few_shape(const GemmShape& g, int rows, int T, bool f16, bool w_mn = false) {
+inline FewShape few_shape(const GemmShape& g, const FfnCall& call, int rows, int T, bool f16, bool w_mn, bool first,
+                          bool last) {
   FewShape w = {};
   w.rows = rows;
   w.T = T;
@@ -380,10 +381,10 @@ inline FewShape few_shape(const GemmShape& g, int rows, int T, bool f16, bool w_
   w.a_mn = w_mn ? 1 : 0;
   w.idesc = f16 ? idesc_f16(kFewRows, w.nt) : idesc_bf16(kFewRows, w.nt);
   if (w_mn) w.idesc |= 1u << 15;
-  w.err = g.err;
-  w.wait_ns = g.wait_ns;
-  w.withhold = g.withhold;
-  w.first = g.clear_err;
+  w.err = call.err;
+  w.wait_ns = call.wait_ns;
+  w.withhold = last ? call.withhold : 0;
+  w.first = first ? 1 : 0;
   return w;
 }
 

@@ -14,18 +14,16 @@ cudaError_t gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<true>(L.x, L.wgu, L.gu, e, L.sms, s);
+  return launch_gemm<true, 1>({{L.x, L.wgu, L.gu}}, L.call, e, true, false, s);
 }
 
 template <bool F16>
 cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
   const cudaError_t e = L.kept == 0 ? gate_up<F16, 0>(L, s) : L.kept == 1 ? gate_up<F16, 1>(L, s) : gate_up<F16, 2>(L, s);
   if (e != cudaSuccess) return e;
-  EpiStore<F16> o;
-  o.out = static_cast<uint16_t*>(L.y);
-  o.M = L.T;
-  o.N = L.D;
-  return launch_gemm<false>(L.a, L.wd, L.down, o, L.sms, s);
+  EpiStore<F16, 1> o;
+  o.to[0] = {static_cast<uint16_t*>(L.y), L.T, L.D};
+  return launch_gemm<false, 1>({{L.a, L.wd, L.down}}, L.call, o, false, true, s);
 }
 
 template <bool F16, int kKept>
@@ -37,7 +35,7 @@ cudaError_t few_gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
   e.scales = static_cast<uint8_t*>(L.scales);
   e.F = L.F;
   e.act = L.act;
-  return launch_few(L.wgu, L.x, few_shape(L.gu, L.F, L.T, F16), e, s);
+  return launch_few(L.wgu, L.x, few_shape(L.gu, L.call, L.F, L.T, F16, false, true, false), e, s);
 }
 
 template <bool F16>
@@ -49,7 +47,7 @@ cudaError_t forward_few(const FfnFwdLaunch& L, cudaStream_t s) {
   FewStore<F16> o;
   o.out = static_cast<uint16_t*>(L.y);
   o.N = L.D;
-  return launch_few(L.wd, L.a, few_shape(L.down, L.D, L.T, F16), o, s);
+  return launch_few(L.wd, L.a, few_shape(L.down, L.call, L.D, L.T, F16, false, false, true), o, s);
 }
 
 }  // namespace

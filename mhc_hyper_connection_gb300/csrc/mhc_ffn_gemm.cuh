@@ -10,6 +10,12 @@
 // products for both into one of two tensor-memory accumulators; and in each CTA
 // two groups of four warps read its 128 rows back alternately and run the
 // epilogue, so that a tile's epilogue overlaps the next tile's products.
+//
+// A launch may hold several products (the backward's last three).  Their tiles
+// differ in depth, so there the pairs draw tile numbers from a counter in the
+// workspace: the even CTA's producer draws one ahead and hands it to the other
+// warps of both CTAs through a small ring.  Which pair forms a tile does not
+// change its bits.
 #pragma once
 
 #include <atomic>
@@ -24,12 +30,26 @@ constexpr int kGemmHalf = 128;             // rows of A and of B that one CTA of
 constexpr int kGemmOpBytes = kGemmHalf * kFfnTileK * 2;
 constexpr int kGemmStageBytes = 2 * kGemmOpBytes;
 
+constexpr int kSchedSlots = 4;
+
 struct GemmTail {
   uint64_t full[kGemmStages], empty[kGemmStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t sched_full[kSchedSlots], sched_empty[kSchedSlots];
   uint64_t mma_done;
   uint32_t tmem_base;
   uint32_t abort;
+  int sched[kSchedSlots];                  // tile numbers, -1: no more
+};
+
+// The products of one launch, in the order of their tiles.
+struct GemmOperands {
+  CUtensorMap a, b;
+  GemmShape g;
+};
+template <int P>
+struct GemmSet {
+  GemmOperands op[P];
 };
 constexpr size_t kGemmSmem = (size_t)kGemmStages * kGemmStageBytes + 8 * 4096 + sizeof(GemmTail) + 1024;
 
@@ -179,13 +199,18 @@ __device__ __forceinline__ void stage_flush8(const uint8_t* buf, uint8_t* base, 
   __syncwarp();
 }
 
-// out[row, col] = round(acc)
-template <bool F16>
-struct EpiStore {
+// out[row, col] = round(acc), one output per product of the launch
+struct StoreTo {
   uint16_t* out;
   int M, N;
-  // taddr: the warp's accumulator lanes; row0: the row of its lane 0
-  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+};
+template <bool F16, int P>
+struct EpiStore {
+  StoreTo to[P];
+  // which: the product; taddr: the warp's accumulator lanes; row0: the row of its lane 0
+  __device__ __forceinline__ void tile(int which, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+    uint16_t* out = to[which].out;
+    const int M = to[which].M, N = to[which].N;
     const int n0 = tn * kFfnTileN;
 #pragma unroll 1
     for (int c = 0; c < kFfnTileN && n0 + c < N; c += 64) {
@@ -209,7 +234,7 @@ struct EpiGateUp {
   uint16_t *a, *gate_up;
   uint8_t *codes, *scales;
   int T, F, act;
-  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
     const int f0 = tn * 128, rows = T - row0;
 #pragma unroll 1
     for (int c = 0; c < 128 && f0 + c < F; c += 64) {
@@ -325,7 +350,7 @@ struct EpiDgate {
     }
   }
 
-  __device__ __forceinline__ void tile(uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
     const int f0 = tn * kFfnTileN, rows = T - row0;
     Kept k;
     load(k, row0, f0, lane);
@@ -411,11 +436,12 @@ struct EpiDgate {
 // 128 of plane 1 (gate and up); else 256 consecutive rows.  A tile's operands
 // may each be K-major or MN-major (g.a_mn, g.b_mn): a stage holds 128 rows of
 // 128 bytes along the depth, or two blocks of 64 depths x 64 rows.
-template <class Epi, bool kPair>
+template <class Epi, bool kPair, int P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
-    ffn_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const GemmShape g,
-                    const Epi epi) {
+    ffn_gemm_kernel(const __grid_constant__ GemmSet<P> set, const FfnCall call, const int first, const int withhold,
+                    const __grid_constant__ Epi epi) {
   constexpr uint32_t kTmemCols = 512;
+  constexpr bool kDraw = P > 1;                  // tiles drawn from the counter
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* bufs = smem + kGemmStages * kGemmStageBytes;          // one staging buffer per epilogue warp
@@ -423,13 +449,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int ntiles = g.tiles_m * g.tiles_n;
-  Ctl ctl{&tail->abort, g.err, g.wait_ns};
+  int ntiles = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) ntiles += set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+  Ctl ctl{&tail->abort, call.err, call.wait_ns};
 
   if (threadIdx.x == 0) {
     // Cleared here rather than by a launch of its own: a wait of this call
-    // sets it wait_ns after its CTA began at the earliest.
-    if (g.clear_err && blockIdx.x == 0) *g.err = 0u;
+    // sets the word wait_ns after its CTA began at the earliest, and the tile
+    // counter serves a later launch of the call.
+    if (first && blockIdx.x == 0) call.err[0] = call.err[1] = 0u;
     for (int s = 0; s < kGemmStages; ++s) {
       mbar_init(&tail->full[s], 1);
       mbar_init(&tail->empty[s], 1);
@@ -438,11 +467,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       mbar_init(&tail->acc_full[b], 1);
       mbar_init(&tail->acc_empty[b], 8);         // four warps of each CTA
     }
+    for (int b = 0; b < kSchedSlots; ++b) {
+      mbar_init(&tail->sched_full[b], 1);
+      mbar_init(&tail->sched_empty[b], 10);      // MMA issuer, the other producer, four epilogue warps of each CTA
+    }
     mbar_init(&tail->mma_done, 1);
     tail->abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_desc(&ta);
-    tma_prefetch_desc(&tb);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      tma_prefetch_desc(&set.op[i].a);
+      tma_prefetch_desc(&set.op[i].b);
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail->tmem_base)),
@@ -455,6 +491,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   cluster_sync_all();                            // the peer's barriers exist
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
+  pdl_trigger();
+  pdl_wait();                                    // operands, and the counter, are earlier launches'
+
+  // The n-th tile of this pair as the roles see it: its number, or -1 after the
+  // last (and when the wait for it gave up).  One call per n and role.
+  auto tile_of = [&](int n, bool whole_warp) -> int {
+    if constexpr (!kDraw) {
+      const long long t = pair + (long long)n * pairs;
+      return t < ntiles ? (int)t : -1;
+    } else {
+      const int slot = n % kSchedSlots;
+      int t = -1;
+      if (mbar_test_cluster(&tail->sched_full[slot], (uint32_t)(n / kSchedSlots) & 1u) ||
+          wait_slow(&tail->sched_full[slot], (uint32_t)(n / kSchedSlots) & 1u, ctl, kErrClusterWait, true))
+        t = *reinterpret_cast<volatile int*>(&tail->sched[slot]);
+      if (whole_warp) t = __shfl_sync(0xFFFFFFFFu, t, 0);
+      if (!whole_warp || lane == 0) mbar_arrive_remote(&tail->sched_empty[slot], 0);
+      return t;
+    }
+  };
+  // Tile t: its product, row and column.
+  auto locate = [&](int t, int& tm, int& tn) -> int {
+    int which = 0;
+#pragma unroll
+    for (int i = 0; i + 1 < P; ++i) {
+      const int tiles = set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+      if (which == i && t >= tiles) {
+        t -= tiles;
+        which = i + 1;
+      }
+    }
+    tile_coords(set.op[which].g, t, tm, tn);
+    return which;
+  };
 
   if (warp == 0) {
     // ===================================================== TMA producer
@@ -463,35 +533,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       uint32_t ph = 0;
       long long iss = 0;
       bool ok = true;
-      for (int t = pair; t < ntiles && ok; t += pairs) {
+      // Hands tile number t out as the pair's n-th.
+      auto publish = [&](int n, int t) -> bool {
+        const int slot = n % kSchedSlots;
+        if (!wait_slow(&tail->sched_empty[slot], ((uint32_t)(n / kSchedSlots) & 1u) ^ 1u, ctl, kErrClusterWait, true)) return false;
+        *reinterpret_cast<volatile int*>(&tail->sched[slot]) = t;
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(map_cluster(&tail->sched[slot], 1)), "r"(t) : "memory");
+        mbar_arrive(&tail->sched_full[slot]);
+        mbar_arrive_remote(&tail->sched_full[slot], 1);
+        return true;
+      };
+      auto draw = [&]() -> int {
+        const unsigned t = (unsigned)pairs + atomicAdd(call.err + 1, 1u);
+        return t < (unsigned)ntiles ? (int)t : -1;
+      };
+      int cur = -1, next = -1;                   // the numbers of tiles n and n + 1, handed out already
+      if (kDraw && rank == 0) {
+        cur = pair;
+        next = draw();
+        ok = publish(0, cur) && publish(1, next);
+      }
+      for (int n = 0; ok; ++n) {
+        const int t = kDraw && rank == 0 ? cur : tile_of(n, false);
+        if (t < 0) break;
         int tm, tn;
-        tile_coords(g, t, tm, tn);
+        const int which = locate(t, tm, tn);
+        const GemmShape& g = set.op[which].g;
+        const CUtensorMap* ta = &set.op[which].a;
+        const CUtensorMap* tb = &set.op[which].b;
         const int m0 = tm * kFfnTileM + (int)rank * kGemmHalf;
         const int n0 = kPair ? tn * kGemmHalf : tn * kFfnTileN + (int)rank * kGemmHalf;
-        const int plane = kPair ? (int)rank : 0;
-        for (int k = 0; k < g.kiters; ++k) {
+        const int plane = kPair ? (int)rank : 0, kiters = g.kiters, a_mn = g.a_mn, b_mn = g.b_mn;
+        int after = -1;                          // tile n + 2, drawn under this tile's copies
+        if (kDraw && rank == 0 && next >= 0) after = draw();
+        for (int k = 0; k < kiters; ++k) {
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-          // test hook: the first pair leaves out its last chunk, so the waits
-          // on it give up (no copy is left in flight)
-          if (g.withhold && pair == 0 && k == g.kiters - 1 && t + pairs >= ntiles) { ok = false; break; }
+          // test hook: the first pair leaves out the last chunk of its first
+          // tile, so the waits on it give up (no copy is left in flight)
+          if (withhold && pair == 0 && n == 0 && k == kiters - 1) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
           const uint32_t bar = map_cluster(&tail->full[s], 0);
           const int k0 = k * kFfnTileK;
           if (rank == 0) mbar_expect_tx(&tail->full[s], 2 * kGemmStageBytes);   // both CTAs' copies
-          if (g.a_mn) {
-            tma_load_3d_pair(sa, &ta, bar, m0, k0, 0);
-            tma_load_3d_pair(sa + 8192, &ta, bar, m0 + 64, k0, 0);
+          if (a_mn) {
+            tma_load_3d_pair(sa, ta, bar, m0, k0, 0);
+            tma_load_3d_pair(sa + 8192, ta, bar, m0 + 64, k0, 0);
           } else {
-            tma_load_3d_pair(sa, &ta, bar, k0, m0, 0);
+            tma_load_3d_pair(sa, ta, bar, k0, m0, 0);
           }
-          if (g.b_mn) {
-            tma_load_3d_pair(sb, &tb, bar, n0, k0, 0);
-            tma_load_3d_pair(sb + 8192, &tb, bar, n0 + 64, k0, 0);
+          if (b_mn) {
+            tma_load_3d_pair(sb, tb, bar, n0, k0, 0);
+            tma_load_3d_pair(sb + 8192, tb, bar, n0 + 64, k0, 0);
           } else {
-            tma_load_3d_pair(sb, &tb, bar, k0, n0, plane);
+            tma_load_3d_pair(sb, tb, bar, k0, n0, plane);
           }
           ++iss;
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
+        }
+        if (kDraw && rank == 0) {                // after the last tile -1 goes out twice, once for each epilogue group
+          ok = ok && publish(n + 2, after);
+          cur = next;
+          next = after;
         }
       }
       if (rank == 0) {
@@ -500,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           mbar_drain(&tail->full[s], ph);
         }
       }
-      if (!ok) {
+      if (!ok || *ctl.abort) {
         // A wait gave up: copies of this CTA that the even CTA no longer
         // counts get a millisecond to land before the pair leaves together.
         const uint64_t t0 = now_ns();
@@ -510,24 +612,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     // ===================================================== MMA issuer
     if (lane == 0 && rank == 0) {
-      // byte step of sixteen depths, and the distance of the next 64 rows
-      const uint64_t a0 = g.a_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0), b0 = g.b_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0);
-      const uint32_t astep = (g.a_mn ? 2048u : 32u) >> 4, bstep = (g.b_mn ? 2048u : 32u) >> 4;
-      int s = 0, n = 0;
+      int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = pair; t < ntiles && ok; t += pairs, ++n) {
-        const int b = n & 1;
+      for (int n = 0; ok; ++n) {
+        const int t = tile_of(n, false);
+        if (t < 0) break;
+        int tm, tn;
+        const GemmShape& g = set.op[locate(t, tm, tn)].g;
+        // byte step of sixteen depths, and the distance of the next 64 rows
+        const uint64_t a0 = g.a_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0), b0 = g.b_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0);
+        const uint32_t astep = (g.a_mn ? 2048u : 32u) >> 4, bstep = (g.b_mn ? 2048u : 32u) >> 4, idesc = g.idesc;
+        const int b = n & 1, kiters = g.kiters;
         if (!wait_slow(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrClusterWait, true)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(b * kFfnTileN);
-        for (int k = 0; k < g.kiters; ++k) {
+        for (int k = 0; k < kiters; ++k) {
           if (!wait_stage(&tail->full[s], ph, ctl)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = desc_addr(smem + s * kGemmStageBytes), sb = sa + (kGemmOpBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < kFfnTileK / 16; ++ks)
-            mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), g.idesc, (k | ks) ? 1u : 0u);
+            mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), idesc, (k | ks) ? 1u : 0u);
           commit_pair(&tail->empty[s]);
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
@@ -541,15 +647,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else {
     // ===================================================== epilogue
     const int grp = (warp - 2) >> 2, q = warp & 3;
-    const uint32_t row0 = (uint32_t)(q * 32);
-    int n = 0;
-    for (int t = pair; t < ntiles; t += pairs, ++n) {
-      if ((n & 1) != grp) continue;
+    for (int n = grp;; n += 2) {
+      const int t = tile_of(n, true);
+      if (t < 0) break;
       int tm, tn;
-      tile_coords(g, t, tm, tn);
-      if (!wait_bar_sleep(&tail->acc_full[grp], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout)) break;
+      const int which = locate(t, tm, tn);
+      if (!__all_sync(0xFFFFFFFFu, wait_bar_sleep(&tail->acc_full[grp], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout))) break;
       tc_fence_after();
-      epi.tile(tmem_base + (row0 << 16) + (uint32_t)(grp * kFfnTileN),
+      epi.tile(which, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kFfnTileN),
                tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, bufs + (warp - 2) * kStageBuf, lane);
       tc_fence_before();
       __syncwarp();
@@ -568,39 +673,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// Pairs that fit the device at once (some SMs may have no partner), looked up
-// once per kernel and device.
-template <class Kernel>
-int resident_pairs(Kernel* k, int sms) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sms & ~1));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return 0;
-  return n;
-}
-
-template <bool kPair, class Epi>
-cudaError_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const GemmShape& g, const Epi& epi, int sms,
-                        cudaStream_t s) {
-  auto* k = ffn_gemm_kernel<Epi, kPair>;
-  // per device: the shared-memory limit is set and the pairs counted once
+// first: the call's first launch (ordered behind everything before it, clears
+// the error word); later ones start as SMs fall free.  last: takes the test hook.
+template <bool kPair, int P, class Epi>
+cudaError_t launch_gemm(const GemmSet<P>& set, const FfnCall& call, const Epi& epi, bool first, bool last, cudaStream_t s) {
+  auto* k = ffn_gemm_kernel<Epi, kPair, P>;
+  // per device: the shared-memory limit is set, and the pairs that fit at once
+  // counted (some SMs may have no partner)
   static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int pairs = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  int pairs = known[dev].load(std::memory_order_relaxed);
   if (pairs == 0) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
     if (e != cudaSuccess) return e;
-    pairs = resident_pairs(k, sms);
-    if (pairs == 0) return cudaErrorInvalidConfiguration;
-    if (dev >= 0 && dev < 64) known[dev].store(pairs, std::memory_order_relaxed);
+    cfg.gridDim = dim3((unsigned)(call.sms & ~1));
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, k, &cfg)) != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    known[dev].store(pairs, std::memory_order_relaxed);
   }
-  const long long tiles = (long long)g.tiles_m * g.tiles_n;
-  k<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kGemmThreads, kGemmSmem, s>>>(ta, tb, g, epi);
-  return cudaGetLastError();
+  long long tiles = 0;
+  for (int i = 0; i < P; ++i) tiles += (long long)set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = first ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, k, set, call, (const int)first, (const int)(last ? call.withhold : 0), epi);
 }
 
 }  // namespace mhc
