@@ -88,6 +88,15 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
 // Start-address field of an operand descriptor.  A shared-memory address holds
 // the CTA's rank in its upper bits, which would run into the fields above.
 __device__ __forceinline__ uint32_t desc_addr(const void* p) { return (smem_u32(p) & 0x3FFFFu) >> 4; }
+// One lane of a whole warp.  The issuing warp stays together and elects a lane
+// only for the instructions themselves: in a branch of one lane's own, four
+// products and their bookkeeping took 640 clocks, 25% more than they execute
+// for; so they take 535 (forward at T = 4096, D = 4096, F = 8192: 498 -> 456 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // Arrive on the barrier at this offset in both CTAs once the products issued
 // so far are done.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
@@ -611,12 +620,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp == 1) {
     // ===================================================== MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        const int t = tile_of(n, false);
+        const int t = tile_of(n, true);
         if (t < 0) break;
         int tm, tn;
         const GemmShape& g = set.op[locate(t, tm, tn)].g;
@@ -631,17 +640,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (!wait_stage(&tail->full[s], ph, ctl)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = desc_addr(smem + s * kGemmStageBytes), sb = sa + (kGemmOpBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kFfnTileK / 16; ++ks)
-            mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), idesc, (k | ks) ? 1u : 0u);
-          commit_pair(&tail->empty[s]);
+            for (int ks = 0; ks < kFfnTileK / 16; ++ks)
+              mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), idesc, (k | ks) ? 1u : 0u);
+            commit_pair(&tail->empty[s]);
+          }
+          __syncwarp();
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
-        if (ok) commit_pair(&tail->acc_full[b]);
+        if (ok && elect_one()) commit_pair(&tail->acc_full[b]);
+        __syncwarp();
       }
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+      if (elect_one()) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                        smem_u32(&tail->mma_done))
                    : "memory");
+      __syncwarp();
       mbar_drain(&tail->mma_done, 0);
     }
   } else {
