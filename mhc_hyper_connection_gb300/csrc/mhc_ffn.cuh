@@ -9,6 +9,7 @@ namespace mhc {
 // k.  "K-major" operands store k contiguously, "MN-major" ones r.
 struct GemmShape {
   int M, N, K;                 // rows, columns, depth of the product
+  int tile_n;                  // width of a tile: 256 or 128
   int tiles_m, tiles_n, kiters;
   int band;                    // tile rows walked together, column by column
   uint32_t idesc;
@@ -53,5 +54,6 @@ cudaError_t launch_ffn_backward(const FfnBwdLaunch& L, bool f16, cudaStream_t s)
 
 constexpr int kFfnTileM = 256, kFfnTileN = 256, kFfnTileK = 64;
 constexpr uint32_t kFfnBoxK = 128, kFfnBoxMn = 64;   // tensor-map box rows of a K-major / MN-major operand
+                                                       // (half of a tile's width for a K-major B)
 
 }  // namespace mhc

@@ -64,16 +64,30 @@ bool map_2d(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool a_mn, bool b_mn) {
+// Width of the tiles of an M x N product: 128 where that shortens the rounds of
+// tiles.  A narrow tile takes 0.6 of a wide one's time, with an MN-major B 0.7
+// (T = 1021, D = 2048, F = 5512, down product, 32 wide tiles or 64 narrow: forward
+// 75.5 or 68.2 us; T = 256, D = 4096, F = 8192, gate gradients: backward 145.7 or
+// 140.1; T = 1536, D = F = 4096 stays wide: 233 us, narrow 240).
+int tile_width(int64_t M, int64_t N, int sms, bool b_mn) {
+  const int64_t pairs = sms / 2, rows = (M + kFfnTileM - 1) / kFfnTileM;
+  const int64_t wide = (rows * ((N + 255) / 256) + pairs - 1) / pairs, narrow = (rows * ((N + 127) / 128) + pairs - 1) / pairs;
+  return 10 * wide > (b_mn ? 7 : 6) * narrow ? 128 : 256;
+}
+
+// pair_of: rows of B come from two planes (gate and up), 128 columns a tile.
+// alone: the only product of its launch (several in one fill their rounds with
+// one another's tiles and stay wide).
+GemmShape shape(int64_t M, int64_t N, int64_t K, bool pair_of, bool alone, int sms, bool f16, bool a_mn, bool b_mn) {
   GemmShape g;
   g.M = (int)M;
   g.N = (int)N;
   g.K = (int)K;
+  g.tile_n = pair_of || !alone ? kFfnTileN : tile_width(M, N, sms, b_mn);
+  const int64_t step = pair_of ? 128 : g.tile_n;
   g.tiles_m = (int)((M + kFfnTileM - 1) / kFfnTileM);
-  g.tiles_n = (int)((N + tile_n - 1) / tile_n);
+  g.tiles_n = (int)((N + step - 1) / step);
   g.kiters = (int)((K + kFfnTileK - 1) / kFfnTileK);
-  g.idesc = (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-            ((uint32_t)(kFfnTileN >> 3) << 17) | ((uint32_t)(kFfnTileM >> 4) << 24);
   // A band of at most 32 MB of A stays in L2 while B passes by (T = 4096, D =
   // 4096, F = 8192 forward: 506 us with 8 tile rows, 490 with these 16).
   const int64_t row_bytes = K * 2 * kFfnTileM;
@@ -81,6 +95,8 @@ GemmShape shape(int64_t M, int64_t N, int64_t K, int64_t tile_n, bool f16, bool 
   g.band = g.band < 4 ? 4 : g.band > 16 ? 16 : g.band;
   g.a_mn = a_mn;
   g.b_mn = b_mn;
+  g.idesc = (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+            ((uint32_t)(g.tile_n >> 3) << 17) | ((uint32_t)(kFfnTileM >> 4) << 24);
   return g;
 }
 
@@ -159,12 +175,14 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   L.gate_up = a->gate_up;
   L.codes = a->codes;
   L.scales = a->scales;
-  const uint32_t tok_box = T <= kFewTokens ? (uint32_t)((T + 15) & ~int64_t(15)) : kFfnBoxK;
+  L.gu = shape(T, F, D, true, true, sms, f16, false, false);
+  L.down = shape(T, D, F, false, true, sms, f16, false, false);
+  const bool few = T <= kFewTokens;
+  const uint32_t tok_box = few ? (uint32_t)((T + 15) & ~int64_t(15)) : kFfnBoxK;
   if (!map_2d(&L.x, a->x, f16, D, T, 1, tok_box) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
-      !map_2d(&L.a, L.a_buf, f16, F, T, 1, tok_box) || !map_2d(&L.wd, a->w_down, f16, F, D, 1, kFfnBoxK))
+      !map_2d(&L.a, L.a_buf, f16, F, T, 1, tok_box) ||
+      !map_2d(&L.wd, a->w_down, f16, F, D, 1, few ? kFfnBoxK : (uint32_t)L.down.tile_n / 2))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
-  L.gu = shape(T, F, D, 128, f16, false, false);
-  L.down = shape(T, D, F, kFfnTileN, f16, false, false);
   const cudaError_t e = launch_ffn_forward(L, f16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;
@@ -224,10 +242,10 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
       !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxMn) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, kFfnBoxMn) ||
       !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, kFfnBoxMn) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
-  L.ga = shape(T, F, D, kFfnTileN, f16, false, true);
-  L.gx = shape(T, D, 2 * F, kFfnTileN, f16, false, true);
-  L.gwgu = shape(2 * F, D, T, kFfnTileN, f16, true, true);
-  L.gwd = shape(D, F, T, kFfnTileN, f16, true, true);
+  L.ga = shape(T, F, D, false, true, sms, f16, false, true);
+  L.gx = shape(T, D, 2 * F, false, false, sms, f16, false, true);
+  L.gwgu = shape(2 * F, D, T, false, false, sms, f16, true, true);
+  L.gwd = shape(D, F, T, false, false, sms, f16, true, true);
   const cudaError_t e = launch_ffn_backward(L, f16, s);
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward backward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;

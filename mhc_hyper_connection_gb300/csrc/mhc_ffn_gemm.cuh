@@ -8,8 +8,8 @@
 // one warp streams its operand rows into the ring (TMA, 128-byte swizzle, all
 // completing on the even CTA's barriers); one thread of the even CTA issues the
 // products for both into one of two tensor-memory accumulators; and in each CTA
-// two groups of four warps read its 128 rows back alternately and run the
-// epilogue, so that a tile's epilogue overlaps the next tile's products.
+// two groups of four warps read its 128 rows back, half the columns each, and run
+// the epilogue, which overlaps the next tile's products.
 //
 // A launch may hold several products (the backward's last three).  Their tiles
 // differ in depth, so there the pairs draw tile numbers from a counter in the
@@ -216,13 +216,15 @@ struct StoreTo {
 template <bool F16, int P>
 struct EpiStore {
   StoreTo to[P];
-  // which: the product; taddr: the warp's accumulator lanes; row0: the row of its lane 0
-  __device__ __forceinline__ void tile(int which, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
+  // which: the product; taddr: the warp's accumulator lanes; row0: the row of its
+  // lane 0; tn, cols: the tile's column and width; grp: which half of them
+  __device__ __forceinline__ void tile(int which, uint32_t taddr, int row0, int tn, int cols, int grp, uint8_t* buf,
+                                       int lane) const {
     uint16_t* out = to[which].out;
     const int M = to[which].M, N = to[which].N;
-    const int n0 = tn * kFfnTileN;
+    const int n0 = tn * cols;
 #pragma unroll 1
-    for (int c = 0; c < kFfnTileN && n0 + c < N; c += 64) {
+    for (int c = grp * (cols / 2); c < (grp + 1) * (cols / 2) && n0 + c < N; c += 64) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
@@ -243,10 +245,9 @@ struct EpiGateUp {
   uint16_t *a, *gate_up;
   uint8_t *codes, *scales;
   int T, F, act;
-  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
-    const int f0 = tn * 128, rows = T - row0;
-#pragma unroll 1
-    for (int c = 0; c < 128 && f0 + c < F; c += 64) {
+  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, int, int grp, uint8_t* buf, int lane) const {
+    const int f0 = tn * 128, rows = T - row0, c = grp * 64;
+    if (f0 + c < F) {
       const int bytes = min(64, F - f0 - c) * 2;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -276,8 +277,8 @@ struct EpiGateUp {
     }
     if constexpr (kKept == 2) {
       const int nblk = (F + kCkptBlock - 1) / kCkptBlock;
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
+      {
+        const int p = grp;                       // one group the gate's blocks, the other the up's
         float amax = 0.0f;                       // columns beyond F hold zeros (or NaN)
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
@@ -359,12 +360,13 @@ struct EpiDgate {
     }
   }
 
-  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, uint8_t* buf, int lane) const {
-    const int f0 = tn * kFfnTileN, rows = T - row0;
+  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, int cols, int grp, uint8_t* buf,
+                                       int lane) const {
+    const int f0 = tn * cols, rows = T - row0, c0 = grp * (cols / 2), c1 = c0 + cols / 2;
     Kept k;
-    load(k, row0, f0, lane);
+    load(k, row0, f0 + c0, lane);
 #pragma unroll 1
-    for (int c = 0; c < kFfnTileN && f0 + c < F; c += 32) {
+    for (int c = c0; c < c1 && f0 + c < F; c += 32) {
       const int f = f0 + c;
       __syncwarp();
 #pragma unroll
@@ -373,7 +375,7 @@ struct EpiDgate {
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(buf + sw128(i * 8 + (lane >> 2), p * 4 + (lane & 3))) = k.v[p][i];
       const float s0 = ckpt_scale(k.s[0]), s1 = ckpt_scale(k.s[1]);
-      if (c + 32 < kFfnTileN) load(k, row0, f + 32, lane);
+      if (c + 32 < c1) load(k, row0, f + 32, lane);
       float ga[32];
       tmem_ld32(taddr + c, ga);
       __syncwarp();
@@ -474,11 +476,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail->acc_full[b], 1);
-      mbar_init(&tail->acc_empty[b], 8);         // four warps of each CTA
+      mbar_init(&tail->acc_empty[b], 16);        // eight warps of each CTA
     }
     for (int b = 0; b < kSchedSlots; ++b) {
       mbar_init(&tail->sched_full[b], 1);
-      mbar_init(&tail->sched_empty[b], 10);      // MMA issuer, the other producer, four epilogue warps of each CTA
+      mbar_init(&tail->sched_empty[b], 18);      // MMA issuer, the other producer, eight epilogue warps of each CTA
     }
     mbar_init(&tail->mma_done, 1);
     tail->abort = 0u;
@@ -571,7 +573,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const CUtensorMap* ta = &set.op[which].a;
         const CUtensorMap* tb = &set.op[which].b;
         const int m0 = tm * kFfnTileM + (int)rank * kGemmHalf;
-        const int n0 = kPair ? tn * kGemmHalf : tn * kFfnTileN + (int)rank * kGemmHalf;
+        const int half_n = g.tile_n / 2;
+        const int n0 = kPair ? tn * kGemmHalf : tn * g.tile_n + (int)rank * half_n;
+        const uint32_t bytes = 2u * (uint32_t)(kGemmOpBytes + half_n * kFfnTileK * 2);   // of both CTAs
         const int plane = kPair ? (int)rank : 0, kiters = g.kiters, a_mn = g.a_mn, b_mn = g.b_mn;
         int after = -1;                          // tile n + 2, drawn under this tile's copies
         if (kDraw && rank == 0 && next >= 0) after = draw();
@@ -583,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
           const uint32_t bar = map_cluster(&tail->full[s], 0);
           const int k0 = k * kFfnTileK;
-          if (rank == 0) mbar_expect_tx(&tail->full[s], 2 * kGemmStageBytes);   // both CTAs' copies
+          if (rank == 0) mbar_expect_tx(&tail->full[s], bytes);
           if (a_mn) {
             tma_load_3d_pair(sa, ta, bar, m0, k0, 0);
             tma_load_3d_pair(sa + 8192, ta, bar, m0 + 64, k0, 0);
@@ -592,14 +596,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           }
           if (b_mn) {
             tma_load_3d_pair(sb, tb, bar, n0, k0, 0);
-            tma_load_3d_pair(sb + 8192, tb, bar, n0 + 64, k0, 0);
+            if (half_n > 64) tma_load_3d_pair(sb + 8192, tb, bar, n0 + 64, k0, 0);
           } else {
             tma_load_3d_pair(sb, tb, bar, k0, n0, plane);
           }
           ++iss;
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
-        if (kDraw && rank == 0) {                // after the last tile -1 goes out twice, once for each epilogue group
+        if (kDraw && rank == 0) {                // after the last tile: -1
           ok = ok && publish(n + 2, after);
           cur = next;
           next = after;
@@ -661,18 +665,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else {
     // ===================================================== epilogue
     const int grp = (warp - 2) >> 2, q = warp & 3;
-    for (int n = grp;; n += 2) {
+    for (int n = 0;; ++n) {
       const int t = tile_of(n, true);
       if (t < 0) break;
       int tm, tn;
-      const int which = locate(t, tm, tn);
-      if (!__all_sync(0xFFFFFFFFu, wait_bar_sleep(&tail->acc_full[grp], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout))) break;
+      const int which = locate(t, tm, tn), b = n & 1;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar_sleep(&tail->acc_full[b], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout))) break;
       tc_fence_after();
-      epi.tile(which, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kFfnTileN),
-               tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, bufs + (warp - 2) * kStageBuf, lane);
+      epi.tile(which, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN),
+               tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, set.op[which].g.tile_n, grp,
+               bufs + (warp - 2) * kStageBuf, lane);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(&tail->acc_empty[grp], 0);
+      if (lane == 0) mbar_arrive_remote(&tail->acc_empty[b], 0);
     }
   }
 
