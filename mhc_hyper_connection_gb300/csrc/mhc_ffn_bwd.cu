@@ -15,7 +15,7 @@ cudaError_t dgate(const FfnBwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<false, 1>({{L.gy_k, L.wd_mn, L.ga}}, L.call, e, true, false, s);
+  return launch_gemm<false, false, 1>({{L.gy_k, L.wd_mn, L.ga}}, L.call, e, true, false, s);
 }
 
 template <bool F16, int kKept>
@@ -50,7 +50,7 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
     EpiStore<F16, 2> o;
     o.to[0] = to_wgu;
     o.to[1] = to_wd;
-    return launch_gemm<false, 2>({{gwgu, gwd}}, L.call, o, false, true, s);
+    return launch_gemm<false, false, 2>({{gwgu, gwd}}, L.call, o, false, true, s);
   }
   // The three products that follow are independent: one launch, tiles of the
   // deepest first.
@@ -59,12 +59,12 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
     o.to[0] = to_x;
     o.to[1] = to_wgu;
     o.to[2] = to_wd;
-    return launch_gemm<false, 3>({{gx, gwgu, gwd}}, L.call, o, false, true, s);
+    return launch_gemm<false, true, 3>({{gx, gwgu, gwd}}, L.call, o, false, true, s);
   }
   o.to[0] = to_wgu;
   o.to[1] = to_wd;
   o.to[2] = to_x;
-  return launch_gemm<false, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
+  return launch_gemm<false, true, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
 }
 
 }  // namespace

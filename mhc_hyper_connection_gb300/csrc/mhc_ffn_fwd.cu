@@ -14,7 +14,7 @@ cudaError_t gate_up(const FfnFwdLaunch& L, cudaStream_t s) {
   e.T = L.T;
   e.F = L.F;
   e.act = L.act;
-  return launch_gemm<true, 1>({{L.x, L.wgu, L.gu}}, L.call, e, true, false, s);
+  return launch_gemm<true, false, 1>({{L.x, L.wgu, L.gu}}, L.call, e, true, false, s);
 }
 
 template <bool F16>
@@ -23,7 +23,7 @@ cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   EpiStore<F16, 1> o;
   o.to[0] = {static_cast<uint16_t*>(L.y), L.T, L.D};
-  return launch_gemm<false, 1>({{L.a, L.wd, L.down}}, L.call, o, false, true, s);
+  return launch_gemm<false, false, 1>({{L.a, L.wd, L.down}}, L.call, o, false, true, s);
 }
 
 template <bool F16, int kKept>

@@ -11,9 +11,8 @@
 // two groups of four warps read its 128 rows back, half the columns each, and run
 // the epilogue, which overlaps the next tile's products.
 //
-// A launch may hold several products (the backward's last three).  Their tiles
-// differ in depth, so there the pairs draw tile numbers from a counter in the
-// workspace: the even CTA's producer draws one ahead and hands it to the other
+// A launch may hold several products (the backward's last).  Where their tiles
+// differ in depth the pairs draw tile numbers from a counter in the workspace: the even CTA's producer draws one ahead and hands it to the other
 // warps of both CTAs through a small ring.  Which pair forms a tile does not
 // change its bits.
 #pragma once
@@ -447,12 +446,13 @@ struct EpiDgate {
 // 128 of plane 1 (gate and up); else 256 consecutive rows.  A tile's operands
 // may each be K-major or MN-major (g.a_mn, g.b_mn): a stage holds 128 rows of
 // 128 bytes along the depth, or two blocks of 64 depths x 64 rows.
-template <class Epi, bool kPair, int P>
+// kDraw: tiles are drawn from the counter, else dealt out in turn (products of
+// one depth: nothing to balance, and no wait for the counter).
+template <class Epi, bool kPair, int P, bool kDraw>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ GemmSet<P> set, const FfnCall call, const int first, const int withhold,
                     const __grid_constant__ Epi epi) {
   constexpr uint32_t kTmemCols = 512;
-  constexpr bool kDraw = P > 1;                  // tiles drawn from the counter
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* bufs = smem + kGemmStages * kGemmStageBytes;          // one staging buffer per epilogue warp
@@ -694,9 +694,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
 // first: the call's first launch (ordered behind everything before it, clears
 // the error word); later ones start as SMs fall free.  last: takes the test hook.
-template <bool kPair, int P, class Epi>
+template <bool kPair, bool kDraw, int P, class Epi>
 cudaError_t launch_gemm(const GemmSet<P>& set, const FfnCall& call, const Epi& epi, bool first, bool last, cudaStream_t s) {
-  auto* k = ffn_gemm_kernel<Epi, kPair, P>;
+  auto* k = ffn_gemm_kernel<Epi, kPair, P, kDraw>;
   // per device: the shared-memory limit is set, and the pairs that fit at once
   // counted (some SMs may have no partner)
   static std::atomic<int> known[64];
