@@ -670,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (t < 0) break;
       int tm, tn;
       const int which = locate(t, tm, tn), b = n & 1;
-      if (!__all_sync(0xFFFFFFFFu, wait_bar_sleep(&tail->acc_full[b], (uint32_t)(n >> 1) & 1u, ctl, kErrWaitTimeout))) break;
+      if (!__all_sync(0xFFFFFFFFu, wait_stage(&tail->acc_full[b], (uint32_t)(n >> 1) & 1u, ctl))) break;
       tc_fence_after();
       epi.tile(which, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN),
                tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, set.op[which].g.tile_n, grp,
