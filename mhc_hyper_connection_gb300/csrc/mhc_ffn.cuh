@@ -8,7 +8,6 @@ namespace mhc {
 // One matrix product D[M, N] = A B^T on 16-bit operands: operand row r, depth
 // k.  "K-major" operands store k contiguously, "MN-major" ones r.
 struct GemmShape {
-  int M, N, K;                 // rows, columns, depth of the product
   int tile_n;                  // width of a tile: 256 or 128
   int tiles_m, tiles_n, kiters;
   int band;                    // tile rows walked together, column by column

@@ -80,9 +80,6 @@ int tile_width(int64_t M, int64_t N, int sms, bool b_mn) {
 // one another's tiles and stay wide).
 GemmShape shape(int64_t M, int64_t N, int64_t K, bool pair_of, bool alone, int sms, bool f16, bool a_mn, bool b_mn) {
   GemmShape g;
-  g.M = (int)M;
-  g.N = (int)N;
-  g.K = (int)K;
   g.tile_n = pair_of || !alone ? kFfnTileN : tile_width(M, N, sms, b_mn);
   const int64_t step = pair_of ? 128 : g.tile_n;
   g.tiles_m = (int)((M + kFfnTileM - 1) / kFfnTileM);

@@ -42,7 +42,7 @@ struct FewTail {
 };
 
 struct FewShape {
-  int rows, T;                 // weight rows of one plane (output columns), tokens
+  int T;                       // tokens
   int nt;                      // tokens rounded up to 16
   int tiles, kiters, split;    // 128-row tiles, depth chunks, CTAs that share a tile
   int stages, ring;            // stages and bytes of the ring
@@ -373,7 +373,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 inline FewShape few_shape(const GemmShape& g, const FfnCall& call, int rows, int T, bool f16, bool w_mn, bool first,
                           bool last) {
   FewShape w = {};
-  w.rows = rows;
   w.T = T;
   w.nt = (T + 15) & ~15;
   w.tiles = (rows + kFewRows - 1) / kFewRows;

@@ -5,10 +5,9 @@
 //
 // One pass over g, x and the residual streams.  Bounded by HBM: (2n + 1) 2
 // bytes read (n - n/128 fewer from a checkpoint) and (n + 1) 2 written per
-// column, against 2 (n + n^2) products.  On the CUDA cores those products took
-// as long as the memory from n = 6 up (n = 8, T = 16384, D = 2048 from a
-// checkpoint: 430 us, 51% of measured HBM), so from n = 3 up they run on the
-// tensor cores (post_bwd_mma_kernel); for n = 1 and 2 a lane forms them itself.
+// column, against 2 (n + n^2) products.  Those run on the tensor cores: on the
+// CUDA cores they took longer than the memory (n = 8, T = 16384, D = 2048 from a checkpoint: 430 us, 51% of measured HBM; now
+// 238 us, 92%; n = 4, T = 32768, D = 7168: 1092 us, now 1000, 97%).
 #include <atomic>
 
 #include "mhc_ckpt.cuh"
@@ -48,142 +47,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return o;
 }
 
-// Sums v[0 .. N) over the warp's lanes; lane l gets the sum of v[l].  Halving
-// exchange: at each of five steps a lane sends the half of its values that
-// the partner keeps, N + 11 shuffles for N = 20 instead of 5 N.
-template <int N>
-__device__ __forceinline__ float warp_sums(const float* v, int lane) {
-  float a[32];
-#pragma unroll
-  for (int k = 0; k < 32; ++k) a[k] = k < N ? v[k] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int k = 0; k < o; ++k) {
-      if (k < N) {
-        const float send = up ? a[k] : a[k + o], keep = up ? a[k + o] : a[k];
-        a[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
-      }
-    }
-  }
-  return a[0];
-}
-
-template <int NS, bool kCkpt>
-__global__ void __launch_bounds__(kPbThreads) post_bwd_kernel(const PostBwdParams p) {
-  constexpr int V = NS + NS * NS;
-  __shared__ float part[kPbWarps][V];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wpt = p.wpt, sub = warp & (wpt - 1);
-  const long long t = (long long)blockIdx.x * (kPbWarps / wpt) + warp / wpt;
-  const bool live = t < p.T;
-  const int D = p.D, nv = D >> 3;
-  if (live) {
-    const uint64_t once = policy_evict_first();
-    float pc[NS], cm[NS * NS], acc[V];
-#pragma unroll
-    for (int j = 0; j < NS; ++j) pc[j] = __ldg(p.post + t * NS + j);
-#pragma unroll
-    for (int e = 0; e < NS * NS; ++e) cm[e] = __ldg(p.comb + t * (NS * NS) + e);
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-    const __nv_bfloat16* xt = p.x + t * D;
-    const __nv_bfloat16* gt = p.g + t * NS * D;
-    const int nblk = (D + kCkptBlock - 1) / kCkptBlock;
-    for (int v = sub * 32 + lane; v < nv; v += wpt * 32) {
-      const size_t col = (size_t)v * 8;
-      uint4 graw[NS], rraw[kCkpt ? 1 : NS];
-      uint2 craw[kCkpt ? NS : 1];
-      uint32_t sb[kCkpt ? NS : 1];
-      const uint4 xraw = ld_global_v4_hint(xt + col, once);
-#pragma unroll
-      for (int j = 0; j < NS; ++j) graw[j] = ld_global_v4_hint(gt + (size_t)j * D + col, once);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const size_t row = (size_t)t * NS + i;
-        if constexpr (kCkpt) {
-          craw[i] = __ldcs(reinterpret_cast<const uint2*>(p.codes + row * D + col));
-          sb[i] = __ldg(p.scales + row * nblk + (v >> 4));
-        } else {
-          rraw[i] = ld_global_v4_hint(p.res + row * D + col, once);
-        }
-      }
-      float gf[NS][8], f[8], o[8];
-#pragma unroll
-      for (int j = 0; j < NS; ++j) unpack8(graw[j], gf[j]);
-      unpack8(xraw, f);
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[j] = fmaf(f[e], gf[j][e], acc[j]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[e] = pc[0] * gf[0][e];
-#pragma unroll
-        for (int j = 1; j < NS; ++j) o[e] = fmaf(pc[j], gf[j][e], o[e]);
-      }
-      st_global_v4_hint(p.gx + t * D + col, pack8(o), once);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        if constexpr (kCkpt) {
-          const float s = ckpt_scale(sb[i]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 q = e4m3x2_f2((e < 2 ? craw[i].x : craw[i].y) >> (16 * (e & 1)));
-            f[2 * e] = q.x * s;
-            f[2 * e + 1] = q.y * s;
-          }
-        } else {
-          unpack8(rraw[i], f);
-        }
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[NS + i * NS + j] = fmaf(f[e], gf[j][e], acc[NS + i * NS + j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[e] = cm[i * NS] * gf[0][e];
-#pragma unroll
-          for (int j = 1; j < NS; ++j) o[e] = fmaf(cm[i * NS + j], gf[j][e], o[e]);
-        }
-        st_global_v4_hint(p.gres + ((size_t)t * NS + i) * D + col, pack8(o), once);
-      }
-    }
-    // join the lanes: value k of the token ends in lane k & 31
-#pragma unroll
-    for (int c = 0; c < V; c += 32) {
-      constexpr int kLast = V % 32 == 0 ? 32 : V % 32;
-      float s;
-      if (c + 32 <= V) s = warp_sums<32>(acc + c, lane);
-      else s = warp_sums<kLast>(acc + c, lane);
-      const int k = c + lane;
-      if (k < V) {
-        if (wpt == 1) {
-          if (k < NS) p.gpost[t * NS + k] = s;
-          else p.gcomb[t * (NS * NS) + k - NS] = s;
-        } else {
-          part[warp][k] = s;
-        }
-      }
-    }
-  }
-  if (wpt > 1) {                        // join the token's warps, in warp order
-    __syncthreads();
-    if (live && sub == 0) {
-      for (int k = lane; k < V; k += 32) {
-        float s = 0.0f;
-        for (int w = 0; w < wpt; ++w) s += part[warp + w][k];
-        if (k < NS) p.gpost[t * NS + k] = s;
-        else p.gcomb[t * (NS * NS) + k - NS] = s;
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------- n = 3 .. 8
-// Rows of a warp's 8 x 32 pieces: the streams of one token (n >= 5), or of two
-// at four rows each.  Lane 4 r + q holds row r, eight columns from 8 q, of g
+// Rows of a warp's 8 x 32 pieces: the streams of one token (n >= 5), of two at
+// four rows each (n = 3, 4), of four at two (n = 2) or of eight (n = 1).  Lane 4 r + q holds row r, eight columns from 8 q, of g
 // and of the residual; that is at once both operands' register layout of a
 // 16 x 8 x 16 tensor-core product over the columns (their order inside a sum
 // does not matter), whose result is the dot products of all row pairs: no
@@ -194,7 +59,7 @@ __global__ void __launch_bounds__(kPbThreads) post_bwd_kernel(const PostBwdParam
 // columns).  movmatrix turns a register of g into the B operand, and the result
 // comes out in the layout that g came in: eight consecutive columns a lane.
 // comb and post enter as three bf16 terms (24 bits, as fp32 has), so a product
-// is as exact as in fp32.  Such a split turns an infinity in g into NaN, and two
+// is as exact as in fp32.  Such a split turns an infinity in g into NaN, and the
 // tokens of a warp share the product over rows, so a piece with a result that
 // is not finite is formed again in plain fp32 (direct_piece).
 //
@@ -260,14 +125,14 @@ __device__ __noinline__ uint4 direct_piece(uint4 g, const float* coef, int src, 
 // 128 columns are copied while these are worked on.
 template <int NS, bool kCkpt>
 struct PbStage {
-  static constexpr int kTok = NS <= 4 ? 2 : 1;                       // tokens of a warp
+  static constexpr int kTok = NS == 1 ? 8 : NS == 2 ? 4 : NS <= 4 ? 2 : 1;   // tokens of a warp
   uint4 g[4][32];
   uint4 x[4][4 * kTok];
   uint4 r[kCkpt ? 80 : 128];
 };
 
 template <int NS, bool kCkpt>
-__global__ void __launch_bounds__(kPbThreads, 2) post_bwd_mma_kernel(const PostBwdParams p) {
+__global__ void __launch_bounds__(kPbThreads, 2) post_bwd_kernel(const PostBwdParams p) {
   using Stage = PbStage<NS, kCkpt>;
   constexpr int kTok = Stage::kTok, kStride = 8 / kTok;              // rows between the tokens
   extern __shared__ __align__(16) uint8_t pb_smem[];
@@ -420,10 +285,10 @@ __global__ void __launch_bounds__(kPbThreads, 2) post_bwd_mma_kernel(const PostB
 }
 
 template <int NS, bool kCkpt>
-cudaError_t launch_mma(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
+cudaError_t launch_kept(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
   constexpr size_t smem = 2 * kPbWarps * sizeof(PbStage<NS, kCkpt>);
   static std::atomic<bool> ready[64];                      // per device: the shared-memory limit is set
-  auto* k = post_bwd_mma_kernel<NS, kCkpt>;
+  auto* k = post_bwd_kernel<NS, kCkpt>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -438,13 +303,7 @@ cudaError_t launch_mma(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
 
 template <int NS>
 cudaError_t launch_ns(const PostBwdParams& p, unsigned grid, cudaStream_t s) {
-  if constexpr (NS <= 2) {
-    if (p.codes) post_bwd_kernel<NS, true><<<grid, kPbThreads, 0, s>>>(p);
-    else post_bwd_kernel<NS, false><<<grid, kPbThreads, 0, s>>>(p);
-  } else {
-    return p.codes ? launch_mma<NS, true>(p, grid, s) : launch_mma<NS, false>(p, grid, s);
-  }
-  return cudaGetLastError();
+  return p.codes ? launch_kept<NS, true>(p, grid, s) : launch_kept<NS, false>(p, grid, s);
 }
 
 }  // namespace
@@ -493,10 +352,10 @@ extern "C" mhc_status_t mhc_post_backward_run(const mhc_post_bwd_args* a, void* 
   p.gres = static_cast<__nv_bfloat16*>(a->grad_residual);
   p.gpost = a->grad_post;
   p.gcomb = a->grad_comb;
-  // Few tokens: several warps share one (or two, n = 3 and 4), while each still
-  // has 256 columns, until there are 64 warps per SM (T = 4096, n = 4, D = 4096: 84.9 us
+  // Few tokens: several warps share those of one, while each still has 256
+  // columns, until there are 64 warps per SM (T = 4096, n = 4, D = 4096: 84.9 us
   // with 16, 80.7 with 64: the last round of CTAs is shorter).
-  const int64_t tok = n == 3 || n == 4 ? 2 : 1, units = (T + tok - 1) / tok;
+  const int64_t tok = n == 1 ? 8 : n == 2 ? 4 : n <= 4 ? 2 : 1, units = (T + tok - 1) / tok;
   p.wpt = 1;
   while (p.wpt < kPbWarps && units * p.wpt < (int64_t)di.sms * 64 && p.wpt * 256 < D) p.wpt *= 2;
   const int64_t per = kPbWarps / p.wpt;
