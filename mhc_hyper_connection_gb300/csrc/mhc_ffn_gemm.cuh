@@ -114,6 +114,37 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// 32 consecutive fp32 columns of this warp's 32 accumulator lanes: one load, one
+// wait (a wait costs a few hundred clocks of an epilogue's few thousand).
+__device__ __forceinline__ void acc_ld32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 columns of two ranges.
+__device__ __forceinline__ void acc_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+      "%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]),
+        "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]),
+        "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]),
+        "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+
 // Bounded wait of the product loops.  The clock is read only after a few
 // probes have failed (each may sleep in the barrier for a while): reading it at
 // the head of every wait costs more than a stage of products.
@@ -235,7 +266,7 @@ struct EpiStore {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
-        tmem_ld32(taddr + c + 32 * h, v);
+        acc_ld32(taddr + c + 32 * h, v);
 #pragma unroll
         for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + q)) = pack8v<F16>(v + 8 * q);
       }
@@ -259,8 +290,7 @@ struct EpiGateUp {
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         float g[16], u[16];
-        tmem_ld16(taddr + c + 16 * h, g);
-        tmem_ld16(taddr + 128 + c + 16 * h, u);
+        acc_ld16x2(taddr + c + 16 * h, taddr + 128 + c + 16 * h, g, u);
 #pragma unroll
         for (int e = 0; e < 16; ++e) u[e] *= g[e] * sigmoid_fast(act_arg(g[e], act));
 #pragma unroll
@@ -273,7 +303,7 @@ struct EpiGateUp {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[32];
-            tmem_ld32(taddr + p * 128 + c + 32 * h, v);
+            acc_ld32(taddr + p * 128 + c + 32 * h, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + q)) = pack8v<F16>(v + 8 * q);
           }
@@ -290,7 +320,7 @@ struct EpiGateUp {
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           float v[32];
-          tmem_ld32(taddr + p * 128 + c, v);
+          acc_ld32(taddr + p * 128 + c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const float m = fabsf(v[e]);
@@ -303,7 +333,7 @@ struct EpiGateUp {
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           float v[32];
-          tmem_ld32(taddr + p * 128 + c, v);
+          acc_ld32(taddr + p * 128 + c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             v[e] = fabsf(v[e]) < __int_as_float(0x7F800000) ? v[e] * inv : __int_as_float(0x7FFFFFFF);
@@ -384,7 +414,7 @@ struct EpiDgate {
       const float s0 = ckpt_scale(k.s[0]), s1 = ckpt_scale(k.s[1]);
       if (c + 32 < c1) load(k, row0, f + 32, lane);
       float ga[32];
-      tmem_ld32(taddr + c, ga);
+      acc_ld32(taddr + c, ga);
       __syncwarp();
       uint4 o[3][4];
 #pragma unroll
