@@ -64,10 +64,11 @@ typedef struct {
 } mhc_ffn_args;
 
 /* Device scratch of a forward call: a 256-byte header (its first word is the
- * error word) and a [T, F].  T == 0 gives 0. */
+ * error word), a [T, F] and, where the second product is cut along its depth, fp32
+ * sums of the parts.  T == 0 gives 0. */
 MHC_API mhc_status_t mhc_ffn_workspace_size(int64_t T, int64_t D, int64_t F, size_t *bytes);
 
-/* Enqueue the forward: two kernels.  T == 0 returns MHC_OK, nothing launched.
+/* Enqueue the forward: two kernels (three where parts are joined).  T == 0 returns MHC_OK, nothing launched.
  * MHC_ERR_NULLPTR for a missing tensor, MHC_ERR_PARAM_INVALID for sizes, types,
  * alignment or workspace, MHC_ERR_RUNTIME for no sm_103 device or a launch
  * failure. */
@@ -92,10 +93,11 @@ typedef struct {
   int32_t withhold_copy;
 } mhc_ffn_bwd_args;
 
-/* Device scratch of a backward call: the header, [gg, gu] [T, 2, F], a [T, F]. */
+/* Device scratch of a backward call: the header, [gg, gu] [T, 2, F], a [T, F]
+ * and, where grad_x is cut along its depth, fp32 sums of the parts. */
 MHC_API mhc_status_t mhc_ffn_backward_workspace_size(int64_t T, int64_t D, int64_t F, size_t *bytes);
 
-/* Enqueue the backward: four kernels.  T == 0 writes zeros to both weight
+/* Enqueue the backward: two to three kernels.  T == 0 writes zeros to both weight
  * gradients (x, grad_y, grad_x and the kept sums may be NULL). */
 MHC_API mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args *a, void *stream);
 

@@ -9,11 +9,15 @@ namespace mhc {
 // k.  "K-major" operands store k contiguously, "MN-major" ones r.
 struct GemmShape {
   int tile_n;                  // width of a tile: 256 or 128
-  int tiles_m, tiles_n, kiters;
+  int tiles_m, tiles_n;
+  int slices;                  // parts of the depth that are tiles of their own
+  int kiters, kslice;          // chunks of 64 of the whole depth, and of a slice (the last may have fewer)
   int band;                    // tile rows walked together, column by column
   uint32_t idesc;
   int a_mn, b_mn;              // operand stored MN-major
 };
+
+__host__ __device__ inline int gemm_tiles(const GemmShape& g) { return g.tiles_m * g.tiles_n * g.slices; }
 
 // What the launches of one call share.
 struct FfnCall {
@@ -34,6 +38,7 @@ struct FfnFwdLaunch {
   FfnCall call;
   int T, D, F, act, kept;
   void *a_buf, *y, *gate_up, *codes, *scales;
+  float* part;                     // sums of the slices of down, where it has more than one
 };
 cudaError_t launch_ffn_forward(const FfnFwdLaunch& L, bool f16, cudaStream_t s);
 
@@ -48,6 +53,7 @@ struct FfnBwdLaunch {
   int T, D, F, act, kept;
   const void *gate_up, *codes, *scales;
   void *gg_buf, *a_buf, *grad_x, *grad_w_gate_up, *grad_w_down;
+  float* part;                     // of gx
 };
 cudaError_t launch_ffn_backward(const FfnBwdLaunch& L, bool f16, cudaStream_t s);
 

@@ -10,26 +10,6 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-struct FwdLayout {
-  size_t a, total;
-};
-FwdLayout fwd_layout(int64_t T, int64_t F) {
-  FwdLayout l;
-  l.a = 256;
-  l.total = l.a + up256((size_t)T * F * 2);
-  return l;
-}
-struct BwdLayout {
-  size_t gg, a, total;
-};
-BwdLayout bwd_layout(int64_t T, int64_t F) {
-  BwdLayout l;
-  l.gg = 256;
-  l.a = l.gg + up256((size_t)T * F * 4);
-  l.total = l.a + up256((size_t)T * F * 2);
-  return l;
-}
-
 mhc_status_t check_sizes(int64_t T, int64_t D, int64_t F) {
   if (T < 0 || T > (int64_t(1) << 24)) return fail(MHC_ERR_PARAM_INVALID, "T must be in [0, 2^24] (got %lld)", (long long)T);
   if (D < 8 || D > (int64_t(1) << 20) || D % 8 != 0)
@@ -64,27 +44,98 @@ bool map_2d(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Width of the tiles of an M x N product: 128 where that shortens the rounds of
-// tiles.  A narrow tile takes 0.6 of a wide one's time, with an MN-major B 0.7
-// (T = 1021, D = 2048, F = 5512, down product, 32 wide tiles or 64 narrow: forward
-// 75.5 or 68.2 us; T = 256, D = 4096, F = 8192, gate gradients: backward 145.7 or
-// 140.1; T = 1536, D = F = 4096 stays wide: 233 us, narrow 240).
-int tile_width(int64_t M, int64_t N, int sms, bool b_mn) {
-  const int64_t pairs = sms / 2, rows = (M + kFfnTileM - 1) / kFfnTileM;
-  const int64_t wide = (rows * ((N + 255) / 256) + pairs - 1) / pairs, narrow = (rows * ((N + 127) / 128) + pairs - 1) / pairs;
-  return 10 * wide > (b_mn ? 7 : 6) * narrow ? 128 : 256;
+// How a product is cut into tiles: planned for 76 pairs of CTAs whatever the
+// device, so that workspace sizes follow from T, D and F alone.
+constexpr int64_t kPairs = 76;
+struct Cut {
+  int tile_n, slices, kslice;
+};
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Time of joining `slices` sums of M x N, in stages of a wide tile (0.28 us): a
+// launch, and each sum written and read once.
+double join_cost(int64_t M, int64_t N, int64_t slices) { return slices > 1 ? 10.0 + 8.0 * M * N * slices / 1.9e6 : 0.0; }
+
+// A product that has its launch to itself: tiles 256 or 128 wide and, where few
+// tiles meet a deep product (most > 1), slices of the depth, by the estimated time
+// of the rounds of tiles.  A narrow tile takes 0.6 of a wide one's time, with an
+// MN-major B 0.7; four stages are for a tile's start and end.  (T = 1021, D =
+// 2048, F = 5512, down: 64 narrow tiles, forward 68 us where 32 wide ones took
+// 75.5; T = 256, D = 4096, F = 8192, down in 2 slices: forward 70 -> 60 us.)
+Cut cut_alone(int64_t M, int64_t N, int64_t K, bool b_mn, int most) {
+  const int64_t kiters = div_up(K, kFfnTileK), rows = div_up(M, kFfnTileM);
+  Cut best = {256, 1, (int)kiters};
+  double least = 1e30;
+  for (int w = 256; w >= 128; w -= 128) {
+    for (int64_t s = 1; s <= most && (s == 1 || kiters >= 8 * s); ++s) {
+      const int64_t per = div_up(kiters, s), slices = div_up(kiters, per);
+      const double rounds = (double)div_up(rows * div_up(N, w) * slices, kPairs);
+      const double cost = rounds * (per + 4) * (w == 256 ? 1.0 : b_mn ? 0.7 : 0.6) + join_cost(M, N, slices);
+      if (cost < least - 1e-9) {
+        least = cost;
+        best = {w, (int)slices, (int)per};
+      }
+    }
+  }
+  return best;
+}
+
+// grad_x beside the weight gradients in one launch: wide tiles, the depth sliced
+// where one tile of it would outlast an equal share of the launch by more than the
+// joining costs (T = 1956, D = 144, F = 8584, 4 slices: backward 173 -> 112 us; T =
+// 512, D = 2048, F = 4096, 2 slices: 85 -> 68).
+Cut cut_grad_x(int64_t T, int64_t D, int64_t F) {
+  const int64_t kx = div_up(2 * F, kFfnTileK), kw = div_up(T, kFfnTileK);
+  const int64_t total = div_up(T, 256) * div_up(D, 256) * kx + (div_up(2 * F, 256) * div_up(D, 256) + div_up(D, 256) * div_up(F, 256)) * kw;
+  const int64_t share = div_up(total, kPairs);
+  int64_t s = div_up(kx, share);
+  if (s > 16) s = 16;
+  while (s > 1 && kx < 8 * s) --s;
+  const int64_t per = div_up(kx, s), slices = div_up(kx, per);
+  const int64_t then = per > share ? per : share;
+  if (slices == 1 || kx - then < join_cost(T, D, slices)) return {256, 1, (int)kx};
+  return {256, (int)slices, (int)per};
+}
+Cut whole(int64_t K) { return {256, 1, (int)div_up(K, kFfnTileK)}; }
+constexpr int kMostSlices = 16;
+
+struct FwdLayout {
+  size_t a, part, total;
+};
+// Sums of the slices of a product with M x N outputs.
+size_t part_bytes(const Cut& c, int64_t M, int64_t N) { return c.slices > 1 ? up256((size_t)c.slices * M * N * 4) : 0; }
+Cut cut_down(int64_t T, int64_t D, int64_t F) { return T <= kFewTokens ? whole(F) : cut_alone(T, D, F, false, kMostSlices); }
+Cut cut_gx(int64_t T, int64_t D, int64_t F) { return T <= kFewTokens ? whole(2 * F) : cut_grad_x(T, D, F); }
+
+FwdLayout fwd_layout(int64_t T, int64_t D, int64_t F) {
+  FwdLayout l;
+  l.a = 256;
+  l.part = l.a + up256((size_t)T * F * 2);
+  l.total = l.part + part_bytes(cut_down(T, D, F), T, D);
+  return l;
+}
+struct BwdLayout {
+  size_t gg, a, part, total;
+};
+BwdLayout bwd_layout(int64_t T, int64_t D, int64_t F) {
+  BwdLayout l;
+  l.gg = 256;
+  l.a = l.gg + up256((size_t)T * F * 4);
+  l.part = l.a + up256((size_t)T * F * 2);
+  l.total = l.part + part_bytes(cut_gx(T, D, F), T, D);
+  return l;
 }
 
 // pair_of: rows of B come from two planes (gate and up), 128 columns a tile.
-// alone: the only product of its launch (several in one fill their rounds with
-// one another's tiles and stay wide).
-GemmShape shape(int64_t M, int64_t N, int64_t K, bool pair_of, bool alone, int sms, bool f16, bool a_mn, bool b_mn) {
+GemmShape shape(int64_t M, int64_t N, int64_t K, const Cut& cut, bool pair_of, bool f16, bool a_mn, bool b_mn) {
   GemmShape g;
-  g.tile_n = pair_of || !alone ? kFfnTileN : tile_width(M, N, sms, b_mn);
+  g.tile_n = cut.tile_n;
   const int64_t step = pair_of ? 128 : g.tile_n;
-  g.tiles_m = (int)((M + kFfnTileM - 1) / kFfnTileM);
-  g.tiles_n = (int)((N + step - 1) / step);
-  g.kiters = (int)((K + kFfnTileK - 1) / kFfnTileK);
+  g.tiles_m = (int)div_up(M, kFfnTileM);
+  g.tiles_n = (int)div_up(N, step);
+  g.slices = cut.slices;
+  g.kiters = (int)div_up(K, kFfnTileK);
+  g.kslice = cut.kslice;
   // A band of at most 32 MB of A stays in L2 while B passes by (T = 4096, D =
   // 4096, F = 8192 forward: 506 us with 8 tile rows, 490 with these 16).
   const int64_t row_bytes = K * 2 * kFfnTileM;
@@ -124,7 +175,7 @@ mhc_status_t mhc_ffn_workspace_size(int64_t T, int64_t D, int64_t F, size_t* byt
   if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
   const mhc_status_t st = check_sizes(T, D, F);
   if (st != MHC_OK) return st;
-  *bytes = T ? fwd_layout(T, F).total : 0;
+  *bytes = T ? fwd_layout(T, D, F).total : 0;
   return MHC_OK;
 }
 
@@ -133,7 +184,7 @@ mhc_status_t mhc_ffn_backward_workspace_size(int64_t T, int64_t D, int64_t F, si
   if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
   const mhc_status_t st = check_sizes(T, D, F);
   if (st != MHC_OK) return st;
-  *bytes = T ? bwd_layout(T, F).total : 0;
+  *bytes = T ? bwd_layout(T, D, F).total : 0;
   return MHC_OK;
 }
 
@@ -153,7 +204,7 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   for (const void* p : v16)
     if (!aligned(p, 16)) return fail(MHC_ERR_PARAM_INVALID, "tensors must be 16-byte aligned");
   if (!aligned(a->workspace, 256)) return fail(MHC_ERR_PARAM_INVALID, "the workspace must be 256-byte aligned");
-  const FwdLayout l = fwd_layout(T, F);
+  const FwdLayout l = fwd_layout(T, D, F);
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
   FfnFwdLaunch L;
@@ -172,8 +223,9 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   L.gate_up = a->gate_up;
   L.codes = a->codes;
   L.scales = a->scales;
-  L.gu = shape(T, F, D, true, true, sms, f16, false, false);
-  L.down = shape(T, D, F, false, true, sms, f16, false, false);
+  L.gu = shape(T, F, D, whole(D), true, f16, false, false);
+  L.down = shape(T, D, F, cut_down(T, D, F), false, f16, false, false);
+  L.part = L.down.slices > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   const bool few = T <= kFewTokens;
   const uint32_t tok_box = few ? (uint32_t)((T + 15) & ~int64_t(15)) : kFfnBoxK;
   if (!map_2d(&L.x, a->x, f16, D, T, 1, tok_box) || !map_2d(&L.wgu, a->w_gate_up, f16, D, F, 2, kFfnBoxK) ||
@@ -211,7 +263,7 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
   for (const void* p : v16)
     if (!aligned(p, 16)) return fail(MHC_ERR_PARAM_INVALID, "tensors must be 16-byte aligned");
   if (!aligned(a->workspace, 256)) return fail(MHC_ERR_PARAM_INVALID, "the workspace must be 256-byte aligned");
-  const BwdLayout l = bwd_layout(T, F);
+  const BwdLayout l = bwd_layout(T, D, F);
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
   FfnBwdLaunch L;
@@ -239,10 +291,11 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
       !map_2d(&L.gg_mn, L.gg_buf, f16, 2 * F, T, 1, kFfnBoxMn) || !map_2d(&L.x_mn, a->x, f16, D, T, 1, kFfnBoxMn) ||
       !map_2d(&L.gy_mn, a->grad_y, f16, D, T, 1, kFfnBoxMn) || !map_2d(&L.a_mn, L.a_buf, f16, F, T, 1, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
-  L.ga = shape(T, F, D, false, true, sms, f16, false, true);
-  L.gx = shape(T, D, 2 * F, false, false, sms, f16, false, true);
-  L.gwgu = shape(2 * F, D, T, false, false, sms, f16, true, true);
-  L.gwd = shape(D, F, T, false, false, sms, f16, true, true);
+  L.ga = shape(T, F, D, cut_alone(T, F, D, true, 1), false, f16, false, true);
+  L.gx = shape(T, D, 2 * F, cut_gx(T, D, F), false, f16, false, true);
+  L.gwgu = shape(2 * F, D, T, whole(T), false, f16, true, true);
+  L.gwd = shape(D, F, T, whole(T), false, f16, true, true);
+  L.part = L.gx.slices > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   const cudaError_t e = launch_ffn_backward(L, f16, s);
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward backward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;

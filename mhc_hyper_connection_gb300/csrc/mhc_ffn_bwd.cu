@@ -38,9 +38,9 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
                       : (L.kept == 1 ? dgate<F16, 1>(L, s) : dgate<F16, 2>(L, s));
   if (e != cudaSuccess) return e;
   const GemmOperands gx = {L.gg_k, L.wgu_mn, L.gx}, gwgu = {L.gg_mn, L.x_mn, L.gwgu}, gwd = {L.gy_mn, L.a_mn, L.gwd};
-  const StoreTo to_x = {static_cast<uint16_t*>(L.grad_x), L.T, L.D};
-  const StoreTo to_wgu = {static_cast<uint16_t*>(L.grad_w_gate_up), 2 * L.F, L.D};
-  const StoreTo to_wd = {static_cast<uint16_t*>(L.grad_w_down), L.D, L.F};
+  const StoreTo to_x = {static_cast<uint16_t*>(L.grad_x), L.T, L.D, L.part};
+  const StoreTo to_wgu = {static_cast<uint16_t*>(L.grad_w_gate_up), 2 * L.F, L.D, nullptr};
+  const StoreTo to_wd = {static_cast<uint16_t*>(L.grad_w_down), L.D, L.F, nullptr};
   if (few) {
     FewStore<F16> f;
     f.out = to_x.out;
@@ -55,16 +55,18 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
   // The three products that follow are independent: one launch, tiles of the
   // deepest first.
   EpiStore<F16, 3> o;
-  if (L.gx.kiters >= L.gwgu.kiters) {
+  if (L.gx.kslice >= L.gwgu.kslice) {
     o.to[0] = to_x;
     o.to[1] = to_wgu;
     o.to[2] = to_wd;
-    return launch_gemm<false, true, 3>({{gx, gwgu, gwd}}, L.call, o, false, true, s);
+    e = launch_gemm<false, true, 3>({{gx, gwgu, gwd}}, L.call, o, false, true, s);
+  } else {
+    o.to[0] = to_wgu;
+    o.to[1] = to_wd;
+    o.to[2] = to_x;
+    e = launch_gemm<false, true, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
   }
-  o.to[0] = to_wgu;
-  o.to[1] = to_wd;
-  o.to[2] = to_x;
-  return launch_gemm<false, true, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
+  return e != cudaSuccess || !L.part ? e : launch_sum<F16>(to_x, L.gx.slices, L.call.sms, s);
 }
 
 }  // namespace

@@ -22,8 +22,9 @@ cudaError_t forward(const FfnFwdLaunch& L, cudaStream_t s) {
   const cudaError_t e = L.kept == 0 ? gate_up<F16, 0>(L, s) : L.kept == 1 ? gate_up<F16, 1>(L, s) : gate_up<F16, 2>(L, s);
   if (e != cudaSuccess) return e;
   EpiStore<F16, 1> o;
-  o.to[0] = {static_cast<uint16_t*>(L.y), L.T, L.D};
-  return launch_gemm<false, false, 1>({{L.a, L.wd, L.down}}, L.call, o, false, true, s);
+  o.to[0] = {static_cast<uint16_t*>(L.y), L.T, L.D, L.part};
+  const cudaError_t d = launch_gemm<false, false, 1>({{L.a, L.wd, L.down}}, L.call, o, false, true, s);
+  return d != cudaSuccess || !L.part ? d : launch_sum<F16>(o.to[0], L.down.slices, L.call.sms, s);
 }
 
 template <bool F16, int kKept>

@@ -246,21 +246,37 @@ __device__ __forceinline__ void stage_flush8(const uint8_t* buf, uint8_t* base, 
   __syncwarp();
 }
 
-// out[row, col] = round(acc), one output per product of the launch
+// out[row, col] = round(acc), one output per product of the launch; with slices
+// of the depth their fp32 sums, part[slice][row][col], which ffn_sum_kernel joins.
 struct StoreTo {
   uint16_t* out;
   int M, N;
+  float* part;
 };
 template <bool F16, int P>
 struct EpiStore {
   StoreTo to[P];
-  // which: the product; taddr: the warp's accumulator lanes; row0: the row of its
-  // lane 0; tn, cols: the tile's column and width; grp: which half of them
-  __device__ __forceinline__ void tile(int which, uint32_t taddr, int row0, int tn, int cols, int grp, uint8_t* buf,
-                                       int lane) const {
+  // which, slice: the product and its part; taddr: the warp's accumulator lanes;
+  // row0: the row of its lane 0; tn, cols: the tile's column and width; grp: which
+  // half of them
+  __device__ __forceinline__ void tile(int which, int slice, uint32_t taddr, int row0, int tn, int cols, int grp,
+                                       uint8_t* buf, int lane) const {
     uint16_t* out = to[which].out;
     const int M = to[which].M, N = to[which].N;
     const int n0 = tn * cols;
+    if (to[which].part) {
+      float* part = to[which].part + ((size_t)slice * M + row0) * N + n0;
+#pragma unroll 1
+      for (int c = grp * (cols / 2); c < (grp + 1) * (cols / 2) && n0 + c < N; c += 32) {
+        float v[32];
+        acc_ld32(taddr + c, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(buf + sw128(lane, q)) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        stage_flush(buf, reinterpret_cast<uint8_t*>(part + c), (size_t)N * 4, M - row0, min(32, N - n0 - c) * 4, lane);
+      }
+      return;
+    }
 #pragma unroll 1
     for (int c = grp * (cols / 2); c < (grp + 1) * (cols / 2) && n0 + c < N; c += 64) {
 #pragma unroll
@@ -283,7 +299,7 @@ struct EpiGateUp {
   uint16_t *a, *gate_up;
   uint8_t *codes, *scales;
   int T, F, act;
-  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, int, int grp, uint8_t* buf, int lane) const {
+  __device__ __forceinline__ void tile(int, int, uint32_t taddr, int row0, int tn, int, int grp, uint8_t* buf, int lane) const {
     const int f0 = tn * 128, rows = T - row0, c = grp * 64;
     if (f0 + c < F) {
       const int bytes = min(64, F - f0 - c) * 2;
@@ -397,7 +413,7 @@ struct EpiDgate {
     }
   }
 
-  __device__ __forceinline__ void tile(int, uint32_t taddr, int row0, int tn, int cols, int grp, uint8_t* buf,
+  __device__ __forceinline__ void tile(int, int, uint32_t taddr, int row0, int tn, int cols, int grp, uint8_t* buf,
                                        int lane) const {
     const int f0 = tn * cols, rows = T - row0, c0 = grp * (cols / 2), c1 = c0 + cols / 2;
     Kept k;
@@ -500,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   int ntiles = 0;
 #pragma unroll
-  for (int i = 0; i < P; ++i) ntiles += set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+  for (int i = 0; i < P; ++i) ntiles += gemm_tiles(set.op[i].g);
   Ctl ctl{&tail->abort, call.err, call.wait_ns};
 
   if (threadIdx.x == 0) {
@@ -560,18 +576,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       return t;
     }
   };
-  // Tile t: its product, row and column.
-  auto locate = [&](int t, int& tm, int& tn) -> int {
+  // Tile t: its product, slice, row and column.
+  auto locate = [&](int t, int& slice, int& tm, int& tn) -> int {
     int which = 0;
 #pragma unroll
     for (int i = 0; i + 1 < P; ++i) {
-      const int tiles = set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+      const int tiles = gemm_tiles(set.op[i].g);
       if (which == i && t >= tiles) {
         t -= tiles;
         which = i + 1;
       }
     }
-    tile_coords(set.op[which].g, t, tm, tn);
+    const int area = set.op[which].g.tiles_m * set.op[which].g.tiles_n;
+    slice = t / area;
+    tile_coords(set.op[which].g, t - slice * area, tm, tn);
     return which;
   };
 
@@ -605,8 +623,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       for (int n = 0; ok; ++n) {
         const int t = kDraw && rank == 0 ? cur : tile_of(n, false);
         if (t < 0) break;
-        int tm, tn;
-        const int which = locate(t, tm, tn);
+        int slice, tm, tn;
+        const int which = locate(t, slice, tm, tn);
         const GemmShape& g = set.op[which].g;
         const CUtensorMap* ta = &set.op[which].a;
         const CUtensorMap* tb = &set.op[which].b;
@@ -614,7 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int half_n = g.tile_n / 2;
         const int n0 = kPair ? tn * kGemmHalf : tn * g.tile_n + (int)rank * half_n;
         const uint32_t bytes = 2u * (uint32_t)(kGemmOpBytes + half_n * kFfnTileK * 2);   // of both CTAs
-        const int plane = kPair ? (int)rank : 0, kiters = g.kiters, a_mn = g.a_mn, b_mn = g.b_mn;
+        const int plane = kPair ? (int)rank : 0, a_mn = g.a_mn, b_mn = g.b_mn;
+        const int kbeg = slice * g.kslice, kiters = min(g.kslice, g.kiters - kbeg);
         int after = -1;                          // tile n + 2, drawn under this tile's copies
         if (kDraw && rank == 0 && next >= 0) after = draw();
         for (int k = 0; k < kiters; ++k) {
@@ -624,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (withhold && pair == 0 && n == 0 && k == kiters - 1) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
           const uint32_t bar = map_cluster(&tail->full[s], 0);
-          const int k0 = k * kFfnTileK;
+          const int k0 = (kbeg + k) * kFfnTileK;
           if (rank == 0) mbar_expect_tx(&tail->full[s], bytes);
           if (a_mn) {
             tma_load_3d_pair(sa, ta, bar, m0, k0, 0);
@@ -669,12 +688,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       for (int n = 0; ok; ++n) {
         const int t = tile_of(n, true);
         if (t < 0) break;
-        int tm, tn;
-        const GemmShape& g = set.op[locate(t, tm, tn)].g;
+        int slice, tm, tn;
+        const GemmShape& g = set.op[locate(t, slice, tm, tn)].g;
         // byte step of sixteen depths, and the distance of the next 64 rows
         const uint64_t a0 = g.a_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0), b0 = g.b_mn ? sw128_desc_mn(0, 8192) : sw128_desc(0);
         const uint32_t astep = (g.a_mn ? 2048u : 32u) >> 4, bstep = (g.b_mn ? 2048u : 32u) >> 4, idesc = g.idesc;
-        const int b = n & 1, kiters = g.kiters;
+        const int b = n & 1, kiters = min(g.kslice, g.kiters - slice * g.kslice);
         if (!wait_slow(&tail->acc_empty[b], ((uint32_t)(n >> 1) & 1u) ^ 1u, ctl, kErrClusterWait, true)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(b * kFfnTileN);
@@ -706,11 +725,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for (int n = 0;; ++n) {
       const int t = tile_of(n, true);
       if (t < 0) break;
-      int tm, tn;
-      const int which = locate(t, tm, tn), b = n & 1;
+      int slice, tm, tn;
+      const int which = locate(t, slice, tm, tn), b = n & 1;
       if (!__all_sync(0xFFFFFFFFu, wait_stage(&tail->acc_full[b], (uint32_t)(n >> 1) & 1u, ctl))) break;
       tc_fence_after();
-      epi.tile(which, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN),
+      epi.tile(which, slice, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN),
                tm * kFfnTileM + (int)rank * kGemmHalf + q * 32, tn, set.op[which].g.tile_n, grp,
                bufs + (warp - 2) * kStageBuf, lane);
       tc_fence_before();
@@ -728,6 +747,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
   }
+}
+
+// out = round(sum of the slices), in their order; eight values a thread.
+template <bool F16>
+__global__ void __launch_bounds__(256) ffn_sum_kernel(const float* part, int slices, long long count, uint16_t* out) {
+  pdl_wait();
+  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < count; i += (long long)gridDim.x * 2048) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    for (int s = 0; s < slices; ++s) {
+      const float4 a = *reinterpret_cast<const float4*>(part + s * count + i);
+      const float4 b = *reinterpret_cast<const float4*>(part + s * count + i + 4);
+      v[0] += a.x;
+      v[1] += a.y;
+      v[2] += a.z;
+      v[3] += a.w;
+      v[4] += b.x;
+      v[5] += b.y;
+      v[6] += b.z;
+      v[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(out + i) = pack8v<F16>(v);
+  }
+}
+template <bool F16>
+cudaError_t launch_sum(const StoreTo& to, int slices, int sms, cudaStream_t s) {
+  const long long count = (long long)to.M * to.N, blocks = (count + 2047) / 2048;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(blocks < 8ll * sms ? blocks : 8ll * sms));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ffn_sum_kernel<F16>, (const float*)to.part, (int)slices, (long long)count, to.out);
 }
 
 // first: the call's first launch (ordered behind everything before it, clears
@@ -758,7 +815,7 @@ cudaError_t launch_gemm(const GemmSet<P>& set, const FfnCall& call, const Epi& e
     known[dev].store(pairs, std::memory_order_relaxed);
   }
   long long tiles = 0;
-  for (int i = 0; i < P; ++i) tiles += (long long)set.op[i].g.tiles_m * set.op[i].g.tiles_n;
+  for (int i = 0; i < P; ++i) tiles += gemm_tiles(set.op[i].g);
   cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
   cfg.stream = s;
   cfg.attrs = attr;

@@ -152,6 +152,27 @@ def test_large_and_deep(cuda_device):
     _check_backward(c, "bf16", "silu", gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept), kept)
 
 
+@pytest.mark.parametrize("T,D,F", [(200, 136, 8584), (257, 1032, 6152), (700, 64, 12288)])
+def test_deep_and_narrow(cuda_device, T, D, F):
+    """Few output tiles over a deep product: the depth is cut into slices whose
+    sums are joined; repeated runs agree bit for bit."""
+    import mhc_hyper_connection_gb300 as mp
+    from mhc_hyper_connection_gb300 import gated_ffn, gated_ffn_backward
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    assert mp.mhc_ffn_workspace_size(T, D, F)[1] > 256 + up(2 * T * F)      # room for the slices' sums
+    assert mp.mhc_ffn_backward_workspace_size(T, D, F)[1] > 256 + up(4 * T * F) + up(2 * T * F)
+    for kind, act in (("bf16", "silu"), ("fp16", "gelu")):
+        c = _case(cuda_device, T, D, F, kind, T)
+        y, kept = gated_ffn(c["x"], c["w"], c["wd"], act=act, save="16bit")
+        _check_forward(c, kind, act, y, kept)
+        got = gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept, act=act)
+        _check_backward(c, kind, act, got, kept)
+        for _ in range(5):
+            y2, _ = gated_ffn(c["x"], c["w"], c["wd"], act=act, save="16bit")
+            again = gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept, act=act)
+            assert torch.equal(y, y2) and all(torch.equal(got[k], again[k]) for k in got)
+
+
 def test_against_differences(cuda_device):
     """Central differences of <grad_y, y> in 64 bits, from the kept sums of the
     same inputs.  The kept sums are rounded to fp16 (u = 2^-11), which moves a
