@@ -5,6 +5,22 @@
 
 namespace mhc {
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^sh < d <= 2^(sh + 1) and
+// mul = ceil(2^(32 + sh) / d), mul d exceeds 2^(32 + sh) by less than d, which
+// times n stays below 2^(32 + sh).  (Tiles are found this way by every role: T =
+// 3388, D = 504, F = 15800, forward 172.4 -> 168.8 us.)
+struct FastDiv {
+  uint32_t mul = 0;
+  int sh = -1;                 // -1: d = 1
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    if (d < 2) return;
+    for (sh = 0; (2ull << sh) < d;) ++sh;
+    mul = (uint32_t)(((1ull << (32 + sh)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const { return sh < 0 ? n : (int)(__umulhi((uint32_t)n, mul) >> sh); }
+};
+
 // One matrix product D[M, N] = A B^T on 16-bit operands: operand row r, depth
 // k.  "K-major" operands store k contiguously, "MN-major" ones r.
 struct GemmShape {
@@ -13,6 +29,7 @@ struct GemmShape {
   int slices;                  // parts of the depth that are tiles of their own
   int kiters, kslice;          // chunks of 64 of the whole depth, and of a slice (the last may have fewer)
   int band;                    // tile rows walked together, column by column
+  FastDiv by_area, by_band, by_rows, by_last;   // tiles of a slice, of a band; rows of a band, of the last
   uint32_t idesc;
   int a_mn, b_mn;              // operand stored MN-major
 };

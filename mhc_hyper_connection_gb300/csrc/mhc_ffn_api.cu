@@ -141,6 +141,10 @@ GemmShape shape(int64_t M, int64_t N, int64_t K, const Cut& cut, bool pair_of, b
   const int64_t row_bytes = K * 2 * kFfnTileM;
   g.band = (int)((int64_t(32) << 20) / row_bytes);
   g.band = g.band < 4 ? 4 : g.band > 16 ? 16 : g.band;
+  g.by_area = FastDiv((uint32_t)(g.tiles_m * g.tiles_n));
+  g.by_band = FastDiv((uint32_t)(g.band * g.tiles_n));
+  g.by_rows = FastDiv((uint32_t)g.band);
+  g.by_last = FastDiv((uint32_t)(g.tiles_m % g.band ? g.tiles_m % g.band : g.band));
   g.a_mn = a_mn;
   g.b_mn = b_mn;
   g.idesc = (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |

@@ -171,11 +171,10 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, const
 // Tile t of the persistent loop: bands of g.band tile rows, column by column
 // inside a band, so that the CTAs running at one time share operand rows in L2.
 __device__ __forceinline__ void tile_coords(const GemmShape& g, int t, int& tm, int& tn) {
-  const int band = t / (g.band * g.tiles_n), first = band * g.band;
-  const int rows = min(g.band, g.tiles_m - first);
-  const int r = t - band * g.band * g.tiles_n;
-  tm = first + r % rows;
-  tn = r / rows;
+  const int band = g.by_band(t), first = band * g.band, rows = min(g.band, g.tiles_m - first);
+  const int r = t - first * g.tiles_n;
+  tn = rows == g.band ? g.by_rows(r) : g.by_last(r);
+  tm = first + r - tn * rows;
 }
 
 // ------------------------------------------------------------- epilogues
@@ -588,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       }
     }
     const int area = set.op[which].g.tiles_m * set.op[which].g.tiles_n;
-    slice = t / area;
+    slice = set.op[which].g.by_area(t);
     tile_coords(set.op[which].g, t - slice * area, tm, tn);
     return which;
   };
