@@ -55,14 +55,23 @@ def _x16(x, name="x") -> int:
     return dt
 
 
-def _tokens(shape, rest) -> int:
-    """Token count of the dims before the last `rest`: (T,) or (B, S)."""
-    k = len(shape) - rest
-    if k == 1:
-        return shape[0]
-    if k == 2:
-        return shape[0] * shape[1]
+def _tokens(lead) -> int:
+    """Token count of the leading dims: (T,) or (B, S)."""
+    if len(lead) == 1:
+        return lead[0]
+    if len(lead) == 2:
+        return lead[0] * lead[1]
     raise ValueError("leading dims must be (T,) or (B, S)")
+
+
+def _lead(shape):
+    """(T, leading dims, n, D) of streams [T, n, D] or [B, S, n, D]."""
+    if len(shape) == 3:
+        T, n, D = shape
+        return T, (T,), n, D
+    *lead, n, D = shape if len(shape) > 1 else (0, 0)
+    lead = tuple(lead)
+    return _tokens(lead), lead, n, D
 
 
 def _check(st, where):
@@ -71,7 +80,8 @@ def _check(st, where):
 
 
 def _scales_shape(shape):
-    return shape[:-1] + ((shape[-1] + CKPT_BLOCK - 1) // CKPT_BLOCK,)
+    *lead, D = shape
+    return (*lead, (D + CKPT_BLOCK - 1) // CKPT_BLOCK)
 
 
 def _ckpt_new(shape, device) -> Ckpt8:
@@ -80,7 +90,23 @@ def _ckpt_new(shape, device) -> Ckpt8:
 
 
 def _ckpt_at(ckpt, shape, device):
-    return (_at(ckpt.codes, "codes", _u8, shape, device), _at(ckpt.scales, "scales", _u8, _scales_shape(shape), device))
+    return _at(ckpt.codes, "codes", _u8, shape, device), _at(ckpt.scales, "scales", _u8, _scales_shape(shape), device)
+
+
+def _ckpt_out(ckpt, shape, device):
+    """A checkpoint to write into, given or new, and its addresses."""
+    if ckpt is None:
+        ckpt = _ckpt_new(shape, device)
+        return ckpt, ckpt.codes.data_ptr(), ckpt.scales.data_ptr()
+    return (ckpt,) + _ckpt_at(ckpt, shape, device)
+
+
+def _out(t, name, like):
+    """A tensor to write into, given or new, of another's type and shape, and its address."""
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return t, _at(t, name, like.dtype, like.shape, like.device)
 
 
 def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
@@ -92,9 +118,7 @@ def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
     xp = _at(x, "x", x.dtype, shape, dev)
-    if out is None:
-        out = _ckpt_new(shape, dev)
-    codes, scales = _ckpt_at(out, shape, dev)
+    out, codes, scales = _ckpt_out(out, shape, dev)
     _check(_lib.mhc_ckpt8_pack_run(x.numel() // D if D else 0, D, dt, xp, codes, scales, _stream(stream, dev)),
            "mhc_ckpt8_pack_run")
     return out
@@ -105,14 +129,15 @@ def ckpt8_restore(ckpt, dtype=None, out=None, stream=None):
     packed from, default bf16)."""
     codes = ckpt.codes
     shape, dev = codes.shape, codes.device
+    cp, sp = _ckpt_at(ckpt, shape, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype or _bf16, device=dev)
-    dt = _x16(out, "out")
+        op = out.data_ptr()
+    else:
+        op = _at(out, "out", dtype or out.dtype, shape, dev)
     D = shape[-1]
-    cp, sp = _ckpt_at(ckpt, shape, dev)
-    _check(_lib.mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, dt, cp, sp,
-                                      _at(out, "out", dtype or out.dtype, shape, dev), _stream(stream, dev)),
-           "mhc_ckpt8_restore_run")
+    _check(_lib.mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, _x16(out, "out"), cp, sp, op,
+                                      _stream(stream, dev)), "mhc_ckpt8_restore_run")
     return out
 
 
@@ -120,18 +145,15 @@ def hc_post_ckpt(x, residual, post, comb, out=None, ckpt=None, stream=None):
     """hc_post that also writes the 8-bit checkpoint of its output in the same
     pass; returns (out, Ckpt8).  Same tensors and layouts as hc_post."""
     shape, dev = residual.shape, residual.device
-    T, lead, n, D = _tokens(shape, 2), shape[:-2], shape[-2], shape[-1]
+    T, lead, n, D = _lead(shape)
     rp = _at(residual, "residual", _bf16, shape, dev)
     xp = _at(x, "x", _bf16, lead + (D,), dev)
     pp = _at(post, "post", _f32, lead + (n,), dev)
     cp = _at(comb, "comb", _f32, lead + (n, n), dev)
-    if out is None:
-        out = torch.empty_like(residual)
-    if ckpt is None:
-        ckpt = _ckpt_new(shape, dev)
-    codes, scales = _ckpt_at(ckpt, shape, dev)
-    _check(_lib.mhc_post_ckpt_run(T, n, D, xp, rp, pp, cp, _at(out, "out", _bf16, shape, dev), codes, scales,
-                                  _stream(stream, dev)), "mhc_post_ckpt_run")
+    out, op = _out(out, "out", residual)
+    ckpt, codes, scales = _ckpt_out(ckpt, shape, dev)
+    _check(_lib.mhc_post_ckpt_run(T, n, D, xp, rp, pp, cp, op, codes, scales, _stream(stream, dev)),
+           "mhc_post_ckpt_run")
     return out, ckpt
 
 
@@ -141,7 +163,7 @@ def hc_post_backward(grad_out, x, residual, post, comb, grads=None, stream=None)
     bf16 or as a Ckpt8.  Returns {"grad_x", "grad_residual" (bf16),
     "grad_post", "grad_comb" (fp32)}, written into `grads` when given."""
     shape, dev = grad_out.shape, grad_out.device
-    T, lead, n, D = _tokens(shape, 2), shape[:-2], shape[-2], shape[-1]
+    T, lead, n, D = _lead(shape)
     gp = _at(grad_out, "grad_out", _bf16, shape, dev)
     xp = _at(x, "x", _bf16, lead + (D,), dev)
     pp = _at(post, "post", _f32, lead + (n,), dev)
@@ -210,16 +232,18 @@ def _scratch(workspace, T, D, F, backward, device, stream):
 
 
 def _ffn_inputs(x, w_gate_up, w_down, act):
-    """Checked inputs: (type code, act code, T, D, F, addresses of x, w_gate_up, w_down)."""
+    """Checked inputs: (type code, act code, T, D, F, shape of the kept sums,
+    addresses of x, w_gate_up, w_down)."""
     dt, dev, xt = _x16(x), x.device, x.dtype
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
     ws = w_gate_up.shape
     if len(ws) != 3 or ws[0] != 2:
         raise ValueError("w_gate_up must be [2, F, D]")
-    T, D, F = _tokens(x.shape, 1), x.shape[-1], ws[1]
-    return (dt, _ACTS[act], T, D, F, _at(x, "x", xt, x.shape, dev), _at(w_gate_up, "w_gate_up", xt, (2, F, D), dev),
-            _at(w_down, "w_down", xt, (D, F), dev))
+    *lead, D = x.shape
+    lead, F = tuple(lead), ws[1]
+    return (dt, _ACTS[act], _tokens(lead), D, F, lead + (2, F), _at(x, "x", xt, x.shape, dev),
+            _at(w_gate_up, "w_gate_up", xt, (2, F, D), dev), _at(w_down, "w_down", xt, (D, F), dev))
 
 
 def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, workspace=None, stream=None):
@@ -229,27 +253,21 @@ def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, wo
     backward: "16bit" as a tensor [T, 2, F], "8bit" as a Ckpt8 of that shape.
     Returns (y, kept); kept is None without save.  y, kept and workspace are
     allocated unless given."""
-    dt, ac, T, D, F, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
+    dt, ac, T, D, F, shape, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
     dev = x.device
     kp = codes = scales = None
     if save is None:
         if kept is not None:
             raise ValueError("kept goes with save")
+    elif save == "16bit":
+        if kept is None:
+            kept = torch.empty(shape, dtype=x.dtype, device=dev)
+        kp = _at(kept, "kept", x.dtype, shape, dev)
+    elif save == "8bit":
+        kept, codes, scales = _ckpt_out(kept, shape, dev)
     else:
-        shape = x.shape[:-1] + (2, F)
-        if save == "16bit":
-            if kept is None:
-                kept = torch.empty(shape, dtype=x.dtype, device=dev)
-            kp = _at(kept, "kept", x.dtype, shape, dev)
-        elif save == "8bit":
-            if kept is None:
-                kept = _ckpt_new(shape, dev)
-            codes, scales = _ckpt_at(kept, shape, dev)
-        else:
-            raise ValueError(f'save must be None, "16bit" or "8bit" (got {save!r})')
-    if y is None:
-        y = torch.empty_like(x)
-    yp = _at(y, "y", x.dtype, x.shape, dev)
+        raise ValueError(f'save must be None, "16bit" or "8bit" (got {save!r})')
+    y, yp = _out(y, "y", x)
     raw, workspace, p, n = _scratch(workspace, T, D, F, False, dev, stream)
     a = MhcFfnArgs(T, D, F, dt, ac, xp, gp, wp, yp, kp, codes, scales, p, n)
     _check(_lib.mhc_ffn_run(byref(a), raw), "mhc_ffn_run")
@@ -260,10 +278,9 @@ def gated_ffn_backward(grad_y, x, w_gate_up, w_down, kept, act="silu", grads=Non
     """Backward of gated_ffn from what it kept (a tensor or a Ckpt8): returns
     {"grad_x", "grad_w_gate_up", "grad_w_down"} in x's type, written into
     `grads` when given."""
-    dt, ac, T, D, F, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
+    dt, ac, T, D, F, shape, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
     dev, xt = x.device, x.dtype
     yp = _at(grad_y, "grad_y", xt, x.shape, dev)
-    shape = x.shape[:-1] + (2, F)
     kp = codes = scales = None
     if isinstance(kept, Ckpt8):
         codes, scales = _ckpt_at(kept, shape, dev)

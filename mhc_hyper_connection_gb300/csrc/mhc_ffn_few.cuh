@@ -438,7 +438,8 @@ inline cudaError_t few_clusters(int dev, FewClusters* out) {
 }
 
 // CTAs per tile: the most whose clusters the device holds all at once, with
-// four chunks of the depth each at least.
+// four chunks of the depth each at least (D = 1024, F = 4096, one token: 14.4 us,
+// with eight chunks 15.1, one CTA per tile 29.6).
 template <class Epi>
 cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, cudaStream_t s) {
   auto* k = ffn_few_kernel<Epi>;
