@@ -5,6 +5,10 @@ Argument checks and marshalling only; the computation is in the CUDA library
 (include/mhc_ckpt.h, mhc_post_backward.h, mhc_ffn.h).  A call of these is as
 short as a launch or two, so the checks are one comparison each and torch's
 current stream is read as a raw handle.  Contiguous CUDA tensors only.
+
+A call runs on `stream` (torch's current one if None).  If that is another
+stream, it waits for the current one only where the call allocates something;
+what the inputs still wait for is the caller's to order.
 """
 from __future__ import annotations
 
@@ -37,6 +41,18 @@ def _stream(stream, device) -> int:
             raise ValueError(f"tensors must be on a CUDA device (got {device})")
         return _current_raw_stream(device.index)
     return int(getattr(stream, "cuda_stream", stream))
+
+
+def _on(raw, stream, device, *made):
+    """Tensors that a call allocated come from torch's current stream.  If the
+    call runs on another one (`stream` given), that one first waits for what
+    the current stream may still do with their memory, and the allocator is
+    told that it uses them."""
+    if stream is not None and raw != _current_raw_stream(device.index):
+        ext = torch.cuda.ExternalStream(raw, device=device)
+        ext.wait_stream(torch.cuda.current_stream(device))
+        for t in made:
+            t.record_stream(ext)
 
 
 def _at(t, name, dtype, shape, device) -> int:
@@ -118,9 +134,11 @@ def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
     xp = _at(x, "x", x.dtype, shape, dev)
+    raw, given = _stream(stream, dev), out
     out, codes, scales = _ckpt_out(out, shape, dev)
-    _check(_lib.mhc_ckpt8_pack_run(x.numel() // D if D else 0, D, dt, xp, codes, scales, _stream(stream, dev)),
-           "mhc_ckpt8_pack_run")
+    if stream is not None and given is None:
+        _on(raw, stream, dev, *out)
+    _check(_lib.mhc_ckpt8_pack_run(x.numel() // D if D else 0, D, dt, xp, codes, scales, raw), "mhc_ckpt8_pack_run")
     return out
 
 
@@ -130,14 +148,17 @@ def ckpt8_restore(ckpt, dtype=None, out=None, stream=None):
     codes = ckpt.codes
     shape, dev = codes.shape, codes.device
     cp, sp = _ckpt_at(ckpt, shape, dev)
+    raw = _stream(stream, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype or _bf16, device=dev)
         op = out.data_ptr()
+        if stream is not None:
+            _on(raw, stream, dev, out)
     else:
         op = _at(out, "out", dtype or out.dtype, shape, dev)
     D = shape[-1]
-    _check(_lib.mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, _x16(out, "out"), cp, sp, op,
-                                      _stream(stream, dev)), "mhc_ckpt8_restore_run")
+    _check(_lib.mhc_ckpt8_restore_run(codes.numel() // D if D else 0, D, _x16(out, "out"), cp, sp, op, raw),
+           "mhc_ckpt8_restore_run")
     return out
 
 
@@ -150,10 +171,13 @@ def hc_post_ckpt(x, residual, post, comb, out=None, ckpt=None, stream=None):
     xp = _at(x, "x", _bf16, lead + (D,), dev)
     pp = _at(post, "post", _f32, lead + (n,), dev)
     cp = _at(comb, "comb", _f32, lead + (n, n), dev)
+    raw = _stream(stream, dev)
+    made = () if stream is None else (out is None, ckpt is None)
     out, op = _out(out, "out", residual)
     ckpt, codes, scales = _ckpt_out(ckpt, shape, dev)
-    _check(_lib.mhc_post_ckpt_run(T, n, D, xp, rp, pp, cp, op, codes, scales, _stream(stream, dev)),
-           "mhc_post_ckpt_run")
+    if any(made):
+        _on(raw, stream, dev, *((out,) if made[0] else ()), *(ckpt if made[1] else ()))
+    _check(_lib.mhc_post_ckpt_run(T, n, D, xp, rp, pp, cp, op, codes, scales, raw), "mhc_post_ckpt_run")
     return out, ckpt
 
 
@@ -173,17 +197,20 @@ def hc_post_backward(grad_out, x, residual, post, comb, grads=None, stream=None)
         codes, scales = _ckpt_at(residual, shape, dev)
     else:
         rp = _at(residual, "residual", _bf16, shape, dev)
+    raw = _stream(stream, dev)
     if grads is None:
         grads = {"grad_x": torch.empty_like(x), "grad_residual": torch.empty_like(grad_out),
                  "grad_post": torch.empty_like(post), "grad_comb": torch.empty_like(comb)}
         out = [t.data_ptr() for t in grads.values()]
+        if stream is not None:
+            _on(raw, stream, dev, *grads.values())
     else:
         out = [_at(grads["grad_x"], "grad_x", _bf16, x.shape, dev),
                _at(grads["grad_residual"], "grad_residual", _bf16, shape, dev),
                _at(grads["grad_post"], "grad_post", _f32, post.shape, dev),
                _at(grads["grad_comb"], "grad_comb", _f32, comb.shape, dev)]
     a = MhcPostBwdArgs(T, n, D, gp, xp, rp, codes, scales, pp, cp, *out)
-    _check(_lib.mhc_post_backward_run(byref(a), _stream(stream, dev)), "mhc_post_backward_run")
+    _check(_lib.mhc_post_backward_run(byref(a), raw), "mhc_post_backward_run")
     return grads
 
 
@@ -216,19 +243,15 @@ def gated_ffn_status(workspace=None, stream=None) -> int:
                                _stream(stream, workspace.device))
 
 
-def _scratch(workspace, T, D, F, backward, device, stream):
-    """(raw stream, workspace tensor, its address, its bytes).  Scratch of one
-    call that runs on another stream than torch's current one is kept from
-    reuse until that stream has passed."""
-    raw = _stream(stream, device)
+def _scratch(workspace, T, D, F, backward, device, made):
+    """Workspace of one call: the tensor, its address, its bytes; a new one is
+    added to `made`."""
     if workspace is None:
         n = _scratch_bytes(T, D, F, backward)
         workspace = torch.empty((n,), dtype=_u8, device=device)
-        if stream is not None and n:
-            workspace.record_stream(torch.cuda.ExternalStream(raw, device=device))
-        return raw, workspace, workspace.data_ptr(), n
-    p = _at(workspace, "workspace", _u8, workspace.shape, device)
-    return raw, workspace, p, workspace.numel()
+        made.append(workspace)
+        return workspace, workspace.data_ptr(), n
+    return workspace, _at(workspace, "workspace", _u8, workspace.shape, device), workspace.numel()
 
 
 def _ffn_inputs(x, w_gate_up, w_down, act):
@@ -256,19 +279,29 @@ def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, wo
     dt, ac, T, D, F, shape, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
     dev = x.device
     kp = codes = scales = None
+    raw, made = _stream(stream, dev), []
     if save is None:
         if kept is not None:
             raise ValueError("kept goes with save")
     elif save == "16bit":
         if kept is None:
             kept = torch.empty(shape, dtype=x.dtype, device=dev)
+            made.append(kept)
         kp = _at(kept, "kept", x.dtype, shape, dev)
     elif save == "8bit":
-        kept, codes, scales = _ckpt_out(kept, shape, dev)
+        if kept is None:
+            kept = _ckpt_new(shape, dev)
+            made.extend(kept)
+        codes, scales = _ckpt_at(kept, shape, dev)
     else:
         raise ValueError(f'save must be None, "16bit" or "8bit" (got {save!r})')
-    y, yp = _out(y, "y", x)
-    raw, workspace, p, n = _scratch(workspace, T, D, F, False, dev, stream)
+    if y is None:
+        y = torch.empty_like(x)
+        made.append(y)
+    yp = _at(y, "y", x.dtype, x.shape, dev)
+    workspace, p, n = _scratch(workspace, T, D, F, False, dev, made)
+    if stream is not None and made:
+        _on(raw, stream, dev, *made)
     a = MhcFfnArgs(T, D, F, dt, ac, xp, gp, wp, yp, kp, codes, scales, p, n)
     _check(_lib.mhc_ffn_run(byref(a), raw), "mhc_ffn_run")
     return y, kept
@@ -286,15 +319,19 @@ def gated_ffn_backward(grad_y, x, w_gate_up, w_down, kept, act="silu", grads=Non
         codes, scales = _ckpt_at(kept, shape, dev)
     else:
         kp = _at(kept, "kept", xt, shape, dev)
+    raw, made = _stream(stream, dev), []
     if grads is None:
         grads = {"grad_x": torch.empty_like(x), "grad_w_gate_up": torch.empty_like(w_gate_up),
                  "grad_w_down": torch.empty_like(w_down)}
         out = [t.data_ptr() for t in grads.values()]
+        made.extend(grads.values())
     else:
         out = [_at(grads["grad_x"], "grad_x", xt, x.shape, dev),
                _at(grads["grad_w_gate_up"], "grad_w_gate_up", xt, w_gate_up.shape, dev),
                _at(grads["grad_w_down"], "grad_w_down", xt, w_down.shape, dev)]
-    raw, workspace, p, n = _scratch(workspace, T, D, F, True, dev, stream)
+    workspace, p, n = _scratch(workspace, T, D, F, True, dev, made)
+    if stream is not None and made:
+        _on(raw, stream, dev, *made)
     a = MhcFfnBwdArgs(T, D, F, dt, ac, yp, xp, gp, wp, kp, codes, scales, *out, p, n)
     _check(_lib.mhc_ffn_backward_run(byref(a), raw), "mhc_ffn_backward_run")
     return grads

@@ -332,3 +332,29 @@ def test_refusals(cuda_device):
     for args in ((gy.half(), x, w, wd, gu), (gy, x, w, wd, gu[:, :1]), (gy, x, w, wd, gu.half()), (gy[:2], x, w, wd, gu)):
         with pytest.raises(ValueError):
             gated_ffn_backward(*args)
+
+
+def test_new_outputs_on_another_stream_wait_for_their_memory(cuda_device):
+    """A call on another stream than torch's current one gets memory that the
+    current stream was still writing: its results must not be overwritten."""
+    from mhc_hyper_connection_gb300 import gated_ffn, hc_post_backward
+    from mhc_synth import make_post_case
+    c = _case(cuda_device, 64, 256, 520, "bf16", 12)
+    want, _ = gated_ffn(c["x"], c["w"], c["wd"])
+    pc = make_post_case(device=cuda_device, T=64, n=4, D=256, seed=2)
+    g = pc.residual.clone()
+    want_b = hc_post_backward(g, pc.x, pc.residual, pc.post, pc.comb)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    big = torch.empty((1 << 28,), device=cuda_device)
+    for _ in range(4):
+        for _ in range(10):
+            big.fill_(1.0)                       # the current stream is behind by a millisecond
+        del_me = [torch.empty_like(want) for _ in range(4)] + [torch.empty_like(g), torch.empty_like(pc.post)]
+        for t in del_me:
+            t.fill_(float("nan"))                # queued writes to memory that is now freed
+        del t, del_me
+        y, _ = gated_ffn(c["x"], c["w"], c["wd"], stream=st)
+        b = hc_post_backward(g, pc.x, pc.residual, pc.post, pc.comb, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and all(torch.equal(b[k], want_b[k]) for k in b)
