@@ -189,9 +189,11 @@ __device__ __forceinline__ float act_arg(float z, int act) {
 __device__ __forceinline__ float sigmoid_fast(float r) { return __fdividef(1.0f, 1.0f + __expf(-r)); }
 
 // gg = ga u act'(z), gu = ga act(z) and a = act(z) u; act' = s + z s (1 - s) r'(z).
+// r' is kept finite: z z overflows from |z| = 1.8e19 on, where s is 0 or 1 and the
+// product with it is 0.
 __device__ __forceinline__ void gate_grads(float z, float u, float ga, int act, float& gg, float& gu, float& a) {
   const float s = sigmoid_fast(act_arg(z, act));
-  const float dr = act == 0 ? 1.0f : 1.5957691216f * fmaf(3.0f * 0.044715f, z * z, 1.0f);
+  const float dr = act == 0 ? 1.0f : fminf(1.5957691216f * fmaf(3.0f * 0.044715f, z * z, 1.0f), 3e38f);
   const float h = z * s;
   gg = ga * u * fmaf(h * (1.0f - s), dr, s);
   gu = ga * h;

@@ -6,8 +6,9 @@
 // One pass over g, x and the residual streams.  Bounded by HBM: (2n + 1) 2
 // bytes read (n - n/128 fewer from a checkpoint) and (n + 1) 2 written per
 // column, against 2 (n + n^2) products.  Those run on the tensor cores: on the
-// CUDA cores they took longer than the memory (n = 8, T = 16384, D = 2048 from a checkpoint: 430 us, 51% of measured HBM; now
-// 238 us, 92%; n = 4, T = 32768, D = 7168: 1092 us, now 1000, 97%).
+// CUDA cores they took longer than the memory (n = 8, T = 16384, D = 2048 from a
+// checkpoint: 430 us, 51% of measured HBM; now 238 us, 92%; n = 4, T = 32768, D =
+// 7168: 1092 us, now 1000, 97%).
 #include <atomic>
 
 #include "mhc_ckpt.cuh"

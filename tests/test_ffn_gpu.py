@@ -358,3 +358,25 @@ def test_new_outputs_on_another_stream_wait_for_their_memory(cuda_device):
         b = hc_post_backward(g, pc.x, pc.residual, pc.post, pc.comb, stream=st)
         torch.cuda.synchronize()
         assert torch.equal(y, want) and all(torch.equal(b[k], want_b[k]) for k in b)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [1, 130])
+def test_gates_whose_square_overflows(cuda_device, T, act):
+    """Gates up to the type's largest values: the derivative is 1 and 0 there,
+    not 0 times an overflowed square.  One value of grad_y is not zero, so ga is
+    one exact product; gg and the gradient are then rounded to bf16 once each."""
+    from mhc_hyper_connection_gb300 import gated_ffn_backward
+    c = _case(cuda_device, T, 8, 8, "bf16", 5)
+    z = torch.tensor([1e10, -1e10, 2e19, -2e19, 1e25, -1e25, 3e38, -3e38], device=cuda_device).bfloat16()
+    kept = torch.empty((T, 2, 8), device=cuda_device, dtype=torch.bfloat16)
+    kept[:, 0] = z
+    kept[:, 1] = 0.5
+    c["gy"].zero_()
+    c["gy"][0, 3] = 1.0
+    c["wd"][3] = 2.0 ** -20                      # ga z and grad_x stay finite
+    got = gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept, act=act)
+    assert all(torch.isfinite(v).all() for v in got.values())
+    gg = np.where(_f64(z) > 0, 0.5 * 2.0 ** -20, 0.0)
+    want = gg[:, None] * _f64(c["x"])[0]
+    _near(got["grad_w_gate_up"][0], want, 1.01 * 2.0 ** -8 * np.abs(want), "grad_w_gate_up")
