@@ -5,7 +5,7 @@
 // HBM.  So the weights are the 128-row side of the tensor-core product and the
 // tokens its N side (a multiple of 16), each CTA streams its own rows of the
 // weights through a ring of stages, and where the rows alone do not fill the
-// device, a cluster of 2, 4 or 8 CTAs shares them, each taking a part of the
+// device, a cluster of 2 to 8 CTAs shares them, each taking a part of the
 // depth.  Their fp32 sums are exchanged over distributed shared memory: each
 // CTA gets all parts of its share of the tokens, adds them in rank order (no
 // atomics: the same bits every time) and finishes those tokens.
@@ -33,6 +33,8 @@ constexpr size_t kFewHalfSm = 112 * 1024;        // shared memory of which two C
 constexpr int kFewMinStages = 3;
 constexpr int kFewMaxStages = 12;
 constexpr int kFewRows = 128;                    // weight rows of one accumulator
+constexpr int kFewMostSplit = 8;                 // CTAs of a cluster
+constexpr int kFewMostSmem = 220 * 1024;         // shared memory of a CTA
 
 struct FewTail {
   uint64_t full[kFewMaxStages], empty[kFewMaxStages];
@@ -57,10 +59,19 @@ struct FewShape {
 
 __host__ __device__ constexpr int few_stage_bytes(bool two, int nt) { return (two ? 2 : 1) * 16384 + nt * 128; }
 // Tokens that each of `split` CTAs finishes: an equal share, in fours.
-__host__ __device__ constexpr int few_share(int nt, int split) { return (nt / split + 3) & ~3; }
+__host__ __device__ constexpr int few_share(int nt, int split) { return ((nt + split - 1) / split + 3) & ~3; }
 __host__ __device__ constexpr int few_room_bytes(bool two, int nt, int split) {
   return (two ? 2 : 1) * split * few_share(nt, split) * 512;
 }
+// From 65 tokens on the sums lie in the ring.
+constexpr bool few_rooms_fit() {
+  for (int nt = 16; nt <= kFewTokens; nt += 16)
+    for (int split = 1; split <= kFewMostSplit; ++split)
+      for (int two = 0; two < 2; ++two)
+        if ((split == 1 || nt > 64) && few_room_bytes(two, nt, split) > (two ? kFewRingTwo : kFewRingOne)) return false;
+  return true;
+}
+static_assert(few_rooms_fit(), "the ring holds the sums");
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
@@ -195,9 +206,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int k0 = (int)((long long)g.kiters * rank / g.split), k1 = (int)((long long)g.kiters * (rank + 1) / g.split);
   const int stage_bytes = few_stage_bytes(kTwo, g.nt), stages = g.stages;
   Ctl ctl{&tail->abort, g.err, g.wait_ns};
-  static_assert(kFewRingTwo >= 2 * 128 * 512 && kFewRingOne >= 128 * 512, "the ring holds the sums of 128 tokens");
-  static_assert(few_room_bytes(false, 48, 8) <= kFewRingOne && few_room_bytes(true, 112, 8) <= kFewRingTwo,
-                "and of fewer, with shares rounded up");
 
   if (threadIdx.x == 0) {
     if (g.first && blockIdx.x == 0) g.err[0] = g.err[1] = 0u;   // as in ffn_gemm_kernel
@@ -402,10 +410,10 @@ inline size_t few_layout(FewShape& g, bool two, int split) {
 // counts one CTA per SM for those that do, whatever they allocate.
 static __global__ void __launch_bounds__(kFewThreads) few_shape_kernel() {}
 
-// Clusters of 2, 4 and 8 CTAs that the device holds at once, with the shared
-// memory of two CTAs per SM (first row) or of one; looked up once per device.
+// Clusters of each size that the device holds at once, with the shared memory of
+// two CTAs per SM (first row) or of one; looked up once per device.
 struct FewClusters {
-  int n[2][3];
+  int n[2][kFewMostSplit + 1];
 };
 inline cudaError_t few_clusters(int dev, FewClusters* out) {
   static std::mutex mu;
@@ -414,19 +422,19 @@ inline cudaError_t few_clusters(int dev, FewClusters* out) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (!have[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMostSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.blockDim = dim3(kFewThreads);
-    cfg.gridDim = dim3(1024);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     for (int c = 0; c < 2; ++c) {
-      for (int i = 0; i < 3; ++i) {
-        attr[0].val.clusterDim.x = 2u << i;
+      for (int i = 2; i <= kFewMostSplit; ++i) {
+        attr[0].val.clusterDim.x = (unsigned)i;
+        cfg.gridDim = dim3(1024u * i);
         cfg.dynamicSmemBytes = c == 0 ? kFewHalfSm : 160 * 1024;
         if ((e = cudaOccupancyMaxActiveClusters(&known[dev].n[c][i], few_shape_kernel, &cfg)) != cudaSuccess) return e;
       }
@@ -439,7 +447,11 @@ inline cudaError_t few_clusters(int dev, FewClusters* out) {
 
 // CTAs per tile: the most whose clusters the device holds all at once, with
 // four chunks of the depth each at least (D = 1024, F = 4096, one token: 14.4 us,
-// with eight chunks 15.1, one CTA per tile 29.6).
+// with eight chunks 15.1, one CTA per tile 29.6).  Clusters that start as SMs fall
+// free pack less tightly than on an empty device, so a sixteenth stays free (one
+// token, D = 7168, F = 8192, second product: 56 clusters of 5, of at most 58, 72
+// us, of 4 65.4).  Against sizes of 2, 4 and 8 alone: one token, D = 4424, F =
+// 5192: 38.5 -> 34.5 us; 64 tokens, D = 7168, F = 2048: 32.8 -> 30.5.
 template <class Epi>
 cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g, const Epi& epi, cudaStream_t s) {
   auto* k = ffn_few_kernel<Epi>;
@@ -449,7 +461,7 @@ cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (e = few_clusters(dev, &fit)) != cudaSuccess) return e;
   if (!ready[dev].load(std::memory_order_relaxed)) {
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMostSmem)) != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
@@ -462,12 +474,14 @@ cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, FewShape g,
   cfg.stream = s;
   cfg.attrs = attr;
   size_t smem = few_layout(g, Epi::kTwo, 1);
-  for (int i = 0; i < 3; ++i) {
+  for (int split = kFewMostSplit; split > 1; --split) {
     FewShape w = g;
-    const size_t bytes = few_layout(w, Epi::kTwo, 2 << i);
-    if (g.kiters < 4 * w.split || g.tiles > fit.n[bytes > kFewHalfSm ? 1 : 0][i]) break;
+    const size_t bytes = few_layout(w, Epi::kTwo, split);
+    const int most = fit.n[bytes > kFewHalfSm ? 1 : 0][split];
+    if (bytes > (size_t)kFewMostSmem || g.kiters < 4 * split || g.tiles > most - (g.first ? 0 : most / 16)) continue;
     g = w;
     smem = bytes;
+    break;
   }
   attr[0].val.clusterDim.x = (unsigned)g.split;
   cfg.gridDim = dim3((unsigned)(g.tiles * g.split));

@@ -380,3 +380,17 @@ def test_gates_whose_square_overflows(cuda_device, T, act):
     gg = np.where(_f64(z) > 0, 0.5 * 2.0 ** -20, 0.0)
     want = gg[:, None] * _f64(c["x"])[0]
     _near(got["grad_w_gate_up"][0], want, 1.01 * 2.0 ** -8 * np.abs(want), "grad_w_gate_up")
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 64, 65, 80, 100, 128])
+@pytest.mark.parametrize("D,F", [(768, 1280), (1280, 1536), (1792, 768)])
+def test_few_tokens_in_clusters_of_every_size(cuda_device, T, D, F):
+    """Depths of 12, 20, 24 and 28 chunks: blocks in clusters of 3, 5, 6 and 7,
+    whose shares of the tokens are not equal."""
+    from mhc_hyper_connection_gb300 import gated_ffn, gated_ffn_backward, gated_ffn_status
+    c = _case(cuda_device, T, D, F, "bf16", T + D)
+    y, kept = gated_ffn(c["x"], c["w"], c["wd"], save="8bit")
+    _check_forward(c, "bf16", "silu", y, kept)
+    got = gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept)
+    assert gated_ffn_status() == 0
+    _check_backward(c, "bf16", "silu", got, kept)
