@@ -24,7 +24,7 @@ struct FastDiv {
 // One matrix product D[M, N] = A B^T on 16-bit operands: operand row r, depth
 // k.  "K-major" operands store k contiguously, "MN-major" ones r.
 struct GemmShape {
-  int tile_n;                  // width of a tile: 256 or 128
+  int tile_n;                  // width of a tile: 256, 192 or 128
   int tiles_m, tiles_n;
   int slices;                  // parts of the depth that are tiles of their own
   int kiters, kslice;          // chunks of 64 of the whole depth, and of a slice (the last may have fewer)

@@ -56,21 +56,28 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // launch, and each sum written and read once.
 double join_cost(int64_t M, int64_t N, int64_t slices) { return slices > 1 ? 10.0 + 8.0 * M * N * slices / 1.9e6 : 0.0; }
 
-// A product that has its launch to itself: tiles 256 or 128 wide and, where few
-// tiles meet a deep product (most > 1), slices of the depth, by the estimated time
-// of the rounds of tiles.  A narrow tile takes 0.6 of a wide one's time, with an
-// MN-major B 0.7; four stages are for a tile's start and end.  (T = 1021, D =
-// 2048, F = 5512, down: 64 narrow tiles, forward 68 us where 32 wide ones took
-// 75.5; T = 256, D = 4096, F = 8192, down in 2 slices: forward 70 -> 60 us.)
+// A product that has its launch to itself: tiles 256, 192 or 128 wide and, where
+// few tiles meet a deep product (most > 1), slices of the depth, by the estimated
+// time of the rounds of tiles.  A stage of a narrow tile takes 0.6 of a wide one's
+// time, with an MN-major B 0.7; of a tile 192 wide 0.8, with an MN-major B (which
+// comes in blocks of 64, so as much is copied) what a wide one takes: only its
+// epilogue is shorter.  Four wide stages are for a tile's start and end.  (T =
+// 1021, D = 2048, F = 5512, down: 64 narrow tiles, forward 68 us where 32 wide ones
+// took 75.5; T = 256, D = 4096, F = 8192, down in 2 slices: forward 70 -> 60 us; T =
+// 1500, D = F = 4096, down: two rounds 192 wide where two of 256 took 119 us for the
+// forward, now 104.5; T = 1021, D = 2048, F = 5512, gate gradients: 116 tiles 192
+// wide, backward 135 -> 130.)
 Cut cut_alone(int64_t M, int64_t N, int64_t K, bool b_mn, int most) {
   const int64_t kiters = div_up(K, kFfnTileK), rows = div_up(M, kFfnTileM);
   Cut best = {256, 1, (int)kiters};
   double least = 1e30;
-  for (int w = 256; w >= 128; w -= 128) {
+  for (int w = 256; w >= 128; w -= 64) {
+    const double stage = w == 256 ? 1.0 : w == 192 ? (b_mn ? 1.02 : 0.8) : b_mn ? 0.7 : 0.6;
+    const double ends = w == 192 && b_mn ? 3.0 : 4.0 * stage;
     for (int64_t s = 1; s <= most && (s == 1 || kiters >= 8 * s); ++s) {
       const int64_t per = div_up(kiters, s), slices = div_up(kiters, per);
       const double rounds = (double)div_up(rows * div_up(N, w) * slices, kPairs);
-      const double cost = rounds * (per + 4) * (w == 256 ? 1.0 : b_mn ? 0.7 : 0.6) + join_cost(M, N, slices);
+      const double cost = rounds * (per * stage + ends) + join_cost(M, N, slices);
       if (cost < least - 1e-9) {
         least = cost;
         best = {w, (int)slices, (int)per};

@@ -278,17 +278,19 @@ struct EpiStore {
       }
       return;
     }
+    const int end = (grp + 1) * (cols / 2);        // the last step may have 32 columns
 #pragma unroll 1
-    for (int c = grp * (cols / 2); c < (grp + 1) * (cols / 2) && n0 + c < N; c += 64) {
+    for (int c = grp * (cols / 2); c < end && n0 + c < N; c += 64) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        if (h && c + 32 >= end) break;
         float v[32];
         acc_ld32(taddr + c + 32 * h, v);
 #pragma unroll
         for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + q)) = pack8v<F16>(v + 8 * q);
       }
       stage_flush(buf, reinterpret_cast<uint8_t*>(out + (size_t)row0 * N + n0 + c), (size_t)N * 2, M - row0,
-                  min(64, N - n0 - c) * 2, lane);
+                  min(min(64, end - c), N - n0 - c) * 2, lane);
     }
   }
 };
@@ -632,8 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int m0 = tm * kFfnTileM + (int)rank * kGemmHalf;
         const int half_n = g.tile_n / 2;
         const int n0 = kPair ? tn * kGemmHalf : tn * g.tile_n + (int)rank * half_n;
-        const uint32_t bytes = 2u * (uint32_t)(kGemmOpBytes + half_n * kFfnTileK * 2);   // of both CTAs
         const int plane = kPair ? (int)rank : 0, a_mn = g.a_mn, b_mn = g.b_mn;
+        // of both CTAs; an MN-major B comes in blocks of 64 rows
+        const uint32_t bytes = 2u * (uint32_t)(kGemmOpBytes + (b_mn ? (half_n + 63) & ~63 : half_n) * kFfnTileK * 2);
         const int kbeg = slice * g.kslice, kiters = min(g.kslice, g.kiters - kbeg);
         int after = -1;                          // tile n + 2, drawn under this tile's copies
         if (kDraw && rank == 0 && next >= 0) after = draw();

@@ -394,3 +394,17 @@ def test_few_tokens_in_clusters_of_every_size(cuda_device, T, D, F):
     got = gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept)
     assert gated_ffn_status() == 0
     _check_backward(c, "bf16", "silu", got, kept)
+
+
+@pytest.mark.parametrize("T,D,F", [(300, 64, 10240), (300, 10040, 72), (769, 72, 4104), (420, 7112, 136), (1182, 152, 15360)])
+def test_tiles_of_three_quarters(cuda_device, T, D, F):
+    """Sizes at which tiles 192 wide take the fewest rounds: many columns, few
+    rows, in the gate gradients (wide F) or in the down product (wide D); with the
+    depth cut into slices in the last."""
+    from mhc_hyper_connection_gb300 import gated_ffn, gated_ffn_backward
+    for kind, act in (("bf16", "silu"), ("fp16", "gelu")):
+        c = _case(cuda_device, T, D, F, kind, T + 1)
+        for save in ("16bit", "8bit"):
+            y, kept = gated_ffn(c["x"], c["w"], c["wd"], act=act, save=save)
+            _check_forward(c, kind, act, y, kept)
+            _check_backward(c, kind, act, gated_ffn_backward(c["gy"], c["x"], c["w"], c["wd"], kept, act=act), kept)
