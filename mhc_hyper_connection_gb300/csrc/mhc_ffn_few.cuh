@@ -14,10 +14,10 @@
 // dependent launch) and load the weights' first chunks before they wait for the
 // tokens.
 //
-// One token, D = 7168, F = 8192: 65.5 us for 352 MB of weights, 79% of the
+// One token, D = 7168, F = 8192: 64.4 us for 352 MB of weights, 81% of the
 // measured copy rate; the two products' loops stream at 6.9 and 5.3 TB/s, the
 // rest is their starts and joins, about 4 us each.  24 tokens at D = 4096, F =
-// 8192: 44.9 us (66%).  As ordinary tiles of 256 tokens these took 114 and 80.
+// 8192: 43.9 us (68%).  As ordinary tiles of 256 tokens these took 114 and 80.
 #pragma once
 
 #include <mutex>
@@ -27,14 +27,17 @@
 namespace mhc {
 
 constexpr int kFewThreads = 192;                 // producer, MMA issuer, four epilogue warps
-constexpr int kFewRingTwo = 160 * 1024;          // ring (and room) of the gate and up product
-constexpr int kFewRingOne = 76 * 1024;           // of the others: two CTAs fit an SM
+// Ring and room of the gate and up product, one CTA per SM (24 tokens, D = 4096, F
+// = 8192: 43.9 us, with 160 KB 45.0), and of the others, of which two fit an SM
+// (backward of 24 tokens, D = 1024, F = 4096: 32.2 us, with 76 KB 34.2).
+constexpr int kFewRingTwo = 214 * 1024;
+constexpr int kFewRingOne = 108 * 1024;
 constexpr size_t kFewHalfSm = 112 * 1024;        // shared memory of which two CTAs fit an SM
 constexpr int kFewMinStages = 3;
 constexpr int kFewMaxStages = 12;
 constexpr int kFewRows = 128;                    // weight rows of one accumulator
 constexpr int kFewMostSplit = 8;                 // CTAs of a cluster
-constexpr int kFewMostSmem = 220 * 1024;         // shared memory of a CTA
+constexpr int kFewMostSmem = 224 * 1024;         // shared memory of a CTA
 
 struct FewTail {
   uint64_t full[kFewMaxStages], empty[kFewMaxStages];
@@ -435,7 +438,7 @@ inline cudaError_t few_clusters(int dev, FewClusters* out) {
       for (int i = 2; i <= kFewMostSplit; ++i) {
         attr[0].val.clusterDim.x = (unsigned)i;
         cfg.gridDim = dim3(1024u * i);
-        cfg.dynamicSmemBytes = c == 0 ? kFewHalfSm : 160 * 1024;
+        cfg.dynamicSmemBytes = c == 0 ? kFewHalfSm : kFewMostSmem;
         if ((e = cudaOccupancyMaxActiveClusters(&known[dev].n[c][i], few_shape_kernel, &cfg)) != cudaSuccess) return e;
       }
     }

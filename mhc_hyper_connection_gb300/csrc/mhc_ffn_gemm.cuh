@@ -2,7 +2,8 @@
 // tensor cores, with a fused epilogue.
 //
 // Persistent pairs of CTAs (clusters of two, one tcgen05 cta_group::2) take
-// output tiles of 256 x 256.  Each CTA holds 128 rows of A and 128 of B, so a
+// output tiles of 256 x 256 (or 192 or 128 wide, where that saves a round of tiles,
+// with fewer rows of B).  Each CTA holds 128 rows of A and 128 of B, so a
 // stage of depth 64 is 32 KB per SM where a tile of its own (128 x 256) would
 // be 48: a third less L2 traffic and six stages instead of four.  In each CTA
 // one warp streams its operand rows into the ring (TMA, 128-byte swizzle, all
