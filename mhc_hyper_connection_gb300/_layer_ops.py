@@ -4,7 +4,8 @@ with a checkpoint and its backward, the gated feed-forward block.
 Argument checks and marshalling only; the computation is in the CUDA library
 (include/mhc_ckpt.h, mhc_post_backward.h, mhc_ffn.h).  A call of these is as
 short as a launch or two, so the checks are one comparison each and torch's
-current stream is read as a raw handle.  Contiguous CUDA tensors only.
+current stream is read as a raw handle.  Contiguous CUDA tensors on the current
+device only.
 
 A call runs on `stream` (torch's current one if None).  If that is another
 stream, it waits for the current one only where the call allocates something;
@@ -25,6 +26,7 @@ _bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
 _DTYPES = {torch.bfloat16: MHC_DTYPE_BF16, torch.float16: MHC_DTYPE_FP16}
 _ACTS = {"silu": MHC_FFN_SILU, "gelu": MHC_FFN_GELU}
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class Ckpt8(NamedTuple):
@@ -35,10 +37,15 @@ class Ckpt8(NamedTuple):
 
 
 def _stream(stream, device) -> int:
-    """Raw handle of a torch stream, an integer, or torch's current stream."""
+    """Raw handle of a torch stream, an integer, or torch's current stream.
+    The library launches on the current device, so the tensors' device has to
+    be that one."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device (got {device})")
+    if device.index != _current_device():
+        raise ValueError(f"tensors are on {device}, but the current CUDA device is cuda:{_current_device()} "
+                         "(make theirs current for the call: torch.cuda.device)")
     if stream is None:
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device (got {device})")
         return _current_raw_stream(device.index)
     return int(getattr(stream, "cuda_stream", stream))
 

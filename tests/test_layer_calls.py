@@ -1,0 +1,90 @@
+"""The torch side of the layer operators without a GPU: what a call hands to
+the library, and what it refuses before that.  The library is replaced by a
+record of its calls and tensors by stand-ins, so nothing is launched."""
+import pytest
+import torch
+
+from mhc_hyper_connection_gb300 import build as mbuild
+
+BF16, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
+CURRENT, STREAM = 0, 0x5000      # the current device, and the handle of its current stream
+
+
+class Tensor:
+    """What the argument checks look at."""
+
+    def __init__(self, shape, dtype=BF16, device="cuda:0", at=None):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self.at = at if at is not None else 1 << 20
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return self.shape.numel()
+
+
+class Library:
+    """Records calls: name -> arguments of the last one."""
+
+    def __init__(self):
+        self.calls = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls[name] = args
+            return 0
+        return call
+
+
+@pytest.fixture
+def ops(monkeypatch):
+    mbuild.build()
+    from mhc_hyper_connection_gb300 import _layer_ops
+    monkeypatch.setattr(_layer_ops, "_lib", Library())
+    monkeypatch.setattr(_layer_ops, "_current_device", lambda: CURRENT, raising=False)
+    monkeypatch.setattr(_layer_ops, "_current_raw_stream", lambda index: STREAM + index)
+    return _layer_ops
+
+
+def _calls(ops, device):
+    """Every launching call, with outputs and workspace given: (C function, call of `stream`)."""
+    def t(*shape, d=BF16):
+        return Tensor(shape, d, device)
+    T, n, D, F = 3, 4, 64, 128
+    ck = ops.Ckpt8(t(T, n, D, d=U8), t(T, n, 1, d=U8))
+    x, res, post, comb = t(T, D), t(T, n, D), t(T, n, d=F32), t(T, n, n, d=F32)
+    grads = {"grad_x": t(T, D), "grad_residual": t(T, n, D), "grad_post": t(T, n, d=F32), "grad_comb": t(T, n, n, d=F32)}
+    w, wd, kept, ws = t(2, F, D), t(D, F), t(T, 2, F), t(1 << 20, d=U8)
+    ffn = {"grad_x": t(T, D), "grad_w_gate_up": t(2, F, D), "grad_w_down": t(D, F)}
+    return [("mhc_ckpt8_pack_run", lambda s: ops.ckpt8_pack(res, out=ck, stream=s)),
+            ("mhc_ckpt8_restore_run", lambda s: ops.ckpt8_restore(ck, out=t(T, n, D), stream=s)),
+            ("mhc_post_ckpt_run", lambda s: ops.hc_post_ckpt(x, res, post, comb, out=t(T, n, D), ckpt=ck, stream=s)),
+            ("mhc_post_backward_run", lambda s: ops.hc_post_backward(t(T, n, D), x, res, post, comb, grads=grads, stream=s)),
+            ("mhc_ffn_run", lambda s: ops.gated_ffn(x, w, wd, y=t(T, D), workspace=ws, stream=s)),
+            ("mhc_ffn_backward_run", lambda s: ops.gated_ffn_backward(t(T, D), x, w, wd, kept, grads=ffn, workspace=ws,
+                                                                      stream=s))]
+
+
+@pytest.mark.parametrize("k", range(6))
+def test_streams(ops, k):
+    """A call runs on torch's current stream, a torch stream or a raw handle."""
+    name, call = _calls(ops, "cuda:0")[k]
+    for stream, want in ((None, STREAM), (77, 77), (type("S", (), {"cuda_stream": 99})(), 99)):
+        call(stream)
+        assert ops._lib.calls[name][-1] == want
+
+
+@pytest.mark.parametrize("k", range(6))
+@pytest.mark.parametrize("device", ["cpu", "cuda:1"])
+def test_tensors_of_another_device(ops, k, device):
+    """Neither host tensors nor those of a device that is not the current one
+    reach the library, whatever stream is given."""
+    _, call = _calls(ops, device)[k]
+    for stream in (None, 77):
+        with pytest.raises(ValueError):
+            call(stream)
+    assert not ops._lib.calls
