@@ -240,6 +240,22 @@ def mhc_post_run(T: int, n: int, D: int, x: int, residual: int, post: int, comb:
                                   _P(comb or None), _P(out or None), _P(stream or None))
 
 
+def _launch_stream(stream, device) -> int:
+    """Raw handle of a torch stream, an integer, or torch's current stream on
+    `device`.  The library launches on the current device, so the tensors'
+    device has to be that one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device (got {device})")
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"tensors are on {device}, but the current CUDA device is cuda:{current} "
+                         "(make theirs current for the call: torch.cuda.device)")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return int(getattr(stream, "cuda_stream", stream))
+
+
 def hc_post(x, residual, post, comb, out=None, stream=None):
     """out[t, j, d] = post[t, j] x[t, d] + sum_i comb[t, i, j] residual[t, i, d]
     on torch tensors (x bf16 [T, D], residual bf16 [T, n, D], post fp32 [T, n],
@@ -249,13 +265,10 @@ def hc_post(x, residual, post, comb, out=None, stream=None):
     import torch
     n, D = residual.shape[-2:]
     T = _tokens(residual.shape[:-2])
+    stream = _launch_stream(stream, residual.device)
     if out is None:
         out = torch.empty(residual.shape, dtype=torch.bfloat16, device=residual.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(residual.device).cuda_stream
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    st = mhc_post_run(T, n, D, _ptr(x), _ptr(residual), _ptr(post), _ptr(comb), _ptr(out), int(stream))
+    st = mhc_post_run(T, n, D, _ptr(x), _ptr(residual), _ptr(post), _ptr(comb), _ptr(out), stream)
     if st != MHC_OK:
         raise MhcError(st, "mhc_post_run", last_error())
     return out
@@ -454,12 +467,9 @@ class MhcPre:
         st, nbytes = mhc_pre_weights_size(self.handle)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_weights_size", last_error())
+        stream = _launch_stream(stream, phi.device)
         w = torch.empty((nbytes,), dtype=torch.uint8, device=phi.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(phi.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            stream = stream.cuda_stream
-        st = mhc_pre_prepare_weights(self.handle, _ptr(phi), _ptr(gamma), _ptr(w), nbytes, int(stream))
+        st = mhc_pre_prepare_weights(self.handle, _ptr(phi), _ptr(gamma), _ptr(w), nbytes, stream)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_prepare_weights", last_error())
         return w
@@ -482,12 +492,7 @@ class MhcPre:
         torch's current stream).  `weights` (from prepare_weights) replaces
         phi and gamma.  Raises MhcError on a host-side rejection."""
         args = self.make_args(x, phi, alpha, bias, out, gamma, pre_mix, weights)
-        if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(x.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            stream = stream.cuda_stream
-        st = mhc_pre_run(self.handle, args, int(stream))
+        st = mhc_pre_run(self.handle, args, _launch_stream(stream, x.device))
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_run", last_error())
         return out
@@ -539,12 +544,7 @@ class MhcPre:
         Raises MhcError on a host-side rejection."""
         args = self.make_backward_args(x, phi, alpha, gamma, grad_h_in, grad_h_post, grad_h_res, saved,
                                        grads, grad_x_post)
-        if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(x.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            stream = stream.cuda_stream
-        st = mhc_pre_backward_run(self.handle, args, int(stream))
+        st = mhc_pre_backward_run(self.handle, args, _launch_stream(stream, x.device))
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_backward_run", last_error())
         return grads
@@ -555,22 +555,19 @@ class MhcPre:
         same outputs as run().  A debug aid: slower than the fused run()."""
         import torch
         T = _tokens(x.shape[:-2])
-        if stream is None:
-            stream = torch.cuda.current_stream(x.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            stream = stream.cuda_stream
+        stream = _launch_stream(stream, x.device)
         ir = out.get("inv_rms")
         ir = ir if ir is not None else torch.empty((T,), dtype=torch.float32, device=x.device)
         mx = out.get("h_mix")
         mx = mx if mx is not None else torch.empty((T, self.R), dtype=torch.float32, device=x.device)
-        st = mhc_pre_inv_rms_run(self.handle, T, _ptr(x), _ptr(ir), int(stream))
+        st = mhc_pre_inv_rms_run(self.handle, T, _ptr(x), _ptr(ir), stream)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_inv_rms_run", last_error())
-        st = mhc_pre_mixes_run(self.handle, T, _ptr(x), _ptr(phi), _ptr(gamma), _ptr(mx), int(stream))
+        st = mhc_pre_mixes_run(self.handle, T, _ptr(x), _ptr(phi), _ptr(gamma), _ptr(mx), stream)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_mixes_run", last_error())
         args = self.make_args(x, phi, alpha, bias, out, gamma, pre_mix)
-        st = mhc_pre_sinkhorn_run(self.handle, args, _ptr(mx), _ptr(ir), int(stream))
+        st = mhc_pre_sinkhorn_run(self.handle, args, _ptr(mx), _ptr(ir), stream)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_sinkhorn_run", last_error())
         return out

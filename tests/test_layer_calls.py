@@ -88,3 +88,51 @@ def test_tensors_of_another_device(ops, k, device):
         with pytest.raises(ValueError):
             call(stream)
     assert not ops._lib.calls
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    """The binding of the mappings, its library replaced like that of `ops`."""
+    mbuild.build()
+    from mhc_hyper_connection_gb300 import _binding
+    op = _binding.MhcPre(4, 64)                     # its handle comes from the real library
+    record = Library()
+    monkeypatch.setattr(_binding, "library", lambda: record)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: CURRENT)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device=None: type("S", (), {"cuda_stream": STREAM + (getattr(device, "index", 0) or 0)})())
+    _binding.record, _binding.op = record, op
+    yield _binding
+    monkeypatch.undo()
+    op.close()
+
+
+def _mapping_calls(b, device):
+    def t(*shape, d=BF16):
+        return Tensor(shape, d, device)
+    T, n, D = 3, 4, 64
+    x, phi, alpha, bias = t(T, n, D), t(24, n * D, d=F32), t(3, d=F32), t(24, d=F32)
+    out = {"y": t(T, D), "h_post": t(T, n, d=F32), "inv_rms": t(T, d=F32), "h_mix": t(T, 24, d=F32)}
+    return [("mhc_post_run", lambda s: b.hc_post(t(T, D), x, t(T, n, d=F32), t(T, n, n, d=F32), out=t(T, n, D), stream=s)),
+            ("mhc_pre_run", lambda s: b.op.run(x, phi, alpha, bias, out, stream=s)),
+            ("mhc_pre_sinkhorn_run", lambda s: b.op.run_composite(x, phi, alpha, bias, out, stream=s)),
+            ("mhc_pre_backward_run", lambda s: b.op.backward(x, phi, alpha, None, t(T, D), t(T, n, d=F32), t(T, n, n, d=F32),
+                                                             out, {}, stream=s))]
+
+
+@pytest.mark.parametrize("k", range(4))
+def test_mappings_on_their_device_and_others(binding, k, monkeypatch):
+    """The pre-mapping and the post-mapping: the stream that the library gets,
+    and no call for tensors of another device."""
+    monkeypatch.setattr(Tensor, "element_size", lambda self: 1, raising=False)
+    name, call = _mapping_calls(binding, "cuda:0")[k]
+    for stream, want in ((None, STREAM), (77, 77), (type("S", (), {"cuda_stream": 99})(), 99)):
+        call(stream)
+        got = binding.record.calls[name][-1]
+        assert getattr(got, "value", got) == want
+    binding.record.calls.clear()
+    for device in ("cpu", "cuda:1"):
+        for stream in (None, 77):
+            with pytest.raises(ValueError):
+                _mapping_calls(binding, device)[k][1](stream)
+    assert not binding.record.calls
