@@ -243,9 +243,12 @@ def gated_ffn_workspace(T: int, D: int, F: int, device, backward: bool = False):
 
 def gated_ffn_status(workspace=None, stream=None) -> int:
     """Waits for `stream` (default: torch's current stream), then the device
-    status of the last call that used `workspace`."""
+    status of the last call that used `workspace`: MHC_ERR_RUNTIME if one of its
+    waits gave up.  Without a workspace only the stream's own errors are seen:
+    the status of a call lies in its workspace."""
     if workspace is None:
-        return _lib.mhc_ffn_status(None, int(getattr(stream, "cuda_stream", stream or 0)) or None)
+        raw = _current_raw_stream(_current_device()) if stream is None else int(getattr(stream, "cuda_stream", stream))
+        return _lib.mhc_ffn_status(None, raw or None)
     return _lib.mhc_ffn_status(_at(workspace, "workspace", _u8, workspace.shape, workspace.device),
                                _stream(stream, workspace.device))
 
@@ -282,7 +285,8 @@ def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, wo
     "silu" or "gelu" (tanh form).  save keeps both projections for the
     backward: "16bit" as a tensor [T, 2, F], "8bit" as a Ckpt8 of that shape.
     Returns (y, kept); kept is None without save.  y, kept and workspace are
-    allocated unless given."""
+    allocated unless given; a device wait that gave up (outputs are then
+    incomplete) is reported by gated_ffn_status on a given workspace only."""
     dt, ac, T, D, F, shape, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
     dev = x.device
     kp = codes = scales = None
@@ -317,7 +321,7 @@ def gated_ffn(x, w_gate_up, w_down, act="silu", save=None, y=None, kept=None, wo
 def gated_ffn_backward(grad_y, x, w_gate_up, w_down, kept, act="silu", grads=None, workspace=None, stream=None):
     """Backward of gated_ffn from what it kept (a tensor or a Ckpt8): returns
     {"grad_x", "grad_w_gate_up", "grad_w_down"} in x's type, written into
-    `grads` when given."""
+    `grads` when given.  Status as for gated_ffn."""
     dt, ac, T, D, F, shape, xp, gp, wp = _ffn_inputs(x, w_gate_up, w_down, act)
     dev, xt = x.device, x.dtype
     yp = _at(grad_y, "grad_y", xt, x.shape, dev)

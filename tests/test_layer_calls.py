@@ -136,3 +136,15 @@ def test_mappings_on_their_device_and_others(binding, k, monkeypatch):
             with pytest.raises(ValueError):
                 _mapping_calls(binding, device)[k][1](stream)
     assert not binding.record.calls
+
+
+def test_status_waits_for_the_current_stream(ops):
+    """With and without a workspace the default is torch's current stream, not
+    the legacy default stream, which does not order behind torch's others."""
+    ws = Tensor((1024,), U8)
+    for stream, want in ((None, STREAM), (77, 77), (0, None), (type("S", (), {"cuda_stream": 99})(), 99)):
+        ops.gated_ffn_status(stream=stream)
+        assert ops._lib.calls["mhc_ffn_status"] == (None, want)
+    for stream, want in ((None, STREAM), (77, 77)):
+        ops.gated_ffn_status(ws, stream=stream)
+        assert ops._lib.calls["mhc_ffn_status"] == (ws.at, want)
