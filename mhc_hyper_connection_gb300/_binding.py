@@ -573,9 +573,13 @@ class MhcPre:
         return out
 
     def status(self, out=None, stream=None) -> int:
+        """Waits for `stream` (default: torch's current stream), then the device
+        status of the last run that used `out`'s workspace (None: of the last
+        mhc_pre_run_noalloc)."""
         ws = None if out is None else out.get("workspace")
         if stream is None:
-            stream = 0
+            import torch
+            stream = torch.cuda.current_stream().cuda_stream
         elif hasattr(stream, "cuda_stream"):
             stream = stream.cuda_stream
         return mhc_pre_status(self.handle, _ptr(ws) or 0, int(stream))

@@ -148,3 +148,12 @@ def test_status_waits_for_the_current_stream(ops):
     for stream, want in ((None, STREAM), (77, 77)):
         ops.gated_ffn_status(ws, stream=stream)
         assert ops._lib.calls["mhc_ffn_status"] == (ws.at, want)
+
+
+def test_mapping_status_waits_for_the_current_stream(binding, monkeypatch):
+    """As above for MhcPre.status, which reads the error word of a workspace:
+    read on the legacy default stream it could be read before the run."""
+    monkeypatch.setattr(Tensor, "element_size", lambda self: 1, raising=False)
+    for stream, want in ((None, STREAM), (77, 77), (0, None)):
+        binding.op.status({"workspace": Tensor((1024,), U8)}, stream=stream)
+        assert binding.record.calls["mhc_pre_status"][-1].value == want
