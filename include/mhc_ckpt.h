@@ -22,9 +22,10 @@
  * codes: uint8 [rows, D].  scales: uint8 [rows, ceil(D / 128)], e + 127.
  *
  * Status codes are those of mhc_pre.h; all tensors are contiguous device
- * memory owned by the caller; every call is asynchronous on `stream` (a
- * cudaStream_t, NULL = legacy default stream), needs no workspace and waits
- * for nothing on the device.
+ * memory owned by the caller, outputs apart from inputs and from one another
+ * (an overlap gives MHC_ERR_PARAM_INVALID); every call is asynchronous on
+ * `stream` (a cudaStream_t, NULL = legacy default stream), needs no workspace
+ * and waits for nothing on the device.
  */
 #ifndef MHC_CKPT_H_
 #define MHC_CKPT_H_

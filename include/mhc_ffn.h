@@ -27,9 +27,9 @@
  *
  * Sizes: D and F multiples of 8 in [8, 2^20], 0 <= T <= 2^24.  Every tensor is
  * contiguous device memory owned by the caller, 16-byte aligned (scales: no
- * alignment), outputs not overlapping inputs.  Calls are asynchronous on
- * `stream` (a cudaStream_t, NULL = legacy default).  Status codes are those of
- * mhc_pre.h.
+ * alignment); outputs and workspace overlap neither inputs nor one another (else
+ * MHC_ERR_PARAM_INVALID).  Calls are asynchronous on `stream` (a cudaStream_t,
+ * NULL = legacy default).  Status codes are those of mhc_pre.h.
  */
 #ifndef MHC_FFN_H_
 #define MHC_FFN_H_

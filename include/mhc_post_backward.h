@@ -29,7 +29,7 @@ extern "C" {
 #endif
 
 /* Device pointers to contiguous tensors owned by the caller; outputs must not
- * overlap the inputs or one another. */
+ * overlap the inputs or one another (else MHC_ERR_PARAM_INVALID). */
 typedef struct {
   int64_t T;                 /* tokens; 0 => MHC_OK, nothing launched        */
   int64_t n;                 /* streams, 1..8                                */

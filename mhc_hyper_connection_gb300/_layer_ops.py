@@ -7,6 +7,8 @@ short as a launch or two, so the checks are one comparison each and torch's
 current stream is read as a raw handle.  Contiguous CUDA tensors on the current
 device only.
 
+Outputs given to a call must overlap neither its inputs nor one another (MhcError).
+
 A call runs on `stream` (torch's current one if None).  If that is another
 stream, it waits for the current one only where the call allocates something;
 what the inputs still wait for is the caller's to order.

@@ -298,7 +298,9 @@ cudaError_t launch_post_ckpt(int64_t T, int64_t D, const void* x, const void* re
   return cudaGetLastError();
 }
 
-mhc_status_t check_matrix(int64_t rows, int64_t D, int32_t dtype, const void* x, const void* codes, const void* scales) {
+// pack: x is read and codes and scales are written, else the reverse.
+mhc_status_t check_matrix(int64_t rows, int64_t D, int32_t dtype, const void* x, const void* codes, const void* scales,
+                          bool pack) {
   if (dtype != MHC_DTYPE_BF16 && dtype != MHC_DTYPE_FP16)
     return fail(MHC_ERR_PARAM_INVALID, "dtype must be MHC_DTYPE_BF16 or MHC_DTYPE_FP16 (got %d)", (int)dtype);
   if (D < 8 || D > (int64_t(1) << 20) || (D % 8) != 0)
@@ -309,7 +311,9 @@ mhc_status_t check_matrix(int64_t rows, int64_t D, int32_t dtype, const void* x,
   if (!x || !codes || !scales) return fail(MHC_ERR_NULLPTR, "x, codes and scales are required");
   if (!aligned(x, 16)) return fail(MHC_ERR_PARAM_INVALID, "x must be 16-byte aligned");
   if (!aligned(codes, 8)) return fail(MHC_ERR_PARAM_INVALID, "codes must be 8-byte aligned");
-  return MHC_OK;
+  const size_t values = (size_t)rows * D, blocks = (size_t)rows * ((D + kCkptBlock - 1) / kCkptBlock);
+  const Span c = {"codes", codes, values}, s = {"scales", scales, blocks}, v = {"x", x, 2 * values};
+  return pack ? check_apart({c, s}, {v}) : check_apart({v}, {c, s});
 }
 
 }  // namespace
@@ -322,7 +326,7 @@ extern "C" {
 mhc_status_t mhc_ckpt8_pack_run(int64_t rows, int64_t D, int32_t dtype, const void* x, void* codes, void* scales,
                                 void* stream) {
   clear_error();
-  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales);
+  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales, true);
   if (st != MHC_OK || rows == 0) return st;
   const int nblk = (int)((D + kCkptBlock - 1) / kCkptBlock);
   const long long total = rows * nblk;
@@ -343,7 +347,7 @@ mhc_status_t mhc_ckpt8_pack_run(int64_t rows, int64_t D, int32_t dtype, const vo
 mhc_status_t mhc_ckpt8_restore_run(int64_t rows, int64_t D, int32_t dtype, const void* codes, const void* scales,
                                    void* x, void* stream) {
   clear_error();
-  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales);
+  const mhc_status_t st = check_matrix(rows, D, dtype, x, codes, scales, false);
   if (st != MHC_OK || rows == 0) return st;
   const int nblk = (int)((D + kCkptBlock - 1) / kCkptBlock), vrow = (int)(D / 8);
   const long long vecs = rows * vrow;
@@ -375,6 +379,13 @@ mhc_status_t mhc_post_ckpt_run(int64_t T, int64_t n, int64_t D, const void* x, c
     return fail(MHC_ERR_PARAM_INVALID, "x, residual and out must be 16-byte aligned");
   if (!aligned(codes, 8)) return fail(MHC_ERR_PARAM_INVALID, "codes must be 8-byte aligned");
   if (!aligned(post, 4) || !aligned(comb, 4)) return fail(MHC_ERR_PARAM_INVALID, "post and comb must be 4-byte aligned");
+  const size_t xb = (size_t)T * D * 2, pb = (size_t)T * n * 4, values = (size_t)T * n * D;
+  const mhc_status_t st =
+      check_apart({{"out", out, 2 * values},
+                   {"codes", codes, values},
+                   {"scales", scales, (size_t)T * n * ((D + kCkptBlock - 1) / kCkptBlock)}},
+                  {{"x", x, xb}, {"residual", residual, 2 * values}, {"post", post, pb}, {"comb", comb, pb * n}});
+  if (st != MHC_OK) return st;
   using Fn = cudaError_t (*)(int64_t, int64_t, const void*, const void*, const float*, const float*, void*, void*,
                              void*, cudaStream_t);
   static const Fn table[8] = {launch_post_ckpt<1>, launch_post_ckpt<2>, launch_post_ckpt<3>, launch_post_ckpt<4>,

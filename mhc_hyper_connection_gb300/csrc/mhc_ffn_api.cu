@@ -2,6 +2,7 @@
 // layout, tensor maps and the launches' shapes.
 #include "mhc_ffn.cuh"
 #include "mhc_host.cuh"
+#include "../../include/mhc_ckpt.h"
 #include "../../include/mhc_ffn.h"
 
 using namespace mhc;
@@ -218,6 +219,14 @@ mhc_status_t mhc_ffn_run(const mhc_ffn_args* a, void* stream) {
   const FwdLayout l = fwd_layout(T, D, F);
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
+  const size_t xb = (size_t)T * D * 2, wb = (size_t)F * D * 2, kb = (size_t)T * F * 2, blocks = div_up(F, MHC_CKPT_BLOCK);
+  if ((st = check_apart({{"y", a->y, xb},
+                         {"gate_up", a->gate_up, 2 * kb},
+                         {"codes", a->codes, kb},
+                         {"scales", a->scales, (size_t)T * 2 * blocks},
+                         {"workspace", a->workspace, l.total}},
+                        {{"x", a->x, xb}, {"w_gate_up", a->w_gate_up, 2 * wb}, {"w_down", a->w_down, wb}})) != MHC_OK)
+    return st;
   FfnFwdLaunch L;
   int sms = 0;
   if ((st = device(&sms)) != MHC_OK) return st;
@@ -277,6 +286,19 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
   const BwdLayout l = bwd_layout(T, D, F);
   if (a->workspace_bytes < l.total)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, l.total);
+  const size_t xb = (size_t)T * D * 2, wb = (size_t)F * D * 2, kb = (size_t)T * F * 2, blocks = div_up(F, MHC_CKPT_BLOCK);
+  if ((st = check_apart({{"grad_x", a->grad_x, xb},
+                         {"grad_w_gate_up", a->grad_w_gate_up, 2 * wb},
+                         {"grad_w_down", a->grad_w_down, wb},
+                         {"workspace", a->workspace, l.total}},
+                        {{"grad_y", a->grad_y, xb},
+                         {"x", a->x, xb},
+                         {"w_gate_up", a->w_gate_up, 2 * wb},
+                         {"w_down", a->w_down, wb},
+                         {"gate_up", a->gate_up, 2 * kb},
+                         {"codes", a->codes, kb},
+                         {"scales", a->scales, (size_t)T * 2 * blocks}})) != MHC_OK)
+    return st;
   FfnBwdLaunch L;
   int sms = 0;
   if ((st = device(&sms)) != MHC_OK) return st;

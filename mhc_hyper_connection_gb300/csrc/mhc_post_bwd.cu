@@ -334,6 +334,19 @@ extern "C" mhc_status_t mhc_post_backward_run(const mhc_post_bwd_args* a, void* 
   const void* v4[] = {a->post, a->comb, a->grad_post, a->grad_comb};
   for (const void* q : v4)
     if (!aligned(q, 4)) return fail(MHC_ERR_PARAM_INVALID, "fp32 tensors must be 4-byte aligned");
+  const size_t xb = (size_t)T * D * 2, pb = (size_t)T * n * 4, values = (size_t)T * n * D;
+  const mhc_status_t st = check_apart({{"grad_x", a->grad_x, xb},
+                                       {"grad_residual", a->grad_residual, 2 * values},
+                                       {"grad_post", a->grad_post, pb},
+                                       {"grad_comb", a->grad_comb, pb * n}},
+                                      {{"grad_out", a->grad_out, 2 * values},
+                                       {"x", a->x, xb},
+                                       {"residual", a->residual, 2 * values},
+                                       {"codes", a->codes, values},
+                                       {"scales", a->scales, (size_t)T * n * ((D + kCkptBlock - 1) / kCkptBlock)},
+                                       {"post", a->post, pb},
+                                       {"comb", a->comb, pb * n}});
+  if (st != MHC_OK) return st;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(MHC_ERR_RUNTIME, "no CUDA device");
   const DeviceInfo di = device_info(dev);
