@@ -57,7 +57,12 @@ typedef struct {
                                 most one of gate_up and codes is given        */
   void *workspace;           /* device scratch, 256-byte aligned              */
   size_t workspace_bytes;
-  uint32_t wait_limit_us;    /* device wait limit; 0: the default, 2 s; at most 10 s */
+  uint32_t wait_limit_us;    /* device wait limit; 0: the default, 2 s; at most 10 s.
+                                A bound on hangs: it has to exceed the time that
+                                one block takes for its share of one product
+                                (hundreds of microseconds for weights of several
+                                GB); the time of an earlier product of the call
+                                does not count                                */
   int32_t withhold_copy;     /* 1: leave out one operand copy, so that the waits
                                 on it give up (test of that path; outputs are
                                 then incomplete); 0 otherwise                 */

@@ -235,6 +235,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   pdl_trigger();
   if (g.split > 1) cluster_arrive();             // waited for before the first remote store
 
+  // The timed waits of these warps begin when the product before is complete: a
+  // limit then bounds this product's own waits.
+  if (warp != 0) pdl_wait();
+
   if (warp == 0) {
     // ===================================================== TMA producer
     if (lane == 0) {
