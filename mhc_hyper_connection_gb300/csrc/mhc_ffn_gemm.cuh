@@ -45,6 +45,7 @@ struct GemmTail {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t sched_full[kSchedSlots], sched_empty[kSchedSlots];
   uint64_t mma_done;
+  uint64_t sent[2];                        // of each CTA of the pair: 2 x stages issued, + 1 if a wait gave up
   uint32_t tmem_base;
   uint32_t abort;
   int sched[kSchedSlots];                  // tile numbers, -1: no more
@@ -144,6 +145,32 @@ __device__ __forceinline__ void acc_ld16x2(uint32_t ta, uint32_t tb, float (&a)[
         "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
       : "r"(ta), "r"(tb)
       : "memory");
+}
+
+// Bytes of a stage that one CTA of the pair copies; an MN-major B comes in blocks
+// of 64 rows.
+__device__ __forceinline__ uint32_t stage_bytes_of(const GemmShape& g) {
+  const int half_n = g.tile_n / 2;
+  return (uint32_t)(kGemmOpBytes + (g.b_mn ? (half_n + 63) & ~63 : half_n) * kFfnTileK * 2);
+}
+
+// Completes `bytes` of a barrier's phase without a copy.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// After a wait gave up: every copy that the pair issued lands before it leaves.
+// Both CTAs' copies count on the even CTA's barriers, which expect both halves of
+// a stage; where only one CTA issued its half, the barrier is made to count that
+// half alone.  The ring bounds the difference at its stages.
+static __device__ __noinline__ void settle_copies(GemmTail* tail, long long mine, long long theirs, uint32_t bytes) {
+  const long long both = mine < theirs ? mine : theirs, most = mine < theirs ? theirs : mine;
+  for (long long k = both; k < most; ++k) {
+    if (mine < theirs) mbar_expect_tx(&tail->full[k % kGemmStages], bytes);
+    else mbar_complete_tx(&tail->full[k % kGemmStages], bytes);
+  }
+  for (long long k = most > kGemmStages ? most - kGemmStages : 0; k < most; ++k)
+    mbar_drain(&tail->full[k % kGemmStages], (uint32_t)(k / kGemmStages) & 1u);
 }
 
 // Bounded wait of the product loops.  The clock is read only after a few
@@ -636,16 +663,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int half_n = g.tile_n / 2;
         const int n0 = kPair ? tn * kGemmHalf : tn * g.tile_n + (int)rank * half_n;
         const int plane = kPair ? (int)rank : 0, a_mn = g.a_mn, b_mn = g.b_mn;
-        // of both CTAs; an MN-major B comes in blocks of 64 rows
-        const uint32_t bytes = 2u * (uint32_t)(kGemmOpBytes + (b_mn ? (half_n + 63) & ~63 : half_n) * kFfnTileK * 2);
+        const uint32_t bytes = 2u * stage_bytes_of(g);
         const int kbeg = slice * g.kslice, kiters = min(g.kslice, g.kiters - kbeg);
         int after = -1;                          // tile n + 2, drawn under this tile's copies
         if (kDraw && rank == 0 && next >= 0) after = draw();
         for (int k = 0; k < kiters; ++k) {
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-          // test hook: the first pair leaves out the last chunk of its first
-          // tile, so the waits on it give up (no copy is left in flight)
-          if (withhold && pair == 0 && n == 0 && k == kiters - 1) { ok = false; break; }
+          // test hook: the first two pairs leave out the last chunk of their
+          // first tile, so the waits on it give up; the first pair's odd CTA
+          // and the second pair's even one also leave out the one before it
+          if (withhold && pair < 2 && n == 0 && k == max(kiters - 1 - (int)(rank ^ (uint32_t)pair), 0)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
           const uint32_t bar = map_cluster(&tail->full[s], 0);
           const int k0 = (kbeg + k) * kFfnTileK;
@@ -671,18 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           next = after;
         }
       }
-      if (rank == 0) {
-        for (long long q = 0; q < (iss < kGemmStages ? iss : kGemmStages); ++q) {   // let issued copies land
-          if (--s < 0) { s = kGemmStages - 1; ph ^= 1u; }
-          mbar_drain(&tail->full[s], ph);
-        }
-      }
-      if (!ok || *ctl.abort) {
-        // A wait gave up: copies of this CTA that the even CTA no longer
-        // counts get a millisecond to land before the pair leaves together.
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000ull) __nanosleep(1000);
-      }
+      tail->sent[rank] = (uint64_t)iss << 1;
     }
   } else if (warp == 1) {
     // ===================================================== MMA issuer
@@ -743,11 +759,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   }
 
-  // ---- teardown: the pair leaves together
+  // ---- teardown: the pair leaves together.  Without a give-up both CTAs issued
+  // the same stages and the products have consumed them all.
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint64_t mine = tail->sent[rank] | (*ctl.abort ? 1u : 0u);
+    tail->sent[rank] = mine;
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(map_cluster(&tail->sent[rank], rank ^ 1u)), "l"(mine) : "memory");
+  }
+  __syncwarp();
   cluster_sync_all();
+  const uint64_t s0 = tail->sent[0], s1 = tail->sent[1];
+  if (((s0 | s1) & 1u) || s0 != s1) {            // the same in both CTAs
+    // the products of a launch have tiles of one width and one layout of B
+    if (threadIdx.x == 0 && rank == 0)
+      settle_copies(tail, (long long)(s0 >> 1), (long long)(s1 >> 1), stage_bytes_of(set.op[0].g));
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
