@@ -70,7 +70,7 @@ struct FfnBwdLaunch {
   int T, D, F, act, kept;
   const void *gate_up, *codes, *scales;
   void *gg_buf, *a_buf, *grad_x, *grad_w_gate_up, *grad_w_down;
-  float* part;                     // of gx
+  float *part, *part_gu, *part_down;   // of gx, gwgu and gwd, where they have more than one slice
 };
 cudaError_t launch_ffn_backward(const FfnBwdLaunch& L, bool f16, cudaStream_t s);
 

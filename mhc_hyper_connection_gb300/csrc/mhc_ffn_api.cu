@@ -53,6 +53,13 @@ struct Cut {
 };
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Chunks of the depth (of 64) that one tile sums at most, where its product can be
+// cut.  The tensor core truncates as it adds to its fp32 accumulators: 1e-7 of the
+// running sum per sixteen products, all one way.  Terms of one sign measured 4.2e-4
+// low at a depth of 65536 and 6.7e-3 at a million (weight gradients; fp16 rounds by
+// 4.9e-4 at most); cut at 32768 and joined in fp32 they stay within 2.2e-4.
+constexpr int64_t kDeepest = 512;
+
 // Time of joining `slices` sums of M x N, in stages of a wide tile (0.28 us): a
 // launch, and each sum written and read once.
 double join_cost(int64_t M, int64_t N, int64_t slices) { return slices > 1 ? 10.0 + 8.0 * M * N * slices / 1.9e6 : 0.0; }
@@ -75,7 +82,8 @@ Cut cut_alone(int64_t M, int64_t N, int64_t K, bool b_mn, int most) {
   for (int w = 256; w >= 128; w -= 64) {
     const double stage = w == 256 ? 1.0 : w == 192 ? (b_mn ? 1.02 : 0.8) : b_mn ? 0.7 : 0.6;
     const double ends = w == 192 && b_mn ? 3.0 : 4.0 * stage;
-    for (int64_t s = 1; s <= most && (s == 1 || kiters >= 8 * s); ++s) {
+    const int64_t fewest = most > 1 ? div_up(kiters, kDeepest) : 1;
+    for (int64_t s = fewest; s == fewest || (s <= most && kiters >= 8 * s); ++s) {
       const int64_t per = div_up(kiters, s), slices = div_up(kiters, per);
       const double rounds = (double)div_up(rows * div_up(N, w) * slices, kPairs);
       const double cost = rounds * (per * stage + ends) + join_cost(M, N, slices);
@@ -96,13 +104,20 @@ Cut cut_grad_x(int64_t T, int64_t D, int64_t F) {
   const int64_t kx = div_up(2 * F, kFfnTileK), kw = div_up(T, kFfnTileK);
   const int64_t total = div_up(T, 256) * div_up(D, 256) * kx + (div_up(2 * F, 256) * div_up(D, 256) + div_up(D, 256) * div_up(F, 256)) * kw;
   const int64_t share = div_up(total, kPairs);
+  const int64_t fewest = div_up(kx, kDeepest);
   int64_t s = div_up(kx, share);
   if (s > 16) s = 16;
   while (s > 1 && kx < 8 * s) --s;
+  if (s < fewest) s = fewest;
   const int64_t per = div_up(kx, s), slices = div_up(kx, per);
   const int64_t then = per > share ? per : share;
-  if (slices == 1 || kx - then < join_cost(T, D, slices)) return {256, 1, (int)kx};
+  if (fewest == 1 && (slices == 1 || kx - then < join_cost(T, D, slices))) return {256, 1, (int)kx};
   return {256, (int)slices, (int)per};
+}
+// The weight gradients: sums over the tokens.
+Cut cut_tokens(int64_t T) {
+  const int64_t kiters = div_up(T, kFfnTileK), per = div_up(kiters, div_up(kiters, kDeepest));
+  return {256, (int)div_up(kiters, per), (int)per};
 }
 Cut whole(int64_t K) { return {256, 1, (int)div_up(K, kFfnTileK)}; }
 constexpr int kMostSlices = 16;
@@ -123,14 +138,16 @@ FwdLayout fwd_layout(int64_t T, int64_t D, int64_t F) {
   return l;
 }
 struct BwdLayout {
-  size_t gg, a, part, total;
+  size_t gg, a, part, part_gu, part_down, total;
 };
 BwdLayout bwd_layout(int64_t T, int64_t D, int64_t F) {
   BwdLayout l;
   l.gg = 256;
   l.a = l.gg + up256((size_t)T * F * 4);
   l.part = l.a + up256((size_t)T * F * 2);
-  l.total = l.part + part_bytes(cut_gx(T, D, F), T, D);
+  l.part_gu = l.part + part_bytes(cut_gx(T, D, F), T, D);
+  l.part_down = l.part_gu + part_bytes(cut_tokens(T), 2 * F, D);
+  l.total = l.part_down + part_bytes(cut_tokens(T), D, F);
   return l;
 }
 
@@ -326,9 +343,11 @@ mhc_status_t mhc_ffn_backward_run(const mhc_ffn_bwd_args* a, void* stream) {
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
   L.ga = shape(T, F, D, cut_alone(T, F, D, true, 1), false, f16, false, true);
   L.gx = shape(T, D, 2 * F, cut_gx(T, D, F), false, f16, false, true);
-  L.gwgu = shape(2 * F, D, T, whole(T), false, f16, true, true);
-  L.gwd = shape(D, F, T, whole(T), false, f16, true, true);
+  L.gwgu = shape(2 * F, D, T, cut_tokens(T), false, f16, true, true);
+  L.gwd = shape(D, F, T, cut_tokens(T), false, f16, true, true);
   L.part = L.gx.slices > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+  L.part_gu = L.gwgu.slices > 1 ? reinterpret_cast<float*>(ws + l.part_gu) : nullptr;
+  L.part_down = L.gwd.slices > 1 ? reinterpret_cast<float*>(ws + l.part_down) : nullptr;
   const cudaError_t e = launch_ffn_backward(L, f16, s);
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "feed-forward backward launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;

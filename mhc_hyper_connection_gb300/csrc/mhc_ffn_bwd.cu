@@ -39,8 +39,8 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const GemmOperands gx = {L.gg_k, L.wgu_mn, L.gx}, gwgu = {L.gg_mn, L.x_mn, L.gwgu}, gwd = {L.gy_mn, L.a_mn, L.gwd};
   const StoreTo to_x = {static_cast<uint16_t*>(L.grad_x), L.T, L.D, L.part};
-  const StoreTo to_wgu = {static_cast<uint16_t*>(L.grad_w_gate_up), 2 * L.F, L.D, nullptr};
-  const StoreTo to_wd = {static_cast<uint16_t*>(L.grad_w_down), L.D, L.F, nullptr};
+  const StoreTo to_wgu = {static_cast<uint16_t*>(L.grad_w_gate_up), 2 * L.F, L.D, L.part_gu};
+  const StoreTo to_wd = {static_cast<uint16_t*>(L.grad_w_down), L.D, L.F, L.part_down};
   if (few) {
     FewStore<F16> f;
     f.out = to_x.out;
@@ -66,7 +66,10 @@ cudaError_t backward(const FfnBwdLaunch& L, cudaStream_t s) {
     o.to[2] = to_x;
     e = launch_gemm<false, true, 3>({{gwgu, gwd, gx}}, L.call, o, false, true, s);
   }
-  return e != cudaSuccess || !L.part ? e : launch_sum<F16>(to_x, L.gx.slices, L.call.sms, s);
+  if (e == cudaSuccess && L.part) e = launch_sum<F16>(to_x, L.gx.slices, L.call.sms, s);
+  if (e == cudaSuccess && L.part_gu) e = launch_sum<F16>(to_wgu, L.gwgu.slices, L.call.sms, s);
+  if (e == cudaSuccess && L.part_down) e = launch_sum<F16>(to_wd, L.gwd.slices, L.call.sms, s);
+  return e;
 }
 
 }  // namespace
