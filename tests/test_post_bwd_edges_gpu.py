@@ -1,0 +1,146 @@
+"""Backward of the post-mapping where it can go wrong: values that are not
+finite, in every stream count and from checkpoints, and long dot products.
+
+grad_post and grad_comb: a tensor-core sum takes 64 columns, at most 2^-22 of
+the sum of the magnitudes off per sixteen of them (it truncates); those sums are
+added in fp32 registers, half a unit of the last place each, at most D / 64 of
+them and eight warps: (D / 64 + 24) 2^-24 times the sum of the magnitudes, and
+2^-24 for the last rounding.  (D / 64 + 32) 2^-24 allowed.  grad_x and
+grad_residual: as in the operator's other tests."""
+import numpy as np
+import pytest
+import torch
+
+import layer_refs as ref
+import test_post_bwd_gpu as tp
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+KEYS = ("grad_x", "grad_residual", "grad_post", "grad_comb")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from mhc_hyper_connection_gb300 import build
+    build.build()
+
+
+def _near(case, g, got, residual, what):
+    """Every output against the formula in 64 bits: NaN where that is NaN, the
+    same infinities, and finite values within their bounds."""
+    with np.errstate(all="ignore"):
+        want, mag = ref.post_backward(tp._f64(g), tp._f64(case.x), residual, tp._f64(case.post), tp._f64(case.comb))
+    n, D = case.n, case.D
+    for k in KEYS:
+        v, w, m = tp._f64(got[k]), want[k], mag[k]
+        assert np.array_equal(np.isnan(v), np.isnan(w)), (what, k)
+        inf = np.isinf(w)
+        assert np.array_equal(v[inf], w[inf]) and np.array_equal(np.isinf(v), inf), (what, k)
+        fine = np.isfinite(w)
+        off = np.abs(v[fine] - w[fine])
+        if k in ("grad_x", "grad_residual"):
+            tol = 2.0 ** -8 * np.abs(w[fine]) + n * 2.0 ** -23 * m[fine]
+        else:
+            tol = (D / 64 + 32) * 2.0 ** -24 * m[fine]
+        assert (off <= tol + 1e-38).all(), (what, k, off.max())
+
+
+def _residual(case, ck):
+    if ck is None:
+        return tp._f64(case.residual)
+    return ref.restore(ck.codes.cpu().numpy(), ck.scales.cpu().numpy())
+
+
+@pytest.mark.parametrize("kept", ["bf16", "codes"])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_values_that_are_not_finite(cuda_device, n, kept):
+    """An infinity or a NaN in each input, in one of the tokens that share a
+    warp: that token has what the formulas give, the others what they had."""
+    from mhc_hyper_connection_gb300 import Ckpt8, ckpt8_pack, hc_post_backward
+    T, D, t, j = 19, 264, 10, n - 1
+    case, g = tp._case(cuda_device, T, n, D, n)
+    ck = ckpt8_pack(case.residual) if kept == "codes" else None
+    clean = hc_post_backward(g, case.x, ck or case.residual, case.post, case.comb)
+    others = [i for i in range(T) if i != t]
+    places = [("g", (t, j, 5)), ("g", (t, 0, D - 1)), ("x", (t, 130)), ("post", (t, j)), ("comb", (t, 0, j)), ("comb", (t, j, 0))]
+    places += [("residual", (t, j, 7))] if ck is None else [("codes", (t, j, 7))]
+    for name, at in places:
+        for value in (INF, -INF, NAN) if name != "codes" else (0x7F, 0xFF):
+            c, g2, ck2 = type(case)(**vars(case)), g.clone(), ck
+            if name == "g":
+                g2[at] = value
+            elif name == "codes":
+                ck2 = Ckpt8(ck.codes.clone(), ck.scales)
+                ck2.codes[at] = value
+            else:
+                setattr(c, name, getattr(case, name).clone())
+                getattr(c, name)[at] = value
+            got = hc_post_backward(g2, c.x, ck2 or c.residual, c.post, c.comb)
+            _near(c, g2, got, _residual(c, ck2), (n, kept, name, at, value))
+            for k in KEYS:
+                assert torch.equal(got[k][others], clean[k][others]), (n, kept, name, at, value, k)
+
+
+def test_infinities_of_both_signs(cuda_device):
+    """Two infinities in one column: a sum of opposite ones is NaN, of equal ones
+    stays infinite, and a weight of zero times one is NaN."""
+    from mhc_hyper_connection_gb300 import hc_post_backward
+    for n in (2, 4, 8):
+        case, g = tp._case(cuda_device, 9, n, 136, n)
+        case.post[:, 1] = case.post[:, 0]
+        g[4, 0, 3], g[4, 1, 3] = INF, INF
+        g[5, 0, 4], g[5, 1, 4] = INF, -INF
+        g[6, 0, 5] = -INF
+        case.comb[6, 1, 0] = 0.0
+        case.post[6, 0] = 0.0
+        got = hc_post_backward(g, case.x, case.residual, case.post, case.comb)
+        _near(case, g, got, tp._f64(case.residual), n)
+
+
+def test_largest_finite_values(cuda_device):
+    """Gradients near the type's end whose results overflow or just do not."""
+    from mhc_hyper_connection_gb300 import hc_post_backward
+    case, g = tp._case(cuda_device, 6, 4, 64, 3)
+    g.zero_()
+    case.x.zero_()
+    case.residual.zero_()
+    g[2, :, 9] = 3.0e38
+    case.post[2] = 0.25
+    case.comb[2] = 0.2
+    case.post[4] = 2.0
+    g[4, 1, 1] = -3.0e38
+    got = hc_post_backward(g, case.x, case.residual, case.post, case.comb)
+    gx, gr = tp._f64(got["grad_x"]), tp._f64(got["grad_residual"])
+    top = float(g[2, 0, 9])
+    assert abs(gx[2, 9] - top) <= 2.0 ** -8 * top and np.isneginf(gx[4, 1])
+    assert np.allclose(gr[2, :, 9], 0.8 * top, rtol=2.0 ** -8)
+    assert not np.isnan(gx).any() and not np.isnan(gr).any()
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("T,D", [(1, 16384), (3, 264), (35, 1096), (700, 72)])
+def test_long_sums_and_checkpoints_in_every_stream_count(cuda_device, n, T, D):
+    from mhc_hyper_connection_gb300 import ckpt8_pack, hc_post_backward
+    case, g = tp._case(cuda_device, T, n, D, n + T)
+    for same_sign in (False, True):
+        if same_sign:
+            g, case.x, case.residual = g.abs(), case.x.abs(), case.residual.abs()
+        for ck in (None, ckpt8_pack(case.residual)):
+            got = hc_post_backward(g, case.x, ck or case.residual, case.post, case.comb)
+            _near(case, g, got, _residual(case, ck), (n, T, D, same_sign, ck is not None))
+
+
+def test_codes_at_every_alignment(cuda_device):
+    """Codes that start at multiples of 8 but not of 16 bytes, and rows whose
+    length is one: the two ways of copying them agree bit for bit."""
+    from mhc_hyper_connection_gb300 import Ckpt8, ckpt8_pack, hc_post_backward
+    for n, D in ((4, 512), (8, 272), (2, 264)):
+        case, g = tp._case(cuda_device, 30, n, D, D)
+        ck = ckpt8_pack(case.residual)
+        want = hc_post_backward(g, case.x, ck, case.post, case.comb)
+        room = torch.zeros(ck.codes.numel() + 8, dtype=torch.uint8, device=cuda_device)
+        odd = room[8:].view(ck.codes.shape)
+        odd.copy_(ck.codes)
+        assert odd.data_ptr() % 16 == 8
+        got = hc_post_backward(g, case.x, Ckpt8(odd, ck.scales), case.post, case.comb)
+        assert all(torch.equal(got[k], want[k]) for k in KEYS)
