@@ -144,3 +144,21 @@ def test_codes_at_every_alignment(cuda_device):
         assert odd.data_ptr() % 16 == 8
         got = hc_post_backward(g, case.x, Ckpt8(odd, ck.scales), case.post, case.comb)
         assert all(torch.equal(got[k], want[k]) for k in KEYS)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 5, 8])
+def test_checkpoint_is_the_tensor_it_stands_for(cuda_device, n):
+    """The gradients from a checkpoint are, bit for bit, those from the tensor
+    that it stands for, up to the largest gradients: a product with a code (up
+    to 448) has to carry its block's scale before it is summed."""
+    from mhc_hyper_connection_gb300 import ckpt8_pack, ckpt8_restore, hc_post_backward
+    for T, D, size in ((40, 392, 1.0), (700, 1024, 2.0 ** 60), (6, 264, 2.0 ** 121), (6, 264, 2.0 ** -100)):
+        case, g = tp._case(cuda_device, T, n, D, n + D)
+        g = (g.float() * size).bfloat16()
+        case.x.zero_()                               # grad_post would overflow in truth
+        res = (case.residual.float() * (2.0 ** -8 if size > 1 else 1.0)).bfloat16()
+        ck = ckpt8_pack(res)
+        a = hc_post_backward(g, case.x, ck, case.post, case.comb)
+        b = hc_post_backward(g, case.x, ckpt8_restore(ck), case.post, case.comb)
+        assert torch.isfinite(b["grad_comb"]).all()
+        assert all(torch.equal(a[k], b[k]) for k in KEYS), (T, D, size)
