@@ -45,7 +45,7 @@ struct GemmTail {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t sched_full[kSchedSlots], sched_empty[kSchedSlots];
   uint64_t mma_done;
-  uint64_t sent[2];                        // of each CTA of the pair: 2 x stages issued, + 1 if a wait gave up
+  uint64_t sent[2];                        // even CTA: 1 + the stages that each CTA of the pair issued, once it issues no more
   uint32_t tmem_base;
   uint32_t abort;
   int sched[kSchedSlots];                  // tile numbers, -1: no more
@@ -159,11 +159,21 @@ __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) 
   asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// After a wait gave up: every copy that the pair issued lands before it leaves.
-// Both CTAs' copies count on the even CTA's barriers, which expect both halves of
-// a stage; where only one CTA issued its half, the barrier is made to count that
-// half alone.  The ring bounds the difference at its stages.
-static __device__ __noinline__ void settle_copies(GemmTail* tail, long long mine, long long theirs, uint32_t bytes) {
+// After a wait gave up, in the even CTA: every copy that the pair issued lands
+// before it leaves.  Once neither CTA issues any more (each of their waits is
+// bounded too), both CTAs' copies are counted on the even CTA's barriers.  These
+// expect both halves of a stage; where only one CTA issued its half, the barrier
+// is made to count that half alone.  The ring bounds the difference at its stages.
+static __device__ __noinline__ void settle_copies(GemmTail* tail, uint64_t wait_ns, uint32_t bytes) {
+  uint64_t sent[2];
+  const uint64_t t0 = now_ns();
+  do {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      asm volatile("ld.acquire.cluster.shared::cta.b64 %0, [%1];" : "=l"(sent[r]) : "r"(smem_u32(&tail->sent[r])) : "memory");
+    if (now_ns() - t0 > 2 * wait_ns + 100000000ull) return;
+  } while (!sent[0] || !sent[1]);
+  const long long mine = (long long)sent[0] - 1, theirs = (long long)sent[1] - 1;
   const long long both = mine < theirs ? mine : theirs, most = mine < theirs ? theirs : mine;
   for (long long k = both; k < most; ++k) {
     if (mine < theirs) mbar_expect_tx(&tail->full[k % kGemmStages], bytes);
@@ -569,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     mbar_init(&tail->mma_done, 1);
     tail->abort = 0u;
+    tail->sent[0] = tail->sent[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -665,14 +676,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int plane = kPair ? (int)rank : 0, a_mn = g.a_mn, b_mn = g.b_mn;
         const uint32_t bytes = 2u * stage_bytes_of(g);
         const int kbeg = slice * g.kslice, kiters = min(g.kslice, g.kiters - kbeg);
+        // test hook: the first two pairs leave out the last chunk of their first
+        // tile, so the waits on it give up; the first pair's odd CTA and the
+        // second pair's even one also leave out the one before it
+        const int kend = withhold && pair < 2 && n == 0 ? max(kiters - 1 - (int)(rank ^ (uint32_t)pair), 0) : kiters;
         int after = -1;                          // tile n + 2, drawn under this tile's copies
         if (kDraw && rank == 0 && next >= 0) after = draw();
-        for (int k = 0; k < kiters; ++k) {
+        for (int k = 0; k < kend; ++k) {
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-          // test hook: the first two pairs leave out the last chunk of their
-          // first tile, so the waits on it give up; the first pair's odd CTA
-          // and the second pair's even one also leave out the one before it
-          if (withhold && pair < 2 && n == 0 && k == max(kiters - 1 - (int)(rank ^ (uint32_t)pair), 0)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + s * kGemmStageBytes), sb = sa + kGemmOpBytes;
           const uint32_t bar = map_cluster(&tail->full[s], 0);
           const int k0 = (kbeg + k) * kFfnTileK;
@@ -692,13 +703,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           ++iss;
           if (++s == kGemmStages) { s = 0; ph ^= 1u; }
         }
+        ok = ok && kend == kiters;
         if (kDraw && rank == 0) {                // after the last tile: -1
           ok = ok && publish(n + 2, after);
           cur = next;
           next = after;
         }
       }
-      tail->sent[rank] = (uint64_t)iss << 1;
+      asm volatile("st.release.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cluster(&tail->sent[rank], 0)), "l"(iss + 1)
+                   : "memory");
     }
   } else if (warp == 1) {
     // ===================================================== MMA issuer
@@ -739,6 +752,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                    : "memory");
       __syncwarp();
       mbar_drain(&tail->mma_done, 0);
+      // Products that were all formed have consumed all copies.  The products of
+      // a launch have tiles of one width and one layout of B.
+      if ((!ok || *ctl.abort) && lane == 0) settle_copies(tail, ctl.wait_ns, stage_bytes_of(set.op[0].g));
+      __syncwarp();
     }
   } else {
     // ===================================================== epilogue
@@ -759,26 +776,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   }
 
-  // ---- teardown: the pair leaves together.  Without a give-up both CTAs issued
-  // the same stages and the products have consumed them all.
+  // ---- teardown: the pair leaves together
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint64_t mine = tail->sent[rank] | (*ctl.abort ? 1u : 0u);
-    tail->sent[rank] = mine;
-    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(map_cluster(&tail->sent[rank], rank ^ 1u)), "l"(mine) : "memory");
-  }
-  __syncwarp();
   cluster_sync_all();
-  const uint64_t s0 = tail->sent[0], s1 = tail->sent[1];
-  if (((s0 | s1) & 1u) || s0 != s1) {            // the same in both CTAs
-    // the products of a launch have tiles of one width and one layout of B
-    if (threadIdx.x == 0 && rank == 0)
-      settle_copies(tail, (long long)(s0 >> 1), (long long)(s1 >> 1), stage_bytes_of(set.op[0].g));
-    __syncwarp();
-    cluster_sync_all();
-  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
