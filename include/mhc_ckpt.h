@@ -16,8 +16,9 @@
  *
  * Inside these ranges every value is exact in the element type, so reading
  * a checkpoint back rounds nothing: the backward pass sees exactly what the
- * 8 bits stand for.  A value off by at most half a step has a relative error
- * of at most 2^-4 (2^-10 448 2^e absolute below amax 2^-15).
+ * 8 bits stand for.  A value is off by at most half a step: 2^-4 of itself, or,
+ * where |x| < 2^-6 2^e, 2^-10 2^e.  Magnitudes above 448 times the range's last
+ * power (bf16 448 2^119, fp16 57344) become that product: up to an eighth less.
  *
  * codes: uint8 [rows, D].  scales: uint8 [rows, ceil(D / 128)], e + 127.
  *
@@ -46,7 +47,9 @@ MHC_API mhc_status_t mhc_ckpt8_pack_run(int64_t rows, int64_t D, int32_t dtype, 
                                         void *scales, void *stream);
 
 /* The reverse: x [rows, D] of dtype, written.  A checkpoint is read back in
- * the type it was taken from (another type would round or overflow). */
+ * the type it was taken from.  The codes do not hold that type: a bf16 checkpoint
+ * read as fp16 is rounded like a cast (out of range: infinite); an fp16 one is
+ * exact in bf16 too. */
 MHC_API mhc_status_t mhc_ckpt8_restore_run(int64_t rows, int64_t D, int32_t dtype, const void *codes,
                                            const void *scales, void *x, void *stream);
 

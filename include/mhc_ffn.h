@@ -9,8 +9,11 @@
  * one type, bf16 or fp16.  act is silu, z / (1 + e^-z), or gelu in its tanh
  * form, 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).  Both projections, the
  * activation and the product are one kernel; the products run on the tensor
- * cores with fp32 sums.  a is rounded to the 16-bit type (it is an operand of
- * the second product), y once from its fp32 sum.
+ * cores with fp32 sums; exponential and division are the fast ones, a few 2^-22
+ * of their results off.  a is rounded to the 16-bit type (it is an operand of the
+ * second product), y once from its fp32 sum: y is off by about 1.4 times what one
+ * rounding of exact values would leave.  In fp16, a has fp16's range as well: a
+ * product act(g) u above 65504 is infinite, whatever y would be.
  *
  * For the backward pass the forward can keep g and u, rounded to 16 bits
  * (gate_up [T, 2, F]) or in 8 bits (codes [T, 2, F] and scales
@@ -21,8 +24,9 @@
  *   grad_x = gg Wg + gu Wu                 grad_w_gate_up = [gg^T x, gu^T x]
  *   grad_w_down = grad_y^T a               a = act(g) (.) u, formed again
  *
- * gg, gu and a are rounded to the 16-bit type, the gradients once from their
- * fp32 sums.  Sums run in an order fixed by the sizes and the device: results
+ * gg, gu and a are rounded to the 16-bit type (in fp16 also to its range: above
+ * 65504 infinite, below 6e-8 zero, so small gradients want a scaled loss), the
+ * gradients once from their fp32 sums.  Sums run in an order fixed by the sizes and the device: results
  * are bitwise reproducible.  The tensor cores truncate as they add: sums of terms
  * of one sign measured 1e-7 of the sum too small for every sixteen terms.  Sums over more than 32768 tokens, and sums over F and 2F that are
  * deeper than that, are formed in parts joined in fp32, so that this stays below

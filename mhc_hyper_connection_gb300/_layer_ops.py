@@ -8,6 +8,8 @@ current stream is read as a raw handle.  Contiguous CUDA tensors on the current
 device only.
 
 Outputs given to a call must overlap neither its inputs nor one another (MhcError).
+Nothing is recorded for automatic differentiation: the backward calls are made by
+hand, as examples/train_layer.py does.
 
 A call runs on `stream` (torch's current one if None).  If that is another
 stream, it waits for the current one only where the call allocates something;
@@ -153,7 +155,8 @@ def ckpt8_pack(x, out=None, stream=None) -> Ckpt8:
 
 def ckpt8_restore(ckpt, dtype=None, out=None, stream=None):
     """The 16-bit tensor a checkpoint stands for (exact; dtype: the type it was
-    packed from, default bf16)."""
+    packed from, default bf16).  A Ckpt8 does not hold that type: a bf16
+    checkpoint read as fp16 is rounded as a cast would."""
     codes = ckpt.codes
     shape, dev = codes.shape, codes.device
     cp, sp = _ckpt_at(ckpt, shape, dev)

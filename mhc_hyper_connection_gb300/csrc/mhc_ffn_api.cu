@@ -74,7 +74,7 @@ double join_cost(int64_t M, int64_t N, int64_t slices) { return slices > 1 ? 10.
 // took 75.5; T = 256, D = 4096, F = 8192, down in 2 slices: forward 70 -> 60 us; T =
 // 1500, D = F = 4096, down: two rounds 192 wide where two of 256 took 119 us for the
 // forward, now 104.5; T = 1021, D = 2048, F = 5512, gate gradients: 116 tiles 192
-// wide, backward 135 -> 130.)
+// wide, backward 5 us less.)
 Cut cut_alone(int64_t M, int64_t N, int64_t K, bool b_mn, int most) {
   const int64_t kiters = div_up(K, kFfnTileK), rows = div_up(M, kFfnTileM);
   Cut best = {256, 1, (int)kiters};

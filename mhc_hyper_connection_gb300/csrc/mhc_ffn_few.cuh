@@ -14,10 +14,12 @@
 // dependent launch) and load the weights' first chunks before they wait for the
 // tokens.
 //
-// One token, D = 7168, F = 8192: 64.4 us for 352 MB of weights, 81% of the
+// One token, D = 7168, F = 8192: 66 us a call for 352 MB of weights, 79% of the
 // measured copy rate; the two products' loops stream at 6.9 and 5.3 TB/s, the
 // rest is their starts and joins, about 4 us each.  24 tokens at D = 4096, F =
-// 8192: 43.9 us (68%).  As ordinary tiles of 256 tokens these took 114 and 80.
+// 8192: 45.5 us (66%).  As ordinary tiles of 256 tokens these took 114 and 80.
+// (Calls back to back on changing inputs; where a comment below compares two
+// forms, on the same input the same calls take a microsecond or two less.)
 #pragma once
 
 #include <mutex>

@@ -15,11 +15,12 @@
 // A launch may hold several products (the backward's last).  Where their tiles
 // differ in depth the pairs draw tile numbers from a counter in the workspace: the
 // even CTA's producer draws them ahead and hands them to the other warps of both
-// CTAs through a small ring (T = 1021, D = 2048, F = 5512: backward 132 us, with
-// tiles dealt out in turn 155).  Which pair forms a tile does not change its bits.
+// CTAs through a small ring (T = 1021, D = 2048, F = 5512: backward 134 us, with
+// tiles dealt out in turn 23 more).  Which pair forms a tile does not change its bits.
 //
-// T = 4096, D = 4096, F = 8192, bf16: forward 456 us (1.81 PFLOP/s; 505 with gate
-// and up kept), backward 1085 us (1.52 PFLOP/s), at the card's power limit.  Bound
+// T = 4096, D = 4096, F = 8192, bf16: forward 455 to 495 us (1.81 to 1.67 PFLOP/s;
+// 508 to 520 with gate and up kept), backward 1085 to 1105 us (1.5 PFLOP/s), at the
+// card's power limit, which differs from one to the next.  Bound
 // by the tensor cores: four products of a stage execute in 512 clocks and take 535
 // with K-major operands, 650 to 710 with MN-major ones, whose reads leave the
 // shared memory less room (with the products of a stage issued twice they take

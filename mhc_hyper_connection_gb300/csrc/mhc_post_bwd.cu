@@ -8,7 +8,7 @@
 // column, against 2 (n + n^2) products.  Those run on the tensor cores: on the
 // CUDA cores they took longer than the memory (n = 8, T = 16384, D = 2048 from a
 // checkpoint: 430 us, 51% of measured HBM; now 240 us, 91%; n = 4, T = 32768, D =
-// 7168: 1092 us, now 1000, 97%).
+// 7168: 1092 us, now 1040, 93%).
 #include <atomic>
 
 #include "mhc_ckpt.cuh"
@@ -64,8 +64,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // tokens of a warp share the product over rows, so a piece with a result that
 // is not finite is formed again in plain fp32 (direct_piece).
 //
-// A code is scaled before it enters a product (1.1 us at n = 8, T = 16384, D =
-// 2048): codes run up to 448, and their products with gradients above 2^113 would
+// A code is scaled before it enters a product (1.1 us of 240 at n = 8, T = 16384,
+// D = 2048, 1.4 of 70 at n = 4, T = D = 4096): codes run up to 448, and their products with gradients above 2^113 would
 // overflow in sums whose scaled values do not.
 //
 // Sums: the tensor core adds at most 64 columns, then fp32 registers (a long
