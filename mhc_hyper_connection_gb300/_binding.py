@@ -492,7 +492,9 @@ class MhcPre:
         torch's current stream).  `weights` (from prepare_weights) replaces
         phi and gamma.  Raises MhcError on a host-side rejection."""
         args = self.make_args(x, phi, alpha, bias, out, gamma, pre_mix, weights)
-        st = mhc_pre_run(self.handle, args, _launch_stream(stream, x.device))
+        # without x there are no tokens, and no device to look at
+        stream = _launch_stream(stream, x.device) if x is not None else int(getattr(stream, "cuda_stream", stream or 0))
+        st = mhc_pre_run(self.handle, args, stream)
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_run", last_error())
         return out

@@ -157,3 +157,9 @@ def test_mapping_status_waits_for_the_current_stream(binding, monkeypatch):
     for stream, want in ((None, STREAM), (77, 77), (0, None)):
         binding.op.status({"workspace": Tensor((1024,), U8)}, stream=stream)
         assert binding.record.calls["mhc_pre_status"][-1].value == want
+
+
+def test_run_without_tokens(binding):
+    """x None stands for no tokens: the call still reaches the library."""
+    binding.op.run(None, None, None, None, {"y": None}, stream=77)
+    assert getattr(binding.record.calls["mhc_pre_run"][-1], "value", None) == 77
