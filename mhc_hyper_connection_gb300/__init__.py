@@ -1,6 +1,6 @@
 """GB300 (sm_103a) mHC pre-mapping and post-mapping, the gated feed-forward block
-between them, each forward and backward, and 8-bit activation checkpoints:
-C ABI + thin ctypes binding.
+between them, each forward and backward, 8-bit activation checkpoints, and routed
+experts as the layer's body: C ABI + thin ctypes binding.
 
 The compute lives in ``libmhc_pre.so`` (built from ``csrc/`` by
 ``python -m mhc_hyper_connection_gb300.build``).  This package only loads it
@@ -18,9 +18,17 @@ from ._binding import (  # noqa: F401
     CKPT_BLOCK, MHC_FFN_GELU, MHC_FFN_SILU, MhcFfnArgs, MhcFfnBwdArgs, MhcPostBwdArgs, mhc_ckpt8_pack_run,
     mhc_ckpt8_restore_run, mhc_ffn_backward_run, mhc_ffn_backward_workspace_size, mhc_ffn_run, mhc_ffn_status,
     mhc_ffn_workspace_size, mhc_post_backward_run, mhc_post_ckpt_run)
+from ._binding import (  # noqa: F401
+    MHC_DTYPE_FP32, MHC_GROUP_MAX, MHC_GROUP_TOP2, MHC_SCORE_SIGMOID, MHC_SCORE_SOFTMAX, MhcExpertsArgs,
+    MhcExpertsBwdArgs, MhcRouteArgs, MhcRouteBwdArgs, mhc_expert_plan_rows, mhc_expert_plan_run, mhc_expert_plan_size,
+    mhc_experts_backward_run, mhc_experts_backward_workspace_size, mhc_experts_run, mhc_experts_status,
+    mhc_experts_workspace_size, mhc_route_backward_run, mhc_route_run)
 
 _LAYER_OPS = ("Ckpt8", "ckpt8_pack", "ckpt8_restore", "hc_post_ckpt", "hc_post_backward", "gated_ffn",
               "gated_ffn_backward", "gated_ffn_workspace", "gated_ffn_status")
+
+_EXPERT_OPS = ("ExpertPlan", "Routes", "route_experts", "route_experts_backward", "expert_plan", "experts_ffn",
+               "experts_ffn_backward", "experts_ffn_workspace", "experts_ffn_status")
 
 
 def __getattr__(name):
@@ -29,5 +37,9 @@ def __getattr__(name):
     if name in _LAYER_OPS:
         from . import _layer_ops
         globals().update({k: getattr(_layer_ops, k) for k in _LAYER_OPS})
+        return globals()[name]
+    if name in _EXPERT_OPS:
+        from . import _expert_ops
+        globals().update({k: getattr(_expert_ops, k) for k in _EXPERT_OPS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -20,6 +20,11 @@ MHC_IMPL_FP32 = 0
 MHC_IMPL_TF32 = 1
 MHC_DTYPE_BF16 = 0
 MHC_DTYPE_FP16 = 1
+MHC_DTYPE_FP32 = 2        # router scores, updates
+MHC_SCORE_SOFTMAX = 0
+MHC_SCORE_SIGMOID = 1
+MHC_GROUP_MAX = 0
+MHC_GROUP_TOP2 = 1
 MHC_KERNEL_AUTO = 0
 MHC_KERNEL_CLUSTER = 1
 MHC_KERNEL_GRID = 2
@@ -81,6 +86,36 @@ class MhcFfnBwdArgs(ctypes.Structure):
                 ("gate_up", _P), ("codes", _P), ("scales", _P), ("grad_x", _P), ("grad_w_gate_up", _P),
                 ("grad_w_down", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
                 ("wait_limit_us", ctypes.c_uint32), ("withhold_copy", ctypes.c_int32)]
+
+
+class MhcRouteArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("logits", _P), ("bias", _P), ("experts", _P), ("weights", _P)]
+
+
+class MhcRouteBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float), ("logits", _P),
+                ("experts", _P), ("grad_weights", _P), ("grad_logits", _P)]
+
+
+class MhcExpertsArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("F", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("x", _P), ("weights", _P),
+                ("plan", _P), ("w_gate_up", _P), ("w_down", _P), ("y", _P), ("gate_up", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("wait_limit_us", ctypes.c_uint32),
+                ("withhold_copy", ctypes.c_int32)]
+
+
+class MhcExpertsBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("F", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("grad_y", _P), ("x", _P),
+                ("weights", _P), ("plan", _P), ("w_gate_up", _P), ("w_down", _P), ("gate_up", _P), ("grad_x", _P),
+                ("grad_weights", _P), ("grad_w_gate_up", _P), ("grad_w_down", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("wait_limit_us", ctypes.c_uint32),
+                ("withhold_copy", ctypes.c_int32)]
 
 
 class MhcError(RuntimeError):
@@ -146,6 +181,20 @@ def library() -> ctypes.CDLL:
             lib.mhc_ffn_backward_run.restype = ctypes.c_int32
             lib.mhc_ffn_status.argtypes = [_P, _P]
             lib.mhc_ffn_status.restype = ctypes.c_int32
+            I64 = ctypes.c_int64
+            for name, args in (("mhc_route_run", [ctypes.POINTER(MhcRouteArgs), _P]),
+                               ("mhc_route_backward_run", [ctypes.POINTER(MhcRouteBwdArgs), _P]),
+                               ("mhc_expert_plan_size", [I64] * 3 + [SZP]),
+                               ("mhc_expert_plan_rows", [I64] * 3 + [ctypes.POINTER(I64)]),
+                               ("mhc_expert_plan_run", [I64] * 3 + [_P, _P, ctypes.c_size_t, _P]),
+                               ("mhc_experts_workspace_size", [I64] * 5 + [SZP]),
+                               ("mhc_experts_backward_workspace_size", [I64] * 5 + [SZP]),
+                               ("mhc_experts_run", [ctypes.POINTER(MhcExpertsArgs), _P]),
+                               ("mhc_experts_backward_run", [ctypes.POINTER(MhcExpertsBwdArgs), _P]),
+                               ("mhc_experts_status", [_P, _P])):
+                f = getattr(lib, name)
+                f.argtypes = args
+                f.restype = ctypes.c_int32
             lib.mhc_pre_backward_workspace_size.argtypes = [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
             lib.mhc_pre_backward_workspace_size.restype = ctypes.c_int32
             lib.mhc_pre_backward_run.argtypes = [_P, ctypes.POINTER(MhcPreBwdArgs), _P]
@@ -328,6 +377,59 @@ def mhc_ffn_backward_run(args: MhcFfnBwdArgs, stream: int = 0) -> int:
 
 def mhc_ffn_status(workspace: int = 0, stream: int = 0) -> int:
     return library().mhc_ffn_status(workspace or None, stream or None)
+
+
+# ------------------------------------------------------------- routed experts
+
+def mhc_route_run(args: MhcRouteArgs, stream: int = 0) -> int:
+    return library().mhc_route_run(ctypes.byref(args), stream or None)
+
+
+def mhc_route_backward_run(args: MhcRouteBwdArgs, stream: int = 0) -> int:
+    return library().mhc_route_backward_run(ctypes.byref(args), stream or None)
+
+
+def mhc_expert_plan_size(T: int, k: int, E: int):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t(0)
+    st = library().mhc_expert_plan_size(int(T), int(k), int(E), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_expert_plan_rows(T: int, k: int, E: int):
+    """Returns (status, rows)."""
+    n = ctypes.c_int64(0)
+    st = library().mhc_expert_plan_rows(int(T), int(k), int(E), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_expert_plan_run(T: int, k: int, E: int, experts: int, plan: int, plan_bytes: int, stream: int = 0) -> int:
+    return library().mhc_expert_plan_run(int(T), int(k), int(E), experts or None, plan or None, int(plan_bytes), stream or None)
+
+
+def mhc_experts_workspace_size(T: int, E: int, k: int, D: int, F: int):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t(0)
+    st = library().mhc_experts_workspace_size(int(T), int(E), int(k), int(D), int(F), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_experts_backward_workspace_size(T: int, E: int, k: int, D: int, F: int):
+    n = ctypes.c_size_t(0)
+    st = library().mhc_experts_backward_workspace_size(int(T), int(E), int(k), int(D), int(F), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_experts_run(args: MhcExpertsArgs, stream: int = 0) -> int:
+    return library().mhc_experts_run(ctypes.byref(args), stream or None)
+
+
+def mhc_experts_backward_run(args: MhcExpertsBwdArgs, stream: int = 0) -> int:
+    return library().mhc_experts_backward_run(ctypes.byref(args), stream or None)
+
+
+def mhc_experts_status(workspace: int = 0, stream: int = 0) -> int:
+    return library().mhc_experts_status(workspace or None, stream or None)
 
 
 def mhc_pre_backward_workspace_size(handle, T: int):

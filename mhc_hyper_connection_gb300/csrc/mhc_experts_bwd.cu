@@ -1,0 +1,112 @@
+// mhc_experts_bwd.cu -- backward kernels of the routed experts.
+#include "mhc_experts_gemm.cuh"
+
+namespace mhc {
+namespace {
+
+// Rows of x and grad_y and the weights in the plan's order; zero rows of gg and w a
+// where it is padding.  The call's first launch: clears its header.
+__global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, const PlanView p, int k, int D, int F,
+                                                              const uint16_t* x, const uint16_t* gy, const float* weights,
+                                                              uint16_t* xs, uint16_t* gys, float* w_row, uint16_t* gg,
+                                                              uint16_t* wa) {
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
+  const long long items = (long long)p.head[1] * segs;
+  for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
+    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs), slot = p.rows[r];
+    gather_item(slot, k, r, seg, D, x, xs, lane);
+    gather_item(slot, k, r, seg, D, gy, gys, lane);
+    if (seg == 0) {
+      if (lane == 0) w_row[r] = slot >= 0 ? weights[slot] : 0.0f;
+      if (slot < 0) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        for (int c = lane * 8; c < 2 * F; c += 256) *reinterpret_cast<uint4*>(gg + (size_t)r * 2 * F + c) = z;
+        for (int c = lane * 8; c < F; c += 256) *reinterpret_cast<uint4*>(wa + (size_t)r * F + c) = z;
+      }
+    }
+  }
+}
+
+// grad_x, and grad_weights from the parts of its sums: rows of the plan's order, one a
+// lane; slots without a row get zeros.
+template <bool F16>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p, long long T, int k, int D, int parts,
+                                                               long long cap_rows, const uint16_t* rows, const float* part,
+                                                               uint16_t* grad_x, float* grad_weights) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 511) / 512;
+  const long long groups = (p.head[1] + 31) / 32;
+  for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs + groups; i += (long long)gridDim.x * 8) {
+    if (i < groups) {
+      const long long r = i * 32 + lane;
+      const int slot = r < p.head[1] ? p.rows[r] : -1;
+      if (slot >= 0) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int n = 0; n < parts; ++n) sum += part[n * cap_rows + r];
+        grad_weights[slot] = sum;
+      }
+    } else {
+      const long long item = i - groups, t = item / segs;
+      combine_item<F16>(item, segs, k, D, p.places, nullptr, rows, grad_x, lane);
+      if (item == t * segs && lane < k && p.places[t * k + lane] < 0) grad_weights[t * k + lane] = 0.0f;
+    }
+  }
+}
+
+template <bool F16>
+cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
+  const int D = L.D, F = L.F, sms = L.call.sms, box = token_rows(L.lay.width);
+  cudaError_t e = launch_rows(gather_backward_kernel, L.lay.cap_rows * ((D + 1023) / 1024), sms, false, s, L.call.header, L.plan,
+                              L.k, D, F, static_cast<const uint16_t*>(L.x_in), static_cast<const uint16_t*>(L.grad_y), L.weights,
+                              static_cast<uint16_t*>(L.xs), static_cast<uint16_t*>(L.gys), L.w_row,
+                              static_cast<uint16_t*>(L.gg_buf), static_cast<uint16_t*>(L.wa_buf));
+  if (e != cudaSuccess) return e;
+  {
+    const auto job = experts_job<kRowsMn, F16>(L.wd_mn, L.gy, L.plan, F, kFfnTileM, D);
+    const EpiExpertDgate<F16> o = {static_cast<const uint16_t*>(L.gate_up), L.w_row, static_cast<uint16_t*>(L.gg_buf),
+                                   static_cast<uint16_t*>(L.wa_buf), L.part, F, L.act, L.lay.cap_rows};
+    e = launch_group(job, grp_call(L.call, 1, false, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    WeightGradJob<F16> job;
+    job.a[0] = L.gg_mn;
+    job.b[0] = L.xs_mn;
+    job.a[1] = L.gy_mn;
+    job.b[1] = L.wa_mn;
+    job.counts = L.plan.counts;
+    job.starts = L.plan.starts;
+    job.E = L.E;
+    const int M[2] = {2 * F, D}, N[2] = {D, F};
+    for (int i = 0; i < 2; ++i) {
+      job.width[i] = N[i] >= 256 ? 256 : (N[i] + 63) / 64 * 64;
+      job.tiles_n[i] = (N[i] + job.width[i] - 1) / job.width[i];
+      job.area[i] = (M[i] + kFfnTileM - 1) / kFfnTileM * job.tiles_n[i];
+      job.by_n[i] = FastDiv((uint32_t)job.tiles_n[i]);
+    }
+    job.by_expert = FastDiv((uint32_t)(job.area[0] + job.area[1]));
+    const EpiWeightGrad<F16> o = {{static_cast<uint16_t*>(L.grad_w_gate_up), static_cast<uint16_t*>(L.grad_w_down)},
+                                  {M[0], M[1]}, {N[0], N[1]}, L.room};
+    e = launch_group(job, grp_call(L.call, 2, false, 128), o, (long long)L.E * (job.area[0] + job.area[1]), sms, true, s);
+    if (e != cudaSuccess) return e;
+  }
+  // rows of grad_x over those of x
+  const auto job = experts_job<kRowsMn, F16>(L.wgu_mn, L.gg, L.plan, D, kFfnTileM, 2 * F);
+  const EpiRows<F16> o = {static_cast<uint16_t*>(L.xs), D};
+  e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
+  if (e != cudaSuccess) return e;
+  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 511) / 512) + L.lay.cap_rows / 32 + 1, sms, true, s, L.plan, L.T, L.k,
+                     D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const float*>(L.part),
+                     static_cast<uint16_t*>(L.grad_x), L.grad_weights);
+}
+
+}  // namespace
+
+cudaError_t launch_experts_backward(const ExpertsBwdLaunch& L, bool f16, cudaStream_t s) {
+  return f16 ? backward<true>(L, s) : backward<false>(L, s);
+}
+
+}  // namespace mhc

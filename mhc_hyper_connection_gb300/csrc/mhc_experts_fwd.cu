@@ -1,0 +1,56 @@
+// mhc_experts_fwd.cu -- forward kernels of the routed experts.
+#include "mhc_experts_gemm.cuh"
+
+namespace mhc {
+namespace {
+
+// Rows of x in the plan's order.  The call's first launch: clears its header.
+__global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const PlanView p, int k, int D, const uint16_t* x,
+                                                     uint16_t* xs) {
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
+  const long long items = (long long)p.head[1] * segs;
+  for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
+    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs);
+    gather_item(p.rows[r], k, r, seg, D, x, xs, lane);
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(256) combine_kernel(const PlanView p, long long T, int k, int D, const float* weights,
+                                                      const uint16_t* rows, uint16_t* y) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 511) / 512;
+  for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs; i += (long long)gridDim.x * 8)
+    combine_item<F16>(i, segs, k, D, p.places, weights, rows, y, lane);
+}
+
+template <bool F16, bool kKept>
+cudaError_t gate_up(const ExpertsFwdLaunch& L, cudaStream_t s) {
+  const auto job = experts_job<kRowsGateUp, F16>(L.wgu, L.x, L.plan, L.F, 128, L.D);
+  const EpiExpertGateUp<F16, kKept> e = {static_cast<uint16_t*>(L.a_buf), static_cast<uint16_t*>(L.gate_up), L.F, L.act};
+  return launch_group(job, grp_call(L.call, 1, false, token_rows(L.lay.width)), e, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
+}
+
+template <bool F16>
+cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
+  cudaError_t e = launch_rows(gather_kernel, L.lay.cap_rows * ((L.D + 1023) / 1024), L.call.sms, false, s, L.call.header, L.plan, L.k,
+                              L.D, static_cast<const uint16_t*>(L.x_in), static_cast<uint16_t*>(L.xs));
+  if (e != cudaSuccess) return e;
+  if ((e = L.gate_up ? gate_up<F16, true>(L, s) : gate_up<F16, false>(L, s)) != cudaSuccess) return e;
+  const auto job = experts_job<kRowsK, F16>(L.wd, L.a, L.plan, L.D, kFfnTileM, L.F);
+  const EpiRows<F16> o = {static_cast<uint16_t*>(L.xs), L.D};
+  e = launch_group(job, grp_call(L.call, 2, true, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
+  if (e != cudaSuccess) return e;
+  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 511) / 512), L.call.sms, true, s, L.plan, L.T, L.k, L.D, L.weights,
+                     static_cast<const uint16_t*>(L.xs), static_cast<uint16_t*>(L.y));
+}
+
+}  // namespace
+
+cudaError_t launch_experts_forward(const ExpertsFwdLaunch& L, bool f16, cudaStream_t s) {
+  return f16 ? forward<true>(L, s) : forward<false>(L, s);
+}
+
+}  // namespace mhc

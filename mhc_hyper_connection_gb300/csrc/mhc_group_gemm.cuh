@@ -1,0 +1,417 @@
+// mhc_group_gemm.cuh -- matrix products whose tiles a job describes: the routed
+// experts' products (groups of rows whose sizes only the device knows) and the
+// products of the orthogonalisation (many small matrices, symmetric results).
+//
+// The kernel is built as the feed-forward block's (mhc_ffn_gemm.cuh): persistent
+// pairs of CTAs, one tcgen05 cta_group::2 product of 256 rows of A by up to 256 of
+// B per step, operands by TMA through a ring of stages, two tensor-memory
+// accumulators so that epilogues overlap the next tile's products.  What differs:
+// a job maps a tile number to operands, width and depth (each tile's own), stages
+// are as many as the job's operands leave room for, and a tile deeper than
+// kDeepest chunks is formed in parts that the epilogue joins in fp32.
+#pragma once
+
+#include "mhc_ffn_gemm.cuh"
+
+namespace mhc {
+
+constexpr int kGrpMaxStages = 12;
+constexpr int kGrpRing = 6 * 32768;                  // bytes of the ring of stages
+constexpr int kGrpDeepest = 512;                     // chunks of the depth that one accumulator sums at most (kDeepest)
+
+// A tile of a job.  e < 0: no more tiles.
+struct __align__(16) GTile {
+  int e;                       // group (expert, matrix)
+  int tm, tn;                  // tile row and, where the job has them, column
+  int row0, rows;              // first row of the group's part and its rows that count
+  int width;                   // rows of B, a multiple of 32
+  int kiters;                  // chunks of the depth (0: nothing to sum)
+  int kind;                    // which of the job's products
+};
+
+struct GrpTail {
+  uint64_t full[kGrpMaxStages], empty[kGrpMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t sched_full[kSchedSlots], sched_empty[kSchedSlots];
+  uint64_t mma_done;
+  uint64_t sent[2];                        // as in GemmTail
+  uint32_t sent_bytes[2][kGrpMaxStages];   // bytes of each CTA's last copies into a stage
+  uint32_t tmem_base;
+  uint32_t abort;
+  GTile sched[kSchedSlots];
+};
+constexpr size_t kGrpSmem = (size_t)kGrpRing + 8 * kStageBuf + sizeof(GrpTail) + 1024;
+static_assert(kGrpSmem <= 232448, "shared memory of a CTA");
+
+struct GrpCall {
+  uint32_t* err;               // device error word
+  uint32_t* counter;           // tiles drawn so far, zero at the launch (jobs that draw)
+  uint64_t wait_ns;
+  int withhold;                // test hook
+  int stages, stage_bytes;     // of the ring, per CTA
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// As settle_copies of mhc_ffn_gemm.cuh, for stages whose bytes differ: both CTAs
+// copy the same number of bytes into a stage and leave behind what they last
+// copied into each.
+static __device__ __noinline__ void grp_settle(GrpTail* tail, uint64_t wait_ns, int stages) {
+  uint64_t sent[2];
+  const uint64_t t0 = now_ns();
+  do {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      asm volatile("ld.acquire.cluster.shared::cta.b64 %0, [%1];" : "=l"(sent[r]) : "r"(smem_u32(&tail->sent[r])) : "memory");
+    if (now_ns() - t0 > 2 * wait_ns + 100000000ull) return;
+  } while (!sent[0] || !sent[1]);
+  const long long mine = (long long)sent[0] - 1, theirs = (long long)sent[1] - 1;
+  const long long both = mine < theirs ? mine : theirs, most = mine < theirs ? theirs : mine;
+  for (long long k = both; k < most; ++k) {
+    const int s = (int)(k % stages);
+    if (mine < theirs) mbar_expect_tx(&tail->full[s], *(volatile uint32_t*)&tail->sent_bytes[1][s]);
+    else mbar_complete_tx(&tail->full[s], *(volatile uint32_t*)&tail->sent_bytes[0][s]);
+  }
+  for (long long k = most > stages ? most - stages : 0; k < most; ++k)
+    mbar_drain(&tail->full[k % stages], (uint32_t)(k / stages) & 1u);
+}
+
+__host__ __device__ constexpr uint32_t grp_idesc(bool f16, bool a_mn, bool b_mn, int width) {
+  return (f16 ? (1u << 4) : ((1u << 4) | (1u << 7) | (1u << 10))) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(width >> 3) << 17) | ((uint32_t)(kFfnTileM >> 4) << 24);
+}
+
+// Job:
+//   kAMn, kBMn           operands stored MN-major
+//   kDraw                tiles are drawn from the counter (their work differs), else dealt out in turn
+//   int tiles() const    their number (read once earlier launches are complete)
+//   Raw fetch(int t)     what tile t needs from memory, loaded ahead of its use
+//   GTile make(int t, const Raw&)
+//   int bytes(const GTile&)                       bytes that one CTA copies into a stage
+//   void load(tile, k, sa, sb, bar, rank)         chunk k of the depth into a stage
+//   int steps(tile, k)                            products of depth 16 in chunk k
+//   uint32_t idesc(tile)
+//   void prefetch()                               tensor-map descriptors
+// Epi:
+//   void tile(tile, part, parts, taddr, rank, q, grp, buf, lane, pair)
+template <class Job, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    group_gemm_kernel(const __grid_constant__ Job job, const GrpCall call, const __grid_constant__ Epi epi) {
+  constexpr uint32_t kTmemCols = 512;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* bufs = smem + kGrpRing;
+  GrpTail* tail = reinterpret_cast<GrpTail*>(bufs + 8 * kStageBuf);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int stages = call.stages, stage_bytes = call.stage_bytes;
+  Ctl ctl{&tail->abort, call.err, call.wait_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGrpMaxStages; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+      tail->sent_bytes[0][s] = tail->sent_bytes[1][s] = 0;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tail->acc_full[b], 1);
+      mbar_init(&tail->acc_empty[b], 16);
+    }
+    for (int b = 0; b < kSchedSlots; ++b) {
+      mbar_init(&tail->sched_full[b], 1);
+      mbar_init(&tail->sched_empty[b], 18);
+    }
+    mbar_init(&tail->mma_done, 1);
+    tail->abort = 0u;
+    tail->sent[0] = tail->sent[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    job.prefetch();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();                            // the peer's barriers exist
+  tc_fence_after();
+  const uint32_t tmem_base = tail->tmem_base;
+  pdl_trigger();
+  pdl_wait();                                    // operands, plan and counter are earlier launches'
+  const int ntiles = job.tiles();
+
+  // The n-th tile of this pair as the roles see it (e = -1 after the last, and when
+  // the wait for it gave up).  One call per n and role.
+  auto tile_of = [&](int n, bool whole_warp) -> GTile {
+    GTile g;
+    g.e = -1;
+    if constexpr (!Job::kDraw) {
+      const long long t = pair + (long long)n * pairs;
+      if (t < ntiles) g = job.make((int)t, job.fetch((int)t));
+      return g;
+    } else {
+      const int slot = n % kSchedSlots;
+      const uint32_t par = (uint32_t)(n / kSchedSlots) & 1u;
+      bool ok = mbar_test_cluster(&tail->sched_full[slot], par) ||
+                wait_slow(&tail->sched_full[slot], par, ctl, kErrClusterWait, true);
+      if (whole_warp) ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) {
+        const volatile int* p = reinterpret_cast<const volatile int*>(&tail->sched[slot]);
+        g.e = p[0];
+        g.tm = p[1];
+        g.tn = p[2];
+        g.row0 = p[3];
+        g.rows = p[4];
+        g.width = p[5];
+        g.kiters = p[6];
+        g.kind = p[7];
+      }
+      if (whole_warp) __syncwarp();
+      if (!whole_warp || lane == 0) mbar_arrive_remote(&tail->sched_empty[slot], 0);
+      return g;
+    }
+  };
+
+  if (warp == 0) {
+    // ===================================================== TMA producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      long long iss = 0;
+      bool ok = true;
+      auto publish = [&](int n, const GTile& g) -> bool {
+        const int slot = n % kSchedSlots;
+        if (!wait_slow(&tail->sched_empty[slot], ((uint32_t)(n / kSchedSlots) & 1u) ^ 1u, ctl, kErrClusterWait, true)) return false;
+        const int4 lo = make_int4(g.e, g.tm, g.tn, g.row0), hi = make_int4(g.rows, g.width, g.kiters, g.kind);
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r) {
+          const uint32_t at = map_cluster(&tail->sched[slot], r);
+          st_cluster_v4(at, lo);
+          st_cluster_v4(at + 16, hi);
+        }
+        mbar_arrive_remote(&tail->sched_full[slot], 0);
+        mbar_arrive_remote(&tail->sched_full[slot], 1);
+        return true;
+      };
+      auto draw = [&]() -> int {
+        const unsigned t = (unsigned)pairs + atomicAdd(call.counter, 1u);
+        return t < (unsigned)ntiles ? (int)t : -1;
+      };
+      GTile none, cur, next;
+      none.e = -1;
+      none.tm = none.tn = none.row0 = none.rows = none.width = none.kiters = none.kind = 0;
+      cur = next = none;
+      if (Job::kDraw && rank == 0) {
+        if (pair < ntiles) cur = job.make(pair, job.fetch(pair));
+        const int t = cur.e >= 0 ? draw() : -1;
+        if (t >= 0) next = job.make(t, job.fetch(t));
+        ok = publish(0, cur) && publish(1, next);
+      }
+      for (int n = 0; ok; ++n) {
+        const GTile g = Job::kDraw && rank == 0 ? cur : tile_of(n, false);
+        if (g.e < 0) break;
+        const int bytes = job.bytes(g);
+        // test hook, as in ffn_gemm_kernel
+        const int kend = call.withhold && pair < 2 && n == 0 ? max(g.kiters - 1 - (int)(rank ^ (uint32_t)pair), 0) : g.kiters;
+        // tile n + 2 is drawn under this tile's copies, and what it needs from
+        // memory fetched under them
+        int after = -1;
+        typename Job::Raw raw;
+        const bool more = Job::kDraw && rank == 0 && next.e >= 0;
+        if (more) after = draw();
+        const int half = kend >> 1;
+        for (int k = 0; k < kend; ++k) {
+          if (k == half && after >= 0) raw = job.fetch(after);
+          if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
+          const uint32_t sa = smem_u32(smem + s * stage_bytes);
+          if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * (uint32_t)bytes);
+          job.load(g, k, sa, sa + kGemmOpBytes, map_cluster(&tail->full[s], 0), (int)rank);
+          tail->sent_bytes[rank][s] = (uint32_t)bytes;     // for grp_settle; the odd CTA's are sent over below
+          ++iss;
+          if (++s == stages) { s = 0; ph ^= 1u; }
+        }
+        ok = ok && kend == g.kiters;
+        if (Job::kDraw && rank == 0 && ok) {
+          if (kend == 0 && after >= 0) raw = job.fetch(after);
+          GTile g2 = none;
+          if (after >= 0) g2 = job.make(after, raw);
+          ok = publish(n + 2, g2);
+          cur = next;
+          next = g2;
+        }
+      }
+      if (rank == 1) {
+        const uint32_t at = map_cluster(&tail->sent_bytes[1][0], 0);
+        for (int i = 0; i < stages; ++i)
+          asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(tail->sent_bytes[1][i]) : "memory");
+      }
+      asm volatile("st.release.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cluster(&tail->sent[rank], 0)), "l"(iss + 1)
+                   : "memory");
+    }
+  } else if (warp == 1) {
+    // ===================================================== MMA issuer
+    if (rank == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const uint64_t a0 = Job::kAMn ? sw128_desc_mn(0, 8192) : sw128_desc(0), b0 = Job::kBMn ? sw128_desc_mn(0, 8192) : sw128_desc(0);
+      constexpr uint32_t astep = (Job::kAMn ? 2048u : 32u) >> 4, bstep = (Job::kBMn ? 2048u : 32u) >> 4;
+      for (int n = 0; ok; ++n) {
+        const GTile g = tile_of(n, true);
+        if (g.e < 0) break;
+        const uint32_t idesc = job.idesc(g);
+        for (int k0 = 0; k0 < g.kiters && ok; k0 += kGrpDeepest, ++acc) {
+          const int b = acc & 1, k1 = min(k0 + kGrpDeepest, g.kiters);
+          if (!wait_slow(&tail->acc_empty[b], ((uint32_t)(acc >> 1) & 1u) ^ 1u, ctl, kErrClusterWait, true)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)(b * kFfnTileN);
+          for (int k = k0; k < k1; ++k) {
+            if (!wait_stage(&tail->full[s], ph, ctl)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = desc_addr(smem + s * stage_bytes), sb = sa + (kGemmOpBytes >> 4);
+            const int steps = job.steps(g, k);
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < kFfnTileK / 16; ++ks)
+                if (ks < steps) mma_pair(d, a0 + (sa + ks * astep), b0 + (sb + ks * bstep), idesc, (k > k0 || ks) ? 1u : 0u);
+              commit_pair(&tail->empty[s]);
+            }
+            __syncwarp();
+            if (++s == stages) { s = 0; ph ^= 1u; }
+          }
+          if (ok && elect_one()) commit_pair(&tail->acc_full[b]);
+          __syncwarp();
+        }
+      }
+      if (elect_one()) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&tail->mma_done))
+                   : "memory");
+      __syncwarp();
+      mbar_drain(&tail->mma_done, 0);
+      if ((!ok || *ctl.abort) && lane == 0) grp_settle(tail, ctl.wait_ns, stages);
+      __syncwarp();
+    }
+  } else {
+    // ===================================================== epilogue
+    const int grp = (warp - 2) >> 2, q = warp & 3;
+    uint8_t* buf = bufs + (warp - 2) * kStageBuf;
+    int acc = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const GTile g = tile_of(n, true);
+      if (g.e < 0) break;
+      const int parts = (g.kiters + kGrpDeepest - 1) / kGrpDeepest;
+      if (parts == 0) epi.tile(g, 0, 0, 0u, (int)rank, q, grp, buf, lane, pair);
+      for (int p = 0; p < parts; ++p, ++acc) {
+        const int b = acc & 1;
+        if (!__all_sync(0xFFFFFFFFu, wait_stage(&tail->acc_full[b], (uint32_t)(acc >> 1) & 1u, ctl))) { ok = false; break; }
+        tc_fence_after();
+        epi.tile(g, p, parts, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN), (int)rank, q, grp, buf, lane,
+                 pair);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(&tail->acc_empty[b], 0);
+      }
+    }
+  }
+
+  // ---- teardown: the pair leaves together
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Launch: at most `most` tiles; started as SMs fall free of the launch before.
+template <class Job, class Epi>
+cudaError_t launch_group(const Job& job, const GrpCall& call, const Epi& epi, long long most, int sms, bool dependent,
+                         cudaStream_t s) {
+  auto* k = group_gemm_kernel<Job, Epi>;
+  static std::atomic<int> known[64];             // as in launch_gemm
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGrpSmem;
+  int pairs = known[dev].load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGrpSmem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(sms & ~1));
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, k, &cfg)) != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    known[dev].store(pairs, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, job, call, epi);
+}
+
+// The ring for stages of 128 rows of A and `b_rows` of B per CTA.
+inline void grp_ring(GrpCall* c, int b_rows) {
+  c->stage_bytes = kGemmOpBytes + b_rows * kFfnTileK * 2;
+  c->stages = kGrpRing / c->stage_bytes;
+  if (c->stages > kGrpMaxStages) c->stages = kGrpMaxStages;
+}
+
+// ------------------------------------------------ epilogues' shared pieces
+
+// Thirty-two columns of the warp's accumulator lanes as the transposed rows of a
+// matrix: column j is row j of it, the lanes 32 consecutive elements.  Staged as
+// rows of 64 bytes and written in 16-byte pieces.  `base`: element of lane 0 in
+// row 0; `pitch` in bytes; `rows`: rows that count; `n`: elements of a row that
+// count (a multiple of 8).
+template <bool F16>
+__device__ __forceinline__ void store_transposed(const float (&v)[32], uint8_t* buf, uint8_t* base, size_t pitch, int rows,
+                                                 int n, int lane) {
+  uint16_t* st = reinterpret_cast<uint16_t*>(buf);
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const uint32_t w = pack2<F16>(v[j], v[j + 1]);
+    st[j * 32 + lane] = (uint16_t)w;
+    st[(j + 1) * 32 + lane] = (uint16_t)(w >> 16);
+  }
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + c * 16);
+    if (r < rows && c * 8 < n) *reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16) = w;
+  }
+  __syncwarp();
+}
+
+}  // namespace mhc

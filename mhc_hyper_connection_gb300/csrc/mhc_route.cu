@@ -1,0 +1,851 @@
+// mhc_route.cu -- routing of tokens to experts (include/mhc_route.h): scores,
+// choice and weights, the weights' gradient, and the counting sort of the slots.
+//
+// Routing and its gradient read and write each score once; a row is a warp's, its
+// scores in registers, E / 32 consecutive ones a lane.  Bound by the k + 1 rounds of
+// a maximum over the warp (about 40 instructions each), not by memory.
+#include <math.h>
+
+#include "mhc_experts.cuh"
+#include "mhc_ffn.cuh"
+#include "mhc_host.cuh"
+#include "../../include/mhc_route.h"
+
+namespace mhc {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kRouteWarps = 4;
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int* experts;
+  float* weights;
+  long long T;
+  int E, k, sigmoid, groups, top_groups, top2, renorm;
+  float scale;
+};
+
+// fp32 and fp64 as unsigned numbers of the same order, NaN above all.  -inf (an
+// expert that is out) is kOut.
+__device__ __forceinline__ uint32_t order32(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v != v ? 0xFFFFFFFFu : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long order64(double v) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v);
+  return v != v ? ~0ull : b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+}
+constexpr uint32_t kOut32 = 0x007FFFFFu;                       // order32(-inf)
+constexpr unsigned long long kOut64 = 0x000FFFFFFFFFFFFFull;   // order64(-inf)
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+  const uint32_t hi = warp_max((uint32_t)(v >> 32));
+  const uint32_t lo = warp_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((unsigned long long)hi << 32) | lo;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+template <int kType>
+__device__ __forceinline__ float load_logit(const void* p, long long at) {
+  if constexpr (kType == MHC_DTYPE_FP32) return static_cast<const float*>(p)[at];
+  else if constexpr (kType == MHC_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+  else return __half2float(static_cast<const __half*>(p)[at]);
+}
+
+// The whole choice once more with keys in fp64, for rows where fp32 left two keys
+// too close to order: one in a thousand of ordinary rows with a bias.  keys: E
+// doubles of this warp.  Lane j < k returns the j-th expert (or -1).
+template <int kType>
+__device__ __noinline__ int choose64(const RouteArgs& a, long long row, double* keys, int lane) {
+  const int E = a.E;
+  double top = -INFINITY;
+  for (int e = lane; e < E; e += 32) {
+    const double l = load_logit<kType>(a.logits, row * E + e);
+    if (l > top) top = l;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double v = __shfl_xor_sync(kFull, top, o);
+    if (v > top) top = v;
+  }
+  double sum = 0.0;
+  if (!a.sigmoid) {
+    for (int e = lane; e < E; e += 32) {
+      const double l = load_logit<kType>(a.logits, row * E + e);
+      if (l != -INFINITY) sum += exp(l - top);
+    }
+    sum = warp_sum(sum);
+  }
+  for (int e = lane; e < E; e += 32) {
+    const double l = load_logit<kType>(a.logits, row * E + e);
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
+    keys[e] = l == -INFINITY ? -INFINITY : a.bias ? s + (double)a.bias[e] : s;
+  }
+  __syncwarp();
+  const int per = E / a.groups;
+  uint32_t stays = kFull;
+  if (a.groups > 1) {
+    unsigned long long mark = 0;
+    if (lane < a.groups) {
+      unsigned long long one = kOut64;
+      double best = -INFINITY, next = -INFINITY;
+      for (int i = 0; i < per; ++i) {
+        const double v = keys[lane * per + i];
+        const unsigned long long u = order64(v);
+        if (u > one) {
+          next = best;
+          best = v;
+          one = u;
+        } else if (order64(v) > order64(next)) {
+          next = v;
+        }
+      }
+      mark = order64(a.top2 && next != -INFINITY ? best + next : best);
+    }
+    stays = 0;
+    for (int g = 0; g < a.top_groups; ++g) {
+      const unsigned long long m = warp_max(mark);
+      const uint32_t who = __ballot_sync(kFull, mark == m && lane < a.groups && !((stays >> lane) & 1u));
+      const int w = __ffs(who) - 1;
+      stays |= 1u << w;
+      if (lane == w) mark = 0;
+    }
+  }
+  int mine = -1;
+  // without a bias the order within the groups that stay is that of the logits
+  unsigned long long taken_key = ~0ull;
+  int taken = -1;
+  for (int j = 0; j < a.k; ++j) {
+    // the next in order after (taken_key, taken): largest key, then lowest index
+    unsigned long long best = kOut64;
+    int at = E;
+    for (int e = lane; e < E; e += 32) {
+      if (!((stays >> (e / per)) & 1u) && a.groups > 1) continue;
+      const double l = load_logit<kType>(a.logits, row * E + e);
+      const unsigned long long u = a.bias ? order64(keys[e]) : order64(l);
+      if (u == kOut64 || l == -INFINITY) continue;
+      if (j && (u > taken_key || (u == taken_key && e <= taken))) continue;
+      if (u > best) {
+        best = u;
+        at = e;
+      }
+    }
+    const unsigned long long m = warp_max(best);
+    if (m == kOut64) break;
+    const int e = (int)__reduce_min_sync(kFull, best == m ? (unsigned)at : (unsigned)E);
+    if (lane == j) mine = e;
+    taken_key = m;
+    taken = e;
+  }
+  __syncwarp();
+  return mine;
+}
+
+// V: consecutive scores of a lane.
+template <int kType, int V>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+  extern __shared__ double route_keys[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k, e0 = lane * V, per = E / a.groups;
+  double* keys64 = route_keys + (size_t)warp * E;
+  float* keys32 = reinterpret_cast<float*>(keys64);
+  for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
+    float l[V];
+    const long long base = row * E + e0;
+    bool loaded = false;
+    if constexpr (V >= 4) {
+      if (E % 4 == 0) {                          // rows stay aligned to four elements
+        loaded = true;
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          if (e0 + i < E) {
+            if constexpr (kType == MHC_DTYPE_FP32) {
+              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + i);
+              l[i] = v.x;
+              l[i + 1] = v.y;
+              l[i + 2] = v.z;
+              l[i + 3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + base + i);
+              constexpr bool f16 = kType == MHC_DTYPE_FP16;
+              const float2 p = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.x));
+              const float2 q = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.y));
+              l[i] = p.x;
+              l[i + 1] = p.y;
+              l[i + 2] = q.x;
+              l[i + 3] = q.y;
+            }
+          } else {
+            l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+          }
+        }
+      }
+    }
+    if (!loaded) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_logit<kType>(a.logits, base + i) : -INFINITY;
+    }
+    // Scores; softmax: top and sum of the row.
+    uint32_t topu = kOut32;
+#pragma unroll
+    for (int i = 0; i < V; ++i) topu = max(topu, order32(l[i]));
+    topu = warp_max(topu);
+    const float top = topu == 0xFFFFFFFFu ? NAN : __uint_as_float(topu ^ ((topu >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+    const bool by_key = a.bias != nullptr;
+    const bool scores = by_key || a.groups > 1;
+    float sum = 0.0f, smax = 1.0f;
+    float key[V];
+    if (a.sigmoid) {
+      if (scores) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = l[i] == -INFINITY ? -INFINITY : sigmoid32(l[i]);
+      }
+    } else {
+      const float shift = topu == kOut32 ? 0.0f : top;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        key[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - shift);
+        sum += key[i];
+      }
+      sum = warp_sum(sum);
+      smax = 1.0f / sum;
+      if (scores) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = l[i] == -INFINITY ? -INFINITY : key[i] / sum;
+      }
+    }
+    if (by_key) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) key[i] += a.bias[e0 + i];
+    }
+    // Two keys a and b closer than 2^-19 (smax + max(|a|, |b|)) may stand in the
+    // wrong order: a score is off by a few 2^-24 of itself (softmax: of the largest,
+    // from the rounding of l - top, too), the sum with the bias by 2^-24 of itself.
+    bool unsure = false;
+    uint32_t stays = kFull;
+    if (a.groups > 1) {
+      // marks: lane g has group g's best keys
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) keys32[e0 + i] = key[i];
+      __syncwarp();
+      float best = -INFINITY, next = -INFINITY;
+      // as many lanes as there are for a group, each with every so many-th expert
+      int span = 32 / a.groups;
+      span = 1 << (31 - __clz(span));
+      const int g = lane / span, off = lane - g * span;
+      if (g < a.groups) {
+        // start at different places, so that the lanes' reads spread over the banks
+        const int n = (per - off + span - 1) / span;
+        for (int i = 0; i < n; ++i) {
+          int at = i + g;
+          at -= at >= n ? (at / n) * n : 0;
+          const float v = keys32[g * per + off + at * span];
+          if (order32(v) > order32(best)) {
+            next = best;
+            best = v;
+          } else if (order32(v) > order32(next)) {
+            next = v;
+          }
+        }
+      }
+      for (int o = 1; o < span; o <<= 1) {
+        const float b2 = __shfl_xor_sync(kFull, best, o), n2 = __shfl_xor_sync(kFull, next, o);
+        if (order32(b2) > order32(best)) {
+          next = order32(best) > order32(n2) ? best : n2;
+          best = b2;
+        } else {
+          next = order32(b2) > order32(next) ? b2 : next;
+        }
+      }
+      const float m = a.top2 && next != -INFINITY ? best + next : best;
+      // group g's mark in lane g
+      const float mark = __shfl_sync(kFull, m, min(lane * span, 31));
+      uint32_t u = lane < a.groups ? order32(mark) : 0u;
+      float last = 0.0f;
+      stays = 0;
+      for (int i = 0; i < a.top_groups; ++i) {
+        const uint32_t mu = warp_max(u);
+        const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
+        stays |= 1u << w;
+        if (lane == w) u = 0u;
+        last = __shfl_sync(kFull, mark, w);
+      }
+      // a group left out whose mark is close to the last one taken
+      const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != -INFINITY;
+      unsure = __any_sync(kFull, left && last - mark <= 0x1p-18f * (smax + fabsf(last)));
+    }
+    // Choice: k + 1 rounds.
+    uint32_t u[V], best = kOut32;
+    int grp = a.groups > 1 ? e0 / per : 0, grp_end = (grp + 1) * per;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (e0 + i >= grp_end) {
+        ++grp;
+        grp_end += per;
+      }
+      const bool in = e0 + i < E && ((stays >> (grp & 31)) & 1u);
+      u[i] = in ? order32(by_key ? key[i] : l[i]) : kOut32;
+      if (l[i] == -INFINITY) u[i] = kOut32;
+      best = max(best, u[i]);
+    }
+    int mine = -1;
+    float prev = 0.0f, prevbias = 0.0f, prevl = 0.0f, myl = -INFINITY;
+    const int rounds = by_key ? k + 1 : k;
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t m = warp_max(best);
+      if (m == kOut32) break;
+      const int w = __ffs(__ballot_sync(kFull, best == m)) - 1;
+      int e = 0;
+      float le = 0.0f;
+      if (lane == w) {
+        bool done = false;
+        best = kOut32;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (!done && u[i] == m) {
+            done = true;
+            u[i] = kOut32;
+            e = e0 + i;
+            le = l[i];
+          }
+          best = max(best, u[i]);
+        }
+      }
+      e = __shfl_sync(kFull, e, w);
+      le = __shfl_sync(kFull, le, w);
+      if (by_key) {
+        const float kv = m == 0xFFFFFFFFu ? NAN : __uint_as_float(m ^ ((m >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+        const float bv = a.bias[e];
+        // equal numbers in give equal keys: the index decides, nothing to look at
+        if (j && prev - kv <= 0x1p-19f * (smax + fmaxf(fabsf(prev), fabsf(kv))) && !(le == prevl && bv == prevbias)) unsure = true;
+        prev = kv;
+        prevbias = bv;
+        prevl = le;
+      }
+      if (lane == j && j < k) {
+        mine = e;
+        myl = le;
+      }
+    }
+    if (unsure) {
+      mine = choose64<kType>(a, row, keys64, lane);
+      myl = mine >= 0 ? load_logit<kType>(a.logits, row * E + mine) : -INFINITY;
+    }
+    // Weights: lane j has slot j.
+    float w;
+    if (a.renorm) {
+      float mx = myl;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      if (mx == -INFINITY) mx = 0.0f;
+      float s;
+      if (a.sigmoid) {
+        // all far below 0: the common factor e^mx is left out
+        const float c = fminf(mx, 0.0f);
+        s = mx < 0.0f ? expf(myl - c) / (1.0f + expf(myl)) : sigmoid32(myl);
+      } else {
+        s = expf(myl - mx);
+      }
+      if (mine < 0) s = 0.0f;
+      const float total = warp_sum(s);
+      w = total == 0.0f ? 0.0f : s / total;
+      if (!a.sigmoid && sum != sum) w = NAN;     // a NaN or infinity among the scores, chosen or not
+    } else {
+      w = a.sigmoid ? sigmoid32(myl) : expf(myl - top) / sum;
+    }
+    if (lane < k) {
+      a.experts[row * k + lane] = mine;
+      a.weights[row * k + lane] = mine < 0 ? 0.0f : w * a.scale;
+    }
+    __syncwarp();
+  }
+}
+
+struct RouteBwdArgs {
+  const void* logits;
+  const int* experts;
+  const float* grad_weights;
+  void* grad_logits;
+  long long T;
+  int E, k, sigmoid, renorm;
+  float scale;
+};
+
+// A warp per row; lane j < k has slot j.
+template <int kType>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(const RouteBwdArgs a) {
+  extern __shared__ float route_row[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k;
+  float* g = route_row + (size_t)warp * E;
+  for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
+    int e = lane < k ? a.experts[row * k + lane] : -1;
+    if (e >= E) e = -1;
+    const float d = e >= 0 ? a.grad_weights[row * k + lane] * a.scale : 0.0f;
+    const float l = e >= 0 ? load_logit<kType>(a.logits, row * E + e) : -INFINITY;
+    float v, dot = 0.0f, top = 0.0f, sum = 1.0f;
+    const bool dense = !a.sigmoid && !a.renorm;
+    if (a.renorm) {
+      float mx = l;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      if (mx == -INFINITY) mx = 0.0f;
+      float s, h = 1.0f;
+      if (a.sigmoid) {
+        s = mx < 0.0f ? expf(l - mx) / (1.0f + expf(l)) : sigmoid32(l);
+        h = 1.0f / (1.0f + expf(l));             // 1 - sigmoid, without its cancellation
+      } else {
+        s = expf(l - mx);
+      }
+      if (e < 0) s = 0.0f;
+      const float total = warp_sum(s);
+      const float w = total == 0.0f ? 0.0f : s / total;
+      dot = warp_sum(d * w);
+      v = w * (d - dot) * h;
+    } else if (a.sigmoid) {
+      const float s = sigmoid32(l);
+      v = d * s * (1.0f / (1.0f + expf(l)));
+    } else {
+      top = -INFINITY;
+      bool bad = false;
+      for (int i = lane; i < E; i += 32) {
+        const float x = load_logit<kType>(a.logits, row * E + i);
+        g[i] = x;
+        bad |= x != x;
+        top = fmaxf(top, x);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      if (top == -INFINITY) top = 0.0f;
+      sum = 0.0f;
+      for (int i = lane; i < E; i += 32) {
+        const float s = g[i] == -INFINITY ? 0.0f : expf(g[i] - top);
+        g[i] = s;
+        sum += s;
+      }
+      sum = warp_sum(sum);
+      if (__any_sync(kFull, bad)) sum = NAN;
+      const float s = e >= 0 && sum != 0.0f ? expf(l - top) / sum : 0.0f;
+      v = d * s;
+      dot = warp_sum(v);
+    }
+    if (e < 0) v = 0.0f;
+    if (dense) {
+      const float f = sum == 0.0f ? 0.0f : dot / sum;
+      __syncwarp();
+      for (int i = lane; i < E; i += 32) g[i] = -g[i] * f;
+    } else {
+      for (int i = lane; i < E; i += 32) g[i] = 0.0f;
+    }
+    __syncwarp();
+    // an expert given twice: its first lane adds the others' parts, in their order
+    const uint32_t same = __match_any_sync(kFull, e);
+    const bool first = e >= 0 && (__ffs(same) - 1) == lane;
+    if (__any_sync(kFull, e >= 0 && !first)) {
+      float add = 0.0f;
+      for (int j = 0; j < k; ++j) {
+        const float o = __shfl_sync(kFull, v, j);
+        if ((same >> j) & 1u) add += o;
+      }
+      v = add;
+    }
+    if (first) g[e] += v;
+    __syncwarp();
+    if (kType == MHC_DTYPE_FP32) {
+      float* out = static_cast<float*>(a.grad_logits) + row * E;
+      if (E % 4 == 0) {
+        for (int i = lane * 4; i < E; i += 128)
+          *reinterpret_cast<float4*>(out + i) = *reinterpret_cast<const float4*>(g + i);
+      } else {
+        for (int i = lane; i < E; i += 32) out[i] = g[i];
+      }
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(a.grad_logits) + row * E;
+      constexpr bool f16 = kType == MHC_DTYPE_FP16;
+      if (E % 2 == 0) {
+        for (int i = lane * 2; i < E; i += 64) {
+          const typename XType<f16>::T2 p = XType<f16>::from_f2(g[i], g[i + 1]);
+          *reinterpret_cast<uint32_t*>(out + i) = *reinterpret_cast<const uint32_t*>(&p);
+        }
+      } else {
+        for (int i = lane; i < E; i += 32) {
+          const typename XType<f16>::T2 p = XType<f16>::from_f2(g[i], 0.0f);
+          out[i] = (uint16_t)*reinterpret_cast<const uint32_t*>(&p);
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ the plan
+
+constexpr int kPlanThreads = 1024, kPlanWarps = 32;
+
+struct PlanArgs {
+  const int* experts;
+  PlanView p;
+  int slots, E, chunk;         // slots of a block
+};
+
+// Shared memory of the plan's kernels: the warps' counters.
+__host__ __device__ inline size_t plan_smem(int E) { return (size_t)kPlanWarps * E * 2; }
+
+// Counts of each expert among each warp's slots of this block.
+__device__ __forceinline__ void plan_count(const PlanArgs& a, uint16_t* hist, int first, int last, int warp, int lane) {
+  const int E = a.E;
+  for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  const int per = (((last - first) + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
+  const int b = first + warp * per, n = min(b + per, last);
+  for (int i = b; i < n; i += 32) {
+    const int at = i + lane;
+    int e = at < n ? a.experts[at] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const uint32_t same = __match_any_sync(kFull, e);
+    if (e >= 0 && (__ffs(same) - 1) == lane) hist[warp * E + e] += (uint16_t)__popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+}
+// The counters as what lies before each warp's slots; returns expert e's count.
+__device__ __forceinline__ int plan_prefix(uint16_t* hist, int E, int e) {
+  int run = 0;
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const int c = hist[w * E + e];
+    hist[w * E + e] = (uint16_t)run;
+    run += c;
+  }
+  return run;
+}
+// Exclusive sum over the block; every thread gets it, *total the whole.
+__device__ __forceinline__ int plan_scan(int v, int* sums, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, s, o);
+      if (lane >= o) s += y;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  const int before = warp ? sums[warp - 1] : 0;
+  *total = sums[31];
+  __syncthreads();
+  return before + x - v;
+}
+// Counts -> starts, padding rows, tiles.  Thread e has expert e's count.
+__device__ __forceinline__ void plan_finish(const PlanArgs& a, int count, int* sums, int* tile_at, int* start_at, int* count_at) {
+  const int e = threadIdx.x, E = a.E, width = a.p.width;
+  int rows, tiles;
+  const int padded = (count + kPlanPad - 1) & ~(kPlanPad - 1);
+  const int start = plan_scan(padded, sums, &rows);
+  const int nt = (count + width - 1) / width;
+  const int t0 = plan_scan(nt, sums, &tiles);
+  if (e < E) {
+    a.p.counts[e] = count;
+    a.p.starts[e] = start;
+    for (int i = count; i < padded; ++i) a.p.rows[start + i] = -1;
+  }
+  tile_at[e] = t0;
+  start_at[e] = start;
+  count_at[e] = count;
+  if (e == 0) {
+    a.p.starts[E] = rows;
+    a.p.head[1] = rows;
+    a.p.head[2] = tiles;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles; i += kPlanThreads) {
+    int lo = 0, hi = E - 1;                      // the last expert whose first tile is at most i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile_at[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    const int n = (count_at[lo] + width - 1) / width, j = i - tile_at[lo], band = j / kPlanBand * kPlanBand;
+    // tiles of one width, the last may have fewer rows
+    const int w = ((count_at[lo] + n - 1) / n + 31) & ~31;
+    const int in_band = min(kPlanBand, n - band), first = band * w;
+    a.p.table[2 * i] = make_int4(lo, tile_at[lo] + band, in_band, start_at[lo] + first);
+    a.p.table[2 * i + 1] = make_int4(min(in_band * w, count_at[lo] - first), w, 0, 0);
+  }
+}
+// Rows of the block's slots: base[e] + what lies before them.
+__device__ __forceinline__ void plan_place(const PlanArgs& a, uint16_t* hist, const int* base, int first, int last, int warp,
+                                           int lane) {
+  const int E = a.E;
+  const int per = (((last - first) + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
+  const int b = first + warp * per, n = min(b + per, last);
+  for (int i = b; i < n; i += 32) {
+    const int at = i + lane;
+    int e = at < n ? a.experts[at] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const uint32_t same = __match_any_sync(kFull, e);
+    int row = -1;
+    if (e >= 0) row = base[e] + hist[warp * E + e] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && (__ffs(same) - 1) == lane) hist[warp * E + e] += (uint16_t)__popc(same);
+    __syncwarp();
+    if (at < n) {
+      a.p.places[at] = row;
+      if (row >= 0) a.p.rows[row] = at;
+    }
+  }
+}
+
+// All in one block.
+__global__ void __launch_bounds__(kPlanThreads) plan_alone_kernel(const PlanArgs a) {
+  extern __shared__ uint16_t plan_hist[];
+  __shared__ int sums[32], tile_at[kMostExperts], start_at[kMostExperts], count_at[kMostExperts];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  plan_count(a, plan_hist, 0, a.slots, warp, lane);
+  const int count = (int)threadIdx.x < a.E ? plan_prefix(plan_hist, a.E, threadIdx.x) : 0;
+  plan_finish(a, count, sums, tile_at, start_at, count_at);
+  __syncthreads();
+  plan_place(a, plan_hist, start_at, 0, a.slots, warp, lane);
+}
+// Many slots: counts of each block's, then the sums over blocks, then the rows.
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs a) {
+  extern __shared__ uint16_t plan_hist[];
+  const int first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.slots);
+  plan_count(a, plan_hist, first, last, threadIdx.x >> 5, threadIdx.x & 31);
+  if ((int)threadIdx.x < a.E) a.p.scratch[(size_t)blockIdx.x * a.E + threadIdx.x] = plan_prefix(plan_hist, a.E, threadIdx.x);
+}
+__global__ void __launch_bounds__(kPlanThreads) plan_sum_kernel(const PlanArgs a, const int blocks) {
+  __shared__ int sums[32], tile_at[kMostExperts], start_at[kMostExperts], count_at[kMostExperts];
+  int count = 0;
+  if ((int)threadIdx.x < a.E) {
+    for (int b0 = 0; b0 < blocks; b0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = b0 + i < blocks ? a.p.scratch[(size_t)(b0 + i) * a.E + threadIdx.x] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (b0 + i < blocks) a.p.scratch[(size_t)(b0 + i) * a.E + threadIdx.x] = count;
+        count += c[i];
+      }
+    }
+  }
+  plan_finish(a, count, sums, tile_at, start_at, count_at);
+}
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a) {
+  extern __shared__ uint16_t plan_hist[];
+  __shared__ int base[kMostExperts];
+  const int first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.slots);
+  plan_count(a, plan_hist, first, last, threadIdx.x >> 5, threadIdx.x & 31);
+  if ((int)threadIdx.x < a.E) {
+    plan_prefix(plan_hist, a.E, threadIdx.x);
+    base[threadIdx.x] = a.p.starts[threadIdx.x] + a.p.scratch[(size_t)blockIdx.x * a.E + threadIdx.x];
+  }
+  __syncthreads();
+  plan_place(a, plan_hist, base, first, last, threadIdx.x >> 5, threadIdx.x & 31);
+}
+
+// --------------------------------------------------------------------- host
+
+mhc_status_t check_route(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || T > (int64_t(1) << 20)) return fail(MHC_ERR_PARAM_INVALID, "T must be in [0, 2^20] (got %lld)", (long long)T);
+  if (E < 1 || E > kMostExperts) return fail(MHC_ERR_PARAM_INVALID, "E must be in [1, 1024] (got %lld)", (long long)E);
+  if (k < 1 || k > kMostChoices || k > E)
+    return fail(MHC_ERR_PARAM_INVALID, "k must be in [1, min(E, 32)] (got %lld)", (long long)k);
+  if (T * k > (int64_t(1) << 22)) return fail(MHC_ERR_PARAM_INVALID, "T k must be at most 2^22 (got %lld)", (long long)(T * k));
+  return MHC_OK;
+}
+mhc_status_t check_kind(int32_t dtype, int32_t score, int32_t renorm, float scale) {
+  if (dtype != MHC_DTYPE_BF16 && dtype != MHC_DTYPE_FP16 && dtype != MHC_DTYPE_FP32)
+    return fail(MHC_ERR_PARAM_INVALID, "dtype must be MHC_DTYPE_BF16, _FP16 or _FP32 (got %d)", (int)dtype);
+  if (score != MHC_SCORE_SOFTMAX && score != MHC_SCORE_SIGMOID)
+    return fail(MHC_ERR_PARAM_INVALID, "score must be MHC_SCORE_SOFTMAX or MHC_SCORE_SIGMOID (got %d)", (int)score);
+  if (renorm != 0 && renorm != 1) return fail(MHC_ERR_PARAM_INVALID, "renormalise must be 0 or 1");
+  if (!isfinite(scale)) return fail(MHC_ERR_PARAM_INVALID, "scale must be finite");
+  return MHC_OK;
+}
+mhc_status_t route_device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MHC_ERR_RUNTIME, "no CUDA device");
+  const DeviceInfo di = device_info(dev);
+  if (!di.ok) return fail(MHC_ERR_RUNTIME, "device %d is not an sm_103 GPU", dev);
+  *sms = di.sms;
+  return MHC_OK;
+}
+unsigned row_blocks(int64_t T, int sms) {
+  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)sms * 16;
+  return (unsigned)(b < most ? b : most);
+}
+size_t elem_bytes(int32_t dtype) { return dtype == MHC_DTYPE_FP32 ? 4 : 2; }
+// Vector loads of four logits and stores of four fp32 or two 16-bit gradients.
+size_t logits_align(int32_t dtype, int64_t E) { return E % 4 == 0 ? 4 * elem_bytes(dtype) : E % 2 == 0 ? 2 * elem_bytes(dtype) : elem_bytes(dtype); }
+
+template <int kType>
+cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
+  // where no key is formed again and no group is marked nothing is kept in shared memory
+  const size_t smem = a.bias || a.groups > 1 ? (size_t)kRouteWarps * a.E * 8 : 0;
+  const unsigned grid = row_blocks(a.T, sms);
+  const int v = (a.E + 31) / 32;
+  if (v <= 1) route_kernel<kType, 1><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  else if (v <= 2) route_kernel<kType, 2><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  else if (v <= 4) route_kernel<kType, 4><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  else if (v <= 8) route_kernel<kType, 8><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  else if (v <= 16) route_kernel<kType, 16><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  else route_kernel<kType, 32><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace mhc
+
+using namespace mhc;
+
+extern "C" {
+
+mhc_status_t mhc_route_run(const mhc_route_args* a, void* stream) {
+  clear_error();
+  if (!a) return fail(MHC_ERR_NULLPTR, "args must be non-NULL");
+  mhc_status_t st = check_route(a->T, a->E, a->k);
+  if (st == MHC_OK) st = check_kind(a->dtype, a->score, a->renormalise, a->scale);
+  if (st != MHC_OK) return st;
+  if (a->groups < 1 || a->groups > kMostGroups || a->E % a->groups != 0)
+    return fail(MHC_ERR_PARAM_INVALID, "groups must divide E and be in [1, 32] (got %d)", (int)a->groups);
+  if (a->top_groups < 1 || a->top_groups > a->groups)
+    return fail(MHC_ERR_PARAM_INVALID, "top_groups must be in [1, groups] (got %d)", (int)a->top_groups);
+  if (a->k > a->E / a->groups * a->top_groups)
+    return fail(MHC_ERR_PARAM_INVALID, "k must be at most the experts of top_groups groups (got %lld)", (long long)a->k);
+  if (a->group_score != MHC_GROUP_MAX && a->group_score != MHC_GROUP_TOP2)
+    return fail(MHC_ERR_PARAM_INVALID, "group_score must be MHC_GROUP_MAX or MHC_GROUP_TOP2 (got %d)", (int)a->group_score);
+  if (a->T == 0) return MHC_OK;
+  if (!a->logits || !a->experts || !a->weights) return fail(MHC_ERR_NULLPTR, "logits, experts and weights are required");
+  if (!aligned(a->logits, logits_align(a->dtype, a->E)) || !aligned(a->bias, 4) || !aligned(a->experts, 4) || !aligned(a->weights, 4))
+    return fail(MHC_ERR_PARAM_INVALID, "tensors must be aligned to their elements, logits to the largest of one, two and four elements that divides a row");
+  const size_t lb = (size_t)a->T * a->E * elem_bytes(a->dtype), kb = (size_t)a->T * a->k * 4;
+  if ((st = check_apart({{"experts", a->experts, kb}, {"weights", a->weights, kb}},
+                        {{"logits", a->logits, lb}, {"bias", a->bias, (size_t)a->E * 4}})) != MHC_OK)
+    return st;
+  int sms = 0;
+  if ((st = route_device(&sms)) != MHC_OK) return st;
+  RouteArgs r = {a->logits, a->bias, a->experts, a->weights, a->T, (int)a->E, (int)a->k, a->score == MHC_SCORE_SIGMOID,
+                 a->groups, a->top_groups, a->group_score == MHC_GROUP_TOP2, a->renormalise, a->scale};
+  if (r.top_groups == r.groups) r.groups = r.top_groups = 1;             // every group stays
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == MHC_DTYPE_FP32   ? launch_route<MHC_DTYPE_FP32>(r, sms, s)
+                        : a->dtype == MHC_DTYPE_BF16 ? launch_route<MHC_DTYPE_BF16>(r, sms, s)
+                                                     : launch_route<MHC_DTYPE_FP16>(r, sms, s);
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "routing launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_route_backward_run(const mhc_route_bwd_args* a, void* stream) {
+  clear_error();
+  if (!a) return fail(MHC_ERR_NULLPTR, "args must be non-NULL");
+  mhc_status_t st = check_route(a->T, a->E, a->k);
+  if (st == MHC_OK) st = check_kind(a->dtype, a->score, a->renormalise, a->scale);
+  if (st != MHC_OK || a->T == 0) return st;
+  if (!a->logits || !a->experts || !a->grad_weights || !a->grad_logits)
+    return fail(MHC_ERR_NULLPTR, "logits, experts, grad_weights and grad_logits are required");
+  if (!aligned(a->logits, elem_bytes(a->dtype)) || !aligned(a->grad_logits, logits_align(a->dtype, a->E)) || !aligned(a->experts, 4) ||
+      !aligned(a->grad_weights, 4))
+    return fail(MHC_ERR_PARAM_INVALID, "tensors must be aligned to their elements, grad_logits to the largest of one, two and four elements that divides a row");
+  const size_t lb = (size_t)a->T * a->E * elem_bytes(a->dtype), kb = (size_t)a->T * a->k * 4;
+  if ((st = check_apart({{"grad_logits", a->grad_logits, lb}},
+                        {{"logits", a->logits, lb}, {"experts", a->experts, kb}, {"grad_weights", a->grad_weights, kb}})) != MHC_OK)
+    return st;
+  int sms = 0;
+  if ((st = route_device(&sms)) != MHC_OK) return st;
+  const RouteBwdArgs r = {a->logits, a->experts, a->grad_weights, a->grad_logits, a->T, (int)a->E, (int)a->k,
+                          a->score == MHC_SCORE_SIGMOID, a->renormalise, a->scale};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned grid = row_blocks(a->T, sms);
+  const size_t smem = (size_t)kRouteWarps * ((a->E + 3) & ~int64_t(3)) * 4;
+  if (a->dtype == MHC_DTYPE_FP32) route_backward_kernel<MHC_DTYPE_FP32><<<grid, kRouteWarps * 32, smem, s>>>(r);
+  else if (a->dtype == MHC_DTYPE_BF16) route_backward_kernel<MHC_DTYPE_BF16><<<grid, kRouteWarps * 32, smem, s>>>(r);
+  else route_backward_kernel<MHC_DTYPE_FP16><<<grid, kRouteWarps * 32, smem, s>>>(r);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "routing backward launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+mhc_status_t mhc_expert_plan_size(int64_t T, int64_t k, int64_t E, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
+  const mhc_status_t st = check_route(T, E, k);
+  if (st != MHC_OK) return st;
+  *bytes = (size_t)plan_layout(T, k, E).total * 4;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_expert_plan_rows(int64_t T, int64_t k, int64_t E, int64_t* rows) {
+  clear_error();
+  if (!rows) return fail(MHC_ERR_NULLPTR, "rows must be non-NULL");
+  const mhc_status_t st = check_route(T, E, k);
+  if (st != MHC_OK) return st;
+  *rows = plan_layout(T, k, E).cap_rows;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_expert_plan_run(int64_t T, int64_t k, int64_t E, const int32_t* experts, void* plan, size_t plan_bytes,
+                                 void* stream) {
+  clear_error();
+  mhc_status_t st = check_route(T, E, k);
+  if (st != MHC_OK) return st;
+  if (!plan || (T && !experts)) return fail(MHC_ERR_NULLPTR, "experts and plan are required");
+  if (!aligned(experts, 4) || !aligned(plan, 256))
+    return fail(MHC_ERR_PARAM_INVALID, "experts must be 4-byte and the plan 256-byte aligned");
+  const PlanLayout l = plan_layout(T, k, E);
+  if (plan_bytes < (size_t)l.total * 4)
+    return fail(MHC_ERR_PARAM_INVALID, "plan too small: %zu bytes given, %zu needed", plan_bytes, (size_t)l.total * 4);
+  if ((st = check_apart({{"plan", plan, (size_t)l.total * 4}}, {{"experts", experts, (size_t)l.slots * 4}})) != MHC_OK) return st;
+  int sms = 0;
+  if ((st = route_device(&sms)) != MHC_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const cudaError_t z = cudaMemsetAsync(plan, 0, (size_t)l.total * 4, s);
+    return z == cudaSuccess ? MHC_OK : fail(MHC_ERR_RUNTIME, "clearing the plan failed: %s", cudaGetErrorString(z));
+  }
+  PlanArgs a = {experts, plan_view(l, plan), (int)l.slots, (int)E, kPlanChunk};
+  const size_t smem = plan_smem((int)E);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024) {                        // beside the static arrays more than a kernel has by default
+    for (const void* f : {(const void*)plan_alone_kernel, (const void*)plan_count_kernel, (const void*)plan_place_kernel})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kMostExperts));
+    if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "plan kernels: %s", cudaGetErrorString(e));
+  }
+  if (l.slots <= kPlanAlone) {
+    plan_alone_kernel<<<1, kPlanThreads, smem, s>>>(a);
+  } else {
+    const int blocks = (int)((l.slots + kPlanChunk - 1) / kPlanChunk);
+    plan_count_kernel<<<blocks, kPlanThreads, smem, s>>>(a);
+    plan_sum_kernel<<<1, kPlanThreads, 0, s>>>(a, blocks);
+    plan_place_kernel<<<blocks, kPlanThreads, smem, s>>>(a);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "plan launch failed: %s", cudaGetErrorString(e));
+  return MHC_OK;
+}
+
+}  // extern "C"
