@@ -1,6 +1,6 @@
 """GB300 (sm_103a) mHC pre-mapping and post-mapping, the gated feed-forward block
-between them, each forward and backward, 8-bit activation checkpoints, and routed
-experts as the layer's body: C ABI + thin ctypes binding.
+between them, each forward and backward, 8-bit activation checkpoints, routed
+experts as the layer's body, and orthogonalised updates of its weights: C ABI + thin ctypes binding.
 
 The compute lives in ``libmhc_pre.so`` (built from ``csrc/`` by
 ``python -m mhc_hyper_connection_gb300.build``).  This package only loads it
@@ -23,12 +23,15 @@ from ._binding import (  # noqa: F401
     MhcExpertsBwdArgs, MhcRouteArgs, MhcRouteBwdArgs, mhc_expert_plan_rows, mhc_expert_plan_run, mhc_expert_plan_size,
     mhc_experts_backward_run, mhc_experts_backward_workspace_size, mhc_experts_run, mhc_experts_status,
     mhc_experts_workspace_size, mhc_route_backward_run, mhc_route_run)
+from ._binding import (  # noqa: F401
+    MhcOrthArgs, mhc_orth_run, mhc_orth_status, mhc_orth_workspace_size)
 
 _LAYER_OPS = ("Ckpt8", "ckpt8_pack", "ckpt8_restore", "hc_post_ckpt", "hc_post_backward", "gated_ffn",
               "gated_ffn_backward", "gated_ffn_workspace", "gated_ffn_status")
 
 _EXPERT_OPS = ("ExpertPlan", "Routes", "route_experts", "route_experts_backward", "expert_plan", "experts_ffn",
                "experts_ffn_backward", "experts_ffn_workspace", "experts_ffn_status")
+_UPDATE_OPS = ("NEWTON_SCHULZ", "orthogonalise", "orthogonalise_workspace", "orthogonalise_status")
 
 
 def __getattr__(name):
@@ -41,5 +44,9 @@ def __getattr__(name):
     if name in _EXPERT_OPS:
         from . import _expert_ops
         globals().update({k: getattr(_expert_ops, k) for k in _EXPERT_OPS})
+        return globals()[name]
+    if name in _UPDATE_OPS:
+        from . import _update_ops
+        globals().update({k: getattr(_update_ops, k) for k in _UPDATE_OPS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

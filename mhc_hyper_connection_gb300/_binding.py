@@ -118,6 +118,14 @@ class MhcExpertsBwdArgs(ctypes.Structure):
                 ("withhold_copy", ctypes.c_int32)]
 
 
+class MhcOrthArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("coefficients", ctypes.POINTER(ctypes.c_float)), ("x", _P), ("out", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t), ("wait_limit_us", ctypes.c_uint32),
+                ("withhold_copy", ctypes.c_int32)]
+
+
 class MhcError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -191,7 +199,10 @@ def library() -> ctypes.CDLL:
                                ("mhc_experts_backward_workspace_size", [I64] * 5 + [SZP]),
                                ("mhc_experts_run", [ctypes.POINTER(MhcExpertsArgs), _P]),
                                ("mhc_experts_backward_run", [ctypes.POINTER(MhcExpertsBwdArgs), _P]),
-                               ("mhc_experts_status", [_P, _P])):
+                               ("mhc_experts_status", [_P, _P]),
+                               ("mhc_orth_workspace_size", [I64] * 3 + [SZP]),
+                               ("mhc_orth_run", [ctypes.POINTER(MhcOrthArgs), _P]),
+                               ("mhc_orth_status", [_P, _P])):
                 f = getattr(lib, name)
                 f.argtypes = args
                 f.restype = ctypes.c_int32
@@ -430,6 +441,23 @@ def mhc_experts_backward_run(args: MhcExpertsBwdArgs, stream: int = 0) -> int:
 
 def mhc_experts_status(workspace: int = 0, stream: int = 0) -> int:
     return library().mhc_experts_status(workspace or None, stream or None)
+
+
+# ------------------------------------------------------ orthogonalised updates
+
+def mhc_orth_workspace_size(batch: int, rows: int, cols: int):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t(0)
+    st = library().mhc_orth_workspace_size(int(batch), int(rows), int(cols), ctypes.byref(n))
+    return st, n.value
+
+
+def mhc_orth_run(args: MhcOrthArgs, stream: int = 0) -> int:
+    return library().mhc_orth_run(ctypes.byref(args), stream or None)
+
+
+def mhc_orth_status(workspace: int = 0, stream: int = 0) -> int:
+    return library().mhc_orth_status(workspace or None, stream or None)
 
 
 def mhc_pre_backward_workspace_size(handle, T: int):

@@ -1,0 +1,488 @@
+// mhc_orth.cu -- orthogonalised updates (include/mhc_orth.h): norm, scaled fp16 copy,
+// and the Newton-Schulz products on the tensor cores.
+//
+// Kept in fp16 by powers of two: X as S X, S near sqrt(max(rows, cols)), so that an
+// orthogonal X has entries of size one; A as 2^12 A (its diagonal is near one, its other
+// entries as small as 2^-18); b A + c A A as a power that leaves it below 2^15 for
+// singular values up to 1.4.  Every product's epilogue applies its factors in fp32.
+// A and A A are symmetric: tiles on and below the diagonal are formed, the others
+// written from them.
+#include <math.h>
+
+#include "mhc_group_gemm.cuh"
+#include "mhc_host.cuh"
+#include "../../include/mhc_ffn.h"
+#include "../../include/mhc_orth.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kNormBlock = 32768;                // elements that one block of the norm sums at least
+constexpr int kNormMost = 512;                   // blocks of a matrix at most
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // e in [-126, 127]
+
+template <int kType>
+__device__ __forceinline__ void load8(const void* p, long long at, long long end, bool whole, float (&v)[8]) {
+  if (whole) {
+    if constexpr (kType == MHC_DTYPE_FP32) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack2<kType == MHC_DTYPE_FP16>(w[i]);
+        v[2 * i] = t.x;
+        v[2 * i + 1] = t.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0.0f;
+    if (at + i < end) {
+      if constexpr (kType == MHC_DTYPE_FP32) v[i] = static_cast<const float*>(p)[at + i];
+      else if constexpr (kType == MHC_DTYPE_BF16) v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + i]);
+      else v[i] = __half2float(static_cast<const __half*>(p)[at + i]);
+    }
+  }
+}
+
+// Sum over the block, in every thread.
+__device__ __forceinline__ double block_sum(double v, double* room) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += room[w];
+  return s;
+}
+
+// Sums of squares of one block's part of a matrix.  Eight values share a power of two
+// that brings the largest near one, so no square over- or underflows, and one fp64
+// addition (fp64 is slow here).
+template <int kType>
+__global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const void* x, long long count, bool whole, double* part) {
+  __shared__ double room[8];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
+  pdl_trigger();
+  const long long base = (long long)blockIdx.y * count, end = base + count;
+  double acc = 0.0;
+  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < count; i += (long long)gridDim.x * 2048) {
+    float v[8];
+    load8<kType>(x, base + i, end, whole, v);
+    float top = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float m = fabsf(v[j]);
+      bad |= !(m < __int_as_float(0x7F800000));
+      top = fmaxf(top, m);
+    }
+    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -126);   // of a subnormal -126
+    // v 2^-e, in two factors: 2^126 and more is not a finite power
+    const float f0 = pow2f(-(e >> 1)), f1 = pow2f(-(e - (e >> 1)));
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = v[j] * f0 * f1;
+      s = fmaf(q, q, s);
+    }
+    acc += bad ? (double)NAN : (double)s * __longlong_as_double((long long)(2 * e + 1023) << 52);
+  }
+  const double sum = block_sum(acc, room);
+  if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+}
+
+// S x / (norm + eps) in fp16, rows of `pitch`.
+template <int kType>
+__global__ void __launch_bounds__(256) orth_scale_kernel(const void* x, int rows, int cols, int pitch, bool whole,
+                                                         const double* part, int parts, float eps, double S, uint16_t* out) {
+  __shared__ double room[8];
+  pdl_trigger();
+  pdl_wait();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += 256) s += part[(size_t)blockIdx.y * parts + i];
+  const double norm = sqrt(block_sum(s, room)) + (double)eps;
+  // S / norm as f0 f1: a power and what remains, both within fp32
+  const double f = norm == 0.0 ? 0.0 : S / norm;
+  int e = 0;
+  const double m = frexp(f, &e);
+  e = min(max(e, -200), 200);
+  const float f0 = pow2f(e >> 1), f1 = (float)ldexp(m, e - (e >> 1));
+  const int groups = pitch / 8;
+  const long long base = (long long)blockIdx.y * rows, items = (long long)rows * groups;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
+    const int r = (int)(i / groups), c = (int)(i - (long long)r * groups) * 8;
+    float v[8];
+    const long long at = (base + r) * cols + c;
+    load8<kType>(x, at, at - c + cols, whole, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * f0 * f1;
+    *reinterpret_cast<uint4*>(out + (size_t)(base + r) * pitch + c) = pack8v<true>(v);
+  }
+}
+
+// Products of a batch of matrices.  kSym: A = B, tiles on and below the diagonal.
+template <bool kA, bool kB, bool kSym>
+struct OrthJob {
+  static constexpr bool kAMn = kA, kBMn = kB, kDraw = false;
+  CUtensorMap a, b;
+  GemmShape g;                   // tiles of one matrix
+  int count, per, width, kiters;
+  FastDiv by_matrix;
+
+  struct Raw {};
+  __device__ __forceinline__ void prefetch() const {
+    tma_prefetch_desc(&a);
+    tma_prefetch_desc(&b);
+  }
+  __device__ __forceinline__ int tiles() const { return count; }
+  __device__ __forceinline__ Raw fetch(int) const { return {}; }
+  __device__ __forceinline__ GTile make(int t, const Raw&) const {
+    GTile o;
+    o.e = by_matrix(t);
+    const int r = t - o.e * per;
+    if constexpr (kSym) {        // row tm begins at tm (tm + 1) / 2
+      int tm = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
+      while ((tm + 1) * (tm + 2) / 2 <= r) ++tm;
+      while (tm * (tm + 1) / 2 > r) --tm;
+      o.tm = tm;
+      o.tn = r - tm * (tm + 1) / 2;
+    } else {
+      tile_coords(g, r, o.tm, o.tn);
+    }
+    o.row0 = o.rows = o.kind = 0;
+    o.width = width;
+    o.kiters = kiters;
+    return o;
+  }
+  __device__ __forceinline__ int bytes(const GTile&) const {
+    const int half = width >> 1;
+    return kGemmOpBytes + (kB ? (half + 63) & ~63 : half) * kFfnTileK * 2;
+  }
+  __device__ __forceinline__ int steps(const GTile&, int) const { return kFfnTileK / 16; }
+  __device__ __forceinline__ uint32_t idesc(const GTile&) const { return grp_idesc(true, kA, kB, width); }
+  __device__ __forceinline__ void load(const GTile& o, int k, uint32_t sa, uint32_t sb, uint32_t bar, int rank) const {
+    const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf, n0 = o.tn * width + rank * (width >> 1);
+    if constexpr (kA) {
+      tma_load_3d_pair(sa, &a, bar, m0, k0, o.e);
+      tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, o.e);
+    } else {
+      tma_load_3d_pair(sa, &a, bar, k0, m0, o.e);
+    }
+    if constexpr (kB) {
+      tma_load_3d_pair(sb, &b, bar, n0, k0, o.e);
+      if (width > 128) tma_load_3d_pair(sb + 8192, &b, bar, n0 + 64, k0, o.e);
+    } else {
+      tma_load_3d_pair(sb, &b, bar, k0, n0, o.e);
+    }
+  }
+};
+
+// out = alpha c + beta acc.  fp16 matrices of `pitch` columns (columns behind the last
+// are never read), or with kLast the result itself.  kSym writes the tile's mirror too.
+template <bool kHasC, bool kSym, int kLast>      // kLast: 0 fp16 between products, 1 bf16 result, 2 fp16 result
+struct EpiOrth {
+  const uint16_t* c;
+  uint16_t* out;
+  int M, N, pitch;               // of c and of out but the result's, whose pitch is N
+  float alpha, beta;
+  bool whole;                    // the result's rows are 16-byte aligned
+  __device__ __forceinline__ void tile(const GTile& g, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf, int lane,
+                                       int) const {
+    constexpr bool kF16 = kLast != 1;
+    const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, n0 = g.tn * g.width, half = g.width >> 1;
+    if (m0 >= M) return;
+    const size_t plane = (size_t)g.e * M;
+    const int beg = grp * half, end = beg + half, row = min(m0 + lane, M - 1);
+#pragma unroll 1
+    for (int col = beg; col < end && n0 + col < N; col += 64) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h && (col + 32 >= end || n0 + col + 32 >= N)) break;
+        const int c0 = n0 + col + 32 * h;
+        uint4 w[4];
+        if constexpr (kHasC) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = c0 + 8 * i < pitch ? *reinterpret_cast<const uint4*>(c + (plane + row) * pitch + c0 + 8 * i)
+                                      : make_uint4(0, 0, 0, 0);
+        }
+        float v[32];
+        acc_ld32(taddr + col + 32 * h, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 t = make_float2(0.0f, 0.0f);
+            if constexpr (kHasC) t = unpack2<true>(u[j]);
+            float &x0 = v[8 * i + 2 * j], &x1 = v[8 * i + 2 * j + 1];
+            x0 = kHasC ? fmaf(beta, x0, alpha * t.x) : beta * x0;
+            x1 = kHasC ? fmaf(beta, x1, alpha * t.y) : beta * x1;
+          }
+        }
+        if constexpr (kSym) {
+          if (g.tm != g.tn)
+            store_transposed<true>(v, buf, reinterpret_cast<uint8_t*>(out + (plane + c0) * pitch + m0), (size_t)pitch * 2, N - c0,
+                                   pitch - m0, lane);
+        }
+        // rows of 64 bytes of this half
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + sw128(lane, (kSym ? 0 : h * 4) + i)) = pack8v<kF16>(v + 8 * i);
+        if constexpr (kSym)
+          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * pitch + c0), (size_t)pitch * 2, M - m0,
+                      min(32, pitch - c0) * 2, lane);
+      }
+      if constexpr (!kSym) {
+        const int cols = min(64, end - col);
+        if (kLast == 0) {
+          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * pitch + n0 + col), (size_t)pitch * 2, M - m0,
+                      min(cols, pitch - n0 - col) * 2, lane);
+        } else if (whole) {
+          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * N + n0 + col), (size_t)N * 2, M - m0,
+                      min(cols, N - n0 - col) * 2, lane);
+        } else {
+          __syncwarp();
+          const int rows = min(32, M - m0), n = min(cols, N - n0 - col);
+          for (int r = 0; r < rows; ++r) {
+            uint16_t* o = out + (plane + m0 + r) * N + n0 + col;
+#pragma unroll
+            for (int e = lane; e < 64; e += 32)
+              if (e < n) o[e] = *reinterpret_cast<const uint16_t*>(buf + sw128(r, e >> 3) + (e & 7) * 2);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+};
+
+// --------------------------------------------------------------------- host
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct OrthLayout {
+  int64_t parts, pitch, side, spitch;
+  size_t norm, x[2], p, q, total;
+};
+OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
+  OrthLayout l;
+  const int64_t count = rows * cols;
+  l.parts = (count + kNormBlock - 1) / kNormBlock;
+  if (l.parts > kNormMost) l.parts = kNormMost;
+  l.pitch = (cols + 7) & ~int64_t(7);
+  l.side = rows < cols ? rows : cols;
+  l.spitch = (l.side + 7) & ~int64_t(7);
+  const size_t xb = up256((size_t)batch * rows * l.pitch * 2), pb = up256((size_t)batch * l.side * l.spitch * 2);
+  l.norm = 256;
+  l.x[0] = l.norm + up256((size_t)batch * l.parts * 8);
+  l.x[1] = l.x[0] + xb;
+  l.p = l.x[1] + xb;
+  l.q = l.p + pb;
+  l.total = l.q + pb;
+  return l;
+}
+
+bool orth_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch, int64_t batch, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  cuuint64_t st[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(pitch * rows) * 2};
+  cuuint32_t b[3] = {64, box_rows, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Matrix {
+  void* p;
+  int64_t rows, cols, pitch;
+};
+
+// One product: out = alpha c + beta (op A)(op B)^T.
+struct Product {
+  int64_t batch, M, N, K;
+  GrpCall call;
+  int sms;
+  const uint16_t* c;
+  uint16_t* out;
+  int64_t pitch;
+  double alpha, beta;
+  bool whole;
+};
+template <bool kA, bool kB, bool kHasC, bool kSym, int kLast>
+cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* mapped, cudaStream_t s) {
+  OrthJob<kA, kB, kSym> job;
+  job.width = p.N >= 256 ? 256 : (int)(p.N + 63) / 64 * 64;
+  *mapped = orth_map(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch, kA ? kFfnBoxMn : (uint32_t)kGemmHalf) &&
+            orth_map(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)job.width / 2);
+  if (!*mapped) return cudaErrorInvalidValue;
+  GemmShape& g = job.g;
+  g = GemmShape();
+  g.tiles_m = (int)((p.M + kFfnTileM - 1) / kFfnTileM);
+  g.tiles_n = (int)((p.N + job.width - 1) / job.width);
+  g.band = 8;
+  g.by_band = FastDiv((uint32_t)(g.band * g.tiles_n));
+  g.by_rows = FastDiv((uint32_t)g.band);
+  g.by_last = FastDiv((uint32_t)(g.tiles_m % g.band ? g.tiles_m % g.band : g.band));
+  job.per = kSym ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
+  job.count = (int)(job.per * p.batch);
+  job.by_matrix = FastDiv((uint32_t)job.per);
+  job.kiters = (int)((p.K + kFfnTileK - 1) / kFfnTileK);
+  const EpiOrth<kHasC, kSym, kLast> e = {p.c, p.out, (int)p.M, (int)p.N, (int)p.pitch, (float)p.alpha, (float)p.beta, p.whole};
+  return launch_group(job, p.call, e, job.count, p.sms, true, s);
+}
+
+template <int kType>
+cudaError_t start(const mhc_orth_args& a, const OrthLayout& l, uint8_t* ws, double S, int sms, cudaStream_t s) {
+  const long long count = a.rows * a.cols;
+  const bool flat = count % 8 == 0 && aligned(a.x, 16), rows = a.cols % 8 == 0 && aligned(a.x, 16);
+  double* part = reinterpret_cast<double*>(ws + l.norm);
+  orth_norm_kernel<kType><<<dim3((unsigned)l.parts, (unsigned)a.batch), 256, 0, s>>>(reinterpret_cast<uint32_t*>(ws), a.x, count, flat, part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const long long items = a.rows * (l.pitch / 8), blocks = (items + 1023) / 1024;
+  const long long most = (8ll * sms + a.batch - 1) / a.batch;
+  cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), (unsigned)a.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, orth_scale_kernel<kType>, a.x, (int)a.rows, (int)a.cols, (int)l.pitch, rows,
+                            static_cast<const double*>(part), (int)l.parts, a.eps, S, reinterpret_cast<uint16_t*>(ws + l.x[0]));
+}
+
+}  // namespace
+}  // namespace mhc
+
+using namespace mhc;
+
+extern "C" {
+
+mhc_status_t mhc_orth_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(MHC_ERR_NULLPTR, "bytes must be non-NULL");
+  if (batch < 0 || batch > 65535) return fail(MHC_ERR_PARAM_INVALID, "batch must be in [0, 65535] (got %lld)", (long long)batch);
+  if (rows < 1 || rows > 32768 || cols < 1 || cols > 32768)
+    return fail(MHC_ERR_PARAM_INVALID, "rows and cols must be in [1, 32768] (got %lld, %lld)", (long long)rows, (long long)cols);
+  *bytes = batch ? orth_layout(batch, rows, cols).total : 0;
+  return MHC_OK;
+}
+
+mhc_status_t mhc_orth_run(const mhc_orth_args* a, void* stream) {
+  clear_error();
+  if (!a) return fail(MHC_ERR_NULLPTR, "args must be non-NULL");
+  size_t need = 0;
+  mhc_status_t st = mhc_orth_workspace_size(a->batch, a->rows, a->cols, &need);
+  if (st != MHC_OK) return st;
+  if (a->dtype != MHC_DTYPE_BF16 && a->dtype != MHC_DTYPE_FP16 && a->dtype != MHC_DTYPE_FP32)
+    return fail(MHC_ERR_PARAM_INVALID, "dtype must be MHC_DTYPE_BF16, _FP16 or _FP32 (got %d)", (int)a->dtype);
+  if (a->out_dtype != MHC_DTYPE_BF16 && a->out_dtype != MHC_DTYPE_FP16)
+    return fail(MHC_ERR_PARAM_INVALID, "out_dtype must be MHC_DTYPE_BF16 or MHC_DTYPE_FP16 (got %d)", (int)a->out_dtype);
+  if (a->steps < 1 || a->steps > 32) return fail(MHC_ERR_PARAM_INVALID, "steps must be in [1, 32] (got %d)", (int)a->steps);
+  if (!(a->eps >= 0.0f) || !isfinite(a->eps)) return fail(MHC_ERR_PARAM_INVALID, "eps must be finite and not negative");
+  if (a->wait_limit_us > 10000000u) return fail(MHC_ERR_PARAM_INVALID, "wait_limit_us must be at most 10 s");
+  if (a->withhold_copy != 0 && a->withhold_copy != 1) return fail(MHC_ERR_PARAM_INVALID, "withhold_copy must be 0 or 1");
+  if (!a->coefficients) return fail(MHC_ERR_NULLPTR, "coefficients are required");
+  for (int i = 0; i < 3 * a->steps; ++i)
+    if (!isfinite(a->coefficients[i]) || fabsf(a->coefficients[i]) > 1000.0f)
+      return fail(MHC_ERR_PARAM_INVALID, "coefficients must be finite and at most 1000 in size");
+  if (a->batch == 0) return MHC_OK;
+  if (!a->x || !a->out || !a->workspace) return fail(MHC_ERR_NULLPTR, "x, out and the workspace are required");
+  const size_t esize = a->dtype == MHC_DTYPE_FP32 ? 4 : 2, count = (size_t)a->batch * a->rows * a->cols;
+  if (!aligned(a->x, esize) || !aligned(a->out, 2) || !aligned(a->workspace, 256))
+    return fail(MHC_ERR_PARAM_INVALID, "x and out must be aligned to their elements, the workspace to 256 bytes");
+  if (a->workspace_bytes < need)
+    return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, need);
+  const OrthLayout l = orth_layout(a->batch, a->rows, a->cols);
+  const int64_t tiles = ((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
+  if (tiles > (int64_t(1) << 30)) return fail(MHC_ERR_PARAM_INVALID, "too many tiles");
+  if ((st = check_apart({{"out", a->out, count * 2}, {"workspace", a->workspace, l.total}}, {{"x", a->x, count * esize}})) != MHC_OK)
+    return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MHC_ERR_RUNTIME, "no CUDA device");
+  const DeviceInfo di = device_info(dev);
+  if (!di.ok) return fail(MHC_ERR_RUNTIME, "device %d is not an sm_103 GPU", dev);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  const int64_t m = a->rows, n = a->cols, side = l.side;
+  const bool tall = m > n;
+  const double S = ldexp(1.0, (int)lround(0.5 * log2((double)(m > n ? m : n)))), SA = 4096.0;
+  cudaError_t e = a->dtype == MHC_DTYPE_FP32   ? start<MHC_DTYPE_FP32>(*a, l, ws, S, di.sms, s)
+                  : a->dtype == MHC_DTYPE_BF16 ? start<MHC_DTYPE_BF16>(*a, l, ws, S, di.sms, s)
+                                               : start<MHC_DTYPE_FP16>(*a, l, ws, S, di.sms, s);
+  if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "orthogonalisation launch failed: %s", cudaGetErrorString(e));
+  Product p = {};
+  p.batch = a->batch;
+  p.call.err = reinterpret_cast<uint32_t*>(ws);
+  p.call.counter = nullptr;
+  p.call.wait_ns = a->wait_limit_us ? (uint64_t)a->wait_limit_us * 1000u : 2000000000ull;
+  grp_ring(&p.call, 128);
+  p.sms = di.sms;
+  Matrix A = {ws + l.p, side, side, l.spitch}, B = {ws + l.q, side, side, l.spitch};
+  for (int i = 0; i < a->steps; ++i) {
+    const double ca = a->coefficients[3 * i], cb = a->coefficients[3 * i + 1], cc = a->coefficients[3 * i + 2];
+    const double bound = fmax(2.0 * fabs(cb) + 4.0 * fabs(cc), 1.0);
+    const double SB = ldexp(1.0, (int)floor(log2(32768.0 / bound)));
+    const bool last = i + 1 == a->steps;
+    Matrix X = {ws + l.x[i & 1], m, n, l.pitch};
+    bool mapped = true;
+    p.call.withhold = 0;
+    p.M = p.N = side;
+    p.K = tall ? m : n;
+    p.c = nullptr;
+    p.out = static_cast<uint16_t*>(A.p);
+    p.pitch = l.spitch;
+    p.alpha = 0.0;
+    p.beta = SA / (S * S);
+    e = tall ? product<true, true, false, true, 0>(p, X, X, &mapped, s) : product<false, false, false, true, 0>(p, X, X, &mapped, s);
+    if (e == cudaSuccess) {
+      p.K = side;
+      p.c = static_cast<const uint16_t*>(A.p);
+      p.out = static_cast<uint16_t*>(B.p);
+      p.alpha = cb * SB / SA;
+      p.beta = cc * SB / (SA * SA);
+      e = product<false, false, true, true, 0>(p, A, A, &mapped, s);
+    }
+    if (e == cudaSuccess) {
+      p.call.withhold = last ? a->withhold_copy : 0;
+      p.M = m;
+      p.N = n;
+      p.c = static_cast<const uint16_t*>(X.p);
+      p.out = last ? static_cast<uint16_t*>(a->out) : reinterpret_cast<uint16_t*>(ws + l.x[(i + 1) & 1]);
+      p.pitch = l.pitch;
+      p.alpha = last ? ca / S : ca;
+      p.beta = last ? 1.0 / (SB * S) : 1.0 / SB;
+      p.whole = n % 8 == 0 && aligned(a->out, 16);
+      const int kind = !last ? 0 : a->out_dtype == MHC_DTYPE_BF16 ? 1 : 2;
+      if (tall)
+        e = kind == 0   ? product<false, false, true, false, 0>(p, X, B, &mapped, s)
+            : kind == 1 ? product<false, false, true, false, 1>(p, X, B, &mapped, s)
+                        : product<false, false, true, false, 2>(p, X, B, &mapped, s);
+      else
+        e = kind == 0   ? product<false, true, true, false, 0>(p, B, X, &mapped, s)
+            : kind == 1 ? product<false, true, true, false, 1>(p, B, X, &mapped, s)
+                        : product<false, true, true, false, 2>(p, B, X, &mapped, s);
+    }
+    if (!mapped) return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
+    if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "orthogonalisation launch failed: %s", cudaGetErrorString(e));
+  }
+  return MHC_OK;
+}
+
+mhc_status_t mhc_orth_status(const void* workspace, void* stream) { return mhc_ffn_status(workspace, stream); }
+
+}  // extern "C"
