@@ -46,7 +46,8 @@ inline PlanLayout plan_layout(int64_t T, int64_t k, int64_t E) {
 }
 
 // A plan on the device.  Table entry i (two int4): {expert, first entry of its band,
-// entries of the band, first row of the band}, {rows of the band, rows of a tile}.
+// entries of the band, first row of the band}, {rows of the band, rows of a tile, how many
+// of the band's first tiles have 32 more}.
 struct PlanView {
   int *head, *counts, *starts, *places, *rows, *scratch;
   int4* table;

@@ -71,13 +71,14 @@ bool map_gate_up(CUtensorMap* m, const void* base, bool f16, uint64_t D, uint64_
 }
 
 struct FwdLayout {
-  size_t xs, a, total;
+  size_t xs, a, lo, total;
 };
 FwdLayout fwd_layout(const PlanLayout& p, int64_t D, int64_t F) {
   FwdLayout l;
   l.xs = 256;
   l.a = l.xs + up256((size_t)p.cap_rows * D * 2);
-  l.total = l.a + up256((size_t)p.cap_rows * F * 2);
+  l.lo = l.a + up256((size_t)p.cap_rows * F * 2);
+  l.total = l.lo + up256((size_t)p.cap_rows * D);
   return l;
 }
 struct BwdLayout {
@@ -184,6 +185,7 @@ mhc_status_t mhc_experts_run(const mhc_experts_args* a, void* stream) {
   L.weights = a->weights;
   L.xs = ws + l.xs;
   L.a_buf = ws + l.a;
+  L.lo = ws + l.lo;
   L.y = a->y;
   L.gate_up = a->gate_up;
   if (!map_gate_up(&L.wgu, a->w_gate_up, f16, D, F, E) || !map_weights(&L.wd, a->w_down, f16, F, D, E, kGemmHalf) ||

@@ -33,10 +33,11 @@ __global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, 
 // lane; slots without a row get zeros.
 template <bool F16>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p, long long T, int k, int D, int parts,
-                                                               long long cap_rows, const uint16_t* rows, const float* part,
+                                                               long long cap_rows, const uint16_t* hi, const uint8_t* lo,
+                                                               const float* part,
                                                                uint16_t* grad_x, float* grad_weights) {
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 511) / 512;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
   const long long groups = (p.head[1] + 31) / 32;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs + groups; i += (long long)gridDim.x * 8) {
     if (i < groups) {
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p,
       }
     } else {
       const long long item = i - groups, t = item / segs;
-      combine_item<F16>(item, segs, k, D, p.places, nullptr, rows, grad_x, lane);
+      combine_item<F16>(item, segs, k, D, p.places, nullptr, hi, lo, grad_x, lane);
       if (item == t * segs && lane < k && p.places[t * k + lane] < 0) grad_weights[t * k + lane] = 0.0f;
     }
   }
@@ -82,8 +83,8 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
     job.E = L.E;
     const int M[2] = {2 * F, D}, N[2] = {D, F};
     for (int i = 0; i < 2; ++i) {
-      job.width[i] = N[i] >= 256 ? 256 : (N[i] + 63) / 64 * 64;
-      job.tiles_n[i] = (N[i] + job.width[i] - 1) / job.width[i];
+      job.tiles_n[i] = (N[i] + 255) / 256;       // of one width, a multiple of 64
+      job.width[i] = ((N[i] + job.tiles_n[i] - 1) / job.tiles_n[i] + 63) / 64 * 64;
       job.area[i] = (M[i] + kFfnTileM - 1) / kFfnTileM * job.tiles_n[i];
       job.by_n[i] = FastDiv((uint32_t)job.tiles_n[i]);
     }
@@ -93,13 +94,14 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
     e = launch_group(job, grp_call(L.call, 2, false, 128), o, (long long)L.E * (job.area[0] + job.area[1]), sms, true, s);
     if (e != cudaSuccess) return e;
   }
-  // rows of grad_x over those of x
+  // rows of grad_x over those of x and of grad_y
   const auto job = experts_job<kRowsMn, F16>(L.wgu_mn, L.gg, L.plan, D, kFfnTileM, 2 * F);
-  const EpiRows<F16> o = {static_cast<uint16_t*>(L.xs), D};
+  const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D};
   e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 511) / 512) + L.lay.cap_rows / 32 + 1, sms, true, s, L.plan, L.T, L.k,
-                     D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const float*>(L.part),
+  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, sms, true, s, L.plan, L.T, L.k,
+                     D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.gys),
+                     static_cast<const float*>(L.part),
                      static_cast<uint16_t*>(L.grad_x), L.grad_weights);
 }
 

@@ -19,11 +19,11 @@ __global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const Pla
 
 template <bool F16>
 __global__ void __launch_bounds__(256) combine_kernel(const PlanView p, long long T, int k, int D, const float* weights,
-                                                      const uint16_t* rows, uint16_t* y) {
+                                                      const uint16_t* hi, const uint8_t* lo, uint16_t* y) {
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 511) / 512;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs; i += (long long)gridDim.x * 8)
-    combine_item<F16>(i, segs, k, D, p.places, weights, rows, y, lane);
+    combine_item<F16>(i, segs, k, D, p.places, weights, hi, lo, y, lane);
 }
 
 template <bool F16, bool kKept>
@@ -40,11 +40,11 @@ cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((e = L.gate_up ? gate_up<F16, true>(L, s) : gate_up<F16, false>(L, s)) != cudaSuccess) return e;
   const auto job = experts_job<kRowsK, F16>(L.wd, L.a, L.plan, L.D, kFfnTileM, L.F);
-  const EpiRows<F16> o = {static_cast<uint16_t*>(L.xs), L.D};
+  const EpiRows o = {static_cast<uint16_t*>(L.xs), L.lo, L.D};
   e = launch_group(job, grp_call(L.call, 2, true, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 511) / 512), L.call.sms, true, s, L.plan, L.T, L.k, L.D, L.weights,
-                     static_cast<const uint16_t*>(L.xs), static_cast<uint16_t*>(L.y));
+  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), L.call.sms, true, s, L.plan, L.T, L.k, L.D, L.weights,
+                     static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.lo), static_cast<uint16_t*>(L.y));
 }
 
 }  // namespace

@@ -43,12 +43,12 @@ struct ExpertsJob {
   // Tile t: the tiles of a band share a tile of the weights one after the other.
   __device__ __forceinline__ GTile make(int t, const Raw& w) const {
     GTile g;
-    const int r = t - w.lo.y * tiles_m, j = r % w.lo.z;
+    const int r = t - w.lo.y * tiles_m, j = r % w.lo.z, off = j * w.hi.y + 32 * min(j, w.hi.z);
     g.e = w.lo.x;
     g.tm = r / w.lo.z;
     g.tn = 0;
-    g.row0 = w.lo.w + j * w.hi.y;
-    g.rows = min(w.hi.y, w.hi.x - j * w.hi.y);
+    g.row0 = w.lo.w + off;
+    g.rows = min(w.hi.y + (j < w.hi.z ? 32 : 0), w.hi.x - off);
     g.width = (g.rows + 31) & ~31;
     g.kiters = kiters;
     g.kind = 0;
@@ -133,12 +133,14 @@ struct WeightGradJob {
 
 // ------------------------------------------------------------- epilogues
 
-// out[row, m] of the accumulator's column `row` and lane m.
-template <bool F16>
+// The accumulator's column `row` and lane m as 24 bits at [row, m] of two planes.
 struct EpiRows {
-  uint16_t* out;
+  using Pre = NoPre;
+  uint16_t* hi;
+  uint8_t* lo;
   int M;
-  __device__ __forceinline__ void tile(const GTile& g, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
+  __device__ __forceinline__ void pre(const GTile&, Pre&, int, int, int, int) const {}
+  __device__ __forceinline__ void tile(const GTile& g, Pre&, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
     const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32;
     if (m0 >= M) return;
@@ -146,8 +148,8 @@ struct EpiRows {
     for (int c = grp * 32; c < g.rows; c += 64) {
       float v[32];
       acc_ld32(taddr + c, v);
-      store_transposed<F16>(v, buf, reinterpret_cast<uint8_t*>(out + (size_t)(g.row0 + c) * M + m0), (size_t)M * 2, g.rows - c,
-                            M - m0, lane);
+      const size_t at = (size_t)(g.row0 + c) * M + m0;
+      store_transposed24(v, buf, reinterpret_cast<uint8_t*>(hi + at), lo + at, (size_t)M, g.rows - c, M - m0, lane);
     }
   }
 };
@@ -156,9 +158,11 @@ struct EpiRows {
 // eight apart exchange half their columns, so that each has gate and up of sixteen.
 template <bool F16, bool kKept>
 struct EpiExpertGateUp {
+  using Pre = NoPre;
   uint16_t *a, *gate_up;
   int F, act;
-  __device__ __forceinline__ void tile(const GTile& g, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
+  __device__ __forceinline__ void pre(const GTile&, Pre&, int, int, int, int) const {}
+  __device__ __forceinline__ void tile(const GTile& g, Pre&, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
     const int f0 = g.tm * 128 + rank * 64 + q * 16;
     if (f0 >= F) return;
@@ -217,35 +221,56 @@ struct EpiExpertGateUp {
 };
 
 // acc = ga before the weight: gg, gu, w a, and this warp's 32 terms of a row's
-// sum_f a ga.  Sixteen tokens at a time; kept sums are read a row's 64 bytes per
-// instruction.
+// sum_f a ga.  Sixteen tokens at a time, whose kept sums and weights are loaded one step
+// ahead (the first before the tile's sums are there).
 template <bool F16>
 struct EpiExpertDgate {
+  struct Pre {
+    uint4 k[4];                  // piece i * 32 + lane: token / 8, gate or up / 4, eight columns
+    float w;
+  };
   const uint16_t* gate_up;
   const float* w_row;            // weight of each row
   uint16_t *gg, *wa;
   float* part;                   // [ceil(F / 32)][cap_rows]
   int F, act;
   long long cap_rows;
-  __device__ __forceinline__ void tile(const GTile& g, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
+  __device__ __forceinline__ void load(Pre& p, const GTile& g, int f0, int c, int lane) const {
+    const int rows = g.rows - c, h = (lane & 3) * 8, plane = (lane >> 2) & 1;
+    const size_t row0 = (size_t)(g.row0 + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      p.k[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows && f0 + h < F) p.k[i] = *reinterpret_cast<const uint4*>(gate_up + ((row0 + r) * 2 + plane) * F + f0 + h);
+    }
+    p.w = lane < rows && lane < 16 ? w_row[row0 + lane] : 0.0f;
+  }
+  __device__ __forceinline__ void pre(const GTile& g, Pre& p, int rank, int q, int grp, int lane) const {
+    load(p, g, g.tm * kFfnTileM + rank * kGemmHalf + q * 32, grp * 16, lane);
+  }
+  __device__ __forceinline__ void tile(const GTile& g, Pre& p, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
-    const int f0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, f = f0 + lane;
+    const int f0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32;
     if (f0 >= F) return;
-    const bool in = f < F;
+    const bool in = f0 + lane < F;
     uint16_t* st = reinterpret_cast<uint16_t*>(buf);
 #pragma unroll 1
     for (int c = grp * 16; c < g.rows; c += 32) {
       const int rows = g.rows - c;
       const size_t row0 = (size_t)(g.row0 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 32 + lane) * 16) = p.k[i];
+      const float wl = p.w;
+      if (c + 32 < g.rows) load(p, g, f0, c + 32, lane);
+      __syncwarp();
       uint16_t kz[16], ku[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const bool on = in && j < rows;
-        const uint16_t* at = gate_up + (row0 + j) * 2 * F + f;
-        kz[j] = on ? at[0] : 0;
-        ku[j] = on ? at[F] : 0;
+        kz[j] = st[j * 64 + lane];
+        ku[j] = st[j * 64 + 32 + lane];
       }
-      const float wl = lane < rows && lane < 16 ? w_row[row0 + lane] : 0.0f;
+      __syncwarp();
       float ga[16];
       tmem_ld16(taddr + c, ga);
       float dot[16];
@@ -305,11 +330,13 @@ struct EpiExpertDgate {
 // in several parts is joined in fp32 in a room of the warp's own.
 template <bool F16>
 struct EpiWeightGrad {
+  using Pre = NoPre;
   uint16_t* out[2];
   int M[2], N[2];
   float* room;                   // [CTA][warp][128 columns][32 lanes], where a sum may have parts
-  __device__ __forceinline__ void tile(const GTile& g, int p, int parts, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
-                                       int lane, int pair) const {
+  __device__ __forceinline__ void pre(const GTile&, Pre&, int, int, int, int) const {}
+  __device__ __forceinline__ void tile(const GTile& g, Pre&, int p, int parts, uint32_t taddr, int rank, int q, int grp,
+                                       uint8_t* buf, int lane, int pair) const {
     const int Mk = g.kind ? M[1] : M[0], Nk = g.kind ? N[1] : N[0];
     const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, n0 = g.tn * g.width, half = g.width >> 1;
     uint16_t* o = (g.kind ? out[1] : out[0]) + (size_t)g.e * Mk * Nk;
@@ -365,7 +392,8 @@ struct ExpertsFwdLaunch {
   int E, k, D, F, act;
   const void* x_in;
   const float* weights;
-  void *xs, *a_buf, *y, *gate_up;              // xs: rows of x, then of the experts' outputs
+  void *xs, *a_buf, *y, *gate_up;              // xs: rows of x, then the outputs' upper planes
+  uint8_t* lo;                                 // their lower planes
 };
 cudaError_t launch_experts_forward(const ExpertsFwdLaunch& L, bool f16, cudaStream_t s);
 
@@ -378,7 +406,7 @@ struct ExpertsBwdLaunch {
   int E, k, D, F, act;
   const void *grad_y, *x_in, *gate_up;
   const float* weights;
-  void *xs, *gys, *gg_buf, *wa_buf, *grad_x, *grad_w_gate_up, *grad_w_down;   // xs: then the rows of grad_x
+  void *xs, *gys, *gg_buf, *wa_buf, *grad_x, *grad_w_gate_up, *grad_w_down;   // xs, gys: then grad_x's rows
   float *w_row, *part, *grad_weights, *room;
 };
 cudaError_t launch_experts_backward(const ExpertsBwdLaunch& L, bool f16, cudaStream_t s);
@@ -424,55 +452,47 @@ cudaError_t launch_rows(K* k, long long warps, int sms, bool dependent, cudaStre
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
-// Eight columns of a 16-byte piece, scaled, onto fp32 sums.
-template <bool F16>
-__device__ __forceinline__ void add_piece(float (&s)[8], const uint4& v, float w) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = unpack2<F16>(u[i]);
-    s[2 * i] = fmaf(w, t.x, s[2 * i]);
-    s[2 * i + 1] = fmaf(w, t.y, s[2 * i + 1]);
-  }
-}
-
-// out[t] = sum_j w_tj rows[place_tj], in the order of j; w = 1 without weights.  A
-// warp takes 512 columns of a token, two pieces a lane, four experts in flight.
+// out[t] = sum_j w_tj rows[place_tj] of 24-bit rows, in the order of j; w = 1 without
+// weights.  A warp takes 256 columns of a token, eight a lane, eight experts in flight.
 template <bool F16>
 __device__ __forceinline__ void combine_item(long long item, int segs, int k, int D, const int* places, const float* weights,
-                                             const uint16_t* rows, uint16_t* out, int lane) {
+                                             const uint16_t* hi, const uint8_t* lo, uint16_t* out, int lane) {
   const long long t = item / segs;
-  const int c0 = (int)(item - t * segs) * 512 + lane * 8;
-  float s[2][8];
+  const int c0 = (int)(item - t * segs) * 256 + lane * 8;
+  float s[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[h][i] = 0.0f;
+  for (int i = 0; i < 8; ++i) s[i] = 0.0f;
   const int at = lane < k ? places[t * k + lane] : -1;
   const float wt = lane < k && weights ? weights[t * k + lane] : 1.0f;
 #pragma unroll 1
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    uint4 v[4][2];
-    float w[4];
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    uint4 v[8];
+    uint2 l[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p = j0 + j < k ? __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31) : -1;
-      w[j] = __shfl_sync(0xFFFFFFFFu, wt, (j0 + j) & 31);
-      if (p < 0) w[j] = 0.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v[j][h] = make_uint4(0, 0, 0, 0);
-        if (p >= 0 && c0 + 256 * h < D) v[j][h] = *reinterpret_cast<const uint4*>(rows + (size_t)p * D + c0 + 256 * h);
+    for (int j = 0; j < 8; ++j) {
+      const int p = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
+      v[j] = make_uint4(0, 0, 0, 0);
+      l[j] = make_uint2(0, 0);
+      if (j0 + j < k && p >= 0 && c0 < D) {
+        v[j] = __ldcs(reinterpret_cast<const uint4*>(hi + (size_t)p * D + c0));
+        l[j] = __ldcs(reinterpret_cast<const uint2*>(lo + (size_t)p * D + c0));
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j) {
+      const int p = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
+      float w = __shfl_sync(0xFFFFFFFFu, wt, (j0 + j) & 31);
+      if (j0 + j >= k || p < 0) w = 0.0f;
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) add_piece<F16>(s[h], v[j][h], w[j]);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = i < 2 ? l[j].x >> (16 * (i & 1)) : l[j].y >> (16 * (i & 1));   // two low bytes
+        s[2 * i] = fmaf(w, __uint_as_float((u[i] << 16) | ((b & 0xFFu) << 8)), s[2 * i]);
+        s[2 * i + 1] = fmaf(w, __uint_as_float((u[i] & 0xFFFF0000u) | (b & 0xFF00u)), s[2 * i + 1]);
+      }
+    }
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (c0 + 256 * h < D) *reinterpret_cast<uint4*>(out + (size_t)t * D + c0 + 256 * h) = pack8v<F16>(s[h]);
+  if (c0 < D) *reinterpret_cast<uint4*>(out + (size_t)t * D + c0) = pack8v<F16>(s);
 }
 
 // Row r of the plan's order from row slot / k of a tensor, zeros where it is padding: a

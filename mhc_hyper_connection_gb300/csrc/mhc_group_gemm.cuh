@@ -111,7 +111,8 @@ __host__ __device__ constexpr uint32_t grp_idesc(bool f16, bool a_mn, bool b_mn,
 //   uint32_t idesc(tile)
 //   void prefetch()                               tensor-map descriptors
 // Epi:
-//   void tile(tile, part, parts, taddr, rank, q, grp, buf, lane, pair)
+//   Pre, void pre(tile, Pre&, rank, q, grp, lane)   loads ahead of a tile's sums
+//   void tile(tile, Pre&, part, parts, taddr, rank, q, grp, buf, lane, pair)
 template <class Job, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     group_gemm_kernel(const __grid_constant__ Job job, const GrpCall call, const __grid_constant__ Epi epi) {
@@ -214,18 +215,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         mbar_arrive_remote(&tail->sched_full[slot], 1);
         return true;
       };
-      auto draw = [&]() -> int {
-        const unsigned t = (unsigned)pairs + atomicAdd(call.counter, 1u);
-        return t < (unsigned)ntiles ? (int)t : -1;
-      };
+      // The first two tiles of a pair are dealt out, the others drawn: the number of tile
+      // n + 3 and what tile n + 2 needs from memory are on their way under tile n's copies,
+      // so that neither latency stands before a copy (weight gradients of short tiles).
+      auto draw = [&]() -> long long { return 2ll * pairs + atomicAdd(call.counter, 1u); };
       GTile none, cur, next;
       none.e = -1;
       none.tm = none.tn = none.row0 = none.rows = none.width = none.kiters = none.kind = 0;
       cur = next = none;
+      long long drawn = ntiles;
       if (Job::kDraw && rank == 0) {
-        if (pair < ntiles) cur = job.make(pair, job.fetch(pair));
-        const int t = cur.e >= 0 ? draw() : -1;
-        if (t >= 0) next = job.make(t, job.fetch(t));
+        const int t0 = pair, t1 = pair + pairs;
+        typename Job::Raw r0, r1;
+        if (t0 < ntiles) r0 = job.fetch(t0);
+        if (t1 < ntiles) r1 = job.fetch(t1);
+        if (t1 < ntiles) drawn = draw();
+        if (t0 < ntiles) cur = job.make(t0, r0);
+        if (t1 < ntiles) next = job.make(t1, r1);
         ok = publish(0, cur) && publish(1, next);
       }
       for (int n = 0; ok; ++n) {
@@ -234,15 +240,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int bytes = job.bytes(g);
         // test hook, as in ffn_gemm_kernel
         const int kend = call.withhold && pair < 2 && n == 0 ? max(g.kiters - 1 - (int)(rank ^ (uint32_t)pair), 0) : g.kiters;
-        // tile n + 2 is drawn under this tile's copies, and what it needs from
-        // memory fetched under them
-        int after = -1;
+        const long long after = drawn;
         typename Job::Raw raw;
-        const bool more = Job::kDraw && rank == 0 && next.e >= 0;
-        if (more) after = draw();
         const int half = kend >> 1;
+        if (Job::kDraw && rank == 0 && after < ntiles) drawn = draw();
         for (int k = 0; k < kend; ++k) {
-          if (k == half && after >= 0) raw = job.fetch(after);
+          if (k == half && after < ntiles) raw = job.fetch((int)after);
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + s * stage_bytes);
           if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * (uint32_t)bytes);
@@ -253,9 +256,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
         ok = ok && kend == g.kiters;
         if (Job::kDraw && rank == 0 && ok) {
-          if (kend == 0 && after >= 0) raw = job.fetch(after);
+          if (kend == 0 && after < ntiles) raw = job.fetch((int)after);
           GTile g2 = none;
-          if (after >= 0) g2 = job.make(after, raw);
+          if (after < ntiles) g2 = job.make((int)after, raw);
           ok = publish(n + 2, g2);
           cur = next;
           next = g2;
@@ -322,12 +325,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const GTile g = tile_of(n, true);
       if (g.e < 0) break;
       const int parts = (g.kiters + kGrpDeepest - 1) / kGrpDeepest;
-      if (parts == 0) epi.tile(g, 0, 0, 0u, (int)rank, q, grp, buf, lane, pair);
+      typename Epi::Pre pre;
+      epi.pre(g, pre, (int)rank, q, grp, lane);
+      if (parts == 0) epi.tile(g, pre, 0, 0, 0u, (int)rank, q, grp, buf, lane, pair);
       for (int p = 0; p < parts; ++p, ++acc) {
         const int b = acc & 1;
         if (!__all_sync(0xFFFFFFFFu, wait_stage(&tail->acc_full[b], (uint32_t)(acc >> 1) & 1u, ctl))) { ok = false; break; }
         tc_fence_after();
-        epi.tile(g, p, parts, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN), (int)rank, q, grp, buf, lane,
+        epi.tile(g, pre, p, parts, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kFfnTileN), (int)rank, q, grp, buf, lane,
                  pair);
         tc_fence_before();
         __syncwarp();
@@ -387,6 +392,43 @@ inline void grp_ring(GrpCall* c, int b_rows) {
 }
 
 // ------------------------------------------------ epilogues' shared pieces
+
+// Nothing to load ahead.
+struct NoPre {};
+
+// 24 bits of an fp32 value, rounded to nearest: what a row of an expert's outputs keeps
+// until a token's are added up, in a 16-bit and an 8-bit plane.  (Rounded to 16 bits
+// these rows were half of a result's error: 1.7 instead of 1.4 times what its own
+// rounding leaves.  In fp32 they would cost a third more traffic.)
+__device__ __forceinline__ uint32_t round24(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (b & 0x7F800000u) == 0x7F800000u ? b : b + 0x80u;
+}
+// store_transposed for these planes: rows of 64 and of 32 bytes.
+__device__ __forceinline__ void store_transposed24(const float (&v)[32], uint8_t* buf, uint8_t* hi, uint8_t* lo, size_t pitch,
+                                                   int rows, int n, int lane) {
+  uint16_t* st = reinterpret_cast<uint16_t*>(buf);
+  uint8_t* sl = buf + 2048;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t w = round24(v[j]);
+    st[j * 32 + lane] = (uint16_t)(w >> 16);
+    sl[j * 32 + lane] = (uint8_t)(w >> 8);
+  }
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + c * 16);
+    const uint2 l = *reinterpret_cast<const uint2*>(sl + r * 32 + c * 8);
+    if (r < rows && c * 8 < n) {
+      *reinterpret_cast<uint4*>(hi + (size_t)r * pitch * 2 + c * 16) = w;
+      *reinterpret_cast<uint2*>(lo + (size_t)r * pitch + c * 8) = l;
+    }
+  }
+  __syncwarp();
+}
 
 // Thirty-two columns of the warp's accumulator lanes as the transposed rows of a
 // matrix: column j is row j of it, the lanes 32 consecutive elements.  Staged as

@@ -66,9 +66,10 @@ __device__ __forceinline__ double block_sum(double v, double* room) {
   return s;
 }
 
-// Sums of squares of one block's part of a matrix.  Eight values share a power of two
-// that brings the largest near one, so no square over- or underflows, and one fp64
-// addition (fp64 is slow here).
+// Sums of squares of one block's part of a matrix.  Sixty-four values of a thread share a
+// power of two that brings the largest near one, so no square over- or underflows, and
+// one fp64 addition (with eight values each the fp64 units were the bound: 80 us for 184
+// MB).
 template <int kType>
 __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const void* x, long long count, bool whole, double* part) {
   __shared__ double room[8];
@@ -76,27 +77,42 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const 
   pdl_trigger();
   const long long base = (long long)blockIdx.y * count, end = base + count;
   double acc = 0.0;
-  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < count; i += (long long)gridDim.x * 2048) {
-    float v[8];
-    load8<kType>(x, base + i, end, whole, v);
-    float top = 0.0f;
+  for (long long i0 = (long long)blockIdx.x * 16384 + threadIdx.x * 8; i0 < count; i0 += (long long)gridDim.x * 16384) {
+    float v[8][8], top = 0.0f;
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float m = fabsf(v[j]);
-      bad |= !(m < __int_as_float(0x7F800000));
-      top = fmaxf(top, m);
+    for (int b = 0; b < 8; ++b) {
+      const long long i = i0 + b * 2048;
+      if (i < count) {
+        load8<kType>(x, base + i, end, whole, v[b]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[b][j] = 0.0f;
+      }
     }
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = fabsf(v[b][j]);
+        bad |= !(m < __int_as_float(0x7F800000));
+        top = fmaxf(top, m);
+      }
     const int e = max((int)(__float_as_uint(top) >> 23) - 127, -126);   // of a subnormal -126
     // v 2^-e, in two factors: 2^126 and more is not a finite power
     const float f0 = pow2f(-(e >> 1)), f1 = pow2f(-(e - (e >> 1)));
-    float s = 0.0f;
+    float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float q = v[j] * f0 * f1;
-      s = fmaf(q, q, s);
-    }
-    acc += bad ? (double)NAN : (double)s * __longlong_as_double((long long)(2 * e + 1023) << 52);
+    for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = v[b][j] * f0 * f1;
+        s[j] = fmaf(q, q, s[j]);
+      }
+    const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    acc += bad ? (double)NAN : (double)sum * __longlong_as_double((long long)(2 * e + 1023) << 52);
   }
   const double sum = block_sum(acc, room);
   if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
@@ -197,13 +213,30 @@ struct EpiOrth {
   int M, N, pitch;               // of c and of out but the result's, whose pitch is N
   float alpha, beta;
   bool whole;                    // the result's rows are 16-byte aligned
-  __device__ __forceinline__ void tile(const GTile& g, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf, int lane,
-                                       int) const {
+  // c of two steps of 32 columns, the first two loaded before the tile's sums are there
+  struct Pre {
+    uint4 w[2][4];
+  };
+  __device__ __forceinline__ void load(Pre& p, int h, const GTile& g, int m0, int c0, int lane) const {
+    const uint16_t* at = c + ((size_t)g.e * M + min(m0 + lane, M - 1)) * pitch + c0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p.w[h][i] = c0 < N && c0 + 8 * i < pitch ? *reinterpret_cast<const uint4*>(at + 8 * i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void pre(const GTile& g, Pre& p, int rank, int q, int grp, int lane) const {
+    if constexpr (kHasC) {
+      const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, half = g.width >> 1, c0 = g.tn * g.width + grp * half;
+      load(p, 0, g, m0, c0, lane);
+      load(p, 1, g, m0, half > 32 ? c0 + 32 : N, lane);
+    }
+  }
+  __device__ __forceinline__ void tile(const GTile& g, Pre& ahead, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
+                                       int lane, int) const {
     constexpr bool kF16 = kLast != 1;
     const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, n0 = g.tn * g.width, half = g.width >> 1;
     if (m0 >= M) return;
     const size_t plane = (size_t)g.e * M;
-    const int beg = grp * half, end = beg + half, row = min(m0 + lane, M - 1);
+    const int beg = grp * half, end = beg + half;
 #pragma unroll 1
     for (int col = beg; col < end && n0 + col < N; col += 64) {
 #pragma unroll
@@ -213,9 +246,8 @@ struct EpiOrth {
         uint4 w[4];
         if constexpr (kHasC) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = c0 + 8 * i < pitch ? *reinterpret_cast<const uint4*>(c + (plane + row) * pitch + c0 + 8 * i)
-                                      : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 4; ++i) w[i] = ahead.w[h][i];
+          load(ahead, h, g, m0, col + 64 + 32 * h < end ? c0 + 64 : N, lane);
         }
         float v[32];
         acc_ld32(taddr + col + 32 * h, v);

@@ -27,18 +27,30 @@ struct RouteArgs {
   float scale;
 };
 
-// fp32 and fp64 as unsigned numbers of the same order, NaN above all.  -inf (an
-// expert that is out) is kOut.
-__device__ __forceinline__ uint32_t order32(float v) {
+// fp32 and fp64 as unsigned numbers of the same order, NaN above all; and back.
+__device__ __forceinline__ uint32_t order(float v) {
   const uint32_t b = __float_as_uint(v);
   return v != v ? 0xFFFFFFFFu : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ unsigned long long order64(double v) {
+__device__ __forceinline__ unsigned long long order(double v) {
   const unsigned long long b = (unsigned long long)__double_as_longlong(v);
   return v != v ? ~0ull : b ^ ((b >> 63) ? ~0ull : 1ull << 63);
 }
-constexpr uint32_t kOut32 = 0x007FFFFFu;                       // order32(-inf)
-constexpr unsigned long long kOut64 = 0x000FFFFFFFFFFFFFull;   // order64(-inf)
+__device__ __forceinline__ float unorder(uint32_t u) {
+  return u == 0xFFFFFFFFu ? NAN : __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+template <class K>
+struct Ordered;
+template <>
+struct Ordered<float> {
+  using U = uint32_t;
+  static constexpr U kOut = 0x007FFFFFu;                   // order(-inf): an expert that is out
+};
+template <>
+struct Ordered<double> {
+  using U = unsigned long long;
+  static constexpr U kOut = 0x000FFFFFFFFFFFFFull;
+};
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
@@ -65,93 +77,151 @@ __device__ __forceinline__ float load_logit(const void* p, long long at) {
   else return __half2float(static_cast<const __half*>(p)[at]);
 }
 
-// The whole choice once more with keys in fp64, for rows where fp32 left two keys
-// too close to order: one in a thousand of ordinary rows with a bias.  keys: E
-// doubles of this warp.  Lane j < k returns the j-th expert (or -1).
-template <int kType>
-__device__ __noinline__ int choose64(const RouteArgs& a, long long row, double* keys, int lane) {
-  const int E = a.E;
-  double top = -INFINITY;
-  for (int e = lane; e < E; e += 32) {
-    const double l = load_logit<kType>(a.logits, row * E + e);
-    if (l > top) top = l;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double v = __shfl_xor_sync(kFull, top, o);
-    if (v > top) top = v;
-  }
-  double sum = 0.0;
-  if (!a.sigmoid) {
-    for (int e = lane; e < E; e += 32) {
-      const double l = load_logit<kType>(a.logits, row * E + e);
-      if (l != -INFINITY) sum += exp(l - top);
-    }
-    sum = warp_sum(sum);
-  }
-  for (int e = lane; e < E; e += 32) {
-    const double l = load_logit<kType>(a.logits, row * E + e);
-    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
-    keys[e] = l == -INFINITY ? -INFINITY : a.bias ? s + (double)a.bias[e] : s;
-  }
-  __syncwarp();
-  const int per = E / a.groups;
+// The choice from keys of type K: experts lane * V + i are a lane's.  Returns, in lane j <
+// k, the j-th expert (or -1) and its logit.  With K = float, `unsure` is set where two
+// keys that decide something are so close that they may stand in the wrong order: closer
+// than tol (smax + max(|a|, |b|)), smax the largest score.  room: E values of this warp.
+template <class K, int V>
+__device__ __forceinline__ int choose(const RouteArgs& a, const float (&l)[V], const K (&key)[V], float smax, float tol, K* room,
+                                      int lane, bool& unsure, float& myl) {
+  using U = typename Ordered<K>::U;
+  constexpr U kOut = Ordered<K>::kOut;
+  constexpr bool kCheck = sizeof(K) == 4;
+  const int E = a.E, k = a.k, e0 = lane * V, per = E / a.groups;
+  const bool by_key = a.bias != nullptr;
   uint32_t stays = kFull;
   if (a.groups > 1) {
-    unsigned long long mark = 0;
-    if (lane < a.groups) {
-      unsigned long long one = kOut64;
-      double best = -INFINITY, next = -INFINITY;
-      for (int i = 0; i < per; ++i) {
-        const double v = keys[lane * per + i];
-        const unsigned long long u = order64(v);
-        if (u > one) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) room[e0 + i] = key[i];
+    __syncwarp();
+    K best = (K)-INFINITY, next = (K)-INFINITY;
+    // as many lanes as there are for a group, each with every so many-th expert
+    int span = 32 / a.groups;
+    span = 1 << (31 - __clz(span));
+    const int g = lane / span, off = lane - g * span;
+    if (g < a.groups) {
+      // started at different places, so that the lanes' reads spread over the banks
+      const int n = (per - off + span - 1) / span;
+      int at = n > 0 ? g % n : 0;
+      for (int i = 0; i < n; ++i) {
+        const K v = room[g * per + off + at * span];
+        if (order(v) > order(best)) {
           next = best;
           best = v;
-          one = u;
-        } else if (order64(v) > order64(next)) {
+        } else if (order(v) > order(next)) {
           next = v;
         }
+        if (++at == n) at = 0;
       }
-      mark = order64(a.top2 && next != -INFINITY ? best + next : best);
     }
+    for (int o = 1; o < span; o <<= 1) {
+      const K b2 = __shfl_xor_sync(kFull, best, o), n2 = __shfl_xor_sync(kFull, next, o);
+      if (order(b2) > order(best)) {
+        next = order(best) > order(n2) ? best : n2;
+        best = b2;
+      } else {
+        next = order(b2) > order(next) ? b2 : next;
+      }
+    }
+    const K m = a.top2 && next != (K)-INFINITY ? best + next : best;
+    const K mark = __shfl_sync(kFull, m, min(lane * span, 31));          // group g's in lane g
+    U u = lane < a.groups ? order(mark) : (U)0;
+    K last = 0;
     stays = 0;
-    for (int g = 0; g < a.top_groups; ++g) {
-      const unsigned long long m = warp_max(mark);
-      const uint32_t who = __ballot_sync(kFull, mark == m && lane < a.groups && !((stays >> lane) & 1u));
-      const int w = __ffs(who) - 1;
+    for (int i = 0; i < a.top_groups; ++i) {
+      const U mu = warp_max(u);
+      const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
       stays |= 1u << w;
-      if (lane == w) mark = 0;
+      if (lane == w) u = 0;
+      last = __shfl_sync(kFull, mark, w);
     }
+    if constexpr (kCheck) {                      // a group left out whose mark is close to the last one taken
+      const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != -INFINITY;
+      unsure = __any_sync(kFull, left && last - mark <= 2.0f * tol * (smax + fabsf(last)));
+    }
+  }
+  U u[V], best = kOut;
+  int grp = a.groups > 1 ? e0 / per : 0, grp_end = (grp + 1) * per;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (e0 + i >= grp_end) {
+      ++grp;
+      grp_end += per;
+    }
+    const bool in = e0 + i < E && ((stays >> (grp & 31)) & 1u) && l[i] != -INFINITY;
+    u[i] = in ? order(by_key ? key[i] : (K)l[i]) : kOut;
+    best = u[i] > best ? u[i] : best;
   }
   int mine = -1;
-  // without a bias the order within the groups that stay is that of the logits
-  unsigned long long taken_key = ~0ull;
-  int taken = -1;
-  for (int j = 0; j < a.k; ++j) {
-    // the next in order after (taken_key, taken): largest key, then lowest index
-    unsigned long long best = kOut64;
-    int at = E;
-    for (int e = lane; e < E; e += 32) {
-      if (!((stays >> (e / per)) & 1u) && a.groups > 1) continue;
-      const double l = load_logit<kType>(a.logits, row * E + e);
-      const unsigned long long u = a.bias ? order64(keys[e]) : order64(l);
-      if (u == kOut64 || l == -INFINITY) continue;
-      if (j && (u > taken_key || (u == taken_key && e <= taken))) continue;
-      if (u > best) {
-        best = u;
-        at = e;
+  myl = -INFINITY;
+  float prev = 0.0f, prevl = 0.0f;
+  int preve = 0;
+  const int rounds = kCheck && by_key ? k + 1 : k;
+  for (int j = 0; j < rounds; ++j) {
+    const U m = warp_max(best);
+    if (m == kOut) break;
+    const int w = __ffs(__ballot_sync(kFull, best == m)) - 1;
+    int e = 0;
+    float le = 0.0f;
+    if (lane == w) {
+      bool done = false;
+      best = kOut;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!done && u[i] == m) {
+          done = true;
+          u[i] = kOut;
+          e = e0 + i;
+          le = l[i];
+        }
+        best = u[i] > best ? u[i] : best;
       }
     }
-    const unsigned long long m = warp_max(best);
-    if (m == kOut64) break;
-    const int e = (int)__reduce_min_sync(kFull, best == m ? (unsigned)at : (unsigned)E);
-    if (lane == j) mine = e;
-    taken_key = m;
-    taken = e;
+    e = __shfl_sync(kFull, e, w);
+    le = __shfl_sync(kFull, le, w);
+    if constexpr (kCheck) {
+      if (by_key) {
+        const float kv = unorder((uint32_t)m);
+        // equal numbers in give equal keys: the index decides, nothing to look at
+        if (j && prev - kv <= tol * (smax + fmaxf(fabsf(prev), fabsf(kv))) && !(le == prevl && a.bias[e] == a.bias[preve])) unsure = true;
+        prev = kv;
+        prevl = le;
+        preve = e;
+      }
+    }
+    if (lane == j && j < k) {
+      mine = e;
+      myl = le;
+    }
   }
-  __syncwarp();
   return mine;
+}
+
+// The choice once more with keys in fp64, for rows where fp32 left two keys too close: some
+// of a thousand of ordinary rows with a bias or groups.
+template <int V>
+__device__ __noinline__ int choose64(const RouteArgs& a, const float* logits, float top, double* room, int lane, float* myl) {
+  const int e0 = lane * V;
+  float l[V];
+  double key[V], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    l[i] = logits[i];
+    const double x = l[i];
+    key[i] = l[i] == -INFINITY ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top);
+    sum += key[i];
+  }
+  if (!a.sigmoid) sum = warp_sum(sum);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (!a.sigmoid) key[i] /= sum;
+    if (a.bias && e0 + i < a.E) key[i] += (double)a.bias[e0 + i];
+    if (l[i] == -INFINITY) key[i] = -INFINITY;
+  }
+  bool unsure = false;
+  return choose<double, V>(a, l, key, 0.0f, 0.0f, room, lane, unsure, *myl);
 }
 
 // V: consecutive scores of a lane.
@@ -159,9 +229,8 @@ template <int kType, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
   extern __shared__ double route_keys[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = a.E, k = a.k, e0 = lane * V, per = E / a.groups;
+  const int E = a.E, k = a.k, e0 = lane * V;
   double* keys64 = route_keys + (size_t)warp * E;
-  float* keys32 = reinterpret_cast<float*>(keys64);
   for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
     float l[V];
     const long long base = row * E + e0;
@@ -199,153 +268,54 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
       for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_logit<kType>(a.logits, base + i) : -INFINITY;
     }
     // Scores; softmax: top and sum of the row.
-    uint32_t topu = kOut32;
+    uint32_t topu = Ordered<float>::kOut;
 #pragma unroll
-    for (int i = 0; i < V; ++i) topu = max(topu, order32(l[i]));
+    for (int i = 0; i < V; ++i) topu = max(topu, order(l[i]));
     topu = warp_max(topu);
-    const float top = topu == 0xFFFFFFFFu ? NAN : __uint_as_float(topu ^ ((topu >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-    const bool by_key = a.bias != nullptr;
-    const bool scores = by_key || a.groups > 1;
+    const float top = topu == Ordered<float>::kOut ? 0.0f : unorder(topu);
+    const bool scores = a.bias != nullptr || a.groups > 1;
     float sum = 0.0f, smax = 1.0f;
     float key[V];
     if (a.sigmoid) {
       if (scores) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = l[i] == -INFINITY ? -INFINITY : sigmoid32(l[i]);
+        for (int i = 0; i < V; ++i) key[i] = sigmoid32(l[i]);
       }
     } else {
-      const float shift = topu == kOut32 ? 0.0f : top;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        key[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - shift);
+        key[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
         sum += key[i];
       }
       sum = warp_sum(sum);
-      smax = 1.0f / sum;
       if (scores) {
+        smax = 1.0f / sum;
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = l[i] == -INFINITY ? -INFINITY : key[i] / sum;
+        for (int i = 0; i < V; ++i) key[i] = key[i] / sum;
       }
     }
-    if (by_key) {
+    if (scores) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i < E) key[i] += a.bias[e0 + i];
+      for (int i = 0; i < V; ++i) {
+        if (a.bias && e0 + i < E) key[i] += a.bias[e0 + i];
+        if (l[i] == -INFINITY) key[i] = -INFINITY;
+      }
     }
-    // Two keys a and b closer than 2^-19 (smax + max(|a|, |b|)) may stand in the
-    // wrong order: a score is off by a few 2^-24 of itself (softmax: of the largest,
-    // from the rounding of l - top, too), the sum with the bias by 2^-24 of itself.
+    // How far two keys may be off against one another, of the largest score and their own
+    // size: a sigmoid by 2^-22 of itself, a softmax's by its exponential and the rounding
+    // of l - top (2^-22 of the largest) and its sum (V + 5 roundings, the same for all),
+    // the sum with the bias by 2^-24 of itself; twice that.
+    const float tol = a.sigmoid ? 0x1p-20f : (V + 16) * 0x1p-23f;
     bool unsure = false;
-    uint32_t stays = kFull;
-    if (a.groups > 1) {
-      // marks: lane g has group g's best keys
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i < E) keys32[e0 + i] = key[i];
-      __syncwarp();
-      float best = -INFINITY, next = -INFINITY;
-      // as many lanes as there are for a group, each with every so many-th expert
-      int span = 32 / a.groups;
-      span = 1 << (31 - __clz(span));
-      const int g = lane / span, off = lane - g * span;
-      if (g < a.groups) {
-        // start at different places, so that the lanes' reads spread over the banks
-        const int n = (per - off + span - 1) / span;
-        for (int i = 0; i < n; ++i) {
-          int at = i + g;
-          at -= at >= n ? (at / n) * n : 0;
-          const float v = keys32[g * per + off + at * span];
-          if (order32(v) > order32(best)) {
-            next = best;
-            best = v;
-          } else if (order32(v) > order32(next)) {
-            next = v;
-          }
-        }
-      }
-      for (int o = 1; o < span; o <<= 1) {
-        const float b2 = __shfl_xor_sync(kFull, best, o), n2 = __shfl_xor_sync(kFull, next, o);
-        if (order32(b2) > order32(best)) {
-          next = order32(best) > order32(n2) ? best : n2;
-          best = b2;
-        } else {
-          next = order32(b2) > order32(next) ? b2 : next;
-        }
-      }
-      const float m = a.top2 && next != -INFINITY ? best + next : best;
-      // group g's mark in lane g
-      const float mark = __shfl_sync(kFull, m, min(lane * span, 31));
-      uint32_t u = lane < a.groups ? order32(mark) : 0u;
-      float last = 0.0f;
-      stays = 0;
-      for (int i = 0; i < a.top_groups; ++i) {
-        const uint32_t mu = warp_max(u);
-        const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
-        stays |= 1u << w;
-        if (lane == w) u = 0u;
-        last = __shfl_sync(kFull, mark, w);
-      }
-      // a group left out whose mark is close to the last one taken
-      const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != -INFINITY;
-      unsure = __any_sync(kFull, left && last - mark <= 0x1p-18f * (smax + fabsf(last)));
-    }
-    // Choice: k + 1 rounds.
-    uint32_t u[V], best = kOut32;
-    int grp = a.groups > 1 ? e0 / per : 0, grp_end = (grp + 1) * per;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (e0 + i >= grp_end) {
-        ++grp;
-        grp_end += per;
-      }
-      const bool in = e0 + i < E && ((stays >> (grp & 31)) & 1u);
-      u[i] = in ? order32(by_key ? key[i] : l[i]) : kOut32;
-      if (l[i] == -INFINITY) u[i] = kOut32;
-      best = max(best, u[i]);
-    }
-    int mine = -1;
-    float prev = 0.0f, prevbias = 0.0f, prevl = 0.0f, myl = -INFINITY;
-    const int rounds = by_key ? k + 1 : k;
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t m = warp_max(best);
-      if (m == kOut32) break;
-      const int w = __ffs(__ballot_sync(kFull, best == m)) - 1;
-      int e = 0;
-      float le = 0.0f;
-      if (lane == w) {
-        bool done = false;
-        best = kOut32;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (!done && u[i] == m) {
-            done = true;
-            u[i] = kOut32;
-            e = e0 + i;
-            le = l[i];
-          }
-          best = max(best, u[i]);
-        }
-      }
-      e = __shfl_sync(kFull, e, w);
-      le = __shfl_sync(kFull, le, w);
-      if (by_key) {
-        const float kv = m == 0xFFFFFFFFu ? NAN : __uint_as_float(m ^ ((m >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-        const float bv = a.bias[e];
-        // equal numbers in give equal keys: the index decides, nothing to look at
-        if (j && prev - kv <= 0x1p-19f * (smax + fmaxf(fabsf(prev), fabsf(kv))) && !(le == prevl && bv == prevbias)) unsure = true;
-        prev = kv;
-        prevbias = bv;
-        prevl = le;
-      }
-      if (lane == j && j < k) {
-        mine = e;
-        myl = le;
-      }
-    }
+    float myl;
+    int mine = choose<float, V>(a, l, key, smax, tol, reinterpret_cast<float*>(keys64), lane, unsure, myl);
     if (unsure) {
-      mine = choose64<kType>(a, row, keys64, lane);
-      myl = mine >= 0 ? load_logit<kType>(a.logits, row * E + mine) : -INFINITY;
+      float kept[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) kept[i] = l[i];
+      float chosen;
+      mine = choose64<V>(a, kept, top, keys64, lane, &chosen);
+      myl = chosen;
     }
     // Weights: lane j has slot j.
     float w;
@@ -589,12 +559,12 @@ __device__ __forceinline__ void plan_finish(const PlanArgs& a, int count, int* s
       if (tile_at[mid] <= i) lo = mid;
       else hi = mid - 1;
     }
-    const int n = (count_at[lo] + width - 1) / width, j = i - tile_at[lo], band = j / kPlanBand * kPlanBand;
-    // tiles of one width, the last may have fewer rows
-    const int w = ((count_at[lo] + n - 1) / n + 31) & ~31;
-    const int in_band = min(kPlanBand, n - band), first = band * w;
+    // tiles of one expert differ by 32 rows at most
+    const int units = (count_at[lo] + 31) >> 5, n = (count_at[lo] + width - 1) / width, base = units / n, wide = units - base * n;
+    const int j = i - tile_at[lo], band = j / kPlanBand * kPlanBand, in_band = min(kPlanBand, n - band);
+    const int first = 32 * (band * base + min(band, wide)), w = min(max(wide - band, 0), in_band);
     a.p.table[2 * i] = make_int4(lo, tile_at[lo] + band, in_band, start_at[lo] + first);
-    a.p.table[2 * i + 1] = make_int4(min(in_band * w, count_at[lo] - first), w, 0, 0);
+    a.p.table[2 * i + 1] = make_int4(min(32 * (in_band * base + w), count_at[lo] - first), 32 * base, w, 0);
   }
 }
 // Rows of the block's slots: base[e] + what lies before them.

@@ -200,10 +200,11 @@ def test_plan(cuda_device, T, k, E):
         # tiles cover each expert's rows once
         table = words[64 + up(E) + up(E + 1):][:8 * words[2]].reshape(-1, 8)
         seen = np.zeros(len(rows), int)
-        for i, (x, first, n, row, n_rows, w, _, _) in enumerate(table):
+        for i, (x, first, n, row, n_rows, w, wide, _) in enumerate(table):
             j = i - first
-            assert 0 <= j < n <= 8 and w % 32 == 0 and w <= width
-            b, m = row + j * w, min(w, n_rows - j * w)
+            assert 0 <= j < n <= 8 and w % 32 == 0 and w + (32 if wide else 0) <= width
+            off = j * w + 32 * min(j, wide)
+            b, m = row + off, min(w + (32 if j < wide else 0), n_rows - off)
             assert m > 0
             seen[b:b + m] += 1
             assert (e.cpu().numpy().reshape(-1)[rows[b:b + m]] == x).all()
