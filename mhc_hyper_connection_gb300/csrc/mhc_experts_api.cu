@@ -78,7 +78,7 @@ FwdLayout fwd_layout(const PlanLayout& p, int64_t D, int64_t F) {
   l.xs = 256;
   l.a = l.xs + up256((size_t)p.cap_rows * D * 2);
   l.lo = l.a + up256((size_t)p.cap_rows * F * 2);
-  l.total = l.lo + up256((size_t)p.cap_rows * D);
+  l.total = l.lo + up256((size_t)p.cap_rows * rows_low_pitch((int)D));
   return l;
 }
 struct BwdLayout {

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, 
 // lane; slots without a row get zeros.
 template <bool F16>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p, long long T, int k, int D, int parts,
-                                                               long long cap_rows, const uint16_t* hi, const uint8_t* lo,
+                                                               long long cap_rows, const uint16_t* hi, const uint8_t* lo, int lo_pitch,
                                                                const float* part,
                                                                uint16_t* grad_x, float* grad_weights) {
   pdl_wait();
@@ -51,10 +51,18 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p,
       }
     } else {
       const long long item = i - groups, t = item / segs;
-      combine_item<F16>(item, segs, k, D, p.places, nullptr, hi, lo, grad_x, lane);
+      combine_item<F16>(item, segs, k, D, p.places, nullptr, hi, lo, lo_pitch, grad_x, lane);
       if (item == t * segs && lane < k && p.places[t * k + lane] < 0) grad_weights[t * k + lane] = 0.0f;
     }
   }
+}
+
+template <bool F16, int kAct>
+cudaError_t gate_gradients(const ExpertsBwdLaunch& L, cudaStream_t s) {
+  const auto job = experts_job<kRowsMn, F16>(L.wd_mn, L.gy, L.plan, L.F, kFfnTileM, L.D);
+  const EpiExpertDgate<F16, kAct> o = {static_cast<const uint16_t*>(L.gate_up), L.w_row, static_cast<uint16_t*>(L.gg_buf),
+                                       static_cast<uint16_t*>(L.wa_buf), L.part, L.F, L.lay.cap_rows};
+  return launch_group(job, grp_call(L.call, 1, false, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
 }
 
 template <bool F16>
@@ -65,13 +73,7 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
                               static_cast<uint16_t*>(L.xs), static_cast<uint16_t*>(L.gys), L.w_row,
                               static_cast<uint16_t*>(L.gg_buf), static_cast<uint16_t*>(L.wa_buf));
   if (e != cudaSuccess) return e;
-  {
-    const auto job = experts_job<kRowsMn, F16>(L.wd_mn, L.gy, L.plan, F, kFfnTileM, D);
-    const EpiExpertDgate<F16> o = {static_cast<const uint16_t*>(L.gate_up), L.w_row, static_cast<uint16_t*>(L.gg_buf),
-                                   static_cast<uint16_t*>(L.wa_buf), L.part, F, L.act, L.lay.cap_rows};
-    e = launch_group(job, grp_call(L.call, 1, false, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
-    if (e != cudaSuccess) return e;
-  }
+  if ((e = L.act == 0 ? gate_gradients<F16, 0>(L, s) : gate_gradients<F16, 1>(L, s)) != cudaSuccess) return e;
   {
     WeightGradJob<F16> job;
     job.a[0] = L.gg_mn;
@@ -96,11 +98,11 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
   }
   // rows of grad_x over those of x and of grad_y
   const auto job = experts_job<kRowsMn, F16>(L.wgu_mn, L.gg, L.plan, D, kFfnTileM, 2 * F);
-  const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D};
+  const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D, rows_low_pitch(D)};
   e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
   if (e != cudaSuccess) return e;
   return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, sms, true, s, L.plan, L.T, L.k,
-                     D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.gys),
+                     D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.gys), rows_low_pitch(D),
                      static_cast<const float*>(L.part),
                      static_cast<uint16_t*>(L.grad_x), L.grad_weights);
 }

@@ -19,17 +19,17 @@ __global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const Pla
 
 template <bool F16>
 __global__ void __launch_bounds__(256) combine_kernel(const PlanView p, long long T, int k, int D, const float* weights,
-                                                      const uint16_t* hi, const uint8_t* lo, uint16_t* y) {
+                                                      const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* y) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs; i += (long long)gridDim.x * 8)
-    combine_item<F16>(i, segs, k, D, p.places, weights, hi, lo, y, lane);
+    combine_item<F16>(i, segs, k, D, p.places, weights, hi, lo, lo_pitch, y, lane);
 }
 
-template <bool F16, bool kKept>
+template <bool F16, bool kKept, int kAct>
 cudaError_t gate_up(const ExpertsFwdLaunch& L, cudaStream_t s) {
   const auto job = experts_job<kRowsGateUp, F16>(L.wgu, L.x, L.plan, L.F, 128, L.D);
-  const EpiExpertGateUp<F16, kKept> e = {static_cast<uint16_t*>(L.a_buf), static_cast<uint16_t*>(L.gate_up), L.F, L.act};
+  const EpiExpertGateUp<F16, kKept, kAct> e = {static_cast<uint16_t*>(L.a_buf), static_cast<uint16_t*>(L.gate_up), L.F};
   return launch_group(job, grp_call(L.call, 1, false, token_rows(L.lay.width)), e, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
 }
 
@@ -38,13 +38,16 @@ cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
   cudaError_t e = launch_rows(gather_kernel, L.lay.cap_rows * ((L.D + 1023) / 1024), L.call.sms, false, s, L.call.header, L.plan, L.k,
                               L.D, static_cast<const uint16_t*>(L.x_in), static_cast<uint16_t*>(L.xs));
   if (e != cudaSuccess) return e;
-  if ((e = L.gate_up ? gate_up<F16, true>(L, s) : gate_up<F16, false>(L, s)) != cudaSuccess) return e;
+  e = L.act == 0 ? (L.gate_up ? gate_up<F16, true, 0>(L, s) : gate_up<F16, false, 0>(L, s))
+                 : (L.gate_up ? gate_up<F16, true, 1>(L, s) : gate_up<F16, false, 1>(L, s));
+  if (e != cudaSuccess) return e;
   const auto job = experts_job<kRowsK, F16>(L.wd, L.a, L.plan, L.D, kFfnTileM, L.F);
-  const EpiRows o = {static_cast<uint16_t*>(L.xs), L.lo, L.D};
+  const EpiRows o = {static_cast<uint16_t*>(L.xs), L.lo, L.D, rows_low_pitch(L.D)};
   e = launch_group(job, grp_call(L.call, 2, true, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
   if (e != cudaSuccess) return e;
   return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), L.call.sms, true, s, L.plan, L.T, L.k, L.D, L.weights,
-                     static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.lo), static_cast<uint16_t*>(L.y));
+                     static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.lo), rows_low_pitch(L.D),
+                     static_cast<uint16_t*>(L.y));
 }
 
 }  // namespace

@@ -133,88 +133,106 @@ struct WeightGradJob {
 
 // ------------------------------------------------------------- epilogues
 
-// The accumulator's column `row` and lane m as 24 bits at [row, m] of two planes.
+// The accumulator's column `row` and lane m as the upper 24 bits of the sum at [row, m] of
+// two planes: 16 bits, and 8 whose order inside sixteen columns is 0 8 1 9 .. 7 15.  What a
+// token's sum is off by is then 2^-16 of a term; rows rounded to 16 bits were half of y's
+// error (1.7 times what its own rounding leaves, so 1.4), in fp32 they cost a third more
+// traffic.
 struct EpiRows {
   using Pre = NoPre;
   uint16_t* hi;
   uint8_t* lo;
-  int M;
+  int M, lo_pitch;
   __device__ __forceinline__ void pre(const GTile&, Pre&, int, int, int, int) const {}
   __device__ __forceinline__ void tile(const GTile& g, Pre&, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
     const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32;
     if (m0 >= M) return;
+    const uint32_t sh = smem_u32(buf) + (lane & 7) * kPitch64 + (lane >> 3) * 16;
+    const uint32_t sl = smem_u32(buf) + 32 * kPitch64 + (((lane >> 4) << 3) + (lane & 7)) * kPitch32 + ((lane >> 3) & 1) * 16;
 #pragma unroll 1
     for (int c = grp * 32; c < g.rows; c += 64) {
-      float v[32];
-      acc_ld32(taddr + c, v);
-      const size_t at = (size_t)(g.row0 + c) * M + m0;
-      store_transposed24(v, buf, reinterpret_cast<uint8_t*>(hi + at), lo + at, (size_t)M, g.rows - c, M - m0, lane);
+      float v[4][4][2];
+      frag_ld<4>(taddr + c, v);
+      uint32_t low[4][2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(v[i][b][0]), __float_as_uint(v[i][b][1]), 0x7632);
+        frag_st_t(sh + b * 8 * kPitch64, w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = __byte_perm(__float_as_uint(v[2 * i][b][0]), __float_as_uint(v[2 * i + 1][b][0]), 0x0051);
+          const uint32_t y = __byte_perm(__float_as_uint(v[2 * i][b][1]), __float_as_uint(v[2 * i + 1][b][1]), 0x0051);
+          low[b][i] = __byte_perm(x, y, 0x5410);
+        }
+      }
+      frag_st_t(sl, low[0][0], low[0][1], low[1][0], low[1][1]);
+      frag_st_t(sl + 16 * kPitch32, low[2][0], low[2][1], low[3][0], low[3][1]);
+      __syncwarp();
+      const size_t row0 = (size_t)(g.row0 + c);
+      flush64<32>(buf, reinterpret_cast<uint8_t*>(hi + row0 * M + m0), (size_t)M * 2, g.rows - c, (M - m0 + 7) >> 3, lane);
+      flush32(buf + 32 * kPitch64, lo + row0 * lo_pitch + m0, lo_pitch, g.rows - c, (M - m0 + 15) >> 4, lane);
+      __syncwarp();
     }
   }
 };
 
-// Lanes of a warp: eight gate rows, the same eight up rows, and once more.  Lanes
-// eight apart exchange half their columns, so that each has gate and up of sixteen.
-template <bool F16, bool kKept>
+// Rows of a warp: eight of the gate, the same eight of up, and once more, so that a lane
+// has both sums of its elements.
+template <bool F16, bool kKept, int kAct>
 struct EpiExpertGateUp {
   using Pre = NoPre;
   uint16_t *a, *gate_up;
-  int F, act;
+  int F;
   __device__ __forceinline__ void pre(const GTile&, Pre&, int, int, int, int) const {}
   __device__ __forceinline__ void tile(const GTile& g, Pre&, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
     const int f0 = g.tm * 128 + rank * 64 + q * 16;
     if (f0 >= F) return;
-    const bool up = (lane & 8) != 0;
-    const int fi = ((lane >> 4) << 3) + (lane & 7);
-    uint16_t* st = reinterpret_cast<uint16_t*>(buf);
+    const int pieces = (F - f0) >> 3;
+    // kept: rows of 16 gate and 16 up sums; a: rows of 16
+    const uint32_t sk = smem_u32(buf) + (lane & 7) * kPitch64 + (lane >> 3) * 16;
+    const uint32_t sa = smem_u32(buf) + 32 * kPitch64 + (((lane >> 4) << 3) + (lane & 7)) * kPitch32 + ((lane >> 3) & 1) * 16;
 #pragma unroll 1
     for (int c = grp * 32; c < g.rows; c += 64) {
       const int rows = g.rows - c;
       const size_t row0 = (size_t)(g.row0 + c);
-      float v[32];
-      acc_ld32(taddr + c, v);
-      if constexpr (kKept) {                     // rows of 64 bytes: 16 gate sums, 16 up sums
+      float v[4][4][2];
+      frag_ld<4>(taddr + c, v);
+      if constexpr (kKept) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const uint32_t w = pack2<F16>(v[j], v[j + 1]);
-          st[j * 32 + (up ? 16 : 0) + fi] = (uint16_t)w;
-          st[(j + 1) * 32 + (up ? 16 : 0) + fi] = (uint16_t)(w >> 16);
+        for (int b = 0; b < 4; ++b)
+          frag_st_t(sk + b * 8 * kPitch64, pack2<F16>(v[0][b][0], v[0][b][1]), pack2<F16>(v[2][b][0], v[2][b][1]),
+                    pack2<F16>(v[1][b][0], v[1][b][1]), pack2<F16>(v[3][b][0], v[3][b][1]));
+      }
+      uint32_t o[4][2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float z = v[2 * h][b][e];
+            x[e] = z * sigmoid_fast(act_arg(z, kAct)) * v[2 * h + 1][b][e];
+          }
+          o[b][h] = pack2<F16>(x[0], x[1]);
         }
-        __syncwarp();
-        const int piece = lane & 3, p = piece >> 1, h = (piece & 1) * 8;
+      frag_st_t(sa, o[0][0], o[0][1], o[1][0], o[1][1]);
+      frag_st_t(sa + 16 * kPitch32, o[2][0], o[2][1], o[3][0], o[3][1]);
+      __syncwarp();
+      if constexpr (kKept) {                     // pieces 0 and 1 gate, 2 and 3 up
+        const int p = (lane >> 1) & 1, h = lane & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 8 + (lane >> 2);
-          const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + piece * 16);
-          if (r < rows && f0 + h < F) *reinterpret_cast<uint4*>(gate_up + ((row0 + r) * 2 + p) * F + f0 + h) = w;
+          const uint4 w = *reinterpret_cast<const uint4*>(buf + r * kPitch64 + (lane & 3) * 16);
+          if (r < rows && h < pieces) *reinterpret_cast<uint4*>(gate_up + ((row0 + r) * 2 + p) * F + f0 + 8 * h) = w;
         }
-        __syncwarp();
       }
-      float o[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[16 + j], 8);
-        const float z = up ? got : v[j], u = up ? v[16 + j] : got;
-        o[j] = z * sigmoid_fast(act_arg(z, act)) * u;
-      }
-      // rows of 32 bytes; the second sixteen 32 bytes further, so that the two
-      // halves' writes fall into different banks
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const uint32_t w = pack2<F16>(o[j], o[j + 1]);
-        st[(j + (up ? 17 : 0)) * 16 + fi] = (uint16_t)w;
-        st[(j + 1 + (up ? 17 : 0)) * 16 + fi] = (uint16_t)(w >> 16);
-      }
-      __syncwarp();
-      const int h = (lane & 1) * 8;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = i * 16 + (lane >> 1);
-        const uint4 w = *reinterpret_cast<const uint4*>(buf + (r + i) * 32 + h * 2);
-        if (r < rows && f0 + h < F) *reinterpret_cast<uint4*>(a + (row0 + r) * F + f0 + h) = w;
-      }
+      flush32(buf + 32 * kPitch64, reinterpret_cast<uint8_t*>(a + row0 * F + f0), (size_t)F * 2, rows, pieces, lane);
       __syncwarp();
     }
   }
@@ -223,17 +241,17 @@ struct EpiExpertGateUp {
 // acc = ga before the weight: gg, gu, w a, and this warp's 32 terms of a row's
 // sum_f a ga.  Sixteen tokens at a time, whose kept sums and weights are loaded one step
 // ahead (the first before the tile's sums are there).
-template <bool F16>
+template <bool F16, int kAct>
 struct EpiExpertDgate {
   struct Pre {
     uint4 k[4];                  // piece i * 32 + lane: token / 8, gate or up / 4, eight columns
-    float w;
+    float2 w[2];                 // of the lane's tokens 8 b + 2 (lane % 4)
   };
   const uint16_t* gate_up;
   const float* w_row;            // weight of each row
   uint16_t *gg, *wa;
   float* part;                   // [ceil(F / 32)][cap_rows]
-  int F, act;
+  int F;
   long long cap_rows;
   __device__ __forceinline__ void load(Pre& p, const GTile& g, int f0, int c, int lane) const {
     const int rows = g.rows - c, h = (lane & 3) * 8, plane = (lane >> 2) & 1;
@@ -244,7 +262,12 @@ struct EpiExpertDgate {
       p.k[i] = make_uint4(0, 0, 0, 0);
       if (r < rows && f0 + h < F) p.k[i] = *reinterpret_cast<const uint4*>(gate_up + ((row0 + r) * 2 + plane) * F + f0 + h);
     }
-    p.w = lane < rows && lane < 16 ? w_row[row0 + lane] : 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int r = 8 * b + 2 * (lane & 3);
+      p.w[b].x = r < rows ? w_row[row0 + r] : 0.0f;
+      p.w[b].y = r + 1 < rows ? w_row[row0 + r + 1] : 0.0f;
+    }
   }
   __device__ __forceinline__ void pre(const GTile& g, Pre& p, int rank, int q, int grp, int lane) const {
     load(p, g, g.tm * kFfnTileM + rank * kGemmHalf + q * 32, grp * 16, lane);
@@ -253,74 +276,67 @@ struct EpiExpertDgate {
                                        int lane, int) const {
     const int f0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32;
     if (f0 >= F) return;
-    const bool in = f0 + lane < F;
-    uint16_t* st = reinterpret_cast<uint16_t*>(buf);
+    const uint32_t s0 = smem_u32(buf), frag = (lane & 7) * kPitch64 + (lane >> 3) * 16;
+    const uint32_t sk = s0 + (lane & 7) * kPitch128 + (lane >> 3) * 16;
+    const int pieces = (F - f0) >> 3;
 #pragma unroll 1
     for (int c = grp * 16; c < g.rows; c += 32) {
       const int rows = g.rows - c;
       const size_t row0 = (size_t)(g.row0 + c);
+      // rows of a token's gate and up sums
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 32 + lane) * 16) = p.k[i];
-      const float wl = p.w;
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 4 + (lane >> 3)) * kPitch128 + (lane & 7) * 16) = p.k[i];
+      const float2 wt[2] = {p.w[0], p.w[1]};
       if (c + 32 < g.rows) load(p, g, f0, c + 32, lane);
       __syncwarp();
-      uint16_t kz[16], ku[16];
+      uint32_t kz[2][4], ku[2][4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        kz[j] = st[j * 64 + lane];
-        ku[j] = st[j * 64 + 32 + lane];
+      for (int b = 0; b < 2; ++b) {
+        frag_lds_t(sk + b * 8 * kPitch128, kz[b]);
+        frag_lds_t(sk + b * 8 * kPitch128 + 64, ku[b]);
+      }
+      float ga[4][2][2];
+      frag_ld<2>(taddr + c, ga);
+      __syncwarp();
+      float dot[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t og[4], ou[4], oa[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 z = unpack2<F16>(kz[b][i]), u = unpack2<F16>(ku[b][i]);
+          float g0, u0, a0, g1, u1, a1;
+          gate_grads(z.x, u.x, ga[i][b][0] * wt[b].x, kAct, g0, u0, a0);
+          gate_grads(z.y, u.y, ga[i][b][1] * wt[b].y, kAct, g1, u1, a1);
+          const bool in = f0 + 8 * i < F;        // columns beyond F hold what the sums of nothing times a NaN are
+          dot[b][0] = in ? fmaf(a0, ga[i][b][0], dot[b][0]) : dot[b][0];
+          dot[b][1] = in ? fmaf(a1, ga[i][b][1], dot[b][1]) : dot[b][1];
+          og[i] = pack2<F16>(g0, g1);
+          ou[i] = pack2<F16>(u0, u1);
+          oa[i] = pack2<F16>(a0 * wt[b].x, a1 * wt[b].y);
+        }
+        const uint32_t at = s0 + frag + b * 8 * kPitch64;
+        frag_st_t(at, og[0], og[1], og[2], og[3]);
+        frag_st_t(at + 16 * kPitch64, ou[0], ou[1], ou[2], ou[3]);
+        frag_st_t(at + 32 * kPitch64, oa[0], oa[1], oa[2], oa[3]);
       }
       __syncwarp();
-      float ga[16];
-      tmem_ld16(taddr + c, ga);
-      float dot[16];
+      flush64<16>(buf, reinterpret_cast<uint8_t*>(gg + row0 * 2 * F + f0), (size_t)F * 4, rows, pieces, lane);
+      flush64<16>(buf + 16 * kPitch64, reinterpret_cast<uint8_t*>(gg + (row0 * 2 + 1) * F + f0), (size_t)F * 4, rows, pieces, lane);
+      flush64<16>(buf + 32 * kPitch64, reinterpret_cast<uint8_t*>(wa + row0 * F + f0), (size_t)F * 2, rows, pieces, lane);
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        float og[2], ou[2], oa[2];
+      for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float w = __shfl_sync(0xFFFFFFFFu, wl, j + i);
-          const float z = unpack2<F16>(kz[j + i]).x, u = unpack2<F16>(ku[j + i]).x;
-          float a;
-          gate_grads(z, u, ga[j + i] * w, act, og[i], ou[i], a);
-          dot[j + i] = in ? a * ga[j + i] : 0.0f;
-          oa[i] = a * w;
-        }
-        const uint32_t pg = pack2<F16>(og[0], og[1]), pu = pack2<F16>(ou[0], ou[1]), pa = pack2<F16>(oa[0], oa[1]);
-        st[j * 32 + lane] = (uint16_t)pg;
-        st[(j + 1) * 32 + lane] = (uint16_t)(pg >> 16);
-        st[512 + j * 32 + lane] = (uint16_t)pu;
-        st[512 + (j + 1) * 32 + lane] = (uint16_t)(pu >> 16);
-        st[1024 + j * 32 + lane] = (uint16_t)pa;
-        st[1024 + (j + 1) * 32 + lane] = (uint16_t)(pa >> 16);
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) dot[b][e] += __shfl_xor_sync(0xFFFFFFFFu, dot[b][e], o);
+      if (lane < 8) {                            // lane 4 b + n has tokens 8 b + 2 n and the next
+        const int r = 8 * (lane >> 2) + 2 * (lane & 3);
+        float* to = part + (long long)(f0 >> 5) * cap_rows + row0 + r;
+        const float x = lane < 4 ? dot[0][0] : dot[1][0], y = lane < 4 ? dot[0][1] : dot[1][1];
+        if (r < rows) to[0] = x;
+        if (r + 1 < rows) to[1] = y;
       }
-      __syncwarp();
-      const int h = (lane & 3) * 8;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        const uint4 vg = *reinterpret_cast<const uint4*>(buf + r * 64 + h * 2);
-        const uint4 vu = *reinterpret_cast<const uint4*>(buf + 1024 + r * 64 + h * 2);
-        const uint4 va = *reinterpret_cast<const uint4*>(buf + 2048 + r * 64 + h * 2);
-        if (r < rows && f0 + h < F) {
-          *reinterpret_cast<uint4*>(gg + (row0 + r) * 2 * F + f0 + h) = vg;
-          *reinterpret_cast<uint4*>(gg + ((row0 + r) * 2 + 1) * F + f0 + h) = vu;
-          *reinterpret_cast<uint4*>(wa + (row0 + r) * F + f0 + h) = va;
-        }
-      }
-      // sums over the lanes: lanes halve the columns they carry, column j ends in
-      // lanes 2 j and 2 j + 1
-#pragma unroll
-      for (int n = 8; n > 0; n >>= 1) {
-        const bool hi = (lane & (2 * n)) != 0;
-#pragma unroll
-        for (int j = 0; j < n; ++j) {
-          const float send = hi ? dot[j] : dot[n + j], keep = hi ? dot[n + j] : dot[j];
-          dot[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * n);
-        }
-      }
-      dot[0] += __shfl_xor_sync(0xFFFFFFFFu, dot[0], 1);
-      if (!(lane & 1) && (lane >> 1) < rows) part[(long long)(f0 >> 5) * cap_rows + row0 + (lane >> 1)] = dot[0];
       __syncwarp();
     }
   }
@@ -393,7 +409,7 @@ struct ExpertsFwdLaunch {
   const void* x_in;
   const float* weights;
   void *xs, *a_buf, *y, *gate_up;              // xs: rows of x, then the outputs' upper planes
-  uint8_t* lo;                                 // their lower planes
+  uint8_t* lo;                                 // their lower planes, rows of rows_low_pitch
 };
 cudaError_t launch_experts_forward(const ExpertsFwdLaunch& L, bool f16, cudaStream_t s);
 
@@ -410,6 +426,8 @@ struct ExpertsBwdLaunch {
   float *w_row, *part, *grad_weights, *room;
 };
 cudaError_t launch_experts_backward(const ExpertsBwdLaunch& L, bool f16, cudaStream_t s);
+
+inline int rows_low_pitch(int D) { return (D + 15) & ~15; }
 
 inline GrpCall grp_call(const ExpertsCall& c, int counter, bool last, int b_rows) {
   GrpCall g;
@@ -456,7 +474,7 @@ cudaError_t launch_rows(K* k, long long warps, int sms, bool dependent, cudaStre
 // weights.  A warp takes 256 columns of a token, eight a lane, eight experts in flight.
 template <bool F16>
 __device__ __forceinline__ void combine_item(long long item, int segs, int k, int D, const int* places, const float* weights,
-                                             const uint16_t* hi, const uint8_t* lo, uint16_t* out, int lane) {
+                                             const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* out, int lane) {
   const long long t = item / segs;
   const int c0 = (int)(item - t * segs) * 256 + lane * 8;
   float s[8];
@@ -464,31 +482,31 @@ __device__ __forceinline__ void combine_item(long long item, int segs, int k, in
   for (int i = 0; i < 8; ++i) s[i] = 0.0f;
   const int at = lane < k ? places[t * k + lane] : -1;
   const float wt = lane < k && weights ? weights[t * k + lane] : 1.0f;
+  // a lane's eight low bytes are every second of sixteen, from the first or the second on
+  const uint32_t pick0 = (c0 & 8) ? 0x1050u : 0x1040u, pick1 = (c0 & 8) ? 0x3270u : 0x3260u;
 #pragma unroll 1
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    uint4 v[8];
-    uint2 l[8];
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    uint4 v[4], l[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int p = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
-      v[j] = make_uint4(0, 0, 0, 0);
-      l[j] = make_uint2(0, 0);
+      v[j] = l[j] = make_uint4(0, 0, 0, 0);
       if (j0 + j < k && p >= 0 && c0 < D) {
-        v[j] = __ldcs(reinterpret_cast<const uint4*>(hi + (size_t)p * D + c0));
-        l[j] = __ldcs(reinterpret_cast<const uint2*>(lo + (size_t)p * D + c0));
+        v[j] = *reinterpret_cast<const uint4*>(hi + (size_t)p * D + c0);
+        l[j] = *reinterpret_cast<const uint4*>(lo + (size_t)p * lo_pitch + (c0 & ~15));
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int p = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
       float w = __shfl_sync(0xFFFFFFFFu, wt, (j0 + j) & 31);
       if (j0 + j >= k || p < 0) w = 0.0f;
-      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w}, b[4] = {l[j].x, l[j].y, l[j].z, l[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t b = i < 2 ? l[j].x >> (16 * (i & 1)) : l[j].y >> (16 * (i & 1));   // two low bytes
-        s[2 * i] = fmaf(w, __uint_as_float((u[i] << 16) | ((b & 0xFFu) << 8)), s[2 * i]);
-        s[2 * i + 1] = fmaf(w, __uint_as_float((u[i] & 0xFFFF0000u) | (b & 0xFF00u)), s[2 * i + 1]);
+        // {0, low byte, upper half}: byte 0 is whatever comes after the 24 bits
+        s[2 * i] = fmaf(w, __uint_as_float(__byte_perm(u[i], b[i], pick0) & 0xFFFFFF00u), s[2 * i]);
+        s[2 * i + 1] = fmaf(w, __uint_as_float(__byte_perm(u[i], b[i], pick1) & 0xFFFFFF00u), s[2 * i + 1]);
       }
     }
   }

@@ -66,9 +66,26 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+// 16 bytes to a CTA of the cluster, completing 16 bytes of a barrier there: the waiter sees
+// them without a release by the sender (one costs a thousand clocks or two).
+__device__ __forceinline__ void st_async_v4(uint32_t addr, int4 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
                : "memory");
+}
+__device__ __forceinline__ void expect_tx_relaxed(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Arrive on CTA 0's barrier without a release: what it hands back (tensor memory, a
+// scheduler slot) was only read, and the reads are complete.  A release would first wait
+// for the epilogue's global stores, a microsecond a tile.
+__device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_cluster(bar, 0)) : "memory");
+}
+__device__ __forceinline__ int4 ld_slot(const void* p) {
+  int4 v;
+  asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)) : "memory");
+  return v;
 }
 
 // As settle_copies of mhc_ffn_gemm.cuh, for stages whose bytes differ: both CTAs
@@ -178,18 +195,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 wait_slow(&tail->sched_full[slot], par, ctl, kErrClusterWait, true);
       if (whole_warp) ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
-        const volatile int* p = reinterpret_cast<const volatile int*>(&tail->sched[slot]);
-        g.e = p[0];
-        g.tm = p[1];
-        g.tn = p[2];
-        g.row0 = p[3];
-        g.rows = p[4];
-        g.width = p[5];
-        g.kiters = p[6];
-        g.kind = p[7];
+        const int4 lo = ld_slot(&tail->sched[slot]), hi = ld_slot(&tail->sched[slot].rows);
+        g.e = lo.x;
+        g.tm = lo.y;
+        g.tn = lo.z;
+        g.row0 = lo.w;
+        g.rows = hi.x;
+        g.width = hi.y;
+        g.kiters = hi.z;
+        g.kind = hi.w;
+        if (g.kind < 0 || g.row0 < 0) g.e = -1;            // never so: both loads are complete before the arrival
       }
-      if (whole_warp) __syncwarp();
-      if (!whole_warp || lane == 0) mbar_arrive_remote(&tail->sched_empty[slot], 0);
+      if (whole_warp) ok = __all_sync(0xFFFFFFFFu, g.e >= -1);
+      if (!whole_warp || lane == 0) arrive_relaxed(&tail->sched_empty[slot]);
       return g;
     }
   };
@@ -207,12 +225,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int4 lo = make_int4(g.e, g.tm, g.tn, g.row0), hi = make_int4(g.rows, g.width, g.kiters, g.kind);
 #pragma unroll
         for (uint32_t r = 0; r < 2; ++r) {
-          const uint32_t at = map_cluster(&tail->sched[slot], r);
-          st_cluster_v4(at, lo);
-          st_cluster_v4(at + 16, hi);
+          const uint32_t at = map_cluster(&tail->sched[slot], r), bar = map_cluster(&tail->sched_full[slot], r);
+          expect_tx_relaxed(bar, 32u);
+          st_async_v4(at, lo, bar);
+          st_async_v4(at + 16, hi, bar);
         }
-        mbar_arrive_remote(&tail->sched_full[slot], 0);
-        mbar_arrive_remote(&tail->sched_full[slot], 1);
         return true;
       };
       // The first two tiles of a pair are dealt out, the others drawn: the number of tile
@@ -336,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                  pair);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(&tail->acc_empty[b], 0);
+        if (lane == 0) arrive_relaxed(&tail->acc_empty[b]);
       }
     }
   }
@@ -396,64 +413,96 @@ inline void grp_ring(GrpCall* c, int b_rows) {
 // Nothing to load ahead.
 struct NoPre {};
 
-// 24 bits of an fp32 value, rounded to nearest: what a row of an expert's outputs keeps
-// until a token's are added up, in a 16-bit and an 8-bit plane.  (Rounded to 16 bits
-// these rows were half of a result's error: 1.7 instead of 1.4 times what its own
-// rounding leaves.  In fp32 they would cost a third more traffic.)
-__device__ __forceinline__ uint32_t round24(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return (b & 0x7F800000u) == 0x7F800000u ? b : b + 0x80u;
-}
-// store_transposed for these planes: rows of 64 and of 32 bytes.
-__device__ __forceinline__ void store_transposed24(const float (&v)[32], uint8_t* buf, uint8_t* hi, uint8_t* lo, size_t pitch,
-                                                   int rows, int n, int lane) {
-  uint16_t* st = reinterpret_cast<uint16_t*>(buf);
-  uint8_t* sl = buf + 2048;
+// A warp's part of an accumulator as the fragments of 8 x 8 blocks: with t = lane, element
+// (row 8 i + t / 4, column 8 b + 2 (t % 4) + e) for i in 0..3 and b in 0..kB - 1 is v[i][b][e].
+// Two columns of a row then pack into a word of a 16-bit matrix fragment, which stmatrix
+// writes as rows or, transposed, as columns, and ldmatrix reads: an epilogue that stored
+// and loaded its lanes' elements one by one took 1.5 to 4 times as long, which with two
+// warps per scheduler is time that nothing hides.
+template <int kB>
+__device__ __forceinline__ void frag_ld(uint32_t taddr, float (&v)[4][kB][2]) {
+  static_assert(kB == 2 || kB == 4, "16 or 32 columns");
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t w = round24(v[j]);
-    st[j * 32 + lane] = (uint16_t)(w >> 16);
-    sl[j * 32 + lane] = (uint8_t)(w >> 8);
-  }
-  __syncwarp();
-  const int c = lane & 3;
+  for (int h = 0; h < 2; ++h) {                  // 16 of the warp's 32 lanes
+    float r[4 * kB];
+    const uint32_t at = taddr + ((uint32_t)(h * 16) << 16);
+    if constexpr (kB == 4) {
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+            "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+          : "r"(at)
+          : "memory");
+    } else {
+      asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                   : "r"(at)
+                   : "memory");
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + c * 16);
-    const uint2 l = *reinterpret_cast<const uint2*>(sl + r * 32 + c * 8);
-    if (r < rows && c * 8 < n) {
-      *reinterpret_cast<uint4*>(hi + (size_t)r * pitch * 2 + c * 16) = w;
-      *reinterpret_cast<uint2*>(lo + (size_t)r * pitch + c * 8) = l;
+    for (int b = 0; b < kB; ++b) {
+      v[2 * h][b][0] = r[4 * b];
+      v[2 * h][b][1] = r[4 * b + 1];
+      v[2 * h + 1][b][0] = r[4 * b + 2];
+      v[2 * h + 1][b][1] = r[4 * b + 3];
     }
   }
-  __syncwarp();
-}
-
-// Thirty-two columns of the warp's accumulator lanes as the transposed rows of a
-// matrix: column j is row j of it, the lanes 32 consecutive elements.  Staged as
-// rows of 64 bytes and written in 16-byte pieces.  `base`: element of lane 0 in
-// row 0; `pitch` in bytes; `rows`: rows that count; `n`: elements of a row that
-// count (a multiple of 8).
-template <bool F16>
-__device__ __forceinline__ void store_transposed(const float (&v)[32], uint8_t* buf, uint8_t* base, size_t pitch, int rows,
-                                                 int n, int lane) {
-  uint16_t* st = reinterpret_cast<uint16_t*>(buf);
+  // no use of the values moves above the wait
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const uint32_t w = pack2<F16>(v[j], v[j + 1]);
-    st[j * 32 + lane] = (uint16_t)w;
-    st[(j + 1) * 32 + lane] = (uint16_t)(w >> 16);
-  }
-  __syncwarp();
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < kB; b += 2) {
+      if (i == 0 && b == 0)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0][0][0]), "+f"(v[0][0][1]), "+f"(v[0][1][0]), "+f"(v[0][1][1])::"memory");
+      else
+        asm volatile("" : "+f"(v[i][b][0]), "+f"(v[i][b][1]), "+f"(v[i][b + 1][0]), "+f"(v[i][b + 1][1])::"memory");
+    }
+}
+// Four 8 x 8 blocks of 16-bit elements, one word of each per lane; lane 8 n + r gives the
+// address of row r of block n (16 bytes).
+__device__ __forceinline__ void frag_st(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void frag_st_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void frag_lds(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void frag_lds_t(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+// Pitches of staged rows of 64, 32 and 128 bytes: eight rows in sequence lie in eight
+// different sixteen-byte columns of the banks.
+constexpr int kPitch64 = 80, kPitch32 = 48, kPitch128 = 144;
+
+// Staged rows of 64 (or 32) bytes to memory: row r at base + r pitch, 16-byte pieces below
+// `pieces`, rows below `rows`.
+template <int kRows>
+__device__ __forceinline__ void flush64(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int pieces, int lane) {
   const int c = lane & 3;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kRows / 8; ++i) {
     const int r = i * 8 + (lane >> 2);
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + c * 16);
-    if (r < rows && c * 8 < n) *reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16) = w;
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * kPitch64 + c * 16);
+    if (r < rows && c < pieces) *reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16) = w;
   }
-  __syncwarp();
+}
+__device__ __forceinline__ void flush32(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int pieces, int lane) {
+  const int c = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 16 + (lane >> 1);
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + r * kPitch32 + c * 16);
+    if (r < rows && c < pieces) *reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16) = w;
+  }
 }
 
 }  // namespace mhc

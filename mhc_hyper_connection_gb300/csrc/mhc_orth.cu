@@ -154,6 +154,7 @@ struct OrthJob {
   CUtensorMap a, b;
   GemmShape g;                   // tiles of one matrix
   int count, per, width, kiters;
+  int split;                     // log2(256 / width)
   FastDiv by_matrix;
 
   struct Raw {};
@@ -167,16 +168,19 @@ struct OrthJob {
     GTile o;
     o.e = by_matrix(t);
     const int r = t - o.e * per;
-    if constexpr (kSym) {        // row tm begins at tm (tm + 1) / 2
-      int tm = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
-      while ((tm + 1) * (tm + 2) / 2 <= r) ++tm;
-      while (tm * (tm + 1) / 2 > r) --tm;
+    if constexpr (kSym) {        // row tm begins at tm (tm + 1) / 2 squares of 256
+      const int sq = r >> split;
+      int tm = (int)((sqrtf(8.0f * (float)sq + 1.0f) - 1.0f) * 0.5f);
+      while ((tm + 1) * (tm + 2) / 2 <= sq) ++tm;
+      while (tm * (tm + 1) / 2 > sq) --tm;
       o.tm = tm;
-      o.tn = r - tm * (tm + 1) / 2;
+      o.tn = r - ((tm * (tm + 1) / 2) << split);
+      o.kind = o.tn < (tm << split);             // below the diagonal: its mirror is written too
     } else {
       tile_coords(g, r, o.tm, o.tn);
+      o.kind = 0;
     }
-    o.row0 = o.rows = o.kind = 0;
+    o.row0 = o.rows = 0;
     o.width = width;
     o.kiters = kiters;
     return o;
@@ -213,15 +217,19 @@ struct EpiOrth {
   int M, N, pitch;               // of c and of out but the result's, whose pitch is N
   float alpha, beta;
   bool whole;                    // the result's rows are 16-byte aligned
-  // c of two steps of 32 columns, the first two loaded before the tile's sums are there
+  // c of two steps of 32 columns, the first two loaded before the tile's sums are there:
+  // rows i * 8 + lane / 4, eight columns
   struct Pre {
     uint4 w[2][4];
   };
   __device__ __forceinline__ void load(Pre& p, int h, const GTile& g, int m0, int c0, int lane) const {
-    const uint16_t* at = c + ((size_t)g.e * M + min(m0 + lane, M - 1)) * pitch + c0;
+    const int col = c0 + (lane & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p.w[h][i] = c0 < N && c0 + 8 * i < pitch ? *reinterpret_cast<const uint4*>(at + 8 * i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const int row = m0 + i * 8 + (lane >> 2);
+      p.w[h][i] = make_uint4(0, 0, 0, 0);
+      if (row < M && c0 < N && col < pitch) p.w[h][i] = *reinterpret_cast<const uint4*>(c + ((size_t)g.e * M + row) * pitch + col);
+    }
   }
   __device__ __forceinline__ void pre(const GTile& g, Pre& p, int rank, int q, int grp, int lane) const {
     if constexpr (kHasC) {
@@ -230,71 +238,66 @@ struct EpiOrth {
       load(p, 1, g, m0, half > 32 ? c0 + 32 : N, lane);
     }
   }
+  __device__ __forceinline__ void step(const GTile& g, Pre& ahead, int h, int col, int end, int m0, uint32_t taddr, uint8_t* buf,
+                                       int lane) const {
+    constexpr bool kF16 = kLast != 1;
+    const int c0 = g.tn * g.width + col;
+    const size_t plane = (size_t)g.e * M;
+    const uint32_t frag = smem_u32(buf) + (lane & 7) * kPitch64 + (lane >> 3) * 16;
+    if constexpr (kHasC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + (i * 8 + (lane >> 2)) * kPitch64 + (lane & 3) * 16) = ahead.w[h][i];
+      load(ahead, h, g, m0, col + 64 < end ? c0 + 64 : N, lane);
+      __syncwarp();
+    }
+    float v[4][4][2];
+    frag_ld<4>(taddr + col, v);
+    uint32_t w[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t k[4] = {0, 0, 0, 0};
+      if constexpr (kHasC) frag_lds(frag + i * 8 * kPitch64, k);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float2 t = unpack2<true>(k[b]);
+        w[i][b] = kHasC ? pack2<kF16>(fmaf(beta, v[i][b][0], alpha * t.x), fmaf(beta, v[i][b][1], alpha * t.y))
+                        : pack2<kF16>(beta * v[i][b][0], beta * v[i][b][1]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) frag_st(frag + i * 8 * kPitch64, w[i][0], w[i][1], w[i][2], w[i][3]);
+    __syncwarp();
+    if (kLast == 0) {
+      flush64<32>(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * pitch + c0), (size_t)pitch * 2, M - m0, (pitch - c0) >> 3, lane);
+    } else if (whole) {
+      flush64<32>(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * N + c0), (size_t)N * 2, M - m0, (N - c0) >> 3, lane);
+    } else {
+      const int rows = min(32, M - m0);
+      if (c0 + lane < N)
+        for (int r = 0; r < rows; ++r)
+          out[(plane + m0 + r) * N + c0 + lane] = *reinterpret_cast<const uint16_t*>(buf + r * kPitch64 + lane * 2);
+    }
+    if constexpr (kSym) {
+      if (g.kind) {
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) frag_st_t(frag + b * 8 * kPitch64, w[0][b], w[1][b], w[2][b], w[3][b]);
+        __syncwarp();
+        flush64<32>(buf, reinterpret_cast<uint8_t*>(out + (plane + c0) * pitch + m0), (size_t)pitch * 2, N - c0, (pitch - m0) >> 3, lane);
+      }
+    }
+    __syncwarp();
+  }
   __device__ __forceinline__ void tile(const GTile& g, Pre& ahead, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t* buf,
                                        int lane, int) const {
-    constexpr bool kF16 = kLast != 1;
     const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, n0 = g.tn * g.width, half = g.width >> 1;
     if (m0 >= M) return;
-    const size_t plane = (size_t)g.e * M;
     const int beg = grp * half, end = beg + half;
 #pragma unroll 1
     for (int col = beg; col < end && n0 + col < N; col += 64) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h && (col + 32 >= end || n0 + col + 32 >= N)) break;
-        const int c0 = n0 + col + 32 * h;
-        uint4 w[4];
-        if constexpr (kHasC) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ahead.w[h][i];
-          load(ahead, h, g, m0, col + 64 + 32 * h < end ? c0 + 64 : N, lane);
-        }
-        float v[32];
-        acc_ld32(taddr + col + 32 * h, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 t = make_float2(0.0f, 0.0f);
-            if constexpr (kHasC) t = unpack2<true>(u[j]);
-            float &x0 = v[8 * i + 2 * j], &x1 = v[8 * i + 2 * j + 1];
-            x0 = kHasC ? fmaf(beta, x0, alpha * t.x) : beta * x0;
-            x1 = kHasC ? fmaf(beta, x1, alpha * t.y) : beta * x1;
-          }
-        }
-        if constexpr (kSym) {
-          if (g.tm != g.tn)
-            store_transposed<true>(v, buf, reinterpret_cast<uint8_t*>(out + (plane + c0) * pitch + m0), (size_t)pitch * 2, N - c0,
-                                   pitch - m0, lane);
-        }
-        // rows of 64 bytes of this half
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + sw128(lane, (kSym ? 0 : h * 4) + i)) = pack8v<kF16>(v + 8 * i);
-        if constexpr (kSym)
-          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * pitch + c0), (size_t)pitch * 2, M - m0,
-                      min(32, pitch - c0) * 2, lane);
-      }
-      if constexpr (!kSym) {
-        const int cols = min(64, end - col);
-        if (kLast == 0) {
-          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * pitch + n0 + col), (size_t)pitch * 2, M - m0,
-                      min(cols, pitch - n0 - col) * 2, lane);
-        } else if (whole) {
-          stage_flush(buf, reinterpret_cast<uint8_t*>(out + (plane + m0) * N + n0 + col), (size_t)N * 2, M - m0,
-                      min(cols, N - n0 - col) * 2, lane);
-        } else {
-          __syncwarp();
-          const int rows = min(32, M - m0), n = min(cols, N - n0 - col);
-          for (int r = 0; r < rows; ++r) {
-            uint16_t* o = out + (plane + m0 + r) * N + n0 + col;
-#pragma unroll
-            for (int e = lane; e < 64; e += 32)
-              if (e < n) o[e] = *reinterpret_cast<const uint16_t*>(buf + sw128(r, e >> 3) + (e & 7) * 2);
-          }
-          __syncwarp();
-        }
-      }
+      step(g, ahead, 0, col, end, m0, taddr, buf, lane);
+      if (col + 32 < end && n0 + col + 32 < N) step(g, ahead, 1, col + 32, end, m0, taddr, buf, lane);
     }
   }
 };
@@ -351,10 +354,33 @@ struct Product {
   double alpha, beta;
   bool whole;
 };
+// Width of the tiles: 256, or 128 or 64 where that ends sooner.  In times of a stage of a
+// tile of 256 (0.28 us): a stage of 128 takes 0.6 and of 64 0.5 of it; an epilogue, 9 for
+// 256 columns, runs beside the next tile's stages and after the last one's.  (515 x 259:
+// three tiles of 256 or ten of 64.)
+int tile_width(int64_t batch, int64_t M, int64_t N, int64_t K, bool sym, int sms) {
+  const int64_t kiters = (K + kFfnTileK - 1) / kFfnTileK, tm = (M + 255) / 256;
+  int best = 256;
+  double least = 1e30;
+  for (int w = 256; w >= 64; w /= 2) {
+    if (w > 64 && N <= w / 2) continue;
+    const double stage = w == 256 ? 1.0 : w == 128 ? 0.6 : 0.5, epi = 9.0 * w / 256;
+    const int64_t tiles = batch * (sym ? tm * (tm + 1) / 2 * (256 / w) : tm * ((N + w - 1) / w));
+    const double rounds = (double)((tiles + sms / 2 - 1) / (sms / 2)), main = kiters * stage;
+    const double cost = rounds * (main > epi ? main : epi) + epi;
+    if (cost < least) {
+      least = cost;
+      best = w;
+    }
+  }
+  return best;
+}
+
 template <bool kA, bool kB, bool kHasC, bool kSym, int kLast>
 cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* mapped, cudaStream_t s) {
   OrthJob<kA, kB, kSym> job;
-  job.width = p.N >= 256 ? 256 : (int)(p.N + 63) / 64 * 64;
+  job.width = tile_width(p.batch, p.M, p.N, p.K, kSym, p.sms);
+  job.split = job.width == 256 ? 0 : job.width == 128 ? 1 : 2;
   *mapped = orth_map(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch, kA ? kFfnBoxMn : (uint32_t)kGemmHalf) &&
             orth_map(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)job.width / 2);
   if (!*mapped) return cudaErrorInvalidValue;
@@ -366,7 +392,7 @@ cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* ma
   g.by_band = FastDiv((uint32_t)(g.band * g.tiles_n));
   g.by_rows = FastDiv((uint32_t)g.band);
   g.by_last = FastDiv((uint32_t)(g.tiles_m % g.band ? g.tiles_m % g.band : g.band));
-  job.per = kSym ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
+  job.per = kSym ? (g.tiles_m * (g.tiles_m + 1) / 2) << job.split : g.tiles_m * g.tiles_n;
   job.count = (int)(job.per * p.batch);
   job.by_matrix = FastDiv((uint32_t)job.per);
   job.kiters = (int)((p.K + kFfnTileK - 1) / kFfnTileK);
@@ -440,7 +466,7 @@ mhc_status_t mhc_orth_run(const mhc_orth_args* a, void* stream) {
   if (a->workspace_bytes < need)
     return fail(MHC_ERR_PARAM_INVALID, "workspace too small: %zu bytes given, %zu needed", a->workspace_bytes, need);
   const OrthLayout l = orth_layout(a->batch, a->rows, a->cols);
-  const int64_t tiles = ((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
+  const int64_t tiles = ((a->rows + 255) / 256) * ((a->cols + 63) / 64) * a->batch;
   if (tiles > (int64_t(1) << 30)) return fail(MHC_ERR_PARAM_INVALID, "too many tiles");
   if ((st = check_apart({{"out", a->out, count * 2}, {"workspace", a->workspace, l.total}}, {{"x", a->x, count * esize}})) != MHC_OK)
     return st;

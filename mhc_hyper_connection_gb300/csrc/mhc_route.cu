@@ -39,6 +39,9 @@ __device__ __forceinline__ unsigned long long order(double v) {
 __device__ __forceinline__ float unorder(uint32_t u) {
   return u == 0xFFFFFFFFu ? NAN : __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+__device__ __forceinline__ double unorder(unsigned long long u) {
+  return u == ~0ull ? (double)NAN : __longlong_as_double((long long)(u ^ ((u >> 63) ? 1ull << 63 : ~0ull)));
+}
 template <class K>
 struct Ordered;
 template <>
@@ -77,20 +80,91 @@ __device__ __forceinline__ float load_logit(const void* p, long long at) {
   else return __half2float(static_cast<const __half*>(p)[at]);
 }
 
+// What the scores of a row's logits share: the largest logit and the sum of exponentials.
+template <class K>
+struct RowSum {
+  float top;
+  K sum;
+};
+// Score of a logit.  In fp32 only to be compared: fast exponential and division, a few 2^-23
+// of it off.
+__device__ __forceinline__ float score_of(const RouteArgs& a, float l, const RowSum<float>& r) {
+  return a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __fdividef(expf(l - r.top), r.sum);
+}
+__device__ __forceinline__ double score_of(const RouteArgs& a, double l, const RowSum<double>& r) {
+  return a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)r.top) / r.sum;
+}
+
+// (u, id) of a lane in descending order of u, equal ones by id: id's low byte first.
+template <class U, int V>
+__device__ __forceinline__ void sort_lane(U (&u)[V], int (&id)[V]) {
+  // Batcher's odd-even merges
+#pragma unroll
+  for (int p = 1; p < V; p *= 2) {
+#pragma unroll
+    for (int k = p; k > 0; k /= 2) {
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            U &x = u[i + j], &y = u[i + j + k];
+            int &xi = id[i + j], &yi = id[i + j + k];
+            const bool swap = y > x || (y == x && yi < xi);
+            const U t = swap ? y : x;
+            y = swap ? x : y;
+            x = t;
+            const int ti = swap ? yi : xi;
+            yi = swap ? xi : yi;
+            xi = ti;
+          }
+        }
+      }
+    }
+  }
+}
+
+// Groups of the marks (group g's in lane g): the top_groups best, as bits.  close: a group
+// left out has a mark within `tol` (of its size and smax) of the last one taken.
+template <class K>
+__device__ __forceinline__ uint32_t choose_groups(K mark, const RouteArgs& a, float smax, float tol, int lane, bool& close) {
+  using U = typename Ordered<K>::U;
+  U u = lane < a.groups ? order(mark) : (U)0;
+  K last = 0;
+  uint32_t stays = 0;
+  for (int i = 0; i < a.top_groups; ++i) {
+    const U mu = warp_max(u);
+    const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
+    stays |= 1u << w;
+    if (lane == w) u = 0;
+    last = __shfl_sync(kFull, mark, w);
+  }
+  const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != (K)-INFINITY;
+  close = __any_sync(kFull, left && last - mark <= (K)(2.0f * tol * (smax + fabsf((float)last))));
+  return stays;
+}
+
 // The choice from keys of type K: experts lane * V + i are a lane's.  Returns, in lane j <
-// k, the j-th expert (or -1) and its logit.  With K = float, `unsure` is set where two
-// keys that decide something are so close that they may stand in the wrong order: closer
-// than tol (smax + max(|a|, |b|)), smax the largest score.  room: E values of this warp.
-template <class K, int V>
-__device__ __forceinline__ int choose(const RouteArgs& a, const float (&l)[V], const K (&key)[V], float smax, float tol, K* room,
-                                      int lane, bool& unsure, float& myl) {
+// k, the j-th expert (or -1).  With K = float, `unsure` is set where two keys that decide
+// something are so close that they may stand in the wrong order: closer than tol (smax +
+// max(|a|, |b|)), smax the largest score.  room: E values of this warp.
+// Up to eight scores a lane are sorted first, so that a round takes a lane's next instead
+// of searching it (T = 16384, E = 256, k = 8 of 4 groups of 8: 64 -> 28 us).
+template <int kType, class K, int V>
+__device__ __forceinline__ int choose(const RouteArgs& a, long long row, const float (&l)[V], const K (&key)[V],
+                                      const RowSum<K>& sums, float smax, float tol, K* room, int lane, bool& unsure) {
   using U = typename Ordered<K>::U;
   constexpr U kOut = Ordered<K>::kOut;
-  constexpr bool kCheck = sizeof(K) == 4;
+  constexpr bool kCheck = sizeof(K) == 4, kSorted = V <= 8;
   const int E = a.E, k = a.k, e0 = lane * V, per = E / a.groups;
   const bool by_key = a.bias != nullptr;
-  uint32_t stays = kFull;
-  if (a.groups > 1) {
+  U u[V];
+  int id[V];
+  bool close = false;
+  // whole lanes in a group, and a power of two of them
+  const int lanes = per / V;
+  const bool whole = kSorted && per % V == 0 && (lanes & (lanes - 1)) == 0;
+  if (a.groups > 1 && !whole) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -126,102 +200,145 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const float (&l)[V], c
       }
     }
     const K m = a.top2 && next != (K)-INFINITY ? best + next : best;
-    const K mark = __shfl_sync(kFull, m, min(lane * span, 31));          // group g's in lane g
-    U u = lane < a.groups ? order(mark) : (U)0;
-    K last = 0;
-    stays = 0;
-    for (int i = 0; i < a.top_groups; ++i) {
-      const U mu = warp_max(u);
-      const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
-      stays |= 1u << w;
-      if (lane == w) u = 0;
-      last = __shfl_sync(kFull, mark, w);
-    }
-    if constexpr (kCheck) {                      // a group left out whose mark is close to the last one taken
-      const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != -INFINITY;
-      unsure = __any_sync(kFull, left && last - mark <= 2.0f * tol * (smax + fabsf(last)));
-    }
-  }
-  U u[V], best = kOut;
-  int grp = a.groups > 1 ? e0 / per : 0, grp_end = (grp + 1) * per;
+    const uint32_t stays = choose_groups<K>(__shfl_sync(kFull, m, min(lane * span, 31)), a, smax, tol, lane, close);
+    int grp = e0 / per, grp_end = (grp + 1) * per;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (e0 + i >= grp_end) {
-      ++grp;
-      grp_end += per;
+    for (int i = 0; i < V; ++i) {
+      if (e0 + i >= grp_end) {
+        ++grp;
+        grp_end += per;
+      }
+      u[i] = e0 + i < E && ((stays >> (grp & 31)) & 1u) && l[i] != -INFINITY ? order(by_key ? key[i] : (K)l[i]) : kOut;
     }
-    const bool in = e0 + i < E && ((stays >> (grp & 31)) & 1u) && l[i] != -INFINITY;
-    u[i] = in ? order(by_key ? key[i] : (K)l[i]) : kOut;
-    best = u[i] > best ? u[i] : best;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] = l[i] != -INFINITY ? order(by_key ? key[i] : (K)l[i]) : kOut;
   }
-  int mine = -1;
-  myl = -INFINITY;
-  float prev = 0.0f, prevl = 0.0f;
-  int preve = 0;
+  uint32_t ids = 0;                              // the sorted ones' places in the lane, four bits each
+  if constexpr (kSorted) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) id[i] = i;
+    sort_lane(u, id);
+#pragma unroll
+    for (int i = 0; i < V; ++i) ids |= (uint32_t)id[i] << (4 * i);
+    if (a.groups > 1 && whole) {
+      // a lane's two best; without a bias in the order of the logits, their scores then
+      U b = u[0], n = V > 1 ? u[V > 1 ? 1 : 0] : kOut;
+      for (int o = 1; o < lanes; o <<= 1) {
+        const U b2 = __shfl_xor_sync(kFull, b, o), n2 = __shfl_xor_sync(kFull, n, o);
+        n = b2 > b ? (b > n2 ? b : n2) : (b2 > n ? b2 : n);
+        b = b2 > b ? b2 : b;
+      }
+      K best, next;
+      if (by_key) {
+        best = unorder(b);
+        next = unorder(n);
+      } else {
+        best = b == kOut ? (K)-INFINITY : score_of(a, unorder(b), sums);
+        next = n == kOut ? (K)-INFINITY : score_of(a, unorder(n), sums);
+      }
+      const K m = a.top2 && next != (K)-INFINITY ? best + next : best;
+      const uint32_t stays = choose_groups<K>(__shfl_sync(kFull, m, (lane * lanes) & 31), a, smax, tol, lane, close);
+      if (!((stays >> (lane / lanes)) & 1u)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] = kOut;
+      }
+    }
+  }
+  unsure = kCheck && close;
+  U best = kOut;
+  if constexpr (!kSorted) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = u[i] > best ? u[i] : best;
+  }
+  int mine = -1, after = -1, found = 0;
+  U mykey = kOut, afterkey = kOut;
   const int rounds = kCheck && by_key ? k + 1 : k;
   for (int j = 0; j < rounds; ++j) {
+    if constexpr (kSorted) best = u[0];
     const U m = warp_max(best);
     if (m == kOut) break;
     const int w = __ffs(__ballot_sync(kFull, best == m)) - 1;
     int e = 0;
-    float le = 0.0f;
-    if (lane == w) {
-      bool done = false;
-      best = kOut;
+    if constexpr (kSorted) {
+      e = __shfl_sync(kFull, e0 + (int)(ids & 15u), w);
+      if (lane == w) {
+        ids >>= 4;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (!done && u[i] == m) {
-          done = true;
-          u[i] = kOut;
-          e = e0 + i;
-          le = l[i];
+        for (int i = 0; i + 1 < V; ++i) u[i] = u[i + 1];
+        u[V - 1] = kOut;
+      }
+    } else {
+      if (lane == w) {
+        bool done = false;
+        best = kOut;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (!done && u[i] == m) {
+            done = true;
+            u[i] = kOut;
+            e = e0 + i;
+          }
+          best = u[i] > best ? u[i] : best;
         }
-        best = u[i] > best ? u[i] : best;
       }
+      e = __shfl_sync(kFull, e, w);
     }
-    e = __shfl_sync(kFull, e, w);
-    le = __shfl_sync(kFull, le, w);
-    if constexpr (kCheck) {
-      if (by_key) {
-        const float kv = unorder((uint32_t)m);
-        // equal numbers in give equal keys: the index decides, nothing to look at
-        if (j && prev - kv <= tol * (smax + fmaxf(fabsf(prev), fabsf(kv))) && !(le == prevl && a.bias[e] == a.bias[preve])) unsure = true;
-        prev = kv;
-        prevl = le;
-        preve = e;
-      }
-    }
-    if (lane == j && j < k) {
+    ++found;
+    if (lane == j) {
       mine = e;
-      myl = le;
+      mykey = m;
+    }
+    after = e;
+    afterkey = m;
+  }
+  if constexpr (kCheck) {
+    if (by_key && found > 1) {
+      // lane j against the next one; the last against the first that was left out
+      const int last = found - 1;
+      int ne = __shfl_down_sync(kFull, mine, 1);
+      U nk = __shfl_down_sync(kFull, mykey, 1);
+      if (lane == 31) {
+        ne = after;
+        nk = afterkey;
+      }
+      const float x = unorder(mykey), y = unorder(nk);
+      bool near = lane < last && x - y <= tol * (smax + fmaxf(fabsf(x), fabsf(y)));
+      if (__any_sync(kFull, near)) {
+        // equal numbers in give equal keys: the index decides, nothing to look at
+        if (near)
+          near = !(load_logit<kType>(a.logits, row * E + mine) == load_logit<kType>(a.logits, row * E + ne) &&
+                   a.bias[mine] == a.bias[ne]);
+        unsure = unsure || __any_sync(kFull, near);
+      }
     }
   }
-  return mine;
+  return lane < k ? mine : -1;
 }
 
 // The choice once more with keys in fp64, for rows where fp32 left two keys too close: some
 // of a thousand of ordinary rows with a bias or groups.
-template <int V>
-__device__ __noinline__ int choose64(const RouteArgs& a, const float* logits, float top, double* room, int lane, float* myl) {
+template <int kType, int V>
+__device__ __noinline__ int choose64(const RouteArgs& a, long long row, const float* logits, float top, double* room, int lane) {
   const int e0 = lane * V;
   float l[V];
-  double key[V], sum = 0.0;
+  double key[V];
+  RowSum<double> r = {top, 0.0};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     l[i] = logits[i];
-    const double x = l[i];
-    key[i] = l[i] == -INFINITY ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top);
-    sum += key[i];
+    key[i] = l[i] == -INFINITY ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)top);
+    r.sum += key[i];
   }
-  if (!a.sigmoid) sum = warp_sum(sum);
+  r.sum = warp_sum(r.sum);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (!a.sigmoid) key[i] /= sum;
+    if (!a.sigmoid) key[i] /= r.sum;
     if (a.bias && e0 + i < a.E) key[i] += (double)a.bias[e0 + i];
     if (l[i] == -INFINITY) key[i] = -INFINITY;
   }
   bool unsure = false;
-  return choose<double, V>(a, l, key, 0.0f, 0.0f, room, lane, unsure, *myl);
+  return choose<kType, double, V>(a, row, l, key, r, 0.0f, 0.0f, room, lane, unsure);
 }
 
 // V: consecutive scores of a lane.
@@ -231,6 +348,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k, e0 = lane * V;
   double* keys64 = route_keys + (size_t)warp * E;
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
   for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
     float l[V];
     const long long base = row * E + e0;
@@ -274,49 +394,51 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     topu = warp_max(topu);
     const float top = topu == Ordered<float>::kOut ? 0.0f : unorder(topu);
     const bool scores = a.bias != nullptr || a.groups > 1;
-    float sum = 0.0f, smax = 1.0f;
+    float smax = 1.0f;
+    RowSum<float> r = {top, 0.0f};
     float key[V];
     if (a.sigmoid) {
       if (scores) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = sigmoid32(l[i]);
+        for (int i = 0; i < V; ++i) key[i] = score_of(a, l[i], r);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         key[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
-        sum += key[i];
+        r.sum += key[i];
       }
-      sum = warp_sum(sum);
+      r.sum = warp_sum(r.sum);
       if (scores) {
-        smax = 1.0f / sum;
+        smax = 1.0f / r.sum;
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = key[i] / sum;
+        for (int i = 0; i < V; ++i) key[i] = key[i] * smax;
       }
     }
     if (scores) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (a.bias && e0 + i < E) key[i] += a.bias[e0 + i];
+        key[i] += bias[i];
         if (l[i] == -INFINITY) key[i] = -INFINITY;
       }
     }
     // How far two keys may be off against one another, of the largest score and their own
-    // size: a sigmoid by 2^-22 of itself, a softmax's by its exponential and the rounding
-    // of l - top (2^-22 of the largest) and its sum (V + 5 roundings, the same for all),
-    // the sum with the bias by 2^-24 of itself; twice that.
-    const float tol = a.sigmoid ? 0x1p-20f : (V + 16) * 0x1p-23f;
+    // size.  Sigmoid: fast exponential (2 + 1.2 |l| units of 2^-23 of itself, which counts s
+    // (1 - s), at most 0.8 of 2^-23 in all), the sum and the division 2^-22 each: 2^-21.
+    // Softmax: exponential and rounding of l - top 2^-22 of the largest, reciprocal and
+    // division 2^-22, its sum V + 5 roundings, the same for all.  A key with a bias 2^-24 of
+    // itself.  Twice that for two keys, and as much again.
+    const float tol = a.sigmoid ? 0x1p-19f : (V + 24) * 0x1p-23f;
     bool unsure = false;
-    float myl;
-    int mine = choose<float, V>(a, l, key, smax, tol, reinterpret_cast<float*>(keys64), lane, unsure, myl);
+    int mine = choose<kType, float, V>(a, row, l, key, r, smax, tol, reinterpret_cast<float*>(keys64), lane, unsure);
     if (unsure) {
       float kept[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) kept[i] = l[i];
-      float chosen;
-      mine = choose64<V>(a, kept, top, keys64, lane, &chosen);
-      myl = chosen;
+      mine = choose64<kType, V>(a, row, kept, top, keys64, lane);
     }
+    const float myl = mine >= 0 ? load_logit<kType>(a.logits, row * E + mine) : -INFINITY;
+    const float sum = r.sum;
     // Weights: lane j has slot j.
     float w;
     if (a.renorm) {
