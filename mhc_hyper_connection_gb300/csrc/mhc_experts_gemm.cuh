@@ -20,7 +20,9 @@ enum { kRowsK = 0, kRowsGateUp = 1, kRowsMn = 2 };
 
 template <int kRows, bool F16>
 struct ExpertsJob {
-  static constexpr bool kAMn = kRows == kRowsMn, kBMn = false, kDraw = true;
+  // A call's first launch is ordered behind the plan, so the launches behind it may read
+  // that before they wait.
+  static constexpr bool kAMn = kRows == kRowsMn, kBMn = false, kDraw = true, kEarly = true;
   CUtensorMap a, b[4];           // b: boxes of 16, 32, 64 and 128 tokens
   const int* head;
   const int4* table;
@@ -61,7 +63,7 @@ struct ExpertsJob {
   __device__ __forceinline__ int bytes(const GTile& g) const { return kGemmOpBytes + (16 << box(g)) * kFfnTileK * 2; }
   __device__ __forceinline__ int steps(const GTile&, int) const { return kFfnTileK / 16; }
   __device__ __forceinline__ uint32_t idesc(const GTile& g) const { return grp_idesc(F16, kAMn, false, g.width); }
-  __device__ __forceinline__ void load(const GTile& g, int k, uint32_t sa, uint32_t sb, uint32_t bar, int rank) const {
+  __device__ __forceinline__ void load_a(const GTile& g, int k, uint32_t sa, uint32_t bar, int rank) const {
     const int k0 = k * kFfnTileK;
     if constexpr (kRows == kRowsGateUp) {
       tma_load_5d_pair(sa, &a, bar, k0, 0, 0, g.tm * 16 + rank * 8, g.e);
@@ -72,7 +74,9 @@ struct ExpertsJob {
       tma_load_3d_pair(sa, &a, bar, m0, k0, g.e);
       tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, g.e);
     }
-    tma_load_2d_pair(sb, &b[box(g)], bar, k0, g.row0 + rank * (g.width >> 1));
+  }
+  __device__ __forceinline__ void load_b(const GTile& g, int k, uint32_t sb, uint32_t bar, int rank) const {
+    tma_load_2d_pair(sb, &b[box(g)], bar, k * kFfnTileK, g.row0 + rank * (g.width >> 1));
   }
 };
 
@@ -81,7 +85,7 @@ struct ExpertsJob {
 // the last step of a depth takes nothing of the next expert's.
 template <bool F16>
 struct WeightGradJob {
-  static constexpr bool kAMn = true, kBMn = true, kDraw = true;
+  static constexpr bool kAMn = true, kBMn = true, kDraw = true, kEarly = false;
   CUtensorMap a[2], b[2];
   const int *counts, *starts;
   int E, tiles_n[2], area[2], width[2];
@@ -121,13 +125,17 @@ struct WeightGradJob {
     return min(kFfnTileK / 16, (g.rows - k * kFfnTileK + kPlanPad - 1) / kPlanPad);
   }
   __device__ __forceinline__ uint32_t idesc(const GTile& g) const { return grp_idesc(F16, true, true, g.width); }
-  __device__ __forceinline__ void load(const GTile& g, int k, uint32_t sa, uint32_t sb, uint32_t bar, int rank) const {
-    const int k0 = g.row0 + k * kFfnTileK, m0 = g.tm * kFfnTileM + rank * kGemmHalf, n0 = g.tn * g.width + rank * (g.width >> 1);
-    const CUtensorMap *ta = g.kind ? &a[1] : &a[0], *tb = g.kind ? &b[1] : &b[0];
-    tma_load_2d_pair(sa, ta, bar, m0, k0);
-    tma_load_2d_pair(sa + 8192, ta, bar, m0 + 64, k0);
-    tma_load_2d_pair(sb, tb, bar, n0, k0);
-    if (g.width > 128) tma_load_2d_pair(sb + 8192, tb, bar, n0 + 64, k0);
+  __device__ __forceinline__ void load_a(const GTile& g, int k, uint32_t sa, uint32_t bar, int rank) const {
+    const int k0 = g.row0 + k * kFfnTileK, m0 = g.tm * kFfnTileM + rank * kGemmHalf;
+    const CUtensorMap* t = g.kind ? &a[1] : &a[0];
+    tma_load_2d_pair(sa, t, bar, m0, k0);
+    tma_load_2d_pair(sa + 8192, t, bar, m0 + 64, k0);
+  }
+  __device__ __forceinline__ void load_b(const GTile& g, int k, uint32_t sb, uint32_t bar, int rank) const {
+    const int k0 = g.row0 + k * kFfnTileK, n0 = g.tn * g.width + rank * (g.width >> 1);
+    const CUtensorMap* t = g.kind ? &b[1] : &b[0];
+    tma_load_2d_pair(sb, t, bar, n0, k0);
+    if (g.width > 128) tma_load_2d_pair(sb + 8192, t, bar, n0 + 64, k0);
   }
 };
 
@@ -342,6 +350,24 @@ struct EpiExpertDgate {
   }
 };
 
+#ifdef WG_CS
+__device__ __forceinline__ void stage_flush_cs(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int bytes, int lane) {
+  __syncwarp();
+  const int c = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + sw128(r, c));
+    if (r < rows && c * 16 < bytes) __stcs(reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16), v);
+  }
+  __syncwarp();
+}
+#define STAGE_FLUSH stage_flush_cs
+#elif defined(WG_NONE)
+#define STAGE_FLUSH(...) __syncwarp()
+#else
+#define STAGE_FLUSH stage_flush
+#endif
 // out[e][m, n] of either weight gradient; an expert without rows gets zeros.  A sum
 // in several parts is joined in fp32 in a room of the warp's own.
 template <bool F16>
@@ -383,7 +409,7 @@ struct EpiWeightGrad {
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + i)) = pack8v<F16>(v + 8 * i);
       }
       if (parts <= 1 || p + 1 == parts)
-        stage_flush(buf, reinterpret_cast<uint8_t*>(o + (size_t)m0 * Nk + n0 + c), (size_t)Nk * 2, Mk - m0,
+        STAGE_FLUSH(buf, reinterpret_cast<uint8_t*>(o + (size_t)m0 * Nk + n0 + c), (size_t)Nk * 2, Mk - m0,
                     min(min(64, end - c), Nk - n0 - c) * 2, lane);
       else
         __syncwarp();

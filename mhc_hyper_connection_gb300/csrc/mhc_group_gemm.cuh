@@ -118,12 +118,13 @@ __host__ __device__ constexpr uint32_t grp_idesc(bool f16, bool a_mn, bool b_mn,
 
 // Job:
 //   kAMn, kBMn           operands stored MN-major
+//   kEarly               tiles, Raw and A do not depend on the launches that this one overlaps
 //   kDraw                tiles are drawn from the counter (their work differs), else dealt out in turn
 //   int tiles() const    their number (read once earlier launches are complete)
 //   Raw fetch(int t)     what tile t needs from memory, loaded ahead of its use
 //   GTile make(int t, const Raw&)
 //   int bytes(const GTile&)                       bytes that one CTA copies into a stage
-//   void load(tile, k, sa, sb, bar, rank)         chunk k of the depth into a stage
+//   void load_a(tile, k, sa, bar, rank), load_b   chunk k of the depth into a stage
 //   int steps(tile, k)                            products of depth 16 in chunk k
 //   uint32_t idesc(tile)
 //   void prefetch()                               tensor-map descriptors
@@ -176,7 +177,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = tail->tmem_base;
   pdl_trigger();
-  pdl_wait();                                    // operands, plan and counter are earlier launches'
+  // Operands and the counter are earlier launches'.  The producers of a job whose A is not
+  // (an expert's weights) begin with it before they wait.
+  if (!Job::kEarly || warp != 0) pdl_wait();
   const int ntiles = job.tiles();
 
   // The n-th tile of this pair as the roles see it (e = -1 after the last, and when
@@ -232,50 +235,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
         return true;
       };
-      // The first two tiles of a pair are dealt out, the others drawn: the number of tile
-      // n + 3 and what tile n + 2 needs from memory are on their way under tile n's copies,
-      // so that neither latency stands before a copy (weight gradients of short tiles).
-      auto draw = [&]() -> long long { return 2ll * pairs + atomicAdd(call.counter, 1u); };
+      // The first two tiles of a pair are dealt out, the others drawn: the ticket of tile n +
+      // 3 and what tile n + 2 needs from memory are on their way under tile n's copies, and
+      // nothing is computed from either before they are needed, so that neither latency
+      // stands before a copy.
       GTile none, cur, next;
       none.e = -1;
       none.tm = none.tn = none.row0 = none.rows = none.width = none.kiters = none.kind = 0;
       cur = next = none;
-      long long drawn = ntiles;
+      uint32_t ticket = 0;
+      bool drawing = false;                      // a ticket is held or on its way
       if (Job::kDraw && rank == 0) {
         const int t0 = pair, t1 = pair + pairs;
         typename Job::Raw r0, r1;
         if (t0 < ntiles) r0 = job.fetch(t0);
         if (t1 < ntiles) r1 = job.fetch(t1);
-        if (t1 < ntiles) drawn = draw();
         if (t0 < ntiles) cur = job.make(t0, r0);
         if (t1 < ntiles) next = job.make(t1, r1);
         ok = publish(0, cur) && publish(1, next);
+        drawing = t1 < ntiles;
       }
+      int early = 0;                             // chunks of the first tile whose A is on its way
+      if constexpr (Job::kEarly) {
+        if (rank == 1 && pair < ntiles) cur = job.make(pair, job.fetch(pair));
+        if (cur.e >= 0 && !call.withhold) {
+          early = min(stages, cur.kiters);
+          for (int k = 0; k < early; ++k) {
+            if (rank == 0) mbar_expect_tx(&tail->full[k], 2u * (uint32_t)job.bytes(cur));
+            job.load_a(cur, k, smem_u32(smem + k * stage_bytes), map_cluster(&tail->full[k], 0), (int)rank);
+          }
+        }
+        pdl_wait();
+      }
+      if (drawing) ticket = atomicAdd(call.counter, 1u);
       for (int n = 0; ok; ++n) {
-        const GTile g = Job::kDraw && rank == 0 ? cur : tile_of(n, false);
+        GTile g = cur;
+        if (!Job::kDraw || rank == 1) g = tile_of(n, false);
+        if (n == 0 && early) g = cur;            // its copies are completed whatever became of that wait
         if (g.e < 0) break;
         const int bytes = job.bytes(g);
         // test hook, as in ffn_gemm_kernel
         const int kend = call.withhold && pair < 2 && n == 0 ? max(g.kiters - 1 - (int)(rank ^ (uint32_t)pair), 0) : g.kiters;
-        const long long after = drawn;
+        const uint32_t held = ticket;
+        const bool had = drawing;
         typename Job::Raw raw;
+        long long after = ntiles;
         const int half = kend >> 1;
-        if (Job::kDraw && rank == 0 && after < ntiles) drawn = draw();
+        if (had) ticket = atomicAdd(call.counter, 1u);
         for (int k = 0; k < kend; ++k) {
-          if (k == half && after < ntiles) raw = job.fetch((int)after);
+          if (k == half && had) {
+            after = 2ll * pairs + held;
+            if (after < ntiles) raw = job.fetch((int)after);
+          }
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-          const uint32_t sa = smem_u32(smem + s * stage_bytes);
-          if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * (uint32_t)bytes);
-          job.load(g, k, sa, sa + kGemmOpBytes, map_cluster(&tail->full[s], 0), (int)rank);
+          const uint32_t sa = smem_u32(smem + s * stage_bytes), bar = map_cluster(&tail->full[s], 0);
+          if (n > 0 || k >= early) {
+            if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * (uint32_t)bytes);
+            job.load_a(g, k, sa, bar, (int)rank);
+          }
+          job.load_b(g, k, sa + kGemmOpBytes, bar, (int)rank);
           tail->sent_bytes[rank][s] = (uint32_t)bytes;     // for grp_settle; the odd CTA's are sent over below
           ++iss;
           if (++s == stages) { s = 0; ph ^= 1u; }
         }
         ok = ok && kend == g.kiters;
         if (Job::kDraw && rank == 0 && ok) {
-          if (kend == 0 && after < ntiles) raw = job.fetch((int)after);
+          if (kend == 0 && had) {
+            after = 2ll * pairs + held;
+            if (after < ntiles) raw = job.fetch((int)after);
+          }
           GTile g2 = none;
           if (after < ntiles) g2 = job.make((int)after, raw);
+          drawing = g2.e >= 0;
           ok = publish(n + 2, g2);
           cur = next;
           next = g2;

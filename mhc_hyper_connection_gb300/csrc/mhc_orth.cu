@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(256) orth_scale_kernel(const void* x, int rows
 // Products of a batch of matrices.  kSym: A = B, tiles on and below the diagonal.
 template <bool kA, bool kB, bool kSym>
 struct OrthJob {
-  static constexpr bool kAMn = kA, kBMn = kB, kDraw = false;
+  static constexpr bool kAMn = kA, kBMn = kB, kDraw = false, kEarly = false;
   CUtensorMap a, b;
   GemmShape g;                   // tiles of one matrix
   int count, per, width, kiters;
@@ -191,14 +191,17 @@ struct OrthJob {
   }
   __device__ __forceinline__ int steps(const GTile&, int) const { return kFfnTileK / 16; }
   __device__ __forceinline__ uint32_t idesc(const GTile&) const { return grp_idesc(true, kA, kB, width); }
-  __device__ __forceinline__ void load(const GTile& o, int k, uint32_t sa, uint32_t sb, uint32_t bar, int rank) const {
-    const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf, n0 = o.tn * width + rank * (width >> 1);
+  __device__ __forceinline__ void load_a(const GTile& o, int k, uint32_t sa, uint32_t bar, int rank) const {
+    const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf;
     if constexpr (kA) {
       tma_load_3d_pair(sa, &a, bar, m0, k0, o.e);
       tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, o.e);
     } else {
       tma_load_3d_pair(sa, &a, bar, k0, m0, o.e);
     }
+  }
+  __device__ __forceinline__ void load_b(const GTile& o, int k, uint32_t sb, uint32_t bar, int rank) const {
+    const int k0 = k * kFfnTileK, n0 = o.tn * width + rank * (width >> 1);
     if constexpr (kB) {
       tma_load_3d_pair(sb, &b, bar, n0, k0, o.e);
       if (width > 128) tma_load_3d_pair(sb + 8192, &b, bar, n0 + 64, k0, o.e);
