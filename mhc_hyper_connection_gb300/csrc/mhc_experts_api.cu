@@ -58,6 +58,27 @@ bool map_tokens(CUtensorMap (&m)[4], const void* base, bool f16, uint64_t cols, 
     if (!map_rows(&m[i], base, f16, cols, rows, 16u << i)) return false;
   return true;
 }
+// Columns in blocks of 64, a box of two blocks of 64 rows.  Where the columns are no multiple
+// of 64 the last block runs into the next row (behind the last row: into what follows): it
+// holds columns of the operand whose results are not stored.
+bool map_blocks(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t rows) {
+  const uint64_t d[3] = {64, rows, (cols + 63) / 64}, p[2] = {cols, 64};
+  const uint32_t b[3] = {64, kFfnBoxMn, 2};
+  return map_nd(m, base, f16, 3, d, p, b);
+}
+// An expert's weights MN-major: in blocks where the columns are a multiple of 64 (*blocks =
+// 1), else boxes of 64 columns.
+bool map_weights_mn(CUtensorMap* m, int* blocks, const void* base, bool f16, uint64_t cols, uint64_t rows, uint64_t E) {
+  *blocks = cols % 64 == 0;
+  if (*blocks) {
+    const uint64_t d[4] = {64, rows, cols / 64, E}, p[3] = {cols, 64, cols * rows};
+    const uint32_t b[4] = {64, kFfnBoxMn, 2, 1};
+    return map_nd(m, base, f16, 4, d, p, b);
+  }
+  const uint64_t d[3] = {cols, rows, E}, p[2] = {cols, cols * rows};
+  const uint32_t b[3] = {64, kFfnBoxMn, 1};
+  return map_nd(m, base, f16, 3, d, p, b);
+}
 bool map_weights(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uint64_t rows, uint64_t E, uint32_t box_rows) {
   const uint64_t d[3] = {cols, rows, E}, p[2] = {cols, cols * rows};
   const uint32_t b[3] = {64, box_rows, 1};
@@ -97,7 +118,7 @@ BwdLayout bwd_layout(const PlanLayout& p, int64_t D, int64_t F) {
   l.w_row = l.wa + up256((size_t)p.cap_rows * F * 2);
   l.part = l.w_row + up256((size_t)p.cap_rows * 4);
   l.room = l.part + up256((size_t)p.cap_rows * ((F + 31) / 32) * 4);
-  l.total = l.room + (p.slots > kPartRows ? kRoomBytes : 0);
+  l.total = l.room + (p.slots > kPartRows ? kRoomBytes : 0) + 256;   // map_blocks reads a little past a buffer
   return l;
 }
 
@@ -271,10 +292,12 @@ mhc_status_t mhc_experts_backward_run(const mhc_experts_bwd_args* a, void* strea
   L.part = reinterpret_cast<float*>(ws + l.part);
   L.grad_weights = a->grad_weights;
   L.room = reinterpret_cast<float*>(ws + l.room);
-  if (!map_weights(&L.wd_mn, a->w_down, f16, F, D, E, kFfnBoxMn) || !map_weights(&L.wgu_mn, a->w_gate_up, f16, D, 2 * F, E, kFfnBoxMn) ||
-      !map_tokens(L.gy, L.gys, f16, D, p.cap_rows) || !map_tokens(L.gg, L.gg_buf, f16, 2 * F, p.cap_rows) ||
-      !map_rows(&L.gg_mn, L.gg_buf, f16, 2 * F, p.cap_rows, kFfnBoxMn) || !map_rows(&L.xs_mn, L.xs, f16, D, p.cap_rows, kFfnBoxMn) ||
-      !map_rows(&L.gy_mn, L.gys, f16, D, p.cap_rows, kFfnBoxMn) || !map_rows(&L.wa_mn, L.wa_buf, f16, F, p.cap_rows, kFfnBoxMn))
+  if (!map_weights_mn(&L.wd_mn, &L.wd_blocks, a->w_down, f16, F, D, E) ||
+      !map_weights_mn(&L.wgu_mn, &L.wgu_blocks, a->w_gate_up, f16, D, 2 * F, E) || !map_tokens(L.gy, L.gys, f16, D, p.cap_rows) ||
+      !map_tokens(L.gg, L.gg_buf, f16, 2 * F, p.cap_rows) || !map_blocks(&L.gg_mn, L.gg_buf, f16, 2 * F, p.cap_rows) ||
+      !map_blocks(&L.xs_mn, L.xs, f16, D, p.cap_rows) || !map_blocks(&L.gy_mn, L.gys, f16, D, p.cap_rows) ||
+      !map_blocks(&L.wa_mn, L.wa_buf, f16, F, p.cap_rows) || !map_rows(&L.xs_narrow, L.xs, f16, D, p.cap_rows, kFfnBoxMn) ||
+      !map_rows(&L.wa_narrow, L.wa_buf, f16, F, p.cap_rows, kFfnBoxMn))
     return fail(MHC_ERR_RUNTIME, "encoding a tensor map failed");
   const cudaError_t e = launch_experts_backward(L, f16, s);
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "experts backward launch failed: %s", cudaGetErrorString(e));

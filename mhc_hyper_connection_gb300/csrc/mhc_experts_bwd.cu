@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p,
 
 template <bool F16, int kAct>
 cudaError_t gate_gradients(const ExpertsBwdLaunch& L, cudaStream_t s) {
-  const auto job = experts_job<kRowsMn, F16>(L.wd_mn, L.gy, L.plan, L.F, kFfnTileM, L.D);
+  auto job = experts_job<kRowsMn, F16>(L.wd_mn, L.gy, L.plan, L.F, kFfnTileM, L.D);
+  job.blocks = L.wd_blocks;
   const EpiExpertDgate<F16, kAct> o = {static_cast<const uint16_t*>(L.gate_up), L.w_row, static_cast<uint16_t*>(L.gg_buf),
                                        static_cast<uint16_t*>(L.wa_buf), L.part, L.F, L.lay.cap_rows};
   return launch_group(job, grp_call(L.call, 1, false, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
@@ -80,13 +81,16 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
     job.b[0] = L.xs_mn;
     job.a[1] = L.gy_mn;
     job.b[1] = L.wa_mn;
+    job.narrow[0] = L.xs_narrow;
+    job.narrow[1] = L.wa_narrow;
     job.counts = L.plan.counts;
     job.starts = L.plan.starts;
     job.E = L.E;
     const int M[2] = {2 * F, D}, N[2] = {D, F};
     for (int i = 0; i < 2; ++i) {
-      job.tiles_n[i] = (N[i] + 255) / 256;       // of one width, a multiple of 64
-      job.width[i] = ((N[i] + job.tiles_n[i] - 1) / job.tiles_n[i] + 63) / 64 * 64;
+      const int n256 = (N[i] + 255) / 256, w = (N[i] + n256 - 1) / n256;
+      job.width[i] = w > 128 ? 256 : w > 64 ? 128 : 64;
+      job.tiles_n[i] = (N[i] + job.width[i] - 1) / job.width[i];
       job.area[i] = (M[i] + kFfnTileM - 1) / kFfnTileM * job.tiles_n[i];
       job.by_n[i] = FastDiv((uint32_t)job.tiles_n[i]);
     }
@@ -97,7 +101,8 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   // rows of grad_x over those of x and of grad_y
-  const auto job = experts_job<kRowsMn, F16>(L.wgu_mn, L.gg, L.plan, D, kFfnTileM, 2 * F);
+  auto job = experts_job<kRowsMn, F16>(L.wgu_mn, L.gg, L.plan, D, kFfnTileM, 2 * F);
+  job.blocks = L.wgu_blocks;
   const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D, rows_low_pitch(D)};
   e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
   if (e != cudaSuccess) return e;

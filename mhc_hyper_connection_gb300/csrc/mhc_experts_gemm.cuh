@@ -27,6 +27,7 @@ struct ExpertsJob {
   const int* head;
   const int4* table;
   int tiles_m, kiters;
+  int blocks;                    // kRowsMn: a has blocks of 64 columns as a dimension of its own (columns a multiple of 64)
   FastDiv by_m;
 
   struct Raw {
@@ -71,8 +72,12 @@ struct ExpertsJob {
       tma_load_3d_pair(sa, &a, bar, k0, g.tm * kFfnTileM + rank * kGemmHalf, g.e);
     } else {
       const int m0 = g.tm * kFfnTileM + rank * kGemmHalf;
-      tma_load_3d_pair(sa, &a, bar, m0, k0, g.e);
-      tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, g.e);
+      if (blocks) {
+        tma_load_4d_pair(sa, &a, bar, 0, k0, m0 >> 6, g.e);
+      } else {
+        tma_load_3d_pair(sa, &a, bar, m0, k0, g.e);
+        tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, g.e);
+      }
     }
   }
   __device__ __forceinline__ void load_b(const GTile& g, int k, uint32_t sb, uint32_t bar, int rank) const {
@@ -86,7 +91,10 @@ struct ExpertsJob {
 template <bool F16>
 struct WeightGradJob {
   static constexpr bool kAMn = true, kBMn = true, kDraw = true, kEarly = false;
-  CUtensorMap a[2], b[2];
+  // a, b: blocks of 64 columns are a dimension of their own, so that one copy brings two
+  // (four copies a stage by one thread took twice as long as the products); narrow: b's for
+  // tiles of at most 128 columns
+  CUtensorMap a[2], b[2], narrow[2];
   const int *counts, *starts;
   int E, tiles_n[2], area[2], width[2];
   FastDiv by_expert, by_n[2];
@@ -98,7 +106,7 @@ struct WeightGradJob {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       tma_prefetch_desc(&a[i]);
-      tma_prefetch_desc(&b[i]);
+      tma_prefetch_desc(width[i] > 128 ? &b[i] : &narrow[i]);
     }
   }
   __device__ __forceinline__ int tiles() const { return E * (area[0] + area[1]); }
@@ -127,15 +135,12 @@ struct WeightGradJob {
   __device__ __forceinline__ uint32_t idesc(const GTile& g) const { return grp_idesc(F16, true, true, g.width); }
   __device__ __forceinline__ void load_a(const GTile& g, int k, uint32_t sa, uint32_t bar, int rank) const {
     const int k0 = g.row0 + k * kFfnTileK, m0 = g.tm * kFfnTileM + rank * kGemmHalf;
-    const CUtensorMap* t = g.kind ? &a[1] : &a[0];
-    tma_load_2d_pair(sa, t, bar, m0, k0);
-    tma_load_2d_pair(sa + 8192, t, bar, m0 + 64, k0);
+    tma_load_3d_pair(sa, g.kind ? &a[1] : &a[0], bar, 0, k0, m0 >> 6);
   }
   __device__ __forceinline__ void load_b(const GTile& g, int k, uint32_t sb, uint32_t bar, int rank) const {
     const int k0 = g.row0 + k * kFfnTileK, n0 = g.tn * g.width + rank * (g.width >> 1);
-    const CUtensorMap* t = g.kind ? &b[1] : &b[0];
-    tma_load_2d_pair(sb, t, bar, n0, k0);
-    if (g.width > 128) tma_load_2d_pair(sb + 8192, t, bar, n0 + 64, k0);
+    if (g.width > 128) tma_load_3d_pair(sb, g.kind ? &b[1] : &b[0], bar, 0, k0, n0 >> 6);
+    else tma_load_2d_pair(sb, g.kind ? &narrow[1] : &narrow[0], bar, n0, k0);
   }
 };
 
@@ -440,7 +445,9 @@ struct ExpertsFwdLaunch {
 cudaError_t launch_experts_forward(const ExpertsFwdLaunch& L, bool f16, cudaStream_t s);
 
 struct ExpertsBwdLaunch {
-  CUtensorMap wd_mn, wgu_mn, gy[4], gg[4], gg_mn, xs_mn, gy_mn, wa_mn;
+  CUtensorMap wd_mn, wgu_mn, gy[4], gg[4];
+  CUtensorMap gg_mn, xs_mn, gy_mn, wa_mn, xs_narrow, wa_narrow;
+  int wd_blocks, wgu_blocks;                   // ExpertsJob::blocks
   ExpertsCall call;
   PlanView plan;
   PlanLayout lay;
@@ -472,6 +479,7 @@ ExpertsJob<kRows, F16> experts_job(const CUtensorMap& a, const CUtensorMap (&b)[
   ExpertsJob<kRows, F16> j;
   j.a = a;
   for (int i = 0; i < 4; ++i) j.b[i] = b[i];
+  j.blocks = 0;
   j.head = p.head;
   j.table = p.table;
   j.tiles_m = (m + per_tile - 1) / per_tile;

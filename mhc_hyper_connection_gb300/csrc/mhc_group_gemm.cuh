@@ -15,6 +15,7 @@
 
 namespace mhc {
 
+constexpr int kGrpThreads = 352;                     // producer, MMA issuer, 2 x 4 epilogue warps, scheduler
 constexpr int kGrpMaxStages = 12;
 constexpr int kGrpRing = 6 * 32768;                  // bytes of the ring of stages
 constexpr int kGrpDeepest = 512;                     // chunks of the depth that one accumulator sums at most (kDeepest)
@@ -56,6 +57,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
@@ -132,7 +141,7 @@ __host__ __device__ constexpr uint32_t grp_idesc(bool f16, bool a_mn, bool b_mn,
 //   Pre, void pre(tile, Pre&, rank, q, grp, lane)   loads ahead of a tile's sums
 //   void tile(tile, Pre&, part, parts, taddr, rank, q, grp, buf, lane, pair)
 template <class Job, class Epi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
     group_gemm_kernel(const __grid_constant__ Job job, const GrpCall call, const __grid_constant__ Epi epi) {
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -157,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < kSchedSlots; ++b) {
       mbar_init(&tail->sched_full[b], 1);
-      mbar_init(&tail->sched_empty[b], 18);
+      mbar_init(&tail->sched_empty[b], 19);      // MMA issuer, both producers, eight epilogue warps of each CTA
     }
     mbar_init(&tail->mma_done, 1);
     tail->abort = 0u;
@@ -179,7 +188,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   pdl_trigger();
   // Operands and the counter are earlier launches'.  The producers of a job whose A is not
   // (an expert's weights) begin with it before they wait.
-  if (!Job::kEarly || warp != 0) pdl_wait();
+  const bool scheduler = warp == 10;
+  if (!Job::kEarly || (warp != 0 && !scheduler)) pdl_wait();
   const int ntiles = job.tiles();
 
   // The n-th tile of this pair as the roles see it (e = -1 after the last, and when
@@ -222,95 +232,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       uint32_t ph = 0;
       long long iss = 0;
       bool ok = true;
-      auto publish = [&](int n, const GTile& g) -> bool {
-        const int slot = n % kSchedSlots;
-        if (!wait_slow(&tail->sched_empty[slot], ((uint32_t)(n / kSchedSlots) & 1u) ^ 1u, ctl, kErrClusterWait, true)) return false;
-        const int4 lo = make_int4(g.e, g.tm, g.tn, g.row0), hi = make_int4(g.rows, g.width, g.kiters, g.kind);
-#pragma unroll
-        for (uint32_t r = 0; r < 2; ++r) {
-          const uint32_t at = map_cluster(&tail->sched[slot], r), bar = map_cluster(&tail->sched_full[slot], r);
-          expect_tx_relaxed(bar, 32u);
-          st_async_v4(at, lo, bar);
-          st_async_v4(at + 16, hi, bar);
-        }
-        return true;
-      };
-      // The first two tiles of a pair are dealt out, the others drawn: the ticket of tile n +
-      // 3 and what tile n + 2 needs from memory are on their way under tile n's copies, and
-      // nothing is computed from either before they are needed, so that neither latency
-      // stands before a copy.
-      GTile none, cur, next;
-      none.e = -1;
-      none.tm = none.tn = none.row0 = none.rows = none.width = none.kiters = none.kind = 0;
-      cur = next = none;
-      uint32_t ticket = 0;
-      bool drawing = false;                      // a ticket is held or on its way
-      if (Job::kDraw && rank == 0) {
-        const int t0 = pair, t1 = pair + pairs;
-        typename Job::Raw r0, r1;
-        if (t0 < ntiles) r0 = job.fetch(t0);
-        if (t1 < ntiles) r1 = job.fetch(t1);
-        if (t0 < ntiles) cur = job.make(t0, r0);
-        if (t1 < ntiles) next = job.make(t1, r1);
-        ok = publish(0, cur) && publish(1, next);
-        drawing = t1 < ntiles;
-      }
-      int early = 0;                             // chunks of the first tile whose A is on its way
+      GTile first;                               // the pair's first tile, known without the scheduler
+      int early = 0;                             // chunks of it whose A is on its way
+      const uint32_t ring = smem_u32(smem), full0 = map_cluster(&tail->full[0], 0);
       if constexpr (Job::kEarly) {
-        if (rank == 1 && pair < ntiles) cur = job.make(pair, job.fetch(pair));
-        if (cur.e >= 0 && !call.withhold) {
-          early = min(stages, cur.kiters);
+        first.e = -1;
+        if (pair < ntiles) first = job.make(pair, job.fetch(pair));
+        if (first.e >= 0 && !call.withhold) {
+          early = min(stages, first.kiters);
           for (int k = 0; k < early; ++k) {
-            if (rank == 0) mbar_expect_tx(&tail->full[k], 2u * (uint32_t)job.bytes(cur));
-            job.load_a(cur, k, smem_u32(smem + k * stage_bytes), map_cluster(&tail->full[k], 0), (int)rank);
+            if (rank == 0) mbar_expect_tx(&tail->full[k], 2u * (uint32_t)job.bytes(first));
+            job.load_a(first, k, ring + k * stage_bytes, full0 + 8 * k, (int)rank);
           }
         }
         pdl_wait();
       }
-      if (drawing) ticket = atomicAdd(call.counter, 1u);
       for (int n = 0; ok; ++n) {
-        GTile g = cur;
-        if (!Job::kDraw || rank == 1) g = tile_of(n, false);
-        if (n == 0 && early) g = cur;            // its copies are completed whatever became of that wait
+        GTile g = tile_of(n, false);
+        if (n == 0 && early) g = first;          // its copies are completed whatever became of that wait
         if (g.e < 0) break;
-        const int bytes = job.bytes(g);
+        const uint32_t bytes = (uint32_t)job.bytes(g);
         // test hook, as in ffn_gemm_kernel
         const int kend = call.withhold && pair < 2 && n == 0 ? max(g.kiters - 1 - (int)(rank ^ (uint32_t)pair), 0) : g.kiters;
-        const uint32_t held = ticket;
-        const bool had = drawing;
-        typename Job::Raw raw;
-        long long after = ntiles;
-        const int half = kend >> 1;
-        if (had) ticket = atomicAdd(call.counter, 1u);
         for (int k = 0; k < kend; ++k) {
-          if (k == half && had) {
-            after = 2ll * pairs + held;
-            if (after < ntiles) raw = job.fetch((int)after);
-          }
           if (!wait_stage(&tail->empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-          const uint32_t sa = smem_u32(smem + s * stage_bytes), bar = map_cluster(&tail->full[s], 0);
+          const uint32_t sa = ring + s * stage_bytes, bar = full0 + 8 * s;
           if (n > 0 || k >= early) {
-            if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * (uint32_t)bytes);
+            if (rank == 0) mbar_expect_tx(&tail->full[s], 2u * bytes);
             job.load_a(g, k, sa, bar, (int)rank);
           }
           job.load_b(g, k, sa + kGemmOpBytes, bar, (int)rank);
-          tail->sent_bytes[rank][s] = (uint32_t)bytes;     // for grp_settle; the odd CTA's are sent over below
+          tail->sent_bytes[rank][s] = bytes;     // for grp_settle; the odd CTA's are sent over below
           ++iss;
           if (++s == stages) { s = 0; ph ^= 1u; }
         }
         ok = ok && kend == g.kiters;
-        if (Job::kDraw && rank == 0 && ok) {
-          if (kend == 0 && had) {
-            after = 2ll * pairs + held;
-            if (after < ntiles) raw = job.fetch((int)after);
-          }
-          GTile g2 = none;
-          if (after < ntiles) g2 = job.make((int)after, raw);
-          drawing = g2.e >= 0;
-          ok = publish(n + 2, g2);
-          cur = next;
-          next = g2;
-        }
       }
       if (rank == 1) {
         const uint32_t at = map_cluster(&tail->sent_bytes[1][0], 0);
@@ -363,6 +319,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if ((!ok || *ctl.abort) && lane == 0) grp_settle(tail, ctl.wait_ns, stages);
       __syncwarp();
     }
+  } else if (scheduler) {
+    // ===================================================== scheduler
+    // A warp of its own: in the producer, drawing and handing out a tile held up copies for
+    // a thousand clocks a tile, and its code for half a stage in every stage.
+    if (Job::kDraw && rank == 0 && lane == 0) {
+      GTile none;
+      none.e = -1;
+      none.tm = none.tn = none.row0 = none.rows = none.width = none.kiters = none.kind = 0;
+      auto publish = [&](int n, const GTile& g) -> bool {
+        const int slot = n % kSchedSlots;
+        if (!wait_slow(&tail->sched_empty[slot], ((uint32_t)(n / kSchedSlots) & 1u) ^ 1u, ctl, kErrClusterWait, true)) return false;
+        const int4 lo = make_int4(g.e, g.tm, g.tn, g.row0), hi = make_int4(g.rows, g.width, g.kiters, g.kind);
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r) {
+          const uint32_t at = map_cluster(&tail->sched[slot], r), bar = map_cluster(&tail->sched_full[slot], r);
+          expect_tx_relaxed(bar, 32u);
+          st_async_v4(at, lo, bar);
+          st_async_v4(at + 16, hi, bar);
+        }
+        return true;
+      };
+      // The first two tiles of a pair are dealt out, the others drawn.
+      int t = pair;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        GTile g = none;
+        if (t < ntiles) g = job.make(t, job.fetch(t));
+        ok = publish(n, g) && g.e >= 0;
+        if (n == 0) t = pair + pairs;
+        if (n == 1 && Job::kEarly) pdl_wait();   // the counter is the first launch's
+        if (n >= 1 && ok) {
+          const unsigned drawn = 2u * (unsigned)pairs + atomicAdd(call.counter, 1u);
+          t = drawn < (unsigned)ntiles ? (int)drawn : ntiles;
+        }
+      }
+    }
   } else {
     // ===================================================== epilogue
     const int grp = (warp - 2) >> 2, q = warp & 3;
@@ -414,7 +406,7 @@ cudaError_t launch_group(const Job& job, const GrpCall& call, const Epi& epi, lo
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(kGrpThreads);
   cfg.dynamicSmemBytes = kGrpSmem;
   int pairs = known[dev].load(std::memory_order_relaxed);
   if (pairs == 0) {

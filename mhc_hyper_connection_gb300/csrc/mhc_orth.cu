@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(256) orth_scale_kernel(const void* x, int rows
 template <bool kA, bool kB, bool kSym>
 struct OrthJob {
   static constexpr bool kAMn = kA, kBMn = kB, kDraw = false, kEarly = false;
-  CUtensorMap a, b;
+  CUtensorMap a, b;              // MN-major: blocks of 64 columns are a dimension of their own
+                                 // (b's of tiles narrower than 256 not)
   GemmShape g;                   // tiles of one matrix
   int count, per, width, kiters;
   int split;                     // log2(256 / width)
@@ -194,8 +195,7 @@ struct OrthJob {
   __device__ __forceinline__ void load_a(const GTile& o, int k, uint32_t sa, uint32_t bar, int rank) const {
     const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf;
     if constexpr (kA) {
-      tma_load_3d_pair(sa, &a, bar, m0, k0, o.e);
-      tma_load_3d_pair(sa + 8192, &a, bar, m0 + 64, k0, o.e);
+      tma_load_4d_pair(sa, &a, bar, 0, k0, m0 >> 6, o.e);
     } else {
       tma_load_3d_pair(sa, &a, bar, k0, m0, o.e);
     }
@@ -203,8 +203,8 @@ struct OrthJob {
   __device__ __forceinline__ void load_b(const GTile& o, int k, uint32_t sb, uint32_t bar, int rank) const {
     const int k0 = k * kFfnTileK, n0 = o.tn * width + rank * (width >> 1);
     if constexpr (kB) {
-      tma_load_3d_pair(sb, &b, bar, n0, k0, o.e);
-      if (width > 128) tma_load_3d_pair(sb + 8192, &b, bar, n0 + 64, k0, o.e);
+      if (width > 128) tma_load_4d_pair(sb, &b, bar, 0, k0, n0 >> 6, o.e);
+      else tma_load_3d_pair(sb, &b, bar, n0, k0, o.e);
     } else {
       tma_load_3d_pair(sb, &b, bar, k0, n0, o.e);
     }
@@ -327,7 +327,7 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
   l.x[1] = l.x[0] + xb;
   l.p = l.x[1] + xb;
   l.q = l.p + pb;
-  l.total = l.q + pb;
+  l.total = l.q + pb + 256;                     // orth_map_blocks reads a little past a buffer
   return l;
 }
 
@@ -338,6 +338,18 @@ bool orth_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int6
   cuuint64_t st[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(pitch * rows) * 2};
   cuuint32_t b[3] = {64, box_rows, 1}, es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// MN-major: boxes of two blocks of 64 columns; the last block may run into a row's padding
+// and the next row, whose results are not kept.
+bool orth_map_blocks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch, int64_t batch) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[4] = {64, (cuuint64_t)rows, (cuuint64_t)(cols + 63) / 64, (cuuint64_t)batch};
+  cuuint64_t st[3] = {(cuuint64_t)pitch * 2, 128, (cuuint64_t)(pitch * rows) * 2};
+  cuuint32_t b[4] = {64, kFfnBoxMn, 2, 1}, es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -384,8 +396,10 @@ cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* ma
   OrthJob<kA, kB, kSym> job;
   job.width = tile_width(p.batch, p.M, p.N, p.K, kSym, p.sms);
   job.split = job.width == 256 ? 0 : job.width == 128 ? 1 : 2;
-  *mapped = orth_map(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch, kA ? kFfnBoxMn : (uint32_t)kGemmHalf) &&
-            orth_map(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)job.width / 2);
+  *mapped = (kA ? orth_map_blocks(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch)
+                : orth_map(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch, (uint32_t)kGemmHalf)) &&
+            (kB && job.width > 128 ? orth_map_blocks(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch)
+                                   : orth_map(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)job.width / 2));
   if (!*mapped) return cudaErrorInvalidValue;
   GemmShape& g = job.g;
   g = GemmShape();
