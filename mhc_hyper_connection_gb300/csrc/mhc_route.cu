@@ -144,6 +144,32 @@ __device__ __forceinline__ uint32_t choose_groups(K mark, const RouteArgs& a, fl
   return stays;
 }
 
+// Lane j < n has the j-th of a row's experts by fp32 keys, `after` is the next one (or -1):
+// the n first of them by fp64 keys.  Sigmoid scores with a bias.
+template <int kType>
+__device__ __noinline__ int reorder64(const RouteArgs& a, long long row, int mine, int after, int n, int lane) {
+  auto key_of = [&](int e) {
+    return 1.0 / (1.0 + exp(-(double)load_logit<kType>(a.logits, row * a.E + e))) + (double)a.bias[e];
+  };
+  const double key = lane < n ? key_of(mine) : 0.0;
+  const double key2 = after >= 0 ? key_of(after) : 0.0;
+  int rank = 0, rank2 = 0;                       // how many stand before
+  for (int i = 0; i < n; ++i) {
+    const double o = __shfl_sync(kFull, key, i);
+    const int e = __shfl_sync(kFull, mine, i);
+    rank += order(o) > order(key) || (order(o) == order(key) && e < mine);
+    rank2 += order(o) > order(key2) || (order(o) == order(key2) && e < after);
+  }
+  if (after >= 0) rank += order(key2) > order(key) || (order(key2) == order(key) && after < mine);
+  int got = -1;
+  for (int i = 0; i < n; ++i) {
+    const int r = __shfl_sync(kFull, rank, i), e = __shfl_sync(kFull, mine, i);
+    if (r == lane) got = e;
+  }
+  if (after >= 0 && rank2 == lane) got = after;
+  return lane < n ? got : -1;
+}
+
 // The choice from keys of type K: experts lane * V + i are a lane's.  Returns, in lane j <
 // k, the j-th expert (or -1).  With K = float, `unsure` is set where two keys that decide
 // something are so close that they may stand in the wrong order: closer than tol (smax +
@@ -251,9 +277,10 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
 #pragma unroll
     for (int i = 0; i < V; ++i) best = u[i] > best ? u[i] : best;
   }
-  int mine = -1, after = -1, found = 0;
-  U mykey = kOut, afterkey = kOut;
-  const int rounds = kCheck && by_key ? k + 1 : k;
+  // lane j's; of the two behind the chosen (kCheck) in every lane
+  int mine = -1, found = 0, after = -1;
+  U mykey = kOut, afterkey = kOut, thirdkey = kOut;
+  const int rounds = kCheck && by_key ? k + 2 : k;
   for (int j = 0; j < rounds; ++j) {
     if constexpr (kSorted) best = u[0];
     const U m = warp_max(best);
@@ -285,48 +312,100 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
       e = __shfl_sync(kFull, e, w);
     }
     ++found;
-    if (lane == j) {
+    if (lane == j && j < k) {
       mine = e;
       mykey = m;
     }
-    after = e;
-    afterkey = m;
+    if (j == k) {
+      after = e;
+      afterkey = m;
+    }
+    if (j == k + 1) thirdkey = m;
   }
   if constexpr (kCheck) {
-    if (by_key && found > 1) {
-      // lane j against the next one; the last against the first that was left out
-      const int last = found - 1;
+    if (by_key && found > 1 && !unsure) {
+      // lane j against the next one, the last against the first that was left out
+      const int chosen = min(k, found), pairs = min(k, found - 1);
       int ne = __shfl_down_sync(kFull, mine, 1);
       U nk = __shfl_down_sync(kFull, mykey, 1);
-      if (lane == 31) {
+      if (lane == k - 1) {
         ne = after;
         nk = afterkey;
       }
       const float x = unorder(mykey), y = unorder(nk);
-      bool near = lane < last && x - y <= tol * (smax + fmaxf(fabsf(x), fabsf(y)));
+      bool near = lane < pairs && x - y <= tol * (smax + fmaxf(fabsf(x), fabsf(y)));
       if (__any_sync(kFull, near)) {
         // equal numbers in give equal keys: the index decides, nothing to look at
         if (near)
           near = !(load_logit<kType>(a.logits, row * E + mine) == load_logit<kType>(a.logits, row * E + ne) &&
                    a.bias[mine] == a.bias[ne]);
-        unsure = unsure || __any_sync(kFull, near);
+        if (__any_sync(kFull, near)) {
+          // Where the second left out is clearly behind the last chosen, the order among the
+          // chosen and the first left out is all there is to find.
+          const float last = unorder(__shfl_sync(kFull, mykey, chosen - 1)), third = unorder(thirdkey);
+          if (!a.sigmoid || (found > k + 1 && last - third <= tol * (smax + fmaxf(fabsf(last), fabsf(third))))) {
+            unsure = true;
+          } else {
+            mine = reorder64<kType>(a, row, mine, found > k ? after : -1, chosen, lane);
+          }
+        }
       }
     }
   }
   return lane < k ? mine : -1;
 }
 
+// A lane's V scores of a row, -inf behind the last.
+template <int kType, int V>
+__device__ __forceinline__ void load_row(const RouteArgs& a, long long row, int lane, float (&l)[V]) {
+  const int E = a.E, e0 = lane * V;
+  const long long base = row * E + e0;
+  bool loaded = false;
+  if constexpr (V >= 4) {
+    if (E % 4 == 0) {                          // rows stay aligned to four elements
+      loaded = true;
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        if (e0 + i < E) {
+          if constexpr (kType == MHC_DTYPE_FP32) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + i);
+            l[i] = v.x;
+            l[i + 1] = v.y;
+            l[i + 2] = v.z;
+            l[i + 3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + base + i);
+            constexpr bool f16 = kType == MHC_DTYPE_FP16;
+            const float2 p = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.x));
+            const float2 q = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.y));
+            l[i] = p.x;
+            l[i + 1] = p.y;
+            l[i + 2] = q.x;
+            l[i + 3] = q.y;
+          }
+        } else {
+          l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+        }
+      }
+    }
+  }
+  if (!loaded) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_logit<kType>(a.logits, base + i) : -INFINITY;
+  }
+}
+
 // The choice once more with keys in fp64, for rows where fp32 left two keys too close: some
 // of a thousand of ordinary rows with a bias or groups.
 template <int kType, int V>
-__device__ __noinline__ int choose64(const RouteArgs& a, long long row, const float* logits, float top, double* room, int lane) {
+__device__ __noinline__ int choose64(const RouteArgs& a, long long row, float top, double* room, int lane) {
   const int e0 = lane * V;
   float l[V];
+  load_row<kType, V>(a, row, lane, l);
   double key[V];
   RowSum<double> r = {top, 0.0};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    l[i] = logits[i];
     key[i] = l[i] == -INFINITY ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)top);
     r.sum += key[i];
   }
@@ -343,7 +422,7 @@ __device__ __noinline__ int choose64(const RouteArgs& a, long long row, const fl
 
 // V: consecutive scores of a lane.
 template <int kType, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, V <= 4 ? 8 : V <= 8 ? 6 : V <= 16 ? 4 : 2) route_kernel(const RouteArgs a) {
   extern __shared__ double route_keys[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k, e0 = lane * V;
@@ -351,42 +430,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   float bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
-  for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
+  float ahead[V];
+  const long long row0 = (long long)blockIdx.x * kRouteWarps + warp;
+  if (row0 < a.T) load_row<kType, V>(a, row0, lane, ahead);
+  for (long long row = row0; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
     float l[V];
-    const long long base = row * E + e0;
-    bool loaded = false;
-    if constexpr (V >= 4) {
-      if (E % 4 == 0) {                          // rows stay aligned to four elements
-        loaded = true;
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          if (e0 + i < E) {
-            if constexpr (kType == MHC_DTYPE_FP32) {
-              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + i);
-              l[i] = v.x;
-              l[i + 1] = v.y;
-              l[i + 2] = v.z;
-              l[i + 3] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + base + i);
-              constexpr bool f16 = kType == MHC_DTYPE_FP16;
-              const float2 p = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.x));
-              const float2 q = XType<f16>::to_f2(*reinterpret_cast<const typename XType<f16>::T2*>(&v.y));
-              l[i] = p.x;
-              l[i + 1] = p.y;
-              l[i + 2] = q.x;
-              l[i + 3] = q.y;
-            }
-          } else {
-            l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
-          }
-        }
-      }
-    }
-    if (!loaded) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_logit<kType>(a.logits, base + i) : -INFINITY;
-    }
+    for (int i = 0; i < V; ++i) l[i] = ahead[i];
+    const long long next = row + (long long)gridDim.x * kRouteWarps;
+    if (next < a.T) load_row<kType, V>(a, next, lane, ahead);
     // Scores; softmax: top and sum of the row.
     uint32_t topu = Ordered<float>::kOut;
 #pragma unroll
@@ -431,12 +483,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     const float tol = a.sigmoid ? 0x1p-19f : (V + 24) * 0x1p-23f;
     bool unsure = false;
     int mine = choose<kType, float, V>(a, row, l, key, r, smax, tol, reinterpret_cast<float*>(keys64), lane, unsure);
-    if (unsure) {
-      float kept[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) kept[i] = l[i];
-      mine = choose64<kType, V>(a, row, kept, top, keys64, lane);
-    }
+    if (unsure) mine = choose64<kType, V>(a, row, top, keys64, lane);
     const float myl = mine >= 0 ? load_logit<kType>(a.logits, row * E + mine) : -INFINITY;
     const float sum = r.sum;
     // Weights: lane j has slot j.
@@ -787,8 +834,8 @@ mhc_status_t route_device(int* sms) {
   *sms = di.sms;
   return MHC_OK;
 }
-unsigned row_blocks(int64_t T, int sms) {
-  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)sms * 16;
+unsigned row_blocks(int64_t T, int sms, int per_sm) {
+  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)sms * per_sm;
   return (unsigned)(b < most ? b : most);
 }
 size_t elem_bytes(int32_t dtype) { return dtype == MHC_DTYPE_FP32 ? 4 : 2; }
@@ -799,8 +846,8 @@ template <int kType>
 cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
   // where no key is formed again and no group is marked nothing is kept in shared memory
   const size_t smem = a.bias || a.groups > 1 ? (size_t)kRouteWarps * a.E * 8 : 0;
-  const unsigned grid = row_blocks(a.T, sms);
   const int v = (a.E + 31) / 32;
+  const unsigned grid = row_blocks(a.T, sms, v <= 4 ? 8 : v <= 8 ? 6 : v <= 16 ? 4 : 2);   // as many as run at once
   if (v <= 1) route_kernel<kType, 1><<<grid, kRouteWarps * 32, smem, s>>>(a);
   else if (v <= 2) route_kernel<kType, 2><<<grid, kRouteWarps * 32, smem, s>>>(a);
   else if (v <= 4) route_kernel<kType, 4><<<grid, kRouteWarps * 32, smem, s>>>(a);
@@ -872,7 +919,7 @@ mhc_status_t mhc_route_backward_run(const mhc_route_bwd_args* a, void* stream) {
   const RouteBwdArgs r = {a->logits, a->experts, a->grad_weights, a->grad_logits, a->T, (int)a->E, (int)a->k,
                           a->score == MHC_SCORE_SIGMOID, a->renormalise, a->scale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = row_blocks(a->T, sms);
+  const unsigned grid = row_blocks(a->T, sms, 16);
   const size_t smem = (size_t)kRouteWarps * ((a->E + 3) & ~int64_t(3)) * 4;
   if (a->dtype == MHC_DTYPE_FP32) route_backward_kernel<MHC_DTYPE_FP32><<<grid, kRouteWarps * 32, smem, s>>>(r);
   else if (a->dtype == MHC_DTYPE_BF16) route_backward_kernel<MHC_DTYPE_BF16><<<grid, kRouteWarps * 32, smem, s>>>(r);
