@@ -48,14 +48,17 @@ inline PlanLayout plan_layout(int64_t T, int64_t k, int64_t E) {
 // A plan on the device.  Table entry i (two int4): {expert, first entry of its band,
 // entries of the band, first row of the band}, {rows of the band, rows of a tile, how many
 // of the band's first tiles have 32 more}.
+// What is read from it is held inside these bounds, so a buffer that no plan was
+// written to gives wrong numbers and nothing worse.
 struct PlanView {
   int *head, *counts, *starts, *places, *rows, *scratch;
   int4* table;
-  int width;
+  int width, E, slots, cap_rows, cap_tiles;
 };
-inline PlanView plan_view(const PlanLayout& l, void* plan) {
+inline PlanView plan_view(const PlanLayout& l, int64_t E, void* plan) {
   int* p = static_cast<int*>(plan);
-  return {p, p + l.counts, p + l.starts, p + l.places, p + l.rows, p + l.scratch, reinterpret_cast<int4*>(p + l.table), l.width};
+  return {p, p + l.counts, p + l.starts, p + l.places, p + l.rows, p + l.scratch, reinterpret_cast<int4*>(p + l.table), l.width,
+          (int)E, (int)l.slots, (int)l.cap_rows, (int)l.cap_tiles};
 }
 
 }  // namespace mhc

@@ -194,7 +194,7 @@ mhc_status_t mhc_experts_run(const mhc_experts_args* a, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   ExpertsFwdLaunch L;
   L.call = call(ws, a->wait_limit_us, a->withhold_copy, sms);
-  L.plan = plan_view(p, const_cast<void*>(a->plan));
+  L.plan = plan_view(p, E, const_cast<void*>(a->plan));
   L.lay = p;
   L.T = T;
   L.E = (int)E;
@@ -269,7 +269,7 @@ mhc_status_t mhc_experts_backward_run(const mhc_experts_bwd_args* a, void* strea
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   ExpertsBwdLaunch L;
   L.call = call(ws, a->wait_limit_us, a->withhold_copy, sms);
-  L.plan = plan_view(p, const_cast<void*>(a->plan));
+  L.plan = plan_view(p, E, const_cast<void*>(a->plan));
   L.lay = p;
   L.T = T;
   L.E = (int)E;

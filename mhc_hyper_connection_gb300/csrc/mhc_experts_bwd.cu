@@ -13,9 +13,11 @@ __global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, 
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
-  const long long items = (long long)p.head[1] * segs;
+  const long long items = (long long)min(p.head[1], p.cap_rows) * segs;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
-    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs), slot = p.rows[r];
+    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs);
+    int slot = p.rows[r];
+    if (slot >= p.slots) slot = -1;
     gather_item(slot, k, r, seg, D, x, xs, lane);
     gather_item(slot, k, r, seg, D, gy, gys, lane);
     if (seg == 0) {
@@ -38,12 +40,13 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p,
                                                                uint16_t* grad_x, float* grad_weights) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
-  const long long groups = (p.head[1] + 31) / 32;
+  const int used = min(p.head[1], p.cap_rows);
+  const long long groups = (max(used, 0) + 31) / 32;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs + groups; i += (long long)gridDim.x * 8) {
     if (i < groups) {
       const long long r = i * 32 + lane;
-      const int slot = r < p.head[1] ? p.rows[r] : -1;
-      if (slot >= 0) {
+      const int slot = r < used ? p.rows[r] : -1;
+      if (slot >= 0 && slot < p.slots) {
         float sum = 0.0f;
 #pragma unroll 8
         for (int n = 0; n < parts; ++n) sum += part[n * cap_rows + r];
@@ -51,7 +54,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p,
       }
     } else {
       const long long item = i - groups, t = item / segs;
-      combine_item<F16>(item, segs, k, D, p.places, nullptr, hi, lo, lo_pitch, grad_x, lane);
+      combine_item<F16>(item, segs, k, D, p.places, nullptr, p.cap_rows, hi, lo, lo_pitch, grad_x, lane);
       if (item == t * segs && lane < k && p.places[t * k + lane] < 0) grad_weights[t * k + lane] = 0.0f;
     }
   }
@@ -86,6 +89,7 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
     job.counts = L.plan.counts;
     job.starts = L.plan.starts;
     job.E = L.E;
+    job.cap_rows = L.plan.cap_rows;
     const int M[2] = {2 * F, D}, N[2] = {D, F};
     for (int i = 0; i < 2; ++i) {
       const int n256 = (N[i] + 255) / 256, w = (N[i] + n256 - 1) / n256;

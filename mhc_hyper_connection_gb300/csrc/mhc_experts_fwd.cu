@@ -10,10 +10,11 @@ __global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const Pla
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
-  const long long items = (long long)p.head[1] * segs;
+  const long long items = (long long)min(p.head[1], p.cap_rows) * segs;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
     const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs);
-    gather_item(p.rows[r], k, r, seg, D, x, xs, lane);
+    const int slot = p.rows[r];
+    gather_item(slot < p.slots ? slot : -1, k, r, seg, D, x, xs, lane);
   }
 }
 
@@ -23,7 +24,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const PlanView p, long lon
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
   for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs; i += (long long)gridDim.x * 8)
-    combine_item<F16>(i, segs, k, D, p.places, weights, hi, lo, lo_pitch, y, lane);
+    combine_item<F16>(i, segs, k, D, p.places, weights, p.cap_rows, hi, lo, lo_pitch, y, lane);
 }
 
 template <bool F16, bool kKept, int kAct>

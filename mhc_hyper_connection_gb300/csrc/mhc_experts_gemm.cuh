@@ -26,6 +26,7 @@ struct ExpertsJob {
   CUtensorMap a, b[4];           // b: boxes of 16, 32, 64 and 128 tokens
   const int* head;
   const int4* table;
+  int E, width, cap_rows, cap_tiles;
   int tiles_m, kiters;
   int blocks;                    // kRowsMn: a has blocks of 64 columns as a dimension of its own (columns a multiple of 64)
   FastDiv by_m;
@@ -38,7 +39,7 @@ struct ExpertsJob {
 #pragma unroll
     for (int i = 0; i < 4; ++i) tma_prefetch_desc(&b[i]);
   }
-  __device__ __forceinline__ int tiles() const { return head[2] * tiles_m; }
+  __device__ __forceinline__ int tiles() const { return min(max(head[2], 0), cap_tiles) * tiles_m; }
   __device__ __forceinline__ Raw fetch(int t) const {
     const int i = by_m(t);
     return {table[2 * i], table[2 * i + 1]};
@@ -46,14 +47,15 @@ struct ExpertsJob {
   // Tile t: the tiles of a band share a tile of the weights one after the other.
   __device__ __forceinline__ GTile make(int t, const Raw& w) const {
     GTile g;
-    const int r = t - w.lo.y * tiles_m, j = r % w.lo.z, off = j * w.hi.y + 32 * min(j, w.hi.z);
-    g.e = w.lo.x;
-    g.tm = r / w.lo.z;
+    const int r = t - w.lo.y * tiles_m, n = max(w.lo.z, 1), j = r % n, off = j * w.hi.y + 32 * min(j, w.hi.z);
+    g.e = min(max(w.lo.x, 0), E - 1);
+    g.tm = min(max(r / n, 0), tiles_m - 1);
     g.tn = 0;
-    g.row0 = w.lo.w + off;
-    g.rows = min(w.hi.y + (j < w.hi.z ? 32 : 0), w.hi.x - off);
+    g.row0 = min(max(w.lo.w + off, 0), cap_rows);
+    g.rows = min(min(w.hi.y + (j < w.hi.z ? 32 : 0), w.hi.x - off), min(width, cap_rows - g.row0));
+    g.rows = max(g.rows, 0);
     g.width = (g.rows + 31) & ~31;
-    g.kiters = kiters;
+    g.kiters = g.rows ? kiters : 0;
     g.kind = 0;
     return g;
   }
@@ -96,7 +98,7 @@ struct WeightGradJob {
   // tiles of at most 128 columns
   CUtensorMap a[2], b[2], narrow[2];
   const int *counts, *starts;
-  int E, tiles_n[2], area[2], width[2];
+  int E, cap_rows, tiles_n[2], area[2], width[2];
   FastDiv by_expert, by_n[2];
 
   struct Raw {
@@ -122,10 +124,10 @@ struct WeightGradJob {
     r -= g.kind ? area[0] : 0;
     g.tm = g.kind ? by_n[1](r) : by_n[0](r);
     g.tn = r - g.tm * tiles_n[g.kind];
-    g.row0 = w.start;
-    g.rows = w.count;
+    g.row0 = min(max(w.start, 0), cap_rows);
+    g.rows = min(max(w.count, 0), cap_rows - g.row0);
     g.width = width[g.kind];
-    g.kiters = (w.count + kFfnTileK - 1) / kFfnTileK;
+    g.kiters = (g.rows + kFfnTileK - 1) / kFfnTileK;
     return g;
   }
   __device__ __forceinline__ int bytes(const GTile& g) const { return kGemmOpBytes + (g.width > 128 ? 16384 : 8192); }
@@ -355,24 +357,6 @@ struct EpiExpertDgate {
   }
 };
 
-#ifdef WG_CS
-__device__ __forceinline__ void stage_flush_cs(const uint8_t* buf, uint8_t* base, size_t pitch, int rows, int bytes, int lane) {
-  __syncwarp();
-  const int c = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + (lane >> 3);
-    const uint4 v = *reinterpret_cast<const uint4*>(buf + sw128(r, c));
-    if (r < rows && c * 16 < bytes) __stcs(reinterpret_cast<uint4*>(base + (size_t)r * pitch + c * 16), v);
-  }
-  __syncwarp();
-}
-#define STAGE_FLUSH stage_flush_cs
-#elif defined(WG_NONE)
-#define STAGE_FLUSH(...) __syncwarp()
-#else
-#define STAGE_FLUSH stage_flush
-#endif
 // out[e][m, n] of either weight gradient; an expert without rows gets zeros.  A sum
 // in several parts is joined in fp32 in a room of the warp's own.
 template <bool F16>
@@ -414,7 +398,7 @@ struct EpiWeightGrad {
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + sw128(lane, h * 4 + i)) = pack8v<F16>(v + 8 * i);
       }
       if (parts <= 1 || p + 1 == parts)
-        STAGE_FLUSH(buf, reinterpret_cast<uint8_t*>(o + (size_t)m0 * Nk + n0 + c), (size_t)Nk * 2, Mk - m0,
+        stage_flush(buf, reinterpret_cast<uint8_t*>(o + (size_t)m0 * Nk + n0 + c), (size_t)Nk * 2, Mk - m0,
                     min(min(64, end - c), Nk - n0 - c) * 2, lane);
       else
         __syncwarp();
@@ -481,6 +465,10 @@ ExpertsJob<kRows, F16> experts_job(const CUtensorMap& a, const CUtensorMap (&b)[
   for (int i = 0; i < 4; ++i) j.b[i] = b[i];
   j.blocks = 0;
   j.head = p.head;
+  j.E = p.E;
+  j.width = p.width;
+  j.cap_rows = p.cap_rows;
+  j.cap_tiles = p.cap_tiles;
   j.table = p.table;
   j.tiles_m = (m + per_tile - 1) / per_tile;
   j.kiters = (depth + kFfnTileK - 1) / kFfnTileK;
@@ -508,13 +496,15 @@ cudaError_t launch_rows(K* k, long long warps, int sms, bool dependent, cudaStre
 // weights.  A warp takes 256 columns of a token, eight a lane, eight experts in flight.
 template <bool F16>
 __device__ __forceinline__ void combine_item(long long item, int segs, int k, int D, const int* places, const float* weights,
-                                             const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* out, int lane) {
+                                             int cap_rows, const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* out,
+                                             int lane) {
   const long long t = item / segs;
   const int c0 = (int)(item - t * segs) * 256 + lane * 8;
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-  const int at = lane < k ? places[t * k + lane] : -1;
+  int at = lane < k ? places[t * k + lane] : -1;
+  if (at >= cap_rows) at = -1;
   const float wt = lane < k && weights ? weights[t * k + lane] : 1.0f;
   // a lane's eight low bytes are every second of sixteen, from the first or the second on
   const uint32_t pick0 = (c0 & 8) ? 0x1050u : 0x1040u, pick1 = (c0 & 8) ? 0x3270u : 0x3260u;

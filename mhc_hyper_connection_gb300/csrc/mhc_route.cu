@@ -966,7 +966,7 @@ mhc_status_t mhc_expert_plan_run(int64_t T, int64_t k, int64_t E, const int32_t*
     const cudaError_t z = cudaMemsetAsync(plan, 0, (size_t)l.total * 4, s);
     return z == cudaSuccess ? MHC_OK : fail(MHC_ERR_RUNTIME, "clearing the plan failed: %s", cudaGetErrorString(z));
   }
-  PlanArgs a = {experts, plan_view(l, plan), (int)l.slots, (int)E, kPlanChunk};
+  PlanArgs a = {experts, plan_view(l, E, plan), (int)l.slots, (int)E, kPlanChunk};
   const size_t smem = plan_smem((int)E);
   cudaError_t e = cudaSuccess;
   if (smem > 32 * 1024) {                        // beside the static arrays more than a kernel has by default
