@@ -420,25 +420,33 @@ __device__ __noinline__ int choose64(const RouteArgs& a, long long row, float to
   return choose<kType, double, V>(a, row, l, key, r, 0.0f, 0.0f, room, lane, unsure);
 }
 
-// V: consecutive scores of a lane.
+// Warps of a block, and blocks of an SM.
+__host__ __device__ constexpr int route_warps(int V) { return V <= 8 ? 8 : 4; }
+__host__ __device__ constexpr int route_blocks(int V) { return V <= 4 ? 4 : V <= 8 ? 3 : V <= 16 ? 4 : 2; }
+
+// V: consecutive scores of a lane.  A block's warps take its rows in turn as they come free:
+// a row whose keys are formed again takes several others' time, and the code for it comes
+// into an SM for a row or two.
 template <int kType, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32, V <= 4 ? 8 : V <= 8 ? 6 : V <= 16 ? 4 : 2) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(route_warps(V) * 32, route_blocks(V)) route_kernel(const RouteArgs a) {
   extern __shared__ double route_keys[];
+  __shared__ unsigned taken;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k, e0 = lane * V;
   double* keys64 = route_keys + (size_t)warp * E;
   float bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
-  float ahead[V];
-  const long long row0 = (long long)blockIdx.x * kRouteWarps + warp;
-  if (row0 < a.T) load_row<kType, V>(a, row0, lane, ahead);
-  for (long long row = row0; row < a.T; row += (long long)gridDim.x * kRouteWarps) {
+  const long long first = a.T * blockIdx.x / gridDim.x, last = a.T * (blockIdx.x + 1) / gridDim.x;
+  if (threadIdx.x == 0) taken = 0;
+  __syncthreads();
+  for (;;) {
+    unsigned n = lane == 0 ? atomicAdd(&taken, 1u) : 0u;
+    n = __shfl_sync(kFull, n, 0);
+    const long long row = first + n;
+    if (row >= last) break;
     float l[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = ahead[i];
-    const long long next = row + (long long)gridDim.x * kRouteWarps;
-    if (next < a.T) load_row<kType, V>(a, next, lane, ahead);
+    load_row<kType, V>(a, row, lane, l);
     // Scores; softmax: top and sum of the row.
     uint32_t topu = Ordered<float>::kOut;
 #pragma unroll
@@ -834,8 +842,8 @@ mhc_status_t route_device(int* sms) {
   *sms = di.sms;
   return MHC_OK;
 }
-unsigned row_blocks(int64_t T, int sms, int per_sm) {
-  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)sms * per_sm;
+unsigned row_blocks(int64_t T, int sms) {
+  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)sms * 16;
   return (unsigned)(b < most ? b : most);
 }
 size_t elem_bytes(int32_t dtype) { return dtype == MHC_DTYPE_FP32 ? 4 : 2; }
@@ -845,15 +853,19 @@ size_t logits_align(int32_t dtype, int64_t E) { return E % 4 == 0 ? 4 * elem_byt
 template <int kType>
 cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
   // where no key is formed again and no group is marked nothing is kept in shared memory
-  const size_t smem = a.bias || a.groups > 1 ? (size_t)kRouteWarps * a.E * 8 : 0;
+  auto run = [&](auto* k, int v) {
+    const int warps = route_warps(v);
+    const int64_t rows = (a.T + warps - 1) / warps, most = (int64_t)sms * route_blocks(v);
+    const size_t smem = a.bias || a.groups > 1 ? (size_t)warps * a.E * 8 : 0;
+    k<<<(unsigned)(rows < most ? rows : most), warps * 32, smem, s>>>(a);
+  };
   const int v = (a.E + 31) / 32;
-  const unsigned grid = row_blocks(a.T, sms, v <= 4 ? 8 : v <= 8 ? 6 : v <= 16 ? 4 : 2);   // as many as run at once
-  if (v <= 1) route_kernel<kType, 1><<<grid, kRouteWarps * 32, smem, s>>>(a);
-  else if (v <= 2) route_kernel<kType, 2><<<grid, kRouteWarps * 32, smem, s>>>(a);
-  else if (v <= 4) route_kernel<kType, 4><<<grid, kRouteWarps * 32, smem, s>>>(a);
-  else if (v <= 8) route_kernel<kType, 8><<<grid, kRouteWarps * 32, smem, s>>>(a);
-  else if (v <= 16) route_kernel<kType, 16><<<grid, kRouteWarps * 32, smem, s>>>(a);
-  else route_kernel<kType, 32><<<grid, kRouteWarps * 32, smem, s>>>(a);
+  if (v <= 1) run(route_kernel<kType, 1>, 1);
+  else if (v <= 2) run(route_kernel<kType, 2>, 2);
+  else if (v <= 4) run(route_kernel<kType, 4>, 4);
+  else if (v <= 8) run(route_kernel<kType, 8>, 8);
+  else if (v <= 16) run(route_kernel<kType, 16>, 16);
+  else run(route_kernel<kType, 32>, 32);
   return cudaGetLastError();
 }
 
@@ -919,7 +931,7 @@ mhc_status_t mhc_route_backward_run(const mhc_route_bwd_args* a, void* stream) {
   const RouteBwdArgs r = {a->logits, a->experts, a->grad_weights, a->grad_logits, a->T, (int)a->E, (int)a->k,
                           a->score == MHC_SCORE_SIGMOID, a->renormalise, a->scale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = row_blocks(a->T, sms, 16);
+  const unsigned grid = row_blocks(a->T, sms);
   const size_t smem = (size_t)kRouteWarps * ((a->E + 3) & ~int64_t(3)) * 4;
   if (a->dtype == MHC_DTYPE_FP32) route_backward_kernel<MHC_DTYPE_FP32><<<grid, kRouteWarps * 32, smem, s>>>(r);
   else if (a->dtype == MHC_DTYPE_BF16) route_backward_kernel<MHC_DTYPE_BF16><<<grid, kRouteWarps * 32, smem, s>>>(r);
