@@ -17,8 +17,8 @@
 namespace mhc {
 namespace {
 
-constexpr int kNormBlock = 32768;                // elements that one block of the norm sums at least
-constexpr int kNormMost = 512;                   // blocks of a matrix at most
+constexpr int kNormBlock = 16384;                // elements that one block of the norm sums at least
+constexpr int kNormBlocks = 1216;                // blocks in all, at least one a matrix: eight an SM
 
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // e in [-126, 127]
 
@@ -66,22 +66,23 @@ __device__ __forceinline__ double block_sum(double v, double* room) {
   return s;
 }
 
-// Sums of squares of one block's part of a matrix.  Sixty-four values of a thread share a
-// power of two that brings the largest near one, so no square over- or underflows, and
-// one fp64 addition (with eight values each the fp64 units were the bound: 80 us for 184
-// MB).
+// Sums of squares of one block's part of a matrix.  A thread's 128 bytes (64 values, or 32 of
+// fp32) share a power of two that brings the largest near one, so no square over- or
+// underflows, and one fp64 addition (one for every eight values kept the fp64 units busy
+// for 80 us of 184 MB).
 template <int kType>
 __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const void* x, long long count, bool whole, double* part) {
+  constexpr int kV = kType == MHC_DTYPE_FP32 ? 4 : 8;          // groups of eight values
+  constexpr long long kStep = 256 * 8 * kV;
   __shared__ double room[8];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
   pdl_trigger();
   const long long base = (long long)blockIdx.y * count, end = base + count;
   double acc = 0.0;
-  for (long long i0 = (long long)blockIdx.x * 16384 + threadIdx.x * 8; i0 < count; i0 += (long long)gridDim.x * 16384) {
-    float v[8][8], top = 0.0f;
-    bool bad = false;
+  float v[kV][8];
+  auto load = [&](long long i0) {
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kV; ++b) {
       const long long i = i0 + b * 2048;
       if (i < count) {
         load8<kType>(x, base + i, end, whole, v[b]);
@@ -90,8 +91,13 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const 
         for (int j = 0; j < 8; ++j) v[b][j] = 0.0f;
       }
     }
+  };
+  for (long long i0 = (long long)blockIdx.x * kStep + threadIdx.x * 8; i0 < count; i0 += (long long)gridDim.x * kStep) {
+    load(i0);
+    float top = 0.0f;
+    bool bad = false;
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
+    for (int b = 0; b < kV; ++b)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float m = fabsf(v[b][j]);
@@ -105,7 +111,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const 
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.0f;
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
+    for (int b = 0; b < kV; ++b)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float q = v[b][j] * f0 * f1;
@@ -153,6 +159,8 @@ struct OrthJob {
   static constexpr bool kAMn = kA, kBMn = kB, kDraw = false, kEarly = false;
   CUtensorMap a, b;              // MN-major: blocks of 64 columns are a dimension of their own
                                  // (b's of tiles narrower than 256 not)
+  CUtensorMap b_half;            // b's of the tiles from `whole` on
+  int whole;                     // tiles before these are whole; each later one is half a tile
   GemmShape g;                   // tiles of one matrix
   int count, per, width, kiters;
   int split;                     // log2(256 / width)
@@ -167,6 +175,12 @@ struct OrthJob {
   __device__ __forceinline__ Raw fetch(int) const { return {}; }
   __device__ __forceinline__ GTile make(int t, const Raw&) const {
     GTile o;
+    int half = 0;
+    const bool halved = t >= whole;
+    if (halved) {                // the last round's few tiles in halves, for twice as many pairs
+      half = (t - whole) & 1;
+      t = whole + ((t - whole) >> 1);
+    }
     o.e = by_matrix(t);
     const int r = t - o.e * per;
     if constexpr (kSym) {        // row tm begins at tm (tm + 1) / 2 squares of 256
@@ -182,16 +196,17 @@ struct OrthJob {
       o.kind = 0;
     }
     o.row0 = o.rows = 0;
-    o.width = width;
+    o.width = halved ? width >> 1 : width;
+    if (halved) o.tn = 2 * o.tn + half;
     o.kiters = kiters;
     return o;
   }
-  __device__ __forceinline__ int bytes(const GTile&) const {
-    const int half = width >> 1;
+  __device__ __forceinline__ int bytes(const GTile& o) const {
+    const int half = o.width >> 1;
     return kGemmOpBytes + (kB ? (half + 63) & ~63 : half) * kFfnTileK * 2;
   }
   __device__ __forceinline__ int steps(const GTile&, int) const { return kFfnTileK / 16; }
-  __device__ __forceinline__ uint32_t idesc(const GTile&) const { return grp_idesc(true, kA, kB, width); }
+  __device__ __forceinline__ uint32_t idesc(const GTile& o) const { return grp_idesc(true, kA, kB, o.width); }
   __device__ __forceinline__ void load_a(const GTile& o, int k, uint32_t sa, uint32_t bar, int rank) const {
     const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf;
     if constexpr (kA) {
@@ -201,12 +216,13 @@ struct OrthJob {
     }
   }
   __device__ __forceinline__ void load_b(const GTile& o, int k, uint32_t sb, uint32_t bar, int rank) const {
-    const int k0 = k * kFfnTileK, n0 = o.tn * width + rank * (width >> 1);
+    const int k0 = k * kFfnTileK, n0 = o.tn * o.width + rank * (o.width >> 1);
+    const CUtensorMap* t = o.width == width ? &b : &b_half;
     if constexpr (kB) {
-      if (width > 128) tma_load_4d_pair(sb, &b, bar, 0, k0, n0 >> 6, o.e);
-      else tma_load_3d_pair(sb, &b, bar, n0, k0, o.e);
+      if (o.width > 128) tma_load_4d_pair(sb, t, bar, 0, k0, n0 >> 6, o.e);
+      else tma_load_3d_pair(sb, t, bar, n0, k0, o.e);
     } else {
-      tma_load_3d_pair(sb, &b, bar, k0, n0, o.e);
+      tma_load_3d_pair(sb, t, bar, k0, n0, o.e);
     }
   }
 };
@@ -317,7 +333,8 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
   OrthLayout l;
   const int64_t count = rows * cols;
   l.parts = (count + kNormBlock - 1) / kNormBlock;
-  if (l.parts > kNormMost) l.parts = kNormMost;
+  const int64_t most = batch > kNormBlocks / 2 ? 1 : kNormBlocks / (batch > 0 ? batch : 1);
+  if (l.parts > most) l.parts = most;
   l.pitch = (cols + 7) & ~int64_t(7);
   l.side = rows < cols ? rows : cols;
   l.spitch = (l.side + 7) & ~int64_t(7);
@@ -412,6 +429,20 @@ cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* ma
   job.per = kSym ? (g.tiles_m * (g.tiles_m + 1) / 2) << job.split : g.tiles_m * g.tiles_n;
   job.count = (int)(job.per * p.batch);
   job.by_matrix = FastDiv((uint32_t)job.per);
+  // Where the last round has tiles for at most half the pairs, these are halved: 320 tiles of
+  // 32 matrices of 1024, 5 rounds, now 4.6.
+  const int pairs = p.sms / 2, over = job.count % pairs;
+  job.whole = job.count;
+  if (job.width == 256 && job.count > pairs && over > 0 && 2 * over <= pairs) {
+    job.whole = job.count - over;
+    job.count += over;
+    if (!orth_map(&job.b_half, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : 64u)) {
+      *mapped = false;
+      return cudaErrorInvalidValue;
+    }
+  } else {
+    job.b_half = job.b;
+  }
   job.kiters = (int)((p.K + kFfnTileK - 1) / kFfnTileK);
   const EpiOrth<kHasC, kSym, kLast> e = {p.c, p.out, (int)p.M, (int)p.N, (int)p.pitch, (float)p.alpha, (float)p.beta, p.whole};
   return launch_group(job, p.call, e, job.count, p.sms, true, s);
