@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, 
 // grad_x, and grad_weights from the parts of its sums: rows of the plan's order, one a
 // lane; slots without a row get zeros.
 template <bool F16>
-__global__ void __launch_bounds__(256) combine_backward_kernel(const PlanView p, long long T, int k, int D, int parts,
+__global__ void __launch_bounds__(256, 4) combine_backward_kernel(const PlanView p, long long T, int k, int D, int parts,
                                                                long long cap_rows, const uint16_t* hi, const uint8_t* lo, int lo_pitch,
                                                                const float* part,
                                                                uint16_t* grad_x, float* grad_weights) {
@@ -72,7 +72,7 @@ cudaError_t gate_gradients(const ExpertsBwdLaunch& L, cudaStream_t s) {
 template <bool F16>
 cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
   const int D = L.D, F = L.F, sms = L.call.sms, box = token_rows(L.lay.width);
-  cudaError_t e = launch_rows(gather_backward_kernel, L.lay.cap_rows * ((D + 1023) / 1024), sms, false, s, L.call.header, L.plan,
+  cudaError_t e = launch_rows(gather_backward_kernel, L.lay.cap_rows * ((D + 1023) / 1024), sms, 8, false, s, L.call.header, L.plan,
                               L.k, D, F, static_cast<const uint16_t*>(L.x_in), static_cast<const uint16_t*>(L.grad_y), L.weights,
                               static_cast<uint16_t*>(L.xs), static_cast<uint16_t*>(L.gys), L.w_row,
                               static_cast<uint16_t*>(L.gg_buf), static_cast<uint16_t*>(L.wa_buf));
@@ -110,7 +110,7 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
   const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D, rows_low_pitch(D)};
   e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, sms, true, s, L.plan, L.T, L.k,
+  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, sms, 4, true, s, L.plan, L.T, L.k,
                      D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.gys), rows_low_pitch(D),
                      static_cast<const float*>(L.part),
                      static_cast<uint16_t*>(L.grad_x), L.grad_weights);

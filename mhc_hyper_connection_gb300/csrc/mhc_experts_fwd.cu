@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const Pla
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(256) combine_kernel(const PlanView p, long long T, int k, int D, const float* weights,
+__global__ void __launch_bounds__(256, 4) combine_kernel(const PlanView p, long long T, int k, int D, const float* weights,
                                                       const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* y) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
@@ -36,7 +36,7 @@ cudaError_t gate_up(const ExpertsFwdLaunch& L, cudaStream_t s) {
 
 template <bool F16>
 cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
-  cudaError_t e = launch_rows(gather_kernel, L.lay.cap_rows * ((L.D + 1023) / 1024), L.call.sms, false, s, L.call.header, L.plan, L.k,
+  cudaError_t e = launch_rows(gather_kernel, L.lay.cap_rows * ((L.D + 1023) / 1024), L.call.sms, 8, false, s, L.call.header, L.plan, L.k,
                               L.D, static_cast<const uint16_t*>(L.x_in), static_cast<uint16_t*>(L.xs));
   if (e != cudaSuccess) return e;
   e = L.act == 0 ? (L.gate_up ? gate_up<F16, true, 0>(L, s) : gate_up<F16, false, 0>(L, s))
@@ -46,7 +46,7 @@ cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
   const EpiRows o = {static_cast<uint16_t*>(L.xs), L.lo, L.D, rows_low_pitch(L.D)};
   e = launch_group(job, grp_call(L.call, 2, true, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), L.call.sms, true, s, L.plan, L.T, L.k, L.D, L.weights,
+  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), L.call.sms, 4, true, s, L.plan, L.T, L.k, L.D, L.weights,
                      static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.lo), rows_low_pitch(L.D),
                      static_cast<uint16_t*>(L.y));
 }

@@ -476,14 +476,14 @@ ExpertsJob<kRows, F16> experts_job(const CUtensorMap& a, const CUtensorMap (&b)[
   return j;
 }
 
-// Launches of the row kernels.
+// Launches of the row kernels: at most per_sm blocks of eight warps an SM.
 template <class K, class... A>
-cudaError_t launch_rows(K* k, long long warps, int sms, bool dependent, cudaStream_t s, A... args) {
+cudaError_t launch_rows(K* k, long long warps, int sms, int per_sm, bool dependent, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const long long blocks = (warps + 7) / 8, most = 8ll * sms;
+  const long long blocks = (warps + 7) / 8, most = (long long)per_sm * sms;
   cfg.gridDim = dim3((unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
