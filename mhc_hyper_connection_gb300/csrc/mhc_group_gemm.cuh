@@ -342,18 +342,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
       };
       // The first two tiles of a pair are dealt out, the others drawn.
       int t = pair;
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
+      bool sent = true, more = true;
+      for (int n = 0; more; ++n) {
         GTile g = none;
         if (t < ntiles) g = job.make(t, job.fetch(t));
-        ok = publish(n, g) && g.e >= 0;
+        sent = publish(n, g);
+        more = sent && g.e >= 0;
         if (n == 0) t = pair + pairs;
         if (n == 1 && Job::kEarly) pdl_wait();   // the counter is the first launch's
-        if (n >= 1 && ok) {
+        if (n >= 1 && more) {
           const unsigned drawn = 2u * (unsigned)pairs + atomicAdd(call.counter, 1u);
           t = drawn < (unsigned)ntiles ? (int)drawn : ntiles;
         }
       }
+      // Every role reads up to the last tile's -1, so what was sent has arrived before the pair
+      // leaves; where waits gave up, the last of it is given time to.
+      if (!sent)
+        for (const uint64_t t0 = now_ns(); now_ns() - t0 < 20000;) {
+        }
     }
   } else {
     // ===================================================== epilogue

@@ -211,6 +211,30 @@ def test_plan(cuda_device, T, k, E):
         np.testing.assert_array_equal(seen, rows >= 0)
 
 
+def test_plan_of_very_many_slots(cuda_device):
+    """2^22 slots: the order against a stable sort."""
+    from mhc_hyper_connection_gb300 import expert_plan
+    T, k, E = 1 << 20, 4, 1000
+    e = torch.randint(-1, E, (T, k), generator=torch.Generator(device=cuda_device).manual_seed(1), device=cuda_device, dtype=torch.int32)
+    p = expert_plan(e, E)
+    flat = e.reshape(-1).long()
+    counts = torch.bincount(flat + 1, minlength=E + 1)[1:]
+    assert torch.equal(p.counts.long(), counts)
+    padded = (counts + 15) // 16 * 16
+    start = padded.cumsum(0) - padded
+    order = torch.sort(flat, stable=True).indices[flat.numel() - int(counts.sum()):]        # slots by expert, -1 first
+    rank = torch.arange(order.numel(), device=cuda_device) - (counts.cumsum(0) - counts)[flat[order]]
+    want = torch.full_like(flat, -1)
+    want[order] = start[flat[order]] + rank
+    up = lambda n: (n + 63) // 64 * 64  # noqa: E731
+    tiles = T * k // 256 + E
+    at = 64 + up(E) + up(E + 1) + up(8 * tiles)
+    words = p.buffer.view(torch.int32)
+    assert torch.equal(words[at:at + T * k].long(), want)
+    rows = words[at + up(T * k):][:int(padded.sum())].long()
+    assert torch.equal(rows[want[order]], order) and int((rows < 0).sum()) == int((padded - counts).sum())
+
+
 def up2(n):
     return (n + 31) // 32 * 32
 
