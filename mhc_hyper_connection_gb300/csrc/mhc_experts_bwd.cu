@@ -6,27 +6,35 @@ namespace {
 
 // Rows of x and grad_y and the weights in the plan's order; zero rows of gg and w a
 // where it is padding.  The call's first launch: clears its header.
-__global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, const PlanView p, int k, int D, int F,
-                                                              const uint16_t* x, const uint16_t* gy, const float* weights,
+__global__ void __launch_bounds__(256) gather_backward_kernel(uint32_t* header, const PlanView p, long long T, int k, int D,
+                                                              int F, const uint16_t* x, const uint16_t* gy, const float* weights,
                                                               uint16_t* xs, uint16_t* gys, float* w_row, uint16_t* gg,
                                                               uint16_t* wa) {
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
-  const long long items = (long long)min(p.head[1], p.cap_rows) * segs;
-  for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
-    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs);
-    int slot = p.rows[r];
-    if (slot >= p.slots) slot = -1;
-    gather_item(slot, k, r, seg, D, x, xs, lane);
-    gather_item(slot, k, r, seg, D, gy, gys, lane);
-    if (seg == 0) {
-      if (lane == 0) w_row[r] = slot >= 0 ? weights[slot] : 0.0f;
-      if (slot < 0) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        for (int c = lane * 8; c < 2 * F; c += 256) *reinterpret_cast<uint4*>(gg + (size_t)r * 2 * F + c) = z;
-        for (int c = lane * 8; c < F; c += 256) *reinterpret_cast<uint4*>(wa + (size_t)r * F + c) = z;
-      }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, widest = max(D, 2 * F);
+  const uint32_t segs = (uint32_t)(D + kGatherCols - 1) / kGatherCols, i = blockIdx.x * 8 + warp;
+  const uint32_t tokens = (uint32_t)T * segs;
+  if (i < tokens) {
+    const uint32_t n = i / segs;
+    const int seg = (int)(i - n * segs), c0 = seg * kGatherCols + lane * 8;
+    int at = lane < k ? p.places[(size_t)n * k + lane] : -1;
+    if (at >= p.cap_rows) at = -1;
+    if (seg == 0 && at >= 0) w_row[at] = weights[(size_t)n * k + lane];
+    gather_item(k, at, c0, D, x + (size_t)n * D, xs);
+    gather_item(k, at, c0, D, gy + (size_t)n * D, gys);
+  } else {
+    const uint32_t pieces = (uint32_t)(widest + kGatherCols - 1) / kGatherCols, n = (i - tokens) / pieces;
+    const int seg = (int)(i - tokens - n * pieces), c0 = seg * kGatherCols + lane * 8;
+    if (n >= (uint32_t)p.E) return;
+    int first, last;
+    padding_rows(p, (int)n, &first, &last);
+    for (int r = first; r < last; ++r) {
+      if (seg == 0 && lane == 0) w_row[r] = 0.0f;
+      zero_item(r, c0, D, xs);
+      zero_item(r, c0, D, gys);
+      zero_item(r, c0, 2 * F, gg);
+      zero_item(r, c0, F, wa);
     }
   }
 }
@@ -42,7 +50,8 @@ __global__ void __launch_bounds__(256, 4) combine_backward_kernel(const PlanView
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
   const int used = min(p.head[1], p.cap_rows);
   const long long groups = (max(used, 0) + 31) / 32;
-  for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs + groups; i += (long long)gridDim.x * 8) {
+  const long long i = (long long)blockIdx.x * 8 + warp;
+  if (i < T * segs + groups) {
     if (i < groups) {
       const long long r = i * 32 + lane;
       const int slot = r < used ? p.rows[r] : -1;
@@ -72,8 +81,9 @@ cudaError_t gate_gradients(const ExpertsBwdLaunch& L, cudaStream_t s) {
 template <bool F16>
 cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
   const int D = L.D, F = L.F, sms = L.call.sms, box = token_rows(L.lay.width);
-  cudaError_t e = launch_rows(gather_backward_kernel, L.lay.cap_rows * ((D + 1023) / 1024), sms, 8, false, s, L.call.header, L.plan,
-                              L.k, D, F, static_cast<const uint16_t*>(L.x_in), static_cast<const uint16_t*>(L.grad_y), L.weights,
+  const int widest = D > 2 * F ? D : 2 * F;
+  const long long gathers = L.T * ((D + kGatherCols - 1) / kGatherCols) + (long long)L.E * ((widest + kGatherCols - 1) / kGatherCols);
+  cudaError_t e = launch_rows(gather_backward_kernel, gathers, false, s, L.call.header, L.plan, L.T, L.k, D, F, static_cast<const uint16_t*>(L.x_in), static_cast<const uint16_t*>(L.grad_y), L.weights,
                               static_cast<uint16_t*>(L.xs), static_cast<uint16_t*>(L.gys), L.w_row,
                               static_cast<uint16_t*>(L.gg_buf), static_cast<uint16_t*>(L.wa_buf));
   if (e != cudaSuccess) return e;
@@ -110,7 +120,7 @@ cudaError_t backward(const ExpertsBwdLaunch& L, cudaStream_t s) {
   const EpiRows o = {static_cast<uint16_t*>(L.xs), static_cast<uint8_t*>(L.gys), D, rows_low_pitch(D)};
   e = launch_group(job, grp_call(L.call, 3, true, box), o, L.lay.cap_tiles * job.tiles_m, sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, sms, 4, true, s, L.plan, L.T, L.k,
+  return launch_rows(combine_backward_kernel<F16>, L.T * ((D + 255) / 256) + L.lay.cap_rows / 32 + 1, true, s, L.plan, L.T, L.k,
                      D, (F + 31) / 32, (long long)L.lay.cap_rows, static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.gys), rows_low_pitch(D),
                      static_cast<const float*>(L.part),
                      static_cast<uint16_t*>(L.grad_x), L.grad_weights);

@@ -5,16 +5,20 @@ namespace mhc {
 namespace {
 
 // Rows of x in the plan's order.  The call's first launch: clears its header.
-__global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const PlanView p, int k, int D, const uint16_t* x,
-                                                     uint16_t* xs) {
+__global__ void __launch_bounds__(256) gather_kernel(uint32_t* header, const PlanView p, long long T, int k, int D,
+                                                     const uint16_t* x, uint16_t* xs) {
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 1023) / 1024;
-  const long long items = (long long)min(p.head[1], p.cap_rows) * segs;
-  for (long long i = (long long)blockIdx.x * 8 + warp; i < items; i += (long long)gridDim.x * 8) {
-    const int r = (int)(i / segs), seg = (int)(i - (long long)r * segs);
-    const int slot = p.rows[r];
-    gather_item(slot < p.slots ? slot : -1, k, r, seg, D, x, xs, lane);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t segs = (uint32_t)(D + kGatherCols - 1) / kGatherCols, i = blockIdx.x * 8 + warp, n = i / segs;
+  const int c0 = (int)(i - n * segs) * kGatherCols + lane * 8;
+  if (n < T) {
+    const int at = lane < k ? p.places[(size_t)n * k + lane] : -1;
+    gather_item(k, at < p.cap_rows ? at : -1, c0, D, x + (size_t)n * D, xs);
+  } else if (n < T + p.E) {
+    int first, last;
+    padding_rows(p, (int)(n - T), &first, &last);
+    for (int r = first; r < last; ++r) zero_item(r, c0, D, xs);
   }
 }
 
@@ -23,7 +27,8 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(const PlanView p, long 
                                                       const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* y) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, segs = (D + 255) / 256;
-  for (long long i = (long long)blockIdx.x * 8 + warp; i < T * segs; i += (long long)gridDim.x * 8)
+  const long long i = (long long)blockIdx.x * 8 + warp;
+  if (i < T * segs)
     combine_item<F16>(i, segs, k, D, p.places, weights, p.cap_rows, hi, lo, lo_pitch, y, lane);
 }
 
@@ -36,8 +41,8 @@ cudaError_t gate_up(const ExpertsFwdLaunch& L, cudaStream_t s) {
 
 template <bool F16>
 cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
-  cudaError_t e = launch_rows(gather_kernel, L.lay.cap_rows * ((L.D + 1023) / 1024), L.call.sms, 8, false, s, L.call.header, L.plan, L.k,
-                              L.D, static_cast<const uint16_t*>(L.x_in), static_cast<uint16_t*>(L.xs));
+  cudaError_t e = launch_rows(gather_kernel, (L.T + L.E) * ((L.D + kGatherCols - 1) / kGatherCols), false, s, L.call.header, L.plan,
+                              L.T, L.k, L.D, static_cast<const uint16_t*>(L.x_in), static_cast<uint16_t*>(L.xs));
   if (e != cudaSuccess) return e;
   e = L.act == 0 ? (L.gate_up ? gate_up<F16, true, 0>(L, s) : gate_up<F16, false, 0>(L, s))
                  : (L.gate_up ? gate_up<F16, true, 1>(L, s) : gate_up<F16, false, 1>(L, s));
@@ -46,7 +51,7 @@ cudaError_t forward(const ExpertsFwdLaunch& L, cudaStream_t s) {
   const EpiRows o = {static_cast<uint16_t*>(L.xs), L.lo, L.D, rows_low_pitch(L.D)};
   e = launch_group(job, grp_call(L.call, 2, true, token_rows(L.lay.width)), o, L.lay.cap_tiles * job.tiles_m, L.call.sms, true, s);
   if (e != cudaSuccess) return e;
-  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), L.call.sms, 4, true, s, L.plan, L.T, L.k, L.D, L.weights,
+  return launch_rows(combine_kernel<F16>, L.T * ((L.D + 255) / 256), true, s, L.plan, L.T, L.k, L.D, L.weights,
                      static_cast<const uint16_t*>(L.xs), static_cast<const uint8_t*>(L.lo), rows_low_pitch(L.D),
                      static_cast<uint16_t*>(L.y));
 }

@@ -476,15 +476,14 @@ ExpertsJob<kRows, F16> experts_job(const CUtensorMap& a, const CUtensorMap (&b)[
   return j;
 }
 
-// Launches of the row kernels: at most per_sm blocks of eight warps an SM.
+// Launches of the row kernels: blocks of eight warps.
 template <class K, class... A>
-cudaError_t launch_rows(K* k, long long warps, int sms, int per_sm, bool dependent, cudaStream_t s, A... args) {
+cudaError_t launch_rows(K* k, long long warps, bool dependent, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const long long blocks = (warps + 7) / 8, most = (long long)per_sm * sms;
-  cfg.gridDim = dim3((unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most));
+  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -494,6 +493,7 @@ cudaError_t launch_rows(K* k, long long warps, int sms, int per_sm, bool depende
 
 // out[t] = sum_j w_tj rows[place_tj] of 24-bit rows, in the order of j; w = 1 without
 // weights.  A warp takes 256 columns of a token, eight a lane, eight experts in flight.
+// Bound by HBM: 77 us for 8 rows each of 4096 tokens of 4096 columns (436 MB: 5.7 TB/s).
 template <bool F16>
 __device__ __forceinline__ void combine_item(long long item, int segs, int k, int D, const int* places, const float* weights,
                                              int cap_rows, const uint16_t* hi, const uint8_t* lo, int lo_pitch, uint16_t* out,
@@ -537,19 +537,37 @@ __device__ __forceinline__ void combine_item(long long item, int segs, int k, in
   if (c0 < D) *reinterpret_cast<uint4*>(out + (size_t)t * D + c0) = pack8v<F16>(s);
 }
 
-// Row r of the plan's order from row slot / k of a tensor, zeros where it is padding: a
-// warp takes 1024 columns, four pieces a lane.
-__device__ __forceinline__ void gather_item(int slot, int k, int r, int seg, int D, const uint16_t* from, uint16_t* to, int lane) {
-  const int c0 = seg * 1024 + lane * 8;
-  uint4 v[4];
+// Copies of a token's row to the rows of its slots: a warp takes 512 columns, two pieces a
+// lane, reads them once and writes them k times.  (A warp for each written row read x k
+// times, beyond the L2 where the writes had replaced it: 66 us for 8 copies of 4096 rows of
+// 4096 columns and 74 for 4 of 8192; so it is 49 and 54, 6.1 and 6.2 TB/s, with a block for
+// every eight warps; with as many blocks as fit at once, each taking more in turn, 56 and 63.)
+constexpr int kGatherCols = 512;
+__device__ __forceinline__ void gather_item(int k, int at, int c0, int D, const uint16_t* from, uint16_t* to) {
+  uint4 v[2];
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    v[h] = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && c0 + 256 * h < D) v[h] = *reinterpret_cast<const uint4*>(from + (size_t)(slot / k) * D + c0 + 256 * h);
+  for (int h = 0; h < 2; ++h)
+    if (c0 + 256 * h < D) v[h] = *reinterpret_cast<const uint4*>(from + c0 + 256 * h);
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int p = __shfl_sync(0xFFFFFFFFu, at, j);
+    if (p < 0) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c0 + 256 * h < D) *reinterpret_cast<uint4*>(to + (size_t)p * D + c0 + 256 * h) = v[h];
   }
+}
+__device__ __forceinline__ void zero_item(int row, int c0, int D, uint16_t* to) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h)
-    if (c0 + 256 * h < D) *reinterpret_cast<uint4*>(to + (size_t)r * D + c0 + 256 * h) = v[h];
+  for (int h = 0; h < 2; ++h)
+    if (c0 + 256 * h < D) *reinterpret_cast<uint4*>(to + (size_t)row * D + c0 + 256 * h) = make_uint4(0, 0, 0, 0);
+}
+
+// Rows of padding behind expert e's: [first, last).
+__device__ __forceinline__ void padding_rows(const PlanView& p, int e, int* first, int* last) {
+  const long long f = (long long)p.starts[e] + p.counts[e], l = p.starts[e + 1];
+  *first = (int)max(0ll, min(f, (long long)p.cap_rows));
+  *last = (int)max((long long)*first, min(min(l, f + kPlanPad - 1), (long long)p.cap_rows));
 }
 
 }  // namespace mhc

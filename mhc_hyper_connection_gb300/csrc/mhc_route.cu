@@ -2,8 +2,9 @@
 // choice and weights, the weights' gradient, and the counting sort of the slots.
 //
 // Routing and its gradient read and write each score once; a row is a warp's, its
-// scores in registers, E / 32 consecutive ones a lane.  Bound by the k + 1 rounds of
-// a maximum over the warp (about 40 instructions each), not by memory.
+// scores in registers, E / 32 consecutive ones a lane.  Bound by the warp's instructions
+// (keys, sorting, the groups and a maximum over the warp for each choice: 1430 a row of 256
+// experts, 8 of 4 groups of 8), not by memory: 16384 such rows take 44 us, their bytes 2.6.
 #include <math.h>
 
 #include "mhc_experts.cuh"
@@ -175,7 +176,7 @@ __device__ __noinline__ int reorder64(const RouteArgs& a, long long row, int min
 // something are so close that they may stand in the wrong order: closer than tol (smax +
 // max(|a|, |b|)), smax the largest score.  room: E values of this warp.
 // Up to eight scores a lane are sorted first, so that a round takes a lane's next instead
-// of searching it (T = 16384, E = 256, k = 8 of 4 groups of 8: 64 -> 28 us).
+// of searching it (T = 16384, E = 256, k = 8 of 4 groups of 8: 63 -> 48 us).
 template <int kType, class K, int V>
 __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const float (&l)[V], const K (&key)[V],
                                       const RowSum<K>& sums, float smax, float tol, K* room, int lane, bool& unsure) {
@@ -767,7 +768,7 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, uint16_t* hist, co
   }
 }
 
-// All in one block.
+// All in one block: about 5 us for the slots of a few tokens.
 __global__ void __launch_bounds__(kPlanThreads) plan_alone_kernel(const PlanArgs a) {
   extern __shared__ uint16_t plan_hist[];
   __shared__ int sums[32], tile_at[kMostExperts], start_at[kMostExperts], count_at[kMostExperts];
@@ -778,7 +779,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_alone_kernel(const PlanArgs
   __syncthreads();
   plan_place(a, plan_hist, start_at, 0, a.slots, warp, lane);
 }
-// Many slots: counts of each block's, then the sums over blocks, then the rows.
+// Many slots: counts of each block's, then the sums over blocks, then the rows (32768 slots:
+// 21 us for the three, most of it starts and the latency of dependent loads).
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs a) {
   extern __shared__ uint16_t plan_hist[];
   const int first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.slots);
