@@ -18,9 +18,11 @@ struct PlanLayout {
   int64_t counts, starts, table, places, rows, scratch, total;
 };
 
-// Slots that one block of the counting and placing kernels takes, and the most
-// that a single block sorts alone.
-constexpr int kPlanChunk = 4096, kPlanAlone = 8192;
+// Slots up to which a single block sorts them alone, and those that else one block of the
+// counting and placing kernels takes: 32 a warp or, from 2^17 on, what leaves 128 blocks to
+// sum over.
+constexpr int kPlanAlone = 2048;
+inline int64_t plan_chunk(int64_t slots) { return 1024 * ((slots + (1 << 17) - 1) >> 17); }
 
 inline PlanLayout plan_layout(int64_t T, int64_t k, int64_t E) {
   PlanLayout l;
@@ -40,8 +42,8 @@ inline PlanLayout plan_layout(int64_t T, int64_t k, int64_t E) {
   l.places = l.table + up(8 * l.cap_tiles);
   l.rows = l.places + up(l.slots);
   l.scratch = l.rows + up(l.cap_rows);
-  const int64_t blocks = (l.slots + kPlanChunk - 1) / kPlanChunk;
-  l.total = l.scratch + (l.slots > kPlanAlone ? up(blocks * E) : 0);
+  const int64_t blocks = l.slots > kPlanAlone ? (l.slots + plan_chunk(l.slots) - 1) / plan_chunk(l.slots) : 0;
+  l.total = l.scratch + up(blocks * E);
   return l;
 }
 

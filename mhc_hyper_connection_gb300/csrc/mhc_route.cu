@@ -8,7 +8,7 @@
 #include <math.h>
 
 #include "mhc_experts.cuh"
-#include "mhc_ffn.cuh"
+#include "mhc_ffn_gemm.cuh"
 #include "mhc_host.cuh"
 #include "../../include/mhc_route.h"
 
@@ -655,30 +655,46 @@ struct PlanArgs {
 // Shared memory of the plan's kernels: the warps' counters.
 __host__ __device__ inline size_t plan_smem(int E) { return (size_t)kPlanWarps * E * 2; }
 
+// f(slot, its expert or -1) for a warp's slots of the block's [first, last), 32 at a time,
+// eight loads in flight.
+template <class F>
+__device__ __forceinline__ void plan_slots(const PlanArgs& a, int first, int last, int warp, int lane, F f) {
+  const int per = (((last - first) + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
+  const int b = first + warp * per, n = min(b + per, last);
+  for (int i = b; i < n; i += 256) {
+    int e[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int at = i + 32 * u + lane;
+      e[u] = at < n ? a.experts[at] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + 32 * u < n) f(i + 32 * u + lane, e[u] < 0 || e[u] >= a.E ? -1 : e[u], n);
+  }
+}
+
 // Counts of each expert among each warp's slots of this block.
 __device__ __forceinline__ void plan_count(const PlanArgs& a, uint16_t* hist, int first, int last, int warp, int lane) {
   const int E = a.E;
   for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
-  const int per = (((last - first) + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
-  const int b = first + warp * per, n = min(b + per, last);
-  for (int i = b; i < n; i += 32) {
-    const int at = i + lane;
-    int e = at < n ? a.experts[at] : -1;
-    if (e < 0 || e >= E) e = -1;
+  plan_slots(a, first, last, warp, lane, [&](int, int e, int) {
     const uint32_t same = __match_any_sync(kFull, e);
     if (e >= 0 && (__ffs(same) - 1) == lane) hist[warp * E + e] += (uint16_t)__popc(same);
     __syncwarp();
-  }
+  });
   __syncthreads();
 }
 // The counters as what lies before each warp's slots; returns expert e's count.
 __device__ __forceinline__ int plan_prefix(uint16_t* hist, int E, int e) {
-  int run = 0;
+  int c[kPlanWarps], run = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) c[w] = hist[w * E + e];
+#pragma unroll
   for (int w = 0; w < kPlanWarps; ++w) {
-    const int c = hist[w * E + e];
     hist[w * E + e] = (uint16_t)run;
-    run += c;
+    run += c[w];
   }
   return run;
 }
@@ -749,12 +765,7 @@ __device__ __forceinline__ void plan_finish(const PlanArgs& a, int count, int* s
 __device__ __forceinline__ void plan_place(const PlanArgs& a, uint16_t* hist, const int* base, int first, int last, int warp,
                                            int lane) {
   const int E = a.E;
-  const int per = (((last - first) + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
-  const int b = first + warp * per, n = min(b + per, last);
-  for (int i = b; i < n; i += 32) {
-    const int at = i + lane;
-    int e = at < n ? a.experts[at] : -1;
-    if (e < 0 || e >= E) e = -1;
+  plan_slots(a, first, last, warp, lane, [&](int at, int e, int n) {
     const uint32_t same = __match_any_sync(kFull, e);
     int row = -1;
     if (e >= 0) row = base[e] + hist[warp * E + e] + __popc(same & ((1u << lane) - 1u));
@@ -765,7 +776,7 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, uint16_t* hist, co
       a.p.places[at] = row;
       if (row >= 0) a.p.rows[row] = at;
     }
-  }
+  });
 }
 
 // All in one block: about 5 us for the slots of a few tokens.
@@ -779,24 +790,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_alone_kernel(const PlanArgs
   __syncthreads();
   plan_place(a, plan_hist, start_at, 0, a.slots, warp, lane);
 }
-// Many slots: counts of each block's, then the sums over blocks, then the rows (32768 slots:
-// 21 us for the three, most of it starts and the latency of dependent loads).
+// Many slots: counts of each block's, then the sums over blocks, then the rows.  Each kernel
+// starts beside the one before; what the placing one counts again does not wait for it.
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs a) {
   extern __shared__ uint16_t plan_hist[];
+  pdl_trigger();
   const int first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.slots);
   plan_count(a, plan_hist, first, last, threadIdx.x >> 5, threadIdx.x & 31);
   if ((int)threadIdx.x < a.E) a.p.scratch[(size_t)blockIdx.x * a.E + threadIdx.x] = plan_prefix(plan_hist, a.E, threadIdx.x);
 }
 __global__ void __launch_bounds__(kPlanThreads) plan_sum_kernel(const PlanArgs a, const int blocks) {
   __shared__ int sums[32], tile_at[kMostExperts], start_at[kMostExperts], count_at[kMostExperts];
+  pdl_trigger();
+  pdl_wait();
   int count = 0;
   if ((int)threadIdx.x < a.E) {
-    for (int b0 = 0; b0 < blocks; b0 += 8) {
-      int c[8];
+    for (int b0 = 0; b0 < blocks; b0 += 16) {
+      int c[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = b0 + i < blocks ? a.p.scratch[(size_t)(b0 + i) * a.E + threadIdx.x] : 0;
+      for (int i = 0; i < 16; ++i) c[i] = b0 + i < blocks ? a.p.scratch[(size_t)(b0 + i) * a.E + threadIdx.x] : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 16; ++i) {
         if (b0 + i < blocks) a.p.scratch[(size_t)(b0 + i) * a.E + threadIdx.x] = count;
         count += c[i];
       }
@@ -809,8 +823,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
   __shared__ int base[kMostExperts];
   const int first = blockIdx.x * a.chunk, last = min(first + a.chunk, a.slots);
   plan_count(a, plan_hist, first, last, threadIdx.x >> 5, threadIdx.x & 31);
+  if ((int)threadIdx.x < a.E) plan_prefix(plan_hist, a.E, threadIdx.x);
+  pdl_wait();
   if ((int)threadIdx.x < a.E) {
-    plan_prefix(plan_hist, a.E, threadIdx.x);
     base[threadIdx.x] = a.p.starts[threadIdx.x] + a.p.scratch[(size_t)blockIdx.x * a.E + threadIdx.x];
   }
   __syncthreads();
@@ -980,7 +995,7 @@ mhc_status_t mhc_expert_plan_run(int64_t T, int64_t k, int64_t E, const int32_t*
     const cudaError_t z = cudaMemsetAsync(plan, 0, (size_t)l.total * 4, s);
     return z == cudaSuccess ? MHC_OK : fail(MHC_ERR_RUNTIME, "clearing the plan failed: %s", cudaGetErrorString(z));
   }
-  PlanArgs a = {experts, plan_view(l, E, plan), (int)l.slots, (int)E, kPlanChunk};
+  PlanArgs a = {experts, plan_view(l, E, plan), (int)l.slots, (int)E, (int)plan_chunk(l.slots)};
   const size_t smem = plan_smem((int)E);
   cudaError_t e = cudaSuccess;
   if (smem > 32 * 1024) {                        // beside the static arrays more than a kernel has by default
@@ -991,12 +1006,24 @@ mhc_status_t mhc_expert_plan_run(int64_t T, int64_t k, int64_t E, const int32_t*
   if (l.slots <= kPlanAlone) {
     plan_alone_kernel<<<1, kPlanThreads, smem, s>>>(a);
   } else {
-    const int blocks = (int)((l.slots + kPlanChunk - 1) / kPlanChunk);
+    const int blocks = (int)((l.slots + a.chunk - 1) / a.chunk);
     plan_count_kernel<<<blocks, kPlanThreads, smem, s>>>(a);
-    plan_sum_kernel<<<1, kPlanThreads, 0, s>>>(a, blocks);
-    plan_place_kernel<<<blocks, kPlanThreads, smem, s>>>(a);
+    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, plan_sum_kernel, a, blocks);
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.dynamicSmemBytes = smem;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, plan_place_kernel, a);
   }
-  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MHC_ERR_RUNTIME, "plan launch failed: %s", cudaGetErrorString(e));
   return MHC_OK;
 }
