@@ -19,7 +19,7 @@ namespace mhc {
 namespace {
 
 constexpr int kNormBlock = 16384;                // elements that one block of the norm sums at least
-constexpr int kNormBlocks = 1216;                // blocks in all, at least one a matrix: eight an SM
+constexpr int kNormBlocks = 1216;                // blocks in all, at least one a matrix: eight an SM (608: 41 us for 32 of 2816 x 1024, not 37)
 
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // e in [-126, 127]
 
@@ -54,60 +54,49 @@ __device__ __forceinline__ void load8(const void* p, long long at, long long end
   }
 }
 
-// Sum over the block, in every thread.
-__device__ __forceinline__ double block_sum(double v, double* room) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) s += room[w];
-  return s;
-}
+// The exponent of a positive fp64 number (no subnormal), and a power of two.
+__device__ __forceinline__ int exponent(double v) { return ((__double2hiint(v) >> 20) & 0x7FF) - 1023; }
+__device__ __forceinline__ double pow2d(int e) { return __hiloint2double((e + 1023) << 20, 0); }
 
 // Sums of squares of one block's part of a matrix.  A thread's 128 bytes (64 values, or 32 of
 // fp32) share a power of two that brings the largest near one, so no square over- or
-// underflows, and one fp64 addition (one for every eight values kept the fp64 units busy
-// for 80 us of 184 MB, which now take 41: 4.5 TB/s).
+// underflows; a thread's sum (compensated) and a warp's are an fp32 number and such a power,
+// a block's is fp64.
+// (184 MB: 80 us with an fp64 addition for every eight values, 43 with one a thread and step
+// and for the sum over the block, 37 now: 5.0 TB/s.)
 template <int kType>
 __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const void* x, long long count, bool whole, double* part) {
   constexpr int kV = kType == MHC_DTYPE_FP32 ? 4 : 8;          // groups of eight values
-  constexpr long long kStep = 256 * 8 * kV;
-  __shared__ double room[8];
+  constexpr long long kUnit = 256 * 8;                         // a group of each thread
+  __shared__ float room[8];
+  __shared__ int room_e[8];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) header[threadIdx.x] = 0u;
   pdl_trigger();
-  const long long base = (long long)blockIdx.y * count, end = base + count;
-  double acc = 0.0;
-  float v[kV][8];
-  auto load = [&](long long i0) {
+  const long long base = (long long)blockIdx.y * count, end = base + count, units = (count + kUnit - 1) / kUnit;
+  const long long last = min(units * (blockIdx.x + 1) / gridDim.x * kUnit, count);
+  float acc = 0.0f, low = 0.0f;                  // (acc - low) 4^at, at the largest exponent so far
+  int at = -126;
+  for (long long i0 = units * blockIdx.x / gridDim.x * kUnit + threadIdx.x * 8; i0 < last; i0 += kV * kUnit) {
+    float v[kV][8];
 #pragma unroll
     for (int b = 0; b < kV; ++b) {
-      const long long i = i0 + b * 2048;
-      if (i < count) {
+      const long long i = i0 + b * kUnit;
+      if (i < last) {
         load8<kType>(x, base + i, end, whole, v[b]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[b][j] = 0.0f;
       }
     }
-  };
-  for (long long i0 = (long long)blockIdx.x * kStep + threadIdx.x * 8; i0 < count; i0 += (long long)gridDim.x * kStep) {
-    load(i0);
     float top = 0.0f;
-    bool bad = false;
+    if (kType != MHC_DTYPE_FP16) {               // whose squares fp32 holds as they are
 #pragma unroll
-    for (int b = 0; b < kV; ++b)
+      for (int b = 0; b < kV; ++b)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float m = fabsf(v[b][j]);
-        bad |= !(m < __int_as_float(0x7F800000));
-        top = fmaxf(top, m);
-      }
-    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -126);   // of a subnormal -126
-    // v 2^-e, in two factors: 2^126 and more is not a finite power
-    const float f0 = pow2f(-(e >> 1)), f1 = pow2f(-(e - (e >> 1)));
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[b][j]));
+    }
+    const int e = kType == MHC_DTYPE_FP16 ? 0 : min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);   // of a subnormal -126
+    const float f = pow2f(-e);                   // leaves the largest below 4
     float s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.0f;
@@ -115,34 +104,67 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(uint32_t* header, const 
     for (int b = 0; b < kV; ++b)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float q = v[b][j] * f0 * f1;
+        const float q = kType == MHC_DTYPE_FP16 ? v[b][j] : v[b][j] * f;
         s[j] = fmaf(q, q, s[j]);
       }
-    const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-    acc += bad ? (double)NAN : (double)sum * __longlong_as_double((long long)(2 * e + 1023) << 52);
+    const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));   // not finite: nor were all values
+    const int most = max(at, e);
+    const float old = pow2f(max(2 * (at - most), -126)), y = fmaf(sum, pow2f(max(2 * (e - most), -126)), -low * old);
+    acc *= old;
+    const float t = acc + y;                     // compensated: a block may add thousands
+    low = (t - acc) - y;
+    acc = sum < INFINITY ? t : NAN;
+    at = most;
   }
-  const double sum = block_sum(acc, room);
-  if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+  const int most = __reduce_max_sync(0xFFFFFFFFu, at);
+  acc *= pow2f(max(2 * (at - most), -126));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
+  if ((threadIdx.x & 31) == 0) {
+    room[threadIdx.x >> 5] = acc;
+    room_e[threadIdx.x >> 5] = most;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum = fma((double)room[w], pow2d(2 * room_e[w]), sum);
+    part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+  }
 }
 
-// S x / (norm + eps) in fp16, rows of `pitch`: 184 MB of bf16 to as many take 71 us (5.2
-// TB/s; four times the loads in flight and the last rows first, which the L2 still holds,
-// made no difference).
+// S x / (norm + eps) in fp16, rows of `pitch`: 184 MB of bf16 to as many take 62 us (6.0
+// TB/s; 75 with the factor from fp64 roots and quotients in every thread).
 template <int kType>
 __global__ void __launch_bounds__(256) orth_scale_kernel(const void* x, int rows, int cols, int pitch, bool whole,
                                                          const double* part, int parts, float eps, double S, uint16_t* out) {
   __shared__ double room[8];
+  __shared__ float factor[2];
   pdl_trigger();
   pdl_wait();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) s += part[(size_t)blockIdx.y * parts + i];
-  const double norm = sqrt(block_sum(s, room)) + (double)eps;
-  // S / norm as f0 f1: a power and what remains, both within fp32
-  const double f = norm == 0.0 ? 0.0 : S / norm;
-  int e = 0;
-  const double m = frexp(f, &e);
-  e = min(max(e, -200), 200);
-  const float f0 = pow2f(e >> 1), f1 = (float)ldexp(m, e - (e >> 1));
+  if ((int)(threadIdx.x & ~31u) < parts) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[(size_t)blockIdx.y * parts + i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = room[0];
+    for (int w = 1; w < 8 && w * 32 < parts; ++w) s += room[w];
+    // root and quotient in fp32 of what is left beside powers of two
+    int e = exponent(s) >> 1;
+    const double norm = s == 0.0 ? 0.0 : (double)sqrtf((float)(s * pow2d(-2 * e))) * pow2d(e), d = norm + (double)eps;
+    e = exponent(d);
+    const float q = (float)S / (float)(d * pow2d(-e));
+    // S / d as f0 f1, both within fp32
+    e = min(max(-e, -200), 200);
+    factor[0] = d == 0.0 ? 0.0f : pow2f(e >> 1);
+    factor[1] = d == 0.0 ? 0.0f : d != d ? NAN : q * pow2f(e - (e >> 1));
+  }
+  __syncthreads();
+  const float f0 = factor[0], f1 = factor[1];
   const int groups = pitch / 8;
   const long long base = (long long)blockIdx.y * rows, items = (long long)rows * groups;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
