@@ -37,6 +37,12 @@ __device__ __forceinline__ unsigned long long order(double v) {
   const unsigned long long b = (unsigned long long)__double_as_longlong(v);
   return v != v ? ~0ull : b ^ ((b >> 63) ? ~0ull : 1ull << 63);
 }
+// Of the result of an fp32 sum, whose NaN is 0x7FFFFFFF.
+__device__ __forceinline__ uint32_t order_sum(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long order_sum(double v) { return order(v); }
 __device__ __forceinline__ float unorder(uint32_t u) {
   return u == 0xFFFFFFFFu ? NAN : __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
@@ -235,11 +241,14 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
         ++grp;
         grp_end += per;
       }
-      u[i] = e0 + i < E && ((stays >> (grp & 31)) & 1u) && l[i] != -INFINITY ? order(by_key ? key[i] : (K)l[i]) : kOut;
+      u[i] = e0 + i < E && ((stays >> (grp & 31)) & 1u) ? order(by_key ? key[i] : (K)l[i]) : kOut;
     }
+  } else if (by_key) {                           // -inf, of a logit too, is kOut
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] = order_sum(key[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = l[i] != -INFINITY ? order(by_key ? key[i] : (K)l[i]) : kOut;
+    for (int i = 0; i < V; ++i) u[i] = order((K)l[i]);
   }
   uint32_t ids = 0;                              // the sorted ones' places in the lane, four bits each
   if constexpr (kSorted) {
@@ -449,11 +458,14 @@ __global__ void __launch_bounds__(route_warps(V) * 32, route_blocks(V)) route_ke
     float l[V];
     load_row<kType, V>(a, row, lane, l);
     // Scores; softmax: top and sum of the row.
-    uint32_t topu = Ordered<float>::kOut;
+    float top = 0.0f;
+    if (!a.sigmoid) {
+      uint32_t topu = Ordered<float>::kOut;
 #pragma unroll
-    for (int i = 0; i < V; ++i) topu = max(topu, order(l[i]));
-    topu = warp_max(topu);
-    const float top = topu == Ordered<float>::kOut ? 0.0f : unorder(topu);
+      for (int i = 0; i < V; ++i) topu = max(topu, order(l[i]));
+      topu = warp_max(topu);
+      if (topu != Ordered<float>::kOut) top = unorder(topu);
+    }
     const bool scores = a.bias != nullptr || a.groups > 1;
     float smax = 1.0f;
     RowSum<float> r = {top, 0.0f};
