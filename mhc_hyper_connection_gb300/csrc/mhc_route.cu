@@ -3,8 +3,8 @@
 //
 // Routing and its gradient read and write each score once; a row is a warp's, its
 // scores in registers, E / 32 consecutive ones a lane.  Bound by the warp's instructions
-// (keys, sorting, the groups and a maximum over the warp for each choice: 1430 a row of 256
-// experts, 8 of 4 groups of 8), not by memory: 16384 such rows take 44 us, their bytes 2.6.
+// (keys, sorting, the groups and a maximum over the warp for each choice: 1290 a row of
+// 256 experts, 8 of 4 groups of 8), not by memory: 16384 such rows take 37 us, their bytes 2.6.
 #include <math.h>
 
 #include "mhc_experts.cuh"
@@ -287,16 +287,13 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
 #pragma unroll
     for (int i = 0; i < V; ++i) best = u[i] > best ? u[i] : best;
   }
-  // lane j's; of the two behind the chosen (kCheck) in every lane
-  int mine = -1, found = 0, after = -1;
-  U mykey = kOut, afterkey = kOut, thirdkey = kOut;
-  const int rounds = kCheck && by_key ? k + 2 : k;
-  for (int j = 0; j < rounds; ++j) {
+  // the largest that is left: its key and expert; false: none
+  auto take = [&](U& m, int& e) -> bool {
     if constexpr (kSorted) best = u[0];
-    const U m = warp_max(best);
-    if (m == kOut) break;
+    m = warp_max(best);
+    if (m == kOut) return false;
     const int w = __ffs(__ballot_sync(kFull, best == m)) - 1;
-    int e = 0;
+    e = 0;
     if constexpr (kSorted) {
       e = __shfl_sync(kFull, e0 + (int)(ids & 15u), w);
       if (lane == w) {
@@ -321,16 +318,32 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
       }
       e = __shfl_sync(kFull, e, w);
     }
-    ++found;
-    if (lane == j && j < k) {
-      mine = e;
-      mykey = m;
+    return true;
+  };
+  // lane j's; of the two behind the chosen (kCheck) in every lane
+  int mine = -1, found = 0, after = -1;
+  U mykey = kOut, afterkey = kOut, thirdkey = kOut;
+  {
+    U m;
+    int e;
+    while (found < k && take(m, e)) {
+      if (lane == found) {
+        mine = e;
+        mykey = m;
+      }
+      ++found;
     }
-    if (j == k) {
-      after = e;
-      afterkey = m;
+    if (kCheck && by_key && found == k) {
+#pragma unroll 1
+      while (found < k + 2 && take(m, e)) {
+        if (found == k) {
+          after = e;
+          afterkey = m;
+        }
+        thirdkey = m;
+        ++found;
+      }
     }
-    if (j == k + 1) thirdkey = m;
   }
   if constexpr (kCheck) {
     if (by_key && found > 1 && !unsure) {
@@ -450,11 +463,11 @@ __global__ void __launch_bounds__(route_warps(V) * 32, route_blocks(V)) route_ke
   const long long first = a.T * blockIdx.x / gridDim.x, last = a.T * (blockIdx.x + 1) / gridDim.x;
   if (threadIdx.x == 0) taken = 0;
   __syncthreads();
-  for (;;) {
-    unsigned n = lane == 0 ? atomicAdd(&taken, 1u) : 0u;
-    n = __shfl_sync(kFull, n, 0);
-    const long long row = first + n;
-    if (row >= last) break;
+  auto draw = [&]() -> long long {
+    const unsigned n = lane == 0 ? atomicAdd(&taken, 1u) : 0u;
+    return first + __shfl_sync(kFull, n, 0);
+  };
+  for (long long row = draw(); row < last; row = draw()) {
     float l[V];
     load_row<kType, V>(a, row, lane, l);
     // Scores; softmax: top and sum of the row.
