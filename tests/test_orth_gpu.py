@@ -99,6 +99,23 @@ def test_single(cuda_device, m, n, kind):
     _check(g, orthogonalise(g, out=half))
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("m,n", [(1, 100), (100, 1), (2, 2500), (4, 1000), (1000, 4), (23, 3078), (3078, 23), (130, 6000)])
+def test_few_rows(cuda_device, m, n, kind):
+    """Rows that are nearly orthogonal to start with: A is nearly a multiple of 1, and what its
+    and B's diagonals lost to fp16 would grow up to tenfold (3.9 x 1.4 x 1.6 over the last
+    steps for singular values of 0.2).  These are carried beside, so what stays is random: five
+    roundings of X, 2^-12 rms each, of which nearly all lies across X's rows and keeps its
+    size, granted a factor of 2; the off-diagonals, 1 / sqrt(n) of that; the result's own, u /
+    sqrt(3)."""
+    from mhc_hyper_connection_gb300 import orthogonalise
+    g = _noise(cuda_device, (m, n), torch.float32, 3 * m + n)
+    want = _exact(g)
+    out = orthogonalise(g, out=torch.empty(g.shape, dtype=kind, device=cuda_device)).double()
+    tol = ((2 * 5 ** 0.5 * 2.0 ** -12) ** 2 + U[kind] ** 2 / 3) ** 0.5
+    assert float((out - want).norm()) <= tol * float(want.norm())
+
+
 @pytest.mark.parametrize("shape", [(3, 40, 72), (2, 2, 300, 264), (17, 264, 130), (5, 513, 770)])
 def test_batches(cuda_device, shape):
     """Every matrix of a batch has its own norm, and gives the bits that it gives alone."""
