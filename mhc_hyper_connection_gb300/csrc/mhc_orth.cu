@@ -189,7 +189,8 @@ struct OrthJob {
   GemmShape g;                   // tiles of one matrix
   int count, per, width, kiters;
   int split;                     // log2(256 / width)
-  FastDiv by_matrix;
+  int parts, part_kiters;        // of the depth, tiles of their own: `row0` is a tile's first chunk, `rows` its part
+  FastDiv by_matrix, by_parts;
 
   struct Raw {};
   __device__ __forceinline__ void prefetch() const {
@@ -224,6 +225,13 @@ struct OrthJob {
     o.width = halved ? width >> 1 : width;
     if (halved) o.tn = 2 * o.tn + half;
     o.kiters = kiters;
+    if (parts > 1) {
+      const int e = by_parts(o.e);
+      o.rows = o.e - e * parts;
+      o.e = e;
+      o.row0 = o.rows * part_kiters;
+      o.kiters = min(part_kiters, kiters - o.row0);
+    }
     return o;
   }
   __device__ __forceinline__ int bytes(const GTile& o) const {
@@ -233,7 +241,7 @@ struct OrthJob {
   __device__ __forceinline__ int steps(const GTile&, int) const { return kFfnTileK / 16; }
   __device__ __forceinline__ uint32_t idesc(const GTile& o) const { return grp_idesc(true, kA, kB, o.width); }
   __device__ __forceinline__ void load_a(const GTile& o, int k, uint32_t sa, uint32_t bar, int rank) const {
-    const int k0 = k * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf;
+    const int k0 = (o.row0 + k) * kFfnTileK, m0 = o.tm * kFfnTileM + rank * kGemmHalf;
     if constexpr (kA) {
       tma_load_4d_pair(sa, &a, bar, 0, k0, m0 >> 6, o.e);
     } else {
@@ -241,7 +249,7 @@ struct OrthJob {
     }
   }
   __device__ __forceinline__ void load_b(const GTile& o, int k, uint32_t sb, uint32_t bar, int rank) const {
-    const int k0 = k * kFfnTileK, n0 = o.tn * o.width + rank * (o.width >> 1);
+    const int k0 = (o.row0 + k) * kFfnTileK, n0 = o.tn * o.width + rank * (o.width >> 1);
     const CUtensorMap* t = o.width == width ? &b : &b_half;
     if constexpr (kB) {
       if (o.width > 128) tma_load_4d_pair(sb, t, bar, 0, k0, n0 >> 6, o.e);
@@ -395,13 +403,122 @@ struct EpiOrth {
   }
 };
 
+// A part's sums as they are, for the kernel below to join.
+struct EpiParts {
+  float* room;                   // [matrix][part][M][pitch]
+  int M, pitch, parts;
+  using Pre = NoPre;
+  __device__ __forceinline__ void pre(const GTile&, NoPre&, int, int, int, int) const {}
+  __device__ __forceinline__ void tile(const GTile& g, NoPre&, int, int, uint32_t taddr, int rank, int q, int grp, uint8_t*, int lane,
+                                       int) const {
+    const int m0 = g.tm * kFfnTileM + rank * kGemmHalf + q * 32, n0 = g.tn * g.width, half = g.width >> 1;
+    if (m0 >= M) return;
+    float* to = room + ((size_t)g.e * parts + g.rows) * M * pitch;
+#pragma unroll 1
+    for (int col = grp * half; col < (grp + 1) * half && n0 + col < pitch; col += 32) {
+      float v[4][4][2];
+      frag_ld<4>(taddr + col, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = m0 + i * 8 + (lane >> 2);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int n = n0 + col + b * 8 + (lane & 3) * 2;
+          if (row < M && n < pitch) *reinterpret_cast<float2*>(to + (size_t)row * pitch + n) = make_float2(v[i][b][0], v[i][b][1]);
+        }
+      }
+    }
+  }
+};
+
+// A = beta times the sum of the parts in their order, and what its diagonal leaves.  Squares
+// of 256 on and below the diagonal are there; a block takes 32 x 32 and writes its mirror.
+__global__ void __launch_bounds__(256) orth_join_kernel(const float* room, int parts, int side, int pitch, int blocks, float beta,
+                                                        uint16_t* out, float* leaves) {
+  __shared__ uint16_t tile[32][33];
+  pdl_trigger();
+  const int bi = blockIdx.x / blocks, i0 = bi * 32, j0 = ((int)blockIdx.x - bi * blocks) * 32;
+  const bool mirror = i0 >> 8 != j0 >> 8;
+  if (i0 >> 8 < j0 >> 8) return;
+  pdl_wait();
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, j = j0 + tx;
+  const size_t plane = (size_t)side * pitch;
+  const float* from = room + (size_t)blockIdx.y * parts * plane;
+  uint16_t* to = out + (size_t)blockIdx.y * plane;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + ty + 8 * q;
+      if (i < side && j < side) s[q] += from[p * plane + (size_t)i * pitch + j];
+    }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int i = i0 + ty + 8 * q;
+    const float v = s[q] * beta;
+    const __half h = __float2half_rn(v);
+    const uint16_t w = __half_as_ushort(h);
+    tile[ty + 8 * q][tx] = w;
+    if (i < side && j < side) {
+      to[(size_t)i * pitch + j] = w;
+      if (i == j) leaves[(size_t)blockIdx.y * pitch + i] = v - __half2float(h);
+    }
+  }
+  if (mirror) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = ty + 8 * q;
+      if (j0 + r < side && i0 + tx < side) to[(size_t)(j0 + r) * pitch + i0 + tx] = tile[tx][r];
+    }
+  }
+}
+
 // --------------------------------------------------------------------- host
+
+// How a product's tiles are cut.  In times of a stage of a tile of 256 (0.28 us): a stage of
+// 128 columns takes 0.6 and of 64 0.5 of it; an epilogue, 9 for 256 columns, runs beside the
+// next tile's stages and after the last one's.  (515 x 259: three tiles of 256 or ten of 64.)
+// A product X X^T whose few tiles are deep is cut along its depth too, into parts that leave
+// pairs none idle and take eight chunks or more; another launch joins them (12).
+struct Cut {
+  int width, parts, part_kiters;
+};
+int64_t tiles_of(int64_t M, int64_t N, int w, bool sym) {
+  const int64_t tm = (M + 255) / 256;
+  return !sym ? tm * ((N + w - 1) / w) : tm == 1 ? (N + w - 1) / w : tm * (tm + 1) / 2 * (256 / w);
+}
+Cut cut(int64_t batch, int64_t M, int64_t N, int64_t K, bool sym, bool gram, int pairs) {
+  const int64_t kiters = (K + kFfnTileK - 1) / kFfnTileK;
+  Cut best = {256, 1, (int)kiters};
+  double least = 1e30;
+  for (int w = 256; w >= 64; w /= 2) {
+    if (w > 64 && N <= w / 2) continue;
+    const double stage = w == 256 ? 1.0 : w == 128 ? 0.6 : 0.5, epi = 9.0 * w / 256;
+    const int64_t tiles = batch * tiles_of(M, N, w, sym);
+    int64_t most = gram ? pairs / tiles : 1;
+    if (most > kiters / 8) most = kiters / 8;
+    for (int64_t parts = 1; parts <= (most > 1 ? most : 1); parts += most > 1 ? most - 1 : 1) {
+      const int64_t each = (kiters + parts - 1) / parts;
+      const double rounds = (double)((tiles * parts + pairs - 1) / pairs), main = each * stage;
+      const double cost = rounds * (main > epi ? main : epi) + epi + (parts > 1 ? 12.0 : 0.0);
+      if (cost < least) {
+        least = cost;
+        best = {w, (int)((kiters + each - 1) / each), (int)each};
+      }
+    }
+  }
+  return best;
+}
+constexpr int kPairs = 76;       // that products are cut for, whatever the device: a workspace's size goes by it
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct OrthLayout {
   int64_t parts, pitch, side, spitch;
-  size_t norm, left[2], x[2], p, q, total;
+  Cut gram;                      // X X^T
+  size_t norm, left[2], x[2], p, q, room, total;
 };
 OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
   OrthLayout l;
@@ -421,7 +538,9 @@ OrthLayout orth_layout(int64_t batch, int64_t rows, int64_t cols) {
   l.x[1] = l.x[0] + xb;
   l.p = l.x[1] + xb;
   l.q = l.p + pb;
-  l.total = l.q + pb + 256;                     // orth_map_blocks reads a little past a buffer
+  l.gram = cut(batch, l.side, l.side, rows < cols ? cols : rows, true, true, kPairs);
+  l.room = l.q + pb + 256;                      // orth_map_blocks reads a little past a buffer
+  l.total = l.room + (l.gram.parts > 1 ? up256((size_t)batch * l.gram.parts * l.side * l.spitch * 4) : 0);
   return l;
 }
 
@@ -466,53 +585,44 @@ struct Product {
   double alpha, beta;
   bool whole;
 };
-// Width of the tiles: 256, or 128 or 64 where that ends sooner.  In times of a stage of a
-// tile of 256 (0.28 us): a stage of 128 takes 0.6 and of 64 0.5 of it; an epilogue, 9 for
-// 256 columns, runs beside the next tile's stages and after the last one's.  (515 x 259:
-// three tiles of 256 or ten of 64.)
-int tile_width(int64_t batch, int64_t M, int64_t N, int64_t K, bool sym, int sms) {
-  const int64_t kiters = (K + kFfnTileK - 1) / kFfnTileK, tm = (M + 255) / 256;
-  int best = 256;
-  double least = 1e30;
-  for (int w = 256; w >= 64; w /= 2) {
-    if (w > 64 && N <= w / 2) continue;
-    const double stage = w == 256 ? 1.0 : w == 128 ? 0.6 : 0.5, epi = 9.0 * w / 256;
-    const int64_t tiles = batch * (sym ? tm * (tm + 1) / 2 * (256 / w) : tm * ((N + w - 1) / w));
-    const double rounds = (double)((tiles + sms / 2 - 1) / (sms / 2)), main = kiters * stage;
-    const double cost = rounds * (main > epi ? main : epi) + epi;
-    if (cost < least) {
-      least = cost;
-      best = w;
-    }
-  }
-  return best;
+// A job over matrices a and b of a product cut as `c` says.
+template <bool kA, bool kB, bool kSym>
+bool orth_job(OrthJob<kA, kB, kSym>* job, const Product& p, const Matrix& a, const Matrix& b, const Cut& c) {
+  job->width = c.width;
+  job->split = c.width == 256 ? 0 : c.width == 128 ? 1 : 2;
+  job->parts = c.parts;
+  job->part_kiters = c.part_kiters;
+  if (!(kA ? orth_map_blocks(&job->a, a.p, a.cols, a.rows, a.pitch, p.batch)
+           : orth_map(&job->a, a.p, a.cols, a.rows, a.pitch, p.batch, (uint32_t)kGemmHalf)) ||
+      !(kB && c.width > 128 ? orth_map_blocks(&job->b, b.p, b.cols, b.rows, b.pitch, p.batch)
+                            : orth_map(&job->b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)c.width / 2)))
+    return false;
+  GemmShape& g = job->g;
+  g = GemmShape();
+  g.tiles_m = (int)((p.M + kFfnTileM - 1) / kFfnTileM);
+  g.tiles_n = (int)((p.N + c.width - 1) / c.width);
+  g.band = 8;
+  g.by_band = FastDiv((uint32_t)(g.band * g.tiles_n));
+  g.by_rows = FastDiv((uint32_t)g.band);
+  g.by_last = FastDiv((uint32_t)(g.tiles_m % g.band ? g.tiles_m % g.band : g.band));
+  job->per = (int)tiles_of(p.M, p.N, c.width, kSym);
+  job->count = (int)(job->per * p.batch * c.parts);
+  job->by_matrix = FastDiv((uint32_t)job->per);
+  job->by_parts = FastDiv((uint32_t)c.parts);
+  job->kiters = (int)((p.K + kFfnTileK - 1) / kFfnTileK);
+  job->whole = job->count;
+  job->b_half = job->b;
+  return true;
 }
 
 template <bool kA, bool kB, bool kHasC, bool kSym, int kLast>
 cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* mapped, cudaStream_t s) {
   OrthJob<kA, kB, kSym> job;
-  job.width = tile_width(p.batch, p.M, p.N, p.K, kSym, p.sms);
-  job.split = job.width == 256 ? 0 : job.width == 128 ? 1 : 2;
-  *mapped = (kA ? orth_map_blocks(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch)
-                : orth_map(&job.a, a.p, a.cols, a.rows, a.pitch, p.batch, (uint32_t)kGemmHalf)) &&
-            (kB && job.width > 128 ? orth_map_blocks(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch)
-                                   : orth_map(&job.b, b.p, b.cols, b.rows, b.pitch, p.batch, kB ? kFfnBoxMn : (uint32_t)job.width / 2));
+  *mapped = orth_job(&job, p, a, b, cut(p.batch, p.M, p.N, p.K, kSym, false, p.sms / 2));
   if (!*mapped) return cudaErrorInvalidValue;
-  GemmShape& g = job.g;
-  g = GemmShape();
-  g.tiles_m = (int)((p.M + kFfnTileM - 1) / kFfnTileM);
-  g.tiles_n = (int)((p.N + job.width - 1) / job.width);
-  g.band = 8;
-  g.by_band = FastDiv((uint32_t)(g.band * g.tiles_n));
-  g.by_rows = FastDiv((uint32_t)g.band);
-  g.by_last = FastDiv((uint32_t)(g.tiles_m % g.band ? g.tiles_m % g.band : g.band));
-  job.per = kSym ? (g.tiles_m * (g.tiles_m + 1) / 2) << job.split : g.tiles_m * g.tiles_n;
-  job.count = (int)(job.per * p.batch);
-  job.by_matrix = FastDiv((uint32_t)job.per);
   // Where the last round has tiles for at most half the pairs, these are halved: 320 tiles of
   // 32 matrices of 1024, 5 rounds, now 4.6.
   const int pairs = p.sms / 2, over = job.count % pairs;
-  job.whole = job.count;
   if (job.width == 256 && job.count > pairs && over > 0 && 2 * over <= pairs) {
     job.whole = job.count - over;
     job.count += over;
@@ -520,12 +630,32 @@ cudaError_t product(const Product& p, const Matrix& a, const Matrix& b, bool* ma
       *mapped = false;
       return cudaErrorInvalidValue;
     }
-  } else {
-    job.b_half = job.b;
   }
-  job.kiters = (int)((p.K + kFfnTileK - 1) / kFfnTileK);
   const EpiOrth<kHasC, kSym, kLast, !kSym && !kB> e = {p.left, p.leaves, (int)p.side_pitch, p.c, p.out, (int)p.M, (int)p.N, (int)p.pitch, (float)p.alpha, (float)p.beta, p.whole};
   return launch_group(job, p.call, e, job.count, p.sms, true, s);
+}
+
+// A = beta X X^T (kMn: X^T X) in parts of the depth.
+template <bool kMn>
+cudaError_t gram(const Product& p, const Matrix& x, const Cut& c, float* room, bool* mapped, cudaStream_t s) {
+  OrthJob<kMn, kMn, true> job;
+  *mapped = orth_job(&job, p, x, x, c);
+  if (!*mapped) return cudaErrorInvalidValue;
+  const EpiParts epi = {room, (int)p.M, (int)p.pitch, c.parts};
+  const cudaError_t e = launch_group(job, p.call, epi, job.count, p.sms, true, s);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const unsigned blocks = (unsigned)((p.M + 31) / 32);
+  cfg.gridDim = dim3(blocks * blocks, (unsigned)p.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, orth_join_kernel, static_cast<const float*>(room), c.parts, (int)p.M, (int)p.pitch, (int)blocks,
+                            (float)p.beta, p.out, p.leaves);
 }
 
 template <int kType>
@@ -638,7 +768,12 @@ mhc_status_t mhc_orth_run(const mhc_orth_args* a, void* stream) {
     p.pitch = l.spitch;
     p.alpha = 0.0;
     p.beta = SA / (S * S);
-    e = tall ? product<true, true, false, true, 0>(p, X, X, &mapped, s) : product<false, false, false, true, 0>(p, X, X, &mapped, s);
+    if (l.gram.parts > 1) {
+      float* room = reinterpret_cast<float*>(ws + l.room);
+      e = tall ? gram<true>(p, X, l.gram, room, &mapped, s) : gram<false>(p, X, l.gram, room, &mapped, s);
+    } else {
+      e = tall ? product<true, true, false, true, 0>(p, X, X, &mapped, s) : product<false, false, false, true, 0>(p, X, X, &mapped, s);
+    }
     if (e == cudaSuccess) {
       p.K = side;
       p.left = left_a;

@@ -116,6 +116,22 @@ def test_few_rows(cuda_device, m, n, kind):
     assert float((out - want).norm()) <= tol * float(want.norm())
 
 
+@pytest.mark.parametrize("shape", [(520, 4100), (4100, 520), (3, 300, 5000), (2, 5001, 257), (1025, 9000), (70, 32768), (32768, 70)])
+def test_deep(cuda_device, shape):
+    """X X^T of few tiles is summed in parts of its depth: the bound of every shape, the same
+    bits every time, nothing behind the workspace that was asked for."""
+    from mhc_hyper_connection_gb300 import orthogonalise, orthogonalise_status, orthogonalise_workspace
+    g = _noise(cuda_device, shape, torch.float32, sum(shape))
+    n = orthogonalise_workspace(shape, cuda_device).numel()
+    room = torch.full((n + 4096,), 0x7F, dtype=torch.uint8, device=cuda_device)
+    room[:256] = 0
+    out = orthogonalise(g, workspace=room[:n])
+    assert orthogonalise_status(room[:n]) == 0 and bool((room[n:] == 0x7F).all())
+    for x, y in zip(g.reshape(-1, *shape[-2:]), out.reshape(-1, *shape[-2:])):
+        _check(x, y)
+    assert torch.equal(out, orthogonalise(g, workspace=room[:n]))
+
+
 @pytest.mark.parametrize("shape", [(3, 40, 72), (2, 2, 300, 264), (17, 264, 130), (5, 513, 770)])
 def test_batches(cuda_device, shape):
     """Every matrix of a batch has its own norm, and gives the bits that it gives alone."""
