@@ -10,15 +10,16 @@
  * Each step maps every singular value s of X to a s + b s^3 + c s^5.
  *
  * x [batch, rows, cols] fp32, bf16 or fp16; out of the same shape, bf16 or fp16.
- * The norm is summed in fp32 pairs and fp64 whatever the magnitudes.  X, A and b A + c
- * A A are held in fp16 between the products (11 bits where bf16 has 8), scaled by powers
- * of two into its range; products are summed in fp32, X <- ... is formed in fp32 and
- * rounded once.  A result is off by about 2^-12 of its rows' size for each rounding,
+ * The norm is summed in fp32 beside powers of two (compensated) and fp64, whatever the
+ * magnitudes.  X, A and b A + c A A are held in fp16 between the products (11 bits where
+ * bf16 has 8), scaled by powers of two into its range, what the two diagonals lose by it in
+ * fp32 beside them; products are summed in fp32, X <- ... is formed in fp32 and rounded
+ * once.  A result is off by about 2^-12 of its rows' size for each rounding,
  * more for directions much weaker than the strongest (a singular value r times
  * smaller: r times as much of itself).  Singular values have to stay below 1.6:
  * the coefficients are the caller's to choose so (those in use stay below 1.3).  A zero matrix
  * gives zeros; one with an infinity or NaN gives NaN.  Results are bitwise
- * reproducible.
+ * reproducible; of a matrix in batches of different sizes the sums' order may differ.
  *
  * Sizes: batch in [0, 65535], rows and cols in [1, 32768], 1 to 32 steps.  x and out
  * contiguous device memory aligned to their element; out and workspace overlap neither x

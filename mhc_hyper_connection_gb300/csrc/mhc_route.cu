@@ -817,6 +817,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_alone_kernel(const PlanArgs
 }
 // Many slots: counts of each block's, then the sums over blocks, then the rows.  Each kernel
 // starts beside the one before; what the placing one counts again does not wait for it.
+// Bound by their starts and the latency of dependent loads: 32768 slots take 8.9 us (18.7 one
+// after the other with 4096 slots a block), 8192 take 8.5 (20 in one block alone).
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs a) {
   extern __shared__ uint16_t plan_hist[];
   pdl_trigger();
