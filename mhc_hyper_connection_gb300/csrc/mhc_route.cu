@@ -384,7 +384,7 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, long long row, int 
   const int E = a.E, e0 = lane * V;
   const long long base = row * E + e0;
   bool loaded = false;
-  if constexpr (V >= 4) {
+  if constexpr (V % 4 == 0) {
     if (E % 4 == 0) {                          // rows stay aligned to four elements
       loaded = true;
 #pragma unroll
@@ -894,6 +894,20 @@ size_t elem_bytes(int32_t dtype) { return dtype == MHC_DTYPE_FP32 ? 4 : 2; }
 // Vector loads of four logits and stores of four fp32 or two 16-bit gradients.
 size_t logits_align(int32_t dtype, int64_t E) { return E % 4 == 0 ? 4 * elem_bytes(dtype) : E % 2 == 0 ? 2 * elem_bytes(dtype) : elem_bytes(dtype); }
 
+// Scores of a lane: as few as hold the row (E = 160: five in 32 lanes, 17 us for 16384 rows,
+// with eight in 20 22), but first of all so that a group is whole lanes (8 groups: 23 and 39).
+int route_width(int E, int groups) {
+  constexpr int kWidths[] = {1, 2, 3, 4, 5, 6, 8, 16, 32};
+  int least = 0;
+  for (int v : kWidths) {
+    if (32 * v < E) continue;
+    if (!least) least = v;
+    const int per = E / groups, lanes = per / v;
+    if (groups > 1 && v <= 8 && per % v == 0 && (lanes & (lanes - 1)) == 0) return v;
+  }
+  return least;
+}
+
 template <int kType>
 cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
   // where no key is formed again and no group is marked nothing is kept in shared memory
@@ -903,13 +917,17 @@ cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
     const size_t smem = a.bias || a.groups > 1 ? (size_t)warps * a.E * 8 : 0;
     k<<<(unsigned)(rows < most ? rows : most), warps * 32, smem, s>>>(a);
   };
-  const int v = (a.E + 31) / 32;
-  if (v <= 1) run(route_kernel<kType, 1>, 1);
-  else if (v <= 2) run(route_kernel<kType, 2>, 2);
-  else if (v <= 4) run(route_kernel<kType, 4>, 4);
-  else if (v <= 8) run(route_kernel<kType, 8>, 8);
-  else if (v <= 16) run(route_kernel<kType, 16>, 16);
-  else run(route_kernel<kType, 32>, 32);
+  switch (route_width(a.E, a.groups)) {
+    case 1: run(route_kernel<kType, 1>, 1); break;
+    case 2: run(route_kernel<kType, 2>, 2); break;
+    case 3: run(route_kernel<kType, 3>, 3); break;
+    case 4: run(route_kernel<kType, 4>, 4); break;
+    case 5: run(route_kernel<kType, 5>, 5); break;
+    case 6: run(route_kernel<kType, 6>, 6); break;
+    case 8: run(route_kernel<kType, 8>, 8); break;
+    case 16: run(route_kernel<kType, 16>, 16); break;
+    default: run(route_kernel<kType, 32>, 32);
+  }
   return cudaGetLastError();
 }
 
