@@ -321,7 +321,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
     return true;
   };
   // lane j's; of the two behind the chosen (kCheck) in every lane
-  int mine = -1, found = 0, after = -1;
+  int mine = -1, found = 0, after = -1, third = -1;
   U mykey = kOut, afterkey = kOut, thirdkey = kOut;
   {
     U m;
@@ -340,6 +340,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
           after = e;
           afterkey = m;
         }
+        third = e;
         thirdkey = m;
         ++found;
       }
@@ -356,20 +357,32 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
         nk = afterkey;
       }
       const float x = unorder(mykey), y = unorder(nk);
-      bool near = lane < pairs && x - y <= tol * (smax + fmaxf(fabsf(x), fabsf(y)));
-      if (__any_sync(kFull, near)) {
-        // equal numbers in give equal keys: the index decides, nothing to look at
-        if (near)
-          near = !(load_logit<kType>(a.logits, row * E + mine) == load_logit<kType>(a.logits, row * E + ne) &&
-                   a.bias[mine] == a.bias[ne]);
-        if (__any_sync(kFull, near)) {
+      const bool close2 = lane < pairs && x - y <= tol * (smax + fmaxf(fabsf(x), fabsf(y)));
+      if (__any_sync(kFull, close2)) {
+        // equal numbers in give equal keys: the index decides
+        auto equal = [&](int p, int q) {
+          return load_logit<kType>(a.logits, row * E + p) == load_logit<kType>(a.logits, row * E + q) && a.bias[p] == a.bias[q];
+        };
+        const bool same = close2 && equal(mine, ne);
+        const float last = unorder(__shfl_sync(kFull, mykey, chosen - 1));
+        auto near_last = [&](U key) {
+          const float o = unorder(key);
+          return last - o <= tol * (smax + fmaxf(fabsf(last), fabsf(o)));
+        };
+        if (__any_sync(kFull, close2 && !same)) {
           // Where the second left out is clearly behind the last chosen, the order among the
           // chosen and the first left out is all there is to find.
-          const float last = unorder(__shfl_sync(kFull, mykey, chosen - 1)), third = unorder(thirdkey);
-          if (!a.sigmoid || (found > k + 1 && last - third <= tol * (smax + fmaxf(fabsf(last), fabsf(third))))) {
-            unsure = true;
-          } else {
-            mine = reorder64<kType>(a, row, mine, found > k ? after : -1, chosen, lane);
+          if (!a.sigmoid || (found > k + 1 && near_last(thirdkey))) unsure = true;
+          else mine = reorder64<kType>(a, row, mine, found > k ? after : -1, chosen, lane);
+        } else if (found > k + 1 && ((__ballot_sync(kFull, same) >> (k - 1)) & 1u)) {
+          // The first left out equals the last chosen: what comes behind its equals may have
+          // to stand before them.
+          while (near_last(thirdkey)) {
+            if (!equal(after, third)) {
+              unsure = true;
+              break;
+            }
+            if (!take(thirdkey, third)) break;
           }
         }
       }

@@ -78,6 +78,57 @@ def test_many_rows_near_ties(cuda_device):
                 _check(route_experts(l, 6, **how), l, None, 6, **how)
 
 
+@pytest.mark.parametrize("equals", [1, 2, 3, 6])
+def test_equals_before_a_larger_key(cuda_device, equals):
+    """Behind experts with the same logit and bias one whose key is larger by less than
+    fp32 shows, at the border of what is chosen."""
+    from mhc_hyper_connection_gb300 import route_experts
+    base = torch.linspace(1.0, 6.0, 400, device=cuda_device)
+    l = torch.full((400, 40), -4.0, device=cuda_device)
+    l[:, 1:1 + equals] = base[:, None]
+    l[:, 30] = torch.nextafter(base, base + 1)
+    l[:, 35] = base + 1
+    bias = torch.full((40,), 2.0 ** -12, device=cuda_device)
+    for score in ("sigmoid", "softmax"):
+        for k in range(1, equals + 3):
+            how = dict(score=score, renormalise=True, scale=1.0)
+            _check(route_experts(l, k, bias=bias, **how), l, bias, k, **how)
+
+
+@pytest.mark.parametrize("E,groups,top", [(72, 6, 2), (80, 5, 2), (96, 8, 3), (160, 8, 3), (160, 5, 2), (192, 8, 4), (192, 16, 5), (96, 32, 9)])
+def test_rows_of_three_five_and_six_scores_a_lane(cuda_device, E, groups, top):
+    """Widths between the powers of two: ordinary rows, and rows of the grid above."""
+    from mhc_hyper_connection_gb300 import route_experts
+    gen = torch.Generator(device=cuda_device).manual_seed(E + groups)
+    fine = torch.randint(0, 40, (400, E), generator=gen, device=cuda_device) / 8 - 2.5
+    fine = fine + torch.randint(-2, 3, (400, E), generator=gen, device=cuda_device) * 2.0 ** -22 * fine.abs()
+    for kind in ("fp32", "bf16"):
+        l, bias = _logits(cuda_device, 400, E, kind, E)
+        for x, b in ((l, bias), (fine.to(DT[kind]), torch.randint(0, 2, (E,), generator=gen, device=cuda_device) * 2.0 ** -12)):
+            for score in ("softmax", "sigmoid"):
+                for g, t, mark in ((1, 1, "max"), (groups, top, "top2"), (groups, top, "max")):
+                    how = dict(score=score, groups=g, top_groups=t, group_score=mark, renormalise=True, scale=1.0)
+                    _check(route_experts(x, 6, bias=b, **how), x, b, 6, **how)
+                    _check(route_experts(x, 6, **how), x, None, 6, **how)
+
+
+def test_signed_nan(cuda_device):
+    """A NaN of either sign, of a logit or of the bias, is chosen first."""
+    from mhc_hyper_connection_gb300 import route_experts
+    for bits in (0x7FC00000, -0x400000, 0x7F800001, -0x7FFFFF):
+        nan = torch.tensor([bits], dtype=torch.int32, device=cuda_device).view(torch.float32)[0]
+        assert bool(nan.isnan())
+        for E in (40, 256):
+            l, bias = torch.randn((3, E), device=cuda_device), torch.zeros((E,), device=cuda_device)
+            bad = l.clone()
+            bad[:, 33] = nan
+            worse = bias.clone()
+            worse[33] = nan
+            for x, b in ((bad, None), (bad, bias), (l, worse)):
+                r = route_experts(x, 4, score="sigmoid", bias=b)
+                assert (r.experts[:, 0] == 33).all() and (r.experts[:, 1:] != 33).all()
+
+
 def test_saturated_and_tiny_scores(cuda_device):
     """Logits at which fp32 scores are all 1 or all underflow still have their order and
     their shares."""
