@@ -28,7 +28,7 @@ struct RouteArgs {
   float scale;
 };
 
-// fp32 and fp64 as unsigned numbers of the same order, NaN above all; and back.
+// fp32 and fp64 as unsigned numbers of the same order, NaN above all, -0 below +0; and back.
 __device__ __forceinline__ uint32_t order(float v) {
   const uint32_t b = __float_as_uint(v);
   return v != v ? 0xFFFFFFFFu : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
@@ -191,6 +191,8 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
   constexpr bool kCheck = sizeof(K) == 4, kSorted = V <= 8;
   const int E = a.E, k = a.k, e0 = lane * V, per = E / a.groups;
   const bool by_key = a.bias != nullptr;
+  // Logits are ordered with + 0, which makes one number of the zeros; a key is no -0, being a
+  // sum with a score, nor are marks.
   U u[V];
   int id[V];
   bool close = false;
@@ -241,14 +243,14 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
         ++grp;
         grp_end += per;
       }
-      u[i] = e0 + i < E && ((stays >> (grp & 31)) & 1u) ? order(by_key ? key[i] : (K)l[i]) : kOut;
+      u[i] = e0 + i < E && ((stays >> (grp & 31)) & 1u) ? order(by_key ? key[i] : (K)l[i] + (K)0) : kOut;
     }
   } else if (by_key) {                           // -inf, of a logit too, is kOut
 #pragma unroll
     for (int i = 0; i < V; ++i) u[i] = order_sum(key[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = order((K)l[i]);
+    for (int i = 0; i < V; ++i) u[i] = order((K)l[i] + (K)0);
   }
   uint32_t ids = 0;                              // the sorted ones' places in the lane, four bits each
   if constexpr (kSorted) {
