@@ -209,8 +209,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
       bool ok = mbar_test_cluster(&tail->sched_full[slot], par) ||
                 wait_slow(&tail->sched_full[slot], par, ctl, kErrClusterWait, true);
       if (whole_warp) ok = __all_sync(0xFFFFFFFFu, ok);
+      bool read = true;
       if (ok) {
         const int4 lo = ld_slot(&tail->sched[slot]), hi = ld_slot(&tail->sched[slot].rows);
+        read = lo.x >= -1 && hi.w >= 0;          // always
         g.e = lo.x;
         g.tm = lo.y;
         g.tn = lo.z;
@@ -219,10 +221,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
         g.width = hi.y;
         g.kiters = hi.z;
         g.kind = hi.w;
-        if (g.kind < 0 || g.row0 < 0) g.e = -1;            // never so: both loads are complete before the arrival
       }
-      if (whole_warp) ok = __all_sync(0xFFFFFFFFu, g.e >= -1);
-      if (!whole_warp || lane == 0) arrive_relaxed(&tail->sched_empty[slot]);
+      // The arrival orders nothing by itself, and the scheduler's next write of the slot must
+      // not meet loads still under way: whether it is made goes by a value of each load, so no
+      // thread issues it before these are there, nor lane 0 before all lanes' are.
+      if (whole_warp) read = __all_sync(0xFFFFFFFFu, read);
+      if (!read) g.e = -1;
+      else if (!whole_warp || lane == 0) arrive_relaxed(&tail->sched_empty[slot]);
       return g;
     }
   };
