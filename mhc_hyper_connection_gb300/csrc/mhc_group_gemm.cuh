@@ -41,6 +41,7 @@ struct GrpTail {
   uint32_t sent_bytes[2][kGrpMaxStages];   // bytes of each CTA's last copies into a stage
   uint32_t tmem_base;
   uint32_t abort;
+  uint32_t handed;                         // tiles that the scheduler handed out, the last one's -1 among them
   GTile sched[kSchedSlots];
 };
 constexpr size_t kGrpSmem = (size_t)kGrpRing + 8 * kStageBuf + sizeof(GrpTail) + 1024;
@@ -171,7 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
       mbar_init(&tail->sched_empty[b], 19);      // MMA issuer, both producers, eight epilogue warps of each CTA
     }
     mbar_init(&tail->mma_done, 1);
-    tail->abort = 0u;
+    tail->abort = tail->handed = 0u;
     tail->sent[0] = tail->sent[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     job.prefetch();
@@ -349,11 +350,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
       };
       // The first two tiles of a pair are dealt out, the others drawn.
       int t = pair;
-      bool sent = true, more = true;
+      bool more = true;
+      uint32_t handed = 0;
       for (int n = 0; more; ++n) {
         GTile g = none;
         if (t < ntiles) g = job.make(t, job.fetch(t));
-        sent = publish(n, g);
+        const bool sent = publish(n, g);
+        handed += sent ? 1u : 0u;
         more = sent && g.e >= 0;
         if (n == 0) t = pair + pairs;
         if (n == 1 && Job::kEarly) pdl_wait();   // the counter is the first launch's
@@ -362,11 +365,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
           t = drawn < (unsigned)ntiles ? (int)drawn : ntiles;
         }
       }
-      // Every role reads up to the last tile's -1, so what was sent has arrived before the pair
-      // leaves; where waits gave up, the last of it is given time to.
-      if (!sent)
-        for (const uint64_t t0 = now_ns(); now_ns() - t0 < 20000;) {
-        }
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(map_cluster(&tail->handed, r)), "r"(handed) : "memory");
     }
   } else {
     // ===================================================== epilogue
@@ -399,6 +400,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrpThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
+  // Tiles are sent asynchronously.  Roles read all of them, up to the last one's -1, but where
+  // a wait of theirs gave up: then this CTA does not leave before the last ones are there.
+  if (Job::kDraw && scheduler && lane == 0 && *ctl.abort) {
+    const int handed = (int)*(volatile uint32_t*)&tail->handed;
+    for (int n = max(handed - kSchedSlots, 0); n < handed; ++n) {
+      const uint32_t par = (uint32_t)(n / kSchedSlots) & 1u;
+      if (!mbar_test(&tail->sched_full[n % kSchedSlots], par)) mbar_drain(&tail->sched_full[n % kSchedSlots], par);
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
