@@ -11,10 +11,11 @@
  *
  * The rows are copied together by expert and taken through two grouped products on
  * the tensor cores (fp32 sums), whose tiles follow the plan, so an expert without
- * rows costs nothing and its weights are not read.  a = act(g) (.) u and each
- * expert's output row are rounded to the 16-bit type (operand of the second product;
- * 16-bit rows of the last sum), the weighted sum over a token's experts is formed in
- * fp32 and rounded once.  In fp16 both have fp16's range.
+ * rows costs nothing and its weights are not read.  a = act(g) (.) u is rounded to
+ * the 16-bit type (operand of the second product; in fp16 it has fp16's range), each
+ * expert's output row to 16 significant bits with fp32's range (24-bit rows of the
+ * last sum: off by 2^-16 of themselves at most), the weighted sum over a token's
+ * experts is formed in fp32 and rounded once.
  *
  * Backward, from g and u as the forward kept them in 16 bits (gate_up [rows, 2, F],
  * rows as in the plan, mhc_expert_plan_rows of them):
@@ -23,10 +24,11 @@
  *   gu = w ga (.) act(g)   grad_x_t = sum_j gg Wg_e + gu Wu_e
  *   grad_w_gate_up_e = [gg^T x, gu^T x]      grad_w_down_e = grad_y^T (w a)
  *
- * gg, gu, w a and each expert's row of grad_x are rounded to the 16-bit type, the
- * gradients once from fp32 sums; an expert without rows gets zero gradients.  Every
- * sum's order follows from the sizes, the plan and the device: results are bitwise
- * reproducible.  Sums over more than 32768 rows are formed in parts joined in fp32.
+ * gg, gu and w a are rounded to the 16-bit type, each expert's row of grad_x to 24
+ * bits as an output row is, the gradients once from fp32 sums; an expert without
+ * rows gets zero gradients.  Every sum's order follows from the sizes, the plan and
+ * the device: results are bitwise reproducible.  Sums over more than 32768 rows are
+ * formed in parts joined in fp32.
  *
  * Sizes: D and F multiples of 8 in [8, 16384]; T, k and E as in mhc_route.h.  Tensors
  * are contiguous device memory owned by the caller, 16-byte aligned (weights,

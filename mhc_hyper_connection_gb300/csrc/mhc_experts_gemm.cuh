@@ -153,11 +153,18 @@ struct WeightGradJob {
 
 // ------------------------------------------------------------- epilogues
 
+// An fp32 sum with half a step of its upper 24 bits added, which then are the nearest (16
+// significant bits, 2^-16 of the sum off at most).  Not to infinities and NaN, nor to what
+// would become infinite.
+__device__ __forceinline__ uint32_t upper24(float v) {
+  return __float_as_uint(v) + (fabsf(v) < 0x1.ffffp127f ? 0x80u : 0u);
+}
+
 // The accumulator's column `row` and lane m as the upper 24 bits of the sum at [row, m] of
 // two planes: 16 bits, and 8 whose order inside sixteen columns is 0 8 1 9 .. 7 15.  What a
-// token's sum is off by is then 2^-16 of a term; rows rounded to 16 bits were half of y's
-// error (1.7 times what its own rounding leaves, so 1.4), in fp32 they cost a third more
-// traffic.
+// token's sum is off by is then 2^-16 of a term at most, with either sign; rows rounded to 16
+// bits were half of y's error (1.7 times what its own rounding leaves, so 1.4), in fp32 they
+// cost a third more traffic.
 struct EpiRows {
   using Pre = NoPre;
   uint16_t* hi;
@@ -177,14 +184,18 @@ struct EpiRows {
       uint32_t low[4][2];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t w[4];
+        uint32_t u[4][2], w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(v[i][b][0]), __float_as_uint(v[i][b][1]), 0x7632);
+        for (int i = 0; i < 4; ++i) {
+          u[i][0] = upper24(v[i][b][0]);
+          u[i][1] = upper24(v[i][b][1]);
+          w[i] = __byte_perm(u[i][0], u[i][1], 0x7632);
+        }
         frag_st_t(sh + b * 8 * kPitch64, w[0], w[1], w[2], w[3]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t x = __byte_perm(__float_as_uint(v[2 * i][b][0]), __float_as_uint(v[2 * i + 1][b][0]), 0x0051);
-          const uint32_t y = __byte_perm(__float_as_uint(v[2 * i][b][1]), __float_as_uint(v[2 * i + 1][b][1]), 0x0051);
+          const uint32_t x = __byte_perm(u[2 * i][0], u[2 * i + 1][0], 0x0051);
+          const uint32_t y = __byte_perm(u[2 * i][1], u[2 * i + 1][1], 0x0051);
           low[b][i] = __byte_perm(x, y, 0x5410);
         }
       }
