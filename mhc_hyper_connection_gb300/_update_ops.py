@@ -24,9 +24,9 @@ _IN = {**_DTYPES, torch.float32: MHC_DTYPE_FP32}
 
 @lru_cache(maxsize=64)
 def _coefficients(steps):
-    flat = [float(v) for step in steps for v in step]
-    if len(flat) != 3 * len(steps):
+    if any(len(step) != 3 for step in steps):
         raise ValueError("steps must be (a, b, c) triples")
+    flat = [float(v) for step in steps for v in step]
     return (ctypes.c_float * len(flat))(*flat)
 
 
