@@ -157,10 +157,15 @@ class Momentum:
                 p.sub_((lr * max(1.0, rows / cols) ** 0.5 * update.float()).to(p.dtype))
 
 
-def kept_bytes(tokens, width, hidden, keep):
-    """Bytes of activations that a layer keeps: streams, y, z, feed-forward sums."""
-    streams, sums = tokens * N * width, tokens * 2 * hidden   # of a plain block
-    return (streams + sums) * (129 / 128 if keep == "8bit" else 2) + 4 * tokens * width
+def kept_bytes(tokens, width, hidden, keep, experts=0, choices=2):
+    """Bytes of activations that a layer keeps: streams, y, z, feed-forward sums; with
+    experts the sums of every chosen expert's rows, in 16 bits whatever the streams are
+    kept in (rows for as many slots as a plan may pad), logits, routes and the plan."""
+    low = 129 / 128 if keep == "8bit" else 2
+    if not experts:
+        return tokens * (N * width + 2 * hidden) * low + 4 * tokens * width
+    plan, rows = (mhc.mhc_expert_plan_size(tokens, choices, experts)[1], mhc.mhc_expert_plan_rows(tokens, choices, experts)[1])
+    return tokens * N * width * low + rows * 4 * hidden + 4 * tokens * width + 4 * tokens * experts + 8 * tokens * choices + plan
 
 
 def main():
@@ -184,7 +189,7 @@ def main():
     layers = [kind(a.width, a.hidden, dev, seed=i + 1) for i in range(a.layers)]
     momentum = Momentum(layers) if a.update == "orthogonal" else None
     print(f"{a.layers} layers, {a.tokens} tokens, width {a.width}, hidden {a.hidden}: "
-          f"{kept_bytes(a.tokens, a.width, a.hidden, a.keep) / 2 ** 20:.1f} MiB kept per layer ({a.keep})")
+          f"{kept_bytes(a.tokens, a.width, a.hidden, a.keep, a.experts, a.choices) / 2 ** 20:.1f} MiB kept per layer ({a.keep})")
     for step in range(a.steps):
         loss, grads, _ = forward_backward(layers, X, target, a.keep)
         norm = sum(float(g.float().square().sum()) for d in grads for g in d.values()) ** 0.5
