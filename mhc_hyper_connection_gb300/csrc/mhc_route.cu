@@ -131,23 +131,27 @@ __device__ __forceinline__ void sort_lane(U (&u)[V], int (&id)[V]) {
   }
 }
 
-// Groups of the marks (group g's in lane g): the top_groups best, as bits.  close: a group
-// left out has a mark within `tol` (of its size and smax) of the last one taken.
+// Groups of the marks (group g's in lane g): the top_groups best, as bits.  size: of the keys
+// that a mark is the sum of (with a bias they may cancel).  close: a group left out has a mark
+// within `tol` (of these sizes and smax) of the last one taken.
 template <class K>
-__device__ __forceinline__ uint32_t choose_groups(K mark, const RouteArgs& a, float smax, float tol, int lane, bool& close) {
+__device__ __forceinline__ uint32_t choose_groups(K mark, K size, const RouteArgs& a, float smax, float tol, int lane, bool& close) {
   using U = typename Ordered<K>::U;
   U u = lane < a.groups ? order(mark) : (U)0;
-  K last = 0;
   uint32_t stays = 0;
+  int w = 0;
   for (int i = 0; i < a.top_groups; ++i) {
     const U mu = warp_max(u);
-    const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
+    w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
     stays |= 1u << w;
     if (lane == w) u = 0;
-    last = __shfl_sync(kFull, mark, w);
   }
-  const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != (K)-INFINITY;
-  close = __any_sync(kFull, left && last - mark <= (K)(2.0f * tol * (smax + fabsf((float)last))));
+  close = false;
+  if (sizeof(K) == 4) {
+    const float last = __shfl_sync(kFull, (float)mark, w), of = fmaxf(__shfl_sync(kFull, (float)size, w), (float)size);
+    const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != (K)-INFINITY;
+    close = __any_sync(kFull, left && last - (float)mark <= 2.0f * tol * (smax + of));
+  }
   return stays;
 }
 
@@ -234,8 +238,11 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
         next = order(b2) > order(next) ? b2 : next;
       }
     }
-    const K m = a.top2 && next != (K)-INFINITY ? best + next : best;
-    const uint32_t stays = choose_groups<K>(__shfl_sync(kFull, m, min(lane * span, 31)), a, smax, tol, lane, close);
+    const bool two = a.top2 && next != (K)-INFINITY;
+    const K m = two ? best + next : best, size = two ? fabs(best) + fabs(next) : fabs(best);
+    const int from = min(lane * span, 31);
+    const uint32_t stays =
+        choose_groups<K>(__shfl_sync(kFull, m, from), __shfl_sync(kFull, size, from), a, smax, tol, lane, close);
     int grp = e0 / per, grp_end = (grp + 1) * per;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -275,8 +282,11 @@ __device__ __forceinline__ int choose(const RouteArgs& a, long long row, const f
         best = b == kOut ? (K)-INFINITY : score_of(a, unorder(b), sums);
         next = n == kOut ? (K)-INFINITY : score_of(a, unorder(n), sums);
       }
-      const K m = a.top2 && next != (K)-INFINITY ? best + next : best;
-      const uint32_t stays = choose_groups<K>(__shfl_sync(kFull, m, (lane * lanes) & 31), a, smax, tol, lane, close);
+      const bool two = a.top2 && next != (K)-INFINITY;
+      const K m = two ? best + next : best, size = two ? fabs(best) + fabs(next) : fabs(best);
+      const int from = (lane * lanes) & 31;
+      const uint32_t stays =
+          choose_groups<K>(__shfl_sync(kFull, m, from), __shfl_sync(kFull, size, from), a, smax, tol, lane, close);
       if (!((stays >> (lane / lanes)) & 1u)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] = kOut;
