@@ -52,8 +52,8 @@ typedef struct {
 
 MHC_API mhc_status_t mhc_orth_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t *bytes);
 
-/* Enqueue: two kernels and three for each step.  batch == 0 returns MHC_OK, nothing
- * launched. */
+/* Enqueue: two kernels and three for each step, four where few deep tiles of X X^T are
+ * summed in parts.  batch == 0 returns MHC_OK, nothing launched. */
 MHC_API mhc_status_t mhc_orth_run(const mhc_orth_args *a, void *stream);
 
 /* As mhc_ffn_status. */

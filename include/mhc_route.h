@@ -4,19 +4,19 @@
  * the order in which the experts' products take the tokens.
  *
  * Scores.  l: logits [T, E].  s = softmax over the row, or sigmoid of each.  A
- * logit of -inf takes its expert out; a row of -inf alone (a padded token) takes
- * none.
+ * logit of -inf takes its expert out, as does a bias of -inf; a row of -inf alone
+ * (a padded token) takes none.
  *
  * Choice.  key = s, or s + bias (bias [E] steers the choice alone, not the
  * weights).  Without a bias the order is that of the logits.  With groups > 1 the
  * experts are cut into so many runs of E / groups; a group counts for its largest
  * key or for the sum of its two largest (a lone key for itself), and the top_groups
  * best remain.  Of the experts that remain the k with the largest keys are taken,
- * largest first.  Equal keys: the lower index first, for groups too.  The order is
- * that of the exact keys of the given fp32 or 16-bit numbers: keys that fp32 cannot
- * tell apart are formed again in fp64.  A NaN counts as larger than any number, so
- * that it is chosen and seen.  Fewer than k experts left: the slots behind hold
- * expert -1 and weight 0.
+ * largest first.  Equal keys (-0 and +0 are): the lower index first, for groups too.
+ * The order is that of the exact keys of the given fp32 or 16-bit numbers: keys that
+ * fp32 cannot tell apart are formed again in fp64.  A NaN counts as larger than any
+ * number, so that it is chosen and seen.  Fewer than k experts left: the slots behind
+ * hold expert -1 and weight 0.
  *
  * Weights.  w = s of the chosen, divided by their sum if renormalise (formed from
  * ratios, so scores that underflow fp32 still have their shares), times scale;
@@ -37,8 +37,10 @@
  * Sizes: 0 <= T <= 2^20, T k <= 2^22, E in [1, 1024], 1 <= k <= min(E, 32), groups
  * in [1, 32] and a divisor of E, 1 <= top_groups <= groups, k <= top_groups E /
  * groups.  Tensors are contiguous device memory owned by the caller, aligned to
- * their element (plan: 256 bytes); outputs overlap neither inputs nor one another.
- * Calls are asynchronous on `stream` (a cudaStream_t, NULL = legacy default) and
+ * their element; the plan to 256 bytes; the logits of mhc_route_run and grad_logits to
+ * four elements where E is a multiple of four and to two where it is even (else
+ * MHC_ERR_PARAM_INVALID).  Outputs overlap neither inputs nor one another.  Calls
+ * are asynchronous on `stream` (a cudaStream_t, NULL = legacy default) and
  * wait for nothing on the device.  Status codes are those of mhc_pre.h.
  */
 #ifndef MHC_ROUTE_H_

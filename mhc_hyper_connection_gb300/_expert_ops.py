@@ -74,7 +74,9 @@ def route_experts(logits, top_k, score="softmax", bias=None, groups=1, top_group
     taken, a group counting for its largest ("max") or two largest ("top2") scores.
     Weights are the scores, divided by their sum with renormalise, times scale.  A
     logit of -inf takes its expert out; slots without an expert hold -1 and 0.  Ties
-    go to the lower index.  `out` is a Routes to write into."""
+    go to the lower index, -0 and +0 being one.  `out` is a Routes to write into.
+    Logits begin at an address of four elements where E is a multiple of four, of two
+    where it is even (every tensor that is no view does; else MhcError)."""
     dt, sc = _kind(logits, score)
     if group_score not in _GROUP_SCORES:
         raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)} (got {group_score!r})")
@@ -103,7 +105,8 @@ def route_experts_backward(grad_weights, logits, experts, score="softmax", renor
                            grad_logits=None, stream=None):
     """The gradient of logits from that of the weights (fp32 [T, k]), for the experts
     that route_experts chose with the same score, renormalise and scale.  Returns
-    grad_logits in the logits' type, written into the one given."""
+    grad_logits in the logits' type, written into the one given (aligned as the logits
+    of route_experts)."""
     dt, sc = _kind(logits, score)
     *lead, E = logits.shape
     lead, dev = tuple(lead), logits.device

@@ -10,8 +10,8 @@
 //
 // Bound by: the weights' stream for few tokens (one token, 8 experts of 4096 x 2048: 6.2 and
 // 5.7 TB/s); the tensor cores and their power for many (pipe active at 4096 tokens, 4 of 16
-// experts: 87% in gate and up, down and grad_x, 83% in the weight gradients, 69% in the gate
-// gradients, whose epilogue moves five 16-bit values for each of its sums).
+// experts: 86% in gate and up and in grad_x, 80% in down, 83% in the weight gradients, 70% in
+// the gate gradients, whose epilogue moves five 16-bit values for each of its sums).
 #pragma once
 
 #include "mhc_experts.cuh"

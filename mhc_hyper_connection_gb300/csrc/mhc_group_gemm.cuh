@@ -9,7 +9,7 @@
 // a job maps a tile number to operands, width and depth (each tile's own), stages
 // are as many as the job's operands leave room for, and a tile deeper than
 // kGrpDeepest chunks is formed in parts that the epilogue joins in fp32.  Large products
-// keep the tensor pipe 83 to 88% busy (products whose epilogues read as much as they write
+// keep the tensor pipe 80 to 88% busy (products whose epilogues read as much as they write
 // 70 to 75%) and are then held by the power limit.
 #pragma once
 

@@ -3,8 +3,10 @@
 //
 // Routing and its gradient read and write each score once; a row is a warp's, its
 // scores in registers, E / 32 consecutive ones a lane.  Bound by the warp's instructions
-// (keys, sorting, the groups and a maximum over the warp for each choice: 1290 a row of
-// 256 experts, 8 of 4 groups of 8), not by memory: 16384 such rows take 37 us, their bytes 2.6.
+// (keys, sorting, the groups and a maximum over the warp for each choice: 1270 a row of
+// 256 experts, 8 of 4 groups of 8), not by memory: 16384 such rows take 38 us, their bytes 2.6.
+// Up to 256 experts a lane's scores are sorted; more are searched (8192 rows of 512: 27 us
+// without a bias or groups, 66 with both).
 #include <math.h>
 
 #include "mhc_experts.cuh"
@@ -184,7 +186,8 @@ __device__ __noinline__ int reorder64(const RouteArgs& a, long long row, int min
 // The choice from keys of type K: experts lane * V + i are a lane's.  Returns, in lane j <
 // k, the j-th expert (or -1).  With K = float, `unsure` is set where two keys that decide
 // something are so close that they may stand in the wrong order: closer than tol (smax +
-// max(|a|, |b|)), smax the largest score.  room: E values of this warp.
+// max(|a|, |b|)), smax the largest score, or twice that for groups, of the sizes of the keys
+// that their marks are sums of.  room: E values of this warp.
 // Up to eight scores a lane are sorted first, so that a round takes a lane's next instead
 // of searching it (T = 16384, E = 256, k = 8 of 4 groups of 8: 63 -> 48 us).
 template <int kType, class K, int V>
@@ -443,8 +446,8 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, long long row, int 
   }
 }
 
-// The choice once more with keys in fp64, for rows where fp32 left two keys too close: some
-// of a thousand of ordinary rows with a bias or groups.
+// The choice once more with keys in fp64, for rows where fp32 left two keys too close: two to
+// ten of ten thousand ordinary rows with groups, or of softmax scores with a bias.
 template <int kType, int V>
 __device__ __noinline__ int choose64(const RouteArgs& a, long long row, float top, double* room, int lane) {
   const int e0 = lane * V;
