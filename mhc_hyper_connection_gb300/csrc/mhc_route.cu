@@ -134,25 +134,24 @@ __device__ __forceinline__ void sort_lane(U (&u)[V], int (&id)[V]) {
 }
 
 // Groups of the marks (group g's in lane g): the top_groups best, as bits.  size: of the keys
-// that a mark is the sum of (with a bias they may cancel).  close: a group left out has a mark
-// within `tol` (of these sizes and smax) of the last one taken.
+// that a mark is the sum of (with a bias they may cancel).  close: were every mark off by `tol`
+// of that and smax, a group left out might be ahead of one taken.
 template <class K>
 __device__ __forceinline__ uint32_t choose_groups(K mark, K size, const RouteArgs& a, float smax, float tol, int lane, bool& close) {
   using U = typename Ordered<K>::U;
   U u = lane < a.groups ? order(mark) : (U)0;
   uint32_t stays = 0;
-  int w = 0;
   for (int i = 0; i < a.top_groups; ++i) {
     const U mu = warp_max(u);
-    w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
+    const int w = __ffs(__ballot_sync(kFull, u == mu && lane < a.groups && !((stays >> lane) & 1u))) - 1;
     stays |= 1u << w;
     if (lane == w) u = 0;
   }
   close = false;
   if (sizeof(K) == 4) {
-    const float last = __shfl_sync(kFull, (float)mark, w), of = fmaxf(__shfl_sync(kFull, (float)size, w), (float)size);
-    const bool left = lane < a.groups && !((stays >> lane) & 1u) && mark != (K)-INFINITY;
-    close = __any_sync(kFull, left && last - (float)mark <= 2.0f * tol * (smax + of));
+    const float m = (float)mark, off = tol * (smax + (float)size);
+    const bool any = lane < a.groups && m != -INFINITY, taken = (stays >> lane) & 1u;
+    close = warp_max(order(any && !taken ? m + off : -INFINITY)) >= __reduce_min_sync(kFull, order(any && taken ? m - off : INFINITY));
   }
   return stays;
 }
@@ -186,8 +185,8 @@ __device__ __noinline__ int reorder64(const RouteArgs& a, long long row, int min
 // The choice from keys of type K: experts lane * V + i are a lane's.  Returns, in lane j <
 // k, the j-th expert (or -1).  With K = float, `unsure` is set where two keys that decide
 // something are so close that they may stand in the wrong order: closer than tol (smax +
-// max(|a|, |b|)), smax the largest score, or twice that for groups, of the sizes of the keys
-// that their marks are sums of.  room: E values of this warp.
+// max(|a|, |b|)), smax the largest score; of groups as choose_groups says.  room: E values of
+// this warp.
 // Up to eight scores a lane are sorted first, so that a round takes a lane's next instead
 // of searching it (T = 16384, E = 256, k = 8 of 4 groups of 8: 63 -> 48 us).
 template <int kType, class K, int V>
